@@ -80,6 +80,8 @@ typedef void *mp_stream_t;    /* a cudaStream_t                             */
 #define MP_STATUS_ROWS_OVERFLOW 0x10 /* padded total > out_rows: excess dropped  */
 #define MP_STATUS_BAD_ROW 0x20       /* row_map entry outside [-1,N): skipped    */
 #define MP_STATUS_BAD_PADDED 0x40    /* a padded size below its group's rows     */
+#define MP_STATUS_BAD_OFFSETS 0x80   /* offsets fall, or leave [0,R]: clamped    */
+#define MP_STATUS_STALLED 0x100      /* a kernel gave up a wait: outputs invalid */
 
 /* Token types of the chunk entry points with a dtype argument. */
 #define MP_DTYPE_BF16 0
@@ -88,6 +90,25 @@ typedef void *mp_stream_t;    /* a cudaStream_t                             */
 
 #define MP_MAX_EXPERTS 1024
 #define MP_MAX_CHUNKS 1024
+
+/* Scores of mp_route. */
+#define MP_SCORE_SOFTMAX 0
+#define MP_SCORE_SIGMOID 1
+
+/* Activations of the experts' products.  GELU is the tanh form.  The gated
+ * ones take a product of 2F columns, the gate's F first, to F columns:
+ * act(gate) * other. */
+#define MP_ACT_NONE 0
+#define MP_ACT_RELU 1
+#define MP_ACT_GELU 2
+#define MP_ACT_SILU 3
+#define MP_ACT_GEGLU 4
+#define MP_ACT_SWIGLU 5
+
+/* What mp_expert_gemm keeps of its product for the backward pass. */
+#define MP_SAVE_NONE 0
+#define MP_SAVE_BF16 1
+#define MP_SAVE_E4M3 2
 
 /* Text for a status code (static storage). */
 const char *mp_status_string(mp_status_t status);
@@ -212,6 +233,103 @@ mp_status_t mp_topk_softmax(const float *logits, int64_t T, int32_t E, int32_t K
 mp_status_t mp_topk_softmax_bwd(const float *g_probs, const float *probs, const int32_t *idx,
                                 int64_t T, int32_t E, int32_t K, float *g_logits,
                                 mp_stream_t stream);
+
+/*
+ * The router of a training step with scores, balance bias and renormalised
+ * weights.  Per token, with logits l and
+ *   s_e = softmax(l)_e over all E (MP_SCORE_SOFTMAX) or sigmoid(l_e)
+ *   c_e = s_e + bias_e     (bias device fp32 [E] or NULL: c_e = s_e)
+ * if n_groups > 1, the topk_groups groups of consecutive experts are kept whose
+ * sum of the group_top (1 or 2) largest c is largest; then the K experts with
+ * the largest c among the kept are picked, slot 0 the largest.  Equal values
+ * favour the lower group and expert.  The choice is that of c in 64 bits.
+ *   weights[t,k] = scale * s_k / sum_j s_j over the picks   (renorm != 0)
+ *                = scale * s_k                              (renorm == 0)
+ * An expert whose logit is -inf or NaN, or whose bias is, is never picked;
+ * where fewer than K are left, the last slots are empty: idx -1 (no row in
+ * mp_build_map), weight 0.  A logit of +inf counts as the largest float.
+ *   logits  device [T,E] of type dtype (MP_DTYPE_*)
+ *   idx     device int32 [T,K];  weights device fp32 [T,K]
+ * Limits as mp_topk_softmax.
+ */
+mp_status_t mp_route(const void *logits, int32_t dtype, const float *bias, int64_t T, int32_t E,
+                     int32_t K, int32_t score, int32_t n_groups, int32_t topk_groups,
+                     int32_t group_top, int32_t renorm, float scale, int32_t *idx,
+                     float *weights, mp_stream_t stream);
+
+/*
+ * Backward of mp_route: the gradient of the weights with respect to the logits,
+ * the choice and the bias held fixed.
+ *   g_weights device fp32 [T,K];  logits, idx as mp_route had them;
+ *   g_logits  device [T,E] of type dtype, every element written.
+ * An empty slot gives no gradient.
+ */
+mp_status_t mp_route_bwd(const float *g_weights, const void *logits, int32_t dtype,
+                         const int32_t *idx, int64_t T, int32_t E, int32_t K, int32_t score,
+                         int32_t renorm, float scale, void *g_logits, mp_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* The experts' products, on rows in the order mp_permute gives              */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * One matrix product per expert with bias, activation and residual:
+ *   z[r,:]   = x[r,:] w[e]^T + bias[e]         (fp32, e the expert of row r)
+ *   out[r,:] = act(z[r,:]) + residual[r,:]     (rounded once)
+ * Expert e owns rows [offsets[e], offsets[e+1]), as mp_build_map gives them;
+ * rows at offsets[E] and beyond are neither read nor written.
+ *   x        device bf16 [R,K];  w device bf16 [E,N,K]
+ *   offsets  device int32 [E+1].  Offsets that fall or leave [0,R] are clamped
+ *            to the largest before them and to R (MP_STATUS_BAD_OFFSETS).
+ *   bias     device bf16 [E,N] or NULL
+ *   residual device bf16 [R,F] or NULL (it may be out itself)
+ *   out      device bf16 [R,F], F = N, or N/2 with a gated activation
+ *   save     MP_SAVE_BF16: z device bf16 [R,N] gets z rounded.  MP_SAVE_E4M3: z
+ *            device e4m3 [R,N] and z_exp device uint8 [R, parts*ceil(F/32)]
+ *            (parts 2 if gated, else 1): per row, part and 32 columns z is
+ *            code * 2^(z_exp-127), with the smallest power of two that brings
+ *            the largest to 448 at most; what is not finite is stored as NaN.
+ * Sums are fp32 in an order that depends on K alone for a given kernel, so a
+ * row's result does not depend on the rows around it.
+ * Limits: E <= MP_MAX_EXPERTS; N, K <= 2^22; R < 2^31 - 1024.
+ * Rows whose width K is a multiple of 8 with 16-byte aligned x and w take the
+ * tensor cores; other calls are computed by a slower kernel.
+ */
+mp_status_t mp_expert_gemm(const mp_bf16_t *x, const mp_bf16_t *w, const int32_t *offsets,
+                           int64_t R, int32_t E, int32_t N, int32_t K, const mp_bf16_t *bias,
+                           int32_t act, const mp_bf16_t *residual, mp_bf16_t *out, int32_t save,
+                           void *z, uint8_t *z_exp, int32_t *dev_status, mp_stream_t stream);
+
+/*
+ * Gradient of mp_expert_gemm's product with respect to its rows, and through
+ * the activation before them:
+ *   g_h[r,:] = g[r,:] w[e]                     (fp32, [R,K])
+ *   act NONE: g_x = g_h.   Otherwise g_x = the gradient of act at z, times g_h
+ *   ([R,K], or [R,2K] gated), and h = act(z) again ([R,K], NULL: not written).
+ *   g        device bf16 [R,N];  w device bf16 [E,N,K]
+ *   z, z_exp what mp_expert_gemm saved of the product before the activation
+ *            (`save` says how), K columns a part
+ * Rows, offsets, limits and errors as mp_expert_gemm.
+ */
+mp_status_t mp_expert_dgrad(const mp_bf16_t *g, const mp_bf16_t *w, const int32_t *offsets,
+                            int64_t R, int32_t E, int32_t N, int32_t K, int32_t act,
+                            int32_t save, const void *z, const uint8_t *z_exp, mp_bf16_t *g_x,
+                            mp_bf16_t *h, int32_t *dev_status, mp_stream_t stream);
+
+/*
+ * Gradients of mp_expert_gemm's product with respect to its weights and bias:
+ *   g_w[e] = sum over the expert's rows of g[r,:]^T x[r,:],  g_bias[e] = sum of g[r,:]
+ * in fp32, zero for an expert without rows.
+ *   g device bf16 [R,N];  x device bf16 [R,K]
+ *   g_w    device [E,N,K] of type dtype: MP_DTYPE_BF16, or MP_DTYPE_FP32, which
+ *          with accumulate != 0 adds to what is there.
+ *   g_bias device [E,N] of type dtype (treated alike) or NULL
+ * Rows, offsets, limits and errors as mp_expert_gemm.
+ */
+mp_status_t mp_expert_wgrad(const mp_bf16_t *g, const mp_bf16_t *x, const int32_t *offsets,
+                            int64_t R, int32_t E, int32_t N, int32_t K, int32_t dtype,
+                            int32_t accumulate, void *g_w, void *g_bias, int32_t *dev_status,
+                            mp_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Permute / unpermute  [d9d _permute_kernel, _unpermute_kernel; MBI]        */

@@ -20,7 +20,8 @@ from . import _lib
 
 __all__ = [
     "MPError", "mp_build_map", "mp_build_map_capacity", "mp_build_map_workspace_size",
-    "mp_topk_softmax", "mp_topk_softmax_bwd", "mp_permute", "mp_unpermute", "mp_unpermute_ep", "EP_BF16_PARTIALS", "EP_FP64_CROSS_RANK",
+    "mp_topk_softmax", "mp_topk_softmax_bwd", "mp_route", "mp_route_bwd", "mp_expert_gemm",
+    "mp_expert_dgrad", "mp_expert_wgrad", "mp_permute", "mp_unpermute", "mp_unpermute_ep", "EP_BF16_PARTIALS", "EP_FP64_CROSS_RANK",
     "mp_permute_bwd", "mp_unpermute_bwd", "mp_sort_chunks_pad", "mp_unpad_restore",
     "mp_sort_chunks_pad_bwd", "mp_unpad_restore_bwd", "status_bits", "library_path",
 ]
@@ -28,10 +29,14 @@ __all__ = [
 STATUS_BITS = {
     "bad_expert": 0x1, "bad_split": 0x2, "bad_order": 0x4, "split_overflow": 0x8,
     "rows_overflow": 0x10, "bad_row": 0x20, "bad_padded": 0x40,
+    "bad_offsets": 0x80, "stalled": 0x100,
 }
 
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # MP_DTYPE_*
+SCORES = {"softmax": 0, "sigmoid": 1}                              # MP_SCORE_*
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3, "geglu": 4, "swiglu": 5}   # MP_ACT_*
+SAVES = {"none": 0, "bf16": 1, "e4m3": 2}                          # MP_SAVE_*
 EP_BF16_PARTIALS = 0x1
 EP_FP64_CROSS_RANK = 0x2
 
@@ -223,6 +228,218 @@ def mp_topk_softmax_bwd(g_probs, probs, idx, num_experts: int, *, g_logits=None)
         _check("mp_topk_softmax_bwd", lib.mp_topk_softmax_bwd(
             _ptr(g_probs), _ptr(probs), _ptr(idx), T, E, K, _ptr(g_logits), _stream(dev)))
     return g_logits
+
+
+def _named(value, table, name):
+    if value not in table:
+        raise ValueError(f"{name} must be one of {', '.join(table)}, got {value!r}")
+    return table[value]
+
+
+def mp_route(logits, topk: int, *, score: str = "softmax", bias=None, n_groups: int = 1,
+             topk_groups: int = 1, group_top: int = 1, renorm: bool = True, scale: float = 1.0,
+             idx=None, weights=None):
+    """logits [T,E] (fp32, bf16 or fp16) -> (idx int32 [T,K], weights fp32 [T,K]).
+
+    Scores are the softmax over all experts or the sigmoid; `bias` (fp32 [E])
+    is added to them for the choice only; with groups, the `topk_groups` best of
+    `n_groups` are kept first, by the sum of their `group_top` best.  Weights are
+    the picks' scores, divided by their sum if `renorm`, times `scale`.  A logit of -inf
+    makes an expert unavailable; slots left over are -1 with weight 0."""
+    lib = _lib.load()
+    dt = _token_dtype(logits, "logits")
+    _need(logits, "logits", logits.dtype, 2)
+    dev = logits.device
+    T, E = logits.shape
+    K = int(topk)
+    if bias is not None:
+        _need(bias, "bias", torch.float32, 1, dev)
+        _shape(bias, "bias", (E,))
+    idx = torch.empty((T, K), dtype=torch.int32, device=dev) if idx is None \
+        else _need(idx, "idx", torch.int32, 2, dev)
+    weights = torch.empty((T, K), dtype=torch.float32, device=dev) if weights is None \
+        else _need(weights, "weights", torch.float32, 2, dev)
+    _shape(idx, "idx", (T, K))
+    _shape(weights, "weights", (T, K))
+    with _on(dev):
+        _check("mp_route", lib.mp_route(
+            _ptr(logits), dt, _ptr(bias), T, E, K, _named(score, SCORES, "score"),
+            int(n_groups), int(topk_groups), int(group_top), int(bool(renorm)), float(scale),
+            _ptr(idx), _ptr(weights), _stream(dev)))
+    return idx, weights
+
+
+def mp_route_bwd(g_weights, logits, idx, *, score: str = "softmax", renorm: bool = True,
+                 scale: float = 1.0, g_logits=None):
+    """Gradient of mp_route's weights w.r.t. the logits: [T,E] of the logits' type."""
+    lib = _lib.load()
+    dt = _token_dtype(logits, "logits")
+    _need(logits, "logits", logits.dtype, 2)
+    dev = logits.device
+    T, E = logits.shape
+    _need(idx, "idx", torch.int32, 2, dev)
+    K = idx.shape[1]
+    _shape(idx, "idx", (T, K))
+    _need(g_weights, "g_weights", torch.float32, 2, dev)
+    _shape(g_weights, "g_weights", (T, K))
+    g_logits = torch.empty_like(logits) if g_logits is None \
+        else _need(g_logits, "g_logits", logits.dtype, 2, dev)
+    _shape(g_logits, "g_logits", (T, E))
+    with _on(dev):
+        _check("mp_route_bwd", lib.mp_route_bwd(
+            _ptr(g_weights), _ptr(logits), dt, _ptr(idx), T, E, K,
+            _named(score, SCORES, "score"), int(bool(renorm)), float(scale), _ptr(g_logits),
+            _stream(dev)))
+    return g_logits
+
+
+# --------------------------------------------------------------------------
+# the experts' products
+# --------------------------------------------------------------------------
+
+def _parts(act):
+    return 2 if act in ("geglu", "swiglu") else 1
+
+
+def _checkpoint_shapes(R, F, act, save):
+    """Shapes and types of (z, z_exp) that a product with F output columns keeps."""
+    parts = _parts(act)
+    if save == "bf16":
+        return ((R, parts * F), torch.bfloat16), None
+    return ((R, parts * F), torch.float8_e4m3fn), ((R, parts * -(-F // 32)), torch.uint8)
+
+
+def _checkpoint(z, z_exp, R, F, act, save, dev, make):
+    """(z, z_exp), checked against what `save` means, or made if `make`."""
+    if save == "none":
+        if z is not None or z_exp is not None:
+            raise ValueError("z and z_exp belong to a saved product")
+        return None, None
+    got = []
+    for t, name, want in zip((z, z_exp), ("z", "z_exp"), _checkpoint_shapes(R, F, act, save)):
+        if want is None:
+            if t is not None:
+                raise ValueError(f"{name} belongs to an e4m3 checkpoint")
+        elif t is None and make:
+            t = torch.empty(want[0], dtype=want[1], device=dev)
+        else:
+            _need(t, name, want[1], 2, dev)
+            _shape(t, name, want[0])
+        got.append(t)
+    return tuple(got)
+
+
+def _products(rows, name, w, offsets, width):
+    _need(rows, name, torch.bfloat16, 2)
+    dev = rows.device
+    _need(w, "w", torch.bfloat16, 3, dev)
+    E, N, K = w.shape
+    _shape(rows, name, (rows.shape[0], w.shape[width]))
+    _need(offsets, "offsets", torch.int32, 1, dev)
+    _shape(offsets, "offsets", (E + 1,))
+    return dev, rows.shape[0], E, N, K
+
+
+def mp_expert_gemm(x, w, offsets, *, bias=None, act: str = "none", residual=None,
+                   save: str = "none", out=None, z=None, z_exp=None, status=None):
+    """x bf16 [R,K], w bf16 [E,N,K], offsets int32 [E+1] -> (out bf16 [R,F], z, z_exp):
+    out = act(x w[e]^T + bias[e]) + residual for the rows of each expert, F = N (N/2 for
+    the gated activations geglu and swiglu, whose gate is the first half of w's rows).
+    `save` keeps the product before the activation: "bf16" in z bf16 [R,N], "e4m3" in
+    z float8_e4m3fn [R,N] with z_exp uint8 (one power of two per 32 columns)."""
+    lib = _lib.load()
+    dev, R, E, N, K = _products(x, "x", w, offsets, 2)
+    a, s = _named(act, ACTS, "act"), _named(save, SAVES, "save")
+    if N % _parts(act):
+        raise ValueError(f"a gated activation needs an even number of columns, got {N}")
+    F = N // _parts(act)
+    if bias is not None:
+        _need(bias, "bias", torch.bfloat16, 2, dev)
+        _shape(bias, "bias", (E, N))
+    if residual is not None:
+        _need(residual, "residual", torch.bfloat16, 2, dev)
+        _shape(residual, "residual", (R, F))
+    out = torch.empty((R, F), dtype=torch.bfloat16, device=dev) if out is None \
+        else _need(out, "out", torch.bfloat16, 2, dev)
+    _shape(out, "out", (R, F))
+    z, z_exp = _checkpoint(z, z_exp, R, F, act, save, dev, make=True)
+    _opt(status, "status", torch.int32, 1, dev)
+    with _on(dev):
+        _check("mp_expert_gemm", lib.mp_expert_gemm(
+            _ptr(x), _ptr(w), _ptr(offsets), R, E, N, K, _ptr(bias), a, _ptr(residual),
+            _ptr(out), s, _ptr(z), _ptr(z_exp), _ptr(status), _stream(dev)))
+    return out, z, z_exp
+
+
+def mp_expert_dgrad(g, w, offsets, *, act: str = "none", z=None, z_exp=None,
+                    with_h: bool = False, g_x=None, h=None, status=None):
+    """Gradient of mp_expert_gemm w.r.t. its rows: g bf16 [R,N], w bf16 [E,N,K] -> (g_x, h).
+    With `act`, also through the activation before those rows, whose product was saved
+    as z (and z_exp): g_x is then [R,K] or, gated, [R,2K], and h = act(z) bf16 [R,K] if
+    `with_h` (the rows that mp_expert_wgrad needs)."""
+    lib = _lib.load()
+    dev, R, E, N, K = _products(g, "g", w, offsets, 1)
+    a = _named(act, ACTS, "act")
+    if act == "none":
+        save = "none"
+    elif z is None:
+        raise ValueError("mp_expert_dgrad with an activation needs the saved product z")
+    else:
+        save = "e4m3" if z_exp is not None else "bf16"
+    z, z_exp = _checkpoint(z, z_exp, R, K, act, save, dev, make=False)
+    shape = (R, K * _parts(act))
+    g_x = torch.empty(shape, dtype=torch.bfloat16, device=dev) if g_x is None \
+        else _need(g_x, "g_x", torch.bfloat16, 2, dev)
+    _shape(g_x, "g_x", shape)
+    if h is None and with_h:
+        h = torch.empty((R, K), dtype=torch.bfloat16, device=dev)
+    if h is not None:
+        if act == "none":
+            raise ValueError("h is the result of an activation: there is none")
+        _need(h, "h", torch.bfloat16, 2, dev)
+        _shape(h, "h", (R, K))
+    _opt(status, "status", torch.int32, 1, dev)
+    with _on(dev):
+        _check("mp_expert_dgrad", lib.mp_expert_dgrad(
+            _ptr(g), _ptr(w), _ptr(offsets), R, E, N, K, a, SAVES[save], _ptr(z), _ptr(z_exp),
+            _ptr(g_x), _ptr(h), _ptr(status), _stream(dev)))
+    return g_x, h
+
+
+def mp_expert_wgrad(g, x, offsets, *, with_bias: bool = False, dtype=torch.bfloat16,
+                    accumulate: bool = False, g_w=None, g_bias=None, status=None):
+    """Gradient of mp_expert_gemm w.r.t. weights and bias: g bf16 [R,N], x bf16 [R,K] ->
+    (g_w [E,N,K], g_bias [E,N] or None) of `dtype` (bf16 or fp32).  With `accumulate`
+    the fp32 g_w (and g_bias), which must be given, are added to."""
+    lib = _lib.load()
+    _need(g, "g", torch.bfloat16, 2)
+    dev = g.device
+    R, N = g.shape
+    _need(x, "x", torch.bfloat16, 2, dev)
+    K = x.shape[1]
+    _shape(x, "x", (R, K))
+    _need(offsets, "offsets", torch.int32, 1, dev)
+    E = offsets.shape[0] - 1
+    if g_w is not None:
+        dtype = g_w.dtype
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"weight gradients are bf16 or fp32, got {dtype}")
+    if accumulate and (g_w is None or dtype != torch.float32 or (with_bias and g_bias is None)):
+        raise ValueError("accumulate adds to fp32 gradients that are given")
+    g_w = torch.empty((E, N, K), dtype=dtype, device=dev) if g_w is None \
+        else _need(g_w, "g_w", dtype, 3, dev)
+    _shape(g_w, "g_w", (E, N, K))
+    if g_bias is None and with_bias:
+        g_bias = torch.empty((E, N), dtype=dtype, device=dev)
+    if g_bias is not None:
+        _need(g_bias, "g_bias", dtype, 2, dev)
+        _shape(g_bias, "g_bias", (E, N))
+    _opt(status, "status", torch.int32, 1, dev)
+    with _on(dev):
+        _check("mp_expert_wgrad", lib.mp_expert_wgrad(
+            _ptr(g), _ptr(x), _ptr(offsets), R, E, N, K, DTYPES[dtype], int(bool(accumulate)),
+            _ptr(g_w), _ptr(g_bias), _ptr(status), _stream(dev)))
+    return g_w, g_bias
 
 
 # --------------------------------------------------------------------------

@@ -12,6 +12,7 @@ _lib = None
 
 P = ctypes.c_void_p
 I32, I64, SZ = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+F32 = ctypes.c_float
 
 # name -> (restype, argtypes), exactly the prototypes of include/mp.h
 SIGNATURES = {
@@ -23,6 +24,11 @@ SIGNATURES = {
     "mp_build_map_noalloc": (I32, [P, I64, I32, I32, P, P, P, P, P, P]),
     "mp_topk_softmax": (I32, [P, I64, I32, I32, I32, I32, P, P, P]),
     "mp_topk_softmax_bwd": (I32, [P, P, P, I64, I32, I32, P, P]),
+    "mp_route": (I32, [P, I32, P, I64, I32, I32, I32, I32, I32, I32, I32, F32, P, P, P]),
+    "mp_route_bwd": (I32, [P, P, I32, P, I64, I32, I32, I32, I32, F32, P, P]),
+    "mp_expert_gemm": (I32, [P, P, P, I64, I32, I32, I32, P, I32, P, P, I32, P, P, P, P]),
+    "mp_expert_dgrad": (I32, [P, P, P, I64, I32, I32, I32, I32, I32, P, P, P, P, P, P]),
+    "mp_expert_wgrad": (I32, [P, P, P, I64, I32, I32, I32, I32, I32, P, P, P, P]),
     "mp_permute": (I32, [P, P, P, I64, I32, I32, P, P, P]),
     "mp_unpermute": (I32, [P, P, P, I64, I32, I32, P, P]),
     "mp_unpermute_ep": (I32, [P, P, P, P, I64, I32, I32, I32, I32, I32, P, P]),

@@ -25,13 +25,14 @@ from dataclasses import dataclass
 
 import torch
 
-from . import (mp_build_map, mp_build_map_capacity, mp_permute, mp_permute_bwd,
+from . import (mp_build_map, mp_build_map_capacity, mp_expert_dgrad, mp_expert_gemm,
+               mp_expert_wgrad, mp_permute, mp_permute_bwd, mp_route, mp_route_bwd,
                mp_sort_chunks_pad, mp_sort_chunks_pad_bwd, mp_topk_softmax,
                mp_topk_softmax_bwd, mp_unpad_restore, mp_unpad_restore_bwd, mp_unpermute,
                mp_unpermute_bwd, mp_unpermute_ep, mp_zero_rows_from)
 
-__all__ = ["Dispatch", "topk_softmax", "permute", "unpermute", "unpermute_ep",
-           "sort_chunks_pad", "unpad_restore"]
+__all__ = ["Dispatch", "topk_softmax", "route", "permute", "expert_mlp", "unpermute",
+           "unpermute_ep", "sort_chunks_pad", "unpad_restore"]
 
 
 @dataclass
@@ -117,6 +118,50 @@ class _TopkSoftmax(torch.autograd.Function):
         return g, None, None, None
 
 
+class _Route(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, bias, topk, choice, how):
+        idx, weights = mp_route(logits, topk, bias=bias, **choice, **how)
+        ctx.mark_non_differentiable(idx)
+        ctx.save_for_backward(logits, idx)
+        ctx.how = how
+        return idx, weights
+
+    @staticmethod
+    def backward(ctx, g_idx, g_weights):
+        logits, idx = ctx.saved_tensors
+        return mp_route_bwd(g_weights.contiguous(), logits, idx, **ctx.how), None, None, None, None
+
+
+class _ExpertMlp(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, rows, offsets, w1, w2, b1, b2, act, checkpoint):
+        kept = checkpoint if any(ctx.needs_input_grad) else "none"
+        h, z, z_exp = mp_expert_gemm(rows, w1, offsets, bias=b1, act=act, save=kept)
+        y, _, _ = mp_expert_gemm(h, w2, offsets, bias=b2)
+        mp_zero_rows_from(y, offsets[-1:])
+        ctx.save_for_backward(rows, offsets, w1, w2, z, z_exp)
+        ctx.act = act
+        return y
+
+    @staticmethod
+    def backward(ctx, g_y):
+        rows, offsets, w1, w2, z, z_exp = ctx.saved_tensors
+        need_x, _, need_w1, need_w2, need_b1, need_b2 = ctx.needs_input_grad[:6]
+        g_y = g_y.contiguous()
+        g_x = g_w1 = g_w2 = g_b1 = g_b2 = None
+        g_z, h = mp_expert_dgrad(g_y, w2, offsets, act=ctx.act, z=z, z_exp=z_exp,
+                                 with_h=need_w2 or need_b2)
+        if need_w2 or need_b2:
+            g_w2, g_b2 = mp_expert_wgrad(g_y, h, offsets, with_bias=need_b2)
+        if need_w1 or need_b1:
+            g_w1, g_b1 = mp_expert_wgrad(g_z, rows, offsets, with_bias=need_b1)
+        if need_x:
+            g_x, _ = mp_expert_dgrad(g_z, w1, offsets)
+            mp_zero_rows_from(g_x, offsets[-1:])
+        return g_x, None, g_w1, g_w2, g_b1, g_b2, None, None
+
+
 class _SortChunksPad(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, probs, split_sizes, chunk_order, num_groups, align, out_rows,
@@ -171,6 +216,37 @@ def topk_softmax(logits: torch.Tensor, topk: int, n_groups: int = 1, topk_groups
     """fp32 logits [T,E] -> (idx int32 [T,K], probs fp32 [T,K]); probs is
     differentiable w.r.t. the logits (softmax over the K picks)."""
     return _TopkSoftmax.apply(logits, int(topk), int(n_groups), int(topk_groups))
+
+
+def route(logits: torch.Tensor, topk: int, *, score: str = "softmax", bias=None,
+          n_groups: int = 1, topk_groups: int = 1, group_top: int = 1, renorm: bool = True,
+          scale: float = 1.0):
+    """logits [T,E] (fp32, bf16, fp16) -> (idx int32 [T,K], weights fp32 [T,K]);
+    the weights are differentiable w.r.t. the logits.  `bias` (fp32 [E], no
+    gradient) moves the choice only.  Empty slots are -1 with weight 0."""
+    return _Route.apply(logits, bias, int(topk),
+                        dict(n_groups=n_groups, topk_groups=topk_groups, group_top=group_top),
+                        dict(score=score, renorm=renorm, scale=scale))
+
+
+def expert_mlp(rows: torch.Tensor, offsets, w1: torch.Tensor, w2: torch.Tensor, b1=None,
+               b2=None, *, act: str = "swiglu", checkpoint: str = "e4m3") -> torch.Tensor:
+    """The experts on rows in expert order: act(rows w1[e]^T + b1[e]) w2[e]^T + b2[e].
+
+    rows bf16 [R,H]; `offsets` int32 [E+1], or the Dispatch that permute gave;
+    w1 bf16 [E,F,H] ([E,2F,H] for geglu and swiglu, gate first), w2 bf16
+    [E,H',F].  For the backward pass the product before the activation is kept
+    in 8 bits (checkpoint="e4m3", a power of two per 32 columns) or as "bf16",
+    and the activation's result is computed from it again; its gradients are
+    those at the kept values.  Rows past the routed count are zero in the
+    result and in the gradient."""
+    if act not in ("relu", "gelu", "silu", "geglu", "swiglu"):
+        raise ValueError(f"expert_mlp needs an activation, got {act!r}")
+    if checkpoint not in ("e4m3", "bf16"):
+        raise ValueError(f"checkpoint must be e4m3 or bf16, got {checkpoint!r}")
+    if isinstance(offsets, Dispatch):
+        offsets = offsets.offsets
+    return _ExpertMlp.apply(rows, offsets, w1, w2, b1, b2, act, checkpoint)
 
 
 def permute(x: torch.Tensor, idx: torch.Tensor, num_experts: int, probs=None, *,

@@ -1,0 +1,469 @@
+// What the experts' products share: activations and their derivatives, the
+// 8-bit checkpoint of a row, the epilogues on 32 columns of a row, and the
+// search for the expert of a tile.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+
+namespace mp {
+
+enum ExpertMode { FWD = 0, DGRAD = 1, WGRAD = 2 };
+
+constexpr int EPI_COLS = 32;   // columns an epilogue step handles, and a checkpoint block
+
+__host__ __device__ inline bool act_gated(int act) { return act >= MP_ACT_GEGLU; }
+// The function on the gate (or on every column of an ungated product).
+__host__ __device__ inline int act_inner(int act)
+{
+    return act == MP_ACT_GEGLU ? MP_ACT_GELU : act == MP_ACT_SWIGLU ? MP_ACT_SILU : act;
+}
+__host__ __device__ inline int ckpt_blocks(int n) { return (n + EPI_COLS - 1) / EPI_COLS; }
+
+// ---------------------------------------------------------------------------
+// Activations, in fp32.  expf is the accurate one: the fast one's error grows
+// with its argument, to 2^-17 of the value in gelu's tail.  The
+// division is the fast one (2 ulp).
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ float sigmoid_fast(float z) { return __fdividef(1.0f, 1.0f + expf(-z)); }
+
+// gelu in its tanh form is z * sigmoid(2u), u = sqrt(2/pi) (z + 0.044715 z^3):
+// no difference of nearly equal numbers for negative z.
+constexpr float GELU_A = 1.5957691216057308f;    // 2 sqrt(2/pi)
+constexpr float GELU_B = 0.044715f;
+
+// Past these bounds the derivative is 0 or 1 in fp32; NaN passes.
+__device__ __forceinline__ float act_bounded(float z, float b) { return z > b ? b : (z < -b ? -b : z); }
+
+__device__ __forceinline__ float act_value(float z, int inner)
+{
+    if (inner == MP_ACT_SILU) return z * sigmoid_fast(z);
+    if (inner == MP_ACT_GELU) {
+        const float c = act_bounded(z, 16.0f);
+        return z * sigmoid_fast(GELU_A * c * fmaf(GELU_B * c, c, 1.0f));
+    }
+    if (inner == MP_ACT_RELU) return z < 0.0f ? 0.0f : z;
+    return z;
+}
+
+// act(z), and its derivative through `slope`.
+__device__ __forceinline__ float act_value_slope(float z, int inner, float &slope)
+{
+    if (inner == MP_ACT_SILU) {
+        const float s = sigmoid_fast(z);
+        slope = fmaf(act_bounded(z, 100.0f) * s, 1.0f - s, s);
+        return z * s;
+    }
+    if (inner == MP_ACT_GELU) {
+        const float c = act_bounded(z, 16.0f);
+        const float s = sigmoid_fast(GELU_A * c * fmaf(GELU_B * c, c, 1.0f));
+        const float du = GELU_A * fmaf(3.0f * GELU_B * c, c, 1.0f);
+        slope = fmaf(c * s * (1.0f - s), du, s);
+        return z * s;
+    }
+    if (inner == MP_ACT_RELU) {
+        slope = z > 0.0f ? 1.0f : 0.0f;
+        return z < 0.0f ? 0.0f : z;
+    }
+    slope = 1.0f;
+    return z;
+}
+
+// ---------------------------------------------------------------------------
+// 32 consecutive bf16 values of a row: 32-byte accesses where the address
+// allows, else 16-byte ones, else single elements.  `n` of the 32 exist.
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ void unpack16(const u32x8 &v, float *f)
+{
+    float t[8];
+    unpack(v.a, t);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = t[i];
+    unpack(v.b, t);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[8 + i] = t[i];
+}
+
+__device__ __forceinline__ uint4 pack8(const float *f)
+{
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+}
+
+__device__ __forceinline__ unsigned low_bits(const void *p)
+{
+    return static_cast<unsigned>(reinterpret_cast<uintptr_t>(p)) & 31u;
+}
+
+__device__ __forceinline__ void load32(const mp_bf16_t *p, int n, float (&f)[EPI_COLS])
+{
+    const unsigned low = low_bits(p);
+    if (n >= EPI_COLS && low == 0) {
+        const u32x8 *q = reinterpret_cast<const u32x8 *>(p);
+        const u32x8 v0 = ld_stream(q), v1 = ld_stream(q + 1);
+        unpack16(v0, f);
+        unpack16(v1, f + 16);
+    } else if (n >= EPI_COLS && (low & 15u) == 0) {
+        const uint4 *q = reinterpret_cast<const uint4 *>(p);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float t[8];
+            unpack(ld_stream(q + j), t);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[8 * j + i] = t[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < EPI_COLS; ++i) {
+            float t[1] = {0.0f};
+            if (i < n) unpack(ld_stream(p + i), t);
+            f[i] = t[0];
+        }
+    }
+}
+
+__device__ __forceinline__ void store32(mp_bf16_t *p, int n, const float (&f)[EPI_COLS])
+{
+    const unsigned low = low_bits(p);
+    if (n >= EPI_COLS && low == 0) {
+        u32x8 *q = reinterpret_cast<u32x8 *>(p);
+        st_row(q, u32x8{pack8(f), pack8(f + 8)});
+        st_row(q + 1, u32x8{pack8(f + 16), pack8(f + 24)});
+    } else if (n >= EPI_COLS && (low & 15u) == 0) {
+        uint4 *q = reinterpret_cast<uint4 *>(p);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = pack8(f + 8 * j);
+    } else {
+#pragma unroll
+        for (int i = 0; i < EPI_COLS; ++i)
+            if (i < n) {
+                const float t[1] = {f[i]};
+                p[i] = pack(t);
+            }
+    }
+}
+
+// fp32 weight gradients, added to what is there if `add`.
+__device__ __forceinline__ void store32_f32(float *p, int n, const float (&f)[EPI_COLS], bool add)
+{
+    if (n >= EPI_COLS && (low_bits(p) & 15u) == 0) {
+        float4 *q = reinterpret_cast<float4 *>(p);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float4 v = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+            if (add) {
+                const float4 o = q[j];
+                v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+            }
+            q[j] = v;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < EPI_COLS; ++i)
+            if (i < n) p[i] = add ? p[i] + f[i] : f[i];
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The 8-bit checkpoint: per row and 32 columns one power of two 2^(x-127), the
+// smallest for which the block's largest finite magnitude is at most 448 of
+// them, and e4m3 codes.  Powers of two make the scaling exact, so a value is
+// rounded once, by at most half a step of e4m3 (2^-4 relative, 2^-10 of the
+// unit below 2^-6 units).  What is not finite is stored as e4m3's NaN.
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ int ckpt_exponent(float big)
+{
+    // big = m 2^k, 1 <= m < 2: 448 = 1.75 * 2^8, so the unit is 2^(k-8), or
+    // one more where m > 1.75.
+    const uint32_t u = __float_as_uint(big);
+    const int x = static_cast<int>(u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return x < 1 ? 1 : x;
+}
+
+__device__ __forceinline__ float pow2_biased(int x) { return __uint_as_float(static_cast<uint32_t>(x) << 23); }
+
+__device__ __forceinline__ float finite_or_nan(float z) { return fmaf(z, 0.0f, z); }
+
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
+{
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+
+__device__ __forceinline__ void e4m3x4_values(uint32_t u, float *f)
+{
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(
+            static_cast<__nv_fp8x2_storage_t>(u >> (16 * j)), __NV_E4M3);
+        const float2 v = __half22float2(__half2(r));
+        f[2 * j] = v.x;
+        f[2 * j + 1] = v.y;
+    }
+}
+
+__device__ __forceinline__ void ckpt_write32(uint8_t *codes, uint8_t *exponent, int n,
+                                             const float (&z)[EPI_COLS])
+{
+    float big = 0.0f;
+#pragma unroll
+    for (int i = 0; i < EPI_COLS; ++i)
+        if (i < n) big = fmaxf(big, fabsf(finite_or_nan(z[i])));   // fmaxf passes NaN over
+    const int x = ckpt_exponent(big);
+    const float inv = pow2_biased(254 - x);
+    uint32_t c[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        c[j] = e4m3x4(finite_or_nan(z[4 * j]) * inv, finite_or_nan(z[4 * j + 1]) * inv,
+                      finite_or_nan(z[4 * j + 2]) * inv, finite_or_nan(z[4 * j + 3]) * inv);
+    const unsigned low = low_bits(codes);
+    if (n >= EPI_COLS && low == 0) {
+        st_row(reinterpret_cast<u32x8 *>(codes),
+               u32x8{make_uint4(c[0], c[1], c[2], c[3]), make_uint4(c[4], c[5], c[6], c[7])});
+    } else if (n >= EPI_COLS && (low & 7u) == 0) {
+        uint2 *q = reinterpret_cast<uint2 *>(codes);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = make_uint2(c[2 * j], c[2 * j + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < EPI_COLS; ++i)
+            if (i < n) codes[i] = static_cast<uint8_t>(c[i / 4] >> (8 * (i % 4)));
+    }
+    *exponent = static_cast<uint8_t>(x);
+}
+
+__device__ __forceinline__ void ckpt_read32(const uint8_t *codes, const uint8_t *exponent, int n,
+                                            float (&z)[EPI_COLS])
+{
+    const float unit = pow2_biased(__ldg(exponent));
+    const unsigned low = low_bits(codes);
+    uint32_t c[8];
+    if (n >= EPI_COLS && low == 0) {
+        const u32x8 v = ld_stream(reinterpret_cast<const u32x8 *>(codes));
+        c[0] = v.a.x; c[1] = v.a.y; c[2] = v.a.z; c[3] = v.a.w;
+        c[4] = v.b.x; c[5] = v.b.y; c[6] = v.b.z; c[7] = v.b.w;
+    } else if (n >= EPI_COLS && (low & 7u) == 0) {
+        const uint2 *q = reinterpret_cast<const uint2 *>(codes);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint2 v = __ldg(q + j);
+            c[2 * j] = v.x;
+            c[2 * j + 1] = v.y;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            c[j] = 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (4 * j + i < n) c[j] |= static_cast<uint32_t>(__ldg(codes + 4 * j + i)) << (8 * i);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) e4m3x4_values(c[j], z + 4 * j);
+#pragma unroll
+    for (int i = 0; i < EPI_COLS; ++i) z[i] *= unit;
+}
+
+// ---------------------------------------------------------------------------
+// Epilogues, on 32 columns of one row in fp32.
+// ---------------------------------------------------------------------------
+
+struct ExpertEpi {
+    int act, save;            // MP_ACT_*, MP_SAVE_*
+    int cols;                 // columns of a part: of out (FWD), g_x's part (DGRAD), g_w (WGRAD)
+    const mp_bf16_t *bias;    // FWD: [E, parts*cols] or NULL
+    const mp_bf16_t *residual;
+    mp_bf16_t *out;           // FWD: [R,cols]; DGRAD: [R, parts*cols]; WGRAD: [E,N,cols]
+    void *z;                  // checkpoint [R, parts*cols]: written (FWD), read (DGRAD)
+    uint8_t *z_exp;           // [R, parts*ckpt_blocks(cols)]
+    mp_bf16_t *h;             // DGRAD: act(z) [R,cols] or NULL
+    float *out_f32;           // WGRAD: fp32 gradient in place of `out`
+    bool add;                 // WGRAD: add to out_f32
+};
+
+__device__ __forceinline__ void save32(const ExpertEpi &p, int64_t row, int part, int parts, int c,
+                                       int n, const float (&z)[EPI_COLS])
+{
+    const int64_t at = (row * parts + part) * p.cols + c;
+    if (p.save == MP_SAVE_BF16)
+        store32(static_cast<mp_bf16_t *>(p.z) + at, n, z);
+    else
+        ckpt_write32(static_cast<uint8_t *>(p.z) + at,
+                     p.z_exp + (row * parts + part) * ckpt_blocks(p.cols) + c / EPI_COLS, n, z);
+}
+
+__device__ __forceinline__ void read32(const ExpertEpi &p, int64_t row, int part, int parts, int c,
+                                       int n, float (&z)[EPI_COLS])
+{
+    const int64_t at = (row * parts + part) * p.cols + c;
+    if (p.save == MP_SAVE_BF16)
+        load32(static_cast<const mp_bf16_t *>(p.z) + at, n, z);
+    else
+        ckpt_read32(static_cast<const uint8_t *>(p.z) + at,
+                    p.z_exp + (row * parts + part) * ckpt_blocks(p.cols) + c / EPI_COLS, n, z);
+}
+
+__device__ __forceinline__ void add_bias32(const mp_bf16_t *b, int n, float (&z)[EPI_COLS])
+{
+    float f[EPI_COLS];
+    load32(b, n, f);
+#pragma unroll
+    for (int i = 0; i < EPI_COLS; ++i) z[i] += f[i];
+}
+
+// z: the product's columns c..c+31 (of the gate when GATED, u then the others').
+template <bool GATED>
+__device__ __forceinline__ void epi_fwd(const ExpertEpi &p, int e, int64_t row, int c, int n,
+                                        float (&z)[EPI_COLS], float (&u)[EPI_COLS])
+{
+    constexpr int parts = GATED ? 2 : 1;
+    if (p.bias != nullptr) {
+        const mp_bf16_t *b = p.bias + static_cast<int64_t>(e) * parts * p.cols + c;
+        add_bias32(b, n, z);
+        if (GATED) add_bias32(b + p.cols, n, u);
+    }
+    if (p.save != MP_SAVE_NONE) {
+        save32(p, row, 0, parts, c, n, z);
+        if (GATED) save32(p, row, 1, parts, c, n, u);
+    }
+    const int inner = act_inner(p.act);
+    if (inner != MP_ACT_NONE) {
+#pragma unroll
+        for (int i = 0; i < EPI_COLS; ++i) {
+            z[i] = act_value(z[i], inner);
+            if (GATED) z[i] *= u[i];
+        }
+    }
+    if (p.residual != nullptr) {
+        float f[EPI_COLS];
+        load32(p.residual + row * p.cols + c, n, f);
+#pragma unroll
+        for (int i = 0; i < EPI_COLS; ++i) z[i] += f[i];
+    }
+    store32(p.out + row * p.cols + c, n, z);
+}
+
+// g: the gradient of act's result.
+__device__ __forceinline__ void epi_dgrad(const ExpertEpi &p, int64_t row, int c, int n,
+                                          float (&g)[EPI_COLS])
+{
+    if (p.act == MP_ACT_NONE) {
+        store32(p.out + row * p.cols + c, n, g);
+        return;
+    }
+    const int inner = act_inner(p.act);
+    float z[EPI_COLS], h[EPI_COLS];
+    if (act_gated(p.act)) {
+        float u[EPI_COLS];
+        read32(p, row, 0, 2, c, n, z);
+        read32(p, row, 1, 2, c, n, u);
+#pragma unroll
+        for (int i = 0; i < EPI_COLS; ++i) {
+            float slope;
+            const float a = act_value_slope(z[i], inner, slope);
+            h[i] = a * u[i];
+            z[i] = g[i] * u[i] * slope;
+            u[i] = g[i] * a;
+        }
+        store32(p.out + (row * 2 + 1) * p.cols + c, n, u);
+        store32(p.out + row * 2 * p.cols + c, n, z);
+    } else {
+        read32(p, row, 0, 1, c, n, z);
+#pragma unroll
+        for (int i = 0; i < EPI_COLS; ++i) {
+            float slope;
+            h[i] = act_value_slope(z[i], inner, slope);
+            z[i] = g[i] * slope;
+        }
+        store32(p.out + row * p.cols + c, n, z);
+    }
+    if (p.h != nullptr) store32(p.h + row * p.cols + c, n, h);
+}
+
+__device__ __forceinline__ void epi_wgrad(const ExpertEpi &p, int64_t row, int c, int n,
+                                          const float (&g)[EPI_COLS])
+{
+    if (p.out_f32 != nullptr)
+        store32_f32(p.out_f32 + row * p.cols + c, n, g, p.add);
+    else
+        store32(p.out + row * p.cols + c, n, g);
+}
+
+// ---------------------------------------------------------------------------
+// Where each expert's rows start, clamped to [0,R] and made non-decreasing, so
+// that no offset can lead outside a buffer; anything else sets a status bit.
+// One warp fills start[0..E] and tiles[0..E] (tiles before each expert, of
+// `tile_rows` rows).
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ void expert_starts(const int32_t *offsets, int E, int R, int tile_rows,
+                                              int lane, int *start, int *tiles, int32_t *status)
+{
+    int high = 0, before = 0;
+    bool bad = false;
+    for (int base = 0; base <= E; base += 32) {
+        const int e = base + lane;
+        const int given = e <= E ? __ldg(offsets + e) : 0;
+        int v = min(max(given, 0), R);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(FULL_MASK, v, d);
+            if (lane >= d) v = max(v, o);
+        }
+        v = max(v, high);
+        bad |= e <= E && v != given;
+        int prev = __shfl_up_sync(FULL_MASK, v, 1);
+        if (lane == 0) prev = high;
+        // Tiles of expert e-1, whose rows are [prev, v).
+        int n = (e >= 1 && e <= E) ? (v - prev + tile_rows - 1) / tile_rows : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(FULL_MASK, n, d);
+            if (lane >= d) n += o;
+        }
+        n += before;
+        if (e <= E) {
+            start[e] = v;
+            tiles[e] = n;
+        }
+        high = __shfl_sync(FULL_MASK, v, 31);
+        before = __shfl_sync(FULL_MASK, n, 31);
+    }
+    if (status != nullptr && __any_sync(FULL_MASK, bad) && lane == 0)
+        or_status(status, MP_STATUS_BAD_OFFSETS);
+}
+
+// The expert of row tile t: tiles[e] <= t < tiles[e+1].
+__device__ __forceinline__ int expert_of_tile(const int *tiles, int E, int t)
+{
+    int lo = 0, hi = E - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (tiles[mid + 1] > t)
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    return lo;
+}
+
+// Launchers of the forms of the products (expert_*.cu).
+struct ExpertCall {
+    const mp_bf16_t *a, *b;   // FWD: x, w; DGRAD: g, w; WGRAD: g, x
+    const int32_t *offsets;
+    int R, E, N, K;           // w is [E,N,K]
+    ExpertEpi epi;
+    int32_t *status;
+    cudaStream_t stream;
+};
+
+template <int MODE> mp_status_t expert_simt(const ExpertCall &c);
+
+}  // namespace mp
