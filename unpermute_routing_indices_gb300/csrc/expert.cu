@@ -49,6 +49,11 @@ mp_status_t sizes_ok(int64_t R, int32_t E, int32_t N, int32_t K)
     return MP_OK;
 }
 
+template <int MODE> mp_status_t product(const ExpertCall &c)
+{
+    return expert_tc_takes<MODE>(c) ? expert_tc<MODE>(c) : expert_simt<MODE>(c);
+}
+
 bool act_ok(int32_t act) { return act >= MP_ACT_NONE && act <= MP_ACT_SWIGLU; }
 
 }  // namespace
@@ -79,7 +84,7 @@ extern "C" mp_status_t mp_expert_gemm(const mp_bf16_t *x, const mp_bf16_t *w,
     c.epi.z = z; c.epi.z_exp = z_exp;
     c.status = dev_status;
     c.stream = as_stream(stream);
-    return expert_simt<FWD>(c);
+    return product<FWD>(c);
 }
 
 extern "C" mp_status_t mp_expert_dgrad(const mp_bf16_t *g, const mp_bf16_t *w,
@@ -105,7 +110,7 @@ extern "C" mp_status_t mp_expert_dgrad(const mp_bf16_t *g, const mp_bf16_t *w,
     c.epi.z = const_cast<void *>(z); c.epi.z_exp = const_cast<uint8_t *>(z_exp);
     c.status = dev_status;
     c.stream = as_stream(stream);
-    return expert_simt<DGRAD>(c);
+    return product<DGRAD>(c);
 }
 
 extern "C" mp_status_t mp_expert_wgrad(const mp_bf16_t *g, const mp_bf16_t *x,
@@ -129,7 +134,7 @@ extern "C" mp_status_t mp_expert_wgrad(const mp_bf16_t *g, const mp_bf16_t *x,
     c.epi.add = accumulate != 0;
     c.status = dev_status;
     c.stream = as_stream(stream);
-    const mp_status_t s = expert_simt<WGRAD>(c);
+    const mp_status_t s = product<WGRAD>(c);
     if (s != MP_OK || g_bias == nullptr) return s;
     (void)launch_pdl(k_expert_bias, dim3((N + 31) / 32, E), BIAS_THREADS, 0, c.stream, g, offsets,
                      c.R, E, N, f32 ? nullptr : static_cast<mp_bf16_t *>(g_bias),

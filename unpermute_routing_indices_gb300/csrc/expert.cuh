@@ -464,6 +464,8 @@ struct ExpertCall {
     cudaStream_t stream;
 };
 
-template <int MODE> mp_status_t expert_simt(const ExpertCall &c);
+template <int MODE> mp_status_t expert_simt(const ExpertCall &c);   // any width, any alignment
+template <int MODE> bool expert_tc_takes(const ExpertCall &c);      // TMA's rules hold
+template <int MODE> mp_status_t expert_tc(const ExpertCall &c);
 
 }  // namespace mp
