@@ -4,14 +4,23 @@
 //   s_e = softmax(l)_e or sigmoid(l_e);  c_e = s_e + b_e decides the choice
 //   weights: scale * s_k / sum_j s_j (renorm) or scale * s_k
 //
-// k_route: one warp per token; lane l holds the experts l, l+32, ...  The choice
-// is made in 64 bits, where scores next to each other stay apart; the weights
-// are fp32.
+// k_route: one warp per token; lane l holds the experts l, l+32, ...
+// Choice.  Without a bias the scores rise with the logits, which are compared
+// as they are.  With one, and for the sum of a group's best two, fp32 values of
+// c decide wherever neighbours in the order are further apart than their errors
+// can be (`margin`); a token where two are nearer (about one of a thousand of
+// normal logits) is decided again in 64 bits (choose_exact).  So the choice is
+// that of 64 bits everywhere, at the cost of 32: on 32,768 tokens of 256 experts
+// (sigmoid, bias, 8 groups), all of it in 64 bits took 1,290 us, this 58.
+// Each lane sorts its candidates by a fixed network and a round takes the best
+// head of the warp (topk.cuh); the round after the K-th says how near the best
+// of the rest is.
+// Weights are fp32 from the picks' own logits.
+// k_route_bwd: one warp per token; every gradient is written once.
 #include <cfloat>
-#include <climits>
 #include <cuda_fp16.h>
 
-#include "common.cuh"
+#include "topk.cuh"
 
 namespace mp {
 namespace {
@@ -24,6 +33,7 @@ struct RouteArgs {
     const float *bias;
     int64_t T;
     int E, K, score, n_groups, topk_groups, group_top, renorm;
+    uint32_t group_magic;   // ceil(2^32 / experts a group): (e * magic) >> 32 is e's group
     float scale;
     int32_t *idx;
     float *weights;
@@ -35,6 +45,9 @@ __device__ __forceinline__ float logit(const __nv_bfloat16 *p)
     return __uint_as_float(static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t *>(p))) << 16);
 }
 __device__ __forceinline__ float logit(const __half *p) { return __half2float(__ldg(p)); }
+__device__ __forceinline__ float logit_value(float v) { return v; }
+__device__ __forceinline__ float logit_value(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float logit_value(__half v) { return __half2float(v); }
 
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
@@ -53,31 +66,81 @@ template <typename F> __device__ __forceinline__ F warp_sum(F v)
     return v;
 }
 
-// Arg-max of (value desc, index asc) across the warp; index INT_MAX: no candidate.
-__device__ __forceinline__ void warp_argmax(double &v, int &i)
+using mp::key_value;
+using mp::order_key;
+using mp::warp_argmax_key;
+
+// order_key in 64 bits: 0 stands for no candidate.
+__device__ __forceinline__ uint64_t order_key(double d)
+{
+    const uint64_t u = static_cast<uint64_t>(__double_as_longlong(d + 0.0));   // -0 becomes +0
+    return u ^ (static_cast<uint64_t>(static_cast<int64_t>(u) >> 63) | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double key_value(uint64_t k)
+{
+    return __longlong_as_double(
+        static_cast<int64_t>((k >> 63) ? k & 0x7fffffffffffffffull : ~k));
+}
+// Arg-max on (key desc, index asc); every lane gets both.
+__device__ __forceinline__ uint32_t warp_argmax_key(uint64_t &key, uint32_t idx)
+{
+    const uint32_t hi = static_cast<uint32_t>(key >> 32), lo = static_cast<uint32_t>(key);
+    const uint32_t mh = __reduce_max_sync(FULL_MASK, hi);
+    const uint32_t ml = __reduce_max_sync(FULL_MASK, hi == mh ? lo : 0u);
+    const uint32_t i = __reduce_min_sync(FULL_MASK, hi == mh && lo == ml ? idx : 0xffffffffu);
+    key = static_cast<uint64_t>(mh) << 32 | ml;
+    return i;
+}
+
+// The same over lanes 0..K-1 of a token of KT picks (0: any): with KT a power of
+// two below 32, lanes 0..KT-1 reduce among themselves.
+template <int KT> __device__ __forceinline__ float pick_max(float v)
 {
 #pragma unroll
-    for (int d = 16; d; d >>= 1) {
-        const double ov = __shfl_xor_sync(FULL_MASK, v, d);
-        const int oi = __shfl_xor_sync(FULL_MASK, i, d);
-        if (oi != INT_MAX && (i == INT_MAX || ov > v || (ov == v && oi < i))) {
-            v = ov;
-            i = oi;
-        }
-    }
+    for (int d = KT > 0 ? KT / 2 : 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(FULL_MASK, v, d));
+    return v;
+}
+template <int KT> __device__ __forceinline__ float pick_sum(float v)
+{
+#pragma unroll
+    for (int d = KT > 0 ? KT / 2 : 16; d; d >>= 1) v += __shfl_xor_sync(FULL_MASK, v, d);
+    return v;
 }
 
 // A logit that can be chosen: not -inf and not NaN (an unavailable expert);
 // +inf counts as the largest finite value.
 __device__ __forceinline__ bool usable(float v) { return v > -INFINITY; }
 
-// The choice in 64 bits.  `live`: bit j for expert lane + 32 j.  Lane k gets
-// pick k (-1: none left).
-template <int PER>
-__device__ __forceinline__ int choose_exact(const RouteArgs &a, const float (&v)[PER],
-                                            const float (&b)[PER], unsigned have, unsigned live,
-                                            int lane)
+
+// The token's logits and biases: expert lane + 32 j in slot j; bit j of `have`:
+// it has a logit, of `live`: it can be chosen.
+template <typename L, int PER>
+__device__ __forceinline__ void load_token(const RouteArgs &a, const L *l, int lane, float (&v)[PER],
+                                           float (&b)[PER], unsigned &have, unsigned &live)
 {
+    have = live = 0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int e = lane + 32 * j;
+        v[j] = e < a.E ? logit(l + e) : -INFINITY;
+        b[j] = (e < a.E && a.bias != nullptr) ? __ldg(a.bias + e) : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const bool u = usable(v[j]);   // false for NaN too
+        have |= static_cast<unsigned>(u) << j;
+        live |= static_cast<unsigned>(u && usable(b[j])) << j;
+        v[j] = u ? fminf(v[j], FLT_MAX) : -INFINITY;
+    }
+}
+
+// The choice in 64 bits.  Lane k gets pick k (-1: none left).
+template <typename L, int PER>
+__device__ __noinline__ int choose_exact(const RouteArgs &a, const L *l, int lane)
+{
+    float v[PER], b[PER];
+    unsigned have, live;
+    load_token<L, PER>(a, l, lane, v, b, have, live);
     double c[PER];
     if (a.score == MP_SCORE_SIGMOID) {
 #pragma unroll
@@ -102,70 +165,305 @@ __device__ __forceinline__ int choose_exact(const RouteArgs &a, const float (&v)
 #pragma unroll
         for (int j = 0; j < PER; ++j) c[j] += static_cast<double>(b[j]);
 
-    if (a.n_groups > 1) {
-        const int per_group = a.E / a.n_groups;
-        double worth = 0.0;          // lane g: group g's
-        int mine = INT_MAX;          // lane g: g, if the group has an expert
-        for (int g = 0; g < a.n_groups; ++g) {
-            double total = 0.0;
-            int first = INT_MAX;
-            for (int r = 0; r < a.group_top; ++r) {
-                double bv = 0.0;
-                int bi = INT_MAX;
+    uint64_t key[PER];
 #pragma unroll
-                for (int j = 0; j < PER; ++j) {
-                    const int e = lane + 32 * j;
-                    if ((live >> j & 1u) && e / per_group == g && e != first &&
-                        (bi == INT_MAX || c[j] > bv)) {
-                        bv = c[j];
-                        bi = e;
-                    }
-                }
-                warp_argmax(bv, bi);
-                if (bi != INT_MAX) total += bv;
-                if (r == 0) first = bi;
+    for (int j = 0; j < PER; ++j) key[j] = (live >> j & 1u) ? order_key(c[j]) : 0ull;
+    if (a.n_groups > 1) {
+        uint64_t worth = 0ull;   // lane g: group g's
+        for (int g = 0; g < a.n_groups; ++g) {
+            uint64_t k1 = 0ull, k2 = 0ull;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                const uint64_t k = __umulhi(lane + 32 * j, a.group_magic) == g ? key[j] : 0ull;
+                k2 = max(k2, min(k, k1));
+                k1 = max(k1, k);
             }
-            if (lane == g) {
-                worth = total;
-                mine = first == INT_MAX ? INT_MAX : g;
+            uint64_t w = k1;
+            const uint32_t holder = warp_argmax_key(w, static_cast<uint32_t>(lane));
+            if (a.group_top == 2) {
+                uint64_t m2 = lane == holder ? k2 : k1;
+                (void)warp_argmax_key(m2, static_cast<uint32_t>(lane));
+                if (m2 != 0ull) w = order_key(key_value(w) + key_value(m2));
             }
+            if (lane == g) worth = w;
         }
         unsigned kept = 0;
         for (int r = 0; r < a.topk_groups; ++r) {
-            double bv = worth;
-            int bi = (mine != INT_MAX && !(kept >> lane & 1u)) ? mine : INT_MAX;
-            warp_argmax(bv, bi);
-            if (bi != INT_MAX) kept |= 1u << bi;
+            uint64_t wk = (kept >> lane & 1u) ? 0ull : worth;
+            const uint32_t g = warp_argmax_key(wk, static_cast<uint32_t>(lane));
+            if (wk != 0ull) kept |= 1u << g;
         }
 #pragma unroll
         for (int j = 0; j < PER; ++j)
-            if ((live >> j & 1u) && !(kept >> ((lane + 32 * j) / per_group) & 1u)) live &= ~(1u << j);
+            if (!(kept >> (__umulhi(lane + 32 * j, a.group_magic) & 31) & 1u)) live &= ~(1u << j);
     }
     // Without a bias the scores rise with the logits, which stay apart where
     // scores round to one value.
-    if (a.bias == nullptr)
 #pragma unroll
-        for (int j = 0; j < PER; ++j) c[j] = static_cast<double>(v[j]);
+    for (int j = 0; j < PER; ++j)
+        key[j] = !(live >> j & 1u)   ? 0ull
+                 : a.bias == nullptr ? order_key(static_cast<double>(v[j]))
+                                     : key[j];
     int pick = -1;
     for (int k = 0; k < a.K; ++k) {
-        double bv = 0.0;
-        int bi = INT_MAX;
+        uint64_t bk = 0ull;
+        uint32_t bi = 0xffffffffu;
 #pragma unroll
         for (int j = 0; j < PER; ++j)
-            if ((live >> j & 1u) && (bi == INT_MAX || c[j] > bv)) {
-                bv = c[j];
-                bi = lane + 32 * j;
+            if (key[j] > bk) {
+                bk = key[j];
+                bi = static_cast<uint32_t>(lane + 32 * j);
             }
-        warp_argmax(bv, bi);
-        if (bi == INT_MAX) break;
-        if ((bi & 31) == lane) live &= ~(1u << (bi >> 5));
-        if (lane == k) pick = bi;
+        const uint32_t p = warp_argmax_key(bk, bi);
+        if (bk == 0ull) break;
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            if (lane + 32 * j == p) key[j] = 0ull;
+        if (lane == k) pick = static_cast<int>(p);
     }
     return pick;
 }
 
-template <typename L, int PER>
-__global__ void __launch_bounds__(RT_THREADS) k_route(const RouteArgs a)
+// 2^(x log2 e) and 1/x of the special function unit: within 2 ulp, plus the
+// rounding of the argument.
+__device__ __forceinline__ float exp_fast(float x) { return __expf(x); }
+__device__ __forceinline__ float rcp_fast(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ void into_top2(uint32_t k, uint32_t &k1, uint32_t &k2)
+{
+    k2 = max(k2, min(k, k1));
+    k1 = max(k1, k);
+}
+
+// Picks by 32-bit keys, 0 for none.  Lane k gets pick k's key and expert; `rest`
+// and `rest_i` are those of the best of the rest.
+template <int N, int KT>
+__device__ __forceinline__ void rounds(uint32_t (&key)[N], uint32_t (&ex)[N], int K, int lane,
+                                       uint32_t &my_key, int &my_i, uint32_t &rest, uint32_t &rest_i)
+{
+    sort_desc<N>(key, ex);
+    if (KT > 0) K = KT;
+#pragma unroll
+    for (int k = 0; k < (KT > 0 ? KT : K); ++k) {
+        uint32_t bk = key[0];
+        const uint32_t pick = warp_argmax_key(bk, ex[0]);
+        if (ex[0] == pick) {
+#pragma unroll
+            for (int j = 0; j + 1 < N; ++j) {
+                key[j] = key[j + 1];
+                ex[j] = ex[j + 1];
+            }
+            key[N - 1] = 0u;
+        }
+        if (lane == k) {
+            my_key = bk;
+            my_i = static_cast<int>(pick);
+        }
+    }
+    rest = key[0];
+    rest_i = warp_argmax_key(rest, ex[0]);
+}
+
+// Whether two values next to each other in a descending order, each off by at
+// most err + 2^-24 of its magnitude, may belong the other way round.
+__device__ __forceinline__ bool too_near(uint32_t key, uint32_t next, float err)
+{
+    if (key == 0u || next == 0u) return false;
+    const float c = key_value(key), d = key_value(next);
+    return !(c - d > 2.0f * err + 6.0e-8f * (fabsf(c) + fabsf(d)));
+}
+
+// The choice from fp32 values; false (in every lane): too near to tell.
+template <typename L, int PER, int KT>
+__device__ __forceinline__ bool choose_fast(const RouteArgs &a, const L *l, const float (&v)[PER],
+                                            const float (&b)[PER], unsigned have, unsigned live,
+                                            int lane, int &pick)
+{
+    const int K = KT > 0 ? KT : a.K;
+    const bool by_logit = a.bias == nullptr;
+    const bool pairs = a.n_groups > 1 && a.group_top == 2;
+    uint32_t key[PER];
+    float err = 0.0f;   // absolute error of a score
+    bool near = false;
+    if (!by_logit || pairs) {
+        // sigmoid: exp within (2 + |v|) ulp, its share of the result s (1 - s),
+        // then a sum and a reciprocal: 3e-7 of 1.  softmax: the largest score
+        // times the same, the argument's rounding and the sum of E terms.
+        float c[PER];
+        if (a.score == MP_SCORE_SIGMOID) {
+            err = 4e-7f;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) c[j] = rcp_fast(1.0f + exp_fast(-v[j]));
+        } else {
+            float m = -INFINITY, sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) m = fmaxf(m, v[j]);
+            m = warp_max(m);
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                c[j] = (have >> j & 1u) ? exp_fast(v[j] - m) : 0.0f;
+                sum += c[j];
+            }
+            const float inv = rcp_fast(warp_sum(sum));
+            err = inv * (8e-7f + (PER + 6) * 6e-8f);
+#pragma unroll
+            for (int j = 0; j < PER; ++j) c[j] *= inv;
+        }
+#pragma unroll
+        for (int j = 0; j < PER; ++j) key[j] = (live >> j & 1u) ? order_key(c[j] + b[j]) : 0u;
+    } else {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) key[j] = (live >> j & 1u) ? order_key(v[j]) : 0u;
+    }
+
+    if (a.n_groups > 1) {
+        const int per_group = a.E / a.n_groups;
+        const bool columns = per_group % 32 == 0;   // a group is whole slots
+        uint32_t worth = 0u;                        // lane g: group g's, as a key,
+        float size = 0.0f;                          // and the magnitudes it is the sum of
+        // Group g's worth from each lane's best two of it.
+        const auto finish = [&](int g, uint32_t k1, uint32_t k2) {
+            uint32_t w = __reduce_max_sync(FULL_MASK, k1);
+            float sz = 0.0f;
+            if (a.group_top == 2) {
+                const int holder = __ffs(__ballot_sync(FULL_MASK, k1 == w)) - 1;
+                const uint32_t m2 = __reduce_max_sync(FULL_MASK, lane == holder ? k2 : k1);
+                if (m2 != 0u) {
+                    w = order_key(key_value(w) + key_value(m2));
+                    sz = fabsf(key_value(w)) + 2.0f * fabsf(key_value(m2));
+                }
+            }
+            if (lane == g) {
+                worth = w;
+                size = sz;
+            }
+        };
+        if (columns) {
+            const int slots = per_group / 32;
+            uint32_t k1 = 0u, k2 = 0u;
+            int n = 0, g = 0;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                into_top2(key[j], k1, k2);
+                if (++n == slots && g < a.n_groups) {
+                    finish(g, k1, k2);
+                    k1 = k2 = 0u;
+                    n = 0;
+                    ++g;
+                }
+            }
+        } else {
+            for (int g = 0; g < a.n_groups; ++g) {
+                uint32_t k1 = 0u, k2 = 0u;
+#pragma unroll
+                for (int j = 0; j < PER; ++j)
+                    into_top2(__umulhi(lane + 32 * j, a.group_magic) == g ? key[j] : 0u, k1, k2);
+                finish(g, k1, k2);
+            }
+        }
+        unsigned kept = 0;
+        uint32_t last = 0u;
+        float last_size = 0.0f;
+        for (int r = 0; r <= a.topk_groups; ++r) {
+            uint32_t wk = (kept >> lane & 1u) ? 0u : worth;
+            const uint32_t g = warp_argmax_key(wk, static_cast<uint32_t>(lane));
+            const float sz = __shfl_sync(FULL_MASK, size, g);
+            // Only the last one kept and the first one left out must stand apart.
+            if (r == a.topk_groups)
+                near = err > 0.0f && too_near(last, wk, 2.0f * err + 6.0e-8f * (last_size + sz));
+            else if (wk != 0u)
+                kept |= 1u << g;
+            last = wk;
+            last_size = sz;
+        }
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const uint32_t g = __umulhi(lane + 32 * j, a.group_magic);
+            if (!(kept >> (g & 31) & 1u)) live &= ~(1u << j);
+        }
+    }
+    // Keys of what is left; without a bias the logits' own.
+    uint32_t ex[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        ex[j] = static_cast<uint32_t>(lane + 32 * j);
+        key[j] = !(live >> j & 1u) ? 0u : (by_logit && pairs) ? order_key(v[j]) : key[j];
+    }
+    uint32_t my_key = 0u, rest = 0u, rest_i = 0u;
+    int my_i = -1;
+    if constexpr (PER <= 8) {
+        const unsigned cols = __reduce_or_sync(FULL_MASK, live);
+        if (PER >= 4 && __popc(cols) <= PER / 2) {
+            constexpr int HALF = PER >= 4 ? PER / 2 : 1;
+            uint32_t kc[HALF], xc[HALF];
+#pragma unroll
+            for (int i = 0; i < HALF; ++i) {
+                kc[i] = 0u;
+                xc[i] = 0xffffffffu;
+            }
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                if (cols >> j & 1u) {
+#pragma unroll
+                    for (int i = HALF - 1; i > 0; --i) {
+                        kc[i] = kc[i - 1];
+                        xc[i] = xc[i - 1];
+                    }
+                    kc[0] = key[j];
+                    xc[0] = ex[j];
+                }
+            rounds<HALF, KT>(kc, xc, K, lane, my_key, my_i, rest, rest_i);
+        } else {
+            rounds<PER, KT>(key, ex, K, lane, my_key, my_i, rest, rest_i);
+        }
+    } else {
+        // More than 256 experts: each round looks through the lane's own again.
+        for (int k = 0; k <= K; ++k) {
+            uint32_t bk = 0u, bi = 0xffffffffu;
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                if (key[j] > bk) {
+                    bk = key[j];
+                    bi = ex[j];
+                }
+            const uint32_t p = warp_argmax_key(bk, bi);
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                if (ex[j] == p) key[j] = 0u;
+            if (lane == k && k < K) {
+                my_key = bk;
+                my_i = static_cast<int>(p);
+            }
+            rest = bk;
+            rest_i = p;
+        }
+    }
+    pick = (lane < K && my_key != 0u) ? my_i : -1;
+    if (!by_logit) {
+        // Neighbours of the same logit and bias are equal in any arithmetic,
+        // and stand in the order of their indices already.
+        uint32_t next = __shfl_down_sync(FULL_MASK, my_key, 1);
+        uint32_t next_i = __shfl_down_sync(FULL_MASK, static_cast<uint32_t>(my_i), 1);
+        if (lane == K - 1) {
+            next = rest;
+            next_i = rest_i;
+        }
+        if (lane < K && too_near(my_key, next, err))
+            near |= !(logit(l + my_i) == logit(l + next_i) && __ldg(a.bias + my_i) == __ldg(a.bias + next_i));
+    }
+    return __all_sync(FULL_MASK, !near);
+}
+
+// KT > 0: a form for K = KT with the rounds unrolled.  Compiled for 4 CTAs per
+// SM up to 256 experts: 32,768 x 256 tokens (sigmoid, bias, 8 groups) 59.0 us
+// with 3, 58.1 with 4; the same without groups 41.4 and 38.7.
+template <typename L, int PER, int KT>
+__global__ void __launch_bounds__(RT_THREADS, PER <= 8 ? 4 : 1) k_route(const RouteArgs a)
 {
     pdl_trigger();
     pdl_wait();
@@ -174,25 +472,16 @@ __global__ void __launch_bounds__(RT_THREADS) k_route(const RouteArgs a)
     if (t >= a.T) return;   // whole warps leave together
     const L *l = static_cast<const L *>(a.logits) + t * a.E;
     float v[PER], b[PER];
-    unsigned have = 0, live = 0;   // has a logit; can be chosen
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        const int e = lane + 32 * j;
-        v[j] = e < a.E ? fminf(logit(l + e), FLT_MAX) : -INFINITY;
-        b[j] = (e < a.E && a.bias != nullptr) ? __ldg(a.bias + e) : 0.0f;
-        if (e < a.E && isnan(logit(l + e))) v[j] = -INFINITY;
-        if (usable(v[j])) {
-            have |= 1u << j;
-            if (usable(b[j])) live |= 1u << j;
-        }
-    }
-    const int pick = choose_exact<PER>(a, v, b, have, live, lane);
+    unsigned have, live;
+    load_token<L, PER>(a, l, lane, v, b, have, live);
+    int pick;
+    if (!choose_fast<L, PER, KT>(a, l, v, b, have, live, lane, pick)) pick = choose_exact<L, PER>(a, l, lane);
 
     // The weights.  sigmoid(v) is exp(v) for v far below zero; where all
     // picks are there, their ratio is taken from exp(v_k - m), which does not
     // underflow.
     const float pv = pick >= 0 ? fminf(logit(l + pick), FLT_MAX) : -INFINITY;
-    const float m = warp_max(pv);
+    const float m = pick_max<KT>(pv);
     float s;
     if (a.score == MP_SCORE_SIGMOID && !(a.renorm && m < -40.0f))
         s = pick >= 0 ? __fdiv_rn(1.0f, 1.0f + expf(-pv)) : 0.0f;
@@ -209,7 +498,7 @@ __global__ void __launch_bounds__(RT_THREADS) k_route(const RouteArgs a)
         sum = warp_sum(sum);
         s = pick >= 0 ? __fdiv_rn(expf(pv - top), sum) : 0.0f;
     }
-    if (a.renorm) s = __fdiv_rn(s, warp_sum(s));
+    if (a.renorm) s = __fdiv_rn(s, pick_sum<KT>(s));
     if (lane < a.K) {
         a.idx[t * a.K + lane] = pick;
         a.weights[t * a.K + lane] = pick >= 0 ? a.scale * s : 0.0f;
@@ -229,11 +518,19 @@ struct RouteBwdArgs {
 // renorm: with p the weights before scaling, g_l = scale p_k (g_k - sum_j g_j p_j),
 // times 1 - s_k for the sigmoid.  Raw weights: sigmoid scale g_k s_k (1 - s_k);
 // softmax scale s_e ([e picked] g_k - sum_j g_j s_j) for every expert.
-template <typename L, int PER>
+// VEC: the row is whole chunks of 4 logits, aligned: lane l then holds chunks l,
+// l+32, ...; otherwise single ones.
+template <typename L, int W> struct alignas(sizeof(L) * W) Chunk {
+    L at[W];
+};
+
+template <typename L, int PER, bool VEC>
 __global__ void __launch_bounds__(RT_THREADS) k_route_bwd(const RouteBwdArgs a)
 {
     pdl_trigger();
     pdl_wait();
+    constexpr int W = VEC ? 4 : 1, CHUNKS = PER / W;
+    typedef Chunk<L, W> C;
     const int lane = threadIdx.x & 31;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * RT_WARPS + (threadIdx.x >> 5);
     if (t >= a.T) return;
@@ -246,7 +543,10 @@ __global__ void __launch_bounds__(RT_THREADS) k_route_bwd(const RouteBwdArgs a)
     const bool dense = a.score == MP_SCORE_SOFTMAX && !a.renorm;
     float at_pick;
     if (!dense) {
-        for (int e = lane; e < a.E; e += 32) put(gl + e, 0.0f);
+        C zero;
+#pragma unroll
+        for (int i = 0; i < W; ++i) put(zero.at + i, 0.0f);
+        for (int e = lane * W; e < a.E; e += 32 * W) *reinterpret_cast<C *>(gl + e) = zero;
         float left = 1.0f, s;   // 1 - s of the sigmoid
         const float m = warp_max(pv);
         if (a.score == MP_SCORE_SIGMOID) {
@@ -263,34 +563,43 @@ __global__ void __launch_bounds__(RT_THREADS) k_route_bwd(const RouteBwdArgs a)
         } else {
             at_pick = g * s * left;
         }
-        __syncwarp();   // the zeros above land first
     } else {
-        float v[PER], top = -INFINITY, sum = 0.0f;
+        float v[CHUNKS][W], top = -INFINITY, sum = 0.0f;
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            const int e = lane + 32 * j;
-            v[j] = e < a.E ? fminf(logit(l + e), FLT_MAX) : -INFINITY;
-            if (e < a.E && isnan(logit(l + e))) v[j] = -INFINITY;
-            top = fmaxf(top, v[j]);
+        for (int j = 0; j < CHUNKS; ++j) {
+            const int e = (lane + 32 * j) * W;
+            C x;
+            if (e < a.E) x = *reinterpret_cast<const C *>(l + e);
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                v[j][i] = e < a.E ? logit_value(x.at[i]) : -INFINITY;
+                v[j][i] = usable(v[j][i]) ? fminf(v[j][i], FLT_MAX) : -INFINITY;
+                top = fmaxf(top, v[j][i]);
+            }
         }
         top = warp_max(top);
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            v[j] = usable(v[j]) ? expf(v[j] - top) : 0.0f;
-            sum += v[j];
-        }
+        for (int j = 0; j < CHUNKS; ++j)
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                v[j][i] = usable(v[j][i]) ? expf(v[j][i] - top) : 0.0f;
+                sum += v[j][i];
+            }
         sum = warp_sum(sum);
         const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
         const float s = pick >= 0 ? expf(pv - top) * inv : 0.0f;
         const float d = warp_sum(pick >= 0 ? g * s : 0.0f);
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            const int e = lane + 32 * j;
-            if (e < a.E) put(gl + e, -v[j] * inv * d);
+        for (int j = 0; j < CHUNKS; ++j) {
+            const int e = (lane + 32 * j) * W;
+            C x;
+#pragma unroll
+            for (int i = 0; i < W; ++i) put(x.at + i, -v[j][i] * inv * d);
+            if (e < a.E) *reinterpret_cast<C *>(gl + e) = x;
         }
         at_pick = s * (g - d);
-        __syncwarp();
     }
+    __syncwarp();   // what is stored above lands before the picks' gradients
     if (pick >= 0) put(gl + pick, at_pick);
 }
 
@@ -298,14 +607,18 @@ template <typename L> mp_status_t launch_route(const RouteArgs &a, cudaStream_t 
 {
     const unsigned blocks = static_cast<unsigned>((a.T + RT_WARPS - 1) / RT_WARPS);
     const int per = (a.E + 31) / 32;
-    if (per <= 4)
-        (void)launch_pdl(k_route<L, 4>, blocks, RT_THREADS, 0, s, a);
+    if (per <= 4 && a.K == 8)
+        (void)launch_pdl(k_route<L, 4, 8>, blocks, RT_THREADS, 0, s, a);
+    else if (per <= 8 && a.K == 8)
+        (void)launch_pdl(k_route<L, 8, 8>, blocks, RT_THREADS, 0, s, a);
+    else if (per <= 4)
+        (void)launch_pdl(k_route<L, 4, 0>, blocks, RT_THREADS, 0, s, a);
     else if (per <= 8)
-        (void)launch_pdl(k_route<L, 8>, blocks, RT_THREADS, 0, s, a);
+        (void)launch_pdl(k_route<L, 8, 0>, blocks, RT_THREADS, 0, s, a);
     else if (per <= 16)
-        (void)launch_pdl(k_route<L, 16>, blocks, RT_THREADS, 0, s, a);
+        (void)launch_pdl(k_route<L, 16, 0>, blocks, RT_THREADS, 0, s, a);
     else
-        (void)launch_pdl(k_route<L, 32>, blocks, RT_THREADS, 0, s, a);
+        (void)launch_pdl(k_route<L, 32, 0>, blocks, RT_THREADS, 0, s, a);
     return check_launch();
 }
 
@@ -313,10 +626,14 @@ template <typename L> mp_status_t launch_route_bwd(const RouteBwdArgs &a, cudaSt
 {
     const unsigned blocks = static_cast<unsigned>((a.T + RT_WARPS - 1) / RT_WARPS);
     const int per = (a.E + 31) / 32;
-    if (per <= 8)
-        (void)launch_pdl(k_route_bwd<L, 8>, blocks, RT_THREADS, 0, s, a);
+    const uintptr_t both = reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.g_logits);
+    const bool vec = a.E % 4 == 0 && both % (4 * sizeof(L)) == 0;
+    if (per <= 8 && vec)
+        (void)launch_pdl(k_route_bwd<L, 8, true>, blocks, RT_THREADS, 0, s, a);
+    else if (per <= 8)
+        (void)launch_pdl(k_route_bwd<L, 8, false>, blocks, RT_THREADS, 0, s, a);
     else
-        (void)launch_pdl(k_route_bwd<L, 32>, blocks, RT_THREADS, 0, s, a);
+        (void)launch_pdl(k_route_bwd<L, 32, false>, blocks, RT_THREADS, 0, s, a);
     return check_launch();
 }
 
@@ -349,6 +666,7 @@ extern "C" mp_status_t mp_route(const void *logits, int32_t dtype, const float *
     if (T == 0) return MP_OK;
     if (logits == nullptr || idx == nullptr || weights == nullptr) return MP_ERR_INVALID_ARG;
     const RouteArgs a = {logits, bias, T, E, K, score, n_groups, topk_groups, group_top, renorm,
+                         static_cast<uint32_t>(((1ull << 32) + E / n_groups - 1) / (E / n_groups)),
                          scale, idx, weights};
     const cudaStream_t s = as_stream(stream);
     return dtype == MP_DTYPE_FP32   ? launch_route<float>(a, s)
