@@ -1,43 +1,75 @@
 // The experts' matrix products: argument checks, the choice of the kernel, and
 // the gradient of the bias.
+#include <type_traits>
+
 #include "expert.cuh"
 
 namespace mp {
 namespace {
 
-constexpr int BIAS_THREADS = 256;
+constexpr int BIAS_THREADS = 256, BIAS_WARPS = BIAS_THREADS / 32;
 
-// g_bias[e,n] = sum over the expert's rows of g[row,n], in fp32; one warp takes
-// every eighth row of 32 columns, and the eight sums are added in order.
+// g_bias[e,n] = sum over the expert's rows of g[row,n], in fp32.  A CTA owns 32 V
+// columns of one expert, V = 8 (16-byte loads) where rows are aligned to it; each
+// warp takes every eighth row, four of them in flight, and the eight sums are
+// added in order.  Bound by the bytes of g: 32,768 x 1,024, 256 experts in
+// 14 us (4.8 TB/s); with one column a lane it took 55.
+template <int V>
 __global__ void __launch_bounds__(BIAS_THREADS)
     k_expert_bias(const mp_bf16_t *__restrict__ g, const int32_t *__restrict__ offsets, int R,
                   int E, int N, mp_bf16_t *out, float *out_f32, bool add)
 {
     pdl_trigger();
     pdl_wait();
-    __shared__ int start[MP_MAX_EXPERTS + 1], tiles[MP_MAX_EXPERTS + 1];
-    __shared__ float part[BIAS_THREADS / 32][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (warp == 0) expert_starts(offsets, E, R, 1, lane, start, tiles, nullptr);
-    __syncthreads();
-    const int e = blockIdx.y, n = blockIdx.x * 32 + lane;
-    float s = 0.0f;
-    if (n < N)
-        for (int r = start[e] + warp; r < start[e + 1]; r += BIAS_THREADS / 32) {
-            float f[1];
-            unpack(ld_stream(g + static_cast<int64_t>(r) * N + n), f);
-            s += f[0];
+    __shared__ float part[BIAS_WARPS][32 * V];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.y;
+    // The clamped offsets of this expert: the largest up to each.
+    int a = 0, b = 0;
+    for (int i = lane; i <= e + 1; i += 32) {
+        const int v = min(max(__ldg(offsets + i), 0), R);
+        b = max(b, v);
+        if (i <= e) a = max(a, v);
+    }
+    a = __reduce_max_sync(FULL_MASK, a);
+    b = __reduce_max_sync(FULL_MASK, b);
+    const int n0 = blockIdx.x * 32 * V, n = n0 + lane * V;
+    float s[V] = {};
+    if (n < N) {
+        typedef typename std::conditional<V == 8, uint4, uint16_t>::type Vec;
+        const Vec *p = reinterpret_cast<const Vec *>(g + n);
+        const int64_t pitch = N / V;
+        int r = a + warp;
+        for (; r + 3 * BIAS_WARPS < b; r += 4 * BIAS_WARPS) {
+            Vec v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = ld_stream(p + (r + q * BIAS_WARPS) * pitch);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float f[V];
+                unpack(v[q], f);
+#pragma unroll
+                for (int i = 0; i < V; ++i) s[i] += f[i];
+            }
         }
-    part[warp][lane] = s;
+        for (; r < b; r += BIAS_WARPS) {
+            float f[V];
+            unpack(ld_stream(p + r * pitch), f);
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[i] += f[i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) part[warp][lane * V + i] = s[i];
     __syncthreads();
-    if (warp != 0 || n >= N) return;
-    for (int w = 1; w < BIAS_THREADS / 32; ++w) s += part[w][lane];
-    const int64_t at = static_cast<int64_t>(e) * N + n;
+    if (threadIdx.x >= 32 * V || n0 + static_cast<int>(threadIdx.x) >= N) return;
+    float t = part[0][threadIdx.x];
+    for (int w = 1; w < BIAS_WARPS; ++w) t += part[w][threadIdx.x];
+    const int64_t at = static_cast<int64_t>(e) * N + n0 + threadIdx.x;
     if (out_f32 != nullptr) {
-        out_f32[at] = add ? out_f32[at] + s : s;
+        out_f32[at] = add ? out_f32[at] + t : t;
     } else {
-        const float t[1] = {s};
-        out[at] = pack(t);
+        const float f[1] = {t};
+        out[at] = pack(f);
     }
 }
 
@@ -136,8 +168,13 @@ extern "C" mp_status_t mp_expert_wgrad(const mp_bf16_t *g, const mp_bf16_t *x,
     c.stream = as_stream(stream);
     const mp_status_t s = product<WGRAD>(c);
     if (s != MP_OK || g_bias == nullptr) return s;
-    (void)launch_pdl(k_expert_bias, dim3((N + 31) / 32, E), BIAS_THREADS, 0, c.stream, g, offsets,
-                     c.R, E, N, f32 ? nullptr : static_cast<mp_bf16_t *>(g_bias),
-                     f32 ? static_cast<float *>(g_bias) : nullptr, c.epi.add);
+    mp_bf16_t *gb = f32 ? nullptr : static_cast<mp_bf16_t *>(g_bias);
+    float *gb32 = f32 ? static_cast<float *>(g_bias) : nullptr;
+    if (N % 8 == 0 && aligned16(g))
+        (void)launch_pdl(k_expert_bias<8>, dim3((N + 255) / 256, E), BIAS_THREADS, 0, c.stream, g,
+                         offsets, c.R, E, N, gb, gb32, c.epi.add);
+    else
+        (void)launch_pdl(k_expert_bias<1>, dim3((N + 31) / 32, E), BIAS_THREADS, 0, c.stream, g,
+                         offsets, c.R, E, N, gb, gb32, c.epi.add);
     return check_launch();
 }

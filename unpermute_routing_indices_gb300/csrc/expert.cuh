@@ -23,53 +23,53 @@ __host__ __device__ inline int act_inner(int act)
 __host__ __device__ inline int ckpt_blocks(int n) { return (n + EPI_COLS - 1) / EPI_COLS; }
 
 // ---------------------------------------------------------------------------
-// Activations, in fp32.  expf is the accurate one: the fast one's error grows
-// with its argument, to 2^-17 of the value in gelu's tail.  The
-// division is the fast one (2 ulp).
+// Activations, in fp32.  The reciprocal is the approximate one (1 ulp).  silu's
+// exponential is the fast one, whose error grows with its argument: 2^-20 of
+// the value at z = -10, far below bf16's half step.  gelu's argument grows with
+// z^3, so there it would reach 2^-17: it takes expf.
 // ---------------------------------------------------------------------------
 
-__device__ __forceinline__ float sigmoid_fast(float z) { return __fdividef(1.0f, 1.0f + expf(-z)); }
+__device__ __forceinline__ float rcp_approx(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 
 // gelu in its tanh form is z * sigmoid(2u), u = sqrt(2/pi) (z + 0.044715 z^3):
 // no difference of nearly equal numbers for negative z.
 constexpr float GELU_A = 1.5957691216057308f;    // 2 sqrt(2/pi)
 constexpr float GELU_B = 0.044715f;
 
-// Past these bounds the derivative is 0 or 1 in fp32; NaN passes.
-__device__ __forceinline__ float act_bounded(float z, float b) { return z > b ? b : (z < -b ? -b : z); }
-
-__device__ __forceinline__ float act_value(float z, int inner)
-{
-    if (inner == MP_ACT_SILU) return z * sigmoid_fast(z);
-    if (inner == MP_ACT_GELU) {
-        const float c = act_bounded(z, 16.0f);
-        return z * sigmoid_fast(GELU_A * c * fmaf(GELU_B * c, c, 1.0f));
-    }
-    if (inner == MP_ACT_RELU) return z < 0.0f ? 0.0f : z;
-    return z;
-}
+// Past this bound gelu's derivative is 0 or 1 in fp32; NaN passes.
+__device__ __forceinline__ float gelu_bounded(float z) { return z > 16.0f ? 16.0f : (z < -16.0f ? -16.0f : z); }
 
 // act(z), and its derivative through `slope`.
-__device__ __forceinline__ float act_value_slope(float z, int inner, float &slope)
+template <int INNER> __device__ __forceinline__ float act_value_slope(float z, float &slope)
 {
-    if (inner == MP_ACT_SILU) {
-        const float s = sigmoid_fast(z);
-        slope = fmaf(act_bounded(z, 100.0f) * s, 1.0f - s, s);
+    if (INNER == MP_ACT_SILU) {
+        const float s = rcp_approx(1.0f + __expf(-z)), a = z * s;
+        slope = fmaf(a, 1.0f - s, s);
+        return a;
+    }
+    if (INNER == MP_ACT_GELU) {
+        const float c = gelu_bounded(z), cc = c * c;
+        const float s = rcp_approx(1.0f + expf(-GELU_A * c * fmaf(GELU_B, cc, 1.0f)));
+        slope = fmaf(c * s * (1.0f - s), GELU_A * fmaf(3.0f * GELU_B, cc, 1.0f), s);
         return z * s;
     }
-    if (inner == MP_ACT_GELU) {
-        const float c = act_bounded(z, 16.0f);
-        const float s = sigmoid_fast(GELU_A * c * fmaf(GELU_B * c, c, 1.0f));
-        const float du = GELU_A * fmaf(3.0f * GELU_B * c, c, 1.0f);
-        slope = fmaf(c * s * (1.0f - s), du, s);
-        return z * s;
-    }
-    if (inner == MP_ACT_RELU) {
+    if (INNER == MP_ACT_RELU) {
         slope = z > 0.0f ? 1.0f : 0.0f;
         return z < 0.0f ? 0.0f : z;
     }
     slope = 1.0f;
     return z;
+}
+
+template <int INNER> __device__ __forceinline__ float act_value(float z)
+{
+    float slope;
+    return act_value_slope<INNER>(z, slope);
 }
 
 // ---------------------------------------------------------------------------
@@ -318,6 +318,16 @@ __device__ __forceinline__ void add_bias32(const mp_bf16_t *b, int n, float (&z)
     for (int i = 0; i < EPI_COLS; ++i) z[i] += f[i];
 }
 
+template <int INNER, bool GATED>
+__device__ __forceinline__ void act32(float (&z)[EPI_COLS], const float (&u)[EPI_COLS])
+{
+#pragma unroll
+    for (int i = 0; i < EPI_COLS; ++i) {
+        z[i] = act_value<INNER>(z[i]);
+        if (GATED) z[i] *= u[i];
+    }
+}
+
 // z: the product's columns c..c+31 (of the gate when GATED, u then the others').
 template <bool GATED>
 __device__ __forceinline__ void epi_fwd(const ExpertEpi &p, int e, int64_t row, int c, int n,
@@ -333,13 +343,13 @@ __device__ __forceinline__ void epi_fwd(const ExpertEpi &p, int e, int64_t row, 
         save32(p, row, 0, parts, c, n, z);
         if (GATED) save32(p, row, 1, parts, c, n, u);
     }
-    const int inner = act_inner(p.act);
-    if (inner != MP_ACT_NONE) {
-#pragma unroll
-        for (int i = 0; i < EPI_COLS; ++i) {
-            z[i] = act_value(z[i], inner);
-            if (GATED) z[i] *= u[i];
-        }
+    switch (act_inner(p.act)) {
+    case MP_ACT_SILU: act32<MP_ACT_SILU, GATED>(z, u); break;
+    case MP_ACT_GELU: act32<MP_ACT_GELU, GATED>(z, u); break;
+    case MP_ACT_RELU:
+        if (!GATED) act32<MP_ACT_RELU, false>(z, u);
+        break;
+    default: break;
     }
     if (p.residual != nullptr) {
         float f[EPI_COLS];
@@ -350,7 +360,27 @@ __device__ __forceinline__ void epi_fwd(const ExpertEpi &p, int e, int64_t row, 
     store32(p.out + row * p.cols + c, n, z);
 }
 
-// g: the gradient of act's result.
+// g: the gradient of act's result.  The results replace their inputs: gated,
+// z the gate's gradient, u the others', g act's result.
+template <int INNER, bool GATED>
+__device__ __forceinline__ void act_grad32(float (&g)[EPI_COLS], float (&z)[EPI_COLS], float (&u)[EPI_COLS])
+{
+#pragma unroll
+    for (int i = 0; i < EPI_COLS; ++i) {
+        float slope;
+        const float a = act_value_slope<INNER>(z[i], slope);
+        if (GATED) {
+            z[i] = g[i] * u[i] * slope;
+            const float o = u[i];
+            u[i] = g[i] * a;
+            g[i] = a * o;
+        } else {
+            z[i] = g[i] * slope;
+            g[i] = a;
+        }
+    }
+}
+
 __device__ __forceinline__ void epi_dgrad(const ExpertEpi &p, int64_t row, int c, int n,
                                           float (&g)[EPI_COLS])
 {
@@ -358,33 +388,26 @@ __device__ __forceinline__ void epi_dgrad(const ExpertEpi &p, int64_t row, int c
         store32(p.out + row * p.cols + c, n, g);
         return;
     }
-    const int inner = act_inner(p.act);
-    float z[EPI_COLS], h[EPI_COLS];
+    float z[EPI_COLS], u[EPI_COLS];
     if (act_gated(p.act)) {
-        float u[EPI_COLS];
         read32(p, row, 0, 2, c, n, z);
         read32(p, row, 1, 2, c, n, u);
-#pragma unroll
-        for (int i = 0; i < EPI_COLS; ++i) {
-            float slope;
-            const float a = act_value_slope(z[i], inner, slope);
-            h[i] = a * u[i];
-            z[i] = g[i] * u[i] * slope;
-            u[i] = g[i] * a;
-        }
+        if (p.act == MP_ACT_SWIGLU)
+            act_grad32<MP_ACT_SILU, true>(g, z, u);
+        else
+            act_grad32<MP_ACT_GELU, true>(g, z, u);
         store32(p.out + (row * 2 + 1) * p.cols + c, n, u);
         store32(p.out + row * 2 * p.cols + c, n, z);
     } else {
         read32(p, row, 0, 1, c, n, z);
-#pragma unroll
-        for (int i = 0; i < EPI_COLS; ++i) {
-            float slope;
-            h[i] = act_value_slope(z[i], inner, slope);
-            z[i] = g[i] * slope;
+        switch (p.act) {
+        case MP_ACT_SILU: act_grad32<MP_ACT_SILU, false>(g, z, u); break;
+        case MP_ACT_GELU: act_grad32<MP_ACT_GELU, false>(g, z, u); break;
+        default: act_grad32<MP_ACT_RELU, false>(g, z, u); break;
         }
         store32(p.out + row * p.cols + c, n, z);
     }
-    if (p.h != nullptr) store32(p.h + row * p.cols + c, n, h);
+    if (p.h != nullptr) store32(p.h + row * p.cols + c, n, g);
 }
 
 __device__ __forceinline__ void epi_wgrad(const ExpertEpi &p, int64_t row, int c, int n,

@@ -6,8 +6,8 @@
 //   DGRAD  rows of g along, w[e] across (its columns are the result's)
 //   WGRAD  g and x both across: the contraction is over the expert's rows
 // Warp 0 loads 64-deep slices of both operands by TMA into a ring, warp 1 issues
-// the products into one of two TMEM accumulators, and warps 2-5 take the other
-// one through the epilogue, 32 columns of a row per thread.  Every CTA derives
+// the products into one of two TMEM accumulators, and warps 2-9 take the other
+// one through the epilogue, 32 columns of a row per thread and step.  Every CTA derives
 // the tiles from the offsets on the device, so that the grid depends on the
 // sizes alone and the call can be captured.
 // Rows of a tile past the expert's end belong to the next expert: they are
@@ -71,7 +71,8 @@ namespace {
 
 constexpr int BM = 128, BN = 256, BK = 64;
 constexpr int STAGES = 4;
-constexpr int TC_THREADS = 192;
+constexpr int EPI_WARPS = 8;   // two for each quarter of the accumulator's lanes
+constexpr int TC_THREADS = 64 + 32 * EPI_WARPS;
 constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int BOX_BYTES = 64 * 64 * 2;   // a box of 64 rows
 constexpr int TMEM_COLS = 2 * BN;
@@ -117,6 +118,26 @@ __device__ __forceinline__ Tile tile_at(const ExpertCall &c, const int *start, c
     return r;
 }
 
+// Brings what the epilogue of columns [c0,c1) of a row will read into L2 while the
+// accumulator fills.
+__device__ __forceinline__ void prefetch_l2(const void *p, int bytes)
+{
+    for (int i = 0; i < bytes; i += 128)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char *>(p) + i));
+}
+template <int MODE>
+__device__ __forceinline__ void epi_prefetch(const ExpertEpi &p, int64_t row, int c0, int c1)
+{
+    if (MODE == FWD) {
+        if (p.residual != nullptr) prefetch_l2(p.residual + row * p.cols + c0, 2 * (c1 - c0));
+    } else if (p.act != MP_ACT_NONE) {
+        const int parts = act_gated(p.act) ? 2 : 1, size = p.save == MP_SAVE_BF16 ? 2 : 1;
+        for (int q = 0; q < parts; ++q)
+            prefetch_l2(static_cast<const char *>(p.z) + ((row * parts + q) * p.cols + c0) * size,
+                        size * (c1 - c0));
+    }
+}
+
 template <int MODE, bool GATED>
 __global__ void __launch_bounds__(TC_THREADS, 1)
     k_expert_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
@@ -137,7 +158,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&s.acc_full[i]), 1);
-            mbar_init(smem_u32(&s.acc_empty[i]), 4);
+            mbar_init(smem_u32(&s.acc_empty[i]), EPI_WARPS);
         }
         mbar_init(smem_u32(&s.drained), 1);
         mbar_init_fence();
@@ -248,20 +269,24 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             or_status(c.status, MP_STATUS_STALLED);
         }
     } else {
-        const int quad = warp & 3;   // the TMEM lanes this warp can read
+        const int quad = warp & 3;            // the TMEM lanes this warp can read
+        const int half = (warp - 2) >> 2;     // and its half of the columns
         uint32_t it = 0;
         for (int64_t t = blockIdx.x; t < total; t += gridDim.x) {
             const Tile w = tile_at<MODE>(c, s.start, s.tiles, t, nt, tile_cols);
             if (MODE == WGRAD && w.depth == 0 && c.epi.add) continue;   // nothing to add
             const int row = w.m0 + quad * 32 + lane;
             const int acc = it & 1;
+            const int j0 = half * (tile_cols / 2), j1 = j0 + tile_cols / 2;
+            if (MODE != WGRAD && row < w.m1 && w.c0 + j0 < c.epi.cols)
+                epi_prefetch<MODE>(c.epi, row, w.c0 + j0, min(w.c0 + j1, c.epi.cols));
             if (w.depth != 0) {
                 if (!__all_sync(FULL_MASK, mbar_wait(smem_u32(&s.acc_full[acc]), (it >> 1) & 1, gave_up)))
                     break;
                 tc_fence_after();
             }
             const uint32_t d = tmem + acc * BN + (static_cast<uint32_t>(quad * 32) << 16);
-            for (int j = 0; j < tile_cols; j += EPI_COLS) {
+            for (int j = j0; j < j1; j += EPI_COLS) {
                 const int col = w.c0 + j;
                 if (col >= c.epi.cols) break;
                 float z[EPI_COLS], u[EPI_COLS];
