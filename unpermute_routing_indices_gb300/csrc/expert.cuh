@@ -272,8 +272,12 @@ __device__ __forceinline__ void ckpt_read32(const uint8_t *codes, const uint8_t 
 }
 
 // ---------------------------------------------------------------------------
-// Epilogues, on 32 columns of one row in fp32.
+// Epilogues, on 32 columns of one row in fp32.  `W` writes bf16 results: a kernel
+// whose warps hold 32 consecutive rows may do so together (every lane then
+// calls, `valid` or not, with a row that exists to read from).
 // ---------------------------------------------------------------------------
+
+enum { TO_OUT = 0, TO_SECOND = 1 };   // the maps of a writer: out; z (FWD) or h (DGRAD)
 
 struct ExpertEpi {
     int act, save;            // MP_ACT_*, MP_SAVE_*
@@ -288,14 +292,24 @@ struct ExpertEpi {
     bool add;                 // WGRAD: add to out_f32
 };
 
-__device__ __forceinline__ void save32(const ExpertEpi &p, int64_t row, int part, int parts, int c,
-                                       int n, const float (&z)[EPI_COLS])
+// Each thread writes its own row.
+struct RowWriter {
+    __device__ __forceinline__ void put(mp_bf16_t *base, int64_t pitch, int, int64_t row, int64_t c,
+                                        int n, bool, const float (&f)[EPI_COLS])
+    {
+        store32(base + row * pitch + c, n, f);
+    }
+};
+
+template <typename W>
+__device__ __forceinline__ void save32(const ExpertEpi &p, W &w, int64_t row, int part, int parts,
+                                       int c, int n, bool valid, const float (&z)[EPI_COLS])
 {
-    const int64_t at = (row * parts + part) * p.cols + c;
     if (p.save == MP_SAVE_BF16)
-        store32(static_cast<mp_bf16_t *>(p.z) + at, n, z);
-    else
-        ckpt_write32(static_cast<uint8_t *>(p.z) + at,
+        w.put(static_cast<mp_bf16_t *>(p.z), static_cast<int64_t>(parts) * p.cols, TO_SECOND, row,
+              static_cast<int64_t>(part) * p.cols + c, n, valid, z);
+    else if (valid)
+        ckpt_write32(static_cast<uint8_t *>(p.z) + (row * parts + part) * p.cols + c,
                      p.z_exp + (row * parts + part) * ckpt_blocks(p.cols) + c / EPI_COLS, n, z);
 }
 
@@ -329,9 +343,9 @@ __device__ __forceinline__ void act32(float (&z)[EPI_COLS], const float (&u)[EPI
 }
 
 // z: the product's columns c..c+31 (of the gate when GATED, u then the others').
-template <bool GATED>
-__device__ __forceinline__ void epi_fwd(const ExpertEpi &p, int e, int64_t row, int c, int n,
-                                        float (&z)[EPI_COLS], float (&u)[EPI_COLS])
+template <bool GATED, typename W>
+__device__ __forceinline__ void epi_fwd(const ExpertEpi &p, W &w, int e, int64_t row, int c, int n,
+                                        bool valid, float (&z)[EPI_COLS], float (&u)[EPI_COLS])
 {
     constexpr int parts = GATED ? 2 : 1;
     if (p.bias != nullptr) {
@@ -340,8 +354,8 @@ __device__ __forceinline__ void epi_fwd(const ExpertEpi &p, int e, int64_t row, 
         if (GATED) add_bias32(b + p.cols, n, u);
     }
     if (p.save != MP_SAVE_NONE) {
-        save32(p, row, 0, parts, c, n, z);
-        if (GATED) save32(p, row, 1, parts, c, n, u);
+        save32(p, w, row, 0, parts, c, n, valid, z);
+        if (GATED) save32(p, w, row, 1, parts, c, n, valid, u);
     }
     switch (act_inner(p.act)) {
     case MP_ACT_SILU: act32<MP_ACT_SILU, GATED>(z, u); break;
@@ -357,7 +371,7 @@ __device__ __forceinline__ void epi_fwd(const ExpertEpi &p, int e, int64_t row, 
 #pragma unroll
         for (int i = 0; i < EPI_COLS; ++i) z[i] += f[i];
     }
-    store32(p.out + row * p.cols + c, n, z);
+    w.put(p.out, p.cols, TO_OUT, row, c, n, valid, z);
 }
 
 // g: the gradient of act's result.  The results replace their inputs: gated,
@@ -381,11 +395,12 @@ __device__ __forceinline__ void act_grad32(float (&g)[EPI_COLS], float (&z)[EPI_
     }
 }
 
-__device__ __forceinline__ void epi_dgrad(const ExpertEpi &p, int64_t row, int c, int n,
-                                          float (&g)[EPI_COLS])
+template <typename W>
+__device__ __forceinline__ void epi_dgrad(const ExpertEpi &p, W &w, int64_t row, int c, int n,
+                                          bool valid, float (&g)[EPI_COLS])
 {
     if (p.act == MP_ACT_NONE) {
-        store32(p.out + row * p.cols + c, n, g);
+        w.put(p.out, p.cols, TO_OUT, row, c, n, valid, g);
         return;
     }
     float z[EPI_COLS], u[EPI_COLS];
@@ -396,8 +411,8 @@ __device__ __forceinline__ void epi_dgrad(const ExpertEpi &p, int64_t row, int c
             act_grad32<MP_ACT_SILU, true>(g, z, u);
         else
             act_grad32<MP_ACT_GELU, true>(g, z, u);
-        store32(p.out + (row * 2 + 1) * p.cols + c, n, u);
-        store32(p.out + row * 2 * p.cols + c, n, z);
+        w.put(p.out, 2ll * p.cols, TO_OUT, row, c, n, valid, z);
+        w.put(p.out, 2ll * p.cols, TO_OUT, row, static_cast<int64_t>(p.cols) + c, n, valid, u);
     } else {
         read32(p, row, 0, 1, c, n, z);
         switch (p.act) {
@@ -405,18 +420,19 @@ __device__ __forceinline__ void epi_dgrad(const ExpertEpi &p, int64_t row, int c
         case MP_ACT_GELU: act_grad32<MP_ACT_GELU, false>(g, z, u); break;
         default: act_grad32<MP_ACT_RELU, false>(g, z, u); break;
         }
-        store32(p.out + row * p.cols + c, n, z);
+        w.put(p.out, p.cols, TO_OUT, row, c, n, valid, z);
     }
-    if (p.h != nullptr) store32(p.h + row * p.cols + c, n, g);
+    if (p.h != nullptr) w.put(p.h, p.cols, TO_SECOND, row, c, n, valid, g);
 }
 
-__device__ __forceinline__ void epi_wgrad(const ExpertEpi &p, int64_t row, int c, int n,
-                                          const float (&g)[EPI_COLS])
+template <typename W>
+__device__ __forceinline__ void epi_wgrad(const ExpertEpi &p, W &w, int64_t row, int c, int n,
+                                          bool valid, const float (&g)[EPI_COLS])
 {
-    if (p.out_f32 != nullptr)
+    if (p.out_f32 == nullptr)
+        w.put(p.out, p.cols, TO_OUT, row, c, n, valid, g);
+    else if (valid)
         store32_f32(p.out_f32 + row * p.cols + c, n, g, p.add);
-    else
-        store32(p.out + row * p.cols + c, n, g);
 }
 
 // ---------------------------------------------------------------------------

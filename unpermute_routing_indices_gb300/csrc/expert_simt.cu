@@ -116,9 +116,11 @@ __global__ void __launch_bounds__(SIMT_THREADS) k_expert_simt(const ExpertCall c
         const int row = m0 + strip * 16 + r, col = n0 + cc;
         if (r < 16 && row < m1 && col < cols) {
             const int n = min(EPI_COLS, cols - col);
-            if (MODE == FWD) epi_fwd<GATED>(c.epi, e, row, col, n, z, u);
-            if (MODE == DGRAD) epi_dgrad(c.epi, row, col, n, z);
-            if (MODE == WGRAD) epi_wgrad(c.epi, static_cast<int64_t>(e) * c.N + row, col, n, z);
+            RowWriter w;
+            if (MODE == FWD) epi_fwd<GATED>(c.epi, w, e, row, col, n, true, z, u);
+            if (MODE == DGRAD) epi_dgrad(c.epi, w, row, col, n, true, z);
+            if (MODE == WGRAD)
+                epi_wgrad(c.epi, w, static_cast<int64_t>(e) * c.N + row, col, n, true, z);
         }
     }
 }

@@ -108,6 +108,18 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *m, uin
         : "memory");
 }
 
+// A tile from shared memory, in a group of its own of the issuing thread.
+__device__ __forceinline__ void tma_store(const CUtensorMap *m, uint32_t src, int x, int y)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(m),
+                 "r"(src), "r"(x), "r"(y)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// The issuing thread's stores have read their shared memory / are done.
+__device__ __forceinline__ void tma_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 // --- tcgen05 ---------------------------------------------------------------
 
 __device__ __forceinline__ void tmem_alloc(uint32_t smem_dst, int cols)
@@ -180,7 +192,8 @@ __host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool a_across, boo
 // --- host ------------------------------------------------------------------
 
 // A tensor map of bf16 rows: `dims` and `box` from the innermost, rows dense,
-// 128-byte swizzle (box[0] is 64), zeros outside.  False: the driver refused.
+// zeros outside, swizzled over box[0]: 128 bytes (64 columns) or 64 (32).
+// False: the driver refused.
 bool make_map(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, const uint32_t *box);
 int sm_count();
 
