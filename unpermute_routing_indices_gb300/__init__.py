@@ -12,8 +12,6 @@ Tensors: bf16 hidden rows, fp32 probabilities, int32 indices and maps.
 from __future__ import annotations
 
 import contextlib
-import ctypes
-
 import torch
 
 from . import _lib
@@ -66,7 +64,7 @@ def _check(fn: str, code: int) -> None:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -75,18 +73,24 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 def _stream(device):
     """The current CUDA stream of `device` as a raw handle."""
     if _raw_stream is not None and device.index is not None:
-        return ctypes.c_void_p(_raw_stream(device.index))
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+_here = contextlib.nullcontext()
 
 
 def _on(device):
     """Context that makes `device` current for the call (free when it is)."""
     if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
+        return _here
     return torch.cuda.device(device)
 
 
 def _need(t, name, dtype, ndim=None, device=None):
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous() \
+            and (ndim is None or t.dim() == ndim) and (device is None or t.device == device):
+        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -107,7 +111,7 @@ def _opt(t, *a, **k):
 
 
 def _shape(t, name, shape):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -340,6 +344,44 @@ def _products(rows, name, w, offsets, width):
     return dev, rows.shape[0], E, N, K
 
 
+# The calls behind the checks: mp_expert_* below, and autograd's backward passes,
+# whose tensors a checked forward pass made.
+
+def _gemm(x, w, offsets, bias, act, residual, out, save, z, z_exp, status):
+    E, N, K = w.shape
+    with _on(x.device):
+        _check("mp_expert_gemm", _lib.load().mp_expert_gemm(
+            x.data_ptr(), w.data_ptr(), offsets.data_ptr(), x.shape[0], E, N, K, _ptr(bias),
+            ACTS[act], _ptr(residual), out.data_ptr(), SAVES[save], _ptr(z), _ptr(z_exp),
+            _ptr(status), _stream(x.device)))
+
+
+def _dgrad(g, w, offsets, act, save, z, z_exp, g_x, h, status=None):
+    E, N, K = w.shape
+    with _on(g.device):
+        _check("mp_expert_dgrad", _lib.load().mp_expert_dgrad(
+            g.data_ptr(), w.data_ptr(), offsets.data_ptr(), g.shape[0], E, N, K, ACTS[act],
+            SAVES[save], _ptr(z), _ptr(z_exp), g_x.data_ptr(), _ptr(h), _ptr(status),
+            _stream(g.device)))
+
+
+def _wgrad(g, x, offsets, accumulate, g_w, g_bias, status=None):
+    E, N, K = g_w.shape
+    with _on(g.device):
+        _check("mp_expert_wgrad", _lib.load().mp_expert_wgrad(
+            g.data_ptr(), x.data_ptr(), offsets.data_ptr(), g.shape[0], E, N, K,
+            DTYPES[g_w.dtype], accumulate, g_w.data_ptr(), _ptr(g_bias), _ptr(status),
+            _stream(g.device)))
+
+
+def _zero_unrouted(rows, offsets):
+    """Zeroes the rows of a bf16 [R,H] from offsets[-1] on."""
+    with _on(rows.device):
+        _check("mp_zero_rows_from", _lib.load().mp_zero_rows_from(
+            rows.data_ptr(), rows.shape[0], 2 * rows.shape[1],
+            offsets.data_ptr() + 4 * (offsets.shape[0] - 1), _stream(rows.device)))
+
+
 def mp_expert_gemm(x, w, offsets, *, bias=None, act: str = "none", residual=None,
                    save: str = "none", out=None, z=None, z_exp=None, status=None):
     """x bf16 [R,K], w bf16 [E,N,K], offsets int32 [E+1] -> (out bf16 [R,F], z, z_exp):
@@ -347,9 +389,9 @@ def mp_expert_gemm(x, w, offsets, *, bias=None, act: str = "none", residual=None
     the gated activations geglu and swiglu, whose gate is the first half of w's rows).
     `save` keeps the product before the activation: "bf16" in z bf16 [R,N], "e4m3" in
     z float8_e4m3fn [R,N] with z_exp uint8 (one power of two per 32 columns)."""
-    lib = _lib.load()
     dev, R, E, N, K = _products(x, "x", w, offsets, 2)
-    a, s = _named(act, ACTS, "act"), _named(save, SAVES, "save")
+    _named(act, ACTS, "act")
+    _named(save, SAVES, "save")
     if N % _parts(act):
         raise ValueError(f"a gated activation needs an even number of columns, got {N}")
     F = N // _parts(act)
@@ -364,10 +406,7 @@ def mp_expert_gemm(x, w, offsets, *, bias=None, act: str = "none", residual=None
     _shape(out, "out", (R, F))
     z, z_exp = _checkpoint(z, z_exp, R, F, act, save, dev, make=True)
     _opt(status, "status", torch.int32, 1, dev)
-    with _on(dev):
-        _check("mp_expert_gemm", lib.mp_expert_gemm(
-            _ptr(x), _ptr(w), _ptr(offsets), R, E, N, K, _ptr(bias), a, _ptr(residual),
-            _ptr(out), s, _ptr(z), _ptr(z_exp), _ptr(status), _stream(dev)))
+    _gemm(x, w, offsets, bias, act, residual, out, save, z, z_exp, status)
     return out, z, z_exp
 
 
@@ -377,9 +416,8 @@ def mp_expert_dgrad(g, w, offsets, *, act: str = "none", z=None, z_exp=None,
     With `act`, also through the activation before those rows, whose product was saved
     as z (and z_exp): g_x is then [R,K] or, gated, [R,2K], and h = act(z) bf16 [R,K] if
     `with_h` (the rows that mp_expert_wgrad needs)."""
-    lib = _lib.load()
     dev, R, E, N, K = _products(g, "g", w, offsets, 1)
-    a = _named(act, ACTS, "act")
+    _named(act, ACTS, "act")
     if act == "none":
         save = "none"
     elif z is None:
@@ -399,10 +437,7 @@ def mp_expert_dgrad(g, w, offsets, *, act: str = "none", z=None, z_exp=None,
         _need(h, "h", torch.bfloat16, 2, dev)
         _shape(h, "h", (R, K))
     _opt(status, "status", torch.int32, 1, dev)
-    with _on(dev):
-        _check("mp_expert_dgrad", lib.mp_expert_dgrad(
-            _ptr(g), _ptr(w), _ptr(offsets), R, E, N, K, a, SAVES[save], _ptr(z), _ptr(z_exp),
-            _ptr(g_x), _ptr(h), _ptr(status), _stream(dev)))
+    _dgrad(g, w, offsets, act, save, z, z_exp, g_x, h, status)
     return g_x, h
 
 
@@ -411,7 +446,6 @@ def mp_expert_wgrad(g, x, offsets, *, with_bias: bool = False, dtype=torch.bfloa
     """Gradient of mp_expert_gemm w.r.t. weights and bias: g bf16 [R,N], x bf16 [R,K] ->
     (g_w [E,N,K], g_bias [E,N] or None) of `dtype` (bf16 or fp32).  With `accumulate`
     the fp32 g_w (and g_bias), which must be given, are added to."""
-    lib = _lib.load()
     _need(g, "g", torch.bfloat16, 2)
     dev = g.device
     R, N = g.shape
@@ -435,10 +469,7 @@ def mp_expert_wgrad(g, x, offsets, *, with_bias: bool = False, dtype=torch.bfloa
         _need(g_bias, "g_bias", dtype, 2, dev)
         _shape(g_bias, "g_bias", (E, N))
     _opt(status, "status", torch.int32, 1, dev)
-    with _on(dev):
-        _check("mp_expert_wgrad", lib.mp_expert_wgrad(
-            _ptr(g), _ptr(x), _ptr(offsets), R, E, N, K, DTYPES[dtype], int(bool(accumulate)),
-            _ptr(g_w), _ptr(g_bias), _ptr(status), _stream(dev)))
+    _wgrad(g, x, offsets, int(bool(accumulate)), g_w, g_bias, status)
     return g_w, g_bias
 
 

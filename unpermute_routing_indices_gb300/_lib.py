@@ -54,6 +54,8 @@ def path() -> str:
 def load(build_if_missing: bool = False) -> ctypes.CDLL:
     """Load libmp.so.  Raises if it is absent (run ``__graft_entry__.build()``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

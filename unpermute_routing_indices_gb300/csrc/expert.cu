@@ -116,6 +116,7 @@ extern "C" mp_status_t mp_expert_gemm(const mp_bf16_t *x, const mp_bf16_t *w,
     c.epi.z = z; c.epi.z_exp = z_exp;
     c.status = dev_status;
     c.stream = as_stream(stream);
+    if (expert_few_takes(c)) return expert_few(c);
     return product<FWD>(c);
 }
 

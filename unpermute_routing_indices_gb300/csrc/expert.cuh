@@ -442,39 +442,44 @@ __device__ __forceinline__ void epi_wgrad(const ExpertEpi &p, W &w, int64_t row,
 // `tile_rows` rows).
 // ---------------------------------------------------------------------------
 
+// Each lane takes a run of entries, so that the two scans (largest so far, tiles so
+// far) cross the warp once whatever E is.
 __device__ __forceinline__ void expert_starts(const int32_t *offsets, int E, int R, int tile_rows,
                                               int lane, int *start, int *tiles, int32_t *status)
 {
-    int high = 0, before = 0;
-    bool bad = false;
-    for (int base = 0; base <= E; base += 32) {
-        const int e = base + lane;
-        const int given = e <= E ? __ldg(offsets + e) : 0;
-        int v = min(max(given, 0), R);
+#pragma unroll 8
+    for (int i = lane; i <= E; i += 32) start[i] = __ldg(offsets + i);
+    __syncwarp();
+    const int run = (E + 32) / 32, i0 = lane * run, i1 = min(i0 + run, E + 1);
+    int high = 0;
+    for (int i = i0; i < i1; ++i) high = max(high, min(start[i], R));
+    int before = high;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(FULL_MASK, v, d);
-            if (lane >= d) v = max(v, o);
-        }
-        v = max(v, high);
-        bad |= e <= E && v != given;
-        int prev = __shfl_up_sync(FULL_MASK, v, 1);
-        if (lane == 0) prev = high;
-        // Tiles of expert e-1, whose rows are [prev, v).
-        int n = (e >= 1 && e <= E) ? (v - prev + tile_rows - 1) / tile_rows : 0;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(FULL_MASK, n, d);
-            if (lane >= d) n += o;
-        }
-        n += before;
-        if (e <= E) {
-            start[e] = v;
-            tiles[e] = n;
-        }
-        high = __shfl_sync(FULL_MASK, v, 31);
-        before = __shfl_sync(FULL_MASK, n, 31);
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(FULL_MASK, before, d);
+        if (lane >= d) before = max(before, o);
     }
+    before = __shfl_up_sync(FULL_MASK, before, 1);
+    if (lane == 0) before = 0;
+    // Entry i ends expert i - 1, whose rows start at the entry before it.
+    bool bad = false;
+    int prev = before, n = 0;
+    for (int i = i0; i < i1; ++i) {
+        const int given = start[i], v = max(prev, min(given, R));
+        bad |= v != given;
+        n += i > 0 ? (v - prev + tile_rows - 1) / tile_rows : 0;
+        start[i] = v;
+        tiles[i] = n;
+        prev = v;
+    }
+    int sum = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(FULL_MASK, sum, d);
+        if (lane >= d) sum += o;
+    }
+    sum -= n;
+    for (int i = i0; i < i1; ++i) tiles[i] += sum;
     if (status != nullptr && __any_sync(FULL_MASK, bad) && lane == 0)
         or_status(status, MP_STATUS_BAD_OFFSETS);
 }
@@ -506,5 +511,7 @@ struct ExpertCall {
 template <int MODE> mp_status_t expert_simt(const ExpertCall &c);   // any width, any alignment
 template <int MODE> bool expert_tc_takes(const ExpertCall &c);      // TMA's rules hold
 template <int MODE> mp_status_t expert_tc(const ExpertCall &c);
+bool expert_few_takes(const ExpertCall &c);                          // FWD, few rows an expert
+mp_status_t expert_few(const ExpertCall &c);
 
 }  // namespace mp

@@ -54,7 +54,7 @@ __device__ __forceinline__ uint64_t now_ns()
 // times the longest work between two arrivals), or that another warp has given
 // up, ends false; *gave_up is then set, and every role of the kernel leaves.
 constexpr uint64_t WAIT_NS = 4000000000ull;
-__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int *gave_up)
+__device__ __noinline__ inline bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int *gave_up)
 {
     const uint64_t t0 = now_ns();
     for (;;) {
