@@ -331,6 +331,38 @@ mp_status_t mp_expert_wgrad(const mp_bf16_t *g, const mp_bf16_t *x, const int32_
                             int32_t accumulate, void *g_w, void *g_bias, int32_t *dev_status,
                             mp_stream_t stream);
 
+/*
+ * An expert's two products in one call, and their gradients in one call: the
+ * calls above in order, so that a training step costs the host two calls.
+ *   y = h w2[e]^T + b2[e],  h = act(x w1[e]^T + b1[e])
+ *   x  device bf16 [R,H];  w1 device bf16 [E,P,H], b1 [E,P] or NULL, P = F or,
+ *      with a gated activation, 2F;  w2 device bf16 [E,O,F], b2 [E,O] or NULL
+ *   h  device bf16 [R,F] out;  y device bf16 [R,O] out.  Rows of y from
+ *      offsets[E] on are zeroed.
+ *   save, z, z_exp  what is kept of the first product, as in mp_expert_gemm
+ */
+mp_status_t mp_expert_mlp(const mp_bf16_t *x, const mp_bf16_t *w1, const mp_bf16_t *b1,
+                          const mp_bf16_t *w2, const mp_bf16_t *b2, const int32_t *offsets,
+                          int64_t R, int32_t E, int32_t H, int32_t F, int32_t O, int32_t act,
+                          mp_bf16_t *h, mp_bf16_t *y, int32_t save, void *z, uint8_t *z_exp,
+                          int32_t *dev_status, mp_stream_t stream);
+
+/*
+ * Gradients of mp_expert_mlp at the kept product.
+ *   g_y  device bf16 [R,O];  save (not MP_SAVE_NONE), z, z_exp as kept
+ *   g_z  device bf16 [R,P]: written (the gradient of the first product)
+ *   h    device bf16 [R,F]: written (act at the kept product); may be NULL if
+ *        g_w2 is
+ *   g_x [R,H], g_w1 [E,P,H], g_b1 [E,P], g_w2 [E,O,F], g_b2 [E,O]: device bf16, each
+ *        written unless NULL.  Rows of g_x from offsets[E] on are zeroed.
+ */
+mp_status_t mp_expert_mlp_bwd(const mp_bf16_t *g_y, const mp_bf16_t *x, const mp_bf16_t *w1,
+                              const mp_bf16_t *w2, const int32_t *offsets, int64_t R, int32_t E,
+                              int32_t H, int32_t F, int32_t O, int32_t act, int32_t save,
+                              const void *z, const uint8_t *z_exp, mp_bf16_t *g_z, mp_bf16_t *h,
+                              mp_bf16_t *g_x, mp_bf16_t *g_w1, mp_bf16_t *g_b1, mp_bf16_t *g_w2,
+                              mp_bf16_t *g_b2, int32_t *dev_status, mp_stream_t stream);
+
 /* ------------------------------------------------------------------------ */
 /* Permute / unpermute  [d9d _permute_kernel, _unpermute_kernel; MBI]        */
 /* ------------------------------------------------------------------------ */

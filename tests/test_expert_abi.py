@@ -104,6 +104,37 @@ def test_expert_wgrad_rejects(lib, new, code):
     assert lib.mp_expert_wgrad(*changed(WGRAD, **new).values()) == code
 
 
+MLP = dict(x=FAKE, w1=FAKE, b1=None, w2=FAKE, b2=None, offsets=FAKE, R=8, E=4, H=64, F=32, O=64,
+           act=5, h=FAKE, y=FAKE, save=0, z=None, z_exp=None, status=None, stream=None)
+
+
+@pytest.mark.parametrize("new,code", [
+    (dict(R=-1), INVALID), (dict(F=0), INVALID), (dict(F=2 ** 22), INVALID), (dict(act=0), INVALID),
+    (dict(act=6), INVALID), (dict(h=None), INVALID), (dict(x=None), INVALID), (dict(w1=None), INVALID),
+    (dict(save=1), INVALID), (dict(H=0), INVALID), (dict(E=1025), UNSUPPORTED),
+    (dict(w2=None), INVALID), (dict(y=None), INVALID), (dict(O=0), INVALID),
+    (dict(R=0, x=None, w1=None, w2=None, h=None, y=None), 0),
+])
+def test_expert_mlp_rejects(lib, new, code):
+    assert lib.mp_expert_mlp(*changed(MLP, **new).values()) == code
+
+
+MLP_BWD = dict(g_y=FAKE, x=FAKE, w1=FAKE, w2=FAKE, offsets=FAKE, R=8, E=4, H=64, F=32, O=64, act=5,
+               save=1, z=FAKE, z_exp=None, g_z=FAKE, h=FAKE, g_x=FAKE, g_w1=FAKE, g_b1=None,
+               g_w2=FAKE, g_b2=None, status=None, stream=None)
+
+
+@pytest.mark.parametrize("new,code", [
+    (dict(R=-1), INVALID), (dict(F=0), INVALID), (dict(O=0), INVALID), (dict(act=0), INVALID),
+    (dict(save=0), INVALID), (dict(save=2), INVALID), (dict(z=None), INVALID), (dict(g_y=None), INVALID),
+    (dict(g_z=None), INVALID), (dict(h=None), INVALID), (dict(offsets=None), INVALID),
+    (dict(w1=None), INVALID), (dict(w2=None), INVALID),
+    (dict(E=5000), UNSUPPORTED),
+])
+def test_expert_mlp_bwd_rejects(lib, new, code):
+    assert lib.mp_expert_mlp_bwd(*changed(MLP_BWD, **new).values()) == code
+
+
 def test_status_bits_have_names():
     assert mp.status_bits(0x80 | 0x100) == {"bad_offsets", "stalled"}
 

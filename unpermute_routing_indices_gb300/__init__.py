@@ -19,7 +19,7 @@ from . import _lib
 __all__ = [
     "MPError", "mp_build_map", "mp_build_map_capacity", "mp_build_map_workspace_size",
     "mp_topk_softmax", "mp_topk_softmax_bwd", "mp_route", "mp_route_bwd", "mp_expert_gemm",
-    "mp_expert_dgrad", "mp_expert_wgrad", "mp_permute", "mp_unpermute", "mp_unpermute_ep", "EP_BF16_PARTIALS", "EP_FP64_CROSS_RANK",
+    "mp_expert_dgrad", "mp_expert_wgrad", "mp_expert_mlp", "mp_expert_mlp_bwd", "mp_permute", "mp_unpermute", "mp_unpermute_ep", "EP_BF16_PARTIALS", "EP_FP64_CROSS_RANK",
     "mp_permute_bwd", "mp_unpermute_bwd", "mp_sort_chunks_pad", "mp_unpad_restore",
     "mp_sort_chunks_pad_bwd", "mp_unpad_restore_bwd", "status_bits", "library_path",
 ]
@@ -344,44 +344,6 @@ def _products(rows, name, w, offsets, width):
     return dev, rows.shape[0], E, N, K
 
 
-# The calls behind the checks: mp_expert_* below, and autograd's backward passes,
-# whose tensors a checked forward pass made.
-
-def _gemm(x, w, offsets, bias, act, residual, out, save, z, z_exp, status):
-    E, N, K = w.shape
-    with _on(x.device):
-        _check("mp_expert_gemm", _lib.load().mp_expert_gemm(
-            x.data_ptr(), w.data_ptr(), offsets.data_ptr(), x.shape[0], E, N, K, _ptr(bias),
-            ACTS[act], _ptr(residual), out.data_ptr(), SAVES[save], _ptr(z), _ptr(z_exp),
-            _ptr(status), _stream(x.device)))
-
-
-def _dgrad(g, w, offsets, act, save, z, z_exp, g_x, h, status=None):
-    E, N, K = w.shape
-    with _on(g.device):
-        _check("mp_expert_dgrad", _lib.load().mp_expert_dgrad(
-            g.data_ptr(), w.data_ptr(), offsets.data_ptr(), g.shape[0], E, N, K, ACTS[act],
-            SAVES[save], _ptr(z), _ptr(z_exp), g_x.data_ptr(), _ptr(h), _ptr(status),
-            _stream(g.device)))
-
-
-def _wgrad(g, x, offsets, accumulate, g_w, g_bias, status=None):
-    E, N, K = g_w.shape
-    with _on(g.device):
-        _check("mp_expert_wgrad", _lib.load().mp_expert_wgrad(
-            g.data_ptr(), x.data_ptr(), offsets.data_ptr(), g.shape[0], E, N, K,
-            DTYPES[g_w.dtype], accumulate, g_w.data_ptr(), _ptr(g_bias), _ptr(status),
-            _stream(g.device)))
-
-
-def _zero_unrouted(rows, offsets):
-    """Zeroes the rows of a bf16 [R,H] from offsets[-1] on."""
-    with _on(rows.device):
-        _check("mp_zero_rows_from", _lib.load().mp_zero_rows_from(
-            rows.data_ptr(), rows.shape[0], 2 * rows.shape[1],
-            offsets.data_ptr() + 4 * (offsets.shape[0] - 1), _stream(rows.device)))
-
-
 def mp_expert_gemm(x, w, offsets, *, bias=None, act: str = "none", residual=None,
                    save: str = "none", out=None, z=None, z_exp=None, status=None):
     """x bf16 [R,K], w bf16 [E,N,K], offsets int32 [E+1] -> (out bf16 [R,F], z, z_exp):
@@ -406,7 +368,10 @@ def mp_expert_gemm(x, w, offsets, *, bias=None, act: str = "none", residual=None
     _shape(out, "out", (R, F))
     z, z_exp = _checkpoint(z, z_exp, R, F, act, save, dev, make=True)
     _opt(status, "status", torch.int32, 1, dev)
-    _gemm(x, w, offsets, bias, act, residual, out, save, z, z_exp, status)
+    with _on(dev):
+        _check("mp_expert_gemm", _lib.load().mp_expert_gemm(
+            _ptr(x), _ptr(w), _ptr(offsets), R, E, N, K, _ptr(bias), ACTS[act], _ptr(residual),
+            _ptr(out), SAVES[save], _ptr(z), _ptr(z_exp), _ptr(status), _stream(dev)))
     return out, z, z_exp
 
 
@@ -437,7 +402,10 @@ def mp_expert_dgrad(g, w, offsets, *, act: str = "none", z=None, z_exp=None,
         _need(h, "h", torch.bfloat16, 2, dev)
         _shape(h, "h", (R, K))
     _opt(status, "status", torch.int32, 1, dev)
-    _dgrad(g, w, offsets, act, save, z, z_exp, g_x, h, status)
+    with _on(dev):
+        _check("mp_expert_dgrad", _lib.load().mp_expert_dgrad(
+            _ptr(g), _ptr(w), _ptr(offsets), R, E, N, K, ACTS[act], SAVES[save], _ptr(z),
+            _ptr(z_exp), _ptr(g_x), _ptr(h), _ptr(status), _stream(dev)))
     return g_x, h
 
 
@@ -469,8 +437,70 @@ def mp_expert_wgrad(g, x, offsets, *, with_bias: bool = False, dtype=torch.bfloa
         _need(g_bias, "g_bias", dtype, 2, dev)
         _shape(g_bias, "g_bias", (E, N))
     _opt(status, "status", torch.int32, 1, dev)
-    _wgrad(g, x, offsets, int(bool(accumulate)), g_w, g_bias, status)
+    with _on(dev):
+        _check("mp_expert_wgrad", _lib.load().mp_expert_wgrad(
+            _ptr(g), _ptr(x), _ptr(offsets), R, E, N, K, DTYPES[dtype], int(bool(accumulate)),
+            _ptr(g_w), _ptr(g_bias), _ptr(status), _stream(dev)))
     return g_w, g_bias
+
+
+def mp_expert_mlp(x, w1, w2, offsets, b1=None, b2=None, *, act: str = "swiglu",
+                  save: str = "none", status=None):
+    """An expert's two products in one call: x bf16 [R,H], w1 bf16 [E,F,H] ([E,2F,H] if act
+    is gated), w2 bf16 [E,O,F] -> (y bf16 [R,O], z, z_exp) with
+    y = act(x w1[e]^T + b1[e]) w2[e]^T + b2[e], zero past the routed rows, and the first
+    product kept as `save` says (mp_expert_gemm)."""
+    dev, R, E, P, H = _products(x, "x", w1, offsets, 2)
+    a, s = _named(act, ACTS, "act"), _named(save, SAVES, "save")
+    _need(w2, "w2", torch.bfloat16, 3, dev)
+    O, F = w2.shape[1], w2.shape[2]
+    _shape(w2, "w2", (E, O, F))
+    if P != F * _parts(act):
+        raise ValueError(f"w1 has {P} columns for the {F} of w2 and act {act}")
+    for b, name, n in ((b1, "b1", P), (b2, "b2", O)):
+        if b is not None:
+            _need(b, name, torch.bfloat16, 2, dev)
+            _shape(b, name, (E, n))
+    _opt(status, "status", torch.int32, 1, dev)
+    h = torch.empty((R, F), dtype=torch.bfloat16, device=dev)
+    y = torch.empty((R, O), dtype=torch.bfloat16, device=dev)
+    z, z_exp = _checkpoint(None, None, R, F, act, save, dev, make=True)
+    with _on(dev):
+        _check("mp_expert_mlp", _lib.load().mp_expert_mlp(
+            _ptr(x), _ptr(w1), _ptr(b1), _ptr(w2), _ptr(b2), _ptr(offsets), R, E, H, F, O, a,
+            _ptr(h), _ptr(y), s, _ptr(z), _ptr(z_exp), _ptr(status), _stream(dev)))
+    return y, z, z_exp
+
+
+def mp_expert_mlp_bwd(g_y, x, w1, w2, offsets, z, z_exp=None, *, act: str = "swiglu",
+                      need=(True, True, True, False, False), status=None):
+    """Gradients of mp_expert_mlp at the kept product z (and z_exp): (g_x, g_w1, g_w2, g_b1,
+    g_b2), bf16, None where `need` is false."""
+    dev, R, E, P, H = _products(x, "x", w1, offsets, 2)
+    _need(w2, "w2", torch.bfloat16, 3, dev)
+    O, F = w2.shape[1], w2.shape[2]
+    _shape(w2, "w2", (E, O, F))
+    _need(g_y, "g_y", torch.bfloat16, 2, dev)
+    _shape(g_y, "g_y", (R, O))
+    a = _named(act, ACTS, "act")
+    if P != F * _parts(act):
+        raise ValueError(f"w1 has {P} columns for the {F} of w2 and act {act}")
+    save = "e4m3" if z_exp is not None else "bf16"
+    _checkpoint(z, z_exp, R, F, act, save, dev, make=False)
+    _opt(status, "status", torch.int32, 1, dev)
+    g_z = torch.empty((R, P), dtype=torch.bfloat16, device=dev)
+    h = torch.empty((R, F), dtype=torch.bfloat16, device=dev) if need[2] else None
+    g_x = torch.empty_like(x) if need[0] else None
+    g_w1 = torch.empty_like(w1) if need[1] else None
+    g_w2 = torch.empty_like(w2) if need[2] else None
+    g_b1 = torch.empty((E, P), dtype=torch.bfloat16, device=dev) if need[3] else None
+    g_b2 = torch.empty((E, O), dtype=torch.bfloat16, device=dev) if need[4] else None
+    with _on(dev):
+        _check("mp_expert_mlp_bwd", _lib.load().mp_expert_mlp_bwd(
+            _ptr(g_y), _ptr(x), _ptr(w1), _ptr(w2), _ptr(offsets), R, E, H, F, O, a, SAVES[save],
+            _ptr(z), _ptr(z_exp), _ptr(g_z), _ptr(h), _ptr(g_x), _ptr(g_w1), _ptr(g_b1),
+            _ptr(g_w2), _ptr(g_b2), _ptr(status), _stream(dev)))
+    return g_x, g_w1, g_w2, g_b1, g_b2
 
 
 # --------------------------------------------------------------------------

@@ -29,6 +29,9 @@ SIGNATURES = {
     "mp_expert_gemm": (I32, [P, P, P, I64, I32, I32, I32, P, I32, P, P, I32, P, P, P, P]),
     "mp_expert_dgrad": (I32, [P, P, P, I64, I32, I32, I32, I32, I32, P, P, P, P, P, P]),
     "mp_expert_wgrad": (I32, [P, P, P, I64, I32, I32, I32, I32, I32, P, P, P, P]),
+    "mp_expert_mlp": (I32, [P, P, P, P, P, P, I64, I32, I32, I32, I32, I32, P, P, I32, P, P, P, P]),
+    "mp_expert_mlp_bwd": (I32, [P, P, P, P, P, I64, I32, I32, I32, I32, I32, I32, P, P, P, P, P, P,
+                                P, P, P, P, P]),
     "mp_permute": (I32, [P, P, P, I64, I32, I32, P, P, P]),
     "mp_unpermute": (I32, [P, P, P, I64, I32, I32, P, P]),
     "mp_unpermute_ep": (I32, [P, P, P, P, I64, I32, I32, I32, I32, I32, P, P]),

@@ -25,8 +25,8 @@ from dataclasses import dataclass
 
 import torch
 
-from . import (_dgrad, _wgrad, _zero_unrouted, mp_build_map, mp_build_map_capacity,
-               mp_expert_gemm, mp_permute, mp_permute_bwd, mp_route, mp_route_bwd,
+from . import (mp_build_map, mp_build_map_capacity, mp_expert_mlp, mp_expert_mlp_bwd,
+               mp_permute, mp_permute_bwd, mp_route, mp_route_bwd,
                mp_sort_chunks_pad, mp_sort_chunks_pad_bwd, mp_topk_softmax,
                mp_topk_softmax_bwd, mp_unpad_restore, mp_unpad_restore_bwd, mp_unpermute,
                mp_unpermute_bwd, mp_unpermute_ep, mp_zero_rows_from)
@@ -137,35 +137,18 @@ class _ExpertMlp(torch.autograd.Function):
     @staticmethod
     def forward(ctx, rows, offsets, w1, w2, b1, b2, act, checkpoint):
         kept = checkpoint if any(ctx.needs_input_grad) else "none"
-        h, z, z_exp = mp_expert_gemm(rows, w1, offsets, bias=b1, act=act, save=kept)
-        y, _, _ = mp_expert_gemm(h, w2, offsets, bias=b2)
-        _zero_unrouted(y, offsets)
+        y, z, z_exp = mp_expert_mlp(rows, w1, w2, offsets, b1, b2, act=act, save=kept)
         ctx.save_for_backward(rows, offsets, w1, w2, z, z_exp)
-        ctx.how = act, kept
+        ctx.act = act
         return y
 
     @staticmethod
     def backward(ctx, g_y):
         rows, offsets, w1, w2, z, z_exp = ctx.saved_tensors
-        act, kept = ctx.how
-        need_x, _, need_w1, need_w2, need_b1, need_b2 = ctx.needs_input_grad[:6]
-        g_y = g_y.contiguous()
-        g_x = g_w1 = g_w2 = g_b1 = g_b2 = None
-        g_z = z.new_empty(z.shape, dtype=rows.dtype)
-        h = g_y.new_empty((g_y.shape[0], w2.shape[2])) if need_w2 or need_b2 else None
-        _dgrad(g_y, w2, offsets, act, kept, z, z_exp, g_z, h)
-        if need_w2 or need_b2:
-            g_w2 = torch.empty_like(w2)
-            g_b2 = w2.new_empty(w2.shape[:2]) if need_b2 else None
-            _wgrad(g_y, h, offsets, 0, g_w2, g_b2)
-        if need_w1 or need_b1:
-            g_w1 = torch.empty_like(w1)
-            g_b1 = w1.new_empty(w1.shape[:2]) if need_b1 else None
-            _wgrad(g_z, rows, offsets, 0, g_w1, g_b1)
-        if need_x:
-            g_x = torch.empty_like(rows)
-            _dgrad(g_z, w1, offsets, "none", "none", None, None, g_x, None)
-            _zero_unrouted(g_x, offsets)
+        need = ctx.needs_input_grad
+        g_x, g_w1, g_w2, g_b1, g_b2 = mp_expert_mlp_bwd(
+            g_y.contiguous(), rows, w1, w2, offsets, z, z_exp, act=ctx.act,
+            need=(need[0], need[2], need[3], need[4], need[5]))
         return g_x, None, g_w1, g_w2, g_b1, g_b2, None, None
 
 

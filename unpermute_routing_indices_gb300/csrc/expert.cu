@@ -81,6 +81,18 @@ mp_status_t sizes_ok(int64_t R, int32_t E, int32_t N, int32_t K)
     return MP_OK;
 }
 
+// g_bias of c.N columns, in bf16 or fp32 (added to if c.epi.add).
+mp_status_t bias_grad(const mp_bf16_t *g, const ExpertCall &c, mp_bf16_t *out, float *out_f32)
+{
+    if (c.N % 8 == 0 && aligned16(g))
+        (void)launch_pdl(k_expert_bias<8>, dim3((c.N + 255) / 256, c.E), BIAS_THREADS, 0, c.stream, g,
+                         c.offsets, c.R, c.E, c.N, out, out_f32, c.epi.add);
+    else
+        (void)launch_pdl(k_expert_bias<1>, dim3((c.N + 31) / 32, c.E), BIAS_THREADS, 0, c.stream, g,
+                         c.offsets, c.R, c.E, c.N, out, out_f32, c.epi.add);
+    return check_launch();
+}
+
 template <int MODE> mp_status_t product(const ExpertCall &c)
 {
     return expert_tc_takes<MODE>(c) ? expert_tc<MODE>(c) : expert_simt<MODE>(c);
@@ -169,13 +181,62 @@ extern "C" mp_status_t mp_expert_wgrad(const mp_bf16_t *g, const mp_bf16_t *x,
     c.stream = as_stream(stream);
     const mp_status_t s = product<WGRAD>(c);
     if (s != MP_OK || g_bias == nullptr) return s;
-    mp_bf16_t *gb = f32 ? nullptr : static_cast<mp_bf16_t *>(g_bias);
-    float *gb32 = f32 ? static_cast<float *>(g_bias) : nullptr;
-    if (N % 8 == 0 && aligned16(g))
-        (void)launch_pdl(k_expert_bias<8>, dim3((N + 255) / 256, E), BIAS_THREADS, 0, c.stream, g,
-                         offsets, c.R, E, N, gb, gb32, c.epi.add);
-    else
-        (void)launch_pdl(k_expert_bias<1>, dim3((N + 31) / 32, E), BIAS_THREADS, 0, c.stream, g,
-                         offsets, c.R, E, N, gb, gb32, c.epi.add);
-    return check_launch();
+    return bias_grad(g, c, f32 ? nullptr : static_cast<mp_bf16_t *>(g_bias),
+                     f32 ? static_cast<float *>(g_bias) : nullptr);
+}
+
+extern "C" mp_status_t mp_expert_mlp(const mp_bf16_t *x, const mp_bf16_t *w1, const mp_bf16_t *b1,
+                                     const mp_bf16_t *w2, const mp_bf16_t *b2,
+                                     const int32_t *offsets, int64_t R, int32_t E, int32_t H,
+                                     int32_t F, int32_t O, int32_t act, mp_bf16_t *h, mp_bf16_t *y,
+                                     int32_t save, void *z, uint8_t *z_exp, int32_t *dev_status,
+                                     mp_stream_t stream)
+{
+    if (!act_ok(act) || act == MP_ACT_NONE || F < 1 || F > (1 << 21)) return MP_ERR_INVALID_ARG;
+    if (const mp_status_t s = sizes_ok(R, E, O, F); s != MP_OK) return s;
+    if (R > 0 && (h == nullptr || w2 == nullptr || y == nullptr)) return MP_ERR_INVALID_ARG;
+    mp_status_t s = mp_expert_gemm(x, w1, offsets, R, E, act_gated(act) ? 2 * F : F, H, b1, act, nullptr,
+                                   h, save, z, z_exp, dev_status, stream);
+    if (s == MP_OK)
+        s = mp_expert_gemm(h, w2, offsets, R, E, O, F, b2, MP_ACT_NONE, nullptr, y, MP_SAVE_NONE,
+                           nullptr, nullptr, dev_status, stream);
+    return s != MP_OK || R == 0 ? s : mp_zero_rows_from(y, R, 2ll * O, offsets + E, stream);
+}
+
+extern "C" mp_status_t mp_expert_mlp_bwd(const mp_bf16_t *g_y, const mp_bf16_t *x,
+                                         const mp_bf16_t *w1, const mp_bf16_t *w2,
+                                         const int32_t *offsets, int64_t R, int32_t E, int32_t H,
+                                         int32_t F, int32_t O, int32_t act, int32_t save,
+                                         const void *z, const uint8_t *z_exp, mp_bf16_t *g_z,
+                                         mp_bf16_t *h, mp_bf16_t *g_x, mp_bf16_t *g_w1,
+                                         mp_bf16_t *g_b1, mp_bf16_t *g_w2, mp_bf16_t *g_b2,
+                                         int32_t *dev_status, mp_stream_t stream)
+{
+    if (!act_ok(act) || act == MP_ACT_NONE || F < 1 || F > (1 << 21)) return MP_ERR_INVALID_ARG;
+    const int32_t P = act_gated(act) ? 2 * F : F;
+    for (const int32_t n : {H, O})
+        if (const mp_status_t s = sizes_ok(R, E, P, n); s != MP_OK) return s;
+    if (offsets == nullptr || (R > 0 && (g_y == nullptr || x == nullptr || g_z == nullptr)) ||
+        (R > 0 && ((g_w2 != nullptr && h == nullptr) || (g_x != nullptr && w1 == nullptr))))
+        return MP_ERR_INVALID_ARG;
+    mp_status_t s = mp_expert_dgrad(g_y, w2, offsets, R, E, O, F, act, save, z, z_exp, g_z, h,
+                                    dev_status, stream);
+    if (s == MP_OK && g_w2 != nullptr)
+        s = mp_expert_wgrad(g_y, h, offsets, R, E, O, F, MP_DTYPE_BF16, 0, g_w2, nullptr, dev_status,
+                            stream);
+    if (s == MP_OK && g_w1 != nullptr)
+        s = mp_expert_wgrad(g_z, x, offsets, R, E, P, H, MP_DTYPE_BF16, 0, g_w1, nullptr, dev_status,
+                            stream);
+    ExpertCall c = {};
+    c.offsets = offsets;
+    c.R = static_cast<int>(R); c.E = E;
+    c.stream = as_stream(stream);
+    c.N = O;
+    if (s == MP_OK && g_b2 != nullptr) s = bias_grad(g_y, c, g_b2, nullptr);
+    c.N = P;
+    if (s == MP_OK && g_b1 != nullptr) s = bias_grad(g_z, c, g_b1, nullptr);
+    if (s != MP_OK || g_x == nullptr || R == 0) return s;
+    s = mp_expert_dgrad(g_z, w1, offsets, R, E, P, H, MP_ACT_NONE, MP_SAVE_NONE, nullptr, nullptr, g_x,
+                        nullptr, dev_status, stream);
+    return s != MP_OK ? s : mp_zero_rows_from(g_x, R, 2ll * H, offsets + E, stream);
 }

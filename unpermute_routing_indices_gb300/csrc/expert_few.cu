@@ -297,12 +297,8 @@ template <bool GATED>
 mp_status_t launch_few(const ExpertCall &c, const CUtensorMap &w, const CUtensorMap &x)
 {
     typedef Few<GATED> L;
-    cudaError_t err = cudaFuncSetAttribute(k_expert_few<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           static_cast<int>(L::smem(c.E)));
-    if (err != cudaSuccess) {
-        set_last_cuda_error(err);
-        return MP_ERR_CUDA;
-    }
+    static std::atomic<uint64_t> allowed{0};
+    if (!allow_smem(k_expert_few<GATED>, allowed, L::smem(MP_MAX_EXPERTS))) return MP_ERR_CUDA;
     // The most tiles that any offsets give, and CTAs that the SMs hold at once.
     const int64_t most = static_cast<int64_t>(c.R / FT + (c.R < c.E ? c.R : c.E)) * ((c.epi.cols + FM - 1) / FM);
     const int64_t room = (L::smem(c.E) <= HALF_SM ? 2 : 1) * sm_count();

@@ -21,10 +21,12 @@ namespace mp {
 
 int sm_count()
 {
+    static std::atomic<int> known[64];
     int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
-        return 1;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 1;
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 
@@ -392,12 +394,8 @@ bool store_map(StoreMaps &m, int which, const void *base, int64_t parts, int64_t
 template <int MODE, bool GATED> mp_status_t launch_tc(const ExpertCall &c, const CUtensorMap &a,
                                                       const CUtensorMap &b, const StoreMaps &m)
 {
-    const cudaError_t err = cudaFuncSetAttribute(
-        k_expert_tc<MODE, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(TC_SMEM));
-    if (err != cudaSuccess) {
-        set_last_cuda_error(err);
-        return MP_ERR_CUDA;
-    }
+    static std::atomic<uint64_t> allowed{0};
+    if (!allow_smem(k_expert_tc<MODE, GATED>, allowed, TC_SMEM)) return MP_ERR_CUDA;
     const int64_t nt = (c.epi.cols + (GATED ? BN / 2 : BN) - 1) / (GATED ? BN / 2 : BN);
     const int64_t mt = MODE == WGRAD ? static_cast<int64_t>(c.E) * ((c.N + BM - 1) / BM)
                                      : c.R / BM + (c.R < c.E ? c.R : c.E);

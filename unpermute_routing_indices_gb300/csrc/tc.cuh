@@ -4,6 +4,8 @@
 
 #include <cuda.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace mp {
@@ -196,5 +198,19 @@ __host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool a_across, boo
 // False: the driver refused.
 bool make_map(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, const uint32_t *box);
 int sm_count();
+
+// Lets `kernel` have `bytes` of dynamic shared memory, once a device.
+template <typename K> bool allow_smem(K kernel, std::atomic<uint64_t> &done, size_t bytes)
+{
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+    if (err == cudaSuccess && !(done.load(std::memory_order_relaxed) & bit)) {
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+        if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    }
+    if (err != cudaSuccess) set_last_cuda_error(err);
+    return err == cudaSuccess;
+}
 
 }  // namespace mp
