@@ -93,6 +93,8 @@ COUNTS = {
     "tokens": [0, 1, 0, 1, 1, 0, 0, 1],
     "few each": [5, 9, 2, 8, 3, 16, 17, 1],
     "big": [300, 513, 128, 1000],
+    "long": [1500, 700, 1031],       # enough rows an expert for pairs of CTAs, all three ragged
+    "long, one empty": [2111, 0, 1985],
 }
 
 # counts, N (columns of w), K, activation, bias, residual, shift of x
@@ -115,6 +117,9 @@ PRODUCTS = [
     ("big", 640, 192, "none", True, True, 0),
     ("many", 64, 64, "gelu", True, False, 1),      # 2-byte aligned rows
     ("many", 128, 128, "silu", True, True, 8),     # 16-byte, not 32-byte aligned
+    ("long", 2 * 136, 200, "swiglu", True, True, 0),
+    ("long", 264, 320, "gelu", False, True, 0),
+    ("long, one empty", 2 * 256, 128, "geglu", False, False, 0),
 ]
 
 
@@ -181,6 +186,8 @@ DGRADS = [
     ("big", 576, 256, "geglu", "e4m3"),
     ("big", 192, 640, "none", None),
     ("big", 256, 328, "swiglu", "bf16"),
+    ("long", 192, 264, "swiglu", "e4m3"),
+    ("long, one empty", 320, 136, "none", None),
 ]
 
 
@@ -232,6 +239,7 @@ WGRADS = [
     ("many", 136, 72, True), ("many", 33, 37, True), ("first empty", 264, 520, True),
     ("first empty", 257, 128, False), ("tokens", 128, 264, True), ("few each", 256, 384, True),
     ("big", 192, 576, True), ("big", 520, 264, False), ("one expert", 384, 512, True),
+    ("long", 264, 520, True), ("long, one empty", 136, 264, False), ("long", 512, 256, False),
 ]
 
 

@@ -39,23 +39,10 @@ constexpr size_t HALF_SM = 233472 / 2 - 1024;
 static_assert(Few<true>::smem(480) <= HALF_SM && Few<false>::smem(MP_MAX_EXPERTS) <= HALF_SM, "two CTAs on an SM");
 static_assert(2 * FM * FT * 4 <= Few<true>::STAGES * Few<true>::STAGE, "partial sums fit the ring");
 
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                     : "memory");
-}
 __device__ __forceinline__ float peer_value(uint32_t addr, uint32_t rank)
 {
-    uint32_t at;
     float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at_rank(addr, rank)) : "memory");
     return v;
 }
 

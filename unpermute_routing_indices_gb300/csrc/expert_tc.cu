@@ -1,7 +1,8 @@
 // The experts' products on the tensor cores.
 //
 // One persistent kernel for the three products, a CTA per SM.  A tile is 128
-// rows by 256 columns (128 gate and 128 other columns when gated) of one expert:
+// rows by 256 columns (128 gate and 128 other columns when gated) of one expert,
+// or 256 rows for a pair of CTAs, which read half of B each:
 //   FWD    rows of x by rows of w[e], contraction along both rows
 //   DGRAD  rows of g along, w[e] across (its columns are the result's)
 //   WGRAD  g and x both across: the contraction is over the expert's rows
@@ -14,6 +15,9 @@
 // computed and dropped (FWD, DGRAD).  In WGRAD, where they would enter the sums,
 // the last slice's rows up to the next 16 are overwritten with zeros in shared
 // memory, whatever they held.
+// What bounds it: for experts of many rows the tensor cores (131,072 x 4,096 by 128
+// experts of 2,048 columns in 1,211 us, 1.82 PFLOP/s, 0.92 of cuBLAS's measured
+// 8,192^3); for few rows the bytes of weights and results and the epilogue.
 #include "expert.cuh"
 #include "tc.cuh"
 
@@ -72,40 +76,49 @@ bool make_map(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, 
 
 namespace {
 
-constexpr int BM = 128, BN = 256, BK = 64;
-constexpr int STAGES = 4;
+constexpr int BM = 128, BN = 256, BK = 64;   // one CTA's rows, columns, depth of a slice
+constexpr int A_BYTES = BM * BK * 2;
+constexpr int BOX_BYTES = 64 * 64 * 2;       // a box of 64 rows
+constexpr int TMEM_COLS = 2 * BN;
+// CG CTAs share a tile of CG * 128 rows and 256 columns; each holds 256 / CG rows
+// of B.
+template <int CG> struct Ring {
+    static constexpr int STAGES = CG == 1 ? 4 : 6;
+    static constexpr int B_BYTES = BN / CG * BK * 2;
+    static constexpr int STAGE = A_BYTES + B_BYTES;
+};
+constexpr int RING_BYTES = Ring<1>::STAGES * Ring<1>::STAGE;
+static_assert(RING_BYTES == Ring<2>::STAGES * Ring<2>::STAGE, "one layout");
+constexpr int MOST_STAGES = 6;
 constexpr int EPI_WARPS = 8;   // two for each quarter of the accumulator's lanes
 constexpr int TC_THREADS = 64 + 32 * EPI_WARPS;
-constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr int BOX_BYTES = 64 * 64 * 2;   // a box of 64 rows
-constexpr int TMEM_COLS = 2 * BN;
-
 constexpr int STAGING = 32 * EPI_COLS * 2;   // bytes of one warp's tile on its way out
 
 struct TcShared {
-    uint64_t full[STAGES], empty[STAGES], acc_full[2], acc_empty[2], drained;
+    uint64_t full[MOST_STAGES], peer_full[MOST_STAGES], empty[MOST_STAGES], acc_full[2], acc_empty[2], drained;
     uint32_t tmem;
     int gave_up;
     int start[MP_MAX_EXPERTS + 1], tiles[MP_MAX_EXPERTS + 1];
 };
-constexpr size_t TC_SMEM = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * STAGING + sizeof(TcShared);
+constexpr size_t TC_SMEM = 1024 + RING_BYTES + EPI_WARPS * STAGING + sizeof(TcShared);
 static_assert(TC_SMEM <= 232448, "shared memory of one SM");
 
 struct Tile {
-    int e, m0, m1, c0, row0, depth;   // rows [m0,m1) of the result (of g's columns in WGRAD)
+    int e, m0, m1, c0, row0, depth;   // rows from m0 (this CTA's) up to m1 of the result (of g's columns in WGRAD)
 };
 
-template <int MODE>
+template <int MODE, int CG>
 __device__ __forceinline__ Tile tile_at(const ExpertCall &c, const int *start, const int *tiles,
-                                        int64_t t, int nt, int tile_cols)
+                                        int64_t t, int nt, int tile_cols, int rank)
 {
+    constexpr int TM = CG * BM;
     Tile r;
     if (MODE == WGRAD) {
-        const int mt = (c.N + BM - 1) / BM;
+        const int mt = (c.N + TM - 1) / TM;
         const int64_t per = static_cast<int64_t>(mt) * nt;
         r.e = static_cast<int>(t / per);
         const int64_t at = t - r.e * per;
-        r.m0 = static_cast<int>(at % mt) * BM;
+        r.m0 = static_cast<int>(at % mt) * TM + rank * BM;
         r.m1 = c.N;
         r.c0 = static_cast<int>(at / mt) * tile_cols;
         r.row0 = start[r.e];
@@ -114,7 +127,7 @@ __device__ __forceinline__ Tile tile_at(const ExpertCall &c, const int *start, c
         r.e = expert_of_tile(tiles, c.E, static_cast<int>(t / nt));
         const int mt = tiles[r.e + 1] - tiles[r.e];
         const int64_t at = t - static_cast<int64_t>(tiles[r.e]) * nt;
-        r.m0 = start[r.e] + static_cast<int>(at % mt) * BM;
+        r.m0 = start[r.e] + static_cast<int>(at % mt) * TM + rank * BM;
         r.m1 = start[r.e + 1];
         r.c0 = static_cast<int>(at / mt) * tile_cols;
         r.row0 = 0;
@@ -191,15 +204,33 @@ __device__ __forceinline__ void epi_prefetch(const ExpertEpi &p, int64_t row, in
     }
 }
 
-template <int MODE, bool GATED>
+// A slice of `rows` rows, contraction across them: zeroes the rows up to the next
+// 16 in every box (128 bytes each, whatever the swizzle), for the products to read,
+// and returns how many steps of 16 there are.
+template <int CG> __device__ __forceinline__ int zero_ragged(uint8_t *tile, int rows, int lane)
+{
+    const int steps = (rows + 15) / 16, n = 16 * steps - rows;
+    for (int v = lane; v < n * (Ring<CG>::STAGE / BOX_BYTES) * 8; v += 32) {
+        const int row = rows + (v >> 3) % n, box = (v >> 3) / n;
+        *reinterpret_cast<uint4 *>(tile + box * BOX_BYTES + row * 128 + (v & 7) * 16) = make_uint4(0, 0, 0, 0);
+    }
+    fence_async_smem();
+    __syncwarp();
+    return steps;
+}
+
+template <int MODE, bool GATED, int CG>
 __global__ void __launch_bounds__(TC_THREADS, 1)
     k_expert_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                 const __grid_constant__ StoreMaps stores, const ExpertCall c)
 {
+    typedef Ring<CG> L;
+    constexpr int STAGES = L::STAGES;
     extern __shared__ uint8_t raw[];
     uint8_t *ring = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-    TcShared &s = *reinterpret_cast<TcShared *>(ring + STAGES * STAGE_BYTES + EPI_WARPS * STAGING);
+    TcShared &s = *reinterpret_cast<TcShared *>(ring + RING_BYTES + EPI_WARPS * STAGING);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = CG == 2 ? static_cast<int>(cluster_rank()) : 0;
     volatile int *gave_up = &s.gave_up;
 
     if (threadIdx.x == 0) {
@@ -207,26 +238,31 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         tma_prefetch(&map_b);
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(smem_u32(&s.full[i]), 1);
+            mbar_init(smem_u32(&s.peer_full[i]), 1);
             mbar_init(smem_u32(&s.empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&s.acc_full[i]), 1);
-            mbar_init(smem_u32(&s.acc_empty[i]), EPI_WARPS);
+            mbar_init(smem_u32(&s.acc_empty[i]), CG * EPI_WARPS);
         }
         mbar_init(smem_u32(&s.drained), 1);
         mbar_init_fence();
         s.gave_up = 0;
     }
-    if (warp == 1) tmem_alloc(smem_u32(&s.tmem), TMEM_COLS);
+    __syncwarp();
+    if (warp == 1) tmem_alloc<CG>(smem_u32(&s.tmem), TMEM_COLS);
     tc_fence_before();
-    __syncthreads();
+    if (CG == 2)
+        cluster_sync();   // the other CTA's barriers exist
+    else
+        __syncthreads();
     tc_fence_after();
     // Only now may the next kernel start: one that took this SM's TMEM and then
     // waited for this kernel would never see it end.
     pdl_trigger();
     pdl_wait();
     if (warp == 0)
-        expert_starts(c.offsets, c.E, c.R, BM, lane, s.start, s.tiles,
+        expert_starts(c.offsets, c.E, c.R, CG * BM, lane, s.start, s.tiles,
                       blockIdx.x == 0 ? c.status : nullptr);
     __syncthreads();
 
@@ -234,48 +270,65 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     constexpr int tile_cols = GATED ? BN / 2 : BN;
     const int nt = (c.epi.cols + tile_cols - 1) / tile_cols;
     const int64_t total = MODE == WGRAD
-                              ? static_cast<int64_t>(c.E) * ((c.N + BM - 1) / BM) * nt
+                              ? static_cast<int64_t>(c.E) * ((c.N + CG * BM - 1) / (CG * BM)) * nt
                               : static_cast<int64_t>(s.tiles[c.E]) * nt;
-    constexpr uint32_t idesc = mma_desc(BM, BN, MODE == WGRAD, MODE != FWD);
+    const int64_t first = blockIdx.x / CG, step = gridDim.x / CG;
+    constexpr uint32_t idesc = mma_desc(CG * BM, BN, MODE == WGRAD, MODE != FWD);
 
     if (warp == 0) {
         if (lane == 0) {
             uint32_t n = 0;   // slices loaded so far
-            for (int64_t t = blockIdx.x; t < total && !*gave_up; t += gridDim.x) {
-                const Tile w = tile_at<MODE>(c, s.start, s.tiles, t, nt, tile_cols);
+            for (int64_t t = first; t < total && !*gave_up; t += step) {
+                const Tile w = tile_at<MODE, CG>(c, s.start, s.tiles, t, nt, tile_cols, rank);
+                const int part = rank * (BN / 2);   // of B's 256 rows or columns
                 for (int k = 0; k < w.depth; k += BK, ++n) {
                     const int i = n % STAGES;
                     if (!mbar_wait(smem_u32(&s.empty[i]), ((n / STAGES) & 1) ^ 1, gave_up)) break;
-                    const uint32_t bar = smem_u32(&s.full[i]);
-                    const uint32_t a = smem_u32(ring + i * STAGE_BYTES), b = a + A_BYTES;
-                    mbar_expect(bar, STAGE_BYTES);
+                    uint32_t bar = smem_u32(&s.full[i]);
+                    const uint32_t a = smem_u32(ring + i * L::STAGE), b = a + A_BYTES;
+                    // In a pair both CTAs' copies arrive at CTA 0's barrier, but those
+                    // of a ragged slice, which CTA 1 has to see itself.
+                    if (CG == 1 || (MODE == WGRAD && k + BK > w.depth))
+                        mbar_expect(bar, L::STAGE);
+                    else if (rank == 0)
+                        mbar_expect(bar, 2 * L::STAGE);
+                    else
+                        bar = at_rank(bar, 0);
                     if (MODE == WGRAD) {
                         for (int j = 0; j < BM / 64; ++j)
-                            tma_load(a + j * BOX_BYTES, &map_a, bar, w.m0 + 64 * j, w.row0 + k);
-                        for (int j = 0; j < BN / 64; ++j)
-                            tma_load(b + j * BOX_BYTES, &map_b, bar, w.c0 + 64 * j, w.row0 + k);
+                            tma_load<CG>(a + j * BOX_BYTES, &map_a, bar, w.m0 + 64 * j, w.row0 + k);
+                        for (int j = 0; j < BN / CG / 64; ++j)
+                            tma_load<CG>(b + j * BOX_BYTES, &map_b, bar, w.c0 + part + 64 * j, w.row0 + k);
                     } else {
-                        tma_load(a, &map_a, bar, k, w.m0);
+                        tma_load<CG>(a, &map_a, bar, k, w.m0);
                         if (MODE == FWD) {
-                            tma_load(b, &map_b, bar, k, w.c0, w.e);
-                            tma_load(b + B_BYTES / 2, &map_b, bar, k,
-                                     GATED ? c.epi.cols + w.c0 : w.c0 + BN / 2, w.e);
+                            // 128 rows of w at a time: the gate's and the others', or neighbours.
+                            for (int j = rank; j < rank + 2 / CG; ++j)
+                                tma_load<CG>(b + (j - rank) * A_BYTES, &map_b, bar, k,
+                                             w.c0 + j * (GATED ? c.epi.cols : BN / 2), w.e);
                         } else {
-                            for (int j = 0; j < BN / 64; ++j)
-                                tma_load(b + j * BOX_BYTES, &map_b, bar, w.c0 + 64 * j, k, w.e);
+                            for (int j = 0; j < BN / CG / 64; ++j)
+                                tma_load<CG>(b + j * BOX_BYTES, &map_b, bar, w.c0 + part + 64 * j, k, w.e);
                         }
                     }
                 }
             }
-            if (*gave_up)   // the copies still in flight end before the CTA does
-                for (uint32_t q = n > STAGES ? n - STAGES : 0; q < n; ++q)
-                    mbar_drain(smem_u32(&s.full[q % STAGES]), (q / STAGES) & 1);
+            if (*gave_up) {   // the copies still in flight end before the CTA does
+                if (rank == 0) {
+                    for (uint32_t q = n > STAGES ? n - STAGES : 0; q < n; ++q)
+                        mbar_drain(smem_u32(&s.full[q % STAGES]), (q / STAGES) & 1);
+                } else {   // theirs are the other CTA's barriers: wait by the clock
+                    const uint64_t t0 = now_ns();
+                    while (now_ns() - t0 < 100000000ull) __nanosleep(1000);
+                }
+            }
         }
-    } else if (warp == 1) {
+    } else if (warp == 1 && rank == 0) {
         uint32_t n = 0, it = 0;   // slices and accumulators used so far
+        uint32_t ragged = 0;      // bit i: the phase of stage i's ragged slices
         bool ok = true;
-        for (int64_t t = blockIdx.x; t < total && ok; t += gridDim.x) {
-            const Tile w = tile_at<MODE>(c, s.start, s.tiles, t, nt, tile_cols);
+        for (int64_t t = first; t < total && ok; t += step) {
+            const Tile w = tile_at<MODE, CG>(c, s.start, s.tiles, t, nt, tile_cols, rank);
             if (w.depth == 0) continue;
             const int acc = it & 1;
             ok = __all_sync(FULL_MASK, mbar_wait(smem_u32(&s.acc_empty[acc]), ((it >> 1) & 1) ^ 1, gave_up));
@@ -286,48 +339,60 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 const int i = n % STAGES;
                 ok = __all_sync(FULL_MASK, mbar_wait(smem_u32(&s.full[i]), (n / STAGES) & 1, gave_up));
                 if (!ok) break;
-                uint8_t *tile = ring + i * STAGE_BYTES;
+                uint8_t *tile = ring + i * L::STAGE;
                 int steps = BK / 16;
                 if (MODE == WGRAD && k + BK > w.depth) {
-                    const int rows = w.depth - k;
-                    steps = (rows + 15) / 16;
-                    // Rows [rows, 16 steps) of the six boxes: 128 bytes each, whatever the swizzle.
-                    for (int v = lane; v < (16 * steps - rows) * (STAGE_BYTES / BOX_BYTES) * 8; v += 32) {
-                        const int row = rows + (v >> 3) % (16 * steps - rows);
-                        const int box = (v >> 3) / (16 * steps - rows);
-                        *reinterpret_cast<uint4 *>(tile + box * BOX_BYTES + row * 128 + (v & 7) * 16) =
-                            make_uint4(0, 0, 0, 0);
+                    steps = zero_ragged<CG>(tile, w.depth - k, lane);
+                    if (CG == 2) {
+                        ok = __all_sync(FULL_MASK, mbar_wait(smem_u32(&s.peer_full[i]), (ragged >> i) & 1, gave_up));
+                        if (!ok) break;
+                        ragged ^= 1u << i;
                     }
-                    fence_async_smem();
-                    __syncwarp();
                 }
                 tc_fence_after();
                 if (lane == 0) {
                     const uint32_t a = smem_u32(tile), b = a + A_BYTES;
                     for (int q = 0; q < steps; ++q)
-                        tc_mma(d, tile_desc(a + q * (MODE == WGRAD ? 2048 : 32), BOX_BYTES),
-                               tile_desc(b + q * (MODE == FWD ? 32 : 2048), BOX_BYTES), idesc,
-                               (k | q) != 0);
-                    tc_commit(smem_u32(&s.empty[i]));
+                        tc_mma<CG>(d, tile_desc(a + q * (MODE == WGRAD ? 2048 : 32), BOX_BYTES),
+                                   tile_desc(b + q * (MODE == FWD ? 32 : 2048), BOX_BYTES), idesc,
+                                   (k | q) != 0);
+                    tc_commit<CG>(smem_u32(&s.empty[i]));
                 }
                 __syncwarp();
             }
-            if (ok && lane == 0) tc_commit(smem_u32(&s.acc_full[acc]));
+            if (ok && lane == 0) tc_commit<CG>(smem_u32(&s.acc_full[acc]));
             __syncwarp();
             ++it;
         }
         if (!ok && lane == 0) {
-            tc_commit(smem_u32(&s.drained));
+            tc_commit<CG>(smem_u32(&s.drained));
             mbar_drain(smem_u32(&s.drained), 0);
             or_status(c.status, MP_STATUS_STALLED);
         }
-    } else {
+    } else if (warp == 1 && MODE == WGRAD) {
+        // CTA 1 of a pair: zeroes its part of the ragged slices, and says so.
+        uint32_t n = 0, ragged = 0;
+        bool ok = true;
+        for (int64_t t = first; t < total && ok; t += step) {
+            const Tile w = tile_at<MODE, CG>(c, s.start, s.tiles, t, nt, tile_cols, rank);
+            n += (w.depth + BK - 1) / BK;
+            if (w.depth % BK == 0) continue;
+            const int i = (n - 1) % STAGES;
+            ok = __all_sync(FULL_MASK, mbar_wait(smem_u32(&s.full[i]), (ragged >> i) & 1, gave_up));
+            if (!ok) break;
+            ragged ^= 1u << i;
+            zero_ragged<CG>(ring + i * L::STAGE, w.depth % BK, lane);
+            if (lane == 0) mbar_arrive_cluster(at_rank(smem_u32(&s.peer_full[i]), 0));
+            __syncwarp();
+        }
+        if (!ok && lane == 0) or_status(c.status, MP_STATUS_STALLED);
+    } else if (warp >= 2) {
         const int quad = warp & 3;            // the TMEM lanes this warp can read
         const int half = (warp - 2) >> 2;     // and its half of the columns
-        WarpWriter out = {ring + STAGES * STAGE_BYTES + (warp - 2) * STAGING, stores, lane, 0};
+        WarpWriter out = {ring + RING_BYTES + (warp - 2) * STAGING, stores, lane, 0};
         uint32_t it = 0;
-        for (int64_t t = blockIdx.x; t < total; t += gridDim.x) {
-            const Tile w = tile_at<MODE>(c, s.start, s.tiles, t, nt, tile_cols);
+        for (int64_t t = first; t < total; t += step) {
+            const Tile w = tile_at<MODE, CG>(c, s.start, s.tiles, t, nt, tile_cols, rank);
             if (MODE == WGRAD && w.depth == 0 && c.epi.add) continue;   // nothing to add
             out.rows = min(w.m1 - (w.m0 + quad * 32), 32);
             const bool valid = lane < out.rows;
@@ -366,17 +431,26 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             if (w.depth != 0) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&s.acc_empty[acc]));
+                if (lane == 0) {
+                    if (CG == 1)
+                        mbar_arrive(smem_u32(&s.acc_empty[acc]));
+                    else
+                        mbar_arrive_cluster(at_rank(smem_u32(&s.acc_empty[acc]), 0));
+                }
                 ++it;
             }
         }
         if (lane == 0) tma_store_done();
     }
+    __syncwarp();
     tc_fence_before();
-    __syncthreads();
+    if (CG == 2)
+        cluster_sync();   // the pair's products and arrivals are done
+    else
+        __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_free(tmem, TMEM_COLS);
+        tmem_free<CG>(tmem, TMEM_COLS);
     }
 }
 
@@ -391,18 +465,64 @@ bool store_map(StoreMaps &m, int which, const void *base, int64_t parts, int64_t
     return !m.use[which] || make_map(&m.map[which], base, 2, dims, box);
 }
 
-template <int MODE, bool GATED> mp_status_t launch_tc(const ExpertCall &c, const CUtensorMap &a,
-                                                      const CUtensorMap &b, const StoreMaps &m)
+// Pairs of CTAs that the device holds at once.
+template <typename K> int pair_count(K kernel)
+{
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = 2;
+    cfg.blockDim = TC_THREADS;
+    cfg.dynamicSmemBytes = TC_SMEM;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) n = sm_count() / 2;
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+template <int MODE, bool GATED, int CG>
+mp_status_t launch_tc(const ExpertCall &c, const CUtensorMap &a, const CUtensorMap &b, const StoreMaps &m)
 {
     static std::atomic<uint64_t> allowed{0};
-    if (!allow_smem(k_expert_tc<MODE, GATED>, allowed, TC_SMEM)) return MP_ERR_CUDA;
+    if (!allow_smem(k_expert_tc<MODE, GATED, CG>, allowed, TC_SMEM)) return MP_ERR_CUDA;
     const int64_t nt = (c.epi.cols + (GATED ? BN / 2 : BN) - 1) / (GATED ? BN / 2 : BN);
-    const int64_t mt = MODE == WGRAD ? static_cast<int64_t>(c.E) * ((c.N + BM - 1) / BM)
-                                     : c.R / BM + (c.R < c.E ? c.R : c.E);
-    const int64_t tiles = nt * mt, sms = sm_count();
-    (void)launch_pdl(k_expert_tc<MODE, GATED>, static_cast<unsigned>(tiles < sms ? tiles : sms),
-                     TC_THREADS, TC_SMEM, c.stream, a, b, m, c);
+    const int64_t mt = MODE == WGRAD ? static_cast<int64_t>(c.E) * ((c.N + CG * BM - 1) / (CG * BM))
+                                     : c.R / (CG * BM) + (c.R < c.E ? c.R : c.E);
+    const int64_t tiles = nt * mt, room = CG == 1 ? sm_count() : pair_count(k_expert_tc<MODE, GATED, CG>);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = static_cast<unsigned>(CG * (tiles < room ? tiles : room));
+    cfg.blockDim = TC_THREADS;
+    cfg.dynamicSmemBytes = TC_SMEM;
+    cfg.stream = c.stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CG == 1 ? 1 : 2;
+    (void)cudaLaunchKernelEx(&cfg, k_expert_tc<MODE, GATED, CG>, a, b, m, c);
     return check_launch();
+}
+
+// Whether pairs of CTAs take the call.  A pair reads a third less per product from
+// L2, which bounds the single CTAs: 131,072 x 4,096 rows by 128 experts of 2,048
+// 1,377 -> 1,211 us; weight gradients of 8 x 2,048 rows, 4,096 x 4,096, 370 -> 344.
+// But its tile has 256 rows, of which an expert leaves half of one empty on
+// average: 384 rows an expert 175 -> 197 us, 512 rows 752 -> 638.  In WGRAD the
+// rows are the contraction, and with few of them the hand-over of the accumulator
+// between the CTAs counts: 128 rows an expert 223 -> 372 us, 384 rows 193 -> 198.
+template <int MODE> bool in_pairs(const ExpertCall &c)
+{
+    return c.R >= (MODE == WGRAD ? 1024 : 512) * static_cast<int64_t>(c.E);
 }
 
 }  // namespace
@@ -435,8 +555,10 @@ template <int MODE> mp_status_t expert_tc(const ExpertCall &c)
         set_last_cuda_error(cudaErrorInvalidValue);
         return MP_ERR_CUDA;
     }
-    if (MODE == FWD && act_gated(c.epi.act)) return launch_tc<MODE, MODE == FWD>(c, a, b, m);
-    return launch_tc<MODE, false>(c, a, b, m);
+    if (MODE == FWD && act_gated(c.epi.act))
+        return in_pairs<MODE>(c) ? launch_tc<MODE, MODE == FWD, 2>(c, a, b, m)
+                                 : launch_tc<MODE, MODE == FWD, 1>(c, a, b, m);
+    return in_pairs<MODE>(c) ? launch_tc<MODE, false, 2>(c, a, b, m) : launch_tc<MODE, false, 1>(c, a, b, m);
 }
 
 template bool expert_tc_takes<FWD>(const ExpertCall &);
