@@ -12,8 +12,8 @@ constexpr int BIAS_THREADS = 256, BIAS_WARPS = BIAS_THREADS / 32;
 // g_bias[e,n] = sum over the expert's rows of g[row,n], in fp32.  A CTA owns 32 V
 // columns of one expert, V = 8 (16-byte loads) where rows are aligned to it; each
 // warp takes every eighth row, four of them in flight, and the eight sums are
-// added in order.  Bound by the bytes of g: 32,768 x 1,024, 256 experts in
-// 14 us (4.8 TB/s); with one column a lane it took 55.
+// added in order.  The tensor-core form of the weight gradient makes these sums
+// itself; this serves the other form, and biases whose weights want no gradient.
 template <int V>
 __global__ void __launch_bounds__(BIAS_THREADS)
     k_expert_bias(const mp_bf16_t *__restrict__ g, const int32_t *__restrict__ offsets, int R,
@@ -25,6 +25,7 @@ __global__ void __launch_bounds__(BIAS_THREADS)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.y;
     // The clamped offsets of this expert: the largest up to each.
     int a = 0, b = 0;
+#pragma unroll 8
     for (int i = lane; i <= e + 1; i += 32) {
         const int v = min(max(__ldg(offsets + i), 0), R);
         b = max(b, v);
@@ -96,6 +97,21 @@ mp_status_t bias_grad(const mp_bf16_t *g, const ExpertCall &c, mp_bf16_t *out, f
 template <int MODE> mp_status_t product(const ExpertCall &c)
 {
     return expert_tc_takes<MODE>(c) ? expert_tc<MODE>(c) : expert_simt<MODE>(c);
+}
+
+// g_w as c.epi has it, and g_bias (NULL: not wanted): within the product, or by a
+// kernel of its own after the slower form.
+mp_status_t weight_grad(ExpertCall &c, void *g_bias, bool f32)
+{
+    mp_bf16_t *b = f32 ? nullptr : static_cast<mp_bf16_t *>(g_bias);
+    float *b32 = f32 ? static_cast<float *>(g_bias) : nullptr;
+    if (expert_tc_takes<WGRAD>(c)) {
+        c.epi.g_bias = b;
+        c.epi.g_bias_f32 = b32;
+        return expert_tc<WGRAD>(c);
+    }
+    const mp_status_t s = expert_simt<WGRAD>(c);
+    return s != MP_OK || g_bias == nullptr ? s : bias_grad(c.a, c, b, b32);
 }
 
 bool act_ok(int32_t act) { return act >= MP_ACT_NONE && act <= MP_ACT_SWIGLU; }
@@ -179,10 +195,7 @@ extern "C" mp_status_t mp_expert_wgrad(const mp_bf16_t *g, const mp_bf16_t *x,
     c.epi.add = accumulate != 0;
     c.status = dev_status;
     c.stream = as_stream(stream);
-    const mp_status_t s = product<WGRAD>(c);
-    if (s != MP_OK || g_bias == nullptr) return s;
-    return bias_grad(g, c, f32 ? nullptr : static_cast<mp_bf16_t *>(g_bias),
-                     f32 ? static_cast<float *>(g_bias) : nullptr);
+    return weight_grad(c, g_bias, f32);
 }
 
 extern "C" mp_status_t mp_expert_mlp(const mp_bf16_t *x, const mp_bf16_t *w1, const mp_bf16_t *b1,
@@ -222,19 +235,18 @@ extern "C" mp_status_t mp_expert_mlp_bwd(const mp_bf16_t *g_y, const mp_bf16_t *
     mp_status_t s = mp_expert_dgrad(g_y, w2, offsets, R, E, O, F, act, save, z, z_exp, g_z, h,
                                     dev_status, stream);
     if (s == MP_OK && g_w2 != nullptr)
-        s = mp_expert_wgrad(g_y, h, offsets, R, E, O, F, MP_DTYPE_BF16, 0, g_w2, nullptr, dev_status,
-                            stream);
+        s = mp_expert_wgrad(g_y, h, offsets, R, E, O, F, MP_DTYPE_BF16, 0, g_w2, g_b2, dev_status, stream);
     if (s == MP_OK && g_w1 != nullptr)
-        s = mp_expert_wgrad(g_z, x, offsets, R, E, P, H, MP_DTYPE_BF16, 0, g_w1, nullptr, dev_status,
-                            stream);
+        s = mp_expert_wgrad(g_z, x, offsets, R, E, P, H, MP_DTYPE_BF16, 0, g_w1, g_b1, dev_status, stream);
+    // A bias's gradient without its weights'.
     ExpertCall c = {};
     c.offsets = offsets;
     c.R = static_cast<int>(R); c.E = E;
     c.stream = as_stream(stream);
     c.N = O;
-    if (s == MP_OK && g_b2 != nullptr) s = bias_grad(g_y, c, g_b2, nullptr);
+    if (s == MP_OK && g_b2 != nullptr && g_w2 == nullptr) s = bias_grad(g_y, c, g_b2, nullptr);
     c.N = P;
-    if (s == MP_OK && g_b1 != nullptr) s = bias_grad(g_z, c, g_b1, nullptr);
+    if (s == MP_OK && g_b1 != nullptr && g_w1 == nullptr) s = bias_grad(g_z, c, g_b1, nullptr);
     if (s != MP_OK || g_x == nullptr || R == 0) return s;
     s = mp_expert_dgrad(g_z, w1, offsets, R, E, P, H, MP_ACT_NONE, MP_SAVE_NONE, nullptr, nullptr, g_x,
                         nullptr, dev_status, stream);

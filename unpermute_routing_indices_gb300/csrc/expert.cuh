@@ -289,7 +289,9 @@ struct ExpertEpi {
     uint8_t *z_exp;           // [R, parts*ckpt_blocks(cols)]
     mp_bf16_t *h;             // DGRAD: act(z) [R,cols] or NULL
     float *out_f32;           // WGRAD: fp32 gradient in place of `out`
-    bool add;                 // WGRAD: add to out_f32
+    bool add;                 // WGRAD: add to out_f32 (and g_bias_f32)
+    mp_bf16_t *g_bias;        // WGRAD: column sums of g [E,N] in bf16,
+    float *g_bias_f32;        // or fp32; at most one of them given
 };
 
 // Each thread writes its own row.

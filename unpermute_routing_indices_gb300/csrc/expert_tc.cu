@@ -91,13 +91,15 @@ constexpr int RING_BYTES = Ring<1>::STAGES * Ring<1>::STAGE;
 static_assert(RING_BYTES == Ring<2>::STAGES * Ring<2>::STAGE, "one layout");
 constexpr int MOST_STAGES = 6;
 constexpr int EPI_WARPS = 8;   // two for each quarter of the accumulator's lanes
-constexpr int TC_THREADS = 64 + 32 * EPI_WARPS;
+constexpr int SUM_WARPS = 4;   // WGRAD: column sums for the bias gradient
+__host__ __device__ constexpr int tc_threads(int mode) { return 64 + 32 * (EPI_WARPS + (mode == WGRAD ? SUM_WARPS : 0)); }
 constexpr int STAGING = 32 * EPI_COLS * 2;   // bytes of one warp's tile on its way out
 
 struct TcShared {
     uint64_t full[MOST_STAGES], peer_full[MOST_STAGES], empty[MOST_STAGES], acc_full[2], acc_empty[2], drained;
     uint32_t tmem;
     int gave_up;
+    float sums[SUM_WARPS][BM];
     int start[MP_MAX_EXPERTS + 1], tiles[MP_MAX_EXPERTS + 1];
 };
 constexpr size_t TC_SMEM = 1024 + RING_BYTES + EPI_WARPS * STAGING + sizeof(TcShared);
@@ -184,26 +186,6 @@ struct WarpWriter {
     }
 };
 
-// Brings what the epilogue of columns [c0,c1) of a row will read into L2 while the
-// accumulator fills.
-__device__ __forceinline__ void prefetch_l2(const void *p, int bytes)
-{
-    for (int i = 0; i < bytes; i += 128)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char *>(p) + i));
-}
-template <int MODE>
-__device__ __forceinline__ void epi_prefetch(const ExpertEpi &p, int64_t row, int c0, int c1)
-{
-    if (MODE == FWD) {
-        if (p.residual != nullptr) prefetch_l2(p.residual + row * p.cols + c0, 2 * (c1 - c0));
-    } else if (p.act != MP_ACT_NONE) {
-        const int parts = act_gated(p.act) ? 2 : 1, size = p.save == MP_SAVE_BF16 ? 2 : 1;
-        for (int q = 0; q < parts; ++q)
-            prefetch_l2(static_cast<const char *>(p.z) + ((row * parts + q) * p.cols + c0) * size,
-                        size * (c1 - c0));
-    }
-}
-
 // A slice of `rows` rows, contraction across them: zeroes the rows up to the next
 // 16 in every box (128 bytes each, whatever the swizzle), for the products to read,
 // and returns how many steps of 16 there are.
@@ -219,8 +201,59 @@ template <int CG> __device__ __forceinline__ int zero_ragged(uint8_t *tile, int 
     return steps;
 }
 
+// The sum warps alone.
+__device__ __forceinline__ void sums_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * SUM_WARPS) : "memory"); }
+
+// The bias gradient of a tile's 128 columns of g: column sums over the expert's
+// rows, by warps that wait for nothing else, beside the product.  A thread has 8
+// columns of every eighth row, eight rows in flight; the sums of a warp, then of the
+// warps, are added in order.  256 experts of 128 rows, 1,024 x 2,048: a kernel of
+// its own after this one took 28 us more, the epilogue warps doing it 24.
+__device__ __forceinline__ void column_sums(const ExpertCall &c, const Tile &w, float (&sums)[SUM_WARPS][BM], int tid)
+{
+    constexpr int ROWS = 2 * SUM_WARPS;
+    const int col = w.m0 + (tid & 15) * 8, warp = tid >> 5;
+    float s[8] = {};
+    if (col < c.N) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(c.a + static_cast<int64_t>(w.row0) * c.N + col);
+        const int64_t pitch = c.N / 8;
+        for (int r = tid >> 4; r < w.depth; r += 8 * ROWS) {
+            uint4 v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                v[q] = r + ROWS * q < w.depth ? ld_stream(p + (r + ROWS * q) * pitch) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                float f[8];
+                unpack(v[q], f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[i] += f[i];
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] += __shfl_xor_sync(FULL_MASK, s[i], 16);
+    sums_sync();   // the sums of the tile before have been read
+    if ((tid & 31) < 16) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sums[warp][(tid & 15) * 8 + i] = s[i];
+    }
+    sums_sync();
+    if (w.m0 + tid >= c.N) return;
+    float t = sums[0][tid];
+    for (int q = 1; q < SUM_WARPS; ++q) t += sums[q][tid];
+    const int64_t at = static_cast<int64_t>(w.e) * c.N + w.m0 + tid;
+    if (c.epi.g_bias_f32 != nullptr) {
+        c.epi.g_bias_f32[at] = c.epi.add ? c.epi.g_bias_f32[at] + t : t;
+    } else {
+        const float f[1] = {t};
+        c.epi.g_bias[at] = pack(f);
+    }
+}
+static_assert(32 * SUM_WARPS == BM, "a column a thread");
+
 template <int MODE, bool GATED, int CG>
-__global__ void __launch_bounds__(TC_THREADS, 1)
+__global__ void __launch_bounds__(tc_threads(MODE), 1)
     k_expert_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                 const __grid_constant__ StoreMaps stores, const ExpertCall c)
 {
@@ -300,7 +333,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                         for (int j = 0; j < BN / CG / 64; ++j)
                             tma_load<CG>(b + j * BOX_BYTES, &map_b, bar, w.c0 + part + 64 * j, w.row0 + k);
                     } else {
-                        tma_load<CG>(a, &map_a, bar, k, w.m0);
+                        // A part without rows reads zeros from past the end of x: the
+                        // products are made all the same, but on less power and no bytes.
+                        tma_load<CG>(a, &map_a, bar, k, w.m0 < w.m1 ? w.m0 : c.R);
                         if (MODE == FWD) {
                             // 128 rows of w at a time: the gate's and the others', or neighbours.
                             for (int j = rank; j < rank + 2 / CG; ++j)
@@ -386,6 +421,15 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             __syncwarp();
         }
         if (!ok && lane == 0) or_status(c.status, MP_STATUS_STALLED);
+    } else if (MODE == WGRAD && warp >= 2 + EPI_WARPS) {
+        if (c.epi.g_bias != nullptr || c.epi.g_bias_f32 != nullptr)
+            for (int64_t t = first; t < total; t += step) {
+                const Tile w = tile_at<MODE, CG>(c, s.start, s.tiles, t, nt, tile_cols, rank);
+                if (w.c0 == 0) {
+                    column_sums(c, w, s.sums, threadIdx.x - 64 - 32 * EPI_WARPS);
+                    __syncwarp();
+                }
+            }
     } else if (warp >= 2) {
         const int quad = warp & 3;            // the TMEM lanes this warp can read
         const int half = (warp - 2) >> 2;     // and its half of the columns
@@ -399,11 +443,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             const int row = min(w.m0 + quad * 32 + lane, w.m1 - 1);   // lanes past the end read the last
             const int acc = it & 1;
             const int j0 = half * (tile_cols / 2), j1 = j0 + tile_cols / 2;
-            if (MODE != WGRAD && valid && w.c0 + j0 < c.epi.cols)
-                epi_prefetch<MODE>(c.epi, row, w.c0 + j0, min(w.c0 + j1, c.epi.cols));
             if (w.depth != 0) {
-                if (!__all_sync(FULL_MASK, mbar_wait(smem_u32(&s.acc_full[acc]), (it >> 1) & 1, gave_up)))
-                    break;
+                // Should the wait be given up, the results are flagged as invalid and
+                // the loop goes on, so that every warp meets the others.
+                (void)mbar_wait(smem_u32(&s.acc_full[acc]), (it >> 1) & 1, gave_up);
+                __syncwarp();
                 tc_fence_after();
             }
             const uint32_t d = tmem + acc * BN + (static_cast<uint32_t>(quad * 32) << 16);
@@ -465,8 +509,9 @@ bool store_map(StoreMaps &m, int which, const void *base, int64_t parts, int64_t
     return !m.use[which] || make_map(&m.map[which], base, 2, dims, box);
 }
 
-// Pairs of CTAs that the device holds at once.
-template <typename K> int pair_count(K kernel)
+// Pairs of CTAs that the device holds at once; the same for all these kernels, one
+// CTA to an SM.
+template <typename K> int pair_count(K kernel, int threads)
 {
     static std::atomic<int> known[64];
     int dev = 0, n = 0;
@@ -474,7 +519,7 @@ template <typename K> int pair_count(K kernel)
     if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = 2;
-    cfg.blockDim = TC_THREADS;
+    cfg.blockDim = threads;
     cfg.dynamicSmemBytes = TC_SMEM;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -495,10 +540,10 @@ mp_status_t launch_tc(const ExpertCall &c, const CUtensorMap &a, const CUtensorM
     const int64_t nt = (c.epi.cols + (GATED ? BN / 2 : BN) - 1) / (GATED ? BN / 2 : BN);
     const int64_t mt = MODE == WGRAD ? static_cast<int64_t>(c.E) * ((c.N + CG * BM - 1) / (CG * BM))
                                      : c.R / (CG * BM) + (c.R < c.E ? c.R : c.E);
-    const int64_t tiles = nt * mt, room = CG == 1 ? sm_count() : pair_count(k_expert_tc<MODE, GATED, CG>);
+    const int64_t tiles = nt * mt, room = CG == 1 ? sm_count() : pair_count(k_expert_tc<MODE, GATED, CG>, tc_threads(MODE));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = static_cast<unsigned>(CG * (tiles < room ? tiles : room));
-    cfg.blockDim = TC_THREADS;
+    cfg.blockDim = tc_threads(MODE);
     cfg.dynamicSmemBytes = TC_SMEM;
     cfg.stream = c.stream;
     cudaLaunchAttribute attr[2];

@@ -8,10 +8,10 @@
 // Choice.  Without a bias the scores rise with the logits, which are compared
 // as they are.  With one, and for the sum of a group's best two, fp32 values of
 // c decide wherever neighbours in the order are further apart than their errors
-// can be (`margin`); a token where two are nearer (about one of a thousand of
+// can be (too_near); a token where two are nearer (about one of a thousand of
 // normal logits) is decided again in 64 bits (choose_exact).  So the choice is
 // that of 64 bits everywhere, at the cost of 32: on 32,768 tokens of 256 experts
-// (sigmoid, bias, 8 groups), all of it in 64 bits took 1,290 us, this 58.
+// (sigmoid, bias, 8 groups), all of it in 64 bits took 1,290 us, this 43.
 // Each lane sorts its candidates by a fixed network and a round takes the best
 // head of the warp (topk.cuh); the round after the K-th says how near the best
 // of the rest is.
@@ -112,13 +112,12 @@ template <int KT> __device__ __forceinline__ float pick_sum(float v)
 __device__ __forceinline__ bool usable(float v) { return v > -INFINITY; }
 
 
-// The token's logits and biases: expert lane + 32 j in slot j; bit j of `have`:
-// it has a logit, of `live`: it can be chosen.
+// The token's logits and biases: expert lane + 32 j in slot j.  What cannot be
+// chosen has logit -inf; +inf is the largest finite value.
 template <typename L, int PER>
 __device__ __forceinline__ void load_token(const RouteArgs &a, const L *l, int lane, float (&v)[PER],
-                                           float (&b)[PER], unsigned &have, unsigned &live)
+                                           float (&b)[PER])
 {
-    have = live = 0;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
         const int e = lane + 32 * j;
@@ -126,12 +125,48 @@ __device__ __forceinline__ void load_token(const RouteArgs &a, const L *l, int l
         b[j] = (e < a.E && a.bias != nullptr) ? __ldg(a.bias + e) : 0.0f;
     }
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        const bool u = usable(v[j]);   // false for NaN too
-        have |= static_cast<unsigned>(u) << j;
-        live |= static_cast<unsigned>(u && usable(b[j])) << j;
-        v[j] = u ? fminf(v[j], FLT_MAX) : -INFINITY;
-    }
+    for (int j = 0; j < PER; ++j) v[j] = usable(v[j]) ? fminf(v[j], FLT_MAX) : -INFINITY;   // NaN is not usable
+}
+
+// exp(-x) for x >= 0 in 64 bits, within 2 units of the last place: x = n ln 2 + r
+// by a reduction in two steps (Cody and Waite), Taylor's series of exp(-r), |r| <= ln 2 / 2,
+// to r^13 (the next term is 4e-18).  Without branches, so that a lane's values
+// are worked on side by side: the units for 64 bits are few, and what counts is the
+// length of the chain (one token of 256 experts: 18 us with exp(), 6 with this).
+__device__ __forceinline__ double exp_neg(double x)
+{
+    x = fmin(x, 745.0);
+    const double n = rint(x * 1.4426950408889634074);
+    double r = fma(n, -0.6931471796706319, x);   // ln 2 cut off after 30 bits: the product is exact
+    r = -fma(n, -8.893134238886677e-10, r);           // and what was cut off
+    double s = 1.0 / 6227020800.0;
+    s = fma(s, r, 1.0 / 479001600.0);
+    s = fma(s, r, 1.0 / 39916800.0);
+    s = fma(s, r, 1.0 / 3628800.0);
+    s = fma(s, r, 1.0 / 362880.0);
+    s = fma(s, r, 1.0 / 40320.0);
+    s = fma(s, r, 1.0 / 5040.0);
+    s = fma(s, r, 1.0 / 720.0);
+    s = fma(s, r, 1.0 / 120.0);
+    s = fma(s, r, 1.0 / 24.0);
+    s = fma(s, r, 1.0 / 6.0);
+    s = fma(s, r, 0.5);
+    s = fma(s, r, 1.0);
+    s = fma(s, r, 1.0);
+    // 2^-n in two factors, so that the smallest results come out rounded once.
+    const int k = static_cast<int>(n), h = k >> 1;
+    const double p = __longlong_as_double(static_cast<long long>(1023 - h) << 52);
+    const double q = __longlong_as_double(static_cast<long long>(1023 - (k - h)) << 52);
+    return s * p * q;
+}
+
+// 1/x for 1 <= x <= 2^11: an fp32 reciprocal and two steps of Newton's, each of which
+// squares the error.
+__device__ __forceinline__ double rcp_exact(double x)
+{
+    double r = static_cast<double>(__frcp_rn(static_cast<float>(x)));
+    r = fma(r, fma(-x, r, 1.0), r);
+    return fma(r, fma(-x, r, 1.0), r);
 }
 
 // The choice in 64 bits.  Lane k gets pick k (-1: none left).
@@ -139,35 +174,34 @@ template <typename L, int PER>
 __device__ __noinline__ int choose_exact(const RouteArgs &a, const L *l, int lane)
 {
     float v[PER], b[PER];
-    unsigned have, live;
-    load_token<L, PER>(a, l, lane, v, b, have, live);
+    load_token<L, PER>(a, l, lane, v, b);
     double c[PER];
     if (a.score == MP_SCORE_SIGMOID) {
+        // 1 / (1 + exp(-v)), with the exponential of -|v|.
 #pragma unroll
-        for (int j = 0; j < PER; ++j) c[j] = 1.0 / (1.0 + exp(-static_cast<double>(v[j])));
+        for (int j = 0; j < PER; ++j) {
+            const double t = exp_neg(fabs(static_cast<double>(v[j])));
+            c[j] = (v[j] < 0.0f ? t : 1.0) * rcp_exact(1.0 + t);
+        }
     } else {
         float m = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < PER; ++j)
-            if (have >> j & 1u) m = fmaxf(m, v[j]);
+        for (int j = 0; j < PER; ++j) m = fmaxf(m, v[j]);
         m = warp_max(m);
         double s = 0.0;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            c[j] = (have >> j & 1u) ? exp(static_cast<double>(v[j]) - m) : 0.0;
+            c[j] = usable(v[j]) ? exp_neg(static_cast<double>(m) - v[j]) : 0.0;
             s += c[j];
         }
-        s = warp_sum(s);
+        s = rcp_exact(fmax(warp_sum(s), 1.0));   // the largest term is 1, if there is any
 #pragma unroll
-        for (int j = 0; j < PER; ++j) c[j] /= s;
+        for (int j = 0; j < PER; ++j) c[j] *= s;
     }
-    if (a.bias != nullptr)
-#pragma unroll
-        for (int j = 0; j < PER; ++j) c[j] += static_cast<double>(b[j]);
-
     uint64_t key[PER];
 #pragma unroll
-    for (int j = 0; j < PER; ++j) key[j] = (live >> j & 1u) ? order_key(c[j]) : 0ull;
+    for (int j = 0; j < PER; ++j)
+        key[j] = usable(v[j]) && usable(b[j]) ? order_key(c[j] + static_cast<double>(b[j])) : 0ull;
     if (a.n_groups > 1) {
         uint64_t worth = 0ull;   // lane g: group g's
         for (int g = 0; g < a.n_groups; ++g) {
@@ -195,15 +229,13 @@ __device__ __noinline__ int choose_exact(const RouteArgs &a, const L *l, int lan
         }
 #pragma unroll
         for (int j = 0; j < PER; ++j)
-            if (!(kept >> (__umulhi(lane + 32 * j, a.group_magic) & 31) & 1u)) live &= ~(1u << j);
+            if (!(kept >> (__umulhi(lane + 32 * j, a.group_magic) & 31) & 1u)) key[j] = 0ull;
     }
     // Without a bias the scores rise with the logits, which stay apart where
     // scores round to one value.
 #pragma unroll
     for (int j = 0; j < PER; ++j)
-        key[j] = !(live >> j & 1u)   ? 0ull
-                 : a.bias == nullptr ? order_key(static_cast<double>(v[j]))
-                                     : key[j];
+        if (a.bias == nullptr && key[j] != 0ull) key[j] = order_key(static_cast<double>(v[j]));
     int pick = -1;
     for (int k = 0; k < a.K; ++k) {
         uint64_t bk = 0ull;
@@ -281,8 +313,7 @@ __device__ __forceinline__ bool too_near(uint32_t key, uint32_t next, float err)
 // The choice from fp32 values; false (in every lane): too near to tell.
 template <typename L, int PER, int KT>
 __device__ __forceinline__ bool choose_fast(const RouteArgs &a, const L *l, const float (&v)[PER],
-                                            const float (&b)[PER], unsigned have, unsigned live,
-                                            int lane, int &pick)
+                                            const float (&b)[PER], int lane, int &pick)
 {
     const int K = KT > 0 ? KT : a.K;
     const bool by_logit = a.bias == nullptr;
@@ -303,44 +334,41 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs &a, const L *l, cons
             float m = -INFINITY, sum = 0.0f;
 #pragma unroll
             for (int j = 0; j < PER; ++j) m = fmaxf(m, v[j]);
-            m = warp_max(m);
+            m = fmaxf(warp_max(m), -FLT_MAX);
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
-                c[j] = (have >> j & 1u) ? exp_fast(v[j] - m) : 0.0f;
+                c[j] = exp_fast(v[j] - m);   // 0 for -inf
                 sum += c[j];
             }
-            const float inv = rcp_fast(warp_sum(sum));
+            const float inv = rcp_fast(fmaxf(warp_sum(sum), 1.0f));
             err = inv * (8e-7f + (PER + 6) * 6e-8f);
 #pragma unroll
             for (int j = 0; j < PER; ++j) c[j] *= inv;
         }
 #pragma unroll
-        for (int j = 0; j < PER; ++j) key[j] = (live >> j & 1u) ? order_key(c[j] + b[j]) : 0u;
+        for (int j = 0; j < PER; ++j)
+            key[j] = usable(v[j]) && usable(b[j]) ? order_key(c[j] + b[j]) : 0u;
     } else {
 #pragma unroll
-        for (int j = 0; j < PER; ++j) key[j] = (live >> j & 1u) ? order_key(v[j]) : 0u;
+        for (int j = 0; j < PER; ++j) key[j] = usable(v[j]) ? order_key(v[j]) : 0u;
     }
 
+    unsigned cols = 0u;   // slots that may hold a candidate, the same in every lane
     if (a.n_groups > 1) {
         const int per_group = a.E / a.n_groups;
         const bool columns = per_group % 32 == 0;   // a group is whole slots
-        uint32_t worth = 0u;                        // lane g: group g's, as a key,
-        float size = 0.0f;                          // and the magnitudes it is the sum of
-        // Group g's worth from each lane's best two of it.
+        uint32_t w1 = 0u, w2 = 0u;                  // lane g: group g's best two
+        // From each lane's best two of group g.
         const auto finish = [&](int g, uint32_t k1, uint32_t k2) {
-            uint32_t w = __reduce_max_sync(FULL_MASK, k1);
-            float sz = 0.0f;
+            const uint32_t m1 = __reduce_max_sync(FULL_MASK, k1);
+            uint32_t m2 = 0u;
             if (a.group_top == 2) {
-                const int holder = __ffs(__ballot_sync(FULL_MASK, k1 == w)) - 1;
-                const uint32_t m2 = __reduce_max_sync(FULL_MASK, lane == holder ? k2 : k1);
-                if (m2 != 0u) {
-                    w = order_key(key_value(w) + key_value(m2));
-                    sz = fabsf(key_value(w)) + 2.0f * fabsf(key_value(m2));
-                }
+                m2 = __reduce_max_sync(FULL_MASK, k1 == m1 ? k2 : k1);
+                if (__popc(__ballot_sync(FULL_MASK, k1 == m1)) > 1) m2 = m1;   // two lanes hold it
             }
             if (lane == g) {
-                worth = w;
-                size = sz;
+                w1 = m1;
+                w2 = m2;
             }
         };
         if (columns) {
@@ -366,38 +394,43 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs &a, const L *l, cons
                 finish(g, k1, k2);
             }
         }
-        unsigned kept = 0;
-        uint32_t last = 0u;
-        float last_size = 0.0f;
-        for (int r = 0; r <= a.topk_groups; ++r) {
-            uint32_t wk = (kept >> lane & 1u) ? 0u : worth;
-            const uint32_t g = warp_argmax_key(wk, static_cast<uint32_t>(lane));
-            const float sz = __shfl_sync(FULL_MASK, size, g);
+        const uint32_t worth = w2 == 0u ? w1 : order_key(key_value(w1) + key_value(w2));
+        const float size = w2 == 0u ? 0.0f : fabsf(key_value(w1)) + fabsf(key_value(w2));
+        // A group is kept if fewer than topk_groups stand before it.
+        int before = 0;
+        for (int g = 0; g < a.n_groups; ++g) {
+            const uint32_t o = __shfl_sync(FULL_MASK, worth, g);
+            before += o > worth || (o == worth && g < lane);
+        }
+        const bool mine = worth != 0u && before < a.topk_groups;
+        const unsigned kept = __ballot_sync(FULL_MASK, mine);
+        if (err > 0.0f) {
             // Only the last one kept and the first one left out must stand apart.
-            if (r == a.topk_groups)
-                near = err > 0.0f && too_near(last, wk, 2.0f * err + 6.0e-8f * (last_size + sz));
-            else if (wk != 0u)
-                kept |= 1u << g;
-            last = wk;
-            last_size = sz;
+            const uint32_t last = __reduce_min_sync(FULL_MASK, mine ? worth : 0xffffffffu);
+            const uint32_t next = __reduce_max_sync(FULL_MASK, mine ? 0u : worth);
+            const float slack = __uint_as_float(__reduce_max_sync(FULL_MASK, __float_as_uint(size)));
+            near = kept != 0u && too_near(last, next, 2.0f * err + 1.2e-7f * slack);
         }
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            const uint32_t g = __umulhi(lane + 32 * j, a.group_magic);
-            if (!(kept >> (g & 31) & 1u)) live &= ~(1u << j);
+            const unsigned in = kept >> (__umulhi(columns ? 32 * j : lane + 32 * j, a.group_magic) & 31) & 1u;
+            key[j] = in ? key[j] : 0u;
+            if (!columns || in) cols |= 1u << j;
         }
+    } else {
+        cols = (1u << (PER - 1) << 1) - 1u;
     }
-    // Keys of what is left; without a bias the logits' own.
+    if ((a.E + 31) / 32 < PER) cols &= (1u << ((a.E + 31) / 32)) - 1u;
+    if (by_logit && pairs) {   // without a bias the logits decide inside the groups
+#pragma unroll
+        for (int j = 0; j < PER; ++j) key[j] = key[j] ? order_key(v[j]) : 0u;
+    }
     uint32_t ex[PER];
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        ex[j] = static_cast<uint32_t>(lane + 32 * j);
-        key[j] = !(live >> j & 1u) ? 0u : (by_logit && pairs) ? order_key(v[j]) : key[j];
-    }
+    for (int j = 0; j < PER; ++j) ex[j] = static_cast<uint32_t>(lane + 32 * j);
     uint32_t my_key = 0u, rest = 0u, rest_i = 0u;
     int my_i = -1;
     if constexpr (PER <= 8) {
-        const unsigned cols = __reduce_or_sync(FULL_MASK, live);
         if (PER >= 4 && __popc(cols) <= PER / 2) {
             constexpr int HALF = PER >= 4 ? PER / 2 : 1;
             uint32_t kc[HALF], xc[HALF];
@@ -460,10 +493,11 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs &a, const L *l, cons
 }
 
 // KT > 0: a form for K = KT with the rounds unrolled.  Compiled for 4 CTAs per
-// SM up to 256 experts: 32,768 x 256 tokens (sigmoid, bias, 8 groups) 59.0 us
-// with 3, 58.1 with 4; the same without groups 41.4 and 38.7.
+// SM up to 256 experts (32,768 x 256, sigmoid, bias: 41.4 us with 3, 38.7 with 4),
+// 3 up to 512 (16,383 x 512: 64.5 us with 1, 51.9 with 2, 48.7 with 3) and 2 up to
+// 1,024 (106.8 with 1, 90.9 with 2).
 template <typename L, int PER, int KT>
-__global__ void __launch_bounds__(RT_THREADS, PER <= 8 ? 4 : 1) k_route(const RouteArgs a)
+__global__ void __launch_bounds__(RT_THREADS, PER <= 8 ? 4 : PER <= 16 ? 3 : 2) k_route(const RouteArgs a)
 {
     pdl_trigger();
     pdl_wait();
@@ -472,10 +506,9 @@ __global__ void __launch_bounds__(RT_THREADS, PER <= 8 ? 4 : 1) k_route(const Ro
     if (t >= a.T) return;   // whole warps leave together
     const L *l = static_cast<const L *>(a.logits) + t * a.E;
     float v[PER], b[PER];
-    unsigned have, live;
-    load_token<L, PER>(a, l, lane, v, b, have, live);
+    load_token<L, PER>(a, l, lane, v, b);
     int pick;
-    if (!choose_fast<L, PER, KT>(a, l, v, b, have, live, lane, pick)) pick = choose_exact<L, PER>(a, l, lane);
+    if (!choose_fast<L, PER, KT>(a, l, v, b, lane, pick)) pick = choose_exact<L, PER>(a, l, lane);
 
     // The weights.  sigmoid(v) is exp(v) for v far below zero; where all
     // picks are there, their ratio is taken from exp(v_k - m), which does not
@@ -493,8 +526,7 @@ __global__ void __launch_bounds__(RT_THREADS, PER <= 8 ? 4 : 1) k_route(const Ro
         for (int j = 0; j < PER; ++j) top = fmaxf(top, v[j]);
         top = warp_max(top);
 #pragma unroll
-        for (int j = 0; j < PER; ++j)
-            if (have >> j & 1u) sum += expf(v[j] - top);
+        for (int j = 0; j < PER; ++j) sum += usable(v[j]) ? expf(v[j] - top) : 0.0f;
         sum = warp_sum(sum);
         s = pick >= 0 ? __fdiv_rn(expf(pv - top), sum) : 0.0f;
     }
