@@ -292,8 +292,9 @@ mp_status_t mp_route_bwd(const float *g_weights, const void *logits, int32_t dty
  * Sums are fp32 in an order that depends on K alone for a given kernel, so a
  * row's result does not depend on the rows around it.
  * Limits: E <= MP_MAX_EXPERTS; N, K <= 2^22; R < 2^31 - 1024.
- * Rows whose width K is a multiple of 8 with 16-byte aligned x and w take the
- * tensor cores; other calls are computed by a slower kernel.
+ * A K that is a multiple of 8, with 16-byte aligned x and w, takes the tensor
+ * cores; other calls are computed by a much slower kernel.  (mp_expert_dgrad and
+ * mp_expert_wgrad ask the same of N.)
  */
 mp_status_t mp_expert_gemm(const mp_bf16_t *x, const mp_bf16_t *w, const int32_t *offsets,
                            int64_t R, int32_t E, int32_t N, int32_t K, const mp_bf16_t *bias,

@@ -459,6 +459,110 @@ def test_expert_mlp_gradient_against_differences(act):
             6 * 4 * 2.0 ** -8 * (sizes[k] * d).square().sum().sqrt()
 
 
+@pytest.mark.parametrize("counts", ["few each", "many", "long"])
+def test_captured_and_replayed(counts):
+    """The calls in a CUDA graph, replayed with other rows and other offsets in the
+    same buffers, give what eager calls give."""
+    counts = COUNTS[counts]
+    E, R, H, F = len(counts), sum(counts), 136, 72
+    first, second = offsets_of(counts), offsets_of(counts[::-1])
+    x, g = normal(R, H, seed=1), normal(R, H, seed=2)
+    w1, w2 = normal(E, 2 * F, H, seed=3, std=0.1), normal(E, H, F, seed=4, std=0.1)
+    b1, l = normal(E, 2 * F, seed=5), torch.randn(R, E, device=DEV)
+    offsets = first.clone()
+
+    def calls():
+        idx, weights = mp.mp_route(l, 1, score="sigmoid")
+        y, z, z_exp = mp.mp_expert_mlp(x, w1, w2, offsets, b1, save="e4m3")
+        grads = mp.mp_expert_mlp_bwd(g, x, w1, w2, offsets, z, z_exp, need=(True,) * 5)
+        return [idx, weights, mp.mp_route_bwd(weights, l, idx, score="sigmoid"), y, *grads]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        calls()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = calls()
+    for o, seed in ((second, 11), (first, 12)):
+        offsets.copy_(o)
+        x.copy_(normal(R, H, seed=seed))
+        l.copy_(torch.randn(R, E, device=DEV))
+        graph.replay()
+        got = [t.clone() for t in outs]
+        for a, b in zip(got, calls()):
+            assert torch.equal(a, b)
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, started together again and again, give what they give
+    alone (the persistent kernels share SMs and tensor memory)."""
+    counts = COUNTS["long"]
+    R, offsets = sum(counts), offsets_of(counts)
+    small = offsets_of(COUNTS["few each"])
+    x, w, g = normal(R, 256, seed=1), normal(3, 512, 256, seed=2), normal(R, 512, seed=3)
+    xs, ws = normal(sum(COUNTS["few each"]), 512, seed=4), normal(8, 384, 512, seed=5)
+    want = [mp.mp_expert_gemm(x, w, offsets)[0], mp.mp_expert_wgrad(g, x, offsets)[0],
+            mp.mp_expert_gemm(xs, ws, small, act="silu")[0], mp.mp_expert_dgrad(g, w, offsets)[0]]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(30):
+        with torch.cuda.stream(streams[0]):
+            got.append((0, mp.mp_expert_gemm(x, w, offsets)[0]))
+            got.append((2, mp.mp_expert_gemm(xs, ws, small, act="silu")[0]))
+        with torch.cuda.stream(streams[1]):
+            got.append((1, mp.mp_expert_wgrad(g, x, offsets)[0]))
+            got.append((2, mp.mp_expert_gemm(xs, ws, small, act="silu")[0]))
+            got.append((3, mp.mp_expert_dgrad(g, w, offsets)[0]))
+    torch.cuda.synchronize()
+    for k, t in got:
+        assert torch.equal(t, want[k])
+
+
+def test_repeated_calls_are_equal():
+    counts = COUNTS["big"]
+    R, offsets = sum(counts), offsets_of(counts)
+    x, w, g = normal(R, 576, seed=1), normal(4, 512, 576, seed=2), normal(R, 512, seed=3)
+    once = [mp.mp_expert_gemm(x, w, offsets, act="swiglu")[0], mp.mp_expert_dgrad(g, w, offsets)[0],
+            *mp.mp_expert_wgrad(g, x, offsets, with_bias=True)]
+    for _ in range(5):
+        again = [mp.mp_expert_gemm(x, w, offsets, act="swiglu")[0],
+                 mp.mp_expert_dgrad(g, w, offsets)[0],
+                 *mp.mp_expert_wgrad(g, x, offsets, with_bias=True)]
+        for a, b in zip(once, again):
+            assert torch.equal(a, b)
+
+
+def test_buffers_past_two_thirty_one_elements():
+    """Rows whose offsets need 64 bits: the last ones come out right."""
+    R, K, N = 540_000, 4096, 64
+    offsets = torch.tensor([0, 1000, R], dtype=torch.int32, device=DEV)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    x = torch.empty((R, K), dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    w = normal(2, N, K, seed=2, std=K ** -0.5)
+    tail = slice(R - 700, R)
+    out, _, _ = mp.mp_expert_gemm(x, w, offsets)
+    want, size = x[tail].double() @ w[1].double().T, x[tail].double().abs() @ w[1].double().abs().T
+    bound = (K + 2) * 2.0 ** -23 * size * (1 + BF16) + BF16 * want.abs()
+    assert ((out[tail].double() - want).abs() <= bound).all()
+    # The gradient of the weights of an expert whose rows all lie past 2^31 elements.
+    offsets = torch.tensor([0, R - 700, R], dtype=torch.int32, device=DEV)
+    gy = normal(R, N, seed=3)
+    g_w, g_b = mp.mp_expert_wgrad(gy, x, offsets, with_bias=True)
+    want = gy[tail].double().T @ x[tail].double()
+    size = gy[tail].double().abs().T @ x[tail].double().abs()
+    assert ((g_w[1].double() - want).abs() <= 702 * 2.0 ** -23 * size + BF16 * want.abs()).all()
+    want, size = gy[tail].double().sum(0), gy[tail].double().abs().sum(0)
+    assert ((g_b[1].double() - want).abs() <= 702 * 2.0 ** -24 * size + BF16 * want.abs()).all()
+    del x
+    g_x, _ = mp.mp_expert_dgrad(gy, w, offsets)
+    want, size = gy[tail].double() @ w[1].double(), gy[tail].double().abs() @ w[1].double().abs()
+    bound = (N + 2) * 2.0 ** -23 * size * (1 + BF16) + BF16 * want.abs()
+    assert ((g_x[tail].double() - want).abs() <= bound).all()
+
+
 def test_refusals():
     x, w = normal(10, 64, seed=1), normal(3, 64, 64, seed=2)
     offsets = offsets_of([3, 3, 4])
