@@ -95,6 +95,8 @@ COUNTS = {
     "big": [300, 513, 128, 1000],
     "long": [1500, 700, 1031],       # enough rows an expert for pairs of CTAs, all three ragged
     "long, one empty": [2111, 0, 1985],
+    "single long": [5001],           # few tiles: split contractions, ragged at the end
+    "two, short and long": [3, 2500],
 }
 
 # counts, N (columns of w), K, activation, bias, residual, shift of x
@@ -120,6 +122,8 @@ PRODUCTS = [
     ("long", 2 * 136, 200, "swiglu", True, True, 0),
     ("long", 264, 320, "gelu", False, True, 0),
     ("long, one empty", 2 * 256, 128, "geglu", False, False, 0),
+    ("two, short and long", 2 * 72, 1032, "swiglu", True, True, 0),
+    ("single long", 40, 4096, "gelu", True, False, 0),
 ]
 
 
@@ -188,6 +192,7 @@ DGRADS = [
     ("big", 256, 328, "swiglu", "bf16"),
     ("long", 192, 264, "swiglu", "e4m3"),
     ("long, one empty", 320, 136, "none", None),
+    ("two, short and long", 1544, 72, "geglu", "e4m3"),
 ]
 
 
@@ -240,6 +245,7 @@ WGRADS = [
     ("first empty", 257, 128, False), ("tokens", 128, 264, True), ("few each", 256, 384, True),
     ("big", 192, 576, True), ("big", 520, 264, False), ("one expert", 384, 512, True),
     ("long", 264, 520, True), ("long, one empty", 136, 264, False), ("long", 512, 256, False),
+    ("single long", 136, 264, True), ("single long", 24, 1000, True), ("two, short and long", 264, 72, True),
 ]
 
 

@@ -15,6 +15,9 @@
 // computed and dropped (FWD, DGRAD).  In WGRAD, where they would enter the sums,
 // the last slice's rows up to the next 16 are overwritten with zeros in shared
 // memory, whatever they held.
+// Where the tiles are fewer than the SMs (one expert, narrow results) the contraction
+// of each is split over a cluster of up to 8 CTAs, whose parts are added in rank order
+// through distributed shared memory, so a result does not depend on timing.
 // What bounds it: for experts of many rows the tensor cores (131,072 x 4,096 by 128
 // experts of 2,048 columns in 1,211 us, 1.82 PFLOP/s, 0.92 of cuBLAS's measured
 // 8,192^3); for few rows the bytes of weights and results and the epilogue.
@@ -99,7 +102,7 @@ struct TcShared {
     uint64_t full[MOST_STAGES], peer_full[MOST_STAGES], empty[MOST_STAGES], acc_full[2], acc_empty[2], drained;
     uint32_t tmem;
     int gave_up;
-    float sums[SUM_WARPS][BM];
+    float sums[SUM_WARPS][BM], sum[BM];
     int start[MP_MAX_EXPERTS + 1], tiles[MP_MAX_EXPERTS + 1];
 };
 constexpr size_t TC_SMEM = 1024 + RING_BYTES + EPI_WARPS * STAGING + sizeof(TcShared);
@@ -107,11 +110,12 @@ static_assert(TC_SMEM <= 232448, "shared memory of one SM");
 
 struct Tile {
     int e, m0, m1, c0, row0, depth;   // rows from m0 (this CTA's) up to m1 of the result (of g's columns in WGRAD)
+    int k0, k1;                       // this CTA's part of the contraction, whole slices but its end
 };
 
 template <int MODE, int CG>
 __device__ __forceinline__ Tile tile_at(const ExpertCall &c, const int *start, const int *tiles,
-                                        int64_t t, int nt, int tile_cols, int rank)
+                                        int64_t t, int nt, int tile_cols, int rank, int part, int parts)
 {
     constexpr int TM = CG * BM;
     Tile r;
@@ -135,6 +139,9 @@ __device__ __forceinline__ Tile tile_at(const ExpertCall &c, const int *start, c
         r.row0 = 0;
         r.depth = MODE == FWD ? c.K : c.N;
     }
+    const int64_t slices = (r.depth + BK - 1) / BK;
+    r.k0 = static_cast<int>(slices * part / parts) * BK;
+    r.k1 = min(static_cast<int>(slices * (part + 1) / parts) * BK, r.depth);
     return r;
 }
 
@@ -206,24 +213,24 @@ __device__ __forceinline__ void sums_sync() { asm volatile("bar.sync 1, %0;" ::"
 
 // The bias gradient of a tile's 128 columns of g: column sums over the expert's
 // rows, by warps that wait for nothing else, beside the product.  A thread has 8
-// columns of every eighth row, eight rows in flight; the sums of a warp, then of the
+// columns of every eighth row, sixteen rows in flight; the sums of a warp, then of the
 // warps, are added in order.  256 experts of 128 rows, 1,024 x 2,048: a kernel of
 // its own after this one took 28 us more, the epilogue warps doing it 24.
-__device__ __forceinline__ void column_sums(const ExpertCall &c, const Tile &w, float (&sums)[SUM_WARPS][BM], int tid)
+__device__ __forceinline__ float column_sum(const ExpertCall &c, const Tile &w, float (&sums)[SUM_WARPS][BM], int tid)
 {
-    constexpr int ROWS = 2 * SUM_WARPS;
+    constexpr int ROWS = 2 * SUM_WARPS, DEEP = 16;
     const int col = w.m0 + (tid & 15) * 8, warp = tid >> 5;
     float s[8] = {};
     if (col < c.N) {
         const uint4 *p = reinterpret_cast<const uint4 *>(c.a + static_cast<int64_t>(w.row0) * c.N + col);
         const int64_t pitch = c.N / 8;
-        for (int r = tid >> 4; r < w.depth; r += 8 * ROWS) {
-            uint4 v[8];
+        for (int r = w.k0 + (tid >> 4); r < w.k1; r += DEEP * ROWS) {
+            uint4 v[DEEP];
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-                v[q] = r + ROWS * q < w.depth ? ld_stream(p + (r + ROWS * q) * pitch) : make_uint4(0, 0, 0, 0);
+            for (int q = 0; q < DEEP; ++q)
+                v[q] = r + ROWS * q < w.k1 ? ld_stream(p + (r + ROWS * q) * pitch) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
+            for (int q = 0; q < DEEP; ++q) {
                 float f[8];
                 unpack(v[q], f);
 #pragma unroll
@@ -239,9 +246,14 @@ __device__ __forceinline__ void column_sums(const ExpertCall &c, const Tile &w, 
         for (int i = 0; i < 8; ++i) sums[warp][(tid & 15) * 8 + i] = s[i];
     }
     sums_sync();
-    if (w.m0 + tid >= c.N) return;
     float t = sums[0][tid];
     for (int q = 1; q < SUM_WARPS; ++q) t += sums[q][tid];
+    return t;
+}
+
+__device__ __forceinline__ void put_bias_grad(const ExpertCall &c, const Tile &w, int tid, float t)
+{
+    if (w.m0 + tid >= c.N) return;
     const int64_t at = static_cast<int64_t>(w.e) * c.N + w.m0 + tid;
     if (c.epi.g_bias_f32 != nullptr) {
         c.epi.g_bias_f32[at] = c.epi.add ? c.epi.g_bias_f32[at] + t : t;
@@ -252,10 +264,59 @@ __device__ __forceinline__ void column_sums(const ExpertCall &c, const Tile &w, 
 }
 static_assert(32 * SUM_WARPS == BM, "a column a thread");
 
+// The epilogue of 32 columns, from j, of the 32 rows of a tile's quarter.
+template <int MODE, bool GATED>
+__device__ __forceinline__ void finish(const ExpertCall &c, WarpWriter &out, const Tile &w, int quad, int j,
+                                       float (&z)[EPI_COLS], float (&u)[EPI_COLS])
+{
+    out.rows = min(w.m1 - (w.m0 + quad * 32), 32);
+    if (out.rows <= 0) return;
+    const bool valid = out.lane < out.rows;
+    const int row = min(w.m0 + quad * 32 + out.lane, w.m1 - 1);   // lanes past the end read the last
+    const int col = w.c0 + j, n = min(EPI_COLS, c.epi.cols - col);
+    if (MODE == FWD) epi_fwd<GATED>(c.epi, out, w.e, row, col, n, valid, z, u);
+    if (MODE == DGRAD) epi_dgrad(c.epi, out, row, col, n, valid, z);
+    if (MODE == WGRAD) epi_wgrad(c.epi, out, static_cast<int64_t>(w.e) * c.N + row, col, n, valid, z);
+}
+
+// Floats of a row of a CTA's part of a split tile; 8 rows on different banks.
+constexpr int JOIN_PITCH = BN + 4;
+constexpr int JOIN_BYTES = BM * JOIN_PITCH * 4, TURN_BYTES = 32 * 33 * 4;
+static_assert(JOIN_BYTES + EPI_WARPS * TURN_BYTES <= RING_BYTES, "a part, and a turn for each warp, fit the ring");
+
+__device__ __forceinline__ float peer_float(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+// Sums 32 rows of 32 floats over the ranks, in rank order: a lane reads a column, so
+// that every load is a line of the peer's memory (a row a lane, 16 bytes each, took
+// 25 us more for a cluster of 8), and gets its row through `turn`.
+__device__ __forceinline__ void join32(uint32_t addr, int split, float *turn, int lane, float (&z)[EPI_COLS])
+{
+#pragma unroll
+    for (int i = 0; i < 32; ++i) z[i] = 0.0f;
+    for (int r = 0; r < split; ++r) {
+        const uint32_t from = at_rank(addr, r) + lane * 4;
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = peer_float(from + i * JOIN_PITCH * 4);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) z[i] += v[i];
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) turn[i * 33 + lane] = z[i];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) z[i] = turn[lane * 33 + i];
+}
+
 template <int MODE, bool GATED, int CG>
 __global__ void __launch_bounds__(tc_threads(MODE), 1)
     k_expert_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                const __grid_constant__ StoreMaps stores, const ExpertCall c)
+                const __grid_constant__ StoreMaps stores, const ExpertCall c, int split)
 {
     typedef Ring<CG> L;
     constexpr int STAGES = L::STAGES;
@@ -264,6 +325,7 @@ __global__ void __launch_bounds__(tc_threads(MODE), 1)
     TcShared &s = *reinterpret_cast<TcShared *>(ring + RING_BYTES + EPI_WARPS * STAGING);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = CG == 2 ? static_cast<int>(cluster_rank()) : 0;
+    const int part = CG == 1 && split > 1 ? static_cast<int>(cluster_rank()) : 0;
     volatile int *gave_up = &s.gave_up;
 
     if (threadIdx.x == 0) {
@@ -305,16 +367,16 @@ __global__ void __launch_bounds__(tc_threads(MODE), 1)
     const int64_t total = MODE == WGRAD
                               ? static_cast<int64_t>(c.E) * ((c.N + CG * BM - 1) / (CG * BM)) * nt
                               : static_cast<int64_t>(s.tiles[c.E]) * nt;
-    const int64_t first = blockIdx.x / CG, step = gridDim.x / CG;
+    const int64_t first = blockIdx.x / (CG * split), step = gridDim.x / (CG * split);
     constexpr uint32_t idesc = mma_desc(CG * BM, BN, MODE == WGRAD, MODE != FWD);
 
     if (warp == 0) {
         if (lane == 0) {
             uint32_t n = 0;   // slices loaded so far
             for (int64_t t = first; t < total && !*gave_up; t += step) {
-                const Tile w = tile_at<MODE, CG>(c, s.start, s.tiles, t, nt, tile_cols, rank);
-                const int part = rank * (BN / 2);   // of B's 256 rows or columns
-                for (int k = 0; k < w.depth; k += BK, ++n) {
+                const Tile w = tile_at<MODE, CG>(c, s.start, s.tiles, t, nt, tile_cols, rank, part, split);
+                const int off = rank * (BN / 2);   // in B's 256 rows or columns
+                for (int k = w.k0; k < w.k1; k += BK, ++n) {
                     const int i = n % STAGES;
                     if (!mbar_wait(smem_u32(&s.empty[i]), ((n / STAGES) & 1) ^ 1, gave_up)) break;
                     uint32_t bar = smem_u32(&s.full[i]);
@@ -331,7 +393,7 @@ __global__ void __launch_bounds__(tc_threads(MODE), 1)
                         for (int j = 0; j < BM / 64; ++j)
                             tma_load<CG>(a + j * BOX_BYTES, &map_a, bar, w.m0 + 64 * j, w.row0 + k);
                         for (int j = 0; j < BN / CG / 64; ++j)
-                            tma_load<CG>(b + j * BOX_BYTES, &map_b, bar, w.c0 + part + 64 * j, w.row0 + k);
+                            tma_load<CG>(b + j * BOX_BYTES, &map_b, bar, w.c0 + off + 64 * j, w.row0 + k);
                     } else {
                         // A part without rows reads zeros from past the end of x: the
                         // products are made all the same, but on less power and no bytes.
@@ -343,7 +405,7 @@ __global__ void __launch_bounds__(tc_threads(MODE), 1)
                                              w.c0 + j * (GATED ? c.epi.cols : BN / 2), w.e);
                         } else {
                             for (int j = 0; j < BN / CG / 64; ++j)
-                                tma_load<CG>(b + j * BOX_BYTES, &map_b, bar, w.c0 + part + 64 * j, k, w.e);
+                                tma_load<CG>(b + j * BOX_BYTES, &map_b, bar, w.c0 + off + 64 * j, k, w.e);
                         }
                     }
                 }
@@ -363,14 +425,14 @@ __global__ void __launch_bounds__(tc_threads(MODE), 1)
         uint32_t ragged = 0;      // bit i: the phase of stage i's ragged slices
         bool ok = true;
         for (int64_t t = first; t < total && ok; t += step) {
-            const Tile w = tile_at<MODE, CG>(c, s.start, s.tiles, t, nt, tile_cols, rank);
-            if (w.depth == 0) continue;
+            const Tile w = tile_at<MODE, CG>(c, s.start, s.tiles, t, nt, tile_cols, rank, part, split);
+            if (w.k0 >= w.k1) continue;
             const int acc = it & 1;
             ok = __all_sync(FULL_MASK, mbar_wait(smem_u32(&s.acc_empty[acc]), ((it >> 1) & 1) ^ 1, gave_up));
             if (!ok) break;
             tc_fence_after();
             const uint32_t d = tmem + acc * BN;
-            for (int k = 0; k < w.depth; k += BK, ++n) {
+            for (int k = w.k0; k < w.k1; k += BK, ++n) {
                 const int i = n % STAGES;
                 ok = __all_sync(FULL_MASK, mbar_wait(smem_u32(&s.full[i]), (n / STAGES) & 1, gave_up));
                 if (!ok) break;
@@ -390,7 +452,7 @@ __global__ void __launch_bounds__(tc_threads(MODE), 1)
                     for (int q = 0; q < steps; ++q)
                         tc_mma<CG>(d, tile_desc(a + q * (MODE == WGRAD ? 2048 : 32), BOX_BYTES),
                                    tile_desc(b + q * (MODE == FWD ? 32 : 2048), BOX_BYTES), idesc,
-                                   (k | q) != 0);
+                                   k != w.k0 || q != 0);
                     tc_commit<CG>(smem_u32(&s.empty[i]));
                 }
                 __syncwarp();
@@ -409,7 +471,7 @@ __global__ void __launch_bounds__(tc_threads(MODE), 1)
         uint32_t n = 0, ragged = 0;
         bool ok = true;
         for (int64_t t = first; t < total && ok; t += step) {
-            const Tile w = tile_at<MODE, CG>(c, s.start, s.tiles, t, nt, tile_cols, rank);
+            const Tile w = tile_at<MODE, CG>(c, s.start, s.tiles, t, nt, tile_cols, rank, part, split);
             n += (w.depth + BK - 1) / BK;
             if (w.depth % BK == 0) continue;
             const int i = (n - 1) % STAGES;
@@ -424,9 +486,14 @@ __global__ void __launch_bounds__(tc_threads(MODE), 1)
     } else if (MODE == WGRAD && warp >= 2 + EPI_WARPS) {
         if (c.epi.g_bias != nullptr || c.epi.g_bias_f32 != nullptr)
             for (int64_t t = first; t < total; t += step) {
-                const Tile w = tile_at<MODE, CG>(c, s.start, s.tiles, t, nt, tile_cols, rank);
+                const Tile w = tile_at<MODE, CG>(c, s.start, s.tiles, t, nt, tile_cols, rank, part, split);
                 if (w.c0 == 0) {
-                    column_sums(c, w, s.sums, threadIdx.x - 64 - 32 * EPI_WARPS);
+                    const int tid = threadIdx.x - 64 - 32 * EPI_WARPS;
+                    const float sum = column_sum(c, w, s.sums, tid);
+                    if (split == 1)
+                        put_bias_grad(c, w, tid, sum);
+                    else
+                        s.sum[tid] = sum;
                     __syncwarp();
                 }
             }
@@ -436,43 +503,43 @@ __global__ void __launch_bounds__(tc_threads(MODE), 1)
         WarpWriter out = {ring + RING_BYTES + (warp - 2) * STAGING, stores, lane, 0};
         uint32_t it = 0;
         for (int64_t t = first; t < total; t += step) {
-            const Tile w = tile_at<MODE, CG>(c, s.start, s.tiles, t, nt, tile_cols, rank);
-            if (MODE == WGRAD && w.depth == 0 && c.epi.add) continue;   // nothing to add
-            out.rows = min(w.m1 - (w.m0 + quad * 32), 32);
-            const bool valid = lane < out.rows;
-            const int row = min(w.m0 + quad * 32 + lane, w.m1 - 1);   // lanes past the end read the last
+            const Tile w = tile_at<MODE, CG>(c, s.start, s.tiles, t, nt, tile_cols, rank, part, split);
+            const bool any = w.k0 < w.k1;   // products were made
+            if (MODE == WGRAD && !any && c.epi.add && split == 1) continue;   // nothing to add
             const int acc = it & 1;
-            const int j0 = half * (tile_cols / 2), j1 = j0 + tile_cols / 2;
-            if (w.depth != 0) {
+            if (any) {
                 // Should the wait be given up, the results are flagged as invalid and
                 // the loop goes on, so that every warp meets the others.
                 (void)mbar_wait(smem_u32(&s.acc_full[acc]), (it >> 1) & 1, gave_up);
                 __syncwarp();
                 tc_fence_after();
             }
+            const int j0 = half * (tile_cols / 2), j1 = j0 + tile_cols / 2;
             const uint32_t d = tmem + acc * BN + (static_cast<uint32_t>(quad * 32) << 16);
             for (int j = j0; j < j1; j += EPI_COLS) {
-                const int col = w.c0 + j;
-                if (col >= c.epi.cols) break;
+                if (w.c0 + j >= c.epi.cols) break;
                 float z[EPI_COLS], u[EPI_COLS];
-                if (w.depth != 0) {
+                if (any) {
                     tmem_load32(d + j, z);
                     if (GATED) tmem_load32(d + BN / 2 + j, u);
                     tmem_load_wait();
                 } else {
 #pragma unroll
-                    for (int i = 0; i < EPI_COLS; ++i) z[i] = 0.0f;
+                    for (int i = 0; i < EPI_COLS; ++i) z[i] = u[i] = 0.0f;
                 }
-                if (out.rows > 0) {
-                    const int n = min(EPI_COLS, c.epi.cols - col);
-                    if (MODE == FWD) epi_fwd<GATED>(c.epi, out, w.e, row, col, n, valid, z, u);
-                    if (MODE == DGRAD) epi_dgrad(c.epi, out, row, col, n, valid, z);
-                    if (MODE == WGRAD)
-                        epi_wgrad(c.epi, out, static_cast<int64_t>(w.e) * c.N + row, col, n, valid, z);
+                if (split == 1) {
+                    finish<MODE, GATED>(c, out, w, quad, j, z, u);
+                } else {   // the ring is idle: all of this CTA's products are done
+                    float4 *to = reinterpret_cast<float4 *>(ring) + ((quad * 32 + lane) * JOIN_PITCH + j) / 4;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        to[i] = make_float4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]);
+                        if (GATED) to[i + BN / 8] = make_float4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+                    }
                 }
                 __syncwarp();
             }
-            if (w.depth != 0) {
+            if (any) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
@@ -484,9 +551,38 @@ __global__ void __launch_bounds__(tc_threads(MODE), 1)
                 ++it;
             }
         }
-        if (lane == 0) tma_store_done();
+        if (split == 1 && lane == 0) tma_store_done();
     }
     __syncwarp();
+    if (CG == 1 && split > 1) {   // one tile a cluster: its parts are joined
+        cluster_sync();
+        if (first < total) {
+            const Tile w = tile_at<MODE, CG>(c, s.start, s.tiles, first, nt, tile_cols, rank, part, split);
+            if (warp >= 2 && warp < 2 + EPI_WARPS) {
+                WarpWriter out = {ring + RING_BYTES + (warp - 2) * STAGING, stores, lane, 0};
+                for (int q = (warp - 2) * split + part; q < 4 * (tile_cols / EPI_COLS); q += EPI_WARPS * split) {
+                    const int quad = q & 3, j = (q >> 2) * EPI_COLS;
+                    if (w.c0 + j >= c.epi.cols) continue;
+                    const uint32_t at = smem_u32(ring) + (quad * 32 * JOIN_PITCH + j) * 4;
+                    float *turn = reinterpret_cast<float *>(ring + JOIN_BYTES + (warp - 2) * TURN_BYTES);
+                    float z[EPI_COLS], u[EPI_COLS];
+                    join32(at, split, turn, lane, z);
+                    if (GATED) join32(at + BN / 2 * 4, split, turn, lane, u);
+                    finish<MODE, GATED>(c, out, w, quad, j, z, u);
+                    __syncwarp();
+                }
+                if (lane == 0) tma_store_done();
+            } else if (MODE == WGRAD && warp >= 2 + EPI_WARPS && part == 0 && w.c0 == 0 &&
+                       (c.epi.g_bias != nullptr || c.epi.g_bias_f32 != nullptr)) {
+                const int tid = threadIdx.x - 64 - 32 * EPI_WARPS;
+                float t = 0.0f;
+                for (int r = 0; r < split; ++r) t += peer_float(at_rank(smem_u32(&s.sum[tid]), r));
+                put_bias_grad(c, w, tid, t);
+            }
+        }
+        __syncwarp();
+        cluster_sync();   // peers have read this CTA's part
+    }
     tc_fence_before();
     if (CG == 2)
         cluster_sync();   // the pair's products and arrivals are done
@@ -540,9 +636,17 @@ mp_status_t launch_tc(const ExpertCall &c, const CUtensorMap &a, const CUtensorM
     const int64_t nt = (c.epi.cols + (GATED ? BN / 2 : BN) - 1) / (GATED ? BN / 2 : BN);
     const int64_t mt = MODE == WGRAD ? static_cast<int64_t>(c.E) * ((c.N + CG * BM - 1) / (CG * BM))
                                      : c.R / (CG * BM) + (c.R < c.E ? c.R : c.E);
+    // Too few tiles for the SMs: the contraction of each is split over a cluster,
+    // four slices a CTA at least.  Weight gradients of one expert of 21,063 rows,
+    // 112 x 1,624, 7 tiles: 168 us whole, 93, 56, 39 with 2, 4, 8 parts; 64 rows by
+    // 512 x 4,096, 4 tiles: 25.2, then 19.7, 18.3, 18.8.
+    int split = 1;
+    const int64_t depth = MODE == FWD ? c.K : MODE == DGRAD ? c.N : c.R / c.E;
+    if (CG == 1)
+        while (split < 8 && nt * mt * split * 2 <= sm_count() && depth / BK >= 4 * split) split *= 2;
     const int64_t tiles = nt * mt, room = CG == 1 ? sm_count() : pair_count(k_expert_tc<MODE, GATED, CG>, tc_threads(MODE));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = static_cast<unsigned>(CG * (tiles < room ? tiles : room));
+    cfg.gridDim = static_cast<unsigned>(split > 1 ? split * tiles : CG * (tiles < room ? tiles : room));
     cfg.blockDim = tc_threads(MODE);
     cfg.dynamicSmemBytes = TC_SMEM;
     cfg.stream = c.stream;
@@ -550,11 +654,11 @@ mp_status_t launch_tc(const ExpertCall &c, const CUtensorMap &a, const CUtensorM
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.x = CG * split;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CG == 1 ? 1 : 2;
-    (void)cudaLaunchKernelEx(&cfg, k_expert_tc<MODE, GATED, CG>, a, b, m, c);
+    cfg.numAttrs = CG * split == 1 ? 1 : 2;
+    (void)cudaLaunchKernelEx(&cfg, k_expert_tc<MODE, GATED, CG>, a, b, m, c, split);
     return check_launch();
 }
 
@@ -565,9 +669,12 @@ mp_status_t launch_tc(const ExpertCall &c, const CUtensorMap &a, const CUtensorM
 // average: 384 rows an expert 175 -> 197 us, 512 rows 752 -> 638.  In WGRAD the
 // rows are the contraction, and with few of them the hand-over of the accumulator
 // between the CTAs counts: 128 rows an expert 223 -> 372 us, 384 rows 193 -> 198.
+// With fewer tiles than SMs a split of each tile does more (launch_tc).
 template <int MODE> bool in_pairs(const ExpertCall &c)
 {
-    return c.R >= (MODE == WGRAD ? 1024 : 512) * static_cast<int64_t>(c.E);
+    const int64_t cols = act_gated(c.epi.act) && MODE == FWD ? 2ll * c.epi.cols : c.epi.cols;
+    return c.R >= (MODE == WGRAD ? 1024 : 512) * static_cast<int64_t>(c.E) &&
+           (cols + BN - 1) / BN * (MODE == WGRAD ? static_cast<int64_t>(c.E) * ((c.N + BM - 1) / BM) : c.R / BM) >= sm_count();
 }
 
 }  // namespace
