@@ -78,11 +78,12 @@ def _stream(device):
 
 
 _here = contextlib.nullcontext()
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _on(device):
     """Context that makes `device` current for the call (free when it is)."""
-    if device.index == torch.cuda.current_device():
+    if device.index == _current_device():
         return _here
     return torch.cuda.device(device)
 
@@ -337,11 +338,14 @@ def _products(rows, name, w, offsets, width):
     _need(rows, name, torch.bfloat16, 2)
     dev = rows.device
     _need(w, "w", torch.bfloat16, 3, dev)
-    E, N, K = w.shape
-    _shape(rows, name, (rows.shape[0], w.shape[width]))
     _need(offsets, "offsets", torch.int32, 1, dev)
-    _shape(offsets, "offsets", (E + 1,))
-    return dev, rows.shape[0], E, N, K
+    shape = E, N, K = w.shape
+    R, columns = rows.shape
+    if columns != shape[width]:
+        _shape(rows, name, (R, shape[width]))
+    if offsets.shape[0] != E + 1:
+        _shape(offsets, "offsets", (E + 1,))
+    return dev, R, E, N, K
 
 
 def mp_expert_gemm(x, w, offsets, *, bias=None, act: str = "none", residual=None,
