@@ -115,33 +115,40 @@ struct Tile {
 
 template <int MODE, int CG>
 __device__ __forceinline__ Tile tile_at(const ExpertCall &c, const int *start, const int *tiles,
-                                        int64_t t, int nt, int tile_cols, int rank, int part, int parts)
+                                        int t, int nt, int tile_cols, int rank, int part, int parts)
 {
     constexpr int TM = CG * BM;
     Tile r;
+    int at, mt;   // the tile's place among its expert's, which are mt high
     if (MODE == WGRAD) {
-        const int mt = (c.N + TM - 1) / TM;
-        const int64_t per = static_cast<int64_t>(mt) * nt;
-        r.e = static_cast<int>(t / per);
-        const int64_t at = t - r.e * per;
-        r.m0 = static_cast<int>(at % mt) * TM + rank * BM;
+        mt = (c.N + TM - 1) / TM;
+        r.e = t / (mt * nt);
+        at = t - r.e * (mt * nt);
+    } else {
+        r.e = expert_of_tile(tiles, c.E, t / nt);
+        mt = tiles[r.e + 1] - tiles[r.e];
+        at = t - tiles[r.e] * nt;
+    }
+    const int column = at / mt, m0 = (at - column * mt) * TM + rank * BM;
+    r.c0 = column * tile_cols;
+    if (MODE == WGRAD) {
+        r.m0 = m0;
         r.m1 = c.N;
-        r.c0 = static_cast<int>(at / mt) * tile_cols;
         r.row0 = start[r.e];
         r.depth = start[r.e + 1] - r.row0;
     } else {
-        r.e = expert_of_tile(tiles, c.E, static_cast<int>(t / nt));
-        const int mt = tiles[r.e + 1] - tiles[r.e];
-        const int64_t at = t - static_cast<int64_t>(tiles[r.e]) * nt;
-        r.m0 = start[r.e] + static_cast<int>(at % mt) * TM + rank * BM;
+        r.m0 = start[r.e] + m0;
         r.m1 = start[r.e + 1];
-        r.c0 = static_cast<int>(at / mt) * tile_cols;
         r.row0 = 0;
         r.depth = MODE == FWD ? c.K : c.N;
     }
-    const int64_t slices = (r.depth + BK - 1) / BK;
-    r.k0 = static_cast<int>(slices * part / parts) * BK;
-    r.k1 = min(static_cast<int>(slices * (part + 1) / parts) * BK, r.depth);
+    r.k0 = 0;
+    r.k1 = r.depth;
+    if (parts > 1) {
+        const int slices = (r.depth + BK - 1) / BK;   // at most 2^25, and parts at most 8
+        r.k0 = slices * part / parts * BK;
+        r.k1 = min(slices * (part + 1) / parts * BK, r.depth);
+    }
     return r;
 }
 
@@ -213,12 +220,12 @@ __device__ __forceinline__ void sums_sync() { asm volatile("bar.sync 1, %0;" ::"
 
 // The bias gradient of a tile's 128 columns of g: column sums over the expert's
 // rows, by warps that wait for nothing else, beside the product.  A thread has 8
-// columns of every eighth row, sixteen rows in flight; the sums of a warp, then of the
+// columns of every eighth row, eight rows in flight; the sums of a warp, then of the
 // warps, are added in order.  256 experts of 128 rows, 1,024 x 2,048: a kernel of
 // its own after this one took 28 us more, the epilogue warps doing it 24.
 __device__ __forceinline__ float column_sum(const ExpertCall &c, const Tile &w, float (&sums)[SUM_WARPS][BM], int tid)
 {
-    constexpr int ROWS = 2 * SUM_WARPS, DEEP = 16;
+    constexpr int ROWS = 2 * SUM_WARPS, DEEP = 8;
     const int col = w.m0 + (tid & 15) * 8, warp = tid >> 5;
     float s[8] = {};
     if (col < c.N) {
@@ -364,16 +371,14 @@ __global__ void __launch_bounds__(tc_threads(MODE), 1)
     const uint32_t tmem = s.tmem;
     constexpr int tile_cols = GATED ? BN / 2 : BN;
     const int nt = (c.epi.cols + tile_cols - 1) / tile_cols;
-    const int64_t total = MODE == WGRAD
-                              ? static_cast<int64_t>(c.E) * ((c.N + CG * BM - 1) / (CG * BM)) * nt
-                              : static_cast<int64_t>(s.tiles[c.E]) * nt;
-    const int64_t first = blockIdx.x / (CG * split), step = gridDim.x / (CG * split);
+    const int total = (MODE == WGRAD ? c.E * ((c.N + CG * BM - 1) / (CG * BM)) : s.tiles[c.E]) * nt;
+    const int first = blockIdx.x / (CG * split), step = gridDim.x / (CG * split);
     constexpr uint32_t idesc = mma_desc(CG * BM, BN, MODE == WGRAD, MODE != FWD);
 
     if (warp == 0) {
         if (lane == 0) {
             uint32_t n = 0;   // slices loaded so far
-            for (int64_t t = first; t < total && !*gave_up; t += step) {
+            for (int t = first; t < total && !*gave_up; t += step) {
                 const Tile w = tile_at<MODE, CG>(c, s.start, s.tiles, t, nt, tile_cols, rank, part, split);
                 const int off = rank * (BN / 2);   // in B's 256 rows or columns
                 for (int k = w.k0; k < w.k1; k += BK, ++n) {
@@ -424,7 +429,7 @@ __global__ void __launch_bounds__(tc_threads(MODE), 1)
         uint32_t n = 0, it = 0;   // slices and accumulators used so far
         uint32_t ragged = 0;      // bit i: the phase of stage i's ragged slices
         bool ok = true;
-        for (int64_t t = first; t < total && ok; t += step) {
+        for (int t = first; t < total && ok; t += step) {
             const Tile w = tile_at<MODE, CG>(c, s.start, s.tiles, t, nt, tile_cols, rank, part, split);
             if (w.k0 >= w.k1) continue;
             const int acc = it & 1;
@@ -470,7 +475,7 @@ __global__ void __launch_bounds__(tc_threads(MODE), 1)
         // CTA 1 of a pair: zeroes its part of the ragged slices, and says so.
         uint32_t n = 0, ragged = 0;
         bool ok = true;
-        for (int64_t t = first; t < total && ok; t += step) {
+        for (int t = first; t < total && ok; t += step) {
             const Tile w = tile_at<MODE, CG>(c, s.start, s.tiles, t, nt, tile_cols, rank, part, split);
             n += (w.depth + BK - 1) / BK;
             if (w.depth % BK == 0) continue;
@@ -485,7 +490,7 @@ __global__ void __launch_bounds__(tc_threads(MODE), 1)
         if (!ok && lane == 0) or_status(c.status, MP_STATUS_STALLED);
     } else if (MODE == WGRAD && warp >= 2 + EPI_WARPS) {
         if (c.epi.g_bias != nullptr || c.epi.g_bias_f32 != nullptr)
-            for (int64_t t = first; t < total; t += step) {
+            for (int t = first; t < total; t += step) {
                 const Tile w = tile_at<MODE, CG>(c, s.start, s.tiles, t, nt, tile_cols, rank, part, split);
                 if (w.c0 == 0) {
                     const int tid = threadIdx.x - 64 - 32 * EPI_WARPS;
@@ -502,7 +507,7 @@ __global__ void __launch_bounds__(tc_threads(MODE), 1)
         const int half = (warp - 2) >> 2;     // and its half of the columns
         WarpWriter out = {ring + RING_BYTES + (warp - 2) * STAGING, stores, lane, 0};
         uint32_t it = 0;
-        for (int64_t t = first; t < total; t += step) {
+        for (int t = first; t < total; t += step) {
             const Tile w = tile_at<MODE, CG>(c, s.start, s.tiles, t, nt, tile_cols, rank, part, split);
             const bool any = w.k0 < w.k1;   // products were made
             if (MODE == WGRAD && !any && c.epi.add && split == 1) continue;   // nothing to add
@@ -636,6 +641,7 @@ mp_status_t launch_tc(const ExpertCall &c, const CUtensorMap &a, const CUtensorM
     const int64_t nt = (c.epi.cols + (GATED ? BN / 2 : BN) - 1) / (GATED ? BN / 2 : BN);
     const int64_t mt = MODE == WGRAD ? static_cast<int64_t>(c.E) * ((c.N + CG * BM - 1) / (CG * BM))
                                      : c.R / (CG * BM) + (c.R < c.E ? c.R : c.E);
+    if (nt * mt > INT32_MAX / 2) return MP_ERR_UNSUPPORTED;   // tiles are counted in 32 bits
     // Too few tiles for the SMs: the contraction of each is split over a cluster,
     // four slices a CTA at least.  Weight gradients of one expert of 21,063 rows,
     // 112 x 1,624, 7 tiles: 168 us whole, 93, 56, 39 with 2, 4, 8 parts; 64 rows by
