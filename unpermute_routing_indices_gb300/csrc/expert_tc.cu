@@ -205,11 +205,13 @@ struct WarpWriter {
 // and returns how many steps of 16 there are.
 template <int CG> __device__ __forceinline__ int zero_ragged(uint8_t *tile, int rows, int lane)
 {
-    const int steps = (rows + 15) / 16, n = 16 * steps - rows;
-    for (int v = lane; v < n * (Ring<CG>::STAGE / BOX_BYTES) * 8; v += 32) {
-        const int row = rows + (v >> 3) % n, box = (v >> 3) / n;
-        *reinterpret_cast<uint4 *>(tile + box * BOX_BYTES + row * 128 + (v & 7) * 16) = make_uint4(0, 0, 0, 0);
-    }
+    const int steps = (rows + 15) / 16;
+    uint8_t *piece = tile + (lane >> 3) * BOX_BYTES + (lane & 7) * 16;   // four boxes at a time
+    for (int row = rows; row < 16 * steps; ++row)
+#pragma unroll
+        for (int box = 0; box < Ring<CG>::STAGE / BOX_BYTES; box += 4)
+            if (box + (lane >> 3) < Ring<CG>::STAGE / BOX_BYTES)
+                *reinterpret_cast<uint4 *>(piece + box * BOX_BYTES + row * 128) = make_uint4(0, 0, 0, 0);
     fence_async_smem();
     __syncwarp();
     return steps;
@@ -671,15 +673,18 @@ mp_status_t launch_tc(const ExpertCall &c, const CUtensorMap &a, const CUtensorM
 // Whether pairs of CTAs take the call.  A pair reads a third less per product from
 // L2, which bounds the single CTAs: 131,072 x 4,096 rows by 128 experts of 2,048
 // 1,377 -> 1,211 us; weight gradients of 8 x 2,048 rows, 4,096 x 4,096, 370 -> 344.
-// But its tile has 256 rows, of which an expert leaves half of one empty on
-// average: 384 rows an expert 175 -> 197 us, 512 rows 752 -> 638.  In WGRAD the
-// rows are the contraction, and with few of them the hand-over of the accumulator
-// between the CTAs counts: 128 rows an expert 223 -> 372 us, 384 rows 193 -> 198.
+// But its tile has 256 rows, of which an expert leaves half of one empty on average,
+// and in WGRAD, where the rows are the contraction, the hand-over of the accumulator
+// between the CTAs counts when there are few.  64 experts of 2,048 columns, one in
+// eight empty, depth 2,048 / 1,024: 384 rows an expert 177.6 -> 177.0 / 94.0 -> 90.5 us,
+// 512 rows 216 -> 211 / 114 -> 108, 1,024 rows 391 -> 373 / 204 -> 188.  Weight
+// gradients: 128 rows an expert (256 experts) 223 -> 372, 384 rows 219.6 -> 220.1,
+// 512 rows 263 -> 253.
 // With fewer tiles than SMs a split of each tile does more (launch_tc).
 template <int MODE> bool in_pairs(const ExpertCall &c)
 {
     const int64_t cols = act_gated(c.epi.act) && MODE == FWD ? 2ll * c.epi.cols : c.epi.cols;
-    return c.R >= (MODE == WGRAD ? 1024 : 512) * static_cast<int64_t>(c.E) &&
+    return c.R >= (MODE == WGRAD ? 512 : 384) * static_cast<int64_t>(c.E) &&
            (cols + BN - 1) / BN * (MODE == WGRAD ? static_cast<int64_t>(c.E) * ((c.N + BM - 1) / BM) : c.R / BM) >= sm_count();
 }
 
