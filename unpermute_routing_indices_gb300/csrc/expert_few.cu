@@ -310,9 +310,15 @@ mp_status_t launch_few(const ExpertCall &c, const CUtensorMap &w, const CUtensor
 
 }  // namespace
 
+// Up to 8 rows an expert, 16 when gated (the tile then has twice the weights to a
+// row of x), and up to 64 rows in all, where k_expert_tc has too few tiles.  us
+// here / there: 64 experts of 2,048 (gated, depth 2,048) 64 rows 52 / 63, 1,024 rows 87 / 89,
+// 2,048 rows 94 / 90; depth 1,024, not gated, 64 rows 34.4 / 35.5, 512 rows 48.7 / 48.2, 1,024
+// rows 52 / 49; one expert of 2,048 x 4,096, 16 rows 8.3 / 19.0, 64 rows 13 / 19, 128 rows
+// 19.7 / 19.4.
 bool expert_few_takes(const ExpertCall &c)
 {
-    return expert_tc_takes<FWD>(c) && c.R <= 32 * static_cast<int64_t>(c.E);
+    return expert_tc_takes<FWD>(c) && (c.R <= 64 || c.R <= (act_gated(c.epi.act) ? 16 : 8) * static_cast<int64_t>(c.E));
 }
 
 mp_status_t expert_few(const ExpertCall &c)
