@@ -198,6 +198,57 @@ def test_scores_next_to_each_other():
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("E,top,copies", [(32, 2, 1), (32, 1, 1), (128, 2, 1), (128, 2, 2), (96, 1, 2)])
+def test_groups_next_to_each_other(score, with_bias, E, top, copies):
+    """Groups whose worths differ by a step of one logit, at the border of those
+    kept: two of them, and three."""
+    G, K, T = 4, 6, 200
+    n = E // G
+    rng = np.random.default_rng(E + top + copies)
+    l = rng.standard_normal((T, G, n)).astype(np.float32)
+    bias = (0.05 * rng.standard_normal((G, n))).astype(np.float32)
+    l[:, 0] += 3                                   # kept in any case
+    for g in range(2, 2 + copies):                 # the copies of group 1, a step off
+        l[:, g] = l[:, 1]
+        bias[g] = bias[1]
+        t = np.arange(T)
+        best = np.argmax(l[:, g] + 4 * bias[g], axis=1)
+        l[t, g, best] = np.nextafter(l[t, g, best], np.where(t % 3 == g % 3, np.float32(9), np.float32(-9)))
+    l[:, 2 + copies:] -= 3
+    l, bias = l.reshape(T, E), bias.reshape(E)
+    idx, _ = mp.mp_route(torch.from_numpy(l).to(DEV), K, score=score, n_groups=G, topk_groups=2,
+                         group_top=top, bias=torch.from_numpy(bias).to(DEV) if with_bias else None)
+    s, usable = scores(l.astype(np.float64), score)
+    want = choose(l.astype(np.float64), s, usable, K, bias.astype(np.float64) if with_bias else None,
+                  G, 2, top)
+    np.testing.assert_array_equal(idx.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("step", [1, 3, 40])
+def test_picks_next_to_each_other(step):
+    """Runs of scores a few steps of fp32 apart around the last place."""
+    E, K, T = 96, 8, 300
+    rng = np.random.default_rng(step)
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    bias = (0.1 * rng.standard_normal(E)).astype(np.float32)
+    c = 1 / (1 + np.exp(-l.astype(np.float64))) + bias
+    order = np.argsort(-c, axis=1)
+    for t in range(T):
+        at = order[t, K - 1]
+        for i in range(1 + t % 3):                 # the next one, two, three
+            e = order[t, K + i]
+            target = c[t, at] - bias[e] + (rng.integers(-step, step + 1)) * 2.0 ** -25
+            target = min(max(target, 1e-3), 1 - 1e-3)
+            l[t, e] = np.float32(np.log(target / (1 - target)))
+    idx, _ = mp.mp_route(torch.from_numpy(l).to(DEV), K, score="sigmoid",
+                         bias=torch.from_numpy(bias).to(DEV))
+    s, usable = scores(l.astype(np.float64), "sigmoid")
+    want = choose(l.astype(np.float64), s, usable, K, bias.astype(np.float64), 1, 1, 1)
+    np.testing.assert_array_equal(idx.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [False, True])
 @pytest.mark.parametrize("groups", [(1, 1, 1), (4, 2, 2)])
 def test_unavailable_experts(score, renorm, groups):

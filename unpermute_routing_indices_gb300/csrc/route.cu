@@ -8,10 +8,11 @@
 // Choice.  Without a bias the scores rise with the logits, which are compared
 // as they are.  With one, and for the sum of a group's best two, fp32 values of
 // c decide wherever neighbours in the order are further apart than their errors
-// can be (too_near); a token where two are nearer (about one of a thousand of
-// normal logits) is decided again in 64 bits (choose_exact).  So the choice is
+// can be (too_near); a token where two are nearer (about one of two thousand of
+// normal logits) is decided again in 64 bits: the two groups or the picks and the best
+// of the rest where that is enough, else everything (choose_exact).  So the choice is
 // that of 64 bits everywhere, at the cost of 32: on 32,768 tokens of 256 experts
-// (sigmoid, bias, 8 groups), all of it in 64 bits took 1,290 us, this 43.
+// (sigmoid, bias, 8 groups), all of it in 64 bits took 1,290 us, this 39 (43 with choose_exact for all near tokens).
 // Each lane sorts its candidates by a fixed network and a round takes the best
 // head of the warp (topk.cuh); the round after the K-th says how near the best
 // of the rest is.
@@ -169,6 +170,73 @@ __device__ __forceinline__ double rcp_exact(double x)
     return fma(r, fma(-x, r, 1.0), r);
 }
 
+// A score that decides, in 64 bits: for softmax without the common divisor, and so
+// only where there is no bias.  `m`: the largest logit (softmax).  0: cannot be chosen.
+template <typename L>
+__device__ __forceinline__ uint64_t exact_key(const RouteArgs &a, const L *l, int e, float m)
+{
+    const float v = logit(l + e), b = a.bias != nullptr ? __ldg(a.bias + e) : 0.0f;
+    if (!usable(v) || !usable(b)) return 0ull;
+    const double x = fminf(v, FLT_MAX);
+    double c;
+    if (a.score == MP_SCORE_SIGMOID) {
+        const double t = exp_neg(fabs(x));
+        c = (x < 0.0 ? t : 1.0) * rcp_exact(1.0 + t);
+    } else {
+        c = exp_neg(static_cast<double>(m) - x);
+    }
+    return order_key(c + static_cast<double>(b));
+}
+
+// Whether group gb stands before ga in 64 bits, by the sum of their best one or two.
+template <typename L>
+__device__ __noinline__ bool groups_turned(const RouteArgs &a, const L *l, int lane, int ga, int gb)
+{
+    float m = -INFINITY;
+    if (a.score == MP_SCORE_SOFTMAX) {
+        for (int e = lane; e < a.E; e += 32) m = fmaxf(m, fminf(logit(l + e), FLT_MAX));   // NaN is passed over
+        m = warp_max(m);
+    }
+    const int n = a.E / a.n_groups;
+    uint64_t worth[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        uint64_t k1 = 0ull, k2 = 0ull;
+        for (int i = lane; i < n; i += 32) {
+            const uint64_t k = exact_key(a, l, (q ? gb : ga) * n + i, m);
+            k2 = max(k2, min(k, k1));
+            k1 = max(k1, k);
+        }
+        uint64_t w = k1;
+        const uint32_t holder = warp_argmax_key(w, static_cast<uint32_t>(lane));
+        if (a.group_top == 2) {
+            uint64_t m2 = lane == holder ? k2 : k1;
+            (void)warp_argmax_key(m2, static_cast<uint32_t>(lane));
+            if (m2 != 0ull) w = order_key(key_value(w) + key_value(m2));
+        }
+        worth[q] = w;
+    }
+    return worth[1] > worth[0] || (worth[1] == worth[0] && gb < ga);
+}
+
+// Orders the experts of lanes 0..K (-1: none) in 64 bits; lane k < K gets the k-th.
+template <typename L>
+__device__ __noinline__ int picks_in_order(const RouteArgs &a, const L *l, int lane, int K, int expert)
+{
+    const uint64_t key = expert >= 0 ? exact_key(a, l, expert, 0.0f) : 0ull;
+    int rank = 0, got = -1;
+    for (int j = 0; j <= K; ++j) {
+        const uint64_t k = __shfl_sync(FULL_MASK, key, j);
+        const int e = __shfl_sync(FULL_MASK, expert, j);
+        rank += k > key || (k == key && e < expert);
+    }
+    for (int j = 0; j <= K; ++j) {
+        const int at = __shfl_sync(FULL_MASK, rank, j), e = __shfl_sync(FULL_MASK, expert, j);
+        if (at == lane && e >= 0) got = e;
+    }
+    return lane < K ? got : -1;
+}
+
 // The choice in 64 bits.  Lane k gets pick k (-1: none left).
 template <typename L, int PER>
 __device__ __noinline__ int choose_exact(const RouteArgs &a, const L *l, int lane)
@@ -273,10 +341,11 @@ __device__ __forceinline__ void into_top2(uint32_t k, uint32_t &k1, uint32_t &k2
 }
 
 // Picks by 32-bit keys, 0 for none.  Lane k gets pick k's key and expert; `rest`
-// and `rest_i` are those of the best of the rest.
+// and `rest_i` are those of the best of the rest, `after` the key of the next.
 template <int N, int KT>
 __device__ __forceinline__ void rounds(uint32_t (&key)[N], uint32_t (&ex)[N], int K, int lane,
-                                       uint32_t &my_key, int &my_i, uint32_t &rest, uint32_t &rest_i)
+                                       uint32_t &my_key, int &my_i, uint32_t &rest, uint32_t &rest_i,
+                                       uint32_t &after)
 {
     sort_desc<N>(key, ex);
     if (KT > 0) K = KT;
@@ -299,6 +368,7 @@ __device__ __forceinline__ void rounds(uint32_t (&key)[N], uint32_t (&ex)[N], in
     }
     rest = key[0];
     rest_i = warp_argmax_key(rest, ex[0]);
+    after = __reduce_max_sync(FULL_MASK, ex[0] == rest_i ? key[1] : key[0]);
 }
 
 // Whether two values next to each other in a descending order, each off by at
@@ -403,13 +473,23 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs &a, const L *l, cons
             before += o > worth || (o == worth && g < lane);
         }
         const bool mine = worth != 0u && before < a.topk_groups;
-        const unsigned kept = __ballot_sync(FULL_MASK, mine);
+        unsigned kept = __ballot_sync(FULL_MASK, mine);
         if (err > 0.0f) {
             // Only the last one kept and the first one left out must stand apart.
             const uint32_t last = __reduce_min_sync(FULL_MASK, mine ? worth : 0xffffffffu);
             const uint32_t next = __reduce_max_sync(FULL_MASK, mine ? 0u : worth);
             const float slack = __uint_as_float(__reduce_max_sync(FULL_MASK, __float_as_uint(size)));
-            near = kept != 0u && too_near(last, next, 2.0f * err + 1.2e-7f * slack);
+            const float off = 2.0f * err + 1.2e-7f * slack;
+            near = kept != 0u && too_near(last, next, off);
+            if (near && (by_logit || a.score == MP_SCORE_SIGMOID)) {
+                // Mostly it is these two alone.
+                const unsigned set = __ballot_sync(
+                    FULL_MASK, worth != 0u && (mine ? too_near(worth, next, off) : too_near(last, worth, off)));
+                if (__popc(set) == 2) {
+                    if (groups_turned(a, l, lane, __ffs(set & kept) - 1, __ffs(set & ~kept) - 1)) kept ^= set;
+                    near = false;
+                }
+            }
         }
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
@@ -428,7 +508,7 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs &a, const L *l, cons
     uint32_t ex[PER];
 #pragma unroll
     for (int j = 0; j < PER; ++j) ex[j] = static_cast<uint32_t>(lane + 32 * j);
-    uint32_t my_key = 0u, rest = 0u, rest_i = 0u;
+    uint32_t my_key = 0u, rest = 0u, rest_i = 0u, after = 0u;
     int my_i = -1;
     if constexpr (PER <= 8) {
         if (PER >= 4 && __popc(cols) <= PER / 2) {
@@ -450,9 +530,9 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs &a, const L *l, cons
                     kc[0] = key[j];
                     xc[0] = ex[j];
                 }
-            rounds<HALF, KT>(kc, xc, K, lane, my_key, my_i, rest, rest_i);
+            rounds<HALF, KT>(kc, xc, K, lane, my_key, my_i, rest, rest_i, after);
         } else {
-            rounds<PER, KT>(key, ex, K, lane, my_key, my_i, rest, rest_i);
+            rounds<PER, KT>(key, ex, K, lane, my_key, my_i, rest, rest_i, after);
         }
     } else {
         // More than 256 experts: each round looks through the lane's own again.
@@ -475,6 +555,9 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs &a, const L *l, cons
             rest = bk;
             rest_i = p;
         }
+#pragma unroll
+        for (int j = 0; j < PER; ++j) after = max(after, key[j]);
+        after = __reduce_max_sync(FULL_MASK, after);
     }
     pick = (lane < K && my_key != 0u) ? my_i : -1;
     if (!by_logit) {
@@ -486,16 +569,27 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs &a, const L *l, cons
             next = rest;
             next_i = rest_i;
         }
+        bool unsure = false;
         if (lane < K && too_near(my_key, next, err))
-            near |= !(logit(l + my_i) == logit(l + next_i) && __ldg(a.bias + my_i) == __ldg(a.bias + next_i));
+            unsure = !(logit(l + my_i) == logit(l + next_i) && __ldg(a.bias + my_i) == __ldg(a.bias + next_i));
+        if (!near && __any_sync(FULL_MASK, unsure)) {
+            // Mostly the picks and the best of the rest have to be ordered, and what
+            // comes after is out of reach of the last place.
+            const uint32_t last = __shfl_sync(FULL_MASK, my_key, K - 1);
+            if (a.score == MP_SCORE_SIGMOID && K < 32 && !too_near(last, after, err))
+                pick = picks_in_order(a, l, lane, K,
+                                      lane == K ? (rest != 0u ? static_cast<int>(rest_i) : -1) : pick);
+            else
+                near = true;
+        }
     }
     return __all_sync(FULL_MASK, !near);
 }
 
 // KT > 0: a form for K = KT with the rounds unrolled.  Compiled for 4 CTAs per
-// SM up to 256 experts (32,768 x 256, sigmoid, bias: 41.4 us with 3, 38.7 with 4),
-// 3 up to 512 (16,383 x 512: 64.5 us with 1, 51.9 with 2, 48.7 with 3) and 2 up to
-// 1,024 (106.8 with 1, 90.9 with 2).
+// SM up to 256 experts (32,768 x 256, sigmoid, bias: 41.4 us with 3, 38.7 with 4
+// when this was chosen, 28.7 now), 3 up to 512 (16,383 x 512: 64.5 us with 1, 51.9 with 2,
+// 48.7 with 3; 29 now) and 2 up to 1,024 (106.8 with 1, 90.9 with 2; 60 now).
 template <typename L, int PER, int KT>
 __global__ void __launch_bounds__(RT_THREADS, PER <= 8 ? 4 : PER <= 16 ? 3 : 2) k_route(const RouteArgs a)
 {
