@@ -303,6 +303,22 @@ def test_rows_past_the_last_expert_stay(N, K):
     assert (g_x[sum(counts):] == 7.0).all() and torch.isfinite(g_x.float()).all()
 
 
+@pytest.mark.parametrize("counts", [[5, 0, 40], [0, 0, 0], [300, 700, 900], [2500]])
+@pytest.mark.parametrize("H,F", [(136, 72), (33, 40), (264, 37)])
+def test_mlp_zeroes_what_is_past_the_last_expert(counts, H, F):
+    E, more = len(counts), 13
+    R, offsets = sum(counts) + more, offsets_of(counts)
+    x, g = normal(R, H, seed=1), normal(R, H, seed=2)
+    w1, w2 = normal(E, F, H, seed=3, std=0.1), normal(E, H, F, seed=4, std=0.1)
+    junk = torch.full((R, 1000), float("nan"), dtype=torch.bfloat16, device=DEV)
+    del junk                                     # new buffers are likely to hold it
+    y, z, z_exp = mp.mp_expert_mlp(x, w1, w2, offsets, act="silu", save="e4m3")
+    g_x = mp.mp_expert_mlp_bwd(g, x, w1, w2, offsets, z, z_exp, act="silu")[0]
+    n = sum(counts)
+    assert (y[n:] == 0).all() and (g_x[n:] == 0).all()
+    assert torch.isfinite(y.float()).all() and torch.isfinite(g_x.float()).all()
+
+
 @pytest.mark.parametrize("N,K", [(64, 64), (264, 520), (33, 37)])
 def test_a_row_does_not_see_its_neighbours(N, K):
     """NaN and infinity stay in the row they are in, and the weight gradient of

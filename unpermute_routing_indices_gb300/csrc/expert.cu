@@ -121,12 +121,14 @@ bool act_ok(int32_t act) { return act >= MP_ACT_NONE && act <= MP_ACT_SWIGLU; }
 
 using namespace mp;
 
-extern "C" mp_status_t mp_expert_gemm(const mp_bf16_t *x, const mp_bf16_t *w,
-                                      const int32_t *offsets, int64_t R, int32_t E, int32_t N,
-                                      int32_t K, const mp_bf16_t *bias, int32_t act,
-                                      const mp_bf16_t *residual, mp_bf16_t *out, int32_t save,
-                                      void *z, uint8_t *z_exp, int32_t *dev_status,
-                                      mp_stream_t stream)
+namespace {
+
+// mp_expert_gemm and mp_expert_dgrad; zero_rest: rows of the result past the last
+// expert's are zeroed.
+mp_status_t gemm(const mp_bf16_t *x, const mp_bf16_t *w, const int32_t *offsets, int64_t R, int32_t E,
+                 int32_t N, int32_t K, const mp_bf16_t *bias, int32_t act, const mp_bf16_t *residual,
+                 mp_bf16_t *out, int32_t save, void *z, uint8_t *z_exp, bool zero_rest,
+                 int32_t *dev_status, mp_stream_t stream)
 {
     if (const mp_status_t s = sizes_ok(R, E, N, K); s != MP_OK) return s;
     if (!act_ok(act) || save < MP_SAVE_NONE || save > MP_SAVE_E4M3) return MP_ERR_INVALID_ARG;
@@ -142,17 +144,17 @@ extern "C" mp_status_t mp_expert_gemm(const mp_bf16_t *x, const mp_bf16_t *w,
     c.epi.act = act; c.epi.save = save; c.epi.cols = gated ? N / 2 : N;
     c.epi.bias = bias; c.epi.residual = residual; c.epi.out = out;
     c.epi.z = z; c.epi.z_exp = z_exp;
+    c.epi.zero_rest = zero_rest;
     c.status = dev_status;
     c.stream = as_stream(stream);
     if (expert_few_takes(c)) return expert_few(c);
     return product<FWD>(c);
 }
 
-extern "C" mp_status_t mp_expert_dgrad(const mp_bf16_t *g, const mp_bf16_t *w,
-                                       const int32_t *offsets, int64_t R, int32_t E, int32_t N,
-                                       int32_t K, int32_t act, int32_t save, const void *z,
-                                       const uint8_t *z_exp, mp_bf16_t *g_x, mp_bf16_t *h,
-                                       int32_t *dev_status, mp_stream_t stream)
+mp_status_t dgrad(const mp_bf16_t *g, const mp_bf16_t *w, const int32_t *offsets, int64_t R, int32_t E,
+                  int32_t N, int32_t K, int32_t act, int32_t save, const void *z,
+                  const uint8_t *z_exp, mp_bf16_t *g_x, mp_bf16_t *h, bool zero_rest,
+                  int32_t *dev_status, mp_stream_t stream)
 {
     if (const mp_status_t s = sizes_ok(R, E, N, K); s != MP_OK) return s;
     if (!act_ok(act)) return MP_ERR_INVALID_ARG;
@@ -169,9 +171,31 @@ extern "C" mp_status_t mp_expert_dgrad(const mp_bf16_t *g, const mp_bf16_t *w,
     c.epi.act = act; c.epi.save = save; c.epi.cols = K;
     c.epi.out = g_x; c.epi.h = h;
     c.epi.z = const_cast<void *>(z); c.epi.z_exp = const_cast<uint8_t *>(z_exp);
+    c.epi.zero_rest = zero_rest;
     c.status = dev_status;
     c.stream = as_stream(stream);
     return product<DGRAD>(c);
+}
+
+}  // namespace
+
+extern "C" mp_status_t mp_expert_gemm(const mp_bf16_t *x, const mp_bf16_t *w,
+                                      const int32_t *offsets, int64_t R, int32_t E, int32_t N,
+                                      int32_t K, const mp_bf16_t *bias, int32_t act,
+                                      const mp_bf16_t *residual, mp_bf16_t *out, int32_t save,
+                                      void *z, uint8_t *z_exp, int32_t *dev_status,
+                                      mp_stream_t stream)
+{
+    return gemm(x, w, offsets, R, E, N, K, bias, act, residual, out, save, z, z_exp, false, dev_status, stream);
+}
+
+extern "C" mp_status_t mp_expert_dgrad(const mp_bf16_t *g, const mp_bf16_t *w,
+                                       const int32_t *offsets, int64_t R, int32_t E, int32_t N,
+                                       int32_t K, int32_t act, int32_t save, const void *z,
+                                       const uint8_t *z_exp, mp_bf16_t *g_x, mp_bf16_t *h,
+                                       int32_t *dev_status, mp_stream_t stream)
+{
+    return dgrad(g, w, offsets, R, E, N, K, act, save, z, z_exp, g_x, h, false, dev_status, stream);
 }
 
 extern "C" mp_status_t mp_expert_wgrad(const mp_bf16_t *g, const mp_bf16_t *x,
@@ -208,12 +232,11 @@ extern "C" mp_status_t mp_expert_mlp(const mp_bf16_t *x, const mp_bf16_t *w1, co
     if (!act_ok(act) || act == MP_ACT_NONE || F < 1 || F > (1 << 21)) return MP_ERR_INVALID_ARG;
     if (const mp_status_t s = sizes_ok(R, E, O, F); s != MP_OK) return s;
     if (R > 0 && (h == nullptr || w2 == nullptr || y == nullptr)) return MP_ERR_INVALID_ARG;
-    mp_status_t s = mp_expert_gemm(x, w1, offsets, R, E, act_gated(act) ? 2 * F : F, H, b1, act, nullptr,
-                                   h, save, z, z_exp, dev_status, stream);
-    if (s == MP_OK)
-        s = mp_expert_gemm(h, w2, offsets, R, E, O, F, b2, MP_ACT_NONE, nullptr, y, MP_SAVE_NONE,
-                           nullptr, nullptr, dev_status, stream);
-    return s != MP_OK || R == 0 ? s : mp_zero_rows_from(y, R, 2ll * O, offsets + E, stream);
+    const mp_status_t s = gemm(x, w1, offsets, R, E, act_gated(act) ? 2 * F : F, H, b1, act, nullptr, h, save,
+                               z, z_exp, false, dev_status, stream);
+    if (s != MP_OK) return s;
+    return gemm(h, w2, offsets, R, E, O, F, b2, MP_ACT_NONE, nullptr, y, MP_SAVE_NONE, nullptr, nullptr, true,
+                dev_status, stream);
 }
 
 extern "C" mp_status_t mp_expert_mlp_bwd(const mp_bf16_t *g_y, const mp_bf16_t *x,
@@ -248,7 +271,6 @@ extern "C" mp_status_t mp_expert_mlp_bwd(const mp_bf16_t *g_y, const mp_bf16_t *
     c.N = P;
     if (s == MP_OK && g_b1 != nullptr && g_w1 == nullptr) s = bias_grad(g_z, c, g_b1, nullptr);
     if (s != MP_OK || g_x == nullptr || R == 0) return s;
-    s = mp_expert_dgrad(g_z, w1, offsets, R, E, P, H, MP_ACT_NONE, MP_SAVE_NONE, nullptr, nullptr, g_x,
-                        nullptr, dev_status, stream);
-    return s != MP_OK ? s : mp_zero_rows_from(g_x, R, 2ll * H, offsets + E, stream);
+    return dgrad(g_z, w1, offsets, R, E, P, H, MP_ACT_NONE, MP_SAVE_NONE, nullptr, nullptr, g_x, nullptr, true,
+                 dev_status, stream);
 }

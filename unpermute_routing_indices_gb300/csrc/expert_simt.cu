@@ -33,6 +33,13 @@ __global__ void __launch_bounds__(SIMT_THREADS) k_expert_simt(const ExpertCall c
                       blockIdx.x + blockIdx.y + blockIdx.z == 0 ? c.status : nullptr);
     __syncthreads();
 
+    if (MODE != WGRAD && c.epi.zero_rest) {
+        const int64_t blocks = static_cast<int64_t>(gridDim.x) * gridDim.y;
+        zero_rest(c.epi, start[c.E], c.R,
+                  (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * SIMT_THREADS + threadIdx.x,
+                  blocks * SIMT_THREADS);
+    }
+
     // Rows m0..m1 of A, columns from n0 of B, contraction over [0,depth).
     int e, m0, m1, depth;
     int64_t sam, sak, sbn, sbk;
