@@ -615,26 +615,29 @@ bool store_map(StoreMaps &m, int which, const void *base, int64_t parts, int64_t
     return !m.use[which] || make_map(&m.map[which], base, 2, dims, box);
 }
 
-// Pairs of CTAs that the device holds at once; the same for all these kernels, one
-// CTA to an SM.
-template <typename K> int pair_count(K kernel, int threads)
+// Clusters of `size` CTAs that the device holds at once; the same for all these
+// kernels, one CTA to an SM.
+template <typename K> int cluster_count(K kernel, int threads, int size)
 {
-    static std::atomic<int> known[64];
+    static std::atomic<int> known[64][9];
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 1;
-    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (dev < 64 && (n = known[dev][size].load(std::memory_order_relaxed)) > 0) return n;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = 2;
+    cfg.gridDim = size;
     cfg.blockDim = threads;
     cfg.dynamicSmemBytes = TC_SMEM;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = size;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) n = sm_count() / 2;
-    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+        (void)cudaGetLastError();
+        n = sm_count() / (2 * size) + 1;
+    }
+    if (dev < 64) known[dev][size].store(n, std::memory_order_relaxed);
     return n;
 }
 
@@ -648,14 +651,18 @@ mp_status_t launch_tc(const ExpertCall &c, const CUtensorMap &a, const CUtensorM
                                      : c.R / (CG * BM) + (c.R < c.E ? c.R : c.E);
     if (nt * mt > INT32_MAX / 2) return MP_ERR_UNSUPPORTED;   // tiles are counted in 32 bits
     // Too few tiles for the SMs: the contraction of each is split over a cluster,
-    // four slices a CTA at least.  Weight gradients of one expert of 21,063 rows,
-    // 112 x 1,624, 7 tiles: 168 us whole, 93, 56, 39 with 2, 4, 8 parts; 64 rows by
-    // 512 x 4,096, 4 tiles: 25.2, then 19.7, 18.3, 18.8.
+    // where 12 slices a CTA are left at least and the clusters fit the device at
+    // once.  us with 1, 2, 4, 8 parts: weight gradients of one expert of 21,063 rows,
+    // 112 x 1,624 (330 slices) 164, 90, 53, 36; 500 rows by 512 x 8,192 (128 slices) 42, 28,
+    // 22, 21; 300 rows by 3 experts of 1,000 x 4,000 (63) 25, 19, 18, 18; x 1,000 (16) 14.5, 14.0,
+    // 15.3, 15.3; 100 rows by 2 experts of 2,048 x 512 (8) 8.4, 10.1, 13.2, 13.2.
     int split = 1;
-    const int64_t depth = MODE == FWD ? c.K : MODE == DGRAD ? c.N : c.R / c.E;
+    const int64_t tiles = nt * mt, depth = MODE == FWD ? c.K : MODE == DGRAD ? c.N : c.R / c.E;
     if (CG == 1)
-        while (split < 8 && nt * mt * split * 2 <= sm_count() && depth / BK >= 4 * split) split *= 2;
-    const int64_t tiles = nt * mt, room = CG == 1 ? sm_count() : pair_count(k_expert_tc<MODE, GATED, CG>, tc_threads(MODE));
+        while (split < 8 && depth / BK >= 24 * split && tiles * split * 2 <= sm_count() &&
+               tiles <= cluster_count(k_expert_tc<MODE, GATED, CG>, tc_threads(MODE), 2 * split))
+            split *= 2;
+    const int64_t room = CG == 1 ? sm_count() : cluster_count(k_expert_tc<MODE, GATED, CG>, tc_threads(MODE), 2);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = static_cast<unsigned>(split > 1 ? split * tiles : CG * (tiles < room ? tiles : room));
     cfg.blockDim = tc_threads(MODE);
