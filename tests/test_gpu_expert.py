@@ -97,6 +97,8 @@ COUNTS = {
     "long, one empty": [2111, 0, 1985],
     "single long": [5001],           # few tiles: split contractions, ragged at the end
     "two, short and long": [3, 2500],
+    "deep": [13001],                 # contractions over rows in 8 parts
+    "deep, one short": [9000, 3, 0],
 }
 
 # counts, N (columns of w), K, activation, bias, residual, shift of x
@@ -124,6 +126,12 @@ PRODUCTS = [
     ("long, one empty", 2 * 256, 128, "geglu", False, False, 0),
     ("two, short and long", 2 * 72, 1032, "swiglu", True, True, 0),
     ("single long", 40, 4096, "gelu", True, False, 0),
+    # Few tiles and a long contraction, in 2, 4 and 8 parts
+    ("many", 264, 1672, "relu", True, True, 0),
+    ("first empty", 2 * 136, 4104, "swiglu", True, True, 0),
+    ("first empty", 520, 3400, "gelu", False, True, 0),
+    ("one expert", 2 * 72, 8200, "geglu", True, False, 0),
+    ("one expert", 328, 6344, "none", True, True, 8),
 ]
 
 
@@ -193,6 +201,10 @@ DGRADS = [
     ("long", 192, 264, "swiglu", "e4m3"),
     ("long, one empty", 320, 136, "none", None),
     ("two, short and long", 1544, 72, "geglu", "e4m3"),
+    ("many", 1672, 264, "gelu", "e4m3"),
+    ("first empty", 4104, 136, "swiglu", "bf16"),
+    ("one expert", 8200, 72, "geglu", "e4m3"),
+    ("one expert", 6344, 328, "none", None),
 ]
 
 
@@ -246,6 +258,8 @@ WGRADS = [
     ("big", 192, 576, True), ("big", 520, 264, False), ("one expert", 384, 512, True),
     ("long", 264, 520, True), ("long, one empty", 136, 264, False), ("long", 512, 256, False),
     ("single long", 136, 264, True), ("single long", 24, 1000, True), ("two, short and long", 264, 72, True),
+    ("deep", 136, 264, True), ("deep", 8, 1000, True), ("deep, one short", 264, 72, True),
+    ("deep, one short", 136, 520, False),
 ]
 
 
