@@ -120,7 +120,7 @@ __device__ __forceinline__ void load32(const mp_bf16_t *p, int n, float (&f)[EPI
 #pragma unroll
         for (int i = 0; i < EPI_COLS; ++i) {
             float t[1] = {0.0f};
-            if (i < n) unpack(ld_stream(p + i), t);
+            if (i < n) unpack(__ldg(p + i), t);   // from L1 but for the first of a sector
             f[i] = t[0];
         }
     }
@@ -272,8 +272,8 @@ __device__ __forceinline__ void ckpt_read32(const uint8_t *codes, const uint8_t 
 }
 
 // ---------------------------------------------------------------------------
-// Epilogues, on 32 columns of one row in fp32.  `W` writes bf16 results: a kernel
-// whose warps hold 32 consecutive rows may do so together (every lane then
+// Epilogues, on 32 columns of one row in fp32.  `W` reads and writes bf16 rows: a
+// kernel whose warps hold 32 consecutive rows may do so together (every lane then
 // calls, `valid` or not, with a row that exists to read from).
 // ---------------------------------------------------------------------------
 
@@ -307,8 +307,15 @@ __device__ __forceinline__ void zero_rest(const ExpertEpi &p, int first, int R, 
     }
 }
 
-// Each thread writes its own row.
+// Each thread reads and writes its own row.
 struct RowWriter {
+    __device__ __forceinline__ void get(const mp_bf16_t *base, int64_t pitch, int64_t row, int64_t c, int n,
+                                        float (&f)[EPI_COLS])
+    {
+        load32(base + row * pitch + c, n, f);
+    }
+    // The same values for all the rows.
+    __device__ __forceinline__ void get_shared(const mp_bf16_t *p, int n, float (&f)[EPI_COLS]) { load32(p, n, f); }
     __device__ __forceinline__ void put(mp_bf16_t *base, int64_t pitch, int, int64_t row, int64_t c,
                                         int n, bool, const float (&f)[EPI_COLS])
     {
@@ -328,21 +335,23 @@ __device__ __forceinline__ void save32(const ExpertEpi &p, W &w, int64_t row, in
                      p.z_exp + (row * parts + part) * ckpt_blocks(p.cols) + c / EPI_COLS, n, z);
 }
 
-__device__ __forceinline__ void read32(const ExpertEpi &p, int64_t row, int part, int parts, int c,
+template <typename W>
+__device__ __forceinline__ void read32(const ExpertEpi &p, W &w, int64_t row, int part, int parts, int c,
                                        int n, float (&z)[EPI_COLS])
 {
-    const int64_t at = (row * parts + part) * p.cols + c;
     if (p.save == MP_SAVE_BF16)
-        load32(static_cast<const mp_bf16_t *>(p.z) + at, n, z);
+        w.get(static_cast<const mp_bf16_t *>(p.z), static_cast<int64_t>(parts) * p.cols, row,
+              static_cast<int64_t>(part) * p.cols + c, n, z);
     else
-        ckpt_read32(static_cast<const uint8_t *>(p.z) + at,
+        ckpt_read32(static_cast<const uint8_t *>(p.z) + (row * parts + part) * p.cols + c,
                     p.z_exp + (row * parts + part) * ckpt_blocks(p.cols) + c / EPI_COLS, n, z);
 }
 
-__device__ __forceinline__ void add_bias32(const mp_bf16_t *b, int n, float (&z)[EPI_COLS])
+template <typename W>
+__device__ __forceinline__ void add_bias32(W &w, const mp_bf16_t *b, int n, float (&z)[EPI_COLS])
 {
     float f[EPI_COLS];
-    load32(b, n, f);
+    w.get_shared(b, n, f);
 #pragma unroll
     for (int i = 0; i < EPI_COLS; ++i) z[i] += f[i];
 }
@@ -365,8 +374,8 @@ __device__ __forceinline__ void epi_fwd(const ExpertEpi &p, W &w, int e, int64_t
     constexpr int parts = GATED ? 2 : 1;
     if (p.bias != nullptr) {
         const mp_bf16_t *b = p.bias + static_cast<int64_t>(e) * parts * p.cols + c;
-        add_bias32(b, n, z);
-        if (GATED) add_bias32(b + p.cols, n, u);
+        add_bias32(w, b, n, z);
+        if (GATED) add_bias32(w, b + p.cols, n, u);
     }
     if (p.save != MP_SAVE_NONE) {
         save32(p, w, row, 0, parts, c, n, valid, z);
@@ -382,7 +391,7 @@ __device__ __forceinline__ void epi_fwd(const ExpertEpi &p, W &w, int e, int64_t
     }
     if (p.residual != nullptr) {
         float f[EPI_COLS];
-        load32(p.residual + row * p.cols + c, n, f);
+        w.get(p.residual, p.cols, row, c, n, f);
 #pragma unroll
         for (int i = 0; i < EPI_COLS; ++i) z[i] += f[i];
     }
@@ -420,8 +429,8 @@ __device__ __forceinline__ void epi_dgrad(const ExpertEpi &p, W &w, int64_t row,
     }
     float z[EPI_COLS], u[EPI_COLS];
     if (act_gated(p.act)) {
-        read32(p, row, 0, 2, c, n, z);
-        read32(p, row, 1, 2, c, n, u);
+        read32(p, w, row, 0, 2, c, n, z);
+        read32(p, w, row, 1, 2, c, n, u);
         if (p.act == MP_ACT_SWIGLU)
             act_grad32<MP_ACT_SILU, true>(g, z, u);
         else
@@ -429,7 +438,7 @@ __device__ __forceinline__ void epi_dgrad(const ExpertEpi &p, W &w, int64_t row,
         w.put(p.out, 2ll * p.cols, TO_OUT, row, c, n, valid, z);
         w.put(p.out, 2ll * p.cols, TO_OUT, row, static_cast<int64_t>(p.cols) + c, n, valid, u);
     } else {
-        read32(p, row, 0, 1, c, n, z);
+        read32(p, w, row, 0, 1, c, n, z);
         switch (p.act) {
         case MP_ACT_SILU: act_grad32<MP_ACT_SILU, false>(g, z, u); break;
         case MP_ACT_GELU: act_grad32<MP_ACT_GELU, false>(g, z, u); break;

@@ -177,7 +177,7 @@ struct WarpWriter {
         __syncwarp();
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<uint4 *>(tile + lane * 64 + ((q ^ ((lane >> 1) & 3)) * 16)) = pack8(f + 8 * q);
+            *piece(lane, q) = pack8(f + 8 * q);
         const int64_t row0 = __shfl_sync(FULL_MASK, row, 0);
         if (rows == 32 && n == EPI_COLS && maps.use[which]) {
             fence_async_smem();
@@ -188,15 +188,77 @@ struct WarpWriter {
         }
         __syncwarp();
         mp_bf16_t *to = base + row0 * pitch + c;
-        if (n == EPI_COLS && maps.use[which]) {
-            for (int r = lane >> 2; r < rows; r += 8)
-                *reinterpret_cast<uint4 *>(to + r * pitch + (lane & 3) * 8) = *reinterpret_cast<const uint4 *>(
-                    tile + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) * 16));
+        if (n % 8 == 0 && maps.use[which]) {
+            if ((lane & 3) * 8 < n)
+#pragma unroll 4
+                for (int r = lane >> 2; r < rows; r += 8)
+                    *reinterpret_cast<uint4 *>(to + r * pitch + (lane & 3) * 8) = *piece(r, lane & 3);
         } else if (lane < n) {
-            for (int r = 0; r < rows; ++r)
-                to[r * pitch + lane] = *reinterpret_cast<const uint16_t *>(
-                    tile + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) * 16) + (lane & 7) * 2);
+#pragma unroll 8
+            for (int r = 0; r < rows; ++r) to[r * pitch + lane] = *element(r, lane);
         }
+    }
+    __device__ __forceinline__ uint4 *piece(int r, int q)
+    {
+        return reinterpret_cast<uint4 *>(tile + r * 64 + ((q ^ ((r >> 1) & 3)) * 16));
+    }
+    __device__ __forceinline__ uint16_t *element(int r, int col)
+    {
+        return reinterpret_cast<uint16_t *>(piece(r, col >> 3)) + (col & 7);
+    }
+    // Rows whose 32-byte sectors a lane cannot read whole are read as they are written,
+    // and turned: 20,000 rows by 64 experts of 1,016 x 1,024 with a residual 87 -> 65 us,
+    // 2,999 rows by 40 experts of 1,009 x 1,000 106 -> 41.
+    __device__ __forceinline__ void get(const mp_bf16_t *base, int64_t pitch, int64_t row, int64_t c, int n,
+                                        float (&f)[EPI_COLS])
+    {
+        const unsigned low = low_bits(base) | ((static_cast<unsigned>(pitch | c) & 15u) * 2);
+        if (n == EPI_COLS && low == 0) {
+            load32(base + row * pitch + c, n, f);
+            return;
+        }
+        if (lane == 0) tma_store_read();   // the tile before this one has left
+        __syncwarp();
+        const mp_bf16_t *from = base + __shfl_sync(FULL_MASK, row, 0) * pitch + c;
+        if (n % 8 == 0 && (low & 15u) == 0) {
+            uint4 v[4] = {};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = (lane >> 2) + 8 * i;
+                if (r < rows && (lane & 3) * 8 < n)
+                    v[i] = ld_stream(reinterpret_cast<const uint4 *>(from + r * pitch) + (lane & 3));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) *piece((lane >> 2) + 8 * i, lane & 3) = v[i];
+        } else {
+            uint16_t v[32] = {};
+#pragma unroll
+            for (int r = 0; r < 32; ++r)
+                if (r < rows && lane < n) v[r] = ld_stream(from + r * pitch + lane);
+#pragma unroll
+            for (int r = 0; r < 32; ++r) *element(r, lane) = v[r];
+        }
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float t[8];
+            unpack(*piece(lane, q), t);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[8 * q + i] = t[i];
+        }
+        __syncwarp();
+    }
+    // The same values for all the rows.
+    __device__ __forceinline__ void get_shared(const mp_bf16_t *p, int n, float (&f)[EPI_COLS])
+    {
+        if (n == EPI_COLS && (low_bits(p) & 15u) == 0) {
+            load32(p, n, f);
+            return;
+        }
+        float t[1] = {0.0f};
+        if (lane < n) unpack(__ldg(p + lane), t);
+#pragma unroll
+        for (int i = 0; i < EPI_COLS; ++i) f[i] = __shfl_sync(FULL_MASK, t[0], i);
     }
 };
 
