@@ -251,8 +251,15 @@ struct WarpWriter {
     // The same values for all the rows.
     __device__ __forceinline__ void get_shared(const mp_bf16_t *p, int n, float (&f)[EPI_COLS])
     {
-        if (n == EPI_COLS && (low_bits(p) & 15u) == 0) {
-            load32(p, n, f);
+        if (n == EPI_COLS && (low_bits(p) & 15u) == 0) {   // from L1 but for the first of four warps
+            const uint4 *q = reinterpret_cast<const uint4 *>(p);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float t[8];
+                unpack(__ldg(q + j), t);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[8 * j + i] = t[i];
+            }
             return;
         }
         float t[1] = {0.0f};
