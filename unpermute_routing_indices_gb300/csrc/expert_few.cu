@@ -312,15 +312,14 @@ mp_status_t launch_few(const ExpertCall &c, const CUtensorMap &w, const CUtensor
 
 }  // namespace
 
-// Up to 8 rows an expert, 16 when gated (the tile then has twice the weights to a
-// row of x), and up to 64 rows in all, where k_expert_tc has too few tiles.  us
-// here / there: 64 experts of 2,048 (gated, depth 2,048) 64 rows 52 / 63, 1,024 rows 87 / 89,
-// 2,048 rows 94 / 90; depth 1,024, not gated, 64 rows 34.4 / 35.5, 512 rows 48.7 / 48.2, 1,024
-// rows 52 / 49; one expert of 2,048 x 4,096, 16 rows 8.3 / 19.0, 64 rows 13 / 19, 128 rows
-// 19.7 / 19.4.
+// Up to 2 rows an expert, 4 when gated (the tile then has twice the weights to a
+// row of x), and up to 64 rows in all.  us here / by k_expert_tc: 32 experts of 1,024 x 512,
+// 64 rows 9.1 / 10.6, 128 rows 9.5 / 9.0; gated 128 rows 9.3 / 9.0, 528 x 2,048 14.5 / 16.2, 256
+// rows 11.5 / 9.0; 128 experts of 4,096 x 2,048, 8 rows 26 / 36; 4 of 1,024 x 1,024, 16 rows 6.0 /
+// 9.0, 64 rows 7.7 / 8.9; one of 512 x 512, 16 rows 6.2 / 6.1, 64 rows 7.8 / 6.2.
 bool expert_few_takes(const ExpertCall &c)
 {
-    return expert_tc_takes<FWD>(c) && (c.R <= 64 || c.R <= (act_gated(c.epi.act) ? 16 : 8) * static_cast<int64_t>(c.E));
+    return expert_tc_takes<FWD>(c) && (c.R <= 64 || c.R <= (act_gated(c.epi.act) ? 4 : 2) * static_cast<int64_t>(c.E));
 }
 
 mp_status_t expert_few(const ExpertCall &c)

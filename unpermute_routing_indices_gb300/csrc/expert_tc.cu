@@ -1,8 +1,8 @@
 // The experts' products on the tensor cores.
 //
 // One persistent kernel for the three products, a CTA per SM.  A tile is 128
-// rows by 256 columns (128 gate and 128 other columns when gated) of one expert,
-// or 256 rows for a pair of CTAs, which read half of B each:
+// rows by up to 256 columns (half of them the gate's when gated) of one expert,
+// or 256 rows and columns for a pair of CTAs, which read half of B each:
 //   FWD    rows of x by rows of w[e], contraction along both rows
 //   DGRAD  rows of g along, w[e] across (its columns are the result's)
 //   WGRAD  g and x both across: the contraction is over the expert's rows
@@ -15,8 +15,8 @@
 // computed and dropped (FWD, DGRAD).  In WGRAD, where they would enter the sums,
 // the last slice's rows up to the next 16 are overwritten with zeros in shared
 // memory, whatever they held.
-// Where the tiles are fewer than the SMs (one expert, narrow results) the contraction
-// of each is split over a cluster of up to 8 CTAs, whose parts are added in rank order
+// Where the tiles are few, they are narrower (choose_cut), and the contraction of
+// each may be split over a cluster of up to 8 CTAs, whose parts are added in rank order
 // through distributed shared memory, so a result does not depend on timing.
 // What bounds it: for experts of many rows the tensor cores (131,072 x 4,096 by 128
 // experts of 2,048 columns in 1,211 us, 1.82 PFLOP/s, 0.92 of cuBLAS's measured
@@ -394,7 +394,7 @@ __device__ __forceinline__ void join32(uint32_t addr, int split, float *turn, in
 template <int MODE, bool GATED, int CG>
 __global__ void __launch_bounds__(tc_threads(MODE), 1)
     k_expert_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                const __grid_constant__ StoreMaps stores, const ExpertCall c, int split)
+                const __grid_constant__ StoreMaps stores, const ExpertCall c, int split, int width)
 {
     typedef Ring<CG> L;
     constexpr int STAGES = L::STAGES;
@@ -440,18 +440,20 @@ __global__ void __launch_bounds__(tc_threads(MODE), 1)
     __syncthreads();
 
     const uint32_t tmem = s.tmem;
-    constexpr int tile_cols = GATED ? BN / 2 : BN;
+    const int wide = CG == 1 ? width : BN;   // columns of B's slice and of the accumulator
+    const int tile_cols = GATED ? wide / 2 : wide;
     const int nt = (c.epi.cols + tile_cols - 1) / tile_cols;
     const int total = (MODE == WGRAD ? c.E * ((c.N + CG * BM - 1) / (CG * BM)) : s.tiles[c.E]) * nt;
     const int first = blockIdx.x / (CG * split), step = gridDim.x / (CG * split);
-    constexpr uint32_t idesc = mma_desc(CG * BM, BN, MODE == WGRAD, MODE != FWD);
+    const uint32_t idesc = mma_desc(CG * BM, wide, MODE == WGRAD, MODE != FWD);
+    const uint32_t slice_bytes = A_BYTES + wide / CG * BK * 2;
 
     if (warp == 0) {
         if (lane == 0) {
             uint32_t n = 0;   // slices loaded so far
             for (int t = first; t < total && !*gave_up; t += step) {
                 const Tile w = tile_at<MODE, CG>(c, s.start, s.tiles, t, nt, tile_cols, rank, part, split);
-                const int off = rank * (BN / 2);   // in B's 256 rows or columns
+                const int off = rank * (wide / 2);   // in B's rows or columns
                 for (int k = w.k0; k < w.k1; k += BK, ++n) {
                     const int i = n % STAGES;
                     if (!mbar_wait(smem_u32(&s.empty[i]), ((n / STAGES) & 1) ^ 1, gave_up)) break;
@@ -460,27 +462,27 @@ __global__ void __launch_bounds__(tc_threads(MODE), 1)
                     // In a pair both CTAs' copies arrive at CTA 0's barrier, but those
                     // of a ragged slice, which CTA 1 has to see itself.
                     if (CG == 1 || (MODE == WGRAD && k + BK > w.depth))
-                        mbar_expect(bar, L::STAGE);
+                        mbar_expect(bar, slice_bytes);
                     else if (rank == 0)
-                        mbar_expect(bar, 2 * L::STAGE);
+                        mbar_expect(bar, 2 * slice_bytes);
                     else
                         bar = at_rank(bar, 0);
                     if (MODE == WGRAD) {
                         for (int j = 0; j < BM / 64; ++j)
                             tma_load<CG>(a + j * BOX_BYTES, &map_a, bar, w.m0 + 64 * j, w.row0 + k);
-                        for (int j = 0; j < BN / CG / 64; ++j)
+                        for (int j = 0; j < wide / CG / 64; ++j)
                             tma_load<CG>(b + j * BOX_BYTES, &map_b, bar, w.c0 + off + 64 * j, w.row0 + k);
                     } else {
                         // A part without rows reads zeros from past the end of x: the
                         // products are made all the same, but on less power and no bytes.
                         tma_load<CG>(a, &map_a, bar, k, w.m0 < w.m1 ? w.m0 : c.R);
                         if (MODE == FWD) {
-                            // 128 rows of w at a time: the gate's and the others', or neighbours.
+                            // Half the rows of w at a time: the gate's and the others', or neighbours.
                             for (int j = rank; j < rank + 2 / CG; ++j)
-                                tma_load<CG>(b + (j - rank) * A_BYTES, &map_b, bar, k,
-                                             w.c0 + j * (GATED ? c.epi.cols : BN / 2), w.e);
+                                tma_load<CG>(b + (j - rank) * (wide / 2) * BK * 2, &map_b, bar, k,
+                                             w.c0 + j * (GATED ? c.epi.cols : wide / 2), w.e);
                         } else {
-                            for (int j = 0; j < BN / CG / 64; ++j)
+                            for (int j = 0; j < wide / CG / 64; ++j)
                                 tma_load<CG>(b + j * BOX_BYTES, &map_b, bar, w.c0 + off + 64 * j, k, w.e);
                         }
                     }
@@ -600,7 +602,7 @@ __global__ void __launch_bounds__(tc_threads(MODE), 1)
                 float z[EPI_COLS], u[EPI_COLS];
                 if (any) {
                     tmem_load32(d + j, z);
-                    if (GATED) tmem_load32(d + BN / 2 + j, u);
+                    if (GATED) tmem_load32(d + wide / 2 + j, u);
                     tmem_load_wait();
                 } else {
 #pragma unroll
@@ -710,27 +712,63 @@ template <typename K> int cluster_count(K kernel, int threads, int size)
     return n;
 }
 
+// How a call is cut: columns of a tile (both parts of a gated one), CTAs a tile's
+// contraction is split over.
+struct Cut {
+    int wide, split;
+};
+
+template <int MODE> int64_t tile_rows(const ExpertCall &c, int high)
+{
+    return MODE == WGRAD ? static_cast<int64_t>(c.E) * ((c.N + high - 1) / high) : c.R / high + (c.R < c.E ? c.R : c.E);
+}
+
+// Single CTAs: the cut that is done first by a count of cycles, fitted to 27 calls
+// measured with all cuts (on 36 others it took the best cut or one at most 9% slower).  A slice takes its bytes at 64 a cycle, but 560 cycles at
+// least with four in flight; a tile's epilogue overlaps the next tile's products; a
+// join grows with its parts.  An expert has half a tile more than its rows fill, and
+// one at least.  us with 256 columns unsplit, and as cut: 300 rows by 3 experts of
+// 1,000 x 1,000 14.4, 9.1 (64); x 4,000 23.3, 15.8 (192 in 4 parts); 2,999 rows by
+// 40 of 1,009 x 1,000 26.9, 23.9 (192); 500 rows by one of 512 x 8,192 42, 16.7 (64 in 4);
+// weight gradients of 2,000 rows, 512 x 1,024 16.5, 12.3 (128 in 4), of 21,063 rows,
+// 112 x 1,624 164, 27.7 (128 in 8).
+template <int MODE, bool GATED> Cut choose_cut(const ExpertCall &c)
+{
+    const int64_t depth = MODE == FWD ? c.K : MODE == DGRAD ? c.N : c.R / c.E, slices = (depth + BK - 1) / BK;
+    const int64_t some = c.R < c.E ? c.R : c.E, filled = c.R / BM + some / 2;
+    const int64_t high = MODE == WGRAD ? tile_rows<MODE>(c, BM) : filled > some ? filled : some;
+    const int sms = sm_count();
+    Cut best = {BN, 1};
+    int64_t least = INT64_MAX;
+    for (int wide = BN; wide >= (GATED ? 128 : 64); wide -= GATED ? 128 : 64) {
+        const int cols = GATED ? wide / 2 : wide;
+        const int64_t nt = (c.epi.cols + cols - 1) / cols, tiles = nt * tile_rows<MODE>(c, BM);
+        for (int split = 1; split <= 8; split *= 2) {
+            if (split > 1 && (tiles * split > sms ||
+                              tiles > cluster_count(k_expert_tc<MODE, GATED, 1>, tc_threads(MODE), split)))
+                break;
+            const int64_t waves = split > 1 ? 1 : (nt * high + sms - 1) / sms;
+            const int64_t slice = 256 + 2 * wide > 560 ? 256 + 2 * wide : 560, epilogue = 1500 + 14 * wide;
+            const int64_t part = (slices + split - 1) / split * slice;
+            const int64_t cycles = waves * (part > epilogue ? part : epilogue) + epilogue +
+                                   (split > 1 ? 3500 + 1000 * split : 0);
+            if (cycles < least) {
+                least = cycles;
+                best = Cut{wide, split};
+            }
+        }
+    }
+    return best;
+}
+
 template <int MODE, bool GATED, int CG>
-mp_status_t launch_tc(const ExpertCall &c, const CUtensorMap &a, const CUtensorMap &b, const StoreMaps &m)
+mp_status_t launch_tc(const ExpertCall &c, const CUtensorMap &a, const CUtensorMap &b, const StoreMaps &m, Cut cut)
 {
     static std::atomic<uint64_t> allowed{0};
     if (!allow_smem(k_expert_tc<MODE, GATED, CG>, allowed, TC_SMEM)) return MP_ERR_CUDA;
-    const int64_t nt = (c.epi.cols + (GATED ? BN / 2 : BN) - 1) / (GATED ? BN / 2 : BN);
-    const int64_t mt = MODE == WGRAD ? static_cast<int64_t>(c.E) * ((c.N + CG * BM - 1) / (CG * BM))
-                                     : c.R / (CG * BM) + (c.R < c.E ? c.R : c.E);
-    if (nt * mt > INT32_MAX / 2) return MP_ERR_UNSUPPORTED;   // tiles are counted in 32 bits
-    // Too few tiles for the SMs: the contraction of each is split over a cluster,
-    // where 12 slices a CTA are left at least and the clusters fit the device at
-    // once.  us with 1, 2, 4, 8 parts: weight gradients of one expert of 21,063 rows,
-    // 112 x 1,624 (330 slices) 164, 90, 53, 36; 500 rows by 512 x 8,192 (128 slices) 42, 28,
-    // 22, 21; 300 rows by 3 experts of 1,000 x 4,000 (63) 25, 19, 18, 18; x 1,000 (16) 14.5, 14.0,
-    // 15.3, 15.3; 100 rows by 2 experts of 2,048 x 512 (8) 8.4, 10.1, 13.2, 13.2.
-    int split = 1;
-    const int64_t tiles = nt * mt, depth = MODE == FWD ? c.K : MODE == DGRAD ? c.N : c.R / c.E;
-    if (CG == 1)
-        while (split < 8 && depth / BK >= 24 * split && tiles * split * 2 <= sm_count() &&
-               tiles <= cluster_count(k_expert_tc<MODE, GATED, CG>, tc_threads(MODE), 2 * split))
-            split *= 2;
+    const int cols = GATED ? cut.wide / 2 : cut.wide, split = cut.split;
+    const int64_t tiles = (c.epi.cols + cols - 1) / cols * tile_rows<MODE>(c, CG * BM);
+    if (tiles > INT32_MAX / 2) return MP_ERR_UNSUPPORTED;   // counted in 32 bits
     const int64_t room = CG == 1 ? sm_count() : cluster_count(k_expert_tc<MODE, GATED, CG>, tc_threads(MODE), 2);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = static_cast<unsigned>(split > 1 ? split * tiles : CG * (tiles < room ? tiles : room));
@@ -745,7 +783,7 @@ mp_status_t launch_tc(const ExpertCall &c, const CUtensorMap &a, const CUtensorM
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CG * split == 1 ? 1 : 2;
-    (void)cudaLaunchKernelEx(&cfg, k_expert_tc<MODE, GATED, CG>, a, b, m, c, split);
+    (void)cudaLaunchKernelEx(&cfg, k_expert_tc<MODE, GATED, CG>, a, b, m, c, split, cut.wide);
     return check_launch();
 }
 
@@ -759,7 +797,7 @@ mp_status_t launch_tc(const ExpertCall &c, const CUtensorMap &a, const CUtensorM
 // 512 rows 216 -> 211 / 114 -> 108, 1,024 rows 391 -> 373 / 204 -> 188.  Weight
 // gradients: 128 rows an expert (256 experts) 223 -> 372, 384 rows 219.6 -> 220.1,
 // 512 rows 263 -> 253.
-// With fewer tiles than SMs a split of each tile does more (launch_tc).
+// With fewer tiles than SMs another cut does more (choose_cut).
 template <int MODE> bool in_pairs(const ExpertCall &c)
 {
     const int64_t cols = act_gated(c.epi.act) && MODE == FWD ? 2ll * c.epi.cols : c.epi.cols;
@@ -767,21 +805,18 @@ template <int MODE> bool in_pairs(const ExpertCall &c)
            (cols + BN - 1) / BN * (MODE == WGRAD ? static_cast<int64_t>(c.E) * ((c.N + BM - 1) / BM) : c.R / BM) >= sm_count();
 }
 
-}  // namespace
-
-template <int MODE> bool expert_tc_takes(const ExpertCall &c)
+template <int MODE, bool GATED> mp_status_t cut_and_launch(const ExpertCall &c)
 {
-    return c.R > 0 && c.K % 8 == 0 && (MODE == FWD || c.N % 8 == 0) && aligned16(c.a) && aligned16(c.b);
-}
-
-template <int MODE> mp_status_t expert_tc(const ExpertCall &c)
-{
+    const bool pairs = in_pairs<MODE>(c);
+    static std::atomic<uint64_t> allowed{0};
+    if (!allow_smem(k_expert_tc<MODE, GATED, 1>, allowed, TC_SMEM)) return MP_ERR_CUDA;
+    const Cut cut = pairs ? Cut{BN, 1} : choose_cut<MODE, GATED>(c);
     CUtensorMap a, b;
     const uint64_t R = c.R, N = c.N, K = c.K, E = c.E;
     const uint64_t da[2] = {MODE == FWD ? K : N, R};
     const uint32_t box_a[2] = {64, MODE == WGRAD ? 64u : static_cast<uint32_t>(BM)};
     const uint64_t db[3] = {K, MODE == WGRAD ? R : N, E};
-    const uint32_t box_b[3] = {64, MODE == FWD ? BN / 2u : 64u, 1};
+    const uint32_t box_b[3] = {64, MODE == FWD ? cut.wide / 2u : 64u, 1};
     if (!make_map(&a, c.a, 2, da, box_a) || !make_map(&b, c.b, MODE == WGRAD ? 2 : 3, db, box_b)) {
         set_last_cuda_error(cudaErrorInvalidValue);
         return MP_ERR_CUDA;
@@ -797,10 +832,20 @@ template <int MODE> mp_status_t expert_tc(const ExpertCall &c)
         set_last_cuda_error(cudaErrorInvalidValue);
         return MP_ERR_CUDA;
     }
-    if (MODE == FWD && act_gated(c.epi.act))
-        return in_pairs<MODE>(c) ? launch_tc<MODE, MODE == FWD, 2>(c, a, b, m)
-                                 : launch_tc<MODE, MODE == FWD, 1>(c, a, b, m);
-    return in_pairs<MODE>(c) ? launch_tc<MODE, false, 2>(c, a, b, m) : launch_tc<MODE, false, 1>(c, a, b, m);
+    return pairs ? launch_tc<MODE, GATED, 2>(c, a, b, m, cut) : launch_tc<MODE, GATED, 1>(c, a, b, m, cut);
+}
+
+}  // namespace
+
+template <int MODE> bool expert_tc_takes(const ExpertCall &c)
+{
+    return c.R > 0 && c.K % 8 == 0 && (MODE == FWD || c.N % 8 == 0) && aligned16(c.a) && aligned16(c.b);
+}
+
+template <int MODE> mp_status_t expert_tc(const ExpertCall &c)
+{
+    if (MODE == FWD && act_gated(c.epi.act)) return cut_and_launch<MODE, MODE == FWD>(c);
+    return cut_and_launch<MODE, false>(c);
 }
 
 template bool expert_tc_takes<FWD>(const ExpertCall &);
