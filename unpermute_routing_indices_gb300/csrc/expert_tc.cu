@@ -391,7 +391,9 @@ __device__ __forceinline__ void join32(uint32_t addr, int split, float *turn, in
     for (int i = 0; i < 32; ++i) z[i] = turn[lane * 33 + i];
 }
 
-template <int MODE, bool GATED, int CG>
+// ANY: tiles of `width` columns; otherwise of BN, which the weight gradients of many
+// experts would feel (64 experts of 384 rows, 2,048 x 2,048: 191 us, as a variable 195).
+template <int MODE, bool GATED, int CG, bool ANY>
 __global__ void __launch_bounds__(tc_threads(MODE), 1)
     k_expert_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                 const __grid_constant__ StoreMaps stores, const ExpertCall c, int split, int width)
@@ -440,7 +442,7 @@ __global__ void __launch_bounds__(tc_threads(MODE), 1)
     __syncthreads();
 
     const uint32_t tmem = s.tmem;
-    const int wide = CG == 1 ? width : BN;   // columns of B's slice and of the accumulator
+    const int wide = ANY ? width : BN;   // columns of B's slice and of the accumulator
     const int tile_cols = GATED ? wide / 2 : wide;
     const int nt = (c.epi.cols + tile_cols - 1) / tile_cols;
     const int total = (MODE == WGRAD ? c.E * ((c.N + CG * BM - 1) / (CG * BM)) : s.tiles[c.E]) * nt;
@@ -745,7 +747,7 @@ template <int MODE, bool GATED> Cut choose_cut(const ExpertCall &c)
         const int64_t nt = (c.epi.cols + cols - 1) / cols, tiles = nt * tile_rows<MODE>(c, BM);
         for (int split = 1; split <= 8; split *= 2) {
             if (split > 1 && (tiles * split > sms ||
-                              tiles > cluster_count(k_expert_tc<MODE, GATED, 1>, tc_threads(MODE), split)))
+                              tiles > cluster_count(k_expert_tc<MODE, GATED, 1, true>, tc_threads(MODE), split)))
                 break;
             const int64_t waves = split > 1 ? 1 : (nt * high + sms - 1) / sms;
             const int64_t slice = 256 + 2 * wide > 560 ? 256 + 2 * wide : 560, epilogue = 1500 + 14 * wide;
@@ -761,15 +763,15 @@ template <int MODE, bool GATED> Cut choose_cut(const ExpertCall &c)
     return best;
 }
 
-template <int MODE, bool GATED, int CG>
+template <int MODE, bool GATED, int CG, bool ANY>
 mp_status_t launch_tc(const ExpertCall &c, const CUtensorMap &a, const CUtensorMap &b, const StoreMaps &m, Cut cut)
 {
     static std::atomic<uint64_t> allowed{0};
-    if (!allow_smem(k_expert_tc<MODE, GATED, CG>, allowed, TC_SMEM)) return MP_ERR_CUDA;
+    if (!allow_smem(k_expert_tc<MODE, GATED, CG, ANY>, allowed, TC_SMEM)) return MP_ERR_CUDA;
     const int cols = GATED ? cut.wide / 2 : cut.wide, split = cut.split;
     const int64_t tiles = (c.epi.cols + cols - 1) / cols * tile_rows<MODE>(c, CG * BM);
     if (tiles > INT32_MAX / 2) return MP_ERR_UNSUPPORTED;   // counted in 32 bits
-    const int64_t room = CG == 1 ? sm_count() : cluster_count(k_expert_tc<MODE, GATED, CG>, tc_threads(MODE), 2);
+    const int64_t room = CG == 1 ? sm_count() : cluster_count(k_expert_tc<MODE, GATED, CG, ANY>, tc_threads(MODE), 2);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = static_cast<unsigned>(split > 1 ? split * tiles : CG * (tiles < room ? tiles : room));
     cfg.blockDim = tc_threads(MODE);
@@ -783,7 +785,7 @@ mp_status_t launch_tc(const ExpertCall &c, const CUtensorMap &a, const CUtensorM
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CG * split == 1 ? 1 : 2;
-    (void)cudaLaunchKernelEx(&cfg, k_expert_tc<MODE, GATED, CG>, a, b, m, c, split, cut.wide);
+    (void)cudaLaunchKernelEx(&cfg, k_expert_tc<MODE, GATED, CG, ANY>, a, b, m, c, split, cut.wide);
     return check_launch();
 }
 
@@ -809,7 +811,7 @@ template <int MODE, bool GATED> mp_status_t cut_and_launch(const ExpertCall &c)
 {
     const bool pairs = in_pairs<MODE>(c);
     static std::atomic<uint64_t> allowed{0};
-    if (!allow_smem(k_expert_tc<MODE, GATED, 1>, allowed, TC_SMEM)) return MP_ERR_CUDA;
+    if (!allow_smem(k_expert_tc<MODE, GATED, 1, true>, allowed, TC_SMEM)) return MP_ERR_CUDA;
     const Cut cut = pairs ? Cut{BN, 1} : choose_cut<MODE, GATED>(c);
     CUtensorMap a, b;
     const uint64_t R = c.R, N = c.N, K = c.K, E = c.E;
@@ -832,7 +834,9 @@ template <int MODE, bool GATED> mp_status_t cut_and_launch(const ExpertCall &c)
         set_last_cuda_error(cudaErrorInvalidValue);
         return MP_ERR_CUDA;
     }
-    return pairs ? launch_tc<MODE, GATED, 2>(c, a, b, m, cut) : launch_tc<MODE, GATED, 1>(c, a, b, m, cut);
+    if (pairs) return launch_tc<MODE, GATED, 2, false>(c, a, b, m, cut);
+    if (MODE == WGRAD && cut.wide == BN) return launch_tc<MODE, GATED, 1, MODE != WGRAD>(c, a, b, m, cut);
+    return launch_tc<MODE, GATED, 1, true>(c, a, b, m, cut);
 }
 
 }  // namespace
