@@ -132,6 +132,12 @@ PRODUCTS = [
     ("first empty", 520, 3400, "gelu", False, True, 0),
     ("one expert", 2 * 72, 8200, "geglu", True, False, 0),
     ("one expert", 328, 6344, "none", True, True, 8),
+    # Widths and bases that are no multiples of 16 bytes, whole and in parts
+    ("big", 2 * 129, 1031, "swiglu", True, True, 0),
+    ("big", 514, 130, "none", True, True, 1),
+    ("first empty", 261, 2050, "gelu", True, False, 0),
+    ("one expert", 2 * 70, 6001, "geglu", False, True, 0),
+    ("one expert", 200, 4096, "silu", True, False, 3),
 ]
 
 
@@ -205,6 +211,9 @@ DGRADS = [
     ("first empty", 4104, 136, "swiglu", "bf16"),
     ("one expert", 8200, 72, "geglu", "e4m3"),
     ("one expert", 6344, 328, "none", None),
+    ("big", 515, 203, "swiglu", "bf16"),
+    ("many", 1034, 131, "gelu", "e4m3"),
+    ("one expert", 4099, 130, "geglu", "e4m3"),
 ]
 
 
@@ -260,6 +269,7 @@ WGRADS = [
     ("single long", 136, 264, True), ("single long", 24, 1000, True), ("two, short and long", 264, 72, True),
     ("deep", 136, 264, True), ("deep", 8, 1000, True), ("deep, one short", 264, 72, True),
     ("deep, one short", 136, 520, False),
+    ("big", 203, 515, True), ("deep", 33, 130, True), ("deep, one short", 130, 259, True),
 ]
 
 

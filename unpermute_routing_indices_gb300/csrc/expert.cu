@@ -12,8 +12,8 @@ constexpr int BIAS_THREADS = 256, BIAS_WARPS = BIAS_THREADS / 32;
 // g_bias[e,n] = sum over the expert's rows of g[row,n], in fp32.  A CTA owns 32 V
 // columns of one expert, V = 8 (16-byte loads) where rows are aligned to it; each
 // warp takes every eighth row, four of them in flight, and the eight sums are
-// added in order.  The tensor-core form of the weight gradient makes these sums
-// itself; this serves the other form, and biases whose weights want no gradient.
+// added in order.  The weight gradient makes these sums itself where TMA reads its
+// operands; this serves the others, and biases whose weights want no gradient.
 template <int V>
 __global__ void __launch_bounds__(BIAS_THREADS)
     k_expert_bias(const mp_bf16_t *__restrict__ g, const int32_t *__restrict__ offsets, int R,
@@ -94,24 +94,19 @@ mp_status_t bias_grad(const mp_bf16_t *g, const ExpertCall &c, mp_bf16_t *out, f
     return check_launch();
 }
 
-template <int MODE> mp_status_t product(const ExpertCall &c)
-{
-    return expert_tc_takes<MODE>(c) ? expert_tc<MODE>(c) : expert_simt<MODE>(c);
-}
-
 // g_w as c.epi has it, and g_bias (NULL: not wanted): within the product, or by a
-// kernel of its own after the slower form.
+// kernel of its own where the load warps read the operands.
 mp_status_t weight_grad(ExpertCall &c, void *g_bias, bool f32)
 {
     mp_bf16_t *b = f32 ? nullptr : static_cast<mp_bf16_t *>(g_bias);
     float *b32 = f32 ? static_cast<float *>(g_bias) : nullptr;
-    if (expert_tc_takes<WGRAD>(c)) {
+    const bool within = expert_by_tma(c, WGRAD);
+    if (within) {
         c.epi.g_bias = b;
         c.epi.g_bias_f32 = b32;
-        return expert_tc<WGRAD>(c);
     }
-    const mp_status_t s = expert_simt<WGRAD>(c);
-    return s != MP_OK || g_bias == nullptr ? s : bias_grad(c.a, c, b, b32);
+    const mp_status_t s = expert_tc<WGRAD>(c);
+    return s != MP_OK || within || g_bias == nullptr ? s : bias_grad(c.a, c, b, b32);
 }
 
 bool act_ok(int32_t act) { return act >= MP_ACT_NONE && act <= MP_ACT_SWIGLU; }
@@ -148,7 +143,7 @@ mp_status_t gemm(const mp_bf16_t *x, const mp_bf16_t *w, const int32_t *offsets,
     c.status = dev_status;
     c.stream = as_stream(stream);
     if (expert_few_takes(c)) return expert_few(c);
-    return product<FWD>(c);
+    return expert_tc<FWD>(c);
 }
 
 mp_status_t dgrad(const mp_bf16_t *g, const mp_bf16_t *w, const int32_t *offsets, int64_t R, int32_t E,
@@ -174,7 +169,7 @@ mp_status_t dgrad(const mp_bf16_t *g, const mp_bf16_t *w, const int32_t *offsets
     c.epi.zero_rest = zero_rest;
     c.status = dev_status;
     c.stream = as_stream(stream);
-    return product<DGRAD>(c);
+    return expert_tc<DGRAD>(c);
 }
 
 }  // namespace

@@ -84,8 +84,7 @@ template <int INNER> __device__ __forceinline__ float act_value(float z)
 }
 
 // ---------------------------------------------------------------------------
-// 32 consecutive bf16 values of a row: 32-byte accesses where the address
-// allows, else 16-byte ones, else single elements.  `n` of the 32 exist.
+// 32 consecutive bf16 values of a row, on a 32-byte boundary.
 // ---------------------------------------------------------------------------
 
 __device__ __forceinline__ void unpack16(const u32x8 &v, float *f)
@@ -110,52 +109,12 @@ __device__ __forceinline__ unsigned low_bits(const void *p)
     return static_cast<unsigned>(reinterpret_cast<uintptr_t>(p)) & 31u;
 }
 
-__device__ __forceinline__ void load32(const mp_bf16_t *p, int n, float (&f)[EPI_COLS])
+__device__ __forceinline__ void load32(const mp_bf16_t *p, float (&f)[EPI_COLS])
 {
-    const unsigned low = low_bits(p);
-    if (n >= EPI_COLS && low == 0) {
-        const u32x8 *q = reinterpret_cast<const u32x8 *>(p);
-        const u32x8 v0 = ld_stream(q), v1 = ld_stream(q + 1);
-        unpack16(v0, f);
-        unpack16(v1, f + 16);
-    } else if (n >= EPI_COLS && (low & 15u) == 0) {
-        const uint4 *q = reinterpret_cast<const uint4 *>(p);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float t[8];
-            unpack(ld_stream(q + j), t);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[8 * j + i] = t[i];
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < EPI_COLS; ++i) {
-            float t[1] = {0.0f};
-            if (i < n) unpack(__ldg(p + i), t);   // from L1 but for the first of a sector
-            f[i] = t[0];
-        }
-    }
-}
-
-__device__ __forceinline__ void store32(mp_bf16_t *p, int n, const float (&f)[EPI_COLS])
-{
-    const unsigned low = low_bits(p);
-    if (n >= EPI_COLS && low == 0) {
-        u32x8 *q = reinterpret_cast<u32x8 *>(p);
-        st_row(q, u32x8{pack8(f), pack8(f + 8)});
-        st_row(q + 1, u32x8{pack8(f + 16), pack8(f + 24)});
-    } else if (n >= EPI_COLS && (low & 15u) == 0) {
-        uint4 *q = reinterpret_cast<uint4 *>(p);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) q[j] = pack8(f + 8 * j);
-    } else {
-#pragma unroll
-        for (int i = 0; i < EPI_COLS; ++i)
-            if (i < n) {
-                const float t[1] = {f[i]};
-                p[i] = pack(t);
-            }
-    }
+    const u32x8 *q = reinterpret_cast<const u32x8 *>(p);
+    const u32x8 v0 = ld_stream(q), v1 = ld_stream(q + 1);
+    unpack16(v0, f);
+    unpack16(v1, f + 16);
 }
 
 // fp32 weight gradients, added to what is there if `add`.
@@ -283,9 +242,9 @@ __device__ __forceinline__ void ckpt_read32(const uint8_t *codes, const uint8_t 
 }
 
 // ---------------------------------------------------------------------------
-// Epilogues, on 32 columns of one row in fp32.  `W` reads and writes bf16 rows: a
-// kernel whose warps hold 32 consecutive rows may do so together (every lane then
-// calls, `valid` or not, with a row that exists to read from).
+// Epilogues, on 32 columns of one row in fp32.  `W` reads and writes the bf16 rows of
+// a warp, 32 consecutive ones, together: every lane calls, `valid` or not, with a
+// row that exists to read from.
 // ---------------------------------------------------------------------------
 
 enum { TO_OUT = 0, TO_SECOND = 1 };   // the maps of a writer: out; z (FWD) or h (DGRAD)
@@ -317,22 +276,6 @@ __device__ __forceinline__ void zero_rest(const ExpertEpi &p, int first, int R, 
         for (; i < count; i += n) to[i] = 0;
     }
 }
-
-// Each thread reads and writes its own row.
-struct RowWriter {
-    __device__ __forceinline__ void get(const mp_bf16_t *base, int64_t pitch, int64_t row, int64_t c, int n,
-                                        float (&f)[EPI_COLS])
-    {
-        load32(base + row * pitch + c, n, f);
-    }
-    // The same values for all the rows.
-    __device__ __forceinline__ void get_shared(const mp_bf16_t *p, int n, float (&f)[EPI_COLS]) { load32(p, n, f); }
-    __device__ __forceinline__ void put(mp_bf16_t *base, int64_t pitch, int, int64_t row, int64_t c,
-                                        int n, bool, const float (&f)[EPI_COLS])
-    {
-        store32(base + row * pitch + c, n, f);
-    }
-};
 
 template <typename W>
 __device__ __forceinline__ void save32(const ExpertEpi &p, W &w, int64_t row, int part, int parts,
@@ -543,8 +486,7 @@ struct ExpertCall {
     cudaStream_t stream;
 };
 
-template <int MODE> mp_status_t expert_simt(const ExpertCall &c);   // any width, any alignment
-template <int MODE> bool expert_tc_takes(const ExpertCall &c);      // TMA's rules hold
+bool expert_by_tma(const ExpertCall &c, int mode);                   // TMA's rules hold
 template <int MODE> mp_status_t expert_tc(const ExpertCall &c);
 bool expert_few_takes(const ExpertCall &c);                          // FWD, few rows an expert
 mp_status_t expert_few(const ExpertCall &c);

@@ -319,7 +319,7 @@ mp_status_t launch_few(const ExpertCall &c, const CUtensorMap &w, const CUtensor
 // 9.0, 64 rows 7.7 / 8.9; one of 512 x 512, 16 rows 6.2 / 6.1, 64 rows 7.8 / 6.2.
 bool expert_few_takes(const ExpertCall &c)
 {
-    return expert_tc_takes<FWD>(c) && (c.R <= 64 || c.R <= (act_gated(c.epi.act) ? 4 : 2) * static_cast<int64_t>(c.E));
+    return expert_by_tma(c, FWD) && (c.R <= 64 || c.R <= (act_gated(c.epi.act) ? 4 : 2) * static_cast<int64_t>(c.E));
 }
 
 mp_status_t expert_few(const ExpertCall &c)

@@ -15,6 +15,10 @@
 // computed and dropped (FWD, DGRAD).  In WGRAD, where they would enter the sums,
 // the last slice's rows up to the next 16 are overwritten with zeros in shared
 // memory, whatever they held.
+// Operands that TMA cannot address (rows that are no multiple of 16 bytes, or begin
+// off them) are read by four more warps, word by word, into the same layout: 24,576
+// rows by 64 experts of 2,046 x 2,045 in 1,033 us (200 TFLOP/s; an element a lane with
+// 64-bit addresses 3,500), of 2,048 x 2,048 by TMA in 160.
 // Where the tiles are few, they are narrower (choose_cut), and the contraction of
 // each may be split over a cluster of up to 8 CTAs, whose parts are added in rank order
 // through distributed shared memory, so a result does not depend on timing.
@@ -95,7 +99,11 @@ static_assert(RING_BYTES == Ring<2>::STAGES * Ring<2>::STAGE, "one layout");
 constexpr int MOST_STAGES = 6;
 constexpr int EPI_WARPS = 8;   // two for each quarter of the accumulator's lanes
 constexpr int SUM_WARPS = 4;   // WGRAD: column sums for the bias gradient
-__host__ __device__ constexpr int tc_threads(int mode) { return 64 + 32 * (EPI_WARPS + (mode == WGRAD ? SUM_WARPS : 0)); }
+constexpr int LOAD_WARPS = 4;  // operands that TMA cannot address
+__host__ __device__ constexpr int tc_threads(int mode, bool raw)
+{
+    return 64 + 32 * (EPI_WARPS + (raw ? LOAD_WARPS : mode == WGRAD ? SUM_WARPS : 0));
+}
 constexpr int STAGING = 32 * EPI_COLS * 2;   // bytes of one warp's tile on its way out
 
 struct TcShared {
@@ -214,7 +222,7 @@ struct WarpWriter {
     {
         const unsigned low = low_bits(base) | ((static_cast<unsigned>(pitch | c) & 15u) * 2);
         if (n == EPI_COLS && low == 0) {
-            load32(base + row * pitch + c, n, f);
+            load32(base + row * pitch + c, f);
             return;
         }
         if (lane == 0) tma_store_read();   // the tile before this one has left
@@ -284,6 +292,126 @@ template <int CG> __device__ __forceinline__ int zero_ragged(uint8_t *tile, int 
     fence_async_smem();
     __syncwarp();
     return steps;
+}
+
+// A load that its predicate may leave out, without a branch.
+__device__ __forceinline__ uint32_t ld_word_if(const uint32_t *p, bool there)
+{
+    uint32_t v;
+    asm volatile("{\n\t.reg .pred there;\n\tsetp.ne.u32 there, %2, 0;\n\tmov.u32 %0, 0;\n\t"
+                 "@there ld.global.nc.u32 %0, [%1];\n\t}"
+                 : "=r"(v)
+                 : "l"(p), "r"(static_cast<uint32_t>(there)));
+    return v;
+}
+
+// 8 neighbouring elements of which the first n exist, zeros in place of the others,
+// by loads of the aligned words that hold them (no word without one is read).
+struct Piece {
+    int shift, words;   // 16: the first element is the upper half of the first word
+    uint32_t mask[4];
+    __device__ __forceinline__ Piece(const mp_bf16_t *p, int n)
+    {
+        const int odd = (reinterpret_cast<uintptr_t>(p) >> 1) & 1;
+        shift = 16 * odd;
+        n = min(max(n, 0), 8);
+        words = n == 0 ? 0 : (odd + n + 1) >> 1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mask[i] = n >= 2 * i + 2 ? 0xffffffffu : n == 2 * i + 1 ? 0xffffu : 0u;
+    }
+    __device__ __forceinline__ void load(uint32_t (&v)[5], const uint32_t *q, bool there) const
+    {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) v[i] = ld_word_if(q + i, there && i < words);
+    }
+    __device__ __forceinline__ uint4 value(const uint32_t (&v)[5]) const
+    {
+        return make_uint4(__funnelshift_r(v[0], v[1], shift) & mask[0], __funnelshift_r(v[1], v[2], shift) & mask[1],
+                          __funnelshift_r(v[2], v[3], shift) & mask[2], __funnelshift_r(v[3], v[4], shift) & mask[3]);
+    }
+};
+
+__device__ __forceinline__ const uint32_t *word_of(const mp_bf16_t *p)
+{
+    return reinterpret_cast<const uint32_t *>(reinterpret_cast<uintptr_t>(p) & ~static_cast<uintptr_t>(3));
+}
+
+// Operands by loads, as TMA would place them: row r of 64 columns at r * 128 bytes,
+// its 16-byte pieces swizzled, zeros for what is not there.  A thread has a piece of
+// every 16th row, so that all of its pieces begin in the same half of a word, and
+// eight in flight.  `from`: this thread's piece of row 0; n: elements from there on.
+constexpr int RAW_STEP = 32 * LOAD_WARPS / 8;
+static_assert(RAW_STEP == 16, "four pieces of a box of 64 rows a thread");
+
+// `total` rows, of which `rows` exist.
+__device__ __forceinline__ void load_rows(uint8_t *to, const mp_bf16_t *from, int64_t pitch, int rows, int total,
+                                          int n, int t, int q)
+{
+    from += t * pitch;
+    const Piece piece(from, n);
+    const uint32_t *word = word_of(from);
+    for (int r0 = t; r0 < total; r0 += 8 * RAW_STEP) {
+        uint32_t v[8][5];
+#pragma unroll
+        for (int i = 0; i < 8; ++i, word += RAW_STEP / 2 * pitch) piece.load(v[i], word, r0 + RAW_STEP * i < rows);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = r0 + RAW_STEP * i;
+            if (r < total) *reinterpret_cast<uint4 *>(to + r * 128 + ((q ^ (r & 7)) * 16)) = piece.value(v[i]);
+        }
+    }
+}
+
+// `boxes` of 64 rows of 64 columns side by side, of whose rows `rows` exist.
+__device__ __forceinline__ void load_boxes(uint8_t *to, const mp_bf16_t *from, int64_t pitch, int rows, int boxes,
+                                           int n, int t, int q)
+{
+    from += t * pitch;
+    const uint32_t *word = word_of(from);
+    for (int box = 0; box < boxes; box += 2, word += 64) {
+        const Piece left(from, n - 64 * box), right(from, box + 1 < boxes ? n - 64 * box - 64 : 0);
+        uint32_t v[8][5];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            (i < 4 ? left : right).load(v[i], word + (i & 3) * (RAW_STEP / 2) * pitch + (i >> 2) * 32,
+                                        t + RAW_STEP * (i & 3) < rows);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = t + RAW_STEP * (i & 3);
+            if (i < 4 || box + 1 < boxes)
+                *reinterpret_cast<uint4 *>(to + (box + (i >> 2)) * BOX_BYTES + r * 128 + ((q ^ (r & 7)) * 16)) =
+                    (i < 4 ? left : right).value(v[i]);
+        }
+    }
+}
+
+// The slice at depth k, by thread `tid` of the load warps.
+template <int MODE, bool GATED>
+__device__ __forceinline__ void load_slice(const ExpertCall &c, const Tile &w, uint8_t *a, int k, int wide, int tid)
+{
+    const int q = tid & 7, t = tid >> 3, col = k + 8 * q;
+    uint8_t *b = a + A_BYTES;
+    if (MODE == WGRAD) {
+        const int64_t row = static_cast<int64_t>(w.row0) + k;
+        const int rows = w.depth - k, am = w.m0 + 8 * q, bn = w.c0 + 8 * q;
+        load_boxes(a, c.a + row * c.N + am, c.N, rows, BM / 64, c.N - am, t, q);
+        load_boxes(b, c.b + row * c.K + bn, c.K, rows, wide / 64, c.K - bn, t, q);
+        return;
+    }
+    const int pitch = MODE == FWD ? c.K : c.N;   // of A
+    load_rows(a, c.a + static_cast<int64_t>(w.m0) * pitch + col, pitch, w.m1 - w.m0, BM, pitch - col, t, q);
+    const mp_bf16_t *weights = c.b + static_cast<int64_t>(w.e) * c.N * c.K;
+    if (MODE == FWD) {
+        const mp_bf16_t *from = weights + static_cast<int64_t>(w.c0) * c.K + col;
+        const int high = GATED ? wide / 2 : wide;
+        load_rows(b, from, c.K, c.epi.cols - w.c0, high, c.K - col, t, q);
+        if (GATED)
+            load_rows(b + high * 128, from + static_cast<int64_t>(c.epi.cols) * c.K, c.K, c.epi.cols - w.c0, high,
+                      c.K - col, t, q);
+    } else {
+        const int bn = w.c0 + 8 * q;
+        load_boxes(b, weights + static_cast<int64_t>(k) * c.K + bn, c.K, c.N - k, wide / 64, c.K - bn, t, q);
+    }
 }
 
 // The sum warps alone.
@@ -393,8 +521,9 @@ __device__ __forceinline__ void join32(uint32_t addr, int split, float *turn, in
 
 // ANY: tiles of `width` columns; otherwise of BN, which the weight gradients of many
 // experts would feel (64 experts of 384 rows, 2,048 x 2,048: 191 us, as a variable 195).
-template <int MODE, bool GATED, int CG, bool ANY>
-__global__ void __launch_bounds__(tc_threads(MODE), 1)
+// RAW: operands of any alignment and width, by load_slice.
+template <int MODE, bool GATED, int CG, bool ANY, bool RAW = false>
+__global__ void __launch_bounds__(tc_threads(MODE, RAW), 1)
     k_expert_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                 const __grid_constant__ StoreMaps stores, const ExpertCall c, int split, int width)
 {
@@ -409,10 +538,12 @@ __global__ void __launch_bounds__(tc_threads(MODE), 1)
     volatile int *gave_up = &s.gave_up;
 
     if (threadIdx.x == 0) {
-        tma_prefetch(&map_a);
-        tma_prefetch(&map_b);
+        if (!RAW) {
+            tma_prefetch(&map_a);
+            tma_prefetch(&map_b);
+        }
         for (int i = 0; i < STAGES; ++i) {
-            mbar_init(smem_u32(&s.full[i]), 1);
+            mbar_init(smem_u32(&s.full[i]), RAW ? LOAD_WARPS : 1);
             mbar_init(smem_u32(&s.peer_full[i]), 1);
             mbar_init(smem_u32(&s.empty[i]), 1);
         }
@@ -451,7 +582,7 @@ __global__ void __launch_bounds__(tc_threads(MODE), 1)
     const uint32_t slice_bytes = A_BYTES + wide / CG * BK * 2;
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (!RAW && lane == 0) {
             uint32_t n = 0;   // slices loaded so far
             for (int t = first; t < total && !*gave_up; t += step) {
                 const Tile w = tile_at<MODE, CG>(c, s.start, s.tiles, t, nt, tile_cols, rank, part, split);
@@ -519,7 +650,7 @@ __global__ void __launch_bounds__(tc_threads(MODE), 1)
                 uint8_t *tile = ring + i * L::STAGE;
                 int steps = BK / 16;
                 if (MODE == WGRAD && k + BK > w.depth) {
-                    steps = zero_ragged<CG>(tile, w.depth - k, lane);
+                    steps = RAW ? (w.depth - k + 15) / 16 : zero_ragged<CG>(tile, w.depth - k, lane);
                     if (CG == 2) {
                         ok = __all_sync(FULL_MASK, mbar_wait(smem_u32(&s.peer_full[i]), (ragged >> i) & 1, gave_up));
                         if (!ok) break;
@@ -563,6 +694,21 @@ __global__ void __launch_bounds__(tc_threads(MODE), 1)
             __syncwarp();
         }
         if (!ok && lane == 0) or_status(c.status, MP_STATUS_STALLED);
+    } else if (RAW && warp >= 2 + EPI_WARPS) {
+        uint32_t n = 0;
+        bool ok = true;
+        for (int t = first; t < total && ok; t += step) {
+            const Tile w = tile_at<MODE, CG>(c, s.start, s.tiles, t, nt, tile_cols, rank, part, split);
+            for (int k = w.k0; k < w.k1; k += BK, ++n) {
+                const int i = n % STAGES;
+                ok = __all_sync(FULL_MASK, mbar_wait(smem_u32(&s.empty[i]), ((n / STAGES) & 1) ^ 1, gave_up));
+                if (!ok) break;
+                load_slice<MODE, GATED>(c, w, ring + i * L::STAGE, k, wide, threadIdx.x - 64 - 32 * EPI_WARPS);
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&s.full[i]));
+            }
+        }
     } else if (MODE == WGRAD && warp >= 2 + EPI_WARPS) {
         if (c.epi.g_bias != nullptr || c.epi.g_bias_f32 != nullptr)
             for (int t = first; t < total; t += step) {
@@ -716,6 +862,8 @@ template <typename K> int cluster_count(K kernel, int threads, int size)
 
 // How a call is cut: columns of a tile (both parts of a gated one), CTAs a tile's
 // contraction is split over.
+constexpr int RAW_ROW = 15;
+
 struct Cut {
     int wide, split;
 };
@@ -726,15 +874,16 @@ template <int MODE> int64_t tile_rows(const ExpertCall &c, int high)
 }
 
 // Single CTAs: the cut that is done first by a count of cycles, fitted to 27 calls
-// measured with all cuts (on 36 others it took the best cut or one at most 9% slower).  A slice takes its bytes at 64 a cycle, but 560 cycles at
-// least with four in flight; a tile's epilogue overlaps the next tile's products; a
-// join grows with its parts.  An expert has half a tile more than its rows fill, and
-// one at least.  us with 256 columns unsplit, and as cut: 300 rows by 3 experts of
+// measured with all cuts (on 36 others it took the best cut or one at most 9% slower).
+// A slice takes its bytes at 64 a cycle, but 560 cycles at least with four in flight
+// (15 a row where the load warps read it); a tile's epilogue overlaps the
+// next tile's products; a join grows with its parts.  An expert has half a tile more
+// than its rows fill, and one at least.  us with 256 columns unsplit, and as cut: 300 rows by 3 experts of
 // 1,000 x 1,000 14.4, 9.1 (64); x 4,000 23.3, 15.8 (192 in 4 parts); 2,999 rows by
 // 40 of 1,009 x 1,000 26.9, 23.9 (192); 500 rows by one of 512 x 8,192 42, 16.7 (64 in 4);
 // weight gradients of 2,000 rows, 512 x 1,024 16.5, 12.3 (128 in 4), of 21,063 rows,
 // 112 x 1,624 164, 27.7 (128 in 8).
-template <int MODE, bool GATED> Cut choose_cut(const ExpertCall &c)
+template <int MODE, bool GATED> Cut choose_cut(const ExpertCall &c, bool raw)
 {
     const int64_t depth = MODE == FWD ? c.K : MODE == DGRAD ? c.N : c.R / c.E, slices = (depth + BK - 1) / BK;
     const int64_t some = c.R < c.E ? c.R : c.E, filled = c.R / BM + some / 2;
@@ -747,10 +896,10 @@ template <int MODE, bool GATED> Cut choose_cut(const ExpertCall &c)
         const int64_t nt = (c.epi.cols + cols - 1) / cols, tiles = nt * tile_rows<MODE>(c, BM);
         for (int split = 1; split <= 8; split *= 2) {
             if (split > 1 && (tiles * split > sms ||
-                              tiles > cluster_count(k_expert_tc<MODE, GATED, 1, true>, tc_threads(MODE), split)))
+                              tiles > cluster_count(k_expert_tc<MODE, GATED, 1, true>, tc_threads(MODE, false), split)))
                 break;
             const int64_t waves = split > 1 ? 1 : (nt * high + sms - 1) / sms;
-            const int64_t slice = 256 + 2 * wide > 560 ? 256 + 2 * wide : 560, epilogue = 1500 + 14 * wide;
+            const int64_t slice = raw ? RAW_ROW * (BM + wide) : 256 + 2 * wide > 560 ? 256 + 2 * wide : 560, epilogue = 1500 + 14 * wide;
             const int64_t part = (slices + split - 1) / split * slice;
             const int64_t cycles = waves * (part > epilogue ? part : epilogue) + epilogue +
                                    (split > 1 ? 3500 + 1000 * split : 0);
@@ -763,18 +912,18 @@ template <int MODE, bool GATED> Cut choose_cut(const ExpertCall &c)
     return best;
 }
 
-template <int MODE, bool GATED, int CG, bool ANY>
+template <int MODE, bool GATED, int CG, bool ANY, bool RAW = false>
 mp_status_t launch_tc(const ExpertCall &c, const CUtensorMap &a, const CUtensorMap &b, const StoreMaps &m, Cut cut)
 {
     static std::atomic<uint64_t> allowed{0};
-    if (!allow_smem(k_expert_tc<MODE, GATED, CG, ANY>, allowed, TC_SMEM)) return MP_ERR_CUDA;
+    if (!allow_smem(k_expert_tc<MODE, GATED, CG, ANY, RAW>, allowed, TC_SMEM)) return MP_ERR_CUDA;
     const int cols = GATED ? cut.wide / 2 : cut.wide, split = cut.split;
     const int64_t tiles = (c.epi.cols + cols - 1) / cols * tile_rows<MODE>(c, CG * BM);
     if (tiles > INT32_MAX / 2) return MP_ERR_UNSUPPORTED;   // counted in 32 bits
-    const int64_t room = CG == 1 ? sm_count() : cluster_count(k_expert_tc<MODE, GATED, CG, ANY>, tc_threads(MODE), 2);
+    const int64_t room = CG == 1 ? sm_count() : cluster_count(k_expert_tc<MODE, GATED, CG, ANY, RAW>, tc_threads(MODE, RAW), 2);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = static_cast<unsigned>(split > 1 ? split * tiles : CG * (tiles < room ? tiles : room));
-    cfg.blockDim = tc_threads(MODE);
+    cfg.blockDim = tc_threads(MODE, RAW);
     cfg.dynamicSmemBytes = TC_SMEM;
     cfg.stream = c.stream;
     cudaLaunchAttribute attr[2];
@@ -785,7 +934,7 @@ mp_status_t launch_tc(const ExpertCall &c, const CUtensorMap &a, const CUtensorM
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CG * split == 1 ? 1 : 2;
-    (void)cudaLaunchKernelEx(&cfg, k_expert_tc<MODE, GATED, CG, ANY>, a, b, m, c, split, cut.wide);
+    (void)cudaLaunchKernelEx(&cfg, k_expert_tc<MODE, GATED, CG, ANY, RAW>, a, b, m, c, split, cut.wide);
     return check_launch();
 }
 
@@ -807,19 +956,25 @@ template <int MODE> bool in_pairs(const ExpertCall &c)
            (cols + BN - 1) / BN * (MODE == WGRAD ? static_cast<int64_t>(c.E) * ((c.N + BM - 1) / BM) : c.R / BM) >= sm_count();
 }
 
+// Whether TMA can address the operands.
+template <int MODE> bool by_tma(const ExpertCall &c)
+{
+    return c.R > 0 && c.K % 8 == 0 && (MODE == FWD || c.N % 8 == 0) && aligned16(c.a) && aligned16(c.b);
+}
+
 template <int MODE, bool GATED> mp_status_t cut_and_launch(const ExpertCall &c)
 {
-    const bool pairs = in_pairs<MODE>(c);
+    const bool raw = !by_tma<MODE>(c), pairs = !raw && in_pairs<MODE>(c);
     static std::atomic<uint64_t> allowed{0};
     if (!allow_smem(k_expert_tc<MODE, GATED, 1, true>, allowed, TC_SMEM)) return MP_ERR_CUDA;
-    const Cut cut = pairs ? Cut{BN, 1} : choose_cut<MODE, GATED>(c);
-    CUtensorMap a, b;
+    const Cut cut = pairs ? Cut{BN, 1} : choose_cut<MODE, GATED>(c, raw);
+    CUtensorMap a = {}, b = {};
     const uint64_t R = c.R, N = c.N, K = c.K, E = c.E;
     const uint64_t da[2] = {MODE == FWD ? K : N, R};
     const uint32_t box_a[2] = {64, MODE == WGRAD ? 64u : static_cast<uint32_t>(BM)};
     const uint64_t db[3] = {K, MODE == WGRAD ? R : N, E};
     const uint32_t box_b[3] = {64, MODE == FWD ? cut.wide / 2u : 64u, 1};
-    if (!make_map(&a, c.a, 2, da, box_a) || !make_map(&b, c.b, MODE == WGRAD ? 2 : 3, db, box_b)) {
+    if (!raw && (!make_map(&a, c.a, 2, da, box_a) || !make_map(&b, c.b, MODE == WGRAD ? 2 : 3, db, box_b))) {
         set_last_cuda_error(cudaErrorInvalidValue);
         return MP_ERR_CUDA;
     }
@@ -834,6 +989,7 @@ template <int MODE, bool GATED> mp_status_t cut_and_launch(const ExpertCall &c)
         set_last_cuda_error(cudaErrorInvalidValue);
         return MP_ERR_CUDA;
     }
+    if (raw) return launch_tc<MODE, GATED, 1, true, true>(c, a, b, m, cut);
     if (pairs) return launch_tc<MODE, GATED, 2, false>(c, a, b, m, cut);
     if (MODE == WGRAD && cut.wide == BN) return launch_tc<MODE, GATED, 1, MODE != WGRAD>(c, a, b, m, cut);
     return launch_tc<MODE, GATED, 1, true>(c, a, b, m, cut);
@@ -841,20 +997,17 @@ template <int MODE, bool GATED> mp_status_t cut_and_launch(const ExpertCall &c)
 
 }  // namespace
 
-template <int MODE> bool expert_tc_takes(const ExpertCall &c)
-{
-    return c.R > 0 && c.K % 8 == 0 && (MODE == FWD || c.N % 8 == 0) && aligned16(c.a) && aligned16(c.b);
-}
-
 template <int MODE> mp_status_t expert_tc(const ExpertCall &c)
 {
     if (MODE == FWD && act_gated(c.epi.act)) return cut_and_launch<MODE, MODE == FWD>(c);
     return cut_and_launch<MODE, false>(c);
 }
 
-template bool expert_tc_takes<FWD>(const ExpertCall &);
-template bool expert_tc_takes<DGRAD>(const ExpertCall &);
-template bool expert_tc_takes<WGRAD>(const ExpertCall &);
+bool expert_by_tma(const ExpertCall &c, int mode)
+{
+    return mode == FWD ? by_tma<FWD>(c) : by_tma<DGRAD>(c);   // WGRAD reads the columns DGRAD does
+}
+
 template mp_status_t expert_tc<FWD>(const ExpertCall &);
 template mp_status_t expert_tc<DGRAD>(const ExpertCall &);
 template mp_status_t expert_tc<WGRAD>(const ExpertCall &);
