@@ -899,7 +899,8 @@ template <int MODE, bool GATED> Cut choose_cut(const ExpertCall &c, bool raw)
                               tiles > cluster_count(k_expert_tc<MODE, GATED, 1, true>, tc_threads(MODE, false), split)))
                 break;
             const int64_t waves = split > 1 ? 1 : (nt * high + sms - 1) / sms;
-            const int64_t slice = raw ? RAW_ROW * (BM + wide) : 256 + 2 * wide > 560 ? 256 + 2 * wide : 560, epilogue = 1500 + 14 * wide;
+            const int64_t by_tma = 256 + 2 * wide > 560 ? 256 + 2 * wide : 560;
+            const int64_t slice = raw ? RAW_ROW * (BM + wide) : by_tma, epilogue = 1500 + 14 * wide;
             const int64_t part = (slices + split - 1) / split * slice;
             const int64_t cycles = waves * (part > epilogue ? part : epilogue) + epilogue +
                                    (split > 1 ? 3500 + 1000 * split : 0);
