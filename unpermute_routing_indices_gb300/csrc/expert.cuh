@@ -109,10 +109,43 @@ __device__ __forceinline__ unsigned low_bits(const void *p)
     return static_cast<unsigned>(reinterpret_cast<uintptr_t>(p)) & 31u;
 }
 
-__device__ __forceinline__ void load32(const mp_bf16_t *p, float (&f)[EPI_COLS])
+// Loads of rows that the same kernel may write (a residual that is the result's own
+// buffer): the coherent path, where ld_stream's asks for memory that nobody writes.
+__device__ __forceinline__ uint4 ld_row(const uint4 *p)
+{
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint16_t ld_row(const uint16_t *p)
+{
+    unsigned short v;
+    asm volatile("ld.global.L1::no_allocate.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ u32x8 ld_row(const u32x8 *p)
+{
+    u32x8 v;
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v.a.x), "=r"(v.a.y), "=r"(v.a.z), "=r"(v.a.w), "=r"(v.b.x), "=r"(v.b.y),
+                   "=r"(v.b.z), "=r"(v.b.w)
+                 : "l"(p));
+    return v;
+}
+template <bool WRITTEN, typename V> __device__ __forceinline__ V ld_of(const V *p)
+{
+    if constexpr (WRITTEN)
+        return ld_row(p);
+    else
+        return ld_stream(p);
+}
+
+template <bool WRITTEN> __device__ __forceinline__ void load32(const mp_bf16_t *p, float (&f)[EPI_COLS])
 {
     const u32x8 *q = reinterpret_cast<const u32x8 *>(p);
-    const u32x8 v0 = ld_stream(q), v1 = ld_stream(q + 1);
+    const u32x8 v0 = ld_of<WRITTEN>(q), v1 = ld_of<WRITTEN>(q + 1);
     unpack16(v0, f);
     unpack16(v1, f + 16);
 }
@@ -294,8 +327,8 @@ __device__ __forceinline__ void read32(const ExpertEpi &p, W &w, int64_t row, in
                                        int n, float (&z)[EPI_COLS])
 {
     if (p.save == MP_SAVE_BF16)
-        w.get(static_cast<const mp_bf16_t *>(p.z), static_cast<int64_t>(parts) * p.cols, row,
-              static_cast<int64_t>(part) * p.cols + c, n, z);
+        w.template get<false>(static_cast<const mp_bf16_t *>(p.z), static_cast<int64_t>(parts) * p.cols, row,
+                              static_cast<int64_t>(part) * p.cols + c, n, z);
     else
         ckpt_read32(static_cast<const uint8_t *>(p.z) + (row * parts + part) * p.cols + c,
                     p.z_exp + (row * parts + part) * ckpt_blocks(p.cols) + c / EPI_COLS, n, z);
@@ -345,7 +378,7 @@ __device__ __forceinline__ void epi_fwd(const ExpertEpi &p, W &w, int e, int64_t
     }
     if (p.residual != nullptr) {
         float f[EPI_COLS];
-        w.get(p.residual, p.cols, row, c, n, f);
+        w.template get<true>(p.residual, p.cols, row, c, n, f);   // it may be out itself
 #pragma unroll
         for (int i = 0; i < EPI_COLS; ++i) z[i] += f[i];
     }

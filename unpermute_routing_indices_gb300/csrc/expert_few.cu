@@ -83,10 +83,11 @@ __device__ __forceinline__ void lane_epilogue(const ExpertEpi &p, int64_t row, i
     if (in) p.out[row * p.cols + col] = pack(f);
 }
 
-__device__ __forceinline__ float bf16_or_zero(const mp_bf16_t *p, bool in)
+// WRITTEN: of a buffer that the kernel may write (a residual that is the result).
+template <bool WRITTEN = false> __device__ __forceinline__ float bf16_or_zero(const mp_bf16_t *p, bool in)
 {
     float f[1] = {0.0f};
-    if (in) unpack(ld_stream(p), f);
+    if (in) unpack(ld_of<WRITTEN>(p), f);
     return f[0];
 }
 
@@ -220,8 +221,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 2)
                 if (GATED) bu = bf16_or_zero(bias + cols, c.epi.bias != nullptr && f < cols);
 #pragma unroll
                 for (int i = 0; i < FT; ++i)
-                    residual[i] = bf16_or_zero(c.epi.residual + static_cast<int64_t>(row + i) * cols + f,
-                                               c.epi.residual != nullptr && i < rows && f < cols);
+                    residual[i] = bf16_or_zero<true>(c.epi.residual + static_cast<int64_t>(row + i) * cols + f,
+                                                     c.epi.residual != nullptr && i < rows && f < cols);
             }
             if (!__all_sync(FULL_MASK, mbar_wait(smem_u32(&s.acc_full[acc]), (it >> 1) & 1, gave_up))) break;
             tc_fence_after();
@@ -261,8 +262,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 2)
                 const mp_bf16_t *bias = c.epi.bias + static_cast<int64_t>(e) * PARTS * cols + f;
                 const float bz = bf16_or_zero(bias, c.epi.bias != nullptr && f < cols);
                 const float bu = GATED ? bf16_or_zero(bias + cols, c.epi.bias != nullptr && f < cols) : 0.0f;
-                const float residual = bf16_or_zero(c.epi.residual + static_cast<int64_t>(row + i) * cols + f,
-                                                    c.epi.residual != nullptr && f < cols);
+                const float residual = bf16_or_zero<true>(c.epi.residual + static_cast<int64_t>(row + i) * cols + f,
+                                                          c.epi.residual != nullptr && f < cols);
                 float z = 0.0f, u = 0.0f;
                 for (int r = 0; r < split; ++r) {
                     z += peer_value(at, r);

@@ -217,12 +217,14 @@ struct WarpWriter {
     // Rows whose 32-byte sectors a lane cannot read whole are read as they are written,
     // and turned: 20,000 rows by 64 experts of 1,016 x 1,024 with a residual 87 -> 65 us,
     // 2,999 rows by 40 experts of 1,009 x 1,000 106 -> 41.
+    // WRITTEN: what is read may be what the kernel writes, each element after it is read.
+    template <bool WRITTEN>
     __device__ __forceinline__ void get(const mp_bf16_t *base, int64_t pitch, int64_t row, int64_t c, int n,
                                         float (&f)[EPI_COLS])
     {
         const unsigned low = low_bits(base) | ((static_cast<unsigned>(pitch | c) & 15u) * 2);
         if (n == EPI_COLS && low == 0) {
-            load32(base + row * pitch + c, f);
+            load32<WRITTEN>(base + row * pitch + c, f);
             return;
         }
         if (lane == 0) tma_store_read();   // the tile before this one has left
@@ -234,7 +236,7 @@ struct WarpWriter {
             for (int i = 0; i < 4; ++i) {
                 const int r = (lane >> 2) + 8 * i;
                 if (r < rows && (lane & 3) * 8 < n)
-                    v[i] = ld_stream(reinterpret_cast<const uint4 *>(from + r * pitch) + (lane & 3));
+                    v[i] = ld_of<WRITTEN>(reinterpret_cast<const uint4 *>(from + r * pitch) + (lane & 3));
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) *piece((lane >> 2) + 8 * i, lane & 3) = v[i];
@@ -242,7 +244,7 @@ struct WarpWriter {
             uint16_t v[32] = {};
 #pragma unroll
             for (int r = 0; r < 32; ++r)
-                if (r < rows && lane < n) v[r] = ld_stream(from + r * pitch + lane);
+                if (r < rows && lane < n) v[r] = ld_of<WRITTEN>(from + r * pitch + lane);
 #pragma unroll
             for (int r = 0; r < 32; ++r) *element(r, lane) = v[r];
         }
