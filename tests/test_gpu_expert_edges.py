@@ -1,11 +1,12 @@
 """The experts' calls at edges of their contract: a residual that is the result's own
-buffer."""
+buffer, a contraction that takes longer than a wait may last without progress."""
 from __future__ import annotations
 
 import pytest
 import torch
 
 import unpermute_routing_indices_gb300 as mp
+from tests.gpu_util import DEV, status_word
 from tests.test_gpu_expert import COUNTS, GATED, normal, offsets_of
 
 pytestmark = pytest.mark.gpu
@@ -45,3 +46,20 @@ def test_residual_in_place(case):
         got, _, _ = mp.mp_expert_gemm(x, w, offsets, bias=bias, act=act, residual=both, out=both)
         assert got is both and torch.equal(both, want)
     assert torch.equal(want[R - more:], residual[R - more:])
+
+
+def test_a_long_contraction_is_no_stall():
+    """360 million rows of one expert of 128, 1 x 1: 5.6 million slices of one tile, which
+    take 5 s on one SM, longer than the 4 s that a wait lasts when nothing moves.  The
+    sums are of three ones: exact."""
+    R, E = 360_000_000, 128
+    offsets = torch.full((E + 1,), R, dtype=torch.int32, device=DEV)
+    offsets[0] = 0
+    g = torch.zeros((R, 1), dtype=torch.bfloat16, device=DEV)
+    x = torch.ones((R, 1), dtype=torch.bfloat16, device=DEV)
+    for row in (0, R // 2 + 3, R - 1):
+        g[row] = 1
+    status = status_word()
+    g_w, _ = mp.mp_expert_wgrad(g, x, offsets, dtype=torch.float32, status=status)
+    assert int(status) == 0
+    assert g_w[0].item() == 3.0 and (g_w[1:] == 0).all()

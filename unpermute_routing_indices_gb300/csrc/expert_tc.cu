@@ -110,6 +110,7 @@ struct TcShared {
     uint64_t full[MOST_STAGES], peer_full[MOST_STAGES], empty[MOST_STAGES], acc_full[2], acc_empty[2], drained;
     uint32_t tmem;
     int gave_up;
+    uint32_t loaded;   // slices that this CTA has begun to load: what the waits for a contraction go by
     float sums[SUM_WARPS][BM], sum[BM];
     int start[MP_MAX_EXPERTS + 1], tiles[MP_MAX_EXPERTS + 1];
 };
@@ -538,6 +539,7 @@ __global__ void __launch_bounds__(tc_threads(MODE, RAW), 1)
     const int rank = CG == 2 ? static_cast<int>(cluster_rank()) : 0;
     const int part = CG == 1 && split > 1 ? static_cast<int>(cluster_rank()) : 0;
     volatile int *gave_up = &s.gave_up;
+    volatile uint32_t *loaded = &s.loaded;
 
     if (threadIdx.x == 0) {
         if (!RAW) {
@@ -556,6 +558,7 @@ __global__ void __launch_bounds__(tc_threads(MODE, RAW), 1)
         mbar_init(smem_u32(&s.drained), 1);
         mbar_init_fence();
         s.gave_up = 0;
+        s.loaded = 0;
     }
     __syncwarp();
     if (warp == 1) tmem_alloc<CG>(smem_u32(&s.tmem), TMEM_COLS);
@@ -592,6 +595,7 @@ __global__ void __launch_bounds__(tc_threads(MODE, RAW), 1)
                 for (int k = w.k0; k < w.k1; k += BK, ++n) {
                     const int i = n % STAGES;
                     if (!mbar_wait(smem_u32(&s.empty[i]), ((n / STAGES) & 1) ^ 1, gave_up)) break;
+                    *loaded = n + 1;
                     uint32_t bar = smem_u32(&s.full[i]);
                     const uint32_t a = smem_u32(ring + i * L::STAGE), b = a + A_BYTES;
                     // In a pair both CTAs' copies arrive at CTA 0's barrier, but those
@@ -688,7 +692,7 @@ __global__ void __launch_bounds__(tc_threads(MODE, RAW), 1)
             n += (w.depth + BK - 1) / BK;
             if (w.depth % BK == 0) continue;
             const int i = (n - 1) % STAGES;
-            ok = __all_sync(FULL_MASK, mbar_wait(smem_u32(&s.full[i]), (ragged >> i) & 1, gave_up));
+            ok = __all_sync(FULL_MASK, mbar_wait(smem_u32(&s.full[i]), (ragged >> i) & 1, gave_up, loaded));
             if (!ok) break;
             ragged ^= 1u << i;
             zero_ragged<CG>(ring + i * L::STAGE, w.depth % BK, lane);
@@ -697,6 +701,7 @@ __global__ void __launch_bounds__(tc_threads(MODE, RAW), 1)
         }
         if (!ok && lane == 0) or_status(c.status, MP_STATUS_STALLED);
     } else if (RAW && warp >= 2 + EPI_WARPS) {
+        const int tid = threadIdx.x - 64 - 32 * EPI_WARPS;
         uint32_t n = 0;
         bool ok = true;
         for (int t = first; t < total && ok; t += step) {
@@ -705,7 +710,8 @@ __global__ void __launch_bounds__(tc_threads(MODE, RAW), 1)
                 const int i = n % STAGES;
                 ok = __all_sync(FULL_MASK, mbar_wait(smem_u32(&s.empty[i]), ((n / STAGES) & 1) ^ 1, gave_up));
                 if (!ok) break;
-                load_slice<MODE, GATED>(c, w, ring + i * L::STAGE, k, wide, threadIdx.x - 64 - 32 * EPI_WARPS);
+                if (tid == 0) *loaded = n + 1;
+                load_slice<MODE, GATED>(c, w, ring + i * L::STAGE, k, wide, tid);
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&s.full[i]));
@@ -741,7 +747,7 @@ __global__ void __launch_bounds__(tc_threads(MODE, RAW), 1)
             if (any) {
                 // Should the wait be given up, the results are flagged as invalid and
                 // the loop goes on, so that every warp meets the others.
-                (void)mbar_wait(smem_u32(&s.acc_full[acc]), (it >> 1) & 1, gave_up);
+                (void)mbar_wait(smem_u32(&s.acc_full[acc]), (it >> 1) & 1, gave_up, loaded);
                 __syncwarp();
                 tc_fence_after();
             }

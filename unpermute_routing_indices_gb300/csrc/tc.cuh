@@ -75,27 +75,38 @@ __device__ __forceinline__ uint64_t now_ns()
     return t;
 }
 
-// Waits until the phase of `parity` is over.  A wait that lasts 4 s (a thousand
-// times the longest work between two arrivals), or that another warp has given
-// up, ends false; *gave_up is then set, and every role of the kernel leaves.
+// Waits until the phase of `parity` is over.  A wait that lasts 4 s, or that another warp
+// has given up, ends false; *gave_up is then set, and every role of the kernel leaves.
+// `progress`: a count in shared memory of what the CTA's loads have done, which starts the
+// 4 s anew whenever it moves: a wait for a whole contraction takes as long as there are
+// slices (64 rows each in weight gradients: 2^29 rows of one expert are 2^23 of them, by
+// the load warps 7 s), while a slice takes microseconds.  Without it: waits for one slice,
+// an epilogue, or a contraction of at most 2^16 slices.
 constexpr uint64_t WAIT_NS = 4000000000ull;
-__device__ __noinline__ inline bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int *gave_up)
+__device__ __noinline__ inline bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int *gave_up,
+                                                   const volatile uint32_t *progress)
 {
-    const uint64_t t0 = now_ns();
+    uint64_t t0 = now_ns();
+    uint32_t seen = progress != nullptr ? *progress : 0u;
     for (;;) {
         for (int i = 0; i < 64; ++i)
             if (mbar_try(bar, parity)) return true;
         if (*gave_up) return false;
-        if (now_ns() - t0 > WAIT_NS) {
+        const uint64_t now = now_ns();
+        if (progress != nullptr && *progress != seen) {
+            seen = *progress;
+            t0 = now;
+        } else if (now - t0 > WAIT_NS) {
             *gave_up = 1;
             return false;
         }
     }
 }
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up)
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up,
+                                          const volatile uint32_t *progress = nullptr)
 {
     if (mbar_try(bar, parity)) return true;
-    return mbar_wait_slow(bar, parity, gave_up);
+    return mbar_wait_slow(bar, parity, gave_up, progress);
 }
 // For copies and products in flight when a kernel gives up: waits at most 1 s.
 __device__ __noinline__ inline void mbar_drain(uint32_t bar, uint32_t parity)
