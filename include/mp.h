@@ -277,7 +277,8 @@ mp_status_t mp_route_bwd(const float *g_weights, const void *logits, int32_t dty
  *   z[r,:]   = x[r,:] w[e]^T + bias[e]         (fp32, e the expert of row r)
  *   out[r,:] = act(z[r,:]) + residual[r,:]     (rounded once)
  * Expert e owns rows [offsets[e], offsets[e+1]), as mp_build_map gives them;
- * rows at offsets[E] and beyond are neither read nor written.
+ * rows before offsets[0] and from offsets[E] on have no expert: they enter no
+ * result, and their own are not written.
  *   x        device bf16 [R,K];  w device bf16 [E,N,K]
  *   offsets  device int32 [E+1].  Offsets that fall or leave [0,R] are clamped
  *            to the largest before them and to R (MP_STATUS_BAD_OFFSETS).
@@ -338,8 +339,8 @@ mp_status_t mp_expert_wgrad(const mp_bf16_t *g, const mp_bf16_t *x, const int32_
  *   y = h w2[e]^T + b2[e],  h = act(x w1[e]^T + b1[e])
  *   x  device bf16 [R,H];  w1 device bf16 [E,P,H], b1 [E,P] or NULL, P = F or,
  *      with a gated activation, 2F;  w2 device bf16 [E,O,F], b2 [E,O] or NULL
- *   h  device bf16 [R,F] out;  y device bf16 [R,O] out.  Rows of y from
- *      offsets[E] on are zeroed.
+ *   h  device bf16 [R,F] out;  y device bf16 [R,O] out.  Rows of y that no
+ *      expert has are zeroed.
  *   save, z, z_exp  what is kept of the first product, as in mp_expert_gemm
  */
 mp_status_t mp_expert_mlp(const mp_bf16_t *x, const mp_bf16_t *w1, const mp_bf16_t *b1,
@@ -355,7 +356,7 @@ mp_status_t mp_expert_mlp(const mp_bf16_t *x, const mp_bf16_t *w1, const mp_bf16
  *   h    device bf16 [R,F]: written (act at the kept product); may be NULL if
  *        g_w2 is
  *   g_x [R,H], g_w1 [E,P,H], g_b1 [E,P], g_w2 [E,O,F], g_b2 [E,O]: device bf16, each
- *        written unless NULL.  Rows of g_x from offsets[E] on are zeroed.
+ *        written unless NULL.  Rows of g_x that no expert has are zeroed.
  */
 mp_status_t mp_expert_mlp_bwd(const mp_bf16_t *g_y, const mp_bf16_t *x, const mp_bf16_t *w1,
                               const mp_bf16_t *w2, const int32_t *offsets, int64_t R, int32_t E,

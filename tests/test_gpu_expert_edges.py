@@ -1,5 +1,6 @@
 """The experts' calls at edges of their contract: a residual that is the result's own
-buffer, a contraction that takes longer than a wait may last without progress."""
+buffer, a contraction that takes longer than a wait may last without progress, rows
+before the first expert's."""
 from __future__ import annotations
 
 import pytest
@@ -7,6 +8,7 @@ import torch
 
 import unpermute_routing_indices_gb300 as mp
 from tests.gpu_util import DEV, status_word
+from unpermute_routing_indices_gb300 import _lib
 from tests.test_gpu_expert import COUNTS, GATED, normal, offsets_of
 
 pytestmark = pytest.mark.gpu
@@ -63,3 +65,39 @@ def test_a_long_contraction_is_no_stall():
     g_w, _ = mp.mp_expert_wgrad(g, x, offsets, dtype=torch.float32, status=status)
     assert int(status) == 0
     assert g_w[0].item() == 3.0 and (g_w[1:] == 0).all()
+
+
+@pytest.mark.parametrize("before,counts,after", [(7, [30, 0, 41], 5), (3, [1, 2, 0], 0), (200, [500, 900], 0),
+                                                 (1200, [2300, 1900, 2100], 77), (64, [0, 0], 6)])
+@pytest.mark.parametrize("H,F", [(136, 72), (33, 40), (264, 136)])
+def test_rows_before_the_first_expert(before, counts, after, H, F):
+    """Offsets may begin past row 0 (a part of the experts, with all the rows): the rows
+    before them are zero in the layer's result and gradient, whatever the buffers held,
+    and the others what a call on them alone gives."""
+    E, n = len(counts), sum(counts)
+    R, offsets = before + n + after, offsets_of(counts) + before
+    x, g = normal(R, H, seed=1), normal(R, H, seed=2)
+    w1, w2 = normal(E, 2 * F, H, seed=3, std=0.1), normal(E, H, F, seed=4, std=0.1)
+    none = torch.ones(R, dtype=torch.bool, device=DEV)
+    none[before:before + n] = False
+    x[none], g[none] = float("nan"), float("inf")
+    y, g_x = (torch.full((R, H), 7.0, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    h, g_z = (torch.empty((R, k), dtype=torch.bfloat16, device=DEV) for k in (F, 2 * F))
+    z = torch.empty((R, 2 * F), dtype=torch.bfloat16, device=DEV)
+    status, lib = status_word(), _lib.load()
+    stream = torch.cuda.current_stream().cuda_stream
+
+    def p(t):
+        return t.data_ptr()
+    assert lib.mp_expert_mlp(p(x), p(w1), None, p(w2), None, p(offsets), R, E, H, F, H, mp.ACTS["swiglu"], p(h),
+                             p(y), mp.SAVES["bf16"], p(z), None, p(status), stream) == 0
+    assert lib.mp_expert_mlp_bwd(p(g), p(x), p(w1), p(w2), p(offsets), R, E, H, F, H, mp.ACTS["swiglu"],
+                                 mp.SAVES["bf16"], p(z), None, p(g_z), None, p(g_x), None, None, None, None,
+                                 p(status), stream) == 0
+    assert int(status) == 0
+    assert (y[none] == 0).all() and (g_x[none] == 0).all()
+    assert torch.isfinite(y.float()).all() and torch.isfinite(g_x.float()).all()
+    assert (y[~none] != 7.0).any(1).all() and (g_x[~none] != 7.0).any(1).all()
+    out = torch.full((R, 2 * F), 7.0, dtype=torch.bfloat16, device=DEV)
+    mp.mp_expert_gemm(x, w1, offsets, out=out)
+    assert (out[none] == 7.0).all() and torch.equal(out[~none], z[~none])

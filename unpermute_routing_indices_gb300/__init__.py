@@ -452,8 +452,8 @@ def mp_expert_mlp(x, w1, w2, offsets, b1=None, b2=None, *, act: str = "swiglu",
                   save: str = "none", status=None):
     """An expert's two products in one call: x bf16 [R,H], w1 bf16 [E,F,H] ([E,2F,H] if act
     is gated), w2 bf16 [E,O,F] -> (y bf16 [R,O], z, z_exp) with
-    y = act(x w1[e]^T + b1[e]) w2[e]^T + b2[e], zero past the routed rows, and the first
-    product kept as `save` says (mp_expert_gemm)."""
+    y = act(x w1[e]^T + b1[e]) w2[e]^T + b2[e], zero in rows that no expert has, and the
+    first product kept as `save` says (mp_expert_gemm)."""
     dev, R, E, P, H = _products(x, "x", w1, offsets, 2)
     a, s = _named(act, ACTS, "act"), _named(save, SAVES, "save")
     _need(w2, "w2", torch.bfloat16, 3, dev)
@@ -479,7 +479,7 @@ def mp_expert_mlp(x, w1, w2, offsets, b1=None, b2=None, *, act: str = "swiglu",
 def mp_expert_mlp_bwd(g_y, x, w1, w2, offsets, z, z_exp=None, *, act: str = "swiglu",
                       need=(True, True, True, False, False), status=None):
     """Gradients of mp_expert_mlp at the kept product z (and z_exp): (g_x, g_w1, g_w2, g_b1,
-    g_b2), bf16, None where `need` is false."""
+    g_b2), bf16, None where `need` is false; g_x is zero in rows that no expert has."""
     dev, R, E, P, H = _products(x, "x", w1, offsets, 2)
     _need(w2, "w2", torch.bfloat16, 3, dev)
     O, F = w2.shape[1], w2.shape[2]

@@ -228,8 +228,8 @@ def expert_mlp(rows: torch.Tensor, offsets, w1: torch.Tensor, w2: torch.Tensor, 
     [E,H',F].  For the backward pass the product before the activation is kept
     in 8 bits (checkpoint="e4m3", a power of two per 32 columns) or as "bf16",
     and the activation's result is computed from it again; its gradients are
-    those at the kept values.  Rows past the routed count are zero in the
-    result and in the gradient."""
+    those at the kept values.  Rows that no expert has (before offsets[0], from
+    offsets[E] on) are zero in the result and in the gradient."""
     if act not in ("relu", "gelu", "silu", "geglu", "swiglu"):
         raise ValueError(f"expert_mlp needs an activation, got {act!r}")
     if checkpoint not in ("e4m3", "bf16"):

@@ -118,8 +118,8 @@ using namespace mp;
 
 namespace {
 
-// mp_expert_gemm and mp_expert_dgrad; zero_rest: rows of the result past the last
-// expert's are zeroed.
+// mp_expert_gemm and mp_expert_dgrad; zero_rest: rows of the result that no expert
+// has are zeroed.
 mp_status_t gemm(const mp_bf16_t *x, const mp_bf16_t *w, const int32_t *offsets, int64_t R, int32_t E,
                  int32_t N, int32_t K, const mp_bf16_t *bias, int32_t act, const mp_bf16_t *residual,
                  mp_bf16_t *out, int32_t save, void *z, uint8_t *z_exp, bool zero_rest,

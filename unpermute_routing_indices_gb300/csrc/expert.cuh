@@ -295,19 +295,25 @@ struct ExpertEpi {
     bool add;                 // WGRAD: add to out_f32 (and g_bias_f32)
     mp_bf16_t *g_bias;        // WGRAD: column sums of g [E,N] in bf16,
     float *g_bias_f32;        // or fp32; at most one of them given
-    bool zero_rest;           // FWD, DGRAD (one part): rows of out past the last expert's are zeroed
+    bool zero_rest;           // FWD, DGRAD (one part): rows of out that no expert has are zeroed
 };
 
-// Rows [first,R) of out, by thread `i` of `n`.
-__device__ __forceinline__ void zero_rest(const ExpertEpi &p, int first, int R, int64_t i, int64_t n)
+// Rows [first,last) of out, by thread `i` of `n`.
+__device__ __forceinline__ void zero_rows(const ExpertEpi &p, int first, int last, int64_t i, int64_t n)
 {
     mp_bf16_t *to = p.out + static_cast<int64_t>(first) * p.cols;
-    const int64_t count = static_cast<int64_t>(R - first) * p.cols;
+    const int64_t count = static_cast<int64_t>(last - first) * p.cols;
     if (p.cols % 8 == 0 && (reinterpret_cast<uintptr_t>(to) & 15u) == 0) {
         for (; i < count / 8; i += n) reinterpret_cast<uint4 *>(to)[i] = make_uint4(0, 0, 0, 0);
     } else {
         for (; i < count; i += n) to[i] = 0;
     }
+}
+// The rows of out that no expert has, of experts whose rows are [first,last).
+__device__ __forceinline__ void zero_rest(const ExpertEpi &p, int first, int last, int R, int64_t i, int64_t n)
+{
+    zero_rows(p, 0, first, i, n);
+    zero_rows(p, last, R, i, n);
 }
 
 template <typename W>

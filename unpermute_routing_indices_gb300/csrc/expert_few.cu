@@ -206,7 +206,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 2)
     } else {
         const int quad = warp & 3;
         if (c.epi.zero_rest)
-            zero_rest(c.epi, start[c.E], c.R, blockIdx.x * 128 + threadIdx.x - 64, static_cast<int64_t>(gridDim.x) * 128);
+            zero_rest(c.epi, start[0], start[c.E], c.R, blockIdx.x * 128 + threadIdx.x - 64,
+                      static_cast<int64_t>(gridDim.x) * 128);
         uint32_t it = 0;
         for (int64_t t = first; t < total; t += step, ++it) {
             int e, col, row, rows;

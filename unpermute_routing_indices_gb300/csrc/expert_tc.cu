@@ -736,7 +736,7 @@ __global__ void __launch_bounds__(tc_threads(MODE, RAW), 1)
         const int half = (warp - 2) >> 2;     // and its half of the columns
         WarpWriter out = {ring + RING_BYTES + (warp - 2) * STAGING, stores, lane, 0};
         if (MODE != WGRAD && c.epi.zero_rest)
-            zero_rest(c.epi, s.start[c.E], c.R, blockIdx.x * (32 * EPI_WARPS) + threadIdx.x - 64,
+            zero_rest(c.epi, s.start[0], s.start[c.E], c.R, blockIdx.x * (32 * EPI_WARPS) + threadIdx.x - 64,
                       static_cast<int64_t>(gridDim.x) * (32 * EPI_WARPS));
         uint32_t it = 0;
         for (int t = first; t < total; t += step) {
