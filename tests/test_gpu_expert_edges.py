@@ -1,6 +1,6 @@
 """The experts' calls at edges of their contract: a residual that is the result's own
 buffer, a contraction that takes longer than a wait may last without progress, rows
-before the first expert's."""
+before the first expert's, the status word through autograd."""
 from __future__ import annotations
 
 import pytest
@@ -9,6 +9,7 @@ import torch
 import unpermute_routing_indices_gb300 as mp
 from tests.gpu_util import DEV, status_word
 from unpermute_routing_indices_gb300 import _lib
+from unpermute_routing_indices_gb300 import autograd as ag
 from tests.test_gpu_expert import COUNTS, GATED, normal, offsets_of
 
 pytestmark = pytest.mark.gpu
@@ -101,3 +102,20 @@ def test_rows_before_the_first_expert(before, counts, after, H, F):
     out = torch.full((R, 2 * F), 7.0, dtype=torch.bfloat16, device=DEV)
     mp.mp_expert_gemm(x, w1, offsets, out=out)
     assert (out[none] == 7.0).all() and torch.equal(out[~none], z[~none])
+
+
+def test_status_through_autograd():
+    """Offsets that fall set their bit in the forward and in the backward pass of the
+    layer's differentiable form; good ones set none."""
+    R, H, F = 100, 64, 32
+    x, w1 = normal(R, H, seed=1).requires_grad_(), normal(4, 2 * F, H, seed=2).requires_grad_()
+    w2, g = normal(4, H, F, seed=3).requires_grad_(), normal(R, H, seed=4)
+    for falling in (True, False):
+        offsets = torch.tensor([0, 30, 20 if falling else 40, 90, 100], dtype=torch.int32, device=DEV)
+        status = status_word()
+        y = ag.expert_mlp(x, offsets, w1, w2, status=status)
+        expected = {"bad_offsets"} if falling else set()
+        assert mp.status_bits(int(status)) == expected
+        status.zero_()
+        torch.autograd.grad(y, [x, w1, w2], g)
+        assert mp.status_bits(int(status)) == expected

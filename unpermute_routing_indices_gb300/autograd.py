@@ -135,11 +135,12 @@ class _Route(torch.autograd.Function):
 
 class _ExpertMlp(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, rows, offsets, w1, w2, b1, b2, act, checkpoint):
+    def forward(ctx, rows, offsets, w1, w2, b1, b2, act, checkpoint, status):
         kept = checkpoint if any(ctx.needs_input_grad) else "none"
-        y, z, z_exp = mp_expert_mlp(rows, w1, w2, offsets, b1, b2, act=act, save=kept)
+        y, z, z_exp = mp_expert_mlp(rows, w1, w2, offsets, b1, b2, act=act, save=kept,
+                                    status=status)
         ctx.save_for_backward(rows, offsets, w1, w2, z, z_exp)
-        ctx.act = act
+        ctx.act, ctx.status = act, status
         return y
 
     @staticmethod
@@ -148,8 +149,8 @@ class _ExpertMlp(torch.autograd.Function):
         need = ctx.needs_input_grad
         g_x, g_w1, g_w2, g_b1, g_b2 = mp_expert_mlp_bwd(
             g_y.contiguous(), rows, w1, w2, offsets, z, z_exp, act=ctx.act,
-            need=(need[0], need[2], need[3], need[4], need[5]))
-        return g_x, None, g_w1, g_w2, g_b1, g_b2, None, None
+            need=(need[0], need[2], need[3], need[4], need[5]), status=ctx.status)
+        return g_x, None, g_w1, g_w2, g_b1, g_b2, None, None, None
 
 
 class _SortChunksPad(torch.autograd.Function):
@@ -220,7 +221,8 @@ def route(logits: torch.Tensor, topk: int, *, score: str = "softmax", bias=None,
 
 
 def expert_mlp(rows: torch.Tensor, offsets, w1: torch.Tensor, w2: torch.Tensor, b1=None,
-               b2=None, *, act: str = "swiglu", checkpoint: str = "e4m3") -> torch.Tensor:
+               b2=None, *, act: str = "swiglu", checkpoint: str = "e4m3",
+               status=None) -> torch.Tensor:
     """The experts on rows in expert order: act(rows w1[e]^T + b1[e]) w2[e]^T + b2[e].
 
     rows bf16 [R,H]; `offsets` int32 [E+1], or the Dispatch that permute gave;
@@ -229,14 +231,17 @@ def expert_mlp(rows: torch.Tensor, offsets, w1: torch.Tensor, w2: torch.Tensor, 
     in 8 bits (checkpoint="e4m3", a power of two per 32 columns) or as "bf16",
     and the activation's result is computed from it again; its gradients are
     those at the kept values.  Rows that no expert has (before offsets[0], from
-    offsets[E] on) are zero in the result and in the gradient."""
+    offsets[E] on) are zero in the result and in the gradient.
+    `status` (int32 [1]) gets the bits of both passes, to be read when the
+    caller synchronises: "bad_offsets", and "stalled", which says that results
+    are invalid (status_bits)."""
     if act not in ("relu", "gelu", "silu", "geglu", "swiglu"):
         raise ValueError(f"expert_mlp needs an activation, got {act!r}")
     if checkpoint not in ("e4m3", "bf16"):
         raise ValueError(f"checkpoint must be e4m3 or bf16, got {checkpoint!r}")
     if isinstance(offsets, Dispatch):
         offsets = offsets.offsets
-    return _ExpertMlp.apply(rows, offsets, w1, w2, b1, b2, act, checkpoint)
+    return _ExpertMlp.apply(rows, offsets, w1, w2, b1, b2, act, checkpoint, status)
 
 
 def permute(x: torch.Tensor, idx: torch.Tensor, num_experts: int, probs=None, *,
