@@ -40,3 +40,24 @@ def test_expert_mlp_hands_the_status_word_on(calls):
     assert len(calls) == 2 and all(how["status"] is status for how in calls)
     ag.expert_mlp(x, offsets, w1, w2).sum().backward()
     assert all(how["status"] is None for how in calls[2:])
+
+
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode])
+def test_expert_mlp_keeps_nothing_without_a_backward_pass(calls, mode):
+    """Evaluating a trained layer, or one whose tensors require nothing."""
+    (x, w1, w2), offsets = layer()
+    with mode():
+        assert not ag.expert_mlp(x, offsets, w1, w2).requires_grad
+    tensors, _ = layer(requires_grad=False)
+    ag.expert_mlp(tensors[0], offsets, *tensors[1:])
+    assert [how["save"] for how in calls] == ["none", "none"]
+
+
+@pytest.mark.parametrize("which", range(5))
+@pytest.mark.parametrize("checkpoint", ["e4m3", "bf16"])
+def test_expert_mlp_keeps_what_a_backward_pass_needs(calls, which, checkpoint):
+    (x, w1, w2), offsets = layer(requires_grad=False)
+    tensors = [x, w1, w2, torch.zeros(2, 6), torch.zeros(2, 4)]
+    tensors[which].requires_grad_()
+    y = ag.expert_mlp(x, offsets, w1, w2, *tensors[3:], checkpoint=checkpoint)
+    assert y.requires_grad and calls[0]["save"] == checkpoint

@@ -136,8 +136,7 @@ class _Route(torch.autograd.Function):
 class _ExpertMlp(torch.autograd.Function):
     @staticmethod
     def forward(ctx, rows, offsets, w1, w2, b1, b2, act, checkpoint, status):
-        kept = checkpoint if any(ctx.needs_input_grad) else "none"
-        y, z, z_exp = mp_expert_mlp(rows, w1, w2, offsets, b1, b2, act=act, save=kept,
+        y, z, z_exp = mp_expert_mlp(rows, w1, w2, offsets, b1, b2, act=act, save=checkpoint,
                                     status=status)
         ctx.save_for_backward(rows, offsets, w1, w2, z, z_exp)
         ctx.act, ctx.status = act, status
@@ -241,6 +240,11 @@ def expert_mlp(rows: torch.Tensor, offsets, w1: torch.Tensor, w2: torch.Tensor, 
         raise ValueError(f"checkpoint must be e4m3 or bf16, got {checkpoint!r}")
     if isinstance(offsets, Dispatch):
         offsets = offsets.offsets
+    # Nothing is kept where no backward pass can follow.  (Inside forward(), grad mode is
+    # off and needs_input_grad says what the inputs require whatever the mode was.)
+    if not (torch.is_grad_enabled() and
+            any(t is not None and t.requires_grad for t in (rows, w1, w2, b1, b2))):
+        checkpoint = "none"
     return _ExpertMlp.apply(rows, offsets, w1, w2, b1, b2, act, checkpoint, status)
 
 
