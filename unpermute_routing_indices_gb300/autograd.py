@@ -18,9 +18,13 @@ Rows of the permuted buffer past the routed count (empty slots, routes
 dropped by a capacity) are zero in the forward output and get zero gradient,
 so a computation over the whole buffer stays finite.  Rows of a restored
 tensor that no chunk names (past the sum of the split sizes) are zero too.
+
+Gradients are of first order: one taken with create_graph may be used, but
+differentiating it again raises.
 """
 from __future__ import annotations
 
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -58,6 +62,38 @@ class Dispatch:
         return self.offsets[-1:]
 
 
+class _Final(torch.autograd.Function):
+    """The gradients given, as results of `on` that cannot be differentiated again."""
+
+    @staticmethod
+    def forward(ctx, name, count, *tensors):
+        ctx.name = name
+        return tuple(t.detach() for t in tensors[:count])
+
+    @staticmethod
+    def backward(ctx, *g):
+        raise RuntimeError(f"{ctx.name}: gradients of gradients are not implemented")
+
+
+def _first_order(backward):
+    """A backward pass whose results cannot be differentiated again.  Where a graph of it
+    is asked for (create_graph), they depend on what they are computed from, the
+    gradients given and the tensors kept, by a node that refuses: without it their
+    second derivatives would be left out of a sum without a word."""
+    @functools.wraps(backward)
+    def checked(ctx, *grads):
+        results = backward(ctx, *grads)
+        if not torch.is_grad_enabled():
+            return results
+        on = [t for t in (*grads, *ctx.saved_tensors) if t is not None and t.requires_grad]
+        made = [t for t in results if t is not None]
+        if not on or not made:
+            return results
+        final = iter(_Final.apply(backward.__qualname__.split(".")[0].strip("_"), len(made), *made, *on))
+        return tuple(None if t is None else next(final) for t in results)
+    return checked
+
+
 class _Permute(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, probs, row_id_map, routed, num_rows):
@@ -70,6 +106,7 @@ class _Permute(torch.autograd.Function):
         return out, out_probs
 
     @staticmethod
+    @_first_order
     def backward(ctx, g_out, g_out_probs):
         (row_id_map,) = ctx.saved_tensors
         gp = None
@@ -94,6 +131,7 @@ class _Unpermute(torch.autograd.Function):
         return y
 
     @staticmethod
+    @_first_order
     def backward(ctx, g_y):
         rows, probs, row_id_map, routed = ctx.saved_tensors
         g_rows, g_probs = mp_unpermute_bwd(g_y.contiguous(), row_id_map, rows, probs,
@@ -112,6 +150,7 @@ class _TopkSoftmax(torch.autograd.Function):
         return idx, probs
 
     @staticmethod
+    @_first_order
     def backward(ctx, g_idx, g_probs):
         probs, idx = ctx.saved_tensors
         g = mp_topk_softmax_bwd(g_probs.contiguous(), probs, idx, ctx.num_experts)
@@ -128,6 +167,7 @@ class _Route(torch.autograd.Function):
         return idx, weights
 
     @staticmethod
+    @_first_order
     def backward(ctx, g_idx, g_weights):
         logits, idx = ctx.saved_tensors
         return mp_route_bwd(g_weights.contiguous(), logits, idx, **ctx.how), None, None, None, None
@@ -143,6 +183,7 @@ class _ExpertMlp(torch.autograd.Function):
         return y
 
     @staticmethod
+    @_first_order
     def backward(ctx, g_y):
         rows, offsets, w1, w2, z, z_exp = ctx.saved_tensors
         need = ctx.needs_input_grad
@@ -166,6 +207,7 @@ class _SortChunksPad(torch.autograd.Function):
         return out, out_probs, row_map, group_off
 
     @staticmethod
+    @_first_order
     def backward(ctx, g_out, g_out_probs, g_row_map, g_group_off):
         (row_map,) = ctx.saved_tensors
         g_x = torch.zeros((ctx.num_rows, g_out.shape[1]), dtype=g_out.dtype,
@@ -192,6 +234,7 @@ class _UnpadRestore(torch.autograd.Function):
         return y, y_probs
 
     @staticmethod
+    @_first_order
     def backward(ctx, g_y, g_y_probs):
         (row_map,) = ctx.saved_tensors
         gp = None
