@@ -242,7 +242,10 @@ mp_status_t mp_topk_softmax_bwd(const float *g_probs, const float *probs, const 
  * if n_groups > 1, the topk_groups groups of consecutive experts are kept whose
  * sum of the group_top (1 or 2) largest c is largest; then the K experts with
  * the largest c among the kept are picked, slot 0 the largest.  Equal values
- * favour the lower group and expert.  The choice is that of c in 64 bits.
+ * favour the lower group and expert.  The choice is that of c in 64 bits; but
+ * without a bias experts, and groups of which one expert counts (group_top 1,
+ * or one expert a group), are compared by their logits, which order them as
+ * the scores do and stay apart where scores round to one value.
  *   weights[t,k] = scale * s_k / sum_j s_j over the picks   (renorm != 0)
  *                = scale * s_k                              (renorm == 0)
  * An expert whose logit is -inf or NaN, or whose bias is, is never picked;

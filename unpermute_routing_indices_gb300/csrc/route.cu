@@ -34,7 +34,7 @@ struct RouteArgs {
     const float *bias;
     int64_t T;
     int E, K, score, n_groups, topk_groups, group_top, renorm;
-    uint32_t group_magic;   // ceil(2^32 / experts a group): (e * magic) >> 32 is e's group
+    uint32_t group_magic;   // ceil(2^32 / experts a group): (e * magic) >> 32 is e's group (of 2 experts or more)
     float scale;
     int32_t *idx;
     float *weights;
@@ -791,6 +791,8 @@ extern "C" mp_status_t mp_route(const void *logits, int32_t dtype, const float *
         return MP_ERR_INVALID_ARG;
     if (T == 0) return MP_OK;
     if (logits == nullptr || idx == nullptr || weights == nullptr) return MP_ERR_INVALID_ARG;
+    // Groups of one expert each: the best experts of the best groups are the best experts.
+    if (n_groups == E) n_groups = topk_groups = group_top = 1;
     const RouteArgs a = {logits, bias, T, E, K, score, n_groups, topk_groups, group_top, renorm,
                          static_cast<uint32_t>(((1ull << 32) + E / n_groups - 1) / (E / n_groups)),
                          scale, idx, weights};
