@@ -19,6 +19,8 @@ pytestmark = pytest.mark.gpu
 IN_PLACE = [
     ("big", 640, 192, "none", 0),                  # whole tiles, stored by TMA
     ("long", 512, 320, "silu", 0),
+    ("long", 2 * 1012, 776, "swiglu", 0),          # pairs of CTAs
+    ("long", 2050, 1000, "none", 0),
     ("long", 2 * 264, 200, "swiglu", 8),           # 16-byte, not 32-byte aligned rows
     ("many", 101, 200, "relu", 0),                 # rows off 16 bytes: neighbours share sectors
     ("big", 2 * 129, 1031, "swiglu", 0),           # the load warps
