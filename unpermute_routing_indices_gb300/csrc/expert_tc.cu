@@ -868,10 +868,11 @@ template <typename K> int cluster_count(K kernel, int threads, int size)
     return n;
 }
 
-// How a call is cut: columns of a tile (both parts of a gated one), CTAs a tile's
-// contraction is split over.
+// Cycles that the load warps take for a row of a slice.
 constexpr int RAW_ROW = 15;
 
+// How a call is cut: columns of a tile (both parts of a gated one), CTAs a tile's
+// contraction is split over.
 struct Cut {
     int wide, split;
 };
@@ -884,7 +885,7 @@ template <int MODE> int64_t tile_rows(const ExpertCall &c, int high)
 // Single CTAs: the cut that is done first by a count of cycles, fitted to 27 calls
 // measured with all cuts (on 36 others it took the best cut or one at most 9% slower).
 // A slice takes its bytes at 64 a cycle, but 560 cycles at least with four in flight
-// (15 a row where the load warps read it); a tile's epilogue overlaps the
+// (RAW_ROW a row where the load warps read it); a tile's epilogue overlaps the
 // next tile's products; a join grows with its parts.  An expert has half a tile more
 // than its rows fill, and one at least.  us with 256 columns unsplit, and as cut: 300 rows by 3 experts of
 // 1,000 x 1,000 14.4, 9.1 (64); x 4,000 23.3, 15.8 (192 in 4 parts); 2,999 rows by
@@ -951,17 +952,28 @@ mp_status_t launch_tc(const ExpertCall &c, const CUtensorMap &a, const CUtensorM
 // L2, which bounds the single CTAs: 131,072 x 4,096 rows by 128 experts of 2,048
 // 1,377 -> 1,211 us; weight gradients of 8 x 2,048 rows, 4,096 x 4,096, 370 -> 344.
 // But its tile has 256 rows, of which an expert leaves half of one empty on average,
-// and in WGRAD, where the rows are the contraction, the hand-over of the accumulator
-// between the CTAs counts when there are few.  64 experts of 2,048 columns, one in
-// eight empty, depth 2,048 / 1,024: 384 rows an expert 177.6 -> 177.0 / 94.0 -> 90.5 us,
-// 512 rows 216 -> 211 / 114 -> 108, 1,024 rows 391 -> 373 / 204 -> 188.  Weight
-// gradients: 128 rows an expert (256 experts) 223 -> 372, 384 rows 219.6 -> 220.1,
-// 512 rows 263 -> 253.
+// and the hand-over of the accumulator between the CTAs counts where the contraction
+// is short.  us of single CTAs / pairs, 64 experts, one in eight empty (the bits are the same):
+//   rows an expert            256      320      384      512      1,024
+//   2,048 x 2,048           143/134  148/148  172/161  209/201  375/346
+//   its row gradient        147/129  151/147  176/160  228/212  440/390
+// With loads all equal, 384 rows fill a tile and a half: 168/178 and 177/184, 512 rows
+// 213/186 and 221/189.  The border, 384, lies between the two.
+//   contraction of            512      640      768      896     1,024
+//   384 rows, 2,048 wide     57/67    66/71    76/73    85/82    94/91
+//   row gradient             61/66    70/65    80/70      -      98/91
+//   1,024 rows, 2,048 wide  119/133  140/140  160/148  182/166  205/190
+//   row gradient            129/124  154/132  173/145     -     217/186
+// From 768 (row gradients 640) on neither loses.  Weight gradients, whose contraction is the rows (2,048 x
+// 2,048): 384 rows 199/208, 512 rows 239/238 (equal loads 233/219), 1,024 rows 418/413
+// (408/389).
 // With fewer tiles than SMs another cut does more (choose_cut).
 template <int MODE> bool in_pairs(const ExpertCall &c)
 {
     const int64_t cols = act_gated(c.epi.act) && MODE == FWD ? 2ll * c.epi.cols : c.epi.cols;
+    const int depth = MODE == FWD ? c.K : c.N;   // of the products of rows
     return c.R >= (MODE == WGRAD ? 512 : 384) * static_cast<int64_t>(c.E) &&
+           (MODE == WGRAD || depth >= (MODE == FWD ? 768 : 640)) &&
            (cols + BN - 1) / BN * (MODE == WGRAD ? static_cast<int64_t>(c.E) * ((c.N + BM - 1) / BM) : c.R / BM) >= sm_count();
 }
 
