@@ -293,12 +293,18 @@ mp_status_t mp_route_bwd(const float *g_weights, const void *logits, int32_t dty
  *            (parts 2 if gated, else 1): per row, part and 32 columns z is
  *            code * 2^(z_exp-127), with the smallest power of two that brings
  *            the largest to 448 at most; what is not finite is stored as NaN.
- * Sums are fp32 in an order that depends on K alone for a given kernel, so a
- * row's result does not depend on the rows around it.
- * Limits: E <= MP_MAX_EXPERTS; N, K <= 2^22; R < 2^31 - 1024.
- * A K that is a multiple of 8, with 16-byte aligned x and w, takes the tensor
- * cores; other calls are computed by a much slower kernel.  (mp_expert_dgrad and
- * mp_expert_wgrad ask the same of N.)
+ * Sums are fp32.  Calls of the same R, E, N, K, activation, alignment of x and w, and
+ * device add up a row's products in the same order: a row's result then does not
+ * depend on where it stands, on the offsets or on the rows around it.  Between calls of
+ * different R it may differ within the error of fp32 sums, since the contraction
+ * is split where there are few tiles: batches of any size are not bit-invariant, as
+ * mp_unpermute's are.
+ * Limits: E <= MP_MAX_EXPERTS; N, K <= 2^22; R < 2^31 - 1024; at most 2^30 tiles
+ * (rows / 128 + E, in weight gradients E * ceil(N / 128), times columns / 64);
+ * MP_ERR_UNSUPPORTED beyond.
+ * Every call takes the tensor cores.  Operands that TMA can address, which is to say
+ * a K that is a multiple of 8 and 16-byte aligned x and w, are several times faster
+ * than others.  (mp_expert_dgrad and mp_expert_wgrad ask the same of N.)
  */
 mp_status_t mp_expert_gemm(const mp_bf16_t *x, const mp_bf16_t *w, const int32_t *offsets,
                            int64_t R, int32_t E, int32_t N, int32_t K, const mp_bf16_t *bias,

@@ -1,6 +1,7 @@
 """The experts' calls at edges of their contract: a residual that is the result's own
 buffer, a contraction that takes longer than a wait may last without progress, rows
-before the first expert's, the status word through autograd."""
+before the first expert's, the status word through autograd,
+no rows, the order of sums."""
 from __future__ import annotations
 
 import pytest
@@ -121,3 +122,49 @@ def test_status_through_autograd():
         status.zero_()
         torch.autograd.grad(y, [x, w1, w2], g)
         assert mp.status_bits(int(status)) == expected
+
+
+def test_no_rows_through_autograd():
+    """No rows at all: empty results, zero gradients of the weights."""
+    x = torch.empty((0, 64), dtype=torch.bfloat16, device=DEV, requires_grad=True)
+    w1, w2 = normal(3, 64, 64, seed=1).requires_grad_(), normal(3, 64, 32, seed=2).requires_grad_()
+    b1, b2 = normal(3, 64, seed=3).requires_grad_(), normal(3, 64, seed=4).requires_grad_()
+    for checkpoint in ("e4m3", "bf16"):
+        y = ag.expert_mlp(x, offsets_of([0, 0, 0]), w1, w2, b1, b2, checkpoint=checkpoint)
+        assert y.shape == (0, 64)
+        g_x, *others = torch.autograd.grad(y, [x, w1, w2, b1, b2], torch.empty_like(y))
+        assert g_x.shape == (0, 64) and all((g == 0).all() for g in others)
+
+
+# Two loads of the same experts with the same sum; N, K: few rows whole and split, tiles
+# whole and split, the load warps, pairs of CTAs
+LOADS = [
+    ([5, 9, 2, 0, 16], [0, 3, 20, 8, 1], 264, 512),
+    ([1, 0, 1, 2], [2, 2, 0, 0], 136, 2048),
+    ([300, 513, 128, 1000], [600, 41, 1200, 100], 640, 192),
+    ([70, 30], [1, 99], 264, 4104),
+    ([70, 300], [200, 170], 259, 1031),
+    ([1500, 700, 1031], [31, 2500, 700], 2048, 768),
+]
+
+
+@pytest.mark.parametrize("one,two,N,K", LOADS)
+def test_a_row_does_not_depend_on_its_place(one, two, N, K):
+    """In calls of the same sizes a row of an expert has the same bits wherever it stands
+    and whatever the loads are."""
+    E, R = len(one), sum(one)
+    assert sum(two) == R
+    pool = [normal(max(a, b, 1), K, seed=10 + e) for e, (a, b) in enumerate(zip(one, two))]
+    pool_g = [normal(max(a, b, 1), N, seed=50 + e) for e, (a, b) in enumerate(zip(one, two))]
+    w = normal(E, N, K, seed=2, std=K ** -0.5)
+    got = []
+    for counts in (one, two):
+        x, g = (torch.cat([p[e][:n] for e, n in enumerate(counts)]) for p in (pool, pool_g))
+        offsets = offsets_of(counts)
+        got.append((offsets.tolist(), mp.mp_expert_gemm(x, w, offsets, act="silu")[0],
+                    mp.mp_expert_dgrad(g, w, offsets)[0]))
+    (at1, *first), (at2, *second) = got
+    for a, b in zip(first, second):
+        for e in range(E):
+            n = min(one[e], two[e])
+            assert torch.equal(a[at1[e]:at1[e] + n], b[at2[e]:at2[e] + n])
