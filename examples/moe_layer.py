@@ -21,7 +21,7 @@ if ROOT not in sys.path:
 
 from unpermute_routing_indices_gb300 import autograd as ag  # noqa: E402
 from unpermute_routing_indices_gb300 import (mp_build_map, mp_expert_mlp, mp_permute,  # noqa: E402
-                                             mp_route, mp_unpermute)
+                                             mp_route, mp_unpermute, status_bits)
 
 
 @dataclass
@@ -49,13 +49,15 @@ class MoeLayer:
     def parameters(self):
         return [self.router, self.w1, self.w2]
 
-    def train_step(self, x: torch.Tensor):
+    def train_step(self, x: torch.Tensor, status=None):
         """x bf16 [T,H] -> (y bf16 [T,H], rows of each expert int32 [E]); y is
-        differentiable w.r.t. x and the parameters."""
+        differentiable w.r.t. x and the parameters.  `status` (int32 [1]) collects
+        the experts' status bits of both passes."""
         idx, weights = ag.route(x.float() @ self.router.t(), self.topk, score="sigmoid",
                                 bias=self.bias)
         rows, _, d = ag.permute(x, idx, self.router.shape[0])
-        out = ag.expert_mlp(rows, d, self.w1, self.w2, act="swiglu", checkpoint="e4m3")
+        out = ag.expert_mlp(rows, d, self.w1, self.w2, act="swiglu", checkpoint="e4m3",
+                            status=status)
         return ag.unpermute(out, d, weights), d.counts
 
     @torch.no_grad()
@@ -88,12 +90,13 @@ def train(steps: int = 300, T: int = 2048, H: int = 256, F: int = 128, E: int = 
     g = torch.Generator(device="cuda")
     g.manual_seed(seed + 2)
     losses, loads = [], []
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")   # read once, at the end
     for step in range(steps):
         x = torch.randn(T, H, generator=g, device="cuda").bfloat16()
         for p, m in zip(layer.parameters(), masters):
             p.requires_grad_(False).copy_(m.detach())
             p.requires_grad_(True)
-        y, counts = layer.train_step(x)
+        y, counts = layer.train_step(x, status)
         loss = (y.float() - teacher.answer(x).float()).square().mean()
         for m, d in zip(masters, torch.autograd.grad(loss, layer.parameters())):
             m.grad = d.float()
@@ -105,6 +108,8 @@ def train(steps: int = 300, T: int = 2048, H: int = 256, F: int = 128, E: int = 
         if report and (step % 50 == 0 or step == steps - 1):
             report(f"step {step:4d}  loss {losses[-1].item():.4f}  "
                    f"largest load {loads[-1].item():.2f} of the mean")
+    if int(status):
+        raise RuntimeError(f"the experts' products report {sorted(status_bits(int(status)))}")
     for p in layer.parameters():
         p.requires_grad_(False)
     return layer, teacher, torch.stack(losses), torch.stack(loads)
