@@ -63,6 +63,12 @@ def test_expert_mlp_keeps_what_a_backward_pass_needs(calls, which, checkpoint):
     assert y.requires_grad and calls[0]["save"] == checkpoint
 
 
+def test_expert_mlp_rounds_to_8_bits_only_if_asked(calls):
+    (x, w1, w2), offsets = layer()
+    ag.expert_mlp(x, offsets, w1, w2)
+    assert calls[0]["save"] == "bf16"
+
+
 def stand_ins(monkeypatch):
     """The other entry points on the CPU, as far as their types go: every result is a
     linear form of the floating-point arguments (so gradients depend on them)."""

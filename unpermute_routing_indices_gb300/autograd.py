@@ -263,14 +263,15 @@ def route(logits: torch.Tensor, topk: int, *, score: str = "softmax", bias=None,
 
 
 def expert_mlp(rows: torch.Tensor, offsets, w1: torch.Tensor, w2: torch.Tensor, b1=None,
-               b2=None, *, act: str = "swiglu", checkpoint: str = "e4m3",
+               b2=None, *, act: str = "swiglu", checkpoint: str = "bf16",
                status=None) -> torch.Tensor:
     """The experts on rows in expert order: act(rows w1[e]^T + b1[e]) w2[e]^T + b2[e].
 
     rows bf16 [R,H]; `offsets` int32 [E+1], or the Dispatch that permute gave;
     w1 bf16 [E,F,H] ([E,2F,H] for geglu and swiglu, gate first), w2 bf16
     [E,H',F].  For the backward pass the product before the activation is kept
-    in 8 bits (checkpoint="e4m3", a power of two per 32 columns) or as "bf16",
+    as bf16, or in 8 bits where the caller asks for it (checkpoint="e4m3", 4
+    significant bits and a power of two per 32 columns, 9/16 of the bytes),
     and the activation's result is computed from it again; its gradients are
     those at the kept values.  Rows that no expert has (before offsets[0], from
     offsets[E] on) are zero in the result and in the gradient.
