@@ -23,8 +23,9 @@
 // each may be split over a cluster of up to 8 CTAs, whose parts are added in rank order
 // through distributed shared memory, so a result does not depend on timing.
 // What bounds it: for experts of many rows the tensor cores (131,072 x 4,096 by 128
-// experts of 2,048 columns in 1,211 us, 1.82 PFLOP/s, 0.92 of cuBLAS's measured
-// 8,192^3); for few rows the bytes of weights and results and the epilogue.
+// experts of 2,048 columns, swiglu: in short runs on equal loads 1,211 us, 1.82 PFLOP/s,
+// 0.92 of cuBLAS's measured 8,192^3; on unequal loads and under the power limit 1,490 to
+// 1,560 us, 1.41 to 1.48); for few rows the bytes of weights and results and the epilogue.
 #include "expert.cuh"
 #include "tc.cuh"
 
