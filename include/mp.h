@@ -110,6 +110,18 @@ typedef void *mp_stream_t;    /* a cudaStream_t                             */
 #define MP_SAVE_BF16 1
 #define MP_SAVE_E4M3 2
 
+/* Norms of mp_block_norm, and what its gate is spread over. */
+#define MP_NORM_RMS 0
+#define MP_NORM_LAYER 1
+#define MP_GATE_NONE 0
+#define MP_GATE_CHANNEL 1   /* [H]   */
+#define MP_GATE_TOKEN 2     /* [T]   */
+#define MP_GATE_ELEMENT 3   /* [T,H] */
+#define MP_MAX_NORM_WIDTH 32768
+
+#define MP_MAX_LAYER_TOKENS 64
+#define MP_MAX_LAYER_WIDTH 65536
+
 /* Text for a status code (static storage). */
 const char *mp_status_string(mp_status_t status);
 
@@ -373,6 +385,110 @@ mp_status_t mp_expert_mlp_bwd(const mp_bf16_t *g_y, const mp_bf16_t *x, const mp
                               const void *z, const uint8_t *z_exp, mp_bf16_t *g_z, mp_bf16_t *h,
                               mp_bf16_t *g_x, mp_bf16_t *g_w1, mp_bf16_t *g_b1, mp_bf16_t *g_w2,
                               mp_bf16_t *g_b2, int32_t *dev_status, mp_stream_t stream);
+
+/*
+ * The whole layer for a few tokens: router product, choice, the experts' two products and
+ * the combine, as single tokens of an answer need them.
+ *   l[t,:]  = x[t,:] router^T                     (each logit fp32, from a sum of about
+ *             48 bits: the choice does not depend on an order of sums)
+ *   idx, weights as mp_route gives them for l
+ *   y[t,:]  = sum over k in slot order, fp32 from +0, of weights[t,k] *
+ *             (h[t,k,:] w2[e]^T + b2[e]),  e = idx[t,k], empty slots skipped
+ *   h[t,k,:] = act(x[t,:] w1[e]^T + b1[e])        (fp32 sums, rounded to bf16)
+ * rounded once: what the calls mp_route, mp_build_map, mp_permute, mp_expert_mlp and
+ * mp_unpermute give, but for their rounding of each expert's result to bf16.
+ *   x        device bf16 [T,H]
+ *   router   device [E,H] of type router_dtype (MP_DTYPE_*)
+ *   bias, score, n_groups, topk_groups, group_top, renorm, scale   as mp_route
+ *   w1 device bf16 [E,P,H], b1 [E,P] or NULL, P = F or, with a gated activation, 2F;
+ *   w2 device bf16 [E,O,F], b2 [E,O] or NULL
+ *   idx      device int32 [T,K], weights device fp32 [T,K], y device bf16 [T,O]: out
+ *   workspace device, >= mp_moe_layer_workspace_size(T,E,K,H,F,O) bytes, 16-byte
+ *            aligned; scratch, contents undefined before and after the call.  Calls that
+ *            may overlap (on other streams, or graphs that run at once) need their own.
+ * Calls of the same sizes, activation and alignment of x, w1 and w2 add up a token's
+ * products in the same order: its result then does not depend on the other tokens.
+ * dev_status: MP_STATUS_STALLED.
+ * Limits: T <= MP_MAX_LAYER_TOKENS, E <= MP_MAX_EXPERTS, K <= 32, H, F and O <=
+ * MP_MAX_LAYER_WIDTH; MP_ERR_UNSUPPORTED beyond.
+ */
+size_t mp_moe_layer_workspace_size(int64_t T, int32_t E, int32_t K, int32_t H, int32_t F,
+                                   int32_t O);
+mp_status_t mp_moe_layer(const mp_bf16_t *x, const void *router, int32_t router_dtype,
+                         const float *bias, const mp_bf16_t *w1, const mp_bf16_t *b1,
+                         const mp_bf16_t *w2, const mp_bf16_t *b2, int64_t T, int32_t E,
+                         int32_t K, int32_t H, int32_t F, int32_t O, int32_t act,
+                         int32_t score, int32_t n_groups, int32_t topk_groups,
+                         int32_t group_top, int32_t renorm, float scale, int32_t *idx,
+                         float *weights, mp_bf16_t *y, void *workspace,
+                         size_t workspace_bytes, int32_t *dev_status, mp_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* The norms before and after a block                                        */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * What stands between one block's result x and the next block's input, in one pass:
+ *   u = norm(x) * post_weight + post_bias, or x without a post_weight
+ *   s = residual + scale * gate * u           (the stream; no residual: 0, no gate: 1)
+ *   y = norm(s) * pre_weight + pre_bias       (with a pre_weight)
+ *   norm(v) = v / sqrt(mean(v^2) + eps)                          MP_NORM_RMS
+ *           = (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps)  MP_NORM_LAYER
+ * over the H values of a row, in fp32; s and y are each rounded once (y comes from
+ * the s that is not rounded).
+ *   x, residual  device [T,H] of type dtype (MP_DTYPE_*); residual may be NULL
+ *   gate         device [H], [T] or [T,H] of type dtype as gate_form says
+ *   post_weight, post_bias, pre_weight, pre_bias   device [H] of type dtype or NULL; one
+ *                of the weights is given, and a bias only with its weight
+ *   s            device [T,H] out; may be NULL where it would be x itself (no residual,
+ *                gate or post_weight, scale 1)
+ *   y            device [T,H] out, given exactly when pre_weight is
+ *   stats        device fp32 [T,4] out or NULL, 16-byte aligned: mean and 1/sqrt(...)
+ *                of x (0 without a post_weight; mean 0 for rms), the same of s
+ * s and y may each be the buffer of x, of residual or of a [T,H] gate.  A row's result
+ * depends on nothing but that row.  Limits: H <= MP_MAX_NORM_WIDTH; T < 2^31.
+ */
+mp_status_t mp_block_norm(const void *x, const void *residual, int64_t T, int32_t H,
+                          int32_t dtype, int32_t kind, float eps, const void *post_weight,
+                          const void *post_bias, const void *gate, int32_t gate_form,
+                          float scale, const void *pre_weight, const void *pre_bias, void *s,
+                          void *y, float *stats, mp_stream_t stream);
+
+/* Bytes of device workspace mp_block_norm_bwd needs: a multiple of 256, at least 256; 0
+ * only for invalid sizes. */
+size_t mp_block_norm_bwd_workspace_size(int64_t T, int32_t H);
+
+/*
+ * Gradients of mp_block_norm at the s and stats that it wrote.  With hat = (v - mean) *
+ * rstd of a norm's input v, and N(d) = rstd * (d - mean(d) - hat * mean(d * hat)) over the
+ * row (rms: without mean(d)):
+ *   g_t        = g_s + N(g_y * pre_weight)              (of s; what is absent is 0)
+ *   g_u        = scale * g_t * gate
+ *   g_x        = N(g_u * post_weight), or g_u without a post_weight
+ *   g_residual = g_t
+ *   g_gate     = scale * g_t * u, summed over what shares the gate
+ *   g_pre_weight = sum over rows of g_y * hat, g_pre_bias of g_y; g_post_weight and
+ *   g_post_bias alike of g_u
+ *   g_s, g_y   device [T,H] of type dtype; g_s may be NULL with a pre_weight; g_y is
+ *              given exactly then
+ *   x          as it was; may be NULL without post_weight and gate
+ *   s          as written (or x, where it is x); may be NULL without pre_weight
+ *   g_x, g_residual device [T,H], g_gate as the gate, g_post_weight ... [H]: each out, or
+ *              NULL: not wanted.  What is of the shape [H] is of type grad_dtype, which is
+ *              dtype or MP_DTYPE_FP32; the rest of type dtype.
+ *   workspace  device, >= mp_block_norm_bwd_workspace_size(T,H) bytes, 16-byte
+ *              aligned; may be NULL if no gradient of the shape [H] is wanted
+ * g_x and g_residual may each be the buffer of one of the [T,H] inputs.  Sums over rows
+ * are made in an order that depends on T, H, the types and the device's alone.
+ */
+mp_status_t mp_block_norm_bwd(const void *g_s, const void *g_y, const void *x, const void *s,
+                              const float *stats, int64_t T, int32_t H, int32_t dtype,
+                              int32_t kind, const void *post_weight, const void *post_bias,
+                              const void *gate, int32_t gate_form, float scale,
+                              const void *pre_weight, void *g_x, void *g_residual,
+                              void *g_gate, void *g_post_weight, void *g_post_bias,
+                              void *g_pre_weight, void *g_pre_bias, int32_t grad_dtype,
+                              void *workspace, size_t workspace_bytes, mp_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Permute / unpermute  [d9d _permute_kernel, _unpermute_kernel; MBI]        */

@@ -19,7 +19,9 @@ from . import _lib
 __all__ = [
     "MPError", "mp_build_map", "mp_build_map_capacity", "mp_build_map_workspace_size",
     "mp_topk_softmax", "mp_topk_softmax_bwd", "mp_route", "mp_route_bwd", "mp_expert_gemm",
-    "mp_expert_dgrad", "mp_expert_wgrad", "mp_expert_mlp", "mp_expert_mlp_bwd", "mp_permute", "mp_unpermute", "mp_unpermute_ep", "EP_BF16_PARTIALS", "EP_FP64_CROSS_RANK",
+    "mp_expert_dgrad", "mp_expert_wgrad", "mp_expert_mlp", "mp_expert_mlp_bwd",
+    "mp_moe_layer", "mp_moe_layer_workspace_size", "MAX_LAYER_TOKENS", "mp_block_norm",
+    "mp_block_norm_bwd", "mp_block_norm_bwd_workspace_size", "mp_permute", "mp_unpermute", "mp_unpermute_ep", "EP_BF16_PARTIALS", "EP_FP64_CROSS_RANK",
     "mp_permute_bwd", "mp_unpermute_bwd", "mp_sort_chunks_pad", "mp_unpad_restore",
     "mp_sort_chunks_pad_bwd", "mp_unpad_restore_bwd", "status_bits", "library_path",
 ]
@@ -35,6 +37,8 @@ DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # MP_DTYPE_*
 SCORES = {"softmax": 0, "sigmoid": 1}                              # MP_SCORE_*
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3, "geglu": 4, "swiglu": 5}   # MP_ACT_*
 SAVES = {"none": 0, "bf16": 1, "e4m3": 2}                          # MP_SAVE_*
+NORMS = {"rms": 0, "layer": 1}                                     # MP_NORM_*
+MAX_LAYER_TOKENS = 64                                              # MP_MAX_LAYER_TOKENS
 EP_BF16_PARTIALS = 0x1
 EP_FP64_CROSS_RANK = 0x2
 
@@ -334,17 +338,21 @@ def _checkpoint(z, z_exp, R, F, act, save, dev, make):
     return tuple(got)
 
 
+_NO_OFFSETS = object()   # a call whose rows are not in expert order
+
+
 def _products(rows, name, w, offsets, width):
     _need(rows, name, torch.bfloat16, 2)
     dev = rows.device
     _need(w, "w", torch.bfloat16, 3, dev)
-    _need(offsets, "offsets", torch.int32, 1, dev)
     shape = E, N, K = w.shape
     R, columns = rows.shape
     if columns != shape[width]:
         _shape(rows, name, (R, shape[width]))
-    if offsets.shape[0] != E + 1:
-        _shape(offsets, "offsets", (E + 1,))
+    if offsets is not _NO_OFFSETS:
+        _need(offsets, "offsets", torch.int32, 1, dev)
+        if offsets.shape[0] != E + 1:
+            _shape(offsets, "offsets", (E + 1,))
     return dev, R, E, N, K
 
 
@@ -505,6 +513,201 @@ def mp_expert_mlp_bwd(g_y, x, w1, w2, offsets, z, z_exp=None, *, act: str = "swi
             _ptr(z), _ptr(z_exp), _ptr(g_z), _ptr(h), _ptr(g_x), _ptr(g_w1), _ptr(g_b1),
             _ptr(g_w2), _ptr(g_b2), _ptr(status), _stream(dev)))
     return g_x, g_w1, g_w2, g_b1, g_b2
+
+
+# --------------------------------------------------------------------------
+# the whole layer for a few tokens
+# --------------------------------------------------------------------------
+
+def mp_moe_layer_workspace_size(num_tokens: int, num_experts: int, topk: int, width: int,
+                                expert_width: int, out_width: int) -> int:
+    n = _lib.load().mp_moe_layer_workspace_size(num_tokens, num_experts, topk, width,
+                                                expert_width, out_width)
+    if n == 0:
+        raise ValueError("invalid sizes for mp_moe_layer")
+    return int(n)
+
+
+def mp_moe_layer(x, router, w1, w2, topk: int, *, b1=None, b2=None, act: str = "swiglu",
+                 score: str = "softmax", bias=None, n_groups: int = 1, topk_groups: int = 1,
+                 group_top: int = 1, renorm: bool = True, scale: float = 1.0, y=None, idx=None,
+                 weights=None, workspace=None, status=None):
+    """A whole layer for at most MAX_LAYER_TOKENS tokens: x bf16 [T,H], router [E,H] (fp32,
+    bf16 or fp16), w1 bf16 [E,F,H] ([E,2F,H] for geglu and swiglu, gate first), w2 bf16
+    [E,O,F], b1 and b2 bf16 [E,..] or None -> (y bf16 [T,O], idx int32 [T,K], weights fp32
+    [T,K]).  The choice and its arguments are mp_route's on the logits x router^T; y is
+    the weighted sum of the picks' act(x w1[e]^T + b1[e]) w2[e]^T + b2[e].  `workspace`
+    (uint8, of mp_moe_layer_workspace_size bytes) is the call's own while it runs."""
+    lib = _lib.load()
+    dev, T, E, P, H = _products(x, "x", w1, _NO_OFFSETS, 2)
+    _need(w2, "w2", torch.bfloat16, 3, dev)
+    O, F = w2.shape[1], w2.shape[2]
+    _shape(w2, "w2", (E, O, F))
+    a = _named(act, ACTS, "act")
+    if P != F * _parts(act):
+        raise ValueError(f"w1 has {P} columns for the {F} of w2 and act {act}")
+    dt = _token_dtype(router, "router")
+    _need(router, "router", router.dtype, 2, dev)
+    _shape(router, "router", (E, H))
+    K = int(topk)
+    for t, name, shape, dtype in ((b1, "b1", (E, P), torch.bfloat16),
+                                  (b2, "b2", (E, O), torch.bfloat16),
+                                  (bias, "bias", (E,), torch.float32)):
+        if t is not None:
+            _need(t, name, dtype, len(shape), dev)
+            _shape(t, name, shape)
+    n = lib.mp_moe_layer_workspace_size(T, E, K, H, F, O)
+    if workspace is None:
+        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", torch.uint8, 1, dev)
+    outs = []
+    for t, name, shape, dtype in ((y, "y", (T, O), torch.bfloat16), (idx, "idx", (T, K), torch.int32),
+                                  (weights, "weights", (T, K), torch.float32)):
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=dev)
+        else:
+            _need(t, name, dtype, 2, dev)
+            _shape(t, name, shape)
+        outs.append(t)
+    y, idx, weights = outs
+    _opt(status, "status", torch.int32, 1, dev)
+    with _on(dev):
+        _check("mp_moe_layer", lib.mp_moe_layer(
+            _ptr(x), _ptr(router), dt, _ptr(bias), _ptr(w1), _ptr(b1), _ptr(w2), _ptr(b2), T, E, K,
+            H, F, O, a, _named(score, SCORES, "score"), int(n_groups), int(topk_groups),
+            int(group_top), int(bool(renorm)), float(scale), _ptr(idx), _ptr(weights), _ptr(y),
+            _ptr(workspace), workspace.numel(), _ptr(status), _stream(dev)))
+    return y, idx, weights
+
+
+# --------------------------------------------------------------------------
+# the norms before and after a block
+# --------------------------------------------------------------------------
+
+def _rows_of(t, name, like):
+    if t is not None:
+        _need(t, name, like.dtype, 2, like.device)
+        if t.shape != like.shape:
+            _shape(t, name, like.shape)
+
+
+def _channels_of(t, name, like):
+    if t is not None:
+        _need(t, name, like.dtype, 1, like.device)
+        if t.shape[0] != like.shape[1]:
+            _shape(t, name, like.shape[1:])
+
+
+def _gate_form(gate, like):
+    """MP_GATE_* of a gate [H] (a channel's), [T,1] (a token's) or [T,H] (an element's)."""
+    if gate is None:
+        return 0
+    T, H = like.shape
+    _need(gate, "gate", like.dtype, None, like.device)
+    if gate.dim() == 1 and gate.shape[0] == H:
+        return 1
+    if gate.dim() == 2 and gate.shape[0] == T and gate.shape[1] in (1, H):
+        return 3 if gate.shape[1] == H else 2
+    raise ValueError(f"gate must have shape {(H,)}, {(T, 1)} or {(T, H)}, got {tuple(gate.shape)}")
+
+
+def mp_block_norm(x, residual=None, *, post_weight=None, post_bias=None, gate=None,
+                  scale: float = 1.0, pre_weight=None, pre_bias=None, kind: str = "rms",
+                  eps: float = 1e-6, with_stats: bool = False, s=None, y=None, stats=None):
+    """The norm after a block and the one before the next, with gate, residual scale and
+    residual between them: x [T,H] (fp32, bf16 or fp16) -> (s [T,H], y [T,H] or None,
+    stats fp32 [T,4] or None):
+
+        u = norm(x) * post_weight + post_bias  (x without a post_weight)
+        s = residual + scale * gate * u        (x itself if nothing changes it)
+        y = norm(s) * pre_weight + pre_bias    (None without a pre_weight)
+
+    norm is "rms" or "layer"; gate [H], [T,1] or [T,H]; everything of x's type.  s and y
+    may be given, and be x's or residual's own buffer.  `with_stats` keeps what
+    mp_block_norm_bwd needs beside x and s."""
+    dt = _token_dtype(x, "x")
+    _need(x, "x", x.dtype, 2)
+    dev = x.device
+    T, H = x.shape
+    _rows_of(residual, "residual", x)
+    form = _gate_form(gate, x)
+    for t, name in ((post_weight, "post_weight"), (post_bias, "post_bias"),
+                    (pre_weight, "pre_weight"), (pre_bias, "pre_bias")):
+        _channels_of(t, name, x)
+    as_is = s is None and residual is None and post_weight is None and gate is None and scale == 1.0
+    if not as_is and s is None:
+        s = torch.empty_like(x)
+    if y is None and pre_weight is not None:
+        y = torch.empty_like(x)
+    _rows_of(s, "s", x)
+    _rows_of(y, "y", x)
+    if stats is None and with_stats:
+        stats = torch.empty((T, 4), dtype=torch.float32, device=dev)
+    if stats is not None:
+        _need(stats, "stats", torch.float32, 2, dev)
+        _shape(stats, "stats", (T, 4))
+    with _on(dev):
+        _check("mp_block_norm", _lib.load().mp_block_norm(
+            _ptr(x), _ptr(residual), T, H, dt, _named(kind, NORMS, "kind"), float(eps),
+            _ptr(post_weight), _ptr(post_bias), _ptr(gate), form, float(scale), _ptr(pre_weight),
+            _ptr(pre_bias), _ptr(s), _ptr(y), _ptr(stats), _stream(dev)))
+    return (x if as_is else s), y, stats
+
+
+def mp_block_norm_bwd_workspace_size(num_tokens: int, width: int) -> int:
+    n = _lib.load().mp_block_norm_bwd_workspace_size(num_tokens, width)
+    if n == 0:
+        raise ValueError("invalid sizes for mp_block_norm_bwd")
+    return int(n)
+
+
+def mp_block_norm_bwd(g_s, g_y, x, s, stats, *, post_weight=None, post_bias=None, gate=None,
+                      scale: float = 1.0, pre_weight=None, pre_bias=None, kind: str = "rms",
+                      need=(True,) * 7, grad_dtype=None, workspace=None):
+    """Gradients of mp_block_norm at the s and stats that it gave: (g_x, g_residual, g_gate,
+    g_post_weight, g_post_bias, g_pre_weight, g_pre_bias), None where `need` is false or
+    the argument is absent.  g_s (None: zero) and g_y (None without a pre_weight) are
+    those of s and y.  The gradients of what the rows share (weights, biases, a gate [H]) are of
+    `grad_dtype`: x's type, or torch.float32.  Where nothing stands between x and s,
+    g_x and g_residual are one tensor."""
+    like = s if x is None else x
+    dt = _token_dtype(like, "x")
+    _need(like, "x", like.dtype, 2)
+    dev = like.device
+    T, H = like.shape
+    for t, name in ((x, "x"), (s, "s"), (g_s, "g_s"), (g_y, "g_y")):
+        _rows_of(t, name, like)
+    form = _gate_form(gate, like)
+    for t, name in ((post_weight, "post_weight"), (post_bias, "post_bias"),
+                    (pre_weight, "pre_weight"), (pre_bias, "pre_bias")):
+        _channels_of(t, name, like)
+    _need(stats, "stats", torch.float32, 2, dev)
+    _shape(stats, "stats", (T, 4))
+    grad_dtype = like.dtype if grad_dtype is None else grad_dtype
+    if grad_dtype not in (like.dtype, torch.float32):
+        raise TypeError(f"grad_dtype must be {like.dtype} or torch.float32, got {grad_dtype}")
+    same = post_weight is None and gate is None and scale == 1.0
+    g_residual = torch.empty_like(like) if need[1] or (need[0] and same) else None
+    g_x = torch.empty_like(like) if need[0] and not same else None
+    g_gate = None
+    if gate is not None and need[2]:
+        g_gate = torch.empty_like(gate, dtype=grad_dtype if form == 1 else like.dtype)
+    shared = [torch.empty(H, dtype=grad_dtype, device=dev) if t is not None and n else None
+              for t, n in zip((post_weight, post_bias, pre_weight, pre_bias), need[3:])]
+    if workspace is None:
+        if form == 1 and g_gate is not None or any(t is not None for t in shared):
+            workspace = torch.empty(mp_block_norm_bwd_workspace_size(T, H), dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", torch.uint8, 1, dev)
+    with _on(dev):
+        _check("mp_block_norm_bwd", _lib.load().mp_block_norm_bwd(
+            _ptr(g_s), _ptr(g_y), _ptr(x), _ptr(s), _ptr(stats), T, H, dt,
+            _named(kind, NORMS, "kind"), _ptr(post_weight), _ptr(post_bias), _ptr(gate), form,
+            float(scale), _ptr(pre_weight), _ptr(g_x), _ptr(g_residual), _ptr(g_gate),
+            *(_ptr(t) for t in shared), DTYPES[grad_dtype], _ptr(workspace),
+            0 if workspace is None else workspace.numel(), _stream(dev)))
+    return (g_residual if same and need[0] else g_x), (g_residual if need[1] else None), g_gate, *shared
 
 
 # --------------------------------------------------------------------------

@@ -29,13 +29,13 @@ from dataclasses import dataclass
 
 import torch
 
-from . import (mp_build_map, mp_build_map_capacity, mp_expert_mlp, mp_expert_mlp_bwd,
+from . import (mp_block_norm, mp_block_norm_bwd, mp_build_map, mp_build_map_capacity, mp_expert_mlp, mp_expert_mlp_bwd,
                mp_permute, mp_permute_bwd, mp_route, mp_route_bwd,
                mp_sort_chunks_pad, mp_sort_chunks_pad_bwd, mp_topk_softmax,
                mp_topk_softmax_bwd, mp_unpad_restore, mp_unpad_restore_bwd, mp_unpermute,
                mp_unpermute_bwd, mp_unpermute_ep, mp_zero_rows_from)
 
-__all__ = ["Dispatch", "topk_softmax", "route", "permute", "expert_mlp", "unpermute",
+__all__ = ["Dispatch", "block_norm", "topk_softmax", "route", "permute", "expert_mlp", "unpermute",
            "unpermute_ep", "sort_chunks_pad", "unpad_restore"]
 
 
@@ -193,6 +193,39 @@ class _ExpertMlp(torch.autograd.Function):
         return g_x, None, g_w1, g_w2, g_b1, g_b2, None, None, None
 
 
+class _BlockNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, gate, post_weight, post_bias, pre_weight, pre_bias, kind, eps, scale,
+                keep):
+        s, y, stats = mp_block_norm(x, residual, post_weight=post_weight, post_bias=post_bias,
+                                    gate=gate, scale=scale, pre_weight=pre_weight,
+                                    pre_bias=pre_bias, kind=kind, eps=eps, with_stats=keep)
+        ctx.set_materialize_grads(False)
+        ctx.has_stream = s is not x
+        if keep:
+            ctx.save_for_backward(x if post_weight is not None or gate is not None else None,
+                                  s if pre_weight is not None else None, stats, gate, post_weight,
+                                  post_bias, pre_weight, pre_bias)
+            ctx.kind, ctx.scale = kind, scale
+        return (s if ctx.has_stream else None), y
+
+    @staticmethod
+    @_first_order
+    def backward(ctx, g_s, g_y):
+        x, s, stats, gate, post_weight, post_bias, pre_weight, pre_bias = ctx.saved_tensors
+        if g_s is None and g_y is None:
+            return (None,) * 11
+        if pre_weight is not None and g_y is None:
+            g_y = torch.zeros_like(s)
+        if pre_weight is None and g_s is None:
+            g_s = torch.zeros_like(x)
+        g = mp_block_norm_bwd(
+            None if g_s is None else g_s.contiguous(), None if g_y is None else g_y.contiguous(),
+            x, s, stats, post_weight=post_weight, post_bias=post_bias, gate=gate, scale=ctx.scale,
+            pre_weight=pre_weight, pre_bias=pre_bias, kind=ctx.kind, need=ctx.needs_input_grad[:7])
+        return *g, None, None, None, None
+
+
 class _SortChunksPad(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, probs, split_sizes, chunk_order, num_groups, align, out_rows,
@@ -260,6 +293,24 @@ def route(logits: torch.Tensor, topk: int, *, score: str = "softmax", bias=None,
     return _Route.apply(logits, bias, int(topk),
                         dict(n_groups=n_groups, topk_groups=topk_groups, group_top=group_top),
                         dict(score=score, renorm=renorm, scale=scale))
+
+
+def block_norm(x: torch.Tensor, residual=None, *, post_weight=None, post_bias=None, gate=None,
+               scale: float = 1.0, pre_weight=None, pre_bias=None, kind: str = "rms",
+               eps: float = 1e-6):
+    """The norm after a block and the one before the next, with gate, residual scale and
+    residual between them (mp_block_norm): x [T,H] -> (s, y),
+
+        u = norm(x) * post_weight + post_bias  (x without a post_weight)
+        s = residual + scale * gate * u
+        y = norm(s) * pre_weight + pre_bias    (None without a pre_weight)
+
+    differentiable w.r.t. x, residual, gate ([H], [T,1] or [T,H]), weights and biases.
+    For the backward pass x, s and four fp32 values a row are kept."""
+    tensors = (x, residual, gate, post_weight, post_bias, pre_weight, pre_bias)
+    keep = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+    s, y = _BlockNorm.apply(*tensors, kind, float(eps), float(scale), keep)
+    return (x if s is None else s), y
 
 
 def expert_mlp(rows: torch.Tensor, offsets, w1: torch.Tensor, w2: torch.Tensor, b1=None,
