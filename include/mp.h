@@ -446,7 +446,8 @@ mp_status_t mp_moe_layer(const mp_bf16_t *x, const void *router, int32_t router_
  *   stats        device fp32 [T,4] out or NULL, 16-byte aligned: mean and 1/sqrt(...)
  *                of x (0 without a post_weight; mean 0 for rms), the same of s
  * s and y may each be the buffer of x, of residual or of a [T,H] gate.  A row's result
- * depends on nothing but that row.  Limits: H <= MP_MAX_NORM_WIDTH; T < 2^31.
+ * depends on nothing but that row and on whether rows are whole 16-byte vectors on 16-byte
+ * boundaries, which is the faster way.  Limits: H <= MP_MAX_NORM_WIDTH; T < 2^31.
  */
 mp_status_t mp_block_norm(const void *x, const void *residual, int64_t T, int32_t H,
                           int32_t dtype, int32_t kind, float eps, const void *post_weight,
@@ -478,8 +479,9 @@ size_t mp_block_norm_bwd_workspace_size(int64_t T, int32_t H);
  *              dtype or MP_DTYPE_FP32; the rest of type dtype.
  *   workspace  device, >= mp_block_norm_bwd_workspace_size(T,H) bytes, 16-byte
  *              aligned; may be NULL if no gradient of the shape [H] is wanted
- * g_x and g_residual may each be the buffer of one of the [T,H] inputs.  Sums over rows
- * are made in an order that depends on T, H, the types and the device's alone.
+ * g_residual may be the buffer of g_s or g_y, g_x that of any [T,H] input, g_gate the gate's.
+ * Sums over rows are made in an order that depends on the sizes, types, alignment and
+ * device alone.
  */
 mp_status_t mp_block_norm_bwd(const void *g_s, const void *g_y, const void *x, const void *s,
                               const float *stats, int64_t T, int32_t H, int32_t dtype,

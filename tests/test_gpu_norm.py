@@ -130,7 +130,8 @@ def test_in_place(H, into):
 @pytest.mark.parametrize("shift", [1, 2, 3, 4, 6])
 @pytest.mark.parametrize("H", [64, 1001, 4096])
 def test_tensors_that_start_anywhere(H, shift):
-    """Views off 16 bytes, with guards around each result."""
+    """Views off 16 bytes, with guards around each result.  A row's values lie over other threads
+    there, so its sums are added in another order: the bound is that of any order."""
     T, dtype = 70, torch.bfloat16
     t, how = nu.make(T, H, dtype, kind="layer", post=True, gate="element", bias=True, seed=5)
     plain = mp.mp_block_norm(t["x"], t["residual"], with_stats=True, **{k: t[k] for k in nu.NAMES[2:]}, **how)
@@ -144,8 +145,7 @@ def test_tensors_that_start_anywhere(H, shift):
     m = {k: moved(v, shift + i % 3) for i, (k, v) in enumerate(t.items())}
     s, y = moved(t["x"], shift), moved(t["x"], shift + 1)
     got = mp.mp_block_norm(m["x"], m["residual"], with_stats=True, s=s, y=y, **{k: m[k] for k in nu.NAMES[2:]}, **how)
-    for a, b in zip(got, plain):
-        assert torch.equal(a, b)
+    nu.check_forward(t, how, *got)
     for v, off in ((s, shift), (y, shift + 1)):
         base = v._base if v._base is not None else v
         whole = base.flatten()
@@ -153,12 +153,9 @@ def test_tensors_that_start_anywhere(H, shift):
     g_s, g_y = nu.rows(T, H, dtype, 1), nu.rows(T, H, dtype, 2)
     back = dict(how)
     back.pop("eps")
-    want = mp.mp_block_norm_bwd(g_s, g_y, t["x"], plain[0], plain[2], **{k: t[k] for k in nu.NAMES[2:]}, **back)
     got = mp.mp_block_norm_bwd(moved(g_s, shift), moved(g_y, shift + 2), m["x"], moved(plain[0], 1), plain[2],
                                **{k: m[k] for k in nu.NAMES[2:]}, **back)
     nu.check_backward(t, how, g_s, g_y, plain[0], plain[2], got)
-    for a, b in zip(got[:2], want[:2]):
-        assert torch.equal(a, b)
 
 
 def test_no_rows():

@@ -1,0 +1,310 @@
+// What the norms before and after a block and their gradients share: how a row lies
+// over threads, its way through shared memory, and sums over it.
+//
+// Bytes bound these operators: a row is read once, worked on in registers, and written once.
+// W threads own a row, 8 C values each, and a CTA of up to 512 threads works on R rows at a
+// time, each a group of its own with a barrier of its own.  While a group works on a row, its
+// next ones are on their way into shared memory by cp.async, STAGES - 1 of them.
+//   VEC      rows of whole 16-byte vectors on 16-byte boundaries: a thread copies and reads
+//            vectors tid, tid + W, ... of the row, and nobody else's.
+//   not VEC  rows that start anywhere: the group copies the 16-byte granules that hold the
+//            row, and a thread reads values tid, tid + W, ...; a barrier in between.
+//   C 4      rows of more than 8192 values: not staged, 1024 threads read them as they need them.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "tc.cuh"
+
+namespace mp {
+
+constexpr int NORM_SHARED = 5;      // gradients shared by rows: two weights, two biases, the gate
+constexpr int NORM_PARTS = 304;     // partial sums of each: two CTAs on an SM
+constexpr int NORM_THREADS = 512;   // of a CTA, C 4: twice as many
+constexpr int NORM_BUDGET = 112 * 1024;   // shared memory of one of two CTAs on an SM
+constexpr int NORM_MOST = 225 * 1024;     // of one alone
+
+// How T rows of H values are laid out.
+struct NormPlan {
+    int W, R;         // threads a row, rows a CTA at a time
+    int stages, pitch;   // slots of a group, bytes of one tensor's row in a slot
+    size_t smem;
+};
+
+struct NormRows {
+    const void *at;   // [T,H]
+    int64_t end;      // address past its last byte
+};
+
+__device__ __forceinline__ float norm_value(float v) { return v; }
+__device__ __forceinline__ float norm_value(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float norm_value(__half v) { return __half2float(v); }
+__device__ __forceinline__ void norm_put(float *p, float v) { *p = v; }
+__device__ __forceinline__ void norm_put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void norm_put(__half *p, float v) { *p = __float2half_rn(v); }
+
+// The values of a 16-byte vector.
+__device__ __forceinline__ void vec_values(const uint4 &v, float *f, const __nv_bfloat16 *)
+{
+    float t[8];
+    unpack(v, t);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = t[i];
+}
+__device__ __forceinline__ void vec_values(const uint4 &v, float *f, const __half *)
+{
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(u + i));
+        f[2 * i] = t.x;
+        f[2 * i + 1] = t.y;
+    }
+}
+__device__ __forceinline__ void vec_values(const uint4 &v, float *f, const float *)
+{
+    f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
+}
+__device__ __forceinline__ uint4 vec_of(const float *f, const __nv_bfloat16 *)
+{
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+}
+__device__ __forceinline__ uint4 vec_of(const float *f, const __half *)
+{
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+        u[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+}
+__device__ __forceinline__ uint4 vec_of(const float *f, const float *)
+{
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes = 16)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the last `left` groups of this thread have landed.
+__device__ __forceinline__ void cp_wait(int left)
+{
+    switch (left) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    }
+}
+
+// One group's view of its rows.
+template <typename D, bool VEC, int C> struct NormGroup {
+    static constexpr int N = 8 * C;              // values a thread
+    static constexpr int NV = 16 / sizeof(D);    // values a vector
+    static constexpr int VECS = N / NV;
+    static constexpr bool STAGED = C < 4;
+    static constexpr int WARPS = C < 4 ? NORM_THREADS / 32 : 32;
+
+    int W, H, tid, group;
+    float *red;   // [2][WARPS] float4 of this group: see sums()
+    int phase = 0;
+
+    __device__ __forceinline__ void barrier() const
+    {
+        if (W > 32)
+            asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(W) : "memory");
+        else
+            __syncwarp();
+    }
+
+    // The sums over the row, each added up in a fixed order; every thread gets them.  A
+    // warp's lanes first (W <= 32: the W lanes of the row), then the warps.  Two
+    // buffers in turn: a thread that is still reading one is waited for by the barrier
+    // of the next sum.
+    template <int M> __device__ __forceinline__ void sums(float (&v)[M])
+    {
+#pragma unroll
+        for (int d = 16; d; d >>= 1)
+            if (d < W) {
+#pragma unroll
+                for (int i = 0; i < M; ++i) v[i] += __shfl_xor_sync(FULL_MASK, v[i], d);
+            }
+        if (W <= 32) return;
+        float *to = red + (phase & 1) * M_MOST * WARPS;
+        phase ^= 1;
+        if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+            for (int i = 0; i < M; ++i) to[i * WARPS + (tid >> 5)] = v[i];
+        }
+        barrier();
+        const int warps = W >> 5;
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            float t = 0.0f;
+#pragma unroll
+            for (int q = 0; q < WARPS / 4; ++q)
+                if (4 * q < warps) {
+                    const float4 p = reinterpret_cast<const float4 *>(to + i * WARPS)[q];
+                    t += p.x;
+                    if (4 * q + 1 < warps) t += p.y;
+                    if (4 * q + 2 < warps) t += p.z;
+                    if (4 * q + 3 < warps) t += p.w;
+                }
+            v[i] = t;
+        }
+    }
+    static constexpr int M_MOST = 3;
+    static constexpr int RED = 2 * M_MOST * WARPS;   // floats a group
+
+    // Values of a row (or of what is shared by the rows) at `p`, 0 past its end.
+    __device__ __forceinline__ void load(const D *p, float (&f)[N]) const
+    {
+        if (VEC) {
+#pragma unroll
+            for (int v = 0; v < VECS; ++v) {
+                const int at = (v * W + tid) * NV;
+                if (at < H) {
+                    vec_values(*reinterpret_cast<const uint4 *>(p + at), f + v * NV, p);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) f[v * NV + i] = 0.0f;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int at = i * W + tid;
+                f[i] = at < H ? norm_value(p[at]) : 0.0f;
+            }
+        }
+    }
+    template <typename G> __device__ __forceinline__ void store(G *p, const float (&f)[N]) const
+    {
+        if (VEC) {
+            constexpr int GV = 16 / sizeof(G) < NV ? 16 / sizeof(G) : NV;   // fp32 results of 16-bit rows
+#pragma unroll
+            for (int v = 0; v < VECS; ++v) {
+                const int at = (v * W + tid) * NV;
+                if (at < H) {
+#pragma unroll
+                    for (int i = 0; i < NV; i += GV)
+                        *reinterpret_cast<uint4 *>(p + at + i) = vec_of(f + v * NV + i, p);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int at = i * W + tid;
+                if (at < H) norm_put(p + at, f[i]);
+            }
+        }
+    }
+    // Whether value i of this thread lies in the row.
+    __device__ __forceinline__ bool in(int i) const
+    {
+        return (VEC ? (i / NV * W + tid) * NV : i * W + tid) < H;
+    }
+
+    // Starts the copy of row t of `rows` into `slot`.
+    __device__ __forceinline__ void fetch(const NormRows &rows, int64_t t, uint8_t *slot) const
+    {
+        if (!STAGED) return;
+        const char *row = static_cast<const char *>(rows.at) + t * H * static_cast<int64_t>(sizeof(D));
+        const uint32_t to = smem_u32(slot);
+        if (VEC) {
+#pragma unroll
+            for (int v = 0; v < VECS; ++v) {
+                const int at = (v * W + tid) * 16;
+                if (at < H * static_cast<int>(sizeof(D))) cp_async16(to + at, row + at);
+            }
+        } else {
+            const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15u);
+            const int granules = (off + H * static_cast<int>(sizeof(D)) + 15) / 16;
+            for (int q = tid; q < granules; q += W) {
+                const char *src = row - off + q * 16;
+                const int64_t left = rows.end - reinterpret_cast<int64_t>(src);
+                if (src >= static_cast<const char *>(rows.at)) {
+                    cp_async16(to + q * 16, src, left < 16 ? static_cast<int>(left) : 16);
+                } else {   // the granule begins before the tensor: only what is of it is read
+                    for (int i = off; i < 16 && i < off + H * static_cast<int>(sizeof(D)); i += sizeof(D))
+                        *reinterpret_cast<D *>(slot + i) = *reinterpret_cast<const D *>(src + i);
+                }
+            }
+        }
+    }
+    // Where row t of `rows` can be read: in `slot`, or where it is.
+    __device__ __forceinline__ const D *row(const NormRows &rows, int64_t t, const uint8_t *slot) const
+    {
+        const D *at = static_cast<const D *>(rows.at) + t * H;
+        if (!STAGED) return at;
+        return reinterpret_cast<const D *>(slot + (VEC ? 0u : (reinterpret_cast<uintptr_t>(at) & 15u)));
+    }
+};
+
+// Threads a row, rows at a time, and slots for `tensors` staged rows with `extra` bytes a
+// thread beside them.  Two CTAs on an SM wherever two slots or more fit in half of it.
+template <typename D> NormPlan norm_plan(int64_t T, int H, int C, int tensors, int extra, bool narrow)
+{
+    NormPlan p;
+    const int threads = C < 4 ? NORM_THREADS : 2 * NORM_THREADS, need = (H + 8 * C - 1) / (8 * C);
+    p.W = 1;
+    if (need <= 32)
+        while (p.W < need) p.W *= 2;
+    else
+        p.W = (need + 31) / 32 * 32;
+    p.R = C < 4 ? threads / p.W : 1;
+    while (p.R > 1 && p.W * (p.R / 2) >= 32 && (T + p.R / 2 - 1) / (p.R / 2) <= sm_count()) p.R /= 2;   // few rows: spread
+    const int red = 2 * 3 * (threads / 32) * 4;
+    const size_t fixed = static_cast<size_t>(p.W > 32 ? p.R : 1) * red + static_cast<size_t>(p.W) * p.R * extra;
+    p.pitch = (H * static_cast<int>(sizeof(D)) + 15) / 16 * 16 + 16;
+    const size_t slot = static_cast<size_t>(p.pitch) * tensors * p.R;
+    p.stages = 0;
+    if (C < 4) {
+        const size_t room = narrow && fixed + 2 * slot <= NORM_BUDGET ? NORM_BUDGET : NORM_MOST;
+        p.stages = fixed < room ? static_cast<int>((room - fixed) / slot) : 0;
+        if (p.stages > 4) p.stages = 4;
+    }
+    const int64_t steps = (T + p.R - 1) / p.R;
+    if (p.stages > steps) p.stages = static_cast<int>(steps);
+    p.smem = fixed + slot * p.stages;
+    return p;
+}
+
+// The launchers of the types' kernels (norm_fwd.cu, norm_bwd_*.cu).
+struct NormCall {
+    NormRows x, residual, gate_rows, s, g_s, g_y;   // [T,H], `at` NULL where absent
+    const void *post_w, *post_b, *gate, *pre_w, *pre_b;
+    int64_t T;
+    int H, kind, gate_form;
+    float eps, scale;
+    bool vec;                  // every tensor is whole 16-byte vectors
+    void *s_out, *y;
+    float *stats;
+    void *g_x, *g_residual, *g_gate;
+    float *sums[NORM_SHARED];  // [grid,H] or NULL: post_w, post_b, pre_w, pre_b, gate
+    cudaStream_t stream;
+};
+template <typename D> mp_status_t norm_forward(const NormCall &c);
+template <typename D> mp_status_t norm_backward(const NormCall &c, int &parts);
+
+// Launches `kernel` over the rows.  `two`: compiled for two CTAs on an SM.
+template <typename K, typename... A>
+mp_status_t norm_launch(K kernel, std::atomic<uint64_t> &allowed, NormPlan p, bool two, int64_t T, cudaStream_t stream,
+                        int &grid, A... args)
+{
+    if (!allow_smem(kernel, allowed, NORM_MOST)) return MP_ERR_CUDA;
+    const int64_t steps = (T + p.R - 1) / p.R, most = sm_count() * (two && p.smem <= NORM_BUDGET ? 2 : 1);
+    grid = static_cast<int>(steps < most ? steps : most);
+    if (grid > NORM_PARTS) grid = NORM_PARTS;
+    (void)launch_pdl(kernel, grid, p.W * p.R, p.smem, stream, args..., p);
+    return check_launch();
+}
+
+}  // namespace mp

@@ -1,0 +1,317 @@
+// Gradients of the norms before and after a block (mp_block_norm_bwd): see norm.cuh for the
+// layout and mp.h for the formulas.
+//
+// One pass over the rows: x, s and the two gradients are read once, g_x, g_residual and
+// the gate's gradient written once.  Of what the rows share, a thread sums its columns'
+// gradients over its rows in registers (the weights') or in shared memory (biases and a
+// gate a channel, which few calls have); a CTA adds up its groups in order and leaves one
+// partial sum a column, and a second kernel adds those of the CTAs in order, in 64 bits.
+#pragma once
+
+#include "norm.cuh"
+
+namespace mp {
+namespace {
+
+enum { SUM_POST_W, SUM_POST_B, SUM_PRE_W, SUM_PRE_B, SUM_GATE };
+
+struct NormBwdArgs {
+    NormRows rows[5];    // staged, of these that are there: g_s, g_y, s, x, gate
+    int slot[5];         // a row's place in a slot, -1: absent
+    int tensors;
+    const void *post_w, *post_b, *gate, *pre_w;
+    const float *stats;
+    int64_t T;
+    int H, kind, gate_form;
+    float scale;
+    void *g_x, *g_residual, *g_gate;
+    float *sums[NORM_SHARED];
+    int more;            // sums in shared memory
+};
+enum { ROW_G_S, ROW_G_Y, ROW_S, ROW_X, ROW_GATE };
+
+template <typename D, bool VEC, int C, bool POST, bool PRE>
+__global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, C == 1 && !(POST && PRE) ? 2 : 1)
+    k_block_norm_bwd(const NormBwdArgs a, const NormPlan p)
+{
+    typedef NormGroup<D, VEC, C> G;
+    constexpr int N = G::N;
+    extern __shared__ __align__(16) uint8_t smem[];
+    pdl_trigger();
+    pdl_wait();
+    G g;
+    const int H = a.H;
+    g.W = p.W; g.H = H;
+    g.group = threadIdx.x / p.W;
+    g.tid = threadIdx.x - g.group * p.W;
+    g.red = reinterpret_cast<float *>(smem) + (p.W > 32 ? g.group * G::RED : 0);
+    uint8_t *const rings = smem + (p.W > 32 ? p.R : 1) * G::RED * 4;
+    const int slot_bytes = a.tensors * p.pitch;
+    uint8_t *const ring = rings + static_cast<size_t>(g.group) * p.stages * slot_bytes;
+    // Sums beside the weights': [more][R][wide] after the slots; C 4: the partial sums themselves.
+    const int wide = (H + 3) / 4 * 4;
+    float *more[3];
+    {
+        constexpr int which[3] = {SUM_POST_B, SUM_PRE_B, SUM_GATE};
+        float *at = reinterpret_cast<float *>(rings + static_cast<size_t>(p.R) * p.stages * slot_bytes);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            more[i] = nullptr;
+            if (a.sums[which[i]] == nullptr) continue;
+            if (C == 4) {
+                more[i] = a.sums[which[i]] + static_cast<int64_t>(blockIdx.x) * H;
+            } else {
+                more[i] = at + g.group * wide;
+                at += p.R * wide;
+            }
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (g.in(j)) more[i][VEC ? (j / G::NV * p.W + g.tid) * G::NV + j % G::NV : j * p.W + g.tid] = 0.0f;
+        }
+    }
+    const auto add = [&](float *to, const float (&v)[N]) {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (g.in(j)) to[VEC ? (j / G::NV * p.W + g.tid) * G::NV + j % G::NV : j * p.W + g.tid] += v[j];
+    };
+
+    const int64_t step = static_cast<int64_t>(gridDim.x) * p.R, first = static_cast<int64_t>(blockIdx.x) * p.R;
+    const auto fetch = [&](int64_t t, uint8_t *slot) {
+        if (t < a.T) {
+#pragma unroll
+            for (int i = 0; i < 5; ++i)
+                if (a.slot[i] >= 0) g.fetch(a.rows[i], t, slot + a.slot[i] * p.pitch);
+        }
+        cp_commit();
+    };
+    if (G::STAGED)
+        for (int i = 0; i < p.stages; ++i) fetch(first + i * step + g.group, ring + i * slot_bytes);
+
+    const bool layer = a.kind == MP_NORM_LAYER, token = a.gate_form == MP_GATE_TOKEN;
+    const float inv = 1.0f / static_cast<float>(H);
+    float post_sum[POST ? N : 1], pre_sum[PRE ? N : 1];
+#pragma unroll
+    for (int i = 0; i < (POST ? N : 1); ++i) post_sum[i] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < (PRE ? N : 1); ++i) pre_sum[i] = 0.0f;
+
+    // What a row has one of, read one row ahead.
+    const auto stats_of = [&](int64_t t) {
+        return t < a.T ? __ldg(reinterpret_cast<const float4 *>(a.stats) + t) : make_float4(0, 0, 0, 0);
+    };
+    const auto gate_of = [&](int64_t t) {
+        return token && t < a.T ? norm_value(static_cast<const D *>(a.gate)[t]) : 1.0f;
+    };
+    float4 next = stats_of(first + g.group);
+    float next_gate = gate_of(first + g.group);
+    int at = 0;
+    for (int64_t t0 = first; t0 < a.T; t0 += step) {   // the same count for every group
+        const int64_t t = t0 + g.group;
+        const bool there = t < a.T;
+        uint8_t *const slot = ring + at * slot_bytes;
+        const float4 st = next;
+        const float gate = next_gate;
+        next = stats_of(t + step);
+        next_gate = gate_of(t + step);
+        if (G::STAGED) {
+            cp_wait(p.stages - 1);
+            if (!VEC) g.barrier();
+        }
+        const auto load = [&](int which, float (&f)[N]) {
+            if (there && a.slot[which] >= 0) {
+                g.load(g.row(a.rows[which], t, slot + a.slot[which] * p.pitch), f);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) f[i] = 0.0f;
+            }
+        };
+        float total[N];   // the gradient of s
+        if (PRE) {
+            float hat[N], d[N];
+            load(ROW_S, hat);
+            load(ROW_G_Y, d);
+            if (more[1] != nullptr && there) add(more[1], d);
+            float w[N];
+            g.load(static_cast<const D *>(a.pre_w), w);
+            float t2[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                hat[i] = (hat[i] - st.z) * st.w;
+                if (there) pre_sum[PRE ? i : 0] = fmaf(d[i], hat[i], pre_sum[PRE ? i : 0]);
+                d[i] *= w[i];
+                t2[0] = fmaf(d[i], hat[i], t2[0]);
+                t2[1] += d[i];
+            }
+            if (layer) {
+                g.sums(t2);
+            } else {
+                float t1[1] = {t2[0]};
+                g.sums(t1);
+                t2[0] = t1[0];
+                t2[1] = 0.0f;
+            }
+            const float along = t2[0] * inv, flat = t2[1] * inv;
+            load(ROW_G_S, total);
+#pragma unroll
+            for (int i = 0; i < N; ++i) total[i] = fmaf(st.w, d[i] - flat - hat[i] * along, total[i]);
+        } else {
+            load(ROW_G_S, total);
+        }
+        if (a.g_residual != nullptr && there) g.store(static_cast<D *>(a.g_residual) + t * H, total);
+#pragma unroll
+        for (int i = 0; i < N; ++i) total[i] *= a.scale;
+        if (POST || a.gate_form != MP_GATE_NONE) {
+            float hat[N], w[N];
+            load(ROW_X, hat);
+            if (POST) {
+                g.load(static_cast<const D *>(a.post_w), w);
+#pragma unroll
+                for (int i = 0; i < N; ++i) hat[i] = (hat[i] - st.x) * st.y;
+            }
+            float t3[3] = {0.0f, 0.0f, 0.0f};
+            if (a.gate_form != MP_GATE_NONE) {
+                float u[N];
+#pragma unroll
+                for (int i = 0; i < N; ++i) u[i] = POST ? hat[i] * w[i] : hat[i];
+                if (POST && a.post_b != nullptr) {
+                    float b[N];
+                    g.load(static_cast<const D *>(a.post_b), b);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) u[i] += b[i];
+                }
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    u[i] *= total[i];
+                    t3[2] += u[i];
+                }
+                if (more[2] != nullptr && there) add(more[2], u);
+                // The gate is read before its gradient is written, which may take its place.
+                float k[N];
+                if (a.gate_form == MP_GATE_CHANNEL)
+                    g.load(static_cast<const D *>(a.gate), k);
+                else
+                    load(ROW_GATE, k);
+                if (a.gate_form == MP_GATE_ELEMENT && a.g_gate != nullptr && there)
+                    g.store(static_cast<D *>(a.g_gate) + t * H, u);
+#pragma unroll
+                for (int i = 0; i < N; ++i) total[i] *= token ? gate : k[i];
+            }
+            if (POST) {
+                if (more[0] != nullptr && there) add(more[0], total);
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    if (there) post_sum[POST ? i : 0] = fmaf(total[i], hat[i], post_sum[POST ? i : 0]);
+                    total[i] *= w[i];
+                    t3[0] = fmaf(total[i], hat[i], t3[0]);
+                    t3[1] += total[i];
+                }
+            }
+            if (layer || token) {
+                g.sums(t3);
+            } else if (POST) {
+                float t1[1] = {t3[0]};
+                g.sums(t1);
+                t3[0] = t1[0];
+            }
+            if (token && a.g_gate != nullptr && g.tid == 0 && there) norm_put(static_cast<D *>(a.g_gate) + t, t3[2]);
+            if (POST) {
+                const float along = t3[0] * inv, flat = layer ? t3[1] * inv : 0.0f;
+#pragma unroll
+                for (int i = 0; i < N; ++i) total[i] = st.y * (total[i] - flat - hat[i] * along);
+            }
+        }
+        if (a.g_x != nullptr && there) g.store(static_cast<D *>(a.g_x) + t * H, total);
+        if (G::STAGED) {
+            if (!VEC) g.barrier();   // everyone has read the slot
+            fetch(t + p.stages * step, slot);
+            at = at + 1 == p.stages ? 0 : at + 1;
+        }
+    }
+    if (G::STAGED) cp_wait(0);
+
+    // The groups' sums, in their order, into this CTA's partial sums.  The slots are free now.
+    float *const stack = reinterpret_cast<float *>(rings);
+    const int low = threadIdx.x & 31;
+    const int piles = p.W < 32 ? (p.W * p.R + 31) / 32 : p.R, pile = p.W < 32 ? threadIdx.x >> 5 : g.group;
+    const auto pile_up = [&](float *sums, float *v, const float *in_shared) {
+        if (sums == nullptr) return;
+        float *const to = sums + static_cast<int64_t>(blockIdx.x) * H;
+        if (C == 4) {
+            if (v != nullptr)
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if (g.in(j)) to[VEC ? (j / G::NV * p.W + g.tid) * G::NV + j % G::NV : j * p.W + g.tid] = v[j];
+            return;
+        }
+        __syncthreads();
+        const float *from = in_shared;
+        int count = p.R;
+        if (v != nullptr) {
+            for (int d = p.W; d < 32; d *= 2)
+#pragma unroll
+                for (int j = 0; j < N; ++j) v[j] += __shfl_xor_sync(FULL_MASK, v[j], d);
+            if (p.W >= 32 || low < p.W) {
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if (g.in(j))
+                        stack[pile * wide + (VEC ? (j / G::NV * p.W + g.tid) * G::NV + j % G::NV : j * p.W + g.tid)] = v[j];
+            }
+            __syncthreads();
+            from = stack;
+            count = piles;
+        }
+        for (int c = threadIdx.x; c < H; c += blockDim.x) {
+            float s = 0.0f;
+            for (int i = 0; i < count; ++i) s += from[i * wide + c];
+            to[c] = s;
+        }
+    };
+    if (POST) pile_up(a.sums[SUM_POST_W], post_sum, nullptr);
+    if (PRE) pile_up(a.sums[SUM_PRE_W], pre_sum, nullptr);
+    const float *const shared0 = reinterpret_cast<const float *>(rings + static_cast<size_t>(p.R) * p.stages * slot_bytes);
+    const float *from = shared0;
+    pile_up(a.sums[SUM_POST_B], nullptr, from);
+    if (a.sums[SUM_POST_B] != nullptr) from += p.R * wide;
+    pile_up(a.sums[SUM_PRE_B], nullptr, from);
+    if (a.sums[SUM_PRE_B] != nullptr) from += p.R * wide;
+    pile_up(a.sums[SUM_GATE], nullptr, from);
+}
+
+template <typename D, bool VEC, int C, bool POST, bool PRE> mp_status_t run(const NormCall &c, int &parts)
+{
+    static std::atomic<uint64_t> allowed{0};
+    constexpr bool two = C == 1 && !(POST && PRE);
+    NormBwdArgs a = {};
+    const bool with_x = POST || c.gate_form != MP_GATE_NONE;
+    const NormRows rows[5] = {c.g_s, c.g_y, c.s, c.x, c.gate_rows};
+    const bool there[5] = {c.g_s.at != nullptr, PRE, PRE, with_x, c.gate_rows.at != nullptr};
+    for (int i = 0; i < 5; ++i) {
+        a.rows[i] = rows[i];
+        a.slot[i] = there[i] ? a.tensors++ : -1;
+    }
+    a.post_w = c.post_w; a.post_b = c.post_b; a.gate = c.gate; a.pre_w = c.pre_w;
+    a.stats = c.stats; a.T = c.T; a.H = c.H; a.kind = c.kind; a.gate_form = c.gate_form; a.scale = c.scale;
+    a.g_x = c.g_x; a.g_residual = c.g_residual; a.g_gate = c.g_gate;
+    for (int i = 0; i < NORM_SHARED; ++i) a.sums[i] = c.sums[i];
+    a.more = (c.sums[SUM_POST_B] != nullptr) + (c.sums[SUM_PRE_B] != nullptr) + (c.sums[SUM_GATE] != nullptr);
+    const NormPlan p = norm_plan<D>(c.T, c.H, C, a.tensors, C < 4 ? a.more * 8 * C * 4 : 0, two);
+    if (C < 4 && p.stages < 1) return run<D, VEC, 4, POST, PRE>(c, parts);   // fp32 rows and several sums beside them
+    return norm_launch(k_block_norm_bwd<D, VEC, C, POST, PRE>, allowed, p, two, c.T, c.stream, parts, a);
+}
+
+template <typename D, bool VEC, int C> mp_status_t by_norms(const NormCall &c, int &parts)
+{
+    if (c.post_w == nullptr) return run<D, VEC, C, false, true>(c, parts);
+    return c.pre_w == nullptr ? run<D, VEC, C, true, false>(c, parts) : run<D, VEC, C, true, true>(c, parts);
+}
+
+}  // namespace
+
+template <typename D> mp_status_t norm_backward(const NormCall &c, int &parts)
+{
+    if (c.H <= 8 * NORM_THREADS) return c.vec ? by_norms<D, true, 1>(c, parts) : by_norms<D, false, 1>(c, parts);
+    if (c.H <= 16 * NORM_THREADS) return c.vec ? by_norms<D, true, 2>(c, parts) : by_norms<D, false, 2>(c, parts);
+    return c.vec ? by_norms<D, true, 4>(c, parts) : by_norms<D, false, 4>(c, parts);
+}
+
+}  // namespace mp
