@@ -2,9 +2,11 @@
 // over threads, its way through shared memory, and sums over it.
 //
 // Bytes bound these operators: a row is read once, worked on in registers, and written once.
-// W threads own a row, 8 C values each, and a CTA of up to 512 threads works on R rows at a
+// W threads own a row, 16 values each, and a CTA of up to 512 threads works on R rows at a
 // time, each a group of its own with a barrier of its own.  While a group works on a row, its
-// next ones are on their way into shared memory by cp.async, STAGES - 1 of them.
+// next ones are on their way into shared memory by cp.async, STAGES of them in all.  What
+// counts next is instructions: 8 values a thread took 81 a value (two norms, 4,096 wide: 188
+// us, the issue slots 81% full); hence 16, and arithmetic on pairs of fp32 (fma.rn.f32x2).
 //   VEC      rows of whole 16-byte vectors on 16-byte boundaries: a thread copies and reads
 //            vectors tid, tid + W, ... of the row, and nobody else's.
 //   not VEC  rows that start anywhere: the group copies the 16-byte granules that hold the
@@ -25,6 +27,7 @@ constexpr int NORM_PARTS = 304;     // partial sums of each: two CTAs on an SM
 constexpr int NORM_THREADS = 512;   // of a CTA, C 4: twice as many
 constexpr int NORM_BUDGET = 112 * 1024;   // shared memory of one of two CTAs on an SM
 constexpr int NORM_MOST = 225 * 1024;     // of one alone
+// What a barrier of a group costs is hidden by the other groups of the SM.
 
 // How T rows of H values are laid out.
 struct NormPlan {
@@ -45,47 +48,84 @@ __device__ __forceinline__ void norm_put(float *p, float v) { *p = v; }
 __device__ __forceinline__ void norm_put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void norm_put(__half *p, float v) { *p = __float2half_rn(v); }
 
-// The values of a 16-byte vector.
-__device__ __forceinline__ void vec_values(const uint4 &v, float *f, const __nv_bfloat16 *)
+// Two fp32 values in a register pair, and arithmetic on both at once.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pair(float a, float b)
 {
-    float t[8];
-    unpack(v, t);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = t[i];
+    f2 v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+    return v;
 }
-__device__ __forceinline__ void vec_values(const uint4 &v, float *f, const __half *)
+__device__ __forceinline__ float2 both(f2 v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c)
+{
+    f2 v;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+    return v;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b)
+{
+    f2 v;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b)
+{
+    f2 v;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+__device__ __forceinline__ float sum2(f2 v)
+{
+    const float2 r = both(v);
+    return r.x + r.y;
+}
+
+// The values of a 16-byte vector, in pairs.
+__device__ __forceinline__ void vec_values(const uint4 &v, f2 *f, const __nv_bfloat16 *)
+{
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = pair(bf16_lo(u[i]), bf16_hi(u[i]));
+}
+__device__ __forceinline__ void vec_values(const uint4 &v, f2 *f, const __half *)
 {
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(u + i));
-        f[2 * i] = t.x;
-        f[2 * i + 1] = t.y;
+        f[i] = pair(t.x, t.y);
     }
 }
-__device__ __forceinline__ void vec_values(const uint4 &v, float *f, const float *)
+__device__ __forceinline__ void vec_values(const uint4 &v, f2 *f, const float *)
 {
-    f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y);
-    f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
+    f[0] = pair(__uint_as_float(v.x), __uint_as_float(v.y));
+    f[1] = pair(__uint_as_float(v.z), __uint_as_float(v.w));
 }
-__device__ __forceinline__ uint4 vec_of(const float *f, const __nv_bfloat16 *)
+__device__ __forceinline__ uint32_t two_of(f2 v, const __nv_bfloat16 *)
 {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                      pack_bf16x2(f[6], f[7]));
+    const float2 r = both(v);
+    return pack_bf16x2(r.x, r.y);
 }
-__device__ __forceinline__ uint4 vec_of(const float *f, const __half *)
+__device__ __forceinline__ uint32_t two_of(f2 v, const __half *)
 {
-    uint32_t u[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-        u[i] = *reinterpret_cast<const uint32_t *>(&h);
-    }
-    return make_uint4(u[0], u[1], u[2], u[3]);
+    const float2 r = both(v);
+    const __half2 h = __floats2half2_rn(r.x, r.y);
+    return *reinterpret_cast<const uint32_t *>(&h);
 }
-__device__ __forceinline__ uint4 vec_of(const float *f, const float *)
+template <typename D> __device__ __forceinline__ uint4 vec_of(const f2 *f, const D *p)
 {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    return make_uint4(two_of(f[0], p), two_of(f[1], p), two_of(f[2], p), two_of(f[3], p));
+}
+__device__ __forceinline__ uint4 vec_of(const f2 *f, const float *)
+{
+    const float2 a = both(f[0]), b = both(f[1]);
+    return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes = 16)
@@ -104,9 +144,9 @@ __device__ __forceinline__ void cp_wait(int left)
     }
 }
 
-// One group's view of its rows.
+// One group's view of its rows: N values a thread, in N2 pairs.
 template <typename D, bool VEC, int C> struct NormGroup {
-    static constexpr int N = 8 * C;              // values a thread
+    static constexpr int N = 8 * C, N2 = 4 * C;
     static constexpr int NV = 16 / sizeof(D);    // values a vector
     static constexpr int VECS = N / NV;
     static constexpr bool STAGED = C < 4;
@@ -150,73 +190,89 @@ template <typename D, bool VEC, int C> struct NormGroup {
             float t = 0.0f;
 #pragma unroll
             for (int q = 0; q < WARPS / 4; ++q)
-                if (4 * q < warps) {
+                if (4 * q < warps) {   // slots past the last warp hold 0
                     const float4 p = reinterpret_cast<const float4 *>(to + i * WARPS)[q];
-                    t += p.x;
-                    if (4 * q + 1 < warps) t += p.y;
-                    if (4 * q + 2 < warps) t += p.z;
-                    if (4 * q + 3 < warps) t += p.w;
+                    t += (p.x + p.y) + (p.z + p.w);
                 }
             v[i] = t;
         }
     }
     static constexpr int M_MOST = 3;
     static constexpr int RED = 2 * M_MOST * WARPS;   // floats a group
+    __device__ __forceinline__ void clear_sums() const
+    {
+        if (W > 32)
+            for (int i = tid; i < RED; i += W) red[i] = 0.0f;   // before the group's first barrier
+    }
+
+    // Column of pair i; the second of the pair is `beside` further on.
+    __device__ __forceinline__ int col(int i) const
+    {
+        return VEC ? (2 * i / NV * W + tid) * NV + 2 * i % NV : 2 * i * W + tid;
+    }
+    __device__ __forceinline__ int beside() const { return VEC ? 1 : W; }
 
     // Values of a row (or of what is shared by the rows) at `p`, 0 past its end.
-    __device__ __forceinline__ void load(const D *p, float (&f)[N]) const
+    __device__ __forceinline__ void load(const D *p, f2 (&f)[N2]) const
     {
         if (VEC) {
 #pragma unroll
             for (int v = 0; v < VECS; ++v) {
                 const int at = (v * W + tid) * NV;
-                if (at < H) {
-                    vec_values(*reinterpret_cast<const uint4 *>(p + at), f + v * NV, p);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < NV; ++i) f[v * NV + i] = 0.0f;
-                }
+                uint4 u = make_uint4(0, 0, 0, 0);
+                if (at < H) u = *reinterpret_cast<const uint4 *>(p + at);
+                vec_values(u, f + v * (NV / 2), p);
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int at = i * W + tid;
-                f[i] = at < H ? norm_value(p[at]) : 0.0f;
+            for (int i = 0; i < N2; ++i) {
+                const int at = col(i), next = at + W;
+                f[i] = pair(at < H ? norm_value(p[at]) : 0.0f, next < H ? norm_value(p[next]) : 0.0f);
             }
         }
     }
-    template <typename G> __device__ __forceinline__ void store(G *p, const float (&f)[N]) const
+    __device__ __forceinline__ void store(D *p, const f2 (&f)[N2]) const
     {
         if (VEC) {
-            constexpr int GV = 16 / sizeof(G) < NV ? 16 / sizeof(G) : NV;   // fp32 results of 16-bit rows
 #pragma unroll
             for (int v = 0; v < VECS; ++v) {
                 const int at = (v * W + tid) * NV;
-                if (at < H) {
-#pragma unroll
-                    for (int i = 0; i < NV; i += GV)
-                        *reinterpret_cast<uint4 *>(p + at + i) = vec_of(f + v * NV + i, p);
-                }
+                if (at < H) *reinterpret_cast<uint4 *>(p + at) = vec_of(f + v * (NV / 2), p);
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int at = i * W + tid;
-                if (at < H) norm_put(p + at, f[i]);
+            for (int i = 0; i < N2; ++i) {
+                const int at = col(i), next = at + W;
+                const float2 r = both(f[i]);
+                if (at < H) norm_put(p + at, r.x);
+                if (next < H) norm_put(p + next, r.y);
             }
         }
     }
-    // Whether value i of this thread lies in the row.
-    __device__ __forceinline__ bool in(int i) const
+    // fp32 sums a column: set, or added to.
+    template <bool ADD> __device__ __forceinline__ void columns(float *p, const f2 (&f)[N2]) const
     {
-        return (VEC ? (i / NV * W + tid) * NV : i * W + tid) < H;
+#pragma unroll
+        for (int i = 0; i < N2; ++i) {
+            const int at = col(i), next = at + beside();
+            const float2 r = both(f[i]);
+            if (at < H) p[at] = ADD ? p[at] + r.x : r.x;
+            if (next < H) p[next] = ADD ? p[next] + r.y : r.y;
+        }
+    }
+    // Pair i with 0 in the place of what is past the row's end.
+    __device__ __forceinline__ f2 inside(int i, f2 v) const
+    {
+        if (VEC) return col(i) < H ? v : 0ull;
+        const float2 r = both(v);
+        return pair(col(i) < H ? r.x : 0.0f, col(i) + W < H ? r.y : 0.0f);
     }
 
     // Starts the copy of row t of `rows` into `slot`.
     __device__ __forceinline__ void fetch(const NormRows &rows, int64_t t, uint8_t *slot) const
     {
         if (!STAGED) return;
-        const char *row = static_cast<const char *>(rows.at) + t * H * static_cast<int64_t>(sizeof(D));
+        const char *row = static_cast<const char *>(rows.at) + t * (H * static_cast<int64_t>(sizeof(D)));
         const uint32_t to = smem_u32(slot);
         if (VEC) {
 #pragma unroll
@@ -248,9 +304,12 @@ template <typename D, bool VEC, int C> struct NormGroup {
     }
 };
 
-// Threads a row, rows at a time, and slots for `tensors` staged rows with `extra` bytes a
-// thread beside them.  Two CTAs on an SM wherever two slots or more fit in half of it.
-template <typename D> NormPlan norm_plan(int64_t T, int H, int C, int tensors, int extra, bool narrow)
+// Columns of a group's fp32 sums, to whole 16 bytes.
+__host__ __device__ inline int norm_wide(int H) { return (H + 3) / 4 * 4; }
+
+// Threads a row, rows at a time, and slots for `tensors` staged rows; `held` vectors that the
+// rows share lie beside them, and `sums` fp32 sums a column of each group.  Two CTAs on an SM wherever two slots or more fit in half of it.
+template <typename D> NormPlan norm_plan(int64_t T, int H, int C, int tensors, int held, int sums, bool narrow)
 {
     NormPlan p;
     const int threads = C < 4 ? NORM_THREADS : 2 * NORM_THREADS, need = (H + 8 * C - 1) / (8 * C);
@@ -262,8 +321,9 @@ template <typename D> NormPlan norm_plan(int64_t T, int H, int C, int tensors, i
     p.R = C < 4 ? threads / p.W : 1;
     while (p.R > 1 && p.W * (p.R / 2) >= 32 && (T + p.R / 2 - 1) / (p.R / 2) <= sm_count()) p.R /= 2;   // few rows: spread
     const int red = 2 * 3 * (threads / 32) * 4;
-    const size_t fixed = static_cast<size_t>(p.W > 32 ? p.R : 1) * red + static_cast<size_t>(p.W) * p.R * extra;
     p.pitch = (H * static_cast<int>(sizeof(D)) + 15) / 16 * 16 + 16;
+    const int64_t extra = C < 4 ? static_cast<int64_t>(held) * p.pitch + static_cast<int64_t>(sums) * p.R * norm_wide(H) * 4 : 0;
+    const size_t fixed = static_cast<size_t>(p.W > 32 ? p.R : 1) * red + static_cast<size_t>(extra);
     const size_t slot = static_cast<size_t>(p.pitch) * tensors * p.R;
     p.stages = 0;
     if (C < 4) {

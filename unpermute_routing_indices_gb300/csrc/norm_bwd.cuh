@@ -26,16 +26,15 @@ struct NormBwdArgs {
     float scale;
     void *g_x, *g_residual, *g_gate;
     float *sums[NORM_SHARED];
-    int more;            // sums in shared memory
 };
 enum { ROW_G_S, ROW_G_Y, ROW_S, ROW_X, ROW_GATE };
 
 template <typename D, bool VEC, int C, bool POST, bool PRE>
-__global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, C == 1 && !(POST && PRE) ? 2 : 1)
+__global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, 1)
     k_block_norm_bwd(const NormBwdArgs a, const NormPlan p)
 {
     typedef NormGroup<D, VEC, C> G;
-    constexpr int N = G::N;
+    constexpr int N2 = G::N2;
     extern __shared__ __align__(16) uint8_t smem[];
     pdl_trigger();
     pdl_wait();
@@ -45,35 +44,46 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, C == 
     g.group = threadIdx.x / p.W;
     g.tid = threadIdx.x - g.group * p.W;
     g.red = reinterpret_cast<float *>(smem) + (p.W > 32 ? g.group * G::RED : 0);
+    g.clear_sums();
     uint8_t *const rings = smem + (p.W > 32 ? p.R : 1) * G::RED * 4;
     const int slot_bytes = a.tensors * p.pitch;
     uint8_t *const ring = rings + static_cast<size_t>(g.group) * p.stages * slot_bytes;
-    // Sums beside the weights': [more][R][wide] after the slots; C 4: the partial sums themselves.
-    const int wide = (H + 3) / 4 * 4;
+    // What the rows share, behind the slots.
+    uint8_t *held = rings + static_cast<size_t>(p.R) * p.stages * slot_bytes;
+    const auto hold = [&](const void *v) {
+        const D *from = static_cast<const D *>(v);
+        if (v == nullptr || !G::STAGED) return from;
+        D *const to = reinterpret_cast<D *>(held);
+        held += p.pitch;
+        for (int c = threadIdx.x; c < H; c += blockDim.x) to[c] = from[c];
+        return static_cast<const D *>(to);
+    };
+    const D *const post_w = hold(POST ? a.post_w : nullptr), *const pre_w = hold(PRE ? a.pre_w : nullptr);
+    const D *const post_b = hold(a.post_b);
+    const D *const channel = hold(a.gate_form == MP_GATE_CHANNEL ? a.gate : nullptr);
+    // Sums beside the weights', [R,wide] each; C 4: the partial sums themselves.
+    const int wide = norm_wide(H);
     float *more[3];
+    const float *const more_at = reinterpret_cast<const float *>(held);
     {
         constexpr int which[3] = {SUM_POST_B, SUM_PRE_B, SUM_GATE};
-        float *at = reinterpret_cast<float *>(rings + static_cast<size_t>(p.R) * p.stages * slot_bytes);
+        float *at = reinterpret_cast<float *>(held);
+        f2 zero[N2];
+#pragma unroll
+        for (int i = 0; i < N2; ++i) zero[i] = 0ull;
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
             more[i] = nullptr;
             if (a.sums[which[i]] == nullptr) continue;
-            if (C == 4) {
+            if (!G::STAGED) {
                 more[i] = a.sums[which[i]] + static_cast<int64_t>(blockIdx.x) * H;
             } else {
                 more[i] = at + g.group * wide;
                 at += p.R * wide;
             }
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-                if (g.in(j)) more[i][VEC ? (j / G::NV * p.W + g.tid) * G::NV + j % G::NV : j * p.W + g.tid] = 0.0f;
+            g.template columns<false>(more[i], zero);
         }
     }
-    const auto add = [&](float *to, const float (&v)[N]) {
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            if (g.in(j)) to[VEC ? (j / G::NV * p.W + g.tid) * G::NV + j % G::NV : j * p.W + g.tid] += v[j];
-    };
 
     const int64_t step = static_cast<int64_t>(gridDim.x) * p.R, first = static_cast<int64_t>(blockIdx.x) * p.R;
     const auto fetch = [&](int64_t t, uint8_t *slot) {
@@ -89,11 +99,9 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, C == 
 
     const bool layer = a.kind == MP_NORM_LAYER, token = a.gate_form == MP_GATE_TOKEN;
     const float inv = 1.0f / static_cast<float>(H);
-    float post_sum[POST ? N : 1], pre_sum[PRE ? N : 1];
+    f2 post_sum[N2], pre_sum[N2];
 #pragma unroll
-    for (int i = 0; i < (POST ? N : 1); ++i) post_sum[i] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < (PRE ? N : 1); ++i) pre_sum[i] = 0.0f;
+    for (int i = 0; i < N2; ++i) post_sum[i] = pre_sum[i] = 0ull;
 
     // What a row has one of, read one row ahead.
     const auto stats_of = [&](int64_t t) {
@@ -104,10 +112,12 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, C == 
     };
     float4 next = stats_of(first + g.group);
     float next_gate = gate_of(first + g.group);
+    __syncthreads();
     int at = 0;
     for (int64_t t0 = first; t0 < a.T; t0 += step) {   // the same count for every group
         const int64_t t = t0 + g.group;
         const bool there = t < a.T;
+        const int64_t row = t * H;
         uint8_t *const slot = ring + at * slot_bytes;
         const float4 st = next;
         const float gate = next_gate;
@@ -117,94 +127,119 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, C == 
             cp_wait(p.stages - 1);
             if (!VEC) g.barrier();
         }
-        const auto load = [&](int which, float (&f)[N]) {
-            if (there && a.slot[which] >= 0) {
-                g.load(g.row(a.rows[which], t, slot + a.slot[which] * p.pitch), f);
-            } else {
+        const auto load = [&](int which, f2 (&f)[N2]) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) f[i] = 0.0f;
-            }
+            for (int i = 0; i < N2; ++i) f[i] = 0ull;
+            if (there && a.slot[which] >= 0) g.load(g.row(a.rows[which], t, slot + a.slot[which] * p.pitch), f);
         };
-        float total[N];   // the gradient of s
+        // (v - mean) rstd
+        const auto standard = [&](f2 (&v)[N2], float mean, float rstd) {
+            const f2 off = pair(-mean, -mean), r = pair(rstd, rstd);
+            if (layer) {
+#pragma unroll
+                for (int i = 0; i < N2; ++i) v[i] = add2(v[i], off);
+            }
+#pragma unroll
+            for (int i = 0; i < N2; ++i) v[i] = mul2(v[i], r);
+        };
+        f2 total[N2];   // the gradient of s
         if (PRE) {
-            float hat[N], d[N];
+            f2 hat[N2], d[N2];
             load(ROW_S, hat);
             load(ROW_G_Y, d);
-            if (more[1] != nullptr && there) add(more[1], d);
-            float w[N];
-            g.load(static_cast<const D *>(a.pre_w), w);
-            float t2[2] = {0.0f, 0.0f};
+            if (more[1] != nullptr && there) g.template columns<true>(more[1], d);
+            standard(hat, st.z, st.w);
+            f2 w[N2];
+            g.load(pre_w, w);
+            f2 along2 = 0ull, flat2 = 0ull;
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                hat[i] = (hat[i] - st.z) * st.w;
-                if (there) pre_sum[PRE ? i : 0] = fmaf(d[i], hat[i], pre_sum[PRE ? i : 0]);
-                d[i] *= w[i];
-                t2[0] = fmaf(d[i], hat[i], t2[0]);
-                t2[1] += d[i];
+            for (int i = 0; i < N2; ++i) {   // rows that are not there are 0
+                pre_sum[i] = fma2(d[i], hat[i], pre_sum[i]);
+                d[i] = mul2(d[i], w[i]);
+                along2 = fma2(d[i], hat[i], along2);
             }
+            float t2[2] = {sum2(along2), 0.0f};
             if (layer) {
+#pragma unroll
+                for (int i = 0; i < N2; ++i) flat2 = add2(flat2, d[i]);
+                t2[1] = sum2(flat2);
                 g.sums(t2);
             } else {
                 float t1[1] = {t2[0]};
                 g.sums(t1);
                 t2[0] = t1[0];
-                t2[1] = 0.0f;
             }
-            const float along = t2[0] * inv, flat = t2[1] * inv;
+            // total = g_s + rstd (d - flat - hat along)
+            const float along = -t2[0] * inv, flat = -t2[1] * inv;
+            const f2 m = pair(along, along), f = pair(flat, flat), r = pair(st.w, st.w);
             load(ROW_G_S, total);
+            if (layer) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) total[i] = fmaf(st.w, d[i] - flat - hat[i] * along, total[i]);
+                for (int i = 0; i < N2; ++i) d[i] = add2(d[i], f);
+            }
+#pragma unroll
+            for (int i = 0; i < N2; ++i) total[i] = fma2(r, fma2(hat[i], m, d[i]), total[i]);
         } else {
             load(ROW_G_S, total);
         }
-        if (a.g_residual != nullptr && there) g.store(static_cast<D *>(a.g_residual) + t * H, total);
+        if (a.g_residual != nullptr && there) g.store(static_cast<D *>(a.g_residual) + row, total);
+        if (POST || a.gate_form != MP_GATE_NONE || a.scale != 1.0f) {
+            const f2 by = pair(a.scale, a.scale);
 #pragma unroll
-        for (int i = 0; i < N; ++i) total[i] *= a.scale;
+            for (int i = 0; i < N2; ++i) total[i] = mul2(total[i], by);
+        }
         if (POST || a.gate_form != MP_GATE_NONE) {
-            float hat[N], w[N];
+            f2 hat[N2], w[N2];
             load(ROW_X, hat);
             if (POST) {
-                g.load(static_cast<const D *>(a.post_w), w);
-#pragma unroll
-                for (int i = 0; i < N; ++i) hat[i] = (hat[i] - st.x) * st.y;
+                g.load(post_w, w);
+                standard(hat, st.x, st.y);
             }
             float t3[3] = {0.0f, 0.0f, 0.0f};
             if (a.gate_form != MP_GATE_NONE) {
-                float u[N];
+                f2 u[N2], k[N2];
+                if (POST && post_b != nullptr) {
+                    g.load(post_b, k);
 #pragma unroll
-                for (int i = 0; i < N; ++i) u[i] = POST ? hat[i] * w[i] : hat[i];
-                if (POST && a.post_b != nullptr) {
-                    float b[N];
-                    g.load(static_cast<const D *>(a.post_b), b);
+                    for (int i = 0; i < N2; ++i) u[i] = fma2(hat[i], w[i], k[i]);
+                } else {
 #pragma unroll
-                    for (int i = 0; i < N; ++i) u[i] += b[i];
+                    for (int i = 0; i < N2; ++i) u[i] = POST ? mul2(hat[i], w[i]) : hat[i];
                 }
+                f2 gate2 = 0ull;
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    u[i] *= total[i];
-                    t3[2] += u[i];
+                for (int i = 0; i < N2; ++i) {
+                    u[i] = mul2(u[i], total[i]);
+                    gate2 = add2(gate2, u[i]);
                 }
-                if (more[2] != nullptr && there) add(more[2], u);
+                t3[2] = sum2(gate2);
+                if (more[2] != nullptr && there) g.template columns<true>(more[2], u);
                 // The gate is read before its gradient is written, which may take its place.
-                float k[N];
-                if (a.gate_form == MP_GATE_CHANNEL)
-                    g.load(static_cast<const D *>(a.gate), k);
-                else
-                    load(ROW_GATE, k);
-                if (a.gate_form == MP_GATE_ELEMENT && a.g_gate != nullptr && there)
-                    g.store(static_cast<D *>(a.g_gate) + t * H, u);
+                if (token) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) total[i] *= token ? gate : k[i];
+                    for (int i = 0; i < N2; ++i) k[i] = pair(gate, gate);
+                } else if (channel != nullptr) {
+                    g.load(channel, k);
+                } else {
+                    load(ROW_GATE, k);
+                }
+                if (a.gate_form == MP_GATE_ELEMENT && a.g_gate != nullptr && there)
+                    g.store(static_cast<D *>(a.g_gate) + row, u);
+#pragma unroll
+                for (int i = 0; i < N2; ++i) total[i] = mul2(total[i], k[i]);
             }
             if (POST) {
-                if (more[0] != nullptr && there) add(more[0], total);
+                if (more[0] != nullptr && there) g.template columns<true>(more[0], total);
+                f2 along2 = 0ull, flat2 = 0ull;
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    if (there) post_sum[POST ? i : 0] = fmaf(total[i], hat[i], post_sum[POST ? i : 0]);
-                    total[i] *= w[i];
-                    t3[0] = fmaf(total[i], hat[i], t3[0]);
-                    t3[1] += total[i];
+                for (int i = 0; i < N2; ++i) {
+                    post_sum[i] = fma2(total[i], hat[i], post_sum[i]);
+                    total[i] = mul2(total[i], w[i]);
+                    along2 = fma2(total[i], hat[i], along2);
+                    flat2 = add2(flat2, total[i]);
                 }
+                t3[0] = sum2(along2);
+                t3[1] = sum2(flat2);
             }
             if (layer || token) {
                 g.sums(t3);
@@ -215,12 +250,17 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, C == 
             }
             if (token && a.g_gate != nullptr && g.tid == 0 && there) norm_put(static_cast<D *>(a.g_gate) + t, t3[2]);
             if (POST) {
-                const float along = t3[0] * inv, flat = layer ? t3[1] * inv : 0.0f;
+                const float along = -t3[0] * inv, flat = layer ? -t3[1] * inv : 0.0f;
+                const f2 m = pair(along, along), f = pair(flat, flat), r = pair(st.y, st.y);
+                if (layer) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) total[i] = st.y * (total[i] - flat - hat[i] * along);
+                    for (int i = 0; i < N2; ++i) total[i] = add2(total[i], f);
+                }
+#pragma unroll
+                for (int i = 0; i < N2; ++i) total[i] = mul2(r, fma2(hat[i], m, total[i]));
             }
         }
-        if (a.g_x != nullptr && there) g.store(static_cast<D *>(a.g_x) + t * H, total);
+        if (a.g_x != nullptr && there) g.store(static_cast<D *>(a.g_x) + row, total);
         if (G::STAGED) {
             if (!VEC) g.barrier();   // everyone has read the slot
             fetch(t + p.stages * step, slot);
@@ -233,14 +273,11 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, C == 
     float *const stack = reinterpret_cast<float *>(rings);
     const int low = threadIdx.x & 31;
     const int piles = p.W < 32 ? (p.W * p.R + 31) / 32 : p.R, pile = p.W < 32 ? threadIdx.x >> 5 : g.group;
-    const auto pile_up = [&](float *sums, float *v, const float *in_shared) {
+    const auto pile_up = [&](float *sums, f2 (*v)[N2], const float *in_shared) {
         if (sums == nullptr) return;
         float *const to = sums + static_cast<int64_t>(blockIdx.x) * H;
-        if (C == 4) {
-            if (v != nullptr)
-#pragma unroll
-                for (int j = 0; j < N; ++j)
-                    if (g.in(j)) to[VEC ? (j / G::NV * p.W + g.tid) * G::NV + j % G::NV : j * p.W + g.tid] = v[j];
+        if (!G::STAGED) {
+            if (v != nullptr) g.template columns<false>(to, *v);
             return;
         }
         __syncthreads();
@@ -249,13 +286,8 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, C == 
         if (v != nullptr) {
             for (int d = p.W; d < 32; d *= 2)
 #pragma unroll
-                for (int j = 0; j < N; ++j) v[j] += __shfl_xor_sync(FULL_MASK, v[j], d);
-            if (p.W >= 32 || low < p.W) {
-#pragma unroll
-                for (int j = 0; j < N; ++j)
-                    if (g.in(j))
-                        stack[pile * wide + (VEC ? (j / G::NV * p.W + g.tid) * G::NV + j % G::NV : j * p.W + g.tid)] = v[j];
-            }
+                for (int i = 0; i < N2; ++i) (*v)[i] = add2((*v)[i], __shfl_xor_sync(FULL_MASK, (*v)[i], d));
+            if (p.W >= 32 || low < p.W) g.template columns<false>(stack + pile * wide, *v);
             __syncthreads();
             from = stack;
             count = piles;
@@ -266,10 +298,9 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, C == 
             to[c] = s;
         }
     };
-    if (POST) pile_up(a.sums[SUM_POST_W], post_sum, nullptr);
-    if (PRE) pile_up(a.sums[SUM_PRE_W], pre_sum, nullptr);
-    const float *const shared0 = reinterpret_cast<const float *>(rings + static_cast<size_t>(p.R) * p.stages * slot_bytes);
-    const float *from = shared0;
+    if (POST) pile_up(a.sums[SUM_POST_W], &post_sum, nullptr);
+    if (PRE) pile_up(a.sums[SUM_PRE_W], &pre_sum, nullptr);
+    const float *from = more_at;
     pile_up(a.sums[SUM_POST_B], nullptr, from);
     if (a.sums[SUM_POST_B] != nullptr) from += p.R * wide;
     pile_up(a.sums[SUM_PRE_B], nullptr, from);
@@ -280,7 +311,6 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, C == 
 template <typename D, bool VEC, int C, bool POST, bool PRE> mp_status_t run(const NormCall &c, int &parts)
 {
     static std::atomic<uint64_t> allowed{0};
-    constexpr bool two = C == 1 && !(POST && PRE);
     NormBwdArgs a = {};
     const bool with_x = POST || c.gate_form != MP_GATE_NONE;
     const NormRows rows[5] = {c.g_s, c.g_y, c.s, c.x, c.gate_rows};
@@ -293,10 +323,11 @@ template <typename D, bool VEC, int C, bool POST, bool PRE> mp_status_t run(cons
     a.stats = c.stats; a.T = c.T; a.H = c.H; a.kind = c.kind; a.gate_form = c.gate_form; a.scale = c.scale;
     a.g_x = c.g_x; a.g_residual = c.g_residual; a.g_gate = c.g_gate;
     for (int i = 0; i < NORM_SHARED; ++i) a.sums[i] = c.sums[i];
-    a.more = (c.sums[SUM_POST_B] != nullptr) + (c.sums[SUM_PRE_B] != nullptr) + (c.sums[SUM_GATE] != nullptr);
-    const NormPlan p = norm_plan<D>(c.T, c.H, C, a.tensors, C < 4 ? a.more * 8 * C * 4 : 0, two);
+    const int more = (c.sums[SUM_POST_B] != nullptr) + (c.sums[SUM_PRE_B] != nullptr) + (c.sums[SUM_GATE] != nullptr);
+    const int held = POST + PRE + (c.post_b != nullptr) + (c.gate_form == MP_GATE_CHANNEL);
+    const NormPlan p = norm_plan<D>(c.T, c.H, C, a.tensors, held, more, false);
     if (C < 4 && p.stages < 1) return run<D, VEC, 4, POST, PRE>(c, parts);   // fp32 rows and several sums beside them
-    return norm_launch(k_block_norm_bwd<D, VEC, C, POST, PRE>, allowed, p, two, c.T, c.stream, parts, a);
+    return norm_launch(k_block_norm_bwd<D, VEC, C, POST, PRE>, allowed, p, false, c.T, c.stream, parts, a);
 }
 
 template <typename D, bool VEC, int C> mp_status_t by_norms(const NormCall &c, int &parts)
@@ -309,7 +340,6 @@ template <typename D, bool VEC, int C> mp_status_t by_norms(const NormCall &c, i
 
 template <typename D> mp_status_t norm_backward(const NormCall &c, int &parts)
 {
-    if (c.H <= 8 * NORM_THREADS) return c.vec ? by_norms<D, true, 1>(c, parts) : by_norms<D, false, 1>(c, parts);
     if (c.H <= 16 * NORM_THREADS) return c.vec ? by_norms<D, true, 2>(c, parts) : by_norms<D, false, 2>(c, parts);
     return c.vec ? by_norms<D, true, 4>(c, parts) : by_norms<D, false, 4>(c, parts);
 }
