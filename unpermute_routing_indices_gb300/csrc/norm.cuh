@@ -269,10 +269,10 @@ template <typename D, bool VEC, int C> struct NormGroup {
     }
 
     // Starts the copy of row t of `rows` into `slot`.
-    __device__ __forceinline__ void fetch(const NormRows &rows, int64_t t, uint8_t *slot) const
+    __device__ __forceinline__ void fetch(const NormRows &rows, uint32_t t, uint8_t *slot) const
     {
         if (!STAGED) return;
-        const char *row = static_cast<const char *>(rows.at) + t * (H * static_cast<int64_t>(sizeof(D)));
+        const char *row = static_cast<const char *>(rows.at) + static_cast<uint64_t>(t) * (H * static_cast<uint32_t>(sizeof(D)));
         const uint32_t to = smem_u32(slot);
         if (VEC) {
 #pragma unroll
@@ -296,11 +296,17 @@ template <typename D, bool VEC, int C> struct NormGroup {
         }
     }
     // Where row t of `rows` can be read: in `slot`, or where it is.
-    __device__ __forceinline__ const D *row(const NormRows &rows, int64_t t, const uint8_t *slot) const
+    __device__ __forceinline__ const D *row(const NormRows &rows, uint32_t t, const uint8_t *slot) const
     {
-        const D *at = static_cast<const D *>(rows.at) + t * H;
-        if (!STAGED) return at;
-        return reinterpret_cast<const D *>(slot + (VEC ? 0u : (reinterpret_cast<uintptr_t>(at) & 15u)));
+        if constexpr (STAGED && VEC) {
+            return reinterpret_cast<const D *>(slot);
+        } else {
+            const D *at = static_cast<const D *>(rows.at) + static_cast<uint64_t>(t) * static_cast<uint32_t>(H);
+            if constexpr (STAGED)
+                return reinterpret_cast<const D *>(slot + (reinterpret_cast<uintptr_t>(at) & 15u));
+            else
+                return at;
+        }
     }
 };
 

@@ -52,15 +52,21 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, 1)
     uint8_t *held = rings + static_cast<size_t>(p.R) * p.stages * slot_bytes;
     const auto hold = [&](const void *v) {
         const D *from = static_cast<const D *>(v);
-        if (v == nullptr || !G::STAGED) return from;
-        D *const to = reinterpret_cast<D *>(held);
-        held += p.pitch;
-        for (int c = threadIdx.x; c < H; c += blockDim.x) to[c] = from[c];
-        return static_cast<const D *>(to);
+        if constexpr (G::STAGED) {
+            D *const to = reinterpret_cast<D *>(held);
+            if (v != nullptr) {
+                held += p.pitch;
+                for (int c = threadIdx.x; c < H; c += blockDim.x) to[c] = from[c];
+            }
+            return static_cast<const D *>(to);
+        } else {
+            return from;
+        }
     };
     const D *const post_w = hold(POST ? a.post_w : nullptr), *const pre_w = hold(PRE ? a.pre_w : nullptr);
     const D *const post_b = hold(a.post_b);
-    const D *const channel = hold(a.gate_form == MP_GATE_CHANNEL ? a.gate : nullptr);
+    const bool by_channel = a.gate_form == MP_GATE_CHANNEL;
+    const D *const channel = hold(by_channel ? a.gate : nullptr);
     // Sums beside the weights', [R,wide] each; C 4: the partial sums themselves.
     const int wide = norm_wide(H);
     float *more[3];
@@ -73,21 +79,19 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, 1)
         for (int i = 0; i < N2; ++i) zero[i] = 0ull;
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
-            more[i] = nullptr;
-            if (a.sums[which[i]] == nullptr) continue;
-            if (!G::STAGED) {
-                more[i] = a.sums[which[i]] + static_cast<int64_t>(blockIdx.x) * H;
-            } else {
+            if constexpr (G::STAGED)
                 more[i] = at + g.group * wide;
-                at += p.R * wide;
-            }
+            else
+                more[i] = a.sums[which[i]] + static_cast<int64_t>(blockIdx.x) * H;
+            if (a.sums[which[i]] == nullptr) continue;
+            at += p.R * wide;
             g.template columns<false>(more[i], zero);
         }
     }
 
-    const int64_t step = static_cast<int64_t>(gridDim.x) * p.R, first = static_cast<int64_t>(blockIdx.x) * p.R;
-    const auto fetch = [&](int64_t t, uint8_t *slot) {
-        if (t < a.T) {
+    const uint32_t T = static_cast<uint32_t>(a.T), step = gridDim.x * p.R, first = blockIdx.x * p.R;
+    const auto fetch = [&](uint32_t t, uint8_t *slot) {
+        if (t < T) {
 #pragma unroll
             for (int i = 0; i < 5; ++i)
                 if (a.slot[i] >= 0) g.fetch(a.rows[i], t, slot + a.slot[i] * p.pitch);
@@ -104,20 +108,20 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, 1)
     for (int i = 0; i < N2; ++i) post_sum[i] = pre_sum[i] = 0ull;
 
     // What a row has one of, read one row ahead.
-    const auto stats_of = [&](int64_t t) {
-        return t < a.T ? __ldg(reinterpret_cast<const float4 *>(a.stats) + t) : make_float4(0, 0, 0, 0);
+    const auto stats_of = [&](uint32_t t) {
+        return t < T ? __ldg(reinterpret_cast<const float4 *>(a.stats) + t) : make_float4(0, 0, 0, 0);
     };
-    const auto gate_of = [&](int64_t t) {
-        return token && t < a.T ? norm_value(static_cast<const D *>(a.gate)[t]) : 1.0f;
+    const auto gate_of = [&](uint32_t t) {
+        return token && t < T ? norm_value(static_cast<const D *>(a.gate)[t]) : 1.0f;
     };
     float4 next = stats_of(first + g.group);
     float next_gate = gate_of(first + g.group);
     __syncthreads();
     int at = 0;
-    for (int64_t t0 = first; t0 < a.T; t0 += step) {   // the same count for every group
-        const int64_t t = t0 + g.group;
-        const bool there = t < a.T;
-        const int64_t row = t * H;
+    for (uint32_t t0 = first; t0 < T; t0 += step) {   // the same count for every group
+        const uint32_t t = t0 + g.group;
+        const bool there = t < T;
+        const uint64_t row = static_cast<uint64_t>(t) * static_cast<uint32_t>(H);
         uint8_t *const slot = ring + at * slot_bytes;
         const float4 st = next;
         const float gate = next_gate;
@@ -147,7 +151,7 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, 1)
             f2 hat[N2], d[N2];
             load(ROW_S, hat);
             load(ROW_G_Y, d);
-            if (more[1] != nullptr && there) g.template columns<true>(more[1], d);
+            if (a.sums[SUM_PRE_B] != nullptr && there) g.template columns<true>(more[1], d);
             standard(hat, st.z, st.w);
             f2 w[N2];
             g.load(pre_w, w);
@@ -198,7 +202,7 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, 1)
             float t3[3] = {0.0f, 0.0f, 0.0f};
             if (a.gate_form != MP_GATE_NONE) {
                 f2 u[N2], k[N2];
-                if (POST && post_b != nullptr) {
+                if (POST && a.post_b != nullptr) {
                     g.load(post_b, k);
 #pragma unroll
                     for (int i = 0; i < N2; ++i) u[i] = fma2(hat[i], w[i], k[i]);
@@ -213,12 +217,12 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, 1)
                     gate2 = add2(gate2, u[i]);
                 }
                 t3[2] = sum2(gate2);
-                if (more[2] != nullptr && there) g.template columns<true>(more[2], u);
+                if (a.sums[SUM_GATE] != nullptr && there) g.template columns<true>(more[2], u);
                 // The gate is read before its gradient is written, which may take its place.
                 if (token) {
 #pragma unroll
                     for (int i = 0; i < N2; ++i) k[i] = pair(gate, gate);
-                } else if (channel != nullptr) {
+                } else if (by_channel) {
                     g.load(channel, k);
                 } else {
                     load(ROW_GATE, k);
@@ -229,7 +233,7 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, 1)
                 for (int i = 0; i < N2; ++i) total[i] = mul2(total[i], k[i]);
             }
             if (POST) {
-                if (more[0] != nullptr && there) g.template columns<true>(more[0], total);
+                if (a.sums[SUM_POST_B] != nullptr && there) g.template columns<true>(more[0], total);
                 f2 along2 = 0ull, flat2 = 0ull;
 #pragma unroll
                 for (int i = 0; i < N2; ++i) {

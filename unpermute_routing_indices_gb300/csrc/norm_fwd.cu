@@ -52,7 +52,7 @@ __device__ __forceinline__ void moments(G &g, const f2 (&v)[G::N2], int kind, fl
 // (v - mean) rstd w + b
 template <typename G, typename D>
 __device__ __forceinline__ void normalise(const G &g, f2 (&v)[G::N2], bool layer, float mean, float rstd, const D *w,
-                                          const D *b)
+                                          const D *b, bool with_b)
 {
     f2 t[G::N2];
     g.load(w, t);
@@ -63,7 +63,7 @@ __device__ __forceinline__ void normalise(const G &g, f2 (&v)[G::N2], bool layer
     }
 #pragma unroll
     for (int i = 0; i < G::N2; ++i) v[i] = mul2(mul2(v[i], r), t[i]);
-    if (b != nullptr) {
+    if (with_b) {
         g.load(b, t);
 #pragma unroll
         for (int i = 0; i < G::N2; ++i) v[i] = add2(v[i], t[i]);
@@ -79,7 +79,8 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, C < 4
     pdl_trigger();
     pdl_wait();
     G g;
-    g.W = p.W; g.H = a.H;
+    const int H = a.H;
+    g.W = p.W; g.H = H;
     g.group = threadIdx.x / p.W;
     g.tid = threadIdx.x - g.group * p.W;
     g.red = reinterpret_cast<float *>(smem) + (p.W > 32 ? g.group * G::RED : 0);
@@ -89,9 +90,9 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, C < 4
     const int slot_bytes = tensors * p.pitch;
     uint8_t *const rings = smem + (p.W > 32 ? p.R : 1) * G::RED * 4;
     uint8_t *const ring = rings + static_cast<size_t>(g.group) * p.stages * slot_bytes;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * p.R, first = static_cast<int64_t>(blockIdx.x) * p.R;
-    const auto fetch = [&](int64_t t, uint8_t *slot) {
-        if (t < a.T) {
+    const uint32_t T = static_cast<uint32_t>(a.T), step = gridDim.x * p.R, first = blockIdx.x * p.R;
+    const auto fetch = [&](uint32_t t, uint8_t *slot) {
+        if (t < T) {
             g.fetch(a.x, t, slot);
             if (with_residual) g.fetch(a.residual, t, slot + p.pitch);
             if (with_gate) g.fetch(a.gate_rows, t, slot + (tensors - 1) * p.pitch);
@@ -104,28 +105,34 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, C < 4
     uint8_t *held = rings + static_cast<size_t>(p.R) * p.stages * slot_bytes;
     const auto hold = [&](const void *v) {
         const D *from = static_cast<const D *>(v);
-        if (v == nullptr || !G::STAGED) return from;
-        D *const to = reinterpret_cast<D *>(held);
-        held += p.pitch;
-        for (int c = threadIdx.x; c < a.H; c += blockDim.x) to[c] = from[c];
-        return static_cast<const D *>(to);
+        if constexpr (G::STAGED) {
+            D *const to = reinterpret_cast<D *>(held);
+            if (v != nullptr) {
+                held += p.pitch;
+                for (int c = threadIdx.x; c < H; c += blockDim.x) to[c] = from[c];
+            }
+            return static_cast<const D *>(to);
+        } else {
+            return from;
+        }
     };
     const D *const post_w = hold(a.post_w), *const post_b = hold(a.post_b);
-    const D *const channel = hold(a.gate_form == MP_GATE_CHANNEL ? a.gate : nullptr);
+    const bool by_channel = a.gate_form == MP_GATE_CHANNEL;
+    const D *const channel = hold(by_channel ? a.gate : nullptr);
     const D *const pre_w = hold(a.pre_w), *const pre_b = hold(a.pre_b);
     // A token's gate, read one row ahead.
-    const auto gate_of = [&](int64_t t) {
-        return a.gate_form == MP_GATE_TOKEN && t < a.T ? norm_value(static_cast<const D *>(a.gate)[t]) : 1.0f;
+    const auto gate_of = [&](uint32_t t) {
+        return a.gate_form == MP_GATE_TOKEN && t < T ? norm_value(static_cast<const D *>(a.gate)[t]) : 1.0f;
     };
     float next_gate = gate_of(first + g.group);
     const bool layer = a.kind == MP_NORM_LAYER;
-    const float inv = 1.0f / static_cast<float>(a.H);
+    const float inv = 1.0f / static_cast<float>(H);
     __syncthreads();
     int at = 0;
-    for (int64_t t0 = first; t0 < a.T; t0 += step) {   // the same count for every group
-        const int64_t t = t0 + g.group;
-        const bool there = t < a.T;
-        const int64_t row = t * a.H;
+    for (uint32_t t0 = first; t0 < T; t0 += step) {   // the same count for every group
+        const uint32_t t = t0 + g.group;
+        const bool there = t < T;
+        const uint64_t row = static_cast<uint64_t>(t) * static_cast<uint32_t>(H);
         uint8_t *const slot = ring + at * slot_bytes;
         if (G::STAGED) {
             cp_wait(p.stages - 1);
@@ -138,11 +145,11 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, C < 4
 #pragma unroll
         for (int i = 0; i < G::N2; ++i) v[i] = 0ull;
         if (there) g.load(g.row(a.x, t, slot), v);
-        if (post_w != nullptr) {
+        if (a.post_w != nullptr) {
             moments(g, v, a.kind, a.eps, inv, mean0, rstd0);
-            normalise(g, v, layer, mean0, rstd0, post_w, post_b);
+            normalise(g, v, layer, mean0, rstd0, post_w, post_b, a.post_b != nullptr);
         }
-        if (channel != nullptr) {
+        if (by_channel) {
             g.load(channel, w);
 #pragma unroll
             for (int i = 0; i < G::N2; ++i) v[i] = mul2(v[i], w[i]);
@@ -167,9 +174,9 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, C < 4
             at = at + 1 == p.stages ? 0 : at + 1;
         }
         if (a.s != nullptr && there) g.store(static_cast<D *>(a.s) + row, v);
-        if (pre_w != nullptr) {
+        if (a.pre_w != nullptr) {
             moments(g, v, a.kind, a.eps, inv, mean1, rstd1);
-            normalise(g, v, layer, mean1, rstd1, pre_w, pre_b);
+            normalise(g, v, layer, mean1, rstd1, pre_w, pre_b, a.pre_b != nullptr);
             if (there) g.store(static_cast<D *>(a.y) + row, v);
         }
         if (a.stats != nullptr && g.tid == 0 && there)
