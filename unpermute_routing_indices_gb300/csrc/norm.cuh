@@ -150,7 +150,7 @@ template <typename D, bool VEC, int C> struct NormGroup {
     static constexpr int NV = 16 / sizeof(D);    // values a vector
     static constexpr int VECS = N / NV;
     static constexpr bool STAGED = C < 4;
-    static constexpr int WARPS = C < 4 ? NORM_THREADS / 32 : 32;
+    static constexpr int WARPS = 32;   // of a row at most
 
     int W, H, tid, group;
     float *red;   // [2][WARPS] float4 of this group: see sums()
@@ -184,17 +184,22 @@ template <typename D, bool VEC, int C> struct NormGroup {
             for (int i = 0; i < M; ++i) to[i * WARPS + (tid >> 5)] = v[i];
         }
         barrier();
-        const int warps = W >> 5;
+        const int warps = W >> 5;   // slots past the last warp hold 0
+        if (warps <= 8) {
 #pragma unroll
-        for (int i = 0; i < M; ++i) {
-            float t = 0.0f;
+            for (int i = 0; i < M; ++i) {
+                const float4 p = reinterpret_cast<const float4 *>(to + i * WARPS)[0];
+                const float4 q = reinterpret_cast<const float4 *>(to + i * WARPS)[1];
+                v[i] = ((p.x + p.y) + (p.z + p.w)) + ((q.x + q.y) + (q.z + q.w));
+            }
+        } else {
 #pragma unroll
-            for (int q = 0; q < WARPS / 4; ++q)
-                if (4 * q < warps) {   // slots past the last warp hold 0
-                    const float4 p = reinterpret_cast<const float4 *>(to + i * WARPS)[q];
-                    t += (p.x + p.y) + (p.z + p.w);
-                }
-            v[i] = t;
+            for (int i = 0; i < M; ++i) v[i] = to[i * WARPS + (threadIdx.x & 31)];
+#pragma unroll
+            for (int d = 16; d; d >>= 1) {
+#pragma unroll
+                for (int i = 0; i < M; ++i) v[i] += __shfl_xor_sync(FULL_MASK, v[i], d);
+            }
         }
     }
     static constexpr int M_MOST = 3;
@@ -315,10 +320,10 @@ __host__ __device__ inline int norm_wide(int H) { return (H + 3) / 4 * 4; }
 
 // Threads a row, rows at a time, and slots for `tensors` staged rows; `held` vectors that the
 // rows share lie beside them, and `sums` fp32 sums a column of each group.  Two CTAs on an SM wherever two slots or more fit in half of it.
-template <typename D> NormPlan norm_plan(int64_t T, int H, int C, int tensors, int held, int sums, bool narrow)
+template <typename D> NormPlan norm_plan(int64_t T, int H, int C, int threads, int tensors, int held, int sums, bool two)
 {
     NormPlan p;
-    const int threads = C < 4 ? NORM_THREADS : 2 * NORM_THREADS, need = (H + 8 * C - 1) / (8 * C);
+    const int need = (H + 8 * C - 1) / (8 * C);
     p.W = 1;
     if (need <= 32)
         while (p.W < need) p.W *= 2;
@@ -326,14 +331,14 @@ template <typename D> NormPlan norm_plan(int64_t T, int H, int C, int tensors, i
         p.W = (need + 31) / 32 * 32;
     p.R = C < 4 ? threads / p.W : 1;
     while (p.R > 1 && p.W * (p.R / 2) >= 32 && (T + p.R / 2 - 1) / (p.R / 2) <= sm_count()) p.R /= 2;   // few rows: spread
-    const int red = 2 * 3 * (threads / 32) * 4;
+    const int red = 2 * 3 * 32 * 4;
     p.pitch = (H * static_cast<int>(sizeof(D)) + 15) / 16 * 16 + 16;
     const int64_t extra = C < 4 ? static_cast<int64_t>(held) * p.pitch + static_cast<int64_t>(sums) * p.R * norm_wide(H) * 4 : 0;
     const size_t fixed = static_cast<size_t>(p.W > 32 ? p.R : 1) * red + static_cast<size_t>(extra);
     const size_t slot = static_cast<size_t>(p.pitch) * tensors * p.R;
     p.stages = 0;
     if (C < 4) {
-        const size_t room = narrow && fixed + 2 * slot <= NORM_BUDGET ? NORM_BUDGET : NORM_MOST;
+        const size_t room = two && fixed + 2 * slot <= NORM_BUDGET ? NORM_BUDGET : NORM_MOST;
         p.stages = fixed < room ? static_cast<int>((room - fixed) / slot) : 0;
         if (p.stages > 4) p.stages = 4;
     }

@@ -329,7 +329,7 @@ template <typename D, bool VEC, int C, bool POST, bool PRE> mp_status_t run(cons
     for (int i = 0; i < NORM_SHARED; ++i) a.sums[i] = c.sums[i];
     const int more = (c.sums[SUM_POST_B] != nullptr) + (c.sums[SUM_PRE_B] != nullptr) + (c.sums[SUM_GATE] != nullptr);
     const int held = POST + PRE + (c.post_b != nullptr) + (c.gate_form == MP_GATE_CHANNEL);
-    const NormPlan p = norm_plan<D>(c.T, c.H, C, a.tensors, held, more, false);
+    const NormPlan p = norm_plan<D>(c.T, c.H, C, C < 4 ? NORM_THREADS : 2 * NORM_THREADS, a.tensors, held, more, false);
     if (C < 4 && p.stages < 1) return run<D, VEC, 4, POST, PRE>(c, parts);   // fp32 rows and several sums beside them
     return norm_launch(k_block_norm_bwd<D, VEC, C, POST, PRE>, allowed, p, false, c.T, c.stream, parts, a);
 }

@@ -193,7 +193,7 @@ template <typename D, bool VEC, int C> mp_status_t forward(const NormCall &c)
                         c.kind, c.gate_form, c.eps, c.scale, c.s_out, c.y, c.stats};
     const int held = (c.post_w != nullptr) + (c.post_b != nullptr) + (c.gate_form == MP_GATE_CHANNEL) +
                      (c.pre_w != nullptr) + (c.pre_b != nullptr);
-    const NormPlan p = norm_plan<D>(c.T, c.H, C, tensors, held, 0, true);
+    const NormPlan p = norm_plan<D>(c.T, c.H, C, C < 4 ? NORM_THREADS : 2 * NORM_THREADS, tensors, held, 0, true);
     if (C < 4 && p.stages < 1) return forward<D, VEC, 4>(c);
     int grid;
     return norm_launch(k_block_norm<D, VEC, C>, allowed, p, true, c.T, c.stream, grid, a);
