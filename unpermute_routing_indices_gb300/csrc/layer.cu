@@ -3,16 +3,50 @@
 //   l = x router^T;  (idx, w) = the router's choice;
 //   y[t] = sum_k w[t,k] (act(x[t] w1[e]^T + b1[e]) w2[e]^T + b2[e]),  e = idx[t,k]
 //
-// The logits are sums in pairs of fp32 (a sum and what its roundings lost), so that
-// they are those of 64 bits rounded once, and the choice with them.
+// The picked experts' weights are read once and bound it; rows are nothing beside them.  Two
+// kernels (three above ROUTE_TOKENS tokens, whose choice is worth a kernel of its own):
+// k_layer_logits, then k_layer, which runs from the choice to the result on every SM.
+//
+// Logits are sums in pairs of fp32 (a sum and what its roundings lost), so that they are those
+// of 64 bits rounded once, and the choice with them: sums in 64 bits would take 16 times the
+// instructions' time on this part.
+//
+// k_layer: one CTA an SM, launched cooperatively.  A unit of work is U rows of an expert's
+// weights against all tokens of that expert (an entry: up to 8 NT of them).  One warp streams
+// the weights of the CTA's units through a ring in shared memory by bulk copies of row pieces,
+// another the tokens' rows; eight warps multiply (mma.m16n8k16: weight rows are its 16, tokens
+// its 8; the bytes bound it, so the tensor cores' older form is enough, and it needs no tile
+// of 128 rows) and leave partial sums in shared memory, where they are joined in a fixed
+// order.  The ring does not stop between the two products: while the grid waits at the barrier
+// after the first one for the last activations h, the second's weights are already on their
+// way.  Sums over an expert's rows stay in fp32 until every slot of a token is there; a second
+// barrier, and the slots are added in order.
+//
+// A piece of a row is KC columns: bulk copies of 2 KB (U 16) or 512 bytes (U 64).  Rows in the
+// ring are 64 bytes further apart than they are long, so that the 16-byte reads of eight lanes
+// (two rows, four pieces) touch all banks once.  Lane (g, c) reads columns 8c .. 8c+7 of 32 in
+// one load and feeds them to two products as if they were the fragment's k = 2c, 2c+1, 2c+8,
+// 2c+9: both operands agree on that order, which is all that a sum over k asks.
 #include "expert.cuh"
 #include "route.cuh"
 #include "tc.cuh"
 
+#include <type_traits>
+
 namespace mp {
 namespace {
 
-constexpr int LAYER_THREADS = 256, LAYER_WARPS = LAYER_THREADS / 32;
+constexpr int ROUTE_TOKENS = 8;          // tokens that every CTA routes for itself, a warp each
+constexpr int LOGIT_THREADS = 128, LOGIT_WARPS = LOGIT_THREADS / 32;
+constexpr int MATH_WARPS = 8, MATH_THREADS = 32 * MATH_WARPS;
+constexpr int LAYER_THREADS = MATH_THREADS + 64;   // and two warps of copies
+constexpr int ROW_PAD = 64;              // bytes between rows in a ring
+constexpr int RING_MOST = 6;
+constexpr size_t LAYER_SMEM = 226 * 1024;
+
+struct LayerControl {
+    unsigned arrived[2];   // CTAs at the two barriers of k_layer
+};
 
 struct LayerArgs {
     const mp_bf16_t *x, *w1, *b1, *w2, *b2;
@@ -21,13 +55,26 @@ struct LayerArgs {
     int T, E, K, H, F, O, act;
     int32_t *idx;
     float *weights;
-    mp_bf16_t *h, *y;
+    mp_bf16_t *y;
+    int32_t *status;
+    // workspace
+    LayerControl *control;
+    float *logits;          // [T,E]
+    mp_bf16_t *xp;          // [T,Hp]: x with rows of whole 16 bytes, NULL where x is that
+    mp_bf16_t *h;           // [T*K,Fp]
+    float *out;             // [T*K,O]: each slot's result
+    int Hp, Fp;
+    bool routed;            // idx and weights are there when k_layer starts
 };
 
 __device__ __forceinline__ float bf16_value(const mp_bf16_t *p)
 {
     return __uint_as_float(static_cast<uint32_t>(__ldg(p)) << 16);
 }
+
+// ---------------------------------------------------------------------------
+// logits
+// ---------------------------------------------------------------------------
 
 // A sum of fp32 values and what its roundings lost (Knuth's two-sum).
 struct PairSum {
@@ -37,6 +84,11 @@ struct PairSum {
         const float t = __fadd_rn(s, p), z = __fsub_rn(t, s);
         lost = __fadd_rn(lost, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(p, z)));
         s = t;
+    }
+    __device__ __forceinline__ void add(const PairSum &o)
+    {
+        add(o.s);
+        lost = __fadd_rn(lost, o.lost);
     }
     // a b, and what the product's rounding lost (nothing for two bf16 values)
     template <bool EXACT> __device__ __forceinline__ void add_product(float a, float b)
@@ -48,27 +100,119 @@ struct PairSum {
     __device__ __forceinline__ float sum() const { return isfinite(s) ? __fadd_rn(s, lost) : s; }
 };
 
-template <typename L, int PER> __global__ void __launch_bounds__(LAYER_THREADS) k_layer_route(const LayerArgs a)
+// Logits of one expert and TB tokens, a CTA each; the first CTAs also clear k_layer's barriers and
+// lay x out in rows of whole 16 bytes where k_layer wants that.  VEC: rows of x and the
+// router are whole chunks of 4 on 16 (8) bytes.
+template <typename L, int TB, bool VEC> __global__ void __launch_bounds__(LOGIT_THREADS) k_layer_logits(const LayerArgs a)
 {
-    extern __shared__ SharedLogit logits[];
+    __shared__ PairSum part[LOGIT_WARPS][TB];
     pdl_trigger();
     pdl_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = blockIdx.x;
-    const mp_bf16_t *x = a.x + static_cast<int64_t>(t) * a.H;
-    for (int e = warp; e < a.E; e += LAYER_WARPS) {
-        const L *r = static_cast<const L *>(a.router) + static_cast<int64_t>(e) * a.H;
-        PairSum v;
-        for (int c = lane; c < a.H; c += 32) v.add_product<sizeof(L) == 2>(bf16_value(x + c), logit(r + c));
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x, t0 = blockIdx.y * TB;
+    if (e == 0 && t0 == 0 && threadIdx.x < 2) a.control->arrived[threadIdx.x] = 0;
+    if (a.xp != nullptr)
+        for (int t = t0 + e; t < min(t0 + TB, a.T); t += gridDim.x)
+            for (int c = threadIdx.x; c < a.Hp; c += LOGIT_THREADS)
+                a.xp[static_cast<int64_t>(t) * a.Hp + c] = c < a.H ? a.x[static_cast<int64_t>(t) * a.H + c] : 0;
+    const L *r = static_cast<const L *>(a.router) + static_cast<int64_t>(e) * a.H;
+    PairSum v[TB];
+    if (VEC) {
+        typedef typename std::conditional<sizeof(L) == 4, float4, uint2>::type Four;
+#pragma unroll 4
+        for (int c = threadIdx.x * 4; c < a.H; c += LOGIT_THREADS * 4) {
+            const Four w = __ldg(reinterpret_cast<const Four *>(r + c));
+            const L *wl = reinterpret_cast<const L *>(&w);
+#pragma unroll
+            for (int b = 0; b < TB; ++b) {
+                const uint2 u = __ldg(reinterpret_cast<const uint2 *>(a.x + static_cast<int64_t>(min(t0 + b, a.T - 1)) * a.H + c));
+                const float f[4] = {bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y)};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[b].add_product<sizeof(L) == 2>(f[i], logit_value(wl[i]));
+            }
+        }
+    } else {
+        for (int c = threadIdx.x; c < a.H; c += LOGIT_THREADS) {
+            const float w = logit(r + c);
+#pragma unroll
+            for (int b = 0; b < TB; ++b)
+                v[b].add_product<sizeof(L) == 2>(bf16_value(a.x + static_cast<int64_t>(min(t0 + b, a.T - 1)) * a.H + c), w);
+        }
+    }
+#pragma unroll
+    for (int b = 0; b < TB; ++b) {
 #pragma unroll
         for (int d = 16; d; d >>= 1) {
-            const float s = __shfl_xor_sync(FULL_MASK, v.s, d), lost = __shfl_xor_sync(FULL_MASK, v.lost, d);
-            v.add(s);
-            v.lost = __fadd_rn(v.lost, lost);
+            PairSum o;
+            o.s = __shfl_xor_sync(FULL_MASK, v[b].s, d);
+            o.lost = __shfl_xor_sync(FULL_MASK, v[b].lost, d);
+            v[b].add(o);
         }
-        if (lane == 0) logits[e].v = v.sum();
+        if (lane == 0) part[warp][b] = v[b];
     }
     __syncthreads();
-    if (warp == 0) route_token<SharedLogit, PER, 0>(a.route, logits, t, lane);
+    if (threadIdx.x < TB && t0 + static_cast<int>(threadIdx.x) < a.T) {
+        PairSum s = part[0][threadIdx.x];
+        for (int w = 1; w < LOGIT_WARPS; ++w) s.add(part[w][threadIdx.x]);
+        a.logits[static_cast<int64_t>(t0 + threadIdx.x) * a.E + e] = s.sum();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// from the choice to the result
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+__device__ __forceinline__ uint4 lds128(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t at)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+    return v;
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// A wait whose end the whole warp agrees on.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *gave_up)
+{
+    return __all_sync(FULL_MASK, mbar_wait(bar, parity, gave_up)) != 0;
+}
+__device__ __forceinline__ void math_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(MATH_THREADS) : "memory"); }
+
+// Waits until `count` CTAs have arrived; at most 4 s.
+__device__ __forceinline__ bool grid_wait(const unsigned *arrived, unsigned count, volatile int *gave_up)
+{
+    const uint64_t t0 = now_ns();
+    for (int i = 0;; ++i) {
+        unsigned n;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(n) : "l"(arrived) : "memory");
+        if (n >= count) return true;
+        if (*gave_up) return false;
+        if ((i & 63) == 63 && now_ns() - t0 > WAIT_NS) {
+            *gave_up = 1;
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ void grid_arrive(unsigned *arrived)
+{
+    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(arrived) : "memory");
 }
 
 __device__ __forceinline__ float act_of(int act, float z)
@@ -81,72 +225,480 @@ __device__ __forceinline__ float act_of(int act, float z)
     }
 }
 
-__device__ __forceinline__ float warp_dot(const mp_bf16_t *a, const mp_bf16_t *b, int n, int lane)
+// One token's choice by one warp; results through `r`.
+__device__ __noinline__ void route_one(const RouteArgs &r, const float *logits, int t, int lane)
 {
-    float v = 0.0f;
-    for (int c = lane; c < n; c += 32) v = fmaf(bf16_value(a + c), bf16_value(b + c), v);
-    return warp_sum(v);
-}
-
-// h[t,k,f]: a warp each.
-__global__ void __launch_bounds__(LAYER_THREADS) k_layer_up(const LayerArgs a)
-{
-    pdl_trigger();
-    pdl_wait();
-    const int lane = threadIdx.x & 31, f = blockIdx.x * LAYER_WARPS + (threadIdx.x >> 5), r = blockIdx.y;
-    const int e = a.idx[r];
-    if (f >= a.F || e < 0) return;
-    const bool gated = act_gated(a.act);
-    const int64_t P = static_cast<int64_t>(a.F) * (gated ? 2 : 1);
-    const mp_bf16_t *x = a.x + static_cast<int64_t>(r / a.K) * a.H;
-    float z = warp_dot(x, a.w1 + (e * P + f) * a.H, a.H, lane);
-    if (a.b1 != nullptr) z += bf16_value(a.b1 + e * P + f);
-    z = act_of(a.act, z);
-    if (gated) {
-        float u = warp_dot(x, a.w1 + (e * P + a.F + f) * a.H, a.H, lane);
-        if (a.b1 != nullptr) u += bf16_value(a.b1 + e * P + a.F + f);
-        z *= u;
-    }
-    const float v[1] = {z};
-    if (lane == 0) a.h[static_cast<int64_t>(r) * a.F + f] = pack(v);
-}
-
-// y[t,o]: a warp each, the experts in the order of their slots.
-__global__ void __launch_bounds__(LAYER_THREADS) k_layer_down(const LayerArgs a)
-{
-    pdl_trigger();
-    pdl_wait();
-    const int lane = threadIdx.x & 31, o = blockIdx.x * LAYER_WARPS + (threadIdx.x >> 5), t = blockIdx.y;
-    if (o >= a.O) return;
-    float y = 0.0f;
-    for (int k = 0; k < a.K; ++k) {
-        const int64_t r = static_cast<int64_t>(t) * a.K + k;
-        const int e = a.idx[r];
-        if (e < 0) continue;
-        const int64_t row = static_cast<int64_t>(e) * a.O + o;
-        float v = 0.0f;   // h is of the kernel before: no loads past the coherent path
-        for (int c = lane; c < a.F; c += 32) {
-            float h[1];
-            unpack(a.h[r * a.F + c], h);
-            v = fmaf(h[0], bf16_value(a.w2 + row * a.F + c), v);
-        }
-        v = warp_sum(v);
-        if (a.b2 != nullptr) v += bf16_value(a.b2 + row);
-        y = fmaf(a.weights[r], v, y);
-    }
-    const float v[1] = {y};
-    if (lane == 0) a.y[static_cast<int64_t>(t) * a.O + o] = pack(v);
-}
-
-template <typename L> void launch_layer_route(const LayerArgs &a, cudaStream_t s)
-{
-    const size_t smem = a.E * sizeof(SharedLogit);
-    if (a.E <= 128)
-        (void)launch_pdl(k_layer_route<L, 4>, a.T, LAYER_THREADS, smem, s, a);
-    else if (a.E <= 256)
-        (void)launch_pdl(k_layer_route<L, 8>, a.T, LAYER_THREADS, smem, s, a);
+    if (r.E <= 128)
+        route_token<float, 4, 0>(r, logits, t, lane);
+    else if (r.E <= 256)
+        route_token<float, 8, 0>(r, logits, t, lane);
     else
-        (void)launch_pdl(k_layer_route<L, 32>, a.T, LAYER_THREADS, smem, s, a);
+        route_token<float, 32, 0>(r, logits, t, lane);
+}
+
+// RG groups of 16 weight rows, the eight warps' KG = 8 / RG shares of a piece's columns; up to
+// 8 NT tokens an entry.  ODD: weight rows that start anywhere.
+template <int RG, int NT, bool ODD> struct Layer {
+    static constexpr int U = 16 * RG, KG = MATH_WARPS / RG, KC = 128 * KG, TOKENS = 8 * NT;
+    static constexpr int PITCH = KC * 2 + ROW_PAD;
+    static constexpr int W_STAGE = U * PITCH, B_STAGE = TOKENS * PITCH, B_STAGES = 3;
+    static constexpr int UP = U + 4;                        // of a partial sum's column: banks apart
+    static constexpr int RED = KG * TOKENS * UP;            // floats
+    struct Entry {
+        int expert, first, count;   // tokens' routes: order[first ..]
+    };
+    struct Shared {
+        uint64_t full[RING_MOST], empty[RING_MOST], b_full[B_STAGES], b_empty[B_STAGES];
+        int gave_up, entries;
+    };
+    // After the rings: partial sums, two of them; order, counts, entries; idx and weights of few tokens.
+    static size_t tables(int E, int R)
+    {
+        const int entries = (E < R ? E : R) + R / TOKENS;
+        return sizeof(Shared) + 2 * RED * 4 + (static_cast<size_t>(R) + 2 * E) * 4 + static_cast<size_t>(entries) * sizeof(Entry) +
+               static_cast<size_t>(ROUTE_TOKENS) * 32 * 8 + 64;
+    }
+};
+
+template <int RG, int NT, bool ODD>
+__global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, const int stages)
+{
+    typedef Layer<RG, NT, ODD> L;
+    constexpr int U = L::U, KG = L::KG, KC = L::KC, PITCH = L::PITCH, TOKENS = L::TOKENS, UP = L::UP;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, R = a.T * a.K;
+    const uint32_t w_ring = smem_u32(smem), b_ring = w_ring + stages * L::W_STAGE;
+    uint8_t *at = smem + stages * L::W_STAGE + L::B_STAGES * L::B_STAGE;
+    typename L::Shared &s = *reinterpret_cast<typename L::Shared *>(at);
+    at += sizeof(typename L::Shared);
+    float *const red = reinterpret_cast<float *>(at);
+    at += 2 * L::RED * 4;
+    int *const order = reinterpret_cast<int *>(at), *const count = order + R, *const start = count + a.E;
+    typename L::Entry *const entry = reinterpret_cast<typename L::Entry *>(start + a.E);
+    int32_t *const my_idx = reinterpret_cast<int32_t *>(entry + min(a.E, R) + R / TOKENS);
+    float *const my_weights = reinterpret_cast<float *>(my_idx + ROUTE_TOKENS * 32);
+    volatile int *gave_up = &s.gave_up;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; ++i) {
+            mbar_init(smem_u32(&s.full[i]), 1);
+            mbar_init(smem_u32(&s.empty[i]), MATH_WARPS);
+        }
+        for (int i = 0; i < L::B_STAGES; ++i) {
+            mbar_init(smem_u32(&s.b_full[i]), 1);
+            mbar_init(smem_u32(&s.b_empty[i]), MATH_WARPS);
+        }
+        mbar_init_fence();
+        s.gave_up = 0;
+    }
+    for (int e = threadIdx.x; e < a.E; e += LAYER_THREADS) count[e] = 0;
+    pdl_trigger();
+    pdl_wait();
+
+    // The choice, if it is not there yet.
+    const int32_t *idx = a.idx;
+    const float *weights = a.weights;
+    if (!a.routed) {
+        if (warp < a.T) {
+            RouteArgs r = a.route;
+            r.idx = my_idx;
+            r.weights = my_weights;
+            route_one(r, a.logits + static_cast<int64_t>(warp) * a.E, warp, lane);
+        }
+        idx = my_idx;
+        weights = my_weights;
+    }
+    __syncthreads();
+    if (!a.routed && blockIdx.x == 0)
+        for (int r = threadIdx.x; r < R; r += LAYER_THREADS) {
+            a.idx[r] = my_idx[r];
+            a.weights[r] = my_weights[r];
+        }
+    // Routes by expert, in their order (every CTA has to come to the same entries), and entries
+    // of up to TOKENS of them.
+    for (int r = threadIdx.x; r < R; r += LAYER_THREADS)
+        if (idx[r] >= 0) atomicAdd(count + idx[r], 1);
+    __syncthreads();
+    if (warp == 0) {
+        int routes = 0, entries = 0;
+        for (int e0 = 0; e0 < a.E; e0 += 32) {
+            const int e = e0 + lane, n = e < a.E ? count[e] : 0, parts = (n + TOKENS - 1) / TOKENS;
+            int before = n, parts_before = parts;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(FULL_MASK, before, d), q = __shfl_up_sync(FULL_MASK, parts_before, d);
+                if (lane >= d) {
+                    before += o;
+                    parts_before += q;
+                }
+            }
+            const int first = routes + before - n, slot = entries + parts_before - parts;
+            if (e < a.E) start[e] = first;
+            for (int i = 0; i < parts; ++i)
+                entry[slot + i] = {e, first + i * TOKENS, min(TOKENS, n - i * TOKENS)};
+            routes += __shfl_sync(FULL_MASK, before, 31);
+            entries += __shfl_sync(FULL_MASK, parts_before, 31);
+        }
+        if (lane == 0) s.entries = entries;
+        __syncwarp();
+        for (int r0 = 0; r0 < R; r0 += 32) {
+            const int r = r0 + lane, e = r < R ? idx[r] : -1;
+            const unsigned same = __match_any_sync(FULL_MASK, e);
+            const int place = e >= 0 ? start[e] + __popc(same & ((1u << lane) - 1u)) : 0;
+            __syncwarp();
+            if (e >= 0) {
+                order[place] = r;
+                if ((same >> lane) == 1u) start[e] = place + 1;   // the last of them
+            }
+            __syncwarp();
+        }
+    }
+    __syncthreads();
+
+    const bool gated = act_gated(a.act);
+    const int entries = s.entries;
+    const int FU = gated ? U / 2 : U;   // columns of h that a unit makes
+    const int blocks[2] = {(a.F + FU - 1) / FU, (a.O + U - 1) / U};
+    const int depth[2] = {a.H, a.F};
+    const int step = gridDim.x;
+
+    if (warp == MATH_WARPS) {
+        // The weights of every unit of both products, one after another.
+        int at_stage = 0;
+        uint32_t phase = 0;
+        int64_t issued = 0;
+        bool on = true;
+        for (int p = 0; p < 2 && on; ++p) {
+            const int K = depth[p], nb = blocks[p], units = entries * nb;
+            const char *const base = reinterpret_cast<const char *>(p == 0 ? a.w1 : a.w2);
+            const int64_t rows_of_one = p == 0 ? static_cast<int64_t>(a.F) * (gated ? 2 : 1) : a.O;
+            const char *const end = base + rows_of_one * a.E * K * 2;
+            for (int u = blockIdx.x; u < units && on; u += step) {
+                const int64_t e = entry[u / nb].expert;
+                const int block = u % nb;
+                for (int k0 = 0; k0 < K && on; k0 += KC) {
+                    on = warp_wait(smem_u32(&s.empty[at_stage]), phase ^ 1u, gave_up);
+                    if (!on) break;
+                    const uint32_t bar = smem_u32(&s.full[at_stage]), to = w_ring + at_stage * L::W_STAGE;
+                    const int n = min(KC, K - k0);
+                    const char *src[(U + 31) / 32];
+                    uint32_t bytes[(U + 31) / 32], off[(U + 31) / 32], all = 0;
+#pragma unroll
+                    for (int i = 0; i < (U + 31) / 32; ++i) {
+                        const int r = lane + 32 * i;
+                        int64_t row = -1;
+                        if (r < U) {
+                            if (p == 0 && gated) {
+                                const int f = block * FU + (r >> 4) * 8 + (r & 7);
+                                if (f < a.F) row = f + (r & 8 ? a.F : 0);
+                            } else {
+                                const int f = block * U + r;
+                                if (f < rows_of_one) row = f;
+                            }
+                        }
+                        src[i] = base + ((e * rows_of_one + row) * K + k0) * 2;
+                        bytes[i] = row < 0 ? 0u : static_cast<uint32_t>(n) * 2u;
+                        off[i] = 0;
+                        if (ODD && row >= 0) {
+                            // The 16-byte granules that hold the piece; of the tensor's first and last,
+                            // which may reach beyond it, its own values one by one.
+                            const char *lo = reinterpret_cast<const char *>(reinterpret_cast<uintptr_t>(src[i]) & ~static_cast<uintptr_t>(15));
+                            const char *hi = reinterpret_cast<const char *>((reinterpret_cast<uintptr_t>(src[i]) + bytes[i] + 15) & ~static_cast<uintptr_t>(15));
+                            uint8_t *const row_at = smem + at_stage * L::W_STAGE + r * PITCH;
+                            const char *const lo0 = lo;
+                            if (lo < base) {
+                                lo += 16;
+                                for (const char *q = src[i]; q < lo && q < src[i] + bytes[i]; q += 2)
+                                    *reinterpret_cast<uint16_t *>(row_at + (q - lo0)) = __ldg(reinterpret_cast<const uint16_t *>(q));
+                            }
+                            if (hi > end) {
+                                hi -= 16;
+                                for (const char *q = hi > src[i] ? hi : src[i]; q < src[i] + bytes[i]; q += 2)
+                                    *reinterpret_cast<uint16_t *>(row_at + (q - lo0)) = __ldg(reinterpret_cast<const uint16_t *>(q));
+                            }
+                            bytes[i] = hi > lo ? static_cast<uint32_t>(hi - lo) : 0u;
+                            off[i] = static_cast<uint32_t>(lo - lo0);
+                            src[i] = lo;
+                        }
+                        all += bytes[i];
+                    }
+                    all = __reduce_add_sync(FULL_MASK, all);   // and what the lanes stored is ordered before the arrival
+                    __syncwarp();
+                    if (lane == 0) mbar_expect(bar, all);
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < (U + 31) / 32; ++i)
+                        if (bytes[i] != 0) bulk_load(to + (lane + 32 * i) * PITCH + off[i], src[i], bytes[i], bar);
+                    ++issued;
+                    if (++at_stage == stages) {
+                        at_stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+        }
+        if (*gave_up && lane == 0)   // copies in flight land before the shared memory goes
+            for (int i = 0; i < stages && i < issued; ++i) {
+                if (--at_stage < 0) {
+                    at_stage = stages - 1;
+                    phase ^= 1u;
+                }
+                mbar_drain(smem_u32(&s.full[at_stage]), phase);
+            }
+    } else if (warp == MATH_WARPS + 1) {
+        // The tokens' rows: x, and after the grid's barrier h.
+        int at_stage = 0;
+        uint32_t phase = 0;
+        int64_t issued = 0;
+        bool on = true;
+        for (int p = 0; p < 2 && on; ++p) {
+            const int K = p == 0 ? a.Hp : a.Fp, nb = blocks[p], units = entries * nb;
+            const mp_bf16_t *const base = p == 0 ? (a.xp != nullptr ? a.xp : a.x) : a.h;
+            if (p == 1) {
+                if (lane == 0) on = grid_wait(&a.control->arrived[0], gridDim.x, gave_up);
+                on = __shfl_sync(FULL_MASK, static_cast<int>(on), 0) != 0;
+                __syncwarp();
+                fence_async();   // what other SMs stored, by the copies to come
+            }
+            for (int u = blockIdx.x; u < units && on; u += step) {
+                const typename L::Entry en = entry[u / nb];
+                const mp_bf16_t *row = base;
+                if (lane < en.count) {
+                    const int r = order[en.first + lane];
+                    row += static_cast<int64_t>(p == 0 ? r / a.K : r) * K;
+                }
+                for (int k0 = 0; k0 < K; k0 += KC) {
+                    on = warp_wait(smem_u32(&s.b_empty[at_stage]), phase ^ 1u, gave_up);
+                    if (!on) break;
+                    const uint32_t bar = smem_u32(&s.b_full[at_stage]), to = b_ring + at_stage * L::B_STAGE;
+                    const uint32_t bytes = static_cast<uint32_t>(min(KC, K - k0)) * 2u;
+                    if (lane == 0) mbar_expect(bar, bytes * en.count);
+                    __syncwarp();
+                    if (lane < en.count) bulk_load(to + lane * PITCH, row + k0, bytes, bar);
+                    ++issued;
+                    if (++at_stage == L::B_STAGES) {
+                        at_stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+        }
+        if (*gave_up && lane == 0)
+            for (int i = 0; i < L::B_STAGES && i < issued; ++i) {
+                if (--at_stage < 0) {
+                    at_stage = L::B_STAGES - 1;
+                    phase ^= 1u;
+                }
+                mbar_drain(smem_u32(&s.b_full[at_stage]), phase);
+            }
+    } else {
+        // A warp that gives up a wait goes on without waiting or multiplying, so that the barriers
+        // of the others come to their ends.
+        const int rg = warp / KG, kg = warp % KG, g = lane >> 2, c = lane & 3;
+        int ws = 0, bs = 0, buffer = 0;
+        uint32_t wp = 0, bp = 0;
+        bool on = true;
+        for (int p = 0; p < 2; ++p) {
+            const int K = depth[p], nb = blocks[p], units = entries * nb;
+            for (int u = blockIdx.x; u < units; u += step) {
+                const typename L::Entry en = entry[u / nb];
+                const int block = u % nb, tiles = (en.count + 7) >> 3;
+                float acc[NT][4];
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[t][i] = 0.0f;
+                uint32_t shift[2] = {0, 0};   // where a row's first value lies in its granule
+                if (ODD) {
+                    const int64_t rows_of_one = p == 0 ? static_cast<int64_t>(a.F) * (gated ? 2 : 1) : a.O;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = rg * 16 + g + 8 * i;
+                        const int64_t row = p == 0 && gated ? block * FU + (r >> 4) * 8 + (r & 7) + (r & 8 ? a.F : 0)
+                                                            : block * U + r;
+                        shift[i] = static_cast<uint32_t>((reinterpret_cast<uintptr_t>(p == 0 ? a.w1 : a.w2) +
+                                                          (en.expert * rows_of_one + row) * K * 2) & 15u);
+                    }
+                }
+                for (int k0 = 0; k0 < K; k0 += KC) {
+                    if (on) on = warp_wait(smem_u32(&s.full[ws]), wp, gave_up) && warp_wait(smem_u32(&s.b_full[bs]), bp, gave_up);
+                    if (on) {
+                        const int n = min(KC, K - k0);
+                        const uint32_t w_at = w_ring + ws * L::W_STAGE + (rg * 16 + g) * PITCH;
+                        const uint32_t b_at = b_ring + bs * L::B_STAGE + g * PITCH;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int col = kg * 128 + q * 32 + c * 8;
+                            uint4 a0 = make_uint4(0, 0, 0, 0), a1 = a0;
+                            const bool in = col < n;
+                            if (!ODD) {
+                                if (in) {
+                                    a0 = lds128(w_at + col * 2);
+                                    a1 = lds128(w_at + 8 * PITCH + col * 2);
+                                }
+                            } else if (in) {
+                                uint32_t v[2][4];
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    const uint32_t from = w_at + 8 * i * PITCH + ((shift[i] + col * 2) & ~3u);
+                                    const uint32_t by = (shift[i] & 2u) * 8u;
+                                    uint32_t word[5];
+#pragma unroll
+                                    for (int j = 0; j < 5; ++j) word[j] = lds32(from + 4 * j);
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j) {
+                                        // past the row's end is another row, or what the ring held before
+                                        const int left = n - col - 2 * j;
+                                        const uint32_t mask = left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
+                                        v[i][j] = __funnelshift_r(word[j], word[j + 1], by) & mask;
+                                    }
+                                }
+                                a0 = make_uint4(v[0][0], v[0][1], v[0][2], v[0][3]);
+                                a1 = make_uint4(v[1][0], v[1][1], v[1][2], v[1][3]);
+                            }
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) {
+                                if (t >= tiles) break;
+                                uint4 b = make_uint4(0, 0, 0, 0);
+                                if (in) b = lds128(b_at + t * 8 * PITCH + col * 2);
+                                mma16816(acc[t], a0.x, a1.x, a0.y, a1.y, b.x, b.y);
+                                mma16816(acc[t], a0.z, a1.z, a0.w, a1.w, b.z, b.w);
+                            }
+                        }
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(smem_u32(&s.empty[ws]));
+                            mbar_arrive(smem_u32(&s.b_empty[bs]));
+                        }
+                    }
+                    if (++ws == stages) {
+                        ws = 0;
+                        wp ^= 1u;
+                    }
+                    if (++bs == L::B_STAGES) {
+                        bs = 0;
+                        bp ^= 1u;
+                    }
+                }
+                // The warps' shares of the columns, joined in order.  Two buffers in turn: a
+                // thread still reading one is waited for by the barrier of the next unit.
+                float *const to = red + buffer * L::RED;
+                buffer ^= 1;
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    if (t >= tiles) break;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        to[(kg * TOKENS + t * 8 + 2 * c + (i & 1)) * UP + rg * 16 + g + (i & 2 ? 8 : 0)] = acc[t][i];
+                }
+                math_barrier();
+                const auto joined = [&](int token, int row) {
+                    float v = to[token * UP + row];
+#pragma unroll
+                    for (int k = 1; k < KG; ++k) v += to[(k * TOKENS + token) * UP + row];
+                    return v;
+                };
+                if (p == 0) {
+                    const mp_bf16_t *b1 = a.b1 == nullptr ? nullptr
+                                                          : a.b1 + static_cast<int64_t>(en.expert) * a.F * (gated ? 2 : 1);
+                    for (int i = threadIdx.x; i < FU * en.count; i += MATH_THREADS) {
+                        const int token = i / FU, j = i - token * FU, f = block * FU + j;
+                        if (f >= a.Fp) continue;
+                        float h[1] = {0.0f};   // up to a row's last 16 bytes
+                        if (f < a.F) {
+                            float z = joined(token, gated ? (j >> 3) * 16 + (j & 7) : j);
+                            if (b1 != nullptr) z += bf16_value(b1 + f);
+                            z = act_of(a.act, z);
+                            if (gated) {
+                                float o = joined(token, (j >> 3) * 16 + (j & 7) + 8);
+                                if (b1 != nullptr) o += bf16_value(b1 + a.F + f);
+                                z *= o;
+                            }
+                            h[0] = z;
+                        }
+                        a.h[static_cast<int64_t>(order[en.first + token]) * a.Fp + f] = pack(h);
+                    }
+                } else {
+                    const mp_bf16_t *b2 = a.b2 == nullptr ? nullptr : a.b2 + static_cast<int64_t>(en.expert) * a.O;
+                    for (int i = threadIdx.x; i < U * en.count; i += MATH_THREADS) {
+                        const int token = i / U, j = i - token * U, o = block * U + j;
+                        if (o >= a.O) continue;
+                        float v = joined(token, j);
+                        if (b2 != nullptr) v += bf16_value(b2 + o);
+                        a.out[static_cast<int64_t>(order[en.first + token]) * a.O + o] = v;
+                    }
+                }
+            }
+            // What this CTA made is there for the others: their copies read h.
+            if (p == 0) fence_async();
+            __threadfence();
+            math_barrier();
+            if (threadIdx.x == 0) grid_arrive(&a.control->arrived[p]);
+        }
+        if (threadIdx.x == 0) (void)grid_wait(&a.control->arrived[1], gridDim.x, gave_up);
+        math_barrier();
+        for (int64_t i = static_cast<int64_t>(blockIdx.x) * MATH_THREADS + threadIdx.x; i < static_cast<int64_t>(a.T) * a.O;
+             i += static_cast<int64_t>(gridDim.x) * MATH_THREADS) {
+            const int t = static_cast<int>(i / a.O), o = static_cast<int>(i - static_cast<int64_t>(t) * a.O);
+            float y = 0.0f;
+            for (int k = 0; k < a.K; ++k) {
+                const int r = t * a.K + k;
+                if (idx[r] >= 0) y = fmaf(weights[r], __ldcg(a.out + static_cast<int64_t>(r) * a.O + o), y);
+            }
+            const float v[1] = {y};
+            a.y[i] = pack(v);
+        }
+        if (threadIdx.x == 0 && *gave_up) or_status(a.status, MP_STATUS_STALLED);
+    }
+}
+
+template <typename L> void launch_logits(const LayerArgs &a, cudaStream_t s)
+{
+    const bool vec = a.H % 4 == 0 && reinterpret_cast<uintptr_t>(a.x) % 8 == 0 &&
+                     reinterpret_cast<uintptr_t>(a.router) % (4 * sizeof(L)) == 0;
+    const unsigned E = static_cast<unsigned>(a.E);
+    if (a.T <= 2)
+        (void)launch_pdl(vec ? k_layer_logits<L, 1, true> : k_layer_logits<L, 1, false>, dim3(E, a.T), LOGIT_THREADS, 0, s, a);
+    else
+        (void)launch_pdl(vec ? k_layer_logits<L, 4, true> : k_layer_logits<L, 4, false>, dim3(E, (a.T + 3) / 4),
+                         LOGIT_THREADS, 0, s, a);
+}
+
+template <int RG, int NT, bool ODD> mp_status_t launch_layer(const LayerArgs &a, cudaStream_t s)
+{
+    typedef Layer<RG, NT, ODD> L;
+    static std::atomic<uint64_t> allowed{0};
+    if (!allow_smem(k_layer<RG, NT, ODD>, allowed, LAYER_SMEM)) return MP_ERR_CUDA;
+    const int R = a.T * a.K;
+    const size_t other = L::tables(a.E, R) + static_cast<size_t>(L::B_STAGES) * L::B_STAGE;
+    int stages = static_cast<int>((LAYER_SMEM - other) / L::W_STAGE);
+    if (stages > RING_MOST) stages = RING_MOST;
+    // No more CTAs than units: a barrier of few is quicker.
+    const int FU = act_gated(a.act) ? L::U / 2 : L::U;
+    const int64_t entries = (a.E < R ? a.E : R) + R / L::TOKENS;
+    const int64_t wide = a.F / FU > a.O / L::U ? a.F / FU : a.O / L::U, units = entries * (wide + 1);
+    const int sms = sm_count();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = static_cast<unsigned>(units < sms ? units : sms);
+    cfg.blockDim = LAYER_THREADS;
+    cfg.dynamicSmemBytes = other + static_cast<size_t>(stages) * L::W_STAGE;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    (void)cudaLaunchKernelEx(&cfg, k_layer<RG, NT, ODD>, a, stages);
+    return check_launch();
+}
+
+template <bool ODD> mp_status_t choose_layer(const LayerArgs &a, cudaStream_t s)
+{
+    if (a.T <= 8) return launch_layer<1, 1, ODD>(a, s);
+    if (a.T * a.K <= 12 * a.E) return launch_layer<4, 2, ODD>(a, s);
+    return launch_layer<4, 4, ODD>(a, s);
 }
 
 mp_status_t layer_sizes(int64_t T, int32_t E, int32_t K, int32_t H, int32_t F, int32_t O)
@@ -158,6 +710,22 @@ mp_status_t layer_sizes(int64_t T, int32_t E, int32_t K, int32_t H, int32_t F, i
                : MP_OK;
 }
 
+int whole(int n) { return (n + 7) / 8 * 8; }
+
+// Where the parts of the workspace start, in bytes; the last is its size.
+struct LayerSpace {
+    size_t logits, xp, h, out, bytes;
+    LayerSpace(int64_t T, int64_t E, int64_t K, int H, int F, int64_t O)
+    {
+        const auto next = [](size_t from, size_t bytes) { return (from + bytes + 255) / 256 * 256; };
+        logits = 256;
+        xp = next(logits, static_cast<size_t>(T * E) * 4);
+        h = next(xp, static_cast<size_t>(T) * whole(H) * 2);
+        out = next(h, static_cast<size_t>(T * K) * whole(F) * 2);
+        bytes = next(out, static_cast<size_t>(T * K * O) * 4);
+    }
+};
+
 }  // namespace
 }  // namespace mp
 
@@ -165,9 +733,7 @@ using namespace mp;
 
 extern "C" size_t mp_moe_layer_workspace_size(int64_t T, int32_t E, int32_t K, int32_t H, int32_t F, int32_t O)
 {
-    if (layer_sizes(T, E, K, H, F, O) != MP_OK) return 0;
-    const size_t bytes = static_cast<size_t>(T) * K * F * sizeof(mp_bf16_t);
-    return bytes < 256 ? 256 : (bytes + 255) / 256 * 256;
+    return layer_sizes(T, E, K, H, F, O) != MP_OK ? 0 : LayerSpace(T, E, K, H, F, O).bytes;
 }
 
 extern "C" mp_status_t mp_moe_layer(const mp_bf16_t *x, const void *router, int32_t router_dtype,
@@ -189,22 +755,33 @@ extern "C" mp_status_t mp_moe_layer(const mp_bf16_t *x, const void *router, int3
     if (x == nullptr || router == nullptr || w1 == nullptr || w2 == nullptr || idx == nullptr ||
         weights == nullptr || y == nullptr)
         return MP_ERR_INVALID_ARG;
-    if (workspace == nullptr || !aligned16(workspace) ||
-        workspace_bytes < mp_moe_layer_workspace_size(T, E, K, H, F, O))
-        return MP_ERR_WORKSPACE;
-    (void)dev_status;
-    route.T = T; route.idx = idx; route.weights = weights;
+    const LayerSpace space(T, E, K, H, F, O);
+    if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < space.bytes) return MP_ERR_WORKSPACE;
+    uint8_t *const ws = static_cast<uint8_t *>(workspace);
     const cudaStream_t s = as_stream(stream);
-    const LayerArgs a = {x, w1, b1, w2, b2, router, route, static_cast<int>(T), E, K, H, F, O, act, idx, weights,
-                         static_cast<mp_bf16_t *>(workspace), y};
+    route.T = T;
+    LayerArgs a = {};
+    a.x = x; a.w1 = w1; a.b1 = b1; a.w2 = w2; a.b2 = b2; a.router = router; a.route = route;
+    a.T = static_cast<int>(T); a.E = E; a.K = K; a.H = H; a.F = F; a.O = O; a.act = act;
+    a.idx = idx; a.weights = weights; a.y = y; a.status = dev_status;
+    a.control = reinterpret_cast<LayerControl *>(ws);
+    a.logits = reinterpret_cast<float *>(ws + space.logits);
+    a.Hp = whole(H); a.Fp = whole(F);
+    a.xp = H % 8 == 0 && aligned16(x) ? nullptr : reinterpret_cast<mp_bf16_t *>(ws + space.xp);
+    a.h = reinterpret_cast<mp_bf16_t *>(ws + space.h);
+    a.out = reinterpret_cast<float *>(ws + space.out);
+    a.routed = T > ROUTE_TOKENS;
     switch (router_dtype) {
-    case MP_DTYPE_BF16: launch_layer_route<__nv_bfloat16>(a, s); break;
-    case MP_DTYPE_FP16: launch_layer_route<__half>(a, s); break;
-    default: launch_layer_route<float>(a, s); break;
+    case MP_DTYPE_BF16: launch_logits<__nv_bfloat16>(a, s); break;
+    case MP_DTYPE_FP16: launch_logits<__half>(a, s); break;
+    default: launch_logits<float>(a, s); break;
     }
-    const unsigned rows = static_cast<unsigned>(T * K);
-    (void)launch_pdl(k_layer_up, dim3((F + LAYER_WARPS - 1) / LAYER_WARPS, rows), LAYER_THREADS, 0, s, a);
-    (void)launch_pdl(k_layer_down, dim3((O + LAYER_WARPS - 1) / LAYER_WARPS, static_cast<unsigned>(T)),
-                     LAYER_THREADS, 0, s, a);
-    return check_launch();
+    if (const mp_status_t st = check_launch(); st != MP_OK) return st;
+    if (a.routed) {
+        const mp_status_t st = mp_route(a.logits, MP_DTYPE_FP32, bias, T, E, K, score, n_groups, topk_groups, group_top,
+                                        renorm, scale, idx, weights, stream);
+        if (st != MP_OK) return st;
+    }
+    const bool even = H % 8 == 0 && F % 8 == 0 && aligned16(w1) && aligned16(w2);
+    return even ? choose_layer<false>(a, s) : choose_layer<true>(a, s);
 }
