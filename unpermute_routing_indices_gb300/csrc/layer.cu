@@ -12,21 +12,27 @@
 // instructions' time on this part.
 //
 // k_layer: one CTA an SM, launched cooperatively.  A unit of work is U rows of an expert's
-// weights against all tokens of that expert (an entry: up to 8 NT of them).  One warp streams
-// the weights of the CTA's units through a ring in shared memory by bulk copies of row pieces,
-// another the tokens' rows; eight warps multiply (mma.m16n8k16: weight rows are its 16, tokens
-// its 8; the bytes bound it, so the tensor cores' older form is enough, and it needs no tile
-// of 128 rows) and leave partial sums in shared memory, where they are joined in a fixed
-// order.  The ring does not stop between the two products: while the grid waits at the barrier
-// after the first one for the last activations h, the second's weights are already on their
-// way.  Sums over an expert's rows stay in fp32 until every slot of a token is there; a second
+// weights against all tokens of that expert (an entry: up to 8 NT of them).  Each of eight
+// warps multiplies 16 weight rows by its share of the columns, 128 a stage, which it copies
+// itself, by cp.async into a ring of its own; one more warp copies the tokens' rows for all, and
+// four join the eight warps' sums, in a fixed order, and apply bias and activation, so that the
+// eight never wait for a unit's end.
+// (mma.m16n8k16: weight rows are its 16, tokens its 8.  Bytes bound it, so the tensor cores'
+// older form is enough, and it needs no tile of 128 rows.)  The rings do not stop between the
+// two products: while the grid waits at the barrier after the first one for the last
+// activations h, the second's weights are already on their way.  h is kept as two bf16 values, the
+// nearest one and the nearest of what is left, 16 bits of it in all: the second product takes
+// both, which costs no time, and y's error is that of its own rounding (with one: 1.4 times that).
+// Sums over an expert's rows stay in fp32 until every slot of a token is there; a second
 // barrier, and the slots are added in order.
+// (Weights by bulk copies of row pieces, one warp for all: 2 KB pieces 56 us for one token of
+// 128 experts of 1,024 x 4,096, 512-byte pieces 393 us for 64 tokens of 64 of 1,024 x 2,048.)
 //
-// A piece of a row is KC columns: bulk copies of 2 KB (U 16) or 512 bytes (U 64).  Rows in the
-// ring are 64 bytes further apart than they are long, so that the 16-byte reads of eight lanes
-// (two rows, four pieces) touch all banks once.  Lane (g, c) reads columns 8c .. 8c+7 of 32 in
-// one load and feeds them to two products as if they were the fragment's k = 2c, 2c+1, 2c+8,
-// 2c+9: both operands agree on that order, which is all that a sum over k asks.
+// A stage of a warp is 16 rows of 256 bytes; the rows' 64-byte halves are swapped in every
+// other row, so that the 16-byte reads of eight lanes (two rows, four pieces) touch all banks
+// once.  Lane (g, c) reads columns 8c .. 8c+7 of 32 in one load and feeds them to two products
+// as if they were the fragment's k = 2c, 2c+1, 2c+8, 2c+9: both operands agree on that order,
+// which is all that a sum over k asks.
 #include "expert.cuh"
 #include "route.cuh"
 #include "tc.cuh"
@@ -39,10 +45,11 @@ namespace {
 constexpr int ROUTE_TOKENS = 8;          // tokens that every CTA routes for itself, a warp each
 constexpr int LOGIT_THREADS = 128, LOGIT_WARPS = LOGIT_THREADS / 32;
 constexpr int MATH_WARPS = 8, MATH_THREADS = 32 * MATH_WARPS;
-constexpr int LAYER_THREADS = MATH_THREADS + 64;   // and two warps of copies
-constexpr int ROW_PAD = 64;              // bytes between rows in a ring
-constexpr int RING_MOST = 6;
-constexpr size_t LAYER_SMEM = 226 * 1024;
+constexpr int JOIN_WARPS = 4, JOIN_THREADS = 32 * JOIN_WARPS;
+constexpr int LAYER_THREADS = MATH_THREADS + 32 + JOIN_THREADS;   // and a warp of copies
+constexpr int STAGE_COLS = 128;          // of a warp
+constexpr int ROW_PAD = 64;              // bytes between tokens' rows
+constexpr size_t LAYER_SMEM = 227 * 1024;
 
 struct LayerControl {
     unsigned arrived[2];   // CTAs at the two barriers of k_layer
@@ -61,7 +68,7 @@ struct LayerArgs {
     LayerControl *control;
     float *logits;          // [T,E]
     mp_bf16_t *xp;          // [T,Hp]: x with rows of whole 16 bytes, NULL where x is that
-    mp_bf16_t *h;           // [T*K,Fp]
+    mp_bf16_t *h;           // [T*K,2,Fp]: nearest values, and the nearest of what is left
     float *out;             // [T*K,O]: each slot's result
     int Hp, Fp;
     bool routed;            // idx and weights are there when k_layer starts
@@ -167,6 +174,16 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  "l"(src), "r"(bytes), "r"(bar)
                  : "memory");
 }
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes = 16)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but this thread's last S groups of copies have landed.
+template <int S> __device__ __forceinline__ void copy_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(S) : "memory");
+}
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 __device__ __forceinline__ uint4 lds128(uint32_t at)
 {
@@ -193,7 +210,9 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 {
     return __all_sync(FULL_MASK, mbar_wait(bar, parity, gave_up)) != 0;
 }
-__device__ __forceinline__ void math_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(MATH_THREADS) : "memory"); }
+// The joining warps; all but the warp of copies.
+__device__ __forceinline__ void join_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(JOIN_THREADS) : "memory"); }
+__device__ __forceinline__ void most_barrier() { asm volatile("bar.sync 2, %0;" ::"n"(LAYER_THREADS - 32) : "memory"); }
 
 // Waits until `count` CTAs have arrived; at most 4 s.
 __device__ __forceinline__ bool grid_wait(const unsigned *arrived, unsigned count, volatile int *gave_up)
@@ -236,43 +255,48 @@ __device__ __noinline__ void route_one(const RouteArgs &r, const float *logits, 
         route_token<float, 32, 0>(r, logits, t, lane);
 }
 
-// RG groups of 16 weight rows, the eight warps' KG = 8 / RG shares of a piece's columns; up to
+// RG groups of 16 weight rows, the eight warps' KG = 8 / RG shares of the columns; up to
 // 8 NT tokens an entry.  ODD: weight rows that start anywhere.
 template <int RG, int NT, bool ODD> struct Layer {
-    static constexpr int U = 16 * RG, KG = MATH_WARPS / RG, KC = 128 * KG, TOKENS = 8 * NT;
-    static constexpr int PITCH = KC * 2 + ROW_PAD;
-    static constexpr int W_STAGE = U * PITCH, B_STAGE = TOKENS * PITCH, B_STAGES = 3;
+    static constexpr int U = 16 * RG, KG = MATH_WARPS / RG, KC = STAGE_COLS * KG, TOKENS = 8 * NT;
+    static constexpr int W_PITCH = STAGE_COLS * 2 + (ODD ? 16 : 0);   // a row that starts anywhere takes a granule more
+    static constexpr int W_STAGE = MATH_WARPS * 16 * W_PITCH;
+    static constexpr int B_PITCH = KC * 2 + ROW_PAD;
+    static constexpr int B_STAGE = 2 * TOKENS * B_PITCH;    // both values of h
+    static constexpr int B_STAGES = NT == 2 ? 3 : 2;
+    static constexpr int STAGES = RG == 1 ? 4 : NT == 4 ? 3 : 4;
     static constexpr int UP = U + 4;                        // of a partial sum's column: banks apart
-    static constexpr int RED = KG * TOKENS * UP;            // floats
+    static constexpr int RED = KG * TOKENS * UP;            // floats of a unit's sums
+    static constexpr int REDS = NT == 4 ? 1 : 2;
     struct Entry {
         int expert, first, count;   // tokens' routes: order[first ..]
     };
     struct Shared {
-        uint64_t full[RING_MOST], empty[RING_MOST], b_full[B_STAGES], b_empty[B_STAGES];
+        uint64_t b_full[B_STAGES], b_empty[B_STAGES], red_full[REDS], red_empty[REDS];
         int gave_up, entries;
     };
-    // After the rings: partial sums, two of them; order, counts, entries; idx and weights of few tokens.
+    // After the rings: the units' sums; order, counts, entries; idx and weights of few tokens.
     static size_t tables(int E, int R)
     {
         const int entries = (E < R ? E : R) + R / TOKENS;
-        return sizeof(Shared) + 2 * RED * 4 + (static_cast<size_t>(R) + 2 * E) * 4 + static_cast<size_t>(entries) * sizeof(Entry) +
+        return sizeof(Shared) + REDS * RED * 4 + (static_cast<size_t>(R) + 2 * E) * 4 + static_cast<size_t>(entries) * sizeof(Entry) +
                static_cast<size_t>(ROUTE_TOKENS) * 32 * 8 + 64;
     }
 };
 
 template <int RG, int NT, bool ODD>
-__global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, const int stages)
+__global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a)
 {
     typedef Layer<RG, NT, ODD> L;
-    constexpr int U = L::U, KG = L::KG, KC = L::KC, PITCH = L::PITCH, TOKENS = L::TOKENS, UP = L::UP;
+    constexpr int U = L::U, KG = L::KG, KC = L::KC, TOKENS = L::TOKENS, UP = L::UP, STAGES = L::STAGES;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, R = a.T * a.K;
-    const uint32_t w_ring = smem_u32(smem), b_ring = w_ring + stages * L::W_STAGE;
-    uint8_t *at = smem + stages * L::W_STAGE + L::B_STAGES * L::B_STAGE;
+    const uint32_t b_ring = smem_u32(smem) + STAGES * L::W_STAGE;
+    uint8_t *at = smem + STAGES * L::W_STAGE + L::B_STAGES * L::B_STAGE;
     typename L::Shared &s = *reinterpret_cast<typename L::Shared *>(at);
     at += sizeof(typename L::Shared);
     float *const red = reinterpret_cast<float *>(at);
-    at += 2 * L::RED * 4;
+    at += L::REDS * L::RED * 4;
     int *const order = reinterpret_cast<int *>(at), *const count = order + R, *const start = count + a.E;
     typename L::Entry *const entry = reinterpret_cast<typename L::Entry *>(start + a.E);
     int32_t *const my_idx = reinterpret_cast<int32_t *>(entry + min(a.E, R) + R / TOKENS);
@@ -280,13 +304,13 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
     volatile int *gave_up = &s.gave_up;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < stages; ++i) {
-            mbar_init(smem_u32(&s.full[i]), 1);
-            mbar_init(smem_u32(&s.empty[i]), MATH_WARPS);
-        }
         for (int i = 0; i < L::B_STAGES; ++i) {
             mbar_init(smem_u32(&s.b_full[i]), 1);
             mbar_init(smem_u32(&s.b_empty[i]), MATH_WARPS);
+        }
+        for (int i = 0; i < L::REDS; ++i) {
+            mbar_init(smem_u32(&s.red_full[i]), MATH_WARPS);
+            mbar_init(smem_u32(&s.red_empty[i]), JOIN_WARPS);
         }
         mbar_init_fence();
         s.gave_up = 0;
@@ -363,89 +387,6 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
     const int step = gridDim.x;
 
     if (warp == MATH_WARPS) {
-        // The weights of every unit of both products, one after another.
-        int at_stage = 0;
-        uint32_t phase = 0;
-        int64_t issued = 0;
-        bool on = true;
-        for (int p = 0; p < 2 && on; ++p) {
-            const int K = depth[p], nb = blocks[p], units = entries * nb;
-            const char *const base = reinterpret_cast<const char *>(p == 0 ? a.w1 : a.w2);
-            const int64_t rows_of_one = p == 0 ? static_cast<int64_t>(a.F) * (gated ? 2 : 1) : a.O;
-            const char *const end = base + rows_of_one * a.E * K * 2;
-            for (int u = blockIdx.x; u < units && on; u += step) {
-                const int64_t e = entry[u / nb].expert;
-                const int block = u % nb;
-                for (int k0 = 0; k0 < K && on; k0 += KC) {
-                    on = warp_wait(smem_u32(&s.empty[at_stage]), phase ^ 1u, gave_up);
-                    if (!on) break;
-                    const uint32_t bar = smem_u32(&s.full[at_stage]), to = w_ring + at_stage * L::W_STAGE;
-                    const int n = min(KC, K - k0);
-                    const char *src[(U + 31) / 32];
-                    uint32_t bytes[(U + 31) / 32], off[(U + 31) / 32], all = 0;
-#pragma unroll
-                    for (int i = 0; i < (U + 31) / 32; ++i) {
-                        const int r = lane + 32 * i;
-                        int64_t row = -1;
-                        if (r < U) {
-                            if (p == 0 && gated) {
-                                const int f = block * FU + (r >> 4) * 8 + (r & 7);
-                                if (f < a.F) row = f + (r & 8 ? a.F : 0);
-                            } else {
-                                const int f = block * U + r;
-                                if (f < rows_of_one) row = f;
-                            }
-                        }
-                        src[i] = base + ((e * rows_of_one + row) * K + k0) * 2;
-                        bytes[i] = row < 0 ? 0u : static_cast<uint32_t>(n) * 2u;
-                        off[i] = 0;
-                        if (ODD && row >= 0) {
-                            // The 16-byte granules that hold the piece; of the tensor's first and last,
-                            // which may reach beyond it, its own values one by one.
-                            const char *lo = reinterpret_cast<const char *>(reinterpret_cast<uintptr_t>(src[i]) & ~static_cast<uintptr_t>(15));
-                            const char *hi = reinterpret_cast<const char *>((reinterpret_cast<uintptr_t>(src[i]) + bytes[i] + 15) & ~static_cast<uintptr_t>(15));
-                            uint8_t *const row_at = smem + at_stage * L::W_STAGE + r * PITCH;
-                            const char *const lo0 = lo;
-                            if (lo < base) {
-                                lo += 16;
-                                for (const char *q = src[i]; q < lo && q < src[i] + bytes[i]; q += 2)
-                                    *reinterpret_cast<uint16_t *>(row_at + (q - lo0)) = __ldg(reinterpret_cast<const uint16_t *>(q));
-                            }
-                            if (hi > end) {
-                                hi -= 16;
-                                for (const char *q = hi > src[i] ? hi : src[i]; q < src[i] + bytes[i]; q += 2)
-                                    *reinterpret_cast<uint16_t *>(row_at + (q - lo0)) = __ldg(reinterpret_cast<const uint16_t *>(q));
-                            }
-                            bytes[i] = hi > lo ? static_cast<uint32_t>(hi - lo) : 0u;
-                            off[i] = static_cast<uint32_t>(lo - lo0);
-                            src[i] = lo;
-                        }
-                        all += bytes[i];
-                    }
-                    all = __reduce_add_sync(FULL_MASK, all);   // and what the lanes stored is ordered before the arrival
-                    __syncwarp();
-                    if (lane == 0) mbar_expect(bar, all);
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < (U + 31) / 32; ++i)
-                        if (bytes[i] != 0) bulk_load(to + (lane + 32 * i) * PITCH + off[i], src[i], bytes[i], bar);
-                    ++issued;
-                    if (++at_stage == stages) {
-                        at_stage = 0;
-                        phase ^= 1u;
-                    }
-                }
-            }
-        }
-        if (*gave_up && lane == 0)   // copies in flight land before the shared memory goes
-            for (int i = 0; i < stages && i < issued; ++i) {
-                if (--at_stage < 0) {
-                    at_stage = stages - 1;
-                    phase ^= 1u;
-                }
-                mbar_drain(smem_u32(&s.full[at_stage]), phase);
-            }
-    } else if (warp == MATH_WARPS + 1) {
         // The tokens' rows: x, and after the grid's barrier h.
         int at_stage = 0;
         uint32_t phase = 0;
@@ -465,16 +406,19 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
                 const mp_bf16_t *row = base;
                 if (lane < en.count) {
                     const int r = order[en.first + lane];
-                    row += static_cast<int64_t>(p == 0 ? r / a.K : r) * K;
+                    row += static_cast<int64_t>(p == 0 ? r / a.K : 2 * r) * K;
                 }
                 for (int k0 = 0; k0 < K; k0 += KC) {
                     on = warp_wait(smem_u32(&s.b_empty[at_stage]), phase ^ 1u, gave_up);
                     if (!on) break;
                     const uint32_t bar = smem_u32(&s.b_full[at_stage]), to = b_ring + at_stage * L::B_STAGE;
                     const uint32_t bytes = static_cast<uint32_t>(min(KC, K - k0)) * 2u;
-                    if (lane == 0) mbar_expect(bar, bytes * en.count);
+                    if (lane == 0) mbar_expect(bar, bytes * en.count * (p + 1));
                     __syncwarp();
-                    if (lane < en.count) bulk_load(to + lane * PITCH, row + k0, bytes, bar);
+                    if (lane < en.count) {
+                        bulk_load(to + lane * L::B_PITCH, row + k0, bytes, bar);
+                        if (p == 1) bulk_load(to + (TOKENS + lane) * L::B_PITCH, row + K + k0, bytes, bar);
+                    }
                     ++issued;
                     if (++at_stage == L::B_STAGES) {
                         at_stage = 0;
@@ -491,12 +435,98 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
                 }
                 mbar_drain(smem_u32(&s.b_full[at_stage]), phase);
             }
-    } else {
+    } else if (warp < MATH_WARPS) {
         // A warp that gives up a wait goes on without waiting or multiplying, so that the barriers
         // of the others come to their ends.
         const int rg = warp / KG, kg = warp % KG, g = lane >> 2, c = lane & 3;
-        int ws = 0, bs = 0, buffer = 0;
-        uint32_t wp = 0, bp = 0;
+        const int parts = gated ? 2 : 1;
+        uint8_t *const ring = smem + warp * 16 * L::W_PITCH;
+        // A row of the group's 16, of unit (expert, block) in product p; -1: there is none.
+        const auto weight_row = [&](int p, int expert, int block, int i) -> int64_t {
+            if (p == 0 && gated) {   // 8 rows of the gate, 8 of the other half
+                const int f = block * FU + rg * 8 + (i & 7);
+                return f < a.F ? static_cast<int64_t>(expert) * 2 * a.F + f + (i & 8 ? a.F : 0) : -1;
+            }
+            const int f = block * U + rg * 16 + i, rows = p == 0 ? a.F : a.O;
+            return f < rows ? static_cast<int64_t>(expert) * rows + f : -1;
+        };
+        // The stage that is copied next: its product, unit and first column, and where this lane's
+        // part of the unit's rows is: pieces of 16 bytes lane & 15, of rows lane >> 4 and every other on.
+        int f_p = 0, f_u = blockIdx.x, f_k = 0;
+        const char *f_row[2];
+        int f_rows = 0;        // a bit for each of the eight rows that is there
+        const auto aim = [&]() {
+            while (f_p < 2 && f_u >= entries * blocks[f_p]) {
+                ++f_p;
+                f_u = blockIdx.x;
+            }
+            if (f_p == 2) return;
+            const int nb = blocks[f_p], e = entry[f_u / nb].expert, block = f_u % nb;
+            const char *const base = reinterpret_cast<const char *>(f_p == 0 ? a.w1 : a.w2);
+            f_rows = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f_rows |= (weight_row(f_p, e, block, (lane >> 4) + 2 * i) >= 0) << i;
+            // Rows 2 apart lie 2 rows apart, but for the step into the other half.
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                f_row[i] = base + weight_row(f_p, e, block, (lane >> 4) + 8 * i) * depth[f_p] * 2;
+        };
+        const auto fetch = [&](int stage) {
+            if (f_p < 2) {
+                const int K = depth[f_p], n = K - f_k - kg * STAGE_COLS;   // columns that are there
+                const int piece = lane & 15;
+                uint8_t *const to = ring + stage * L::W_STAGE;
+                const int64_t off = (static_cast<int64_t>(f_k) + kg * STAGE_COLS) * 2;
+                if (!ODD) {
+                    if (piece * 8 < n) {
+                        const uint32_t dst = smem_u32(to) + (lane >> 4) * L::W_PITCH + (piece ^ ((lane >> 4) & 1) << 2) * 16;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (f_rows >> i & 1)
+                                copy16(dst + 2 * i * L::W_PITCH,
+                                       f_row[i >> 2] + off + piece * 16 + static_cast<int64_t>(i & 3) * 4 * K);
+                    }
+                } else if (n > 0) {
+                    // The granules of 16 bytes that hold the piece; of the tensor's first and last,
+                    // which may reach beyond it, only what is of it is read.
+                    const char *const base = reinterpret_cast<const char *>(f_p == 0 ? a.w1 : a.w2);
+                    const char *const end = base + (f_p == 0 ? static_cast<int64_t>(a.F) * parts : a.O) * a.E * K * 2;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (!(f_rows >> i & 1)) continue;
+                        const char *const first = f_row[i >> 2] + off + static_cast<int64_t>(i & 3) * 4 * K;
+                        const char *const last = first + min(n, STAGE_COLS) * 2;
+                        uint8_t *const row = to + ((lane >> 4) + 2 * i) * L::W_PITCH;
+                        const char *src = reinterpret_cast<const char *>(reinterpret_cast<uintptr_t>(first) & ~static_cast<uintptr_t>(15));
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {   // and the seventeenth granule, by the first lane
+                            const int gran = q == 0 ? piece : 16;
+                            const char *const at = src + gran * 16;
+                            if ((q == 1 && piece != 0) || at >= last) continue;
+                            if (at < base) {
+                                for (const char *v = first; v < at + 16 && v < last; v += 2)
+                                    *reinterpret_cast<uint16_t *>(row + (v - src)) = __ldg(reinterpret_cast<const uint16_t *>(v));
+                            } else {
+                                copy16(smem_u32(row) + gran * 16, at, end - at < 16 ? static_cast<int>(end - at) : 16);
+                            }
+                        }
+                    }
+                }
+                f_k += KC;
+                if (f_k >= K) {
+                    f_k = 0;
+                    f_u += step;
+                    aim();
+                }
+            }
+            copy_commit();
+        };
+        aim();
+#pragma unroll
+        for (int i = 0; i < STAGES; ++i) fetch(i);
+
+        int ws = 0, bs = 0, reds = 0;
+        uint32_t bp = 0, rp = 0;
         bool on = true;
         for (int p = 0; p < 2; ++p) {
             const int K = depth[p], nb = blocks[p], units = entries * nb;
@@ -510,41 +540,40 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
                     for (int i = 0; i < 4; ++i) acc[t][i] = 0.0f;
                 uint32_t shift[2] = {0, 0};   // where a row's first value lies in its granule
                 if (ODD) {
-                    const int64_t rows_of_one = p == 0 ? static_cast<int64_t>(a.F) * (gated ? 2 : 1) : a.O;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int r = rg * 16 + g + 8 * i;
-                        const int64_t row = p == 0 && gated ? block * FU + (r >> 4) * 8 + (r & 7) + (r & 8 ? a.F : 0)
-                                                            : block * U + r;
+                    for (int i = 0; i < 2; ++i)
                         shift[i] = static_cast<uint32_t>((reinterpret_cast<uintptr_t>(p == 0 ? a.w1 : a.w2) +
-                                                          (en.expert * rows_of_one + row) * K * 2) & 15u);
-                    }
+                                                          weight_row(p, en.expert, block, g + 8 * i) * K * 2) & 15u);
                 }
                 for (int k0 = 0; k0 < K; k0 += KC) {
-                    if (on) on = warp_wait(smem_u32(&s.full[ws]), wp, gave_up) && warp_wait(smem_u32(&s.b_full[bs]), bp, gave_up);
+                    copy_wait<STAGES - 1>();
+                    __syncwarp();
+                    if (on) on = warp_wait(smem_u32(&s.b_full[bs]), bp, gave_up);
                     if (on) {
-                        const int n = min(KC, K - k0);
-                        const uint32_t w_at = w_ring + ws * L::W_STAGE + (rg * 16 + g) * PITCH;
-                        const uint32_t b_at = b_ring + bs * L::B_STAGE + g * PITCH;
+                        const int n = min(KC, K - k0) - kg * STAGE_COLS;   // columns of this warp
+                        const uint32_t w_at = smem_u32(ring + ws * L::W_STAGE) + g * L::W_PITCH;
+                        const uint32_t b_at = b_ring + bs * L::B_STAGE + g * L::B_PITCH + kg * STAGE_COLS * 2;
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const int col = kg * 128 + q * 32 + c * 8;
+                            const int col = q * 32 + c * 8;
                             uint4 a0 = make_uint4(0, 0, 0, 0), a1 = a0;
                             const bool in = col < n;
                             if (!ODD) {
                                 if (in) {
-                                    a0 = lds128(w_at + col * 2);
-                                    a1 = lds128(w_at + 8 * PITCH + col * 2);
+                                    const uint32_t from = w_at + ((q * 4 + c) ^ (g & 1) << 2) * 16;
+                                    a0 = lds128(from);
+                                    a1 = lds128(from + 8 * L::W_PITCH);
                                 }
                             } else if (in) {
                                 uint32_t v[2][4];
 #pragma unroll
                                 for (int i = 0; i < 2; ++i) {
-                                    const uint32_t from = w_at + 8 * i * PITCH + ((shift[i] + col * 2) & ~3u);
+                                    const uint32_t from = w_at + 8 * i * L::W_PITCH + ((shift[i] + col * 2) & ~3u);
                                     const uint32_t by = (shift[i] & 2u) * 8u;
                                     uint32_t word[5];
 #pragma unroll
-                                    for (int j = 0; j < 5; ++j) word[j] = lds32(from + 4 * j);
+                                    for (int j = 0; j < 4; ++j) word[j] = lds32(from + 4 * j);
+                                    word[4] = by != 0 ? lds32(from + 16) : 0u;
 #pragma unroll
                                     for (int j = 0; j < 4; ++j) {
                                         // past the row's end is another row, or what the ring held before
@@ -560,96 +589,134 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
                             for (int t = 0; t < NT; ++t) {
                                 if (t >= tiles) break;
                                 uint4 b = make_uint4(0, 0, 0, 0);
-                                if (in) b = lds128(b_at + t * 8 * PITCH + col * 2);
+                                if (in) b = lds128(b_at + t * 8 * L::B_PITCH + col * 2);
                                 mma16816(acc[t], a0.x, a1.x, a0.y, a1.y, b.x, b.y);
                                 mma16816(acc[t], a0.z, a1.z, a0.w, a1.w, b.z, b.w);
+                                if (p == 1) {
+                                    if (in) b = lds128(b_at + (TOKENS + t * 8) * L::B_PITCH + col * 2);
+                                    mma16816(acc[t], a0.x, a1.x, a0.y, a1.y, b.x, b.y);
+                                    mma16816(acc[t], a0.z, a1.z, a0.w, a1.w, b.z, b.w);
+                                }
                             }
                         }
                         __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(smem_u32(&s.empty[ws]));
-                            mbar_arrive(smem_u32(&s.b_empty[bs]));
-                        }
+                        if (lane == 0) mbar_arrive(smem_u32(&s.b_empty[bs]));
                     }
-                    if (++ws == stages) {
-                        ws = 0;
-                        wp ^= 1u;
-                    }
+                    fetch(ws);
+                    if (++ws == STAGES) ws = 0;
                     if (++bs == L::B_STAGES) {
                         bs = 0;
                         bp ^= 1u;
                     }
                 }
-                // The warps' shares of the columns, joined in order.  Two buffers in turn: a
-                // thread still reading one is waited for by the barrier of the next unit.
-                float *const to = red + buffer * L::RED;
-                buffer ^= 1;
+                if (on) on = warp_wait(smem_u32(&s.red_empty[reds]), rp ^ 1u, gave_up);
+                if (on) {
+                    float *const to = red + reds * L::RED;
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    if (t >= tiles) break;
+                    for (int t = 0; t < NT; ++t) {
+                        if (t >= tiles) break;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        to[(kg * TOKENS + t * 8 + 2 * c + (i & 1)) * UP + rg * 16 + g + (i & 2 ? 8 : 0)] = acc[t][i];
+                        for (int i = 0; i < 4; ++i)
+                            to[(kg * TOKENS + t * 8 + 2 * c + (i & 1)) * UP + rg * 16 + g + (i & 2 ? 8 : 0)] = acc[t][i];
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&s.red_full[reds]));
                 }
-                math_barrier();
-                const auto joined = [&](int token, int row) {
-                    float v = to[token * UP + row];
+                if (++reds == L::REDS) {
+                    reds = 0;
+                    rp ^= 1u;
+                }
+            }
+        }
+        copy_wait<0>();
+    } else {
+        const int tid = threadIdx.x - MATH_THREADS - 32;
+        int reds = 0;
+        uint32_t rp = 0;
+        bool on = true;
+        for (int p = 0; p < 2; ++p) {
+            const int nb = blocks[p], units = entries * nb;
+            for (int u = blockIdx.x; u < units; u += step) {
+                const typename L::Entry en = entry[u / nb];
+                const int block = u % nb;
+                if (on) on = warp_wait(smem_u32(&s.red_full[reds]), rp, gave_up);
+                if (on) {
+                    const float *const from = red + reds * L::RED;
+                    // The warps' shares of the columns, in order.
+                    const auto joined = [&](int token, int row) {
+                        float v = from[token * UP + row];
 #pragma unroll
-                    for (int k = 1; k < KG; ++k) v += to[(k * TOKENS + token) * UP + row];
-                    return v;
-                };
-                if (p == 0) {
-                    const mp_bf16_t *b1 = a.b1 == nullptr ? nullptr
-                                                          : a.b1 + static_cast<int64_t>(en.expert) * a.F * (gated ? 2 : 1);
-                    for (int i = threadIdx.x; i < FU * en.count; i += MATH_THREADS) {
-                        const int token = i / FU, j = i - token * FU, f = block * FU + j;
-                        if (f >= a.Fp) continue;
-                        float h[1] = {0.0f};   // up to a row's last 16 bytes
-                        if (f < a.F) {
-                            float z = joined(token, gated ? (j >> 3) * 16 + (j & 7) : j);
-                            if (b1 != nullptr) z += bf16_value(b1 + f);
-                            z = act_of(a.act, z);
-                            if (gated) {
-                                float o = joined(token, (j >> 3) * 16 + (j & 7) + 8);
-                                if (b1 != nullptr) o += bf16_value(b1 + a.F + f);
-                                z *= o;
+                        for (int k = 1; k < KG; ++k) v += from[(k * TOKENS + token) * UP + row];
+                        return v;
+                    };
+                    if (p == 0) {
+                        const mp_bf16_t *b1 = a.b1 == nullptr ? nullptr
+                                                              : a.b1 + static_cast<int64_t>(en.expert) * a.F * (gated ? 2 : 1);
+                        for (int i = tid; i < FU * en.count; i += JOIN_THREADS) {
+                            const int token = i / FU, j = i - token * FU, f = block * FU + j;
+                            if (f >= a.Fp) continue;
+                            float h = 0.0f;   // up to a row's last 16 bytes
+                            if (f < a.F) {
+                                // Rows of the products: tiles of 8 of the gate and 8 of the other half.
+                                h = joined(token, gated ? (j >> 3) * 16 + (j & 7) : j);
+                                if (b1 != nullptr) h += bf16_value(b1 + f);
+                                h = act_of(a.act, h);
+                                if (gated) {
+                                    float o = joined(token, (j >> 3) * 16 + (j & 7) + 8);
+                                    if (b1 != nullptr) o += bf16_value(b1 + a.F + f);
+                                    h *= o;
+                                }
                             }
-                            h[0] = z;
+                            mp_bf16_t *const to = a.h + static_cast<int64_t>(order[en.first + token]) * 2 * a.Fp + f;
+                            const float value[1] = {h};
+                            const mp_bf16_t near = pack(value);
+                            float back[1];
+                            unpack(near, back);
+                            const float rest[1] = {isfinite(back[0]) ? h - back[0] : 0.0f};
+                            to[0] = near;
+                            to[a.Fp] = pack(rest);
                         }
-                        a.h[static_cast<int64_t>(order[en.first + token]) * a.Fp + f] = pack(h);
+                    } else {
+                        const mp_bf16_t *b2 = a.b2 == nullptr ? nullptr : a.b2 + static_cast<int64_t>(en.expert) * a.O;
+                        for (int i = tid; i < U * en.count; i += JOIN_THREADS) {
+                            const int token = i / U, j = i - token * U, o = block * U + j;
+                            if (o >= a.O) continue;
+                            float v = joined(token, j);
+                            if (b2 != nullptr) v += bf16_value(b2 + o);
+                            a.out[static_cast<int64_t>(order[en.first + token]) * a.O + o] = v;
+                        }
                     }
-                } else {
-                    const mp_bf16_t *b2 = a.b2 == nullptr ? nullptr : a.b2 + static_cast<int64_t>(en.expert) * a.O;
-                    for (int i = threadIdx.x; i < U * en.count; i += MATH_THREADS) {
-                        const int token = i / U, j = i - token * U, o = block * U + j;
-                        if (o >= a.O) continue;
-                        float v = joined(token, j);
-                        if (b2 != nullptr) v += bf16_value(b2 + o);
-                        a.out[static_cast<int64_t>(order[en.first + token]) * a.O + o] = v;
-                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&s.red_empty[reds]));
+                }
+                if (++reds == L::REDS) {
+                    reds = 0;
+                    rp ^= 1u;
                 }
             }
             // What this CTA made is there for the others: their copies read h.
             if (p == 0) fence_async();
             __threadfence();
-            math_barrier();
-            if (threadIdx.x == 0) grid_arrive(&a.control->arrived[p]);
+            join_barrier();
+            if (tid == 0) grid_arrive(&a.control->arrived[p]);
         }
-        if (threadIdx.x == 0) (void)grid_wait(&a.control->arrived[1], gridDim.x, gave_up);
-        math_barrier();
-        for (int64_t i = static_cast<int64_t>(blockIdx.x) * MATH_THREADS + threadIdx.x; i < static_cast<int64_t>(a.T) * a.O;
-             i += static_cast<int64_t>(gridDim.x) * MATH_THREADS) {
-            const int t = static_cast<int>(i / a.O), o = static_cast<int>(i - static_cast<int64_t>(t) * a.O);
-            float y = 0.0f;
-            for (int k = 0; k < a.K; ++k) {
-                const int r = t * a.K + k;
-                if (idx[r] >= 0) y = fmaf(weights[r], __ldcg(a.out + static_cast<int64_t>(r) * a.O + o), y);
-            }
-            const float v[1] = {y};
-            a.y[i] = pack(v);
-        }
-        if (threadIdx.x == 0 && *gave_up) or_status(a.status, MP_STATUS_STALLED);
+        if (tid == 0) (void)grid_wait(&a.control->arrived[1], gridDim.x, gave_up);
     }
+    if (warp == MATH_WARPS) return;
+    most_barrier();
+    const int tid = threadIdx.x < MATH_THREADS ? threadIdx.x : threadIdx.x - 32;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * (LAYER_THREADS - 32) + tid; i < static_cast<int64_t>(a.T) * a.O;
+         i += static_cast<int64_t>(gridDim.x) * (LAYER_THREADS - 32)) {
+        const int t = static_cast<int>(i / a.O), o = static_cast<int>(i - static_cast<int64_t>(t) * a.O);
+        float y = 0.0f;
+        for (int k = 0; k < a.K; ++k) {
+            const int r = t * a.K + k;
+            if (idx[r] >= 0) y = fmaf(weights[r], __ldcg(a.out + static_cast<int64_t>(r) * a.O + o), y);
+        }
+        const float v[1] = {y};
+        a.y[i] = pack(v);
+    }
+    if (tid == 0 && *gave_up) or_status(a.status, MP_STATUS_STALLED);
 }
 
 template <typename L> void launch_logits(const LayerArgs &a, cudaStream_t s)
@@ -670,9 +737,7 @@ template <int RG, int NT, bool ODD> mp_status_t launch_layer(const LayerArgs &a,
     static std::atomic<uint64_t> allowed{0};
     if (!allow_smem(k_layer<RG, NT, ODD>, allowed, LAYER_SMEM)) return MP_ERR_CUDA;
     const int R = a.T * a.K;
-    const size_t other = L::tables(a.E, R) + static_cast<size_t>(L::B_STAGES) * L::B_STAGE;
-    int stages = static_cast<int>((LAYER_SMEM - other) / L::W_STAGE);
-    if (stages > RING_MOST) stages = RING_MOST;
+    const size_t bytes = L::tables(a.E, R) + static_cast<size_t>(L::B_STAGES) * L::B_STAGE + static_cast<size_t>(L::STAGES) * L::W_STAGE;
     // No more CTAs than units: a barrier of few is quicker.
     const int FU = act_gated(a.act) ? L::U / 2 : L::U;
     const int64_t entries = (a.E < R ? a.E : R) + R / L::TOKENS;
@@ -681,7 +746,7 @@ template <int RG, int NT, bool ODD> mp_status_t launch_layer(const LayerArgs &a,
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = static_cast<unsigned>(units < sms ? units : sms);
     cfg.blockDim = LAYER_THREADS;
-    cfg.dynamicSmemBytes = other + static_cast<size_t>(stages) * L::W_STAGE;
+    cfg.dynamicSmemBytes = bytes;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeCooperative;
@@ -690,7 +755,7 @@ template <int RG, int NT, bool ODD> mp_status_t launch_layer(const LayerArgs &a,
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    (void)cudaLaunchKernelEx(&cfg, k_layer<RG, NT, ODD>, a, stages);
+    (void)cudaLaunchKernelEx(&cfg, k_layer<RG, NT, ODD>, a);
     return check_launch();
 }
 
@@ -721,7 +786,7 @@ struct LayerSpace {
         logits = 256;
         xp = next(logits, static_cast<size_t>(T * E) * 4);
         h = next(xp, static_cast<size_t>(T) * whole(H) * 2);
-        out = next(h, static_cast<size_t>(T * K) * whole(F) * 2);
+        out = next(h, static_cast<size_t>(T * K) * whole(F) * 4);
         bytes = next(out, static_cast<size_t>(T * K * O) * 4);
     }
 };
