@@ -49,6 +49,7 @@ constexpr int JOIN_WARPS = 4, JOIN_THREADS = 32 * JOIN_WARPS;
 constexpr int LAYER_THREADS = MATH_THREADS + 32 + JOIN_THREADS;   // and a warp of copies
 constexpr int STAGE_COLS = 128;          // of a warp
 constexpr int ROW_PAD = 64;              // bytes between tokens' rows
+constexpr int B_MOST = 8, RED_MOST = 4;  // slots for tokens' rows, buffers of sums
 constexpr size_t LAYER_SMEM = 227 * 1024;
 
 struct LayerControl {
@@ -210,9 +211,17 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 {
     return __all_sync(FULL_MASK, mbar_wait(bar, parity, gave_up)) != 0;
 }
-// The joining warps; all but the warp of copies.
-__device__ __forceinline__ void join_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(JOIN_THREADS) : "memory"); }
-__device__ __forceinline__ void most_barrier() { asm volatile("bar.sync 2, %0;" ::"n"(LAYER_THREADS - 32) : "memory"); }
+// The joining warps; all but the warp of copies.  A warp comes to a barrier as a whole.
+__device__ __forceinline__ void join_barrier()
+{
+    __syncwarp();
+    asm volatile("bar.sync 1, %0;" ::"n"(JOIN_THREADS) : "memory");
+}
+__device__ __forceinline__ void most_barrier()
+{
+    __syncwarp();
+    asm volatile("bar.sync 2, %0;" ::"n"(LAYER_THREADS - 32) : "memory");
+}
 
 // Waits until `count` CTAs have arrived; at most 4 s.
 __device__ __forceinline__ bool grid_wait(const unsigned *arrived, unsigned count, volatile int *gave_up)
@@ -247,7 +256,9 @@ __device__ __forceinline__ float act_of(int act, float z)
 // One token's choice by one warp; results through `r`.
 __device__ __noinline__ void route_one(const RouteArgs &r, const float *logits, int t, int lane)
 {
-    if (r.E <= 128)
+    if (r.E <= 128 && r.K == 8)
+        route_token<float, 4, 8>(r, logits, t, lane);
+    else if (r.E <= 128)
         route_token<float, 4, 0>(r, logits, t, lane);
     else if (r.E <= 256)
         route_token<float, 8, 0>(r, logits, t, lane);
@@ -255,48 +266,58 @@ __device__ __noinline__ void route_one(const RouteArgs &r, const float *logits, 
         route_token<float, 32, 0>(r, logits, t, lane);
 }
 
-// RG groups of 16 weight rows, the eight warps' KG = 8 / RG shares of the columns; up to
-// 8 NT tokens an entry.  ODD: weight rows that start anywhere.
-template <int RG, int NT, bool ODD> struct Layer {
-    static constexpr int U = 16 * RG, KG = MATH_WARPS / RG, KC = STAGE_COLS * KG, TOKENS = 8 * NT;
+// How a product is cut.  The eight warps are RG groups of 16 weight rows by KG shares of a stage's
+// columns, RG KG = 8: a unit is U = 16 RG rows, a stage KC = 128 KG columns.
+struct Cut {
+    int log_kg;
+    int b_stages;   // slots for the tokens' rows
+    __host__ __device__ int kg() const { return 1 << log_kg; }
+    __host__ __device__ int u() const { return 128 >> log_kg; }
+    __host__ __device__ int kc() const { return STAGE_COLS << log_kg; }
+    __host__ __device__ int b_pitch() const { return kc() * 2 + ROW_PAD; }
+};
+struct LayerCuts {
+    Cut of[2];      // of the first product and of the second
+    int b_rows;     // tokens' rows in a slot; twice as many of the second product, both values of h
+    int reds;       // buffers for the units' sums
+};
+
+// Up to 8 NT tokens an entry.  ODD: weight rows that start anywhere.
+template <int NT, bool ODD> struct Layer {
+    static constexpr int TOKENS = 8 * NT;
     static constexpr int W_PITCH = STAGE_COLS * 2 + (ODD ? 16 : 0);   // a row that starts anywhere takes a granule more
     static constexpr int W_STAGE = MATH_WARPS * 16 * W_PITCH;
-    static constexpr int B_PITCH = KC * 2 + ROW_PAD;
-    static constexpr int B_STAGE = 2 * TOKENS * B_PITCH;    // both values of h
-    static constexpr int B_STAGES = NT == 2 ? 3 : 2;
-    static constexpr int STAGES = RG == 1 ? 4 : NT == 4 ? 3 : 4;
-    static constexpr int UP = U + 4;                        // of a partial sum's column: banks apart
-    static constexpr int RED = KG * TOKENS * UP;            // floats of a unit's sums
-    static constexpr int REDS = NT == 4 ? 1 : 2;
+    static constexpr int STAGES = NT == 4 ? 3 : 4;
+    static constexpr int RED = 160 * TOKENS;   // floats: KG columns' shares, TOKENS, U rows and 4 to part the banks
     struct Entry {
         int expert, first, count;   // tokens' routes: order[first ..]
     };
     struct Shared {
-        uint64_t b_full[B_STAGES], b_empty[B_STAGES], red_full[REDS], red_empty[REDS];
+        uint64_t b_full[2][B_MOST], b_empty[2][B_MOST], red_full[RED_MOST], red_empty[RED_MOST];
         int gave_up, entries;
     };
-    // After the rings: the units' sums; order, counts, entries; idx and weights of few tokens.
+    // After the rings and the units' sums: order, counts, entries; idx and weights of few tokens.
     static size_t tables(int E, int R)
     {
         const int entries = (E < R ? E : R) + R / TOKENS;
-        return sizeof(Shared) + REDS * RED * 4 + (static_cast<size_t>(R) + 2 * E) * 4 + static_cast<size_t>(entries) * sizeof(Entry) +
+        return sizeof(Shared) + (static_cast<size_t>(R) + 2 * E) * 4 + static_cast<size_t>(entries) * sizeof(Entry) +
                static_cast<size_t>(ROUTE_TOKENS) * 32 * 8 + 64;
     }
 };
 
-template <int RG, int NT, bool ODD>
-__global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a)
+template <int NT, bool ODD>
+__global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, const LayerCuts cuts, const int b_bytes)
 {
-    typedef Layer<RG, NT, ODD> L;
-    constexpr int U = L::U, KG = L::KG, KC = L::KC, TOKENS = L::TOKENS, UP = L::UP, STAGES = L::STAGES;
+    typedef Layer<NT, ODD> L;
+    constexpr int TOKENS = L::TOKENS, STAGES = L::STAGES;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, R = a.T * a.K;
     const uint32_t b_ring = smem_u32(smem) + STAGES * L::W_STAGE;
-    uint8_t *at = smem + STAGES * L::W_STAGE + L::B_STAGES * L::B_STAGE;
+    uint8_t *at = smem + STAGES * L::W_STAGE + b_bytes;
     typename L::Shared &s = *reinterpret_cast<typename L::Shared *>(at);
     at += sizeof(typename L::Shared);
     float *const red = reinterpret_cast<float *>(at);
-    at += L::REDS * L::RED * 4;
+    at += cuts.reds * L::RED * 4;
     int *const order = reinterpret_cast<int *>(at), *const count = order + R, *const start = count + a.E;
     typename L::Entry *const entry = reinterpret_cast<typename L::Entry *>(start + a.E);
     int32_t *const my_idx = reinterpret_cast<int32_t *>(entry + min(a.E, R) + R / TOKENS);
@@ -304,11 +325,12 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a)
     volatile int *gave_up = &s.gave_up;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < L::B_STAGES; ++i) {
-            mbar_init(smem_u32(&s.b_full[i]), 1);
-            mbar_init(smem_u32(&s.b_empty[i]), MATH_WARPS);
-        }
-        for (int i = 0; i < L::REDS; ++i) {
+        for (int p = 0; p < 2; ++p)
+            for (int i = 0; i < B_MOST; ++i) {
+                mbar_init(smem_u32(&s.b_full[p][i]), 1);
+                mbar_init(smem_u32(&s.b_empty[p][i]), MATH_WARPS);
+            }
+        for (int i = 0; i < RED_MOST; ++i) {
             mbar_init(smem_u32(&s.red_full[i]), MATH_WARPS);
             mbar_init(smem_u32(&s.red_empty[i]), JOIN_WARPS);
         }
@@ -340,10 +362,40 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a)
         }
     // Routes by expert, in their order (every CTA has to come to the same entries), and entries
     // of up to TOKENS of them.
-    for (int r = threadIdx.x; r < R; r += LAYER_THREADS)
-        if (idx[r] >= 0) atomicAdd(count + idx[r], 1);
-    __syncthreads();
-    if (warp == 0) {
+    if (R <= 32) {
+        // Experts in the order of their first routes.
+        if (warp == 0) {
+            const int e = lane < R ? idx[lane] : -1;
+            const unsigned same = __match_any_sync(FULL_MASK, e), below = (1u << lane) - 1u;
+            const int rank = __popc(same & below), n = __popc(same), first = __ffs(same) - 1;
+            const bool leads = e >= 0 && rank == 0;
+            int before = leads ? n : 0;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(FULL_MASK, before, d);
+                if (lane >= d) before += o;
+            }
+            before -= leads ? n : 0;
+            const int from = __shfl_sync(FULL_MASK, before, first);
+            if (e >= 0) order[from + rank] = lane;
+            // An entry takes up to TOKENS routes: a leader's follow those of the leaders before it.
+            const int parts = leads ? (n + TOKENS - 1) / TOKENS : 0;
+            int slot = parts;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(FULL_MASK, slot, d);
+                if (lane >= d) slot += o;
+            }
+            if (lane == 31) s.entries = slot;
+            slot -= parts;
+            for (int i = 0; i < parts; ++i) entry[slot + i] = {e, from + i * TOKENS, min(TOKENS, n - i * TOKENS)};
+        }
+    } else {
+        for (int r = threadIdx.x; r < R; r += LAYER_THREADS)
+            if (idx[r] >= 0) atomicAdd(count + idx[r], 1);
+        __syncthreads();
+    }
+    if (R > 32 && warp == 0) {
         int routes = 0, entries = 0;
         for (int e0 = 0; e0 < a.E; e0 += 32) {
             const int e = e0 + lane, n = e < a.E ? count[e] : 0, parts = (n + TOKENS - 1) / TOKENS;
@@ -381,19 +433,37 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a)
 
     const bool gated = act_gated(a.act);
     const int entries = s.entries;
-    const int FU = gated ? U / 2 : U;   // columns of h that a unit makes
-    const int blocks[2] = {(a.F + FU - 1) / FU, (a.O + U - 1) / U};
-    const int depth[2] = {a.H, a.F};
+    const int FU = gated ? cuts.of[0].u() / 2 : cuts.of[0].u();   // columns of h that a unit makes
+    const int blocks0 = (a.F + FU - 1) / FU, blocks1 = (a.O + cuts.of[1].u() - 1) / cuts.of[1].u();
     const int step = gridDim.x;
+
+    // The units of a CTA, one after another.
+    struct Walk {
+        int u, entry, block, nb, by_entry, by_block;
+        __device__ __forceinline__ Walk(int from, int step, int blocks) : u(from), nb(blocks)
+        {
+            entry = from / blocks; block = from - entry * blocks;
+            by_entry = step / blocks; by_block = step - by_entry * blocks;
+        }
+        __device__ __forceinline__ void next(int step)
+        {
+            u += step;
+            entry += by_entry;
+            block += by_block;
+            if (block >= nb) {
+                block -= nb;
+                ++entry;
+            }
+        }
+    };
 
     if (warp == MATH_WARPS) {
         // The tokens' rows: x, and after the grid's barrier h.
-        int at_stage = 0;
-        uint32_t phase = 0;
-        int64_t issued = 0;
         bool on = true;
         for (int p = 0; p < 2 && on; ++p) {
-            const int K = p == 0 ? a.Hp : a.Fp, nb = blocks[p], units = entries * nb;
+            const Cut cut = cuts.of[p];
+            const int K = p == 0 ? a.Hp : a.Fp, units = entries * (p == 0 ? blocks0 : blocks1), KC = cut.kc();
+            const int pitch = cut.b_pitch(), slot = cuts.b_rows * (p + 1) * pitch;
             const mp_bf16_t *const base = p == 0 ? (a.xp != nullptr ? a.xp : a.x) : a.h;
             if (p == 1) {
                 if (lane == 0) on = grid_wait(&a.control->arrived[0], gridDim.x, gave_up);
@@ -401,82 +471,99 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a)
                 __syncwarp();
                 fence_async();   // what other SMs stored, by the copies to come
             }
-            for (int u = blockIdx.x; u < units && on; u += step) {
-                const typename L::Entry en = entry[u / nb];
+            int at_stage = 0, issued = 0;
+            uint32_t phase = 0;
+            for (Walk w(blockIdx.x, step, p == 0 ? blocks0 : blocks1); w.u < units && on; w.next(step)) {
+                const typename L::Entry en = entry[w.entry];
                 const mp_bf16_t *row = base;
                 if (lane < en.count) {
                     const int r = order[en.first + lane];
                     row += static_cast<int64_t>(p == 0 ? r / a.K : 2 * r) * K;
                 }
                 for (int k0 = 0; k0 < K; k0 += KC) {
-                    on = warp_wait(smem_u32(&s.b_empty[at_stage]), phase ^ 1u, gave_up);
+                    on = warp_wait(smem_u32(&s.b_empty[p][at_stage]), phase ^ 1u, gave_up);
                     if (!on) break;
-                    const uint32_t bar = smem_u32(&s.b_full[at_stage]), to = b_ring + at_stage * L::B_STAGE;
+                    const uint32_t bar = smem_u32(&s.b_full[p][at_stage]), to = b_ring + at_stage * slot;
                     const uint32_t bytes = static_cast<uint32_t>(min(KC, K - k0)) * 2u;
                     if (lane == 0) mbar_expect(bar, bytes * en.count * (p + 1));
                     __syncwarp();
                     if (lane < en.count) {
-                        bulk_load(to + lane * L::B_PITCH, row + k0, bytes, bar);
-                        if (p == 1) bulk_load(to + (TOKENS + lane) * L::B_PITCH, row + K + k0, bytes, bar);
+                        bulk_load(to + lane * pitch, row + k0, bytes, bar);
+                        if (p == 1) bulk_load(to + (cuts.b_rows + lane) * pitch, row + K + k0, bytes, bar);
                     }
-                    ++issued;
-                    if (++at_stage == L::B_STAGES) {
+                    if (issued < B_MOST) ++issued;
+                    if (++at_stage == cut.b_stages) {
                         at_stage = 0;
                         phase ^= 1u;
                     }
                 }
             }
-        }
-        if (*gave_up && lane == 0)
-            for (int i = 0; i < L::B_STAGES && i < issued; ++i) {
-                if (--at_stage < 0) {
-                    at_stage = L::B_STAGES - 1;
-                    phase ^= 1u;
+            if (*gave_up && lane == 0)   // copies in flight land before the shared memory goes
+                for (int i = 0; i < cut.b_stages && i < issued; ++i) {
+                    if (--at_stage < 0) {
+                        at_stage = cut.b_stages - 1;
+                        phase ^= 1u;
+                    }
+                    mbar_drain(smem_u32(&s.b_full[p][at_stage]), phase);
                 }
-                mbar_drain(smem_u32(&s.b_full[at_stage]), phase);
-            }
+        }
     } else if (warp < MATH_WARPS) {
         // A warp that gives up a wait goes on without waiting or multiplying, so that the barriers
         // of the others come to their ends.
-        const int rg = warp / KG, kg = warp % KG, g = lane >> 2, c = lane & 3;
-        const int parts = gated ? 2 : 1;
+        const int g = lane >> 2, c = lane & 3;
         uint8_t *const ring = smem + warp * 16 * L::W_PITCH;
-        // A row of the group's 16, of unit (expert, block) in product p; -1: there is none.
-        const auto weight_row = [&](int p, int expert, int block, int i) -> int64_t {
+        // Row i of group rg of a unit of product p: its row in the expert's weights, -1: there is none.
+        const auto weight_row = [&](int p, int block, int rg, int i) {
             if (p == 0 && gated) {   // 8 rows of the gate, 8 of the other half
                 const int f = block * FU + rg * 8 + (i & 7);
-                return f < a.F ? static_cast<int64_t>(expert) * 2 * a.F + f + (i & 8 ? a.F : 0) : -1;
+                return f < a.F ? f + (i & 8 ? a.F : 0) : -1;
             }
-            const int f = block * U + rg * 16 + i, rows = p == 0 ? a.F : a.O;
-            return f < rows ? static_cast<int64_t>(expert) * rows + f : -1;
+            const int f = block * cuts.of[p].u() + rg * 16 + i;
+            return f < (p == 0 ? a.F : a.O) ? f : -1;
         };
+        const int rows_of[2] = {a.F * (gated ? 2 : 1), a.O};   // of one expert
         // The stage that is copied next: its product, unit and first column, and where this lane's
         // part of the unit's rows is: pieces of 16 bytes lane & 15, of rows lane >> 4 and every other on.
-        int f_p = 0, f_u = blockIdx.x, f_k = 0;
+        int f_p = 0, f_k = 0, f_depth = a.H, f_kc = cuts.of[0].kc(), f_rg = warp >> cuts.of[0].log_kg;
+        int f_col = (warp & (cuts.of[0].kg() - 1)) * STAGE_COLS;   // this warp's columns of a stage
+        Walk f_walk(blockIdx.x, step, blocks0);
         const char *f_row[2];
-        int f_rows = 0;        // a bit for each of the eight rows that is there
+        unsigned f_rows = 0;   // a bit for each of the eight rows that is there
         const auto aim = [&]() {
-            while (f_p < 2 && f_u >= entries * blocks[f_p]) {
-                ++f_p;
-                f_u = blockIdx.x;
+            if (f_p == 0 && f_walk.u >= entries * blocks0) {
+                f_p = 1;
+                f_walk = Walk(blockIdx.x, step, blocks1);
+                f_depth = a.F;
+                f_kc = cuts.of[1].kc();
+                f_rg = warp >> cuts.of[1].log_kg;
+                f_col = (warp & (cuts.of[1].kg() - 1)) * STAGE_COLS;
             }
+            if (f_p == 1 && f_walk.u >= entries * blocks1) f_p = 2;
             if (f_p == 2) return;
-            const int nb = blocks[f_p], e = entry[f_u / nb].expert, block = f_u % nb;
-            const char *const base = reinterpret_cast<const char *>(f_p == 0 ? a.w1 : a.w2);
+            const char *const base = reinterpret_cast<const char *>(f_p == 0 ? a.w1 : a.w2) +
+                                     static_cast<int64_t>(entry[f_walk.entry].expert) * (f_p == 0 ? rows_of[0] : rows_of[1]) * f_depth * 2;
+            // Rows 2 apart lie 2 rows apart, but for the step into the other half.
             f_rows = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f_rows |= (weight_row(f_p, e, block, (lane >> 4) + 2 * i) >= 0) << i;
-            // Rows 2 apart lie 2 rows apart, but for the step into the other half.
+            for (int i = 0; i < 2; ++i) {
+                const int first = weight_row(f_p, f_walk.block, f_rg, (lane >> 4) + 8 * i);
+                const int last = weight_row(f_p, f_walk.block, f_rg, (lane >> 4) + 8 * i + 6);
+                f_row[i] = base + static_cast<int64_t>(first) * f_depth * 2;
+                if (last >= 0) {
+                    f_rows |= 15u << 4 * i;
+                } else {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                f_row[i] = base + weight_row(f_p, e, block, (lane >> 4) + 8 * i) * depth[f_p] * 2;
+                    for (int j = 0; j < 3; ++j)
+                        f_rows |= static_cast<unsigned>(weight_row(f_p, f_walk.block, f_rg, (lane >> 4) + 8 * i + 2 * j) >= 0) << (4 * i + j);
+                }
+            }
         };
         const auto fetch = [&](int stage) {
             if (f_p < 2) {
-                const int K = depth[f_p], n = K - f_k - kg * STAGE_COLS;   // columns that are there
+                const int n = f_depth - f_k - f_col;   // columns that are there
                 const int piece = lane & 15;
                 uint8_t *const to = ring + stage * L::W_STAGE;
-                const int64_t off = (static_cast<int64_t>(f_k) + kg * STAGE_COLS) * 2;
+                const int64_t off = (static_cast<int64_t>(f_k) + f_col) * 2;
                 if (!ODD) {
                     if (piece * 8 < n) {
                         const uint32_t dst = smem_u32(to) + (lane >> 4) * L::W_PITCH + (piece ^ ((lane >> 4) & 1) << 2) * 16;
@@ -484,38 +571,38 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a)
                         for (int i = 0; i < 8; ++i)
                             if (f_rows >> i & 1)
                                 copy16(dst + 2 * i * L::W_PITCH,
-                                       f_row[i >> 2] + off + piece * 16 + static_cast<int64_t>(i & 3) * 4 * K);
+                                       f_row[i >> 2] + off + piece * 16 + static_cast<int64_t>(i & 3) * 4 * f_depth);
                     }
                 } else if (n > 0) {
                     // The granules of 16 bytes that hold the piece; of the tensor's first and last,
                     // which may reach beyond it, only what is of it is read.
                     const char *const base = reinterpret_cast<const char *>(f_p == 0 ? a.w1 : a.w2);
-                    const char *const end = base + (f_p == 0 ? static_cast<int64_t>(a.F) * parts : a.O) * a.E * K * 2;
+                    const char *const end = base + static_cast<int64_t>(f_p == 0 ? rows_of[0] : rows_of[1]) * a.E * f_depth * 2;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         if (!(f_rows >> i & 1)) continue;
-                        const char *const first = f_row[i >> 2] + off + static_cast<int64_t>(i & 3) * 4 * K;
+                        const char *const first = f_row[i >> 2] + off + static_cast<int64_t>(i & 3) * 4 * f_depth;
                         const char *const last = first + min(n, STAGE_COLS) * 2;
                         uint8_t *const row = to + ((lane >> 4) + 2 * i) * L::W_PITCH;
                         const char *src = reinterpret_cast<const char *>(reinterpret_cast<uintptr_t>(first) & ~static_cast<uintptr_t>(15));
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {   // and the seventeenth granule, by the first lane
                             const int gran = q == 0 ? piece : 16;
-                            const char *const at = src + gran * 16;
-                            if ((q == 1 && piece != 0) || at >= last) continue;
-                            if (at < base) {
-                                for (const char *v = first; v < at + 16 && v < last; v += 2)
+                            const char *const from = src + gran * 16;
+                            if ((q == 1 && piece != 0) || from >= last) continue;
+                            if (from < base) {
+                                for (const char *v = first; v < from + 16 && v < last; v += 2)
                                     *reinterpret_cast<uint16_t *>(row + (v - src)) = __ldg(reinterpret_cast<const uint16_t *>(v));
                             } else {
-                                copy16(smem_u32(row) + gran * 16, at, end - at < 16 ? static_cast<int>(end - at) : 16);
+                                copy16(smem_u32(row) + gran * 16, from, end - from < 16 ? static_cast<int>(end - from) : 16);
                             }
                         }
                     }
                 }
-                f_k += KC;
-                if (f_k >= K) {
+                f_k += f_kc;
+                if (f_k >= f_depth) {
                     f_k = 0;
-                    f_u += step;
+                    f_walk.next(step);
                     aim();
                 }
             }
@@ -525,34 +612,44 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a)
 #pragma unroll
         for (int i = 0; i < STAGES; ++i) fetch(i);
 
-        int ws = 0, bs = 0, reds = 0;
-        uint32_t bp = 0, rp = 0;
+        int ws = 0, reds = 0;
+        uint32_t rp = 0;
         bool on = true;
         for (int p = 0; p < 2; ++p) {
-            const int K = depth[p], nb = blocks[p], units = entries * nb;
-            for (int u = blockIdx.x; u < units; u += step) {
-                const typename L::Entry en = entry[u / nb];
-                const int block = u % nb, tiles = (en.count + 7) >> 3;
-                float acc[NT][4];
+            const Cut cut = cuts.of[p];
+            const int K = p == 0 ? a.H : a.F, units = entries * (p == 0 ? blocks0 : blocks1), KC = cut.kc();
+            const int rg = warp >> cut.log_kg, kg = warp & (cut.kg() - 1), UP = cut.u() + 4;
+            const int pitch = cut.b_pitch(), slot = cuts.b_rows * (p + 1) * pitch;
+            // A column past the last token takes any row that is there: nobody reads its sums.
+            int b_row[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) b_row[t] = min(t * 8 + g, cuts.b_rows - 1) * pitch;
+            int bs = 0;
+            uint32_t bp = 0;
+            for (Walk w(blockIdx.x, step, p == 0 ? blocks0 : blocks1); w.u < units; w.next(step)) {
+                const typename L::Entry en = entry[w.entry];
+                const int tiles = (en.count + 7) >> 3;
+                float acc[NT][2][4];   // two sums a tile: products that do not wait for one another
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[t][i] = 0.0f;
+                    for (int i = 0; i < 8; ++i) acc[t][i >> 2][i & 3] = 0.0f;
                 uint32_t shift[2] = {0, 0};   // where a row's first value lies in its granule
                 if (ODD) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
                         shift[i] = static_cast<uint32_t>((reinterpret_cast<uintptr_t>(p == 0 ? a.w1 : a.w2) +
-                                                          weight_row(p, en.expert, block, g + 8 * i) * K * 2) & 15u);
+                                                          (static_cast<int64_t>(en.expert) * rows_of[p] +
+                                                           weight_row(p, w.block, rg, g + 8 * i)) * K * 2) & 15u);
                 }
                 for (int k0 = 0; k0 < K; k0 += KC) {
                     copy_wait<STAGES - 1>();
                     __syncwarp();
-                    if (on) on = warp_wait(smem_u32(&s.b_full[bs]), bp, gave_up);
+                    if (on) on = warp_wait(smem_u32(&s.b_full[p][bs]), bp, gave_up);
                     if (on) {
                         const int n = min(KC, K - k0) - kg * STAGE_COLS;   // columns of this warp
                         const uint32_t w_at = smem_u32(ring + ws * L::W_STAGE) + g * L::W_PITCH;
-                        const uint32_t b_at = b_ring + bs * L::B_STAGE + g * L::B_PITCH + kg * STAGE_COLS * 2;
+                        const uint32_t b_at = b_ring + bs * slot + kg * STAGE_COLS * 2, b_rest = cuts.b_rows * pitch;
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const int col = q * 32 + c * 8;
@@ -589,22 +686,22 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a)
                             for (int t = 0; t < NT; ++t) {
                                 if (t >= tiles) break;
                                 uint4 b = make_uint4(0, 0, 0, 0);
-                                if (in) b = lds128(b_at + t * 8 * L::B_PITCH + col * 2);
-                                mma16816(acc[t], a0.x, a1.x, a0.y, a1.y, b.x, b.y);
-                                mma16816(acc[t], a0.z, a1.z, a0.w, a1.w, b.z, b.w);
+                                if (in) b = lds128(b_at + b_row[t] + col * 2);
+                                mma16816(acc[t][0], a0.x, a1.x, a0.y, a1.y, b.x, b.y);
+                                mma16816(acc[t][1], a0.z, a1.z, a0.w, a1.w, b.z, b.w);
                                 if (p == 1) {
-                                    if (in) b = lds128(b_at + (TOKENS + t * 8) * L::B_PITCH + col * 2);
-                                    mma16816(acc[t], a0.x, a1.x, a0.y, a1.y, b.x, b.y);
-                                    mma16816(acc[t], a0.z, a1.z, a0.w, a1.w, b.z, b.w);
+                                    if (in) b = lds128(b_at + b_rest + b_row[t] + col * 2);
+                                    mma16816(acc[t][0], a0.x, a1.x, a0.y, a1.y, b.x, b.y);
+                                    mma16816(acc[t][1], a0.z, a1.z, a0.w, a1.w, b.z, b.w);
                                 }
                             }
                         }
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&s.b_empty[bs]));
+                        if (lane == 0) mbar_arrive(smem_u32(&s.b_empty[p][bs]));
                     }
                     fetch(ws);
                     if (++ws == STAGES) ws = 0;
-                    if (++bs == L::B_STAGES) {
+                    if (++bs == cut.b_stages) {
                         bs = 0;
                         bp ^= 1u;
                     }
@@ -617,12 +714,12 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a)
                         if (t >= tiles) break;
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            to[(kg * TOKENS + t * 8 + 2 * c + (i & 1)) * UP + rg * 16 + g + (i & 2 ? 8 : 0)] = acc[t][i];
+                            to[(kg * TOKENS + t * 8 + 2 * c + (i & 1)) * UP + rg * 16 + g + (i & 2 ? 8 : 0)] = acc[t][0][i] + acc[t][1][i];
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&s.red_full[reds]));
                 }
-                if (++reds == L::REDS) {
+                if (++reds == cuts.reds) {
                     reds = 0;
                     rp ^= 1u;
                 }
@@ -635,17 +732,19 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a)
         uint32_t rp = 0;
         bool on = true;
         for (int p = 0; p < 2; ++p) {
-            const int nb = blocks[p], units = entries * nb;
-            for (int u = blockIdx.x; u < units; u += step) {
-                const typename L::Entry en = entry[u / nb];
-                const int block = u % nb;
+            const Cut cut = cuts.of[p];
+            const int units = entries * (p == 0 ? blocks0 : blocks1), KG = cut.kg(), U = cut.u(), UP = U + 4;
+            const int log_fu = 7 - cut.log_kg - (gated ? 1 : 0), log_u = 7 - cut.log_kg;
+            for (Walk w(blockIdx.x, step, p == 0 ? blocks0 : blocks1); w.u < units; w.next(step)) {
+                const typename L::Entry en = entry[w.entry];
+                const int block = w.block;
                 if (on) on = warp_wait(smem_u32(&s.red_full[reds]), rp, gave_up);
                 if (on) {
                     const float *const from = red + reds * L::RED;
                     // The warps' shares of the columns, in order.
                     const auto joined = [&](int token, int row) {
                         float v = from[token * UP + row];
-#pragma unroll
+#pragma unroll 2
                         for (int k = 1; k < KG; ++k) v += from[(k * TOKENS + token) * UP + row];
                         return v;
                     };
@@ -653,7 +752,7 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a)
                         const mp_bf16_t *b1 = a.b1 == nullptr ? nullptr
                                                               : a.b1 + static_cast<int64_t>(en.expert) * a.F * (gated ? 2 : 1);
                         for (int i = tid; i < FU * en.count; i += JOIN_THREADS) {
-                            const int token = i / FU, j = i - token * FU, f = block * FU + j;
+                            const int token = i >> log_fu, j = i & (FU - 1), f = block * FU + j;
                             if (f >= a.Fp) continue;
                             float h = 0.0f;   // up to a row's last 16 bytes
                             if (f < a.F) {
@@ -679,7 +778,7 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a)
                     } else {
                         const mp_bf16_t *b2 = a.b2 == nullptr ? nullptr : a.b2 + static_cast<int64_t>(en.expert) * a.O;
                         for (int i = tid; i < U * en.count; i += JOIN_THREADS) {
-                            const int token = i / U, j = i - token * U, o = block * U + j;
+                            const int token = i >> log_u, j = i & (U - 1), o = block * U + j;
                             if (o >= a.O) continue;
                             float v = joined(token, j);
                             if (b2 != nullptr) v += bf16_value(b2 + o);
@@ -689,7 +788,7 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&s.red_empty[reds]));
                 }
-                if (++reds == L::REDS) {
+                if (++reds == cuts.reds) {
                     reds = 0;
                     rp ^= 1u;
                 }
@@ -708,10 +807,16 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a)
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * (LAYER_THREADS - 32) + tid; i < static_cast<int64_t>(a.T) * a.O;
          i += static_cast<int64_t>(gridDim.x) * (LAYER_THREADS - 32)) {
         const int t = static_cast<int>(i / a.O), o = static_cast<int>(i - static_cast<int64_t>(t) * a.O);
+        const float *const from = a.out + static_cast<int64_t>(t) * a.K * a.O + o;
         float y = 0.0f;
-        for (int k = 0; k < a.K; ++k) {
-            const int r = t * a.K + k;
-            if (idx[r] >= 0) y = fmaf(weights[r], __ldcg(a.out + static_cast<int64_t>(r) * a.O + o), y);
+        for (int k0 = 0; k0 < a.K; k0 += 8) {   // eight loads at a time
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v[k] = k0 + k < a.K && idx[t * a.K + k0 + k] >= 0 ? __ldcg(from + static_cast<int64_t>(k0 + k) * a.O) : 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k0 + k < a.K && idx[t * a.K + k0 + k] >= 0) y = fmaf(weights[t * a.K + k0 + k], v[k], y);
         }
         const float v[1] = {y};
         a.y[i] = pack(v);
@@ -731,22 +836,70 @@ template <typename L> void launch_logits(const LayerArgs &a, cudaStream_t s)
                          LOGIT_THREADS, 0, s, a);
 }
 
-template <int RG, int NT, bool ODD> mp_status_t launch_layer(const LayerArgs &a, cudaStream_t s)
+// The cut of a product of `rows` by `depth`, of `entries` entries: the fewest cycles by this count.
+// A stage of 32 KB takes 1,400 cycles at the copy bandwidth and more with many tokens' rows beside
+// it (which it reads for U rows each); a unit's end 300.  Large U is lighter on those rows, small
+// U divides evenly, and columns that a stage has and the product has not are idle warps.
+Cut cut_product(int64_t entries, int rows, int depth, double tokens, int most_log)
 {
-    typedef Layer<RG, NT, ODD> L;
+    Cut best = {0, 0};
+    double least = 0;
+    const int sms = sm_count();
+    for (int log = 0; log <= most_log; ++log) {
+        const Cut c = {log, 0};
+        const int64_t units = entries * ((rows + c.u() - 1) / c.u()), waves = (units + sms - 1) / sms;
+        const int64_t stages = (depth + c.kc() - 1) / c.kc();
+        const double cycles = static_cast<double>(waves) * (stages * 1400.0 * (1.0 + tokens / c.u()) + 300.0);
+        if (log == 0 || cycles < least) {
+            best = c;
+            least = cycles;
+        }
+    }
+    return best;
+}
+
+template <int NT, bool ODD> mp_status_t launch_layer(const LayerArgs &a, cudaStream_t s)
+{
+    typedef Layer<NT, ODD> L;
     static std::atomic<uint64_t> allowed{0};
-    if (!allow_smem(k_layer<RG, NT, ODD>, allowed, LAYER_SMEM)) return MP_ERR_CUDA;
+    if (!allow_smem(k_layer<NT, ODD>, allowed, LAYER_SMEM)) return MP_ERR_CUDA;
     const int R = a.T * a.K;
-    const size_t bytes = L::tables(a.E, R) + static_cast<size_t>(L::B_STAGES) * L::B_STAGE + static_cast<size_t>(L::STAGES) * L::W_STAGE;
+    const bool gated = act_gated(a.act);
+    // Experts that are picked, if all are alike: E (1 - (1 - K / E)^T).
+    double missed = 1.0;
+    for (int t = 0; t < a.T; ++t) missed *= 1.0 - static_cast<double>(a.K) / a.E;
+    const double busy = a.E * (1.0 - missed), tokens = R / busy;
+    const int64_t entries = static_cast<int64_t>(busy * ((tokens + L::TOKENS - 1) / L::TOKENS > 1.5 ? 2 : 1) + 0.5);
+    const int most_log = NT == 1 ? 3 : NT == 2 ? 2 : 1;   // so that two slots for the tokens' rows fit
+    LayerCuts cuts;
+    cuts.of[0] = cut_product(entries, a.F * (gated ? 2 : 1), a.H, tokens, most_log);
+    cuts.of[1] = cut_product(entries, a.O, a.F, 2.0 * tokens, most_log);
+    cuts.b_rows = a.T < L::TOKENS ? a.T : L::TOKENS;
+    const size_t fixed = L::tables(a.E, R) + static_cast<size_t>(L::STAGES) * L::W_STAGE;
+    const size_t slots[2] = {static_cast<size_t>(cuts.b_rows) * cuts.of[0].b_pitch(),
+                             static_cast<size_t>(cuts.b_rows) * 2 * cuts.of[1].b_pitch()};
+    const size_t slot = slots[0] > slots[1] ? slots[0] : slots[1];
+    for (cuts.reds = RED_MOST; cuts.reds > 1 && fixed + cuts.reds * L::RED * 4 + 3 * slot > LAYER_SMEM; --cuts.reds) {
+    }
+    size_t room = LAYER_SMEM - fixed - static_cast<size_t>(cuts.reds) * L::RED * 4;
+    if (room > B_MOST * slot) room = B_MOST * slot;
+    room = room / 16 * 16;
+    for (int p = 0; p < 2; ++p) {
+        cuts.of[p].b_stages = static_cast<int>(room / slots[p]);
+        if (cuts.of[p].b_stages > B_MOST) cuts.of[p].b_stages = B_MOST;
+    }
     // No more CTAs than units: a barrier of few is quicker.
-    const int FU = act_gated(a.act) ? L::U / 2 : L::U;
-    const int64_t entries = (a.E < R ? a.E : R) + R / L::TOKENS;
-    const int64_t wide = a.F / FU > a.O / L::U ? a.F / FU : a.O / L::U, units = entries * (wide + 1);
+    const int64_t most = (a.E < R ? a.E : R) + R / L::TOKENS;
+    int64_t wide = 0;
+    for (int p = 0; p < 2; ++p) {
+        const int rows = p == 0 ? a.F * (gated ? 2 : 1) : a.O, u = cuts.of[p].u();
+        if ((rows + u - 1) / u > wide) wide = (rows + u - 1) / u;
+    }
     const int sms = sm_count();
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = static_cast<unsigned>(units < sms ? units : sms);
+    cfg.gridDim = static_cast<unsigned>(most * wide < sms ? most * wide : sms);
     cfg.blockDim = LAYER_THREADS;
-    cfg.dynamicSmemBytes = bytes;
+    cfg.dynamicSmemBytes = fixed + static_cast<size_t>(cuts.reds) * L::RED * 4 + room;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeCooperative;
@@ -755,15 +908,15 @@ template <int RG, int NT, bool ODD> mp_status_t launch_layer(const LayerArgs &a,
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    (void)cudaLaunchKernelEx(&cfg, k_layer<RG, NT, ODD>, a);
+    (void)cudaLaunchKernelEx(&cfg, k_layer<NT, ODD>, a, cuts, static_cast<int>(room));
     return check_launch();
 }
 
 template <bool ODD> mp_status_t choose_layer(const LayerArgs &a, cudaStream_t s)
 {
-    if (a.T <= 8) return launch_layer<1, 1, ODD>(a, s);
-    if (a.T * a.K <= 12 * a.E) return launch_layer<4, 2, ODD>(a, s);
-    return launch_layer<4, 4, ODD>(a, s);
+    if (a.T <= 8) return launch_layer<1, ODD>(a, s);
+    if (a.T * a.K <= 12 * a.E) return launch_layer<2, ODD>(a, s);
+    return launch_layer<4, ODD>(a, s);
 }
 
 mp_status_t layer_sizes(int64_t T, int32_t E, int32_t K, int32_t H, int32_t F, int32_t O)

@@ -158,10 +158,9 @@ template <typename D, bool VEC, int C> struct NormGroup {
 
     __device__ __forceinline__ void barrier() const
     {
+        __syncwarp();   // a warp comes to the barrier as a whole
         if (W > 32)
             asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(W) : "memory");
-        else
-            __syncwarp();
     }
 
     // The sums over the row, each added up in a fixed order; every thread gets them.  A
