@@ -4,8 +4,9 @@
 //   y[t] = sum_k w[t,k] (act(x[t] w1[e]^T + b1[e]) w2[e]^T + b2[e]),  e = idx[t,k]
 //
 // The picked experts' weights are read once and bound it; rows are nothing beside them.  Two
-// kernels (three above ROUTE_TOKENS tokens, whose choice is worth a kernel of its own):
-// k_layer_logits, then k_layer, which runs from the choice to the result on every SM.
+// kernels: k_layer_logits, a CTA for each expert, and k_layer, which runs from the choice to the
+// result on every SM.  One token's choice every CTA makes for itself; several tokens' are
+// spread over the CTAs, and the grid waits for them.
 //
 // Logits are sums in pairs of fp32 (a sum and what its roundings lost), so that they are those
 // of 64 bits rounded once, and the choice with them: sums in 64 bits would take 16 times the
@@ -15,7 +16,7 @@
 // weights against all tokens of that expert (an entry: up to 8 NT of them).  Each of eight
 // warps multiplies 16 weight rows by its share of the columns, 128 a stage, which it copies
 // itself, by cp.async into a ring of its own; one more warp copies the tokens' rows for all, and
-// four join the eight warps' sums, in a fixed order, and apply bias and activation, so that the
+// three join the eight warps' sums, in a fixed order, and apply bias and activation, so that the
 // eight never wait for a unit's end.
 // (mma.m16n8k16: weight rows are its 16, tokens its 8.  Bytes bound it, so the tensor cores'
 // older form is enough, and it needs no tile of 128 rows.)  The rings do not stop between the
@@ -34,6 +35,7 @@
 // as if they were the fragment's k = 2c, 2c+1, 2c+8, 2c+9: both operands agree on that order,
 // which is all that a sum over k asks.
 #include "expert.cuh"
+#include "pairs.cuh"
 #include "route.cuh"
 #include "tc.cuh"
 
@@ -42,10 +44,10 @@
 namespace mp {
 namespace {
 
-constexpr int ROUTE_TOKENS = 8;          // tokens that every CTA routes for itself, a warp each
 constexpr int LOGIT_THREADS = 128, LOGIT_WARPS = LOGIT_THREADS / 32;
+constexpr int64_t PREFETCH = 384 * 1024; // bytes of the second product's weights that a CTA asks into L2 early
 constexpr int MATH_WARPS = 8, MATH_THREADS = 32 * MATH_WARPS;
-constexpr int JOIN_WARPS = 4, JOIN_THREADS = 32 * JOIN_WARPS;
+constexpr int JOIN_WARPS = 3, JOIN_THREADS = 32 * JOIN_WARPS;   // 12 warps in all: 168 registers a thread
 constexpr int LAYER_THREADS = MATH_THREADS + 32 + JOIN_THREADS;   // and a warp of copies
 constexpr int STAGE_COLS = 128;          // of a warp
 constexpr int ROW_PAD = 64;              // bytes between tokens' rows
@@ -53,7 +55,7 @@ constexpr int B_MOST = 8, RED_MOST = 4;  // slots for tokens' rows, buffers of s
 constexpr size_t LAYER_SMEM = 227 * 1024;
 
 struct LayerControl {
-    unsigned arrived[2];   // CTAs at the two barriers of k_layer
+    unsigned arrived[3];   // CTAs at the barriers of k_layer: after the products and, before them, the choice
 };
 
 struct LayerArgs {
@@ -72,7 +74,6 @@ struct LayerArgs {
     mp_bf16_t *h;           // [T*K,2,Fp]: nearest values, and the nearest of what is left
     float *out;             // [T*K,O]: each slot's result
     int Hp, Fp;
-    bool routed;            // idx and weights are there when k_layer starts
 };
 
 __device__ __forceinline__ float bf16_value(const mp_bf16_t *p)
@@ -84,28 +85,36 @@ __device__ __forceinline__ float bf16_value(const mp_bf16_t *p)
 // logits
 // ---------------------------------------------------------------------------
 
-// A sum of fp32 values and what its roundings lost (Knuth's two-sum).
-struct PairSum {
-    float s = 0.0f, lost = 0.0f;
-    __device__ __forceinline__ void add(float p)
+// Sums of fp32 values and what their roundings lost (Knuth's two-sum), two side by side.
+struct PairSums {
+    f2 s = 0ull, lost = 0ull;
+    __device__ __forceinline__ void add(f2 p)
     {
-        const float t = __fadd_rn(s, p), z = __fsub_rn(t, s);
-        lost = __fadd_rn(lost, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(p, z)));
+        const f2 minus = pair(-1.0f, -1.0f);
+        const f2 t = add2(s, p), z = fma2(s, minus, t);   // t - s, rounded once
+        lost = add2(lost, add2(fma2(fma2(z, minus, t), minus, s), fma2(z, minus, p)));
         s = t;
     }
-    __device__ __forceinline__ void add(const PairSum &o)
-    {
-        add(o.s);
-        lost = __fadd_rn(lost, o.lost);
-    }
     // a b, and what the product's rounding lost (nothing for two bf16 values)
-    template <bool EXACT> __device__ __forceinline__ void add_product(float a, float b)
+    template <bool EXACT> __device__ __forceinline__ void add_product(f2 a, f2 b)
     {
-        const float p = __fmul_rn(a, b);
-        if (!EXACT) lost = __fadd_rn(lost, __fmaf_rn(a, b, -p));
+        const f2 p = mul2(a, b);
+        if (!EXACT) lost = add2(lost, fma2(a, b, mul2(p, pair(-1.0f, -1.0f))));
         add(p);
     }
-    __device__ __forceinline__ float sum() const { return isfinite(s) ? __fadd_rn(s, lost) : s; }
+    __device__ __forceinline__ void add(const PairSums &o)
+    {
+        add(o.s);
+        lost = add2(lost, o.lost);
+    }
+    // The sum of both.
+    __device__ __forceinline__ float total() const
+    {
+        const float2 v = both(s), l = both(lost);
+        const float t = __fadd_rn(v.x, v.y), z = __fsub_rn(t, v.x);
+        const float rest = __fadd_rn(__fadd_rn(l.x, l.y), __fadd_rn(__fsub_rn(v.x, __fsub_rn(t, z)), __fsub_rn(v.y, z)));
+        return isfinite(t) ? __fadd_rn(t, rest) : t;
+    }
 };
 
 // Logits of one expert and TB tokens, a CTA each; the first CTAs also clear k_layer's barriers and
@@ -113,44 +122,47 @@ struct PairSum {
 // router are whole chunks of 4 on 16 (8) bytes.
 template <typename L, int TB, bool VEC> __global__ void __launch_bounds__(LOGIT_THREADS) k_layer_logits(const LayerArgs a)
 {
-    __shared__ PairSum part[LOGIT_WARPS][TB];
+    __shared__ PairSums part[LOGIT_WARPS][TB];
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x, t0 = blockIdx.y * TB;
-    if (e == 0 && t0 == 0 && threadIdx.x < 2) a.control->arrived[threadIdx.x] = 0;
+    if (e == 0 && t0 == 0 && threadIdx.x < 3) a.control->arrived[threadIdx.x] = 0;
     if (a.xp != nullptr)
         for (int t = t0 + e; t < min(t0 + TB, a.T); t += gridDim.x)
             for (int c = threadIdx.x; c < a.Hp; c += LOGIT_THREADS)
                 a.xp[static_cast<int64_t>(t) * a.Hp + c] = c < a.H ? a.x[static_cast<int64_t>(t) * a.H + c] : 0;
+    const mp_bf16_t *x[TB];
+#pragma unroll
+    for (int b = 0; b < TB; ++b) x[b] = a.x + static_cast<int64_t>(min(t0 + b, a.T - 1)) * a.H;
     const L *r = static_cast<const L *>(a.router) + static_cast<int64_t>(e) * a.H;
-    PairSum v[TB];
+    PairSums v[TB];
     if (VEC) {
         typedef typename std::conditional<sizeof(L) == 4, float4, uint2>::type Four;
-#pragma unroll 4
+#pragma unroll(TB == 1 ? 8 : 4)
         for (int c = threadIdx.x * 4; c < a.H; c += LOGIT_THREADS * 4) {
             const Four w = __ldg(reinterpret_cast<const Four *>(r + c));
             const L *wl = reinterpret_cast<const L *>(&w);
+            const f2 w0 = pair(logit_value(wl[0]), logit_value(wl[1])), w1 = pair(logit_value(wl[2]), logit_value(wl[3]));
 #pragma unroll
             for (int b = 0; b < TB; ++b) {
-                const uint2 u = __ldg(reinterpret_cast<const uint2 *>(a.x + static_cast<int64_t>(min(t0 + b, a.T - 1)) * a.H + c));
-                const float f[4] = {bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y)};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[b].add_product<sizeof(L) == 2>(f[i], logit_value(wl[i]));
+                const uint2 u = __ldg(reinterpret_cast<const uint2 *>(x[b] + c));
+                v[b].template add_product<sizeof(L) == 2>(pair(bf16_lo(u.x), bf16_hi(u.x)), w0);
+                v[b].template add_product<sizeof(L) == 2>(pair(bf16_lo(u.y), bf16_hi(u.y)), w1);
             }
         }
     } else {
+#pragma unroll 4
         for (int c = threadIdx.x; c < a.H; c += LOGIT_THREADS) {
-            const float w = logit(r + c);
+            const f2 w = pair(logit(r + c), 0.0f);
 #pragma unroll
-            for (int b = 0; b < TB; ++b)
-                v[b].add_product<sizeof(L) == 2>(bf16_value(a.x + static_cast<int64_t>(min(t0 + b, a.T - 1)) * a.H + c), w);
+            for (int b = 0; b < TB; ++b) v[b].template add_product<sizeof(L) == 2>(pair(bf16_value(x[b] + c), 0.0f), w);
         }
     }
 #pragma unroll
     for (int b = 0; b < TB; ++b) {
 #pragma unroll
         for (int d = 16; d; d >>= 1) {
-            PairSum o;
+            PairSums o;
             o.s = __shfl_xor_sync(FULL_MASK, v[b].s, d);
             o.lost = __shfl_xor_sync(FULL_MASK, v[b].lost, d);
             v[b].add(o);
@@ -159,9 +171,9 @@ template <typename L, int TB, bool VEC> __global__ void __launch_bounds__(LOGIT_
     }
     __syncthreads();
     if (threadIdx.x < TB && t0 + static_cast<int>(threadIdx.x) < a.T) {
-        PairSum s = part[0][threadIdx.x];
+        PairSums s = part[0][threadIdx.x];
         for (int w = 1; w < LOGIT_WARPS; ++w) s.add(part[w][threadIdx.x]);
-        a.logits[static_cast<int64_t>(t0 + threadIdx.x) * a.E + e] = s.sum();
+        a.logits[static_cast<int64_t>(t0 + threadIdx.x) * a.E + e] = s.total();
     }
 }
 
@@ -253,7 +265,7 @@ __device__ __forceinline__ float act_of(int act, float z)
     }
 }
 
-// One token's choice by one warp; results through `r`.
+// One token's choice by one warp.
 __device__ __noinline__ void route_one(const RouteArgs &r, const float *logits, int t, int lane)
 {
     if (r.E <= 128 && r.K == 8)
@@ -294,14 +306,15 @@ template <int NT, bool ODD> struct Layer {
     };
     struct Shared {
         uint64_t b_full[2][B_MOST], b_empty[2][B_MOST], red_full[RED_MOST], red_empty[RED_MOST];
+        int32_t idx[32];      // of one token
+        float weights[32];
         int gave_up, entries;
     };
-    // After the rings and the units' sums: order, counts, entries; idx and weights of few tokens.
-    static size_t tables(int E, int R)
+    // After the rings: what is above, the units' sums, and the routes: tokens of each expert (a bit
+    // each), where an expert's routes start, routes by expert, entries.
+    static constexpr size_t tables(int E, int R)
     {
-        const int entries = (E < R ? E : R) + R / TOKENS;
-        return sizeof(Shared) + (static_cast<size_t>(R) + 2 * E) * 4 + static_cast<size_t>(entries) * sizeof(Entry) +
-               static_cast<size_t>(ROUTE_TOKENS) * 32 * 8 + 64;
+        return sizeof(Shared) + (3 * static_cast<size_t>(E) + R) * 4 + ((E < R ? E : R) + R / TOKENS) * sizeof(Entry) + 16;
     }
 };
 
@@ -309,7 +322,7 @@ template <int NT, bool ODD>
 __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, const LayerCuts cuts, const int b_bytes)
 {
     typedef Layer<NT, ODD> L;
-    constexpr int TOKENS = L::TOKENS, STAGES = L::STAGES;
+    constexpr int TOKENS = L::TOKENS, STAGES = L::STAGES, CHAINS = NT == 1 ? 4 : 2;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, R = a.T * a.K;
     const uint32_t b_ring = smem_u32(smem) + STAGES * L::W_STAGE;
@@ -318,10 +331,9 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
     at += sizeof(typename L::Shared);
     float *const red = reinterpret_cast<float *>(at);
     at += cuts.reds * L::RED * 4;
-    int *const order = reinterpret_cast<int *>(at), *const count = order + R, *const start = count + a.E;
-    typename L::Entry *const entry = reinterpret_cast<typename L::Entry *>(start + a.E);
-    int32_t *const my_idx = reinterpret_cast<int32_t *>(entry + min(a.E, R) + R / TOKENS);
-    float *const my_weights = reinterpret_cast<float *>(my_idx + ROUTE_TOKENS * 32);
+    unsigned *const tokens_of = reinterpret_cast<unsigned *>(at);
+    int *const start = reinterpret_cast<int *>(tokens_of + 2 * a.E), *const order = start + a.E;
+    typename L::Entry *const entry = reinterpret_cast<typename L::Entry *>(order + R);
     volatile int *gave_up = &s.gave_up;
 
     if (threadIdx.x == 0) {
@@ -337,97 +349,83 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
         mbar_init_fence();
         s.gave_up = 0;
     }
-    for (int e = threadIdx.x; e < a.E; e += LAYER_THREADS) count[e] = 0;
+    for (int e = threadIdx.x; e < 2 * a.E; e += LAYER_THREADS) tokens_of[e] = 0;
     pdl_trigger();
     pdl_wait();
+    __syncthreads();
 
-    // The choice, if it is not there yet.
     const int32_t *idx = a.idx;
     const float *weights = a.weights;
-    if (!a.routed) {
-        if (warp < a.T) {
-            RouteArgs r = a.route;
-            r.idx = my_idx;
-            r.weights = my_weights;
-            route_one(r, a.logits + static_cast<int64_t>(warp) * a.E, warp, lane);
-        }
-        idx = my_idx;
-        weights = my_weights;
-    }
-    __syncthreads();
-    if (!a.routed && blockIdx.x == 0)
-        for (int r = threadIdx.x; r < R; r += LAYER_THREADS) {
-            a.idx[r] = my_idx[r];
-            a.weights[r] = my_weights[r];
-        }
-    // Routes by expert, in their order (every CTA has to come to the same entries), and entries
-    // of up to TOKENS of them.
-    if (R <= 32) {
-        // Experts in the order of their first routes.
+    if (a.T == 1) {
         if (warp == 0) {
-            const int e = lane < R ? idx[lane] : -1;
-            const unsigned same = __match_any_sync(FULL_MASK, e), below = (1u << lane) - 1u;
-            const int rank = __popc(same & below), n = __popc(same), first = __ffs(same) - 1;
-            const bool leads = e >= 0 && rank == 0;
-            int before = leads ? n : 0;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int o = __shfl_up_sync(FULL_MASK, before, d);
-                if (lane >= d) before += o;
+            RouteArgs r = a.route;
+            r.idx = s.idx;
+            r.weights = s.weights;
+            route_one(r, a.logits, 0, lane);
+            __syncwarp();
+            if (blockIdx.x == 0 && lane < a.K) {
+                a.idx[lane] = s.idx[lane];
+                a.weights[lane] = s.weights[lane];
             }
-            before -= leads ? n : 0;
-            const int from = __shfl_sync(FULL_MASK, before, first);
-            if (e >= 0) order[from + rank] = lane;
-            // An entry takes up to TOKENS routes: a leader's follow those of the leaders before it.
-            const int parts = leads ? (n + TOKENS - 1) / TOKENS : 0;
-            int slot = parts;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int o = __shfl_up_sync(FULL_MASK, slot, d);
-                if (lane >= d) slot += o;
-            }
-            if (lane == 31) s.entries = slot;
-            slot -= parts;
-            for (int i = 0; i < parts; ++i) entry[slot + i] = {e, from + i * TOKENS, min(TOKENS, n - i * TOKENS)};
         }
+        idx = s.idx;
+        weights = s.weights;
+        __syncthreads();
     } else {
-        for (int r = threadIdx.x; r < R; r += LAYER_THREADS)
-            if (idx[r] >= 0) atomicAdd(count + idx[r], 1);
+        if (warp == 0) {
+            for (int t = blockIdx.x; t < a.T; t += gridDim.x) route_one(a.route, a.logits + static_cast<int64_t>(t) * a.E, t, lane);
+            __threadfence();
+            __syncwarp();
+            if (lane == 0) {
+                grid_arrive(&a.control->arrived[2]);
+                (void)grid_wait(&a.control->arrived[2], gridDim.x, gave_up);
+            }
+        }
         __syncthreads();
     }
-    if (R > 32 && warp == 0) {
+    // The routes of each expert in the tokens' order (every CTA has to come to the same entries), and
+    // entries of up to TOKENS of them.  After a wait given up idx may be anything: there are none.
+    const int routes_there = *gave_up ? 0 : R;
+    for (int r = threadIdx.x; r < routes_there; r += LAYER_THREADS) {
+        const int e = idx[r], t = r / a.K;
+        if (e >= 0) atomicOr(tokens_of + 2 * e + (t >> 5), 1u << (t & 31));
+    }
+    __syncthreads();
+    if (warp == 0) {
+        // Each lane takes a run of experts, so that the sums cross the warp once.
+        const int run = (a.E + 31) / 32, e0 = min(lane * run, a.E), e1 = min(e0 + run, a.E);
+        const auto routes_of = [&](int e) { return __popc(tokens_of[2 * e]) + __popc(tokens_of[2 * e + 1]); };
         int routes = 0, entries = 0;
-        for (int e0 = 0; e0 < a.E; e0 += 32) {
-            const int e = e0 + lane, n = e < a.E ? count[e] : 0, parts = (n + TOKENS - 1) / TOKENS;
-            int before = n, parts_before = parts;
+        for (int e = e0; e < e1; ++e) {
+            const int n = routes_of(e);
+            routes += n;
+            entries += (n + TOKENS - 1) / TOKENS;
+        }
+        int first = routes, slot = entries;
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int o = __shfl_up_sync(FULL_MASK, before, d), q = __shfl_up_sync(FULL_MASK, parts_before, d);
-                if (lane >= d) {
-                    before += o;
-                    parts_before += q;
-                }
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(FULL_MASK, first, d), q = __shfl_up_sync(FULL_MASK, slot, d);
+            if (lane >= d) {
+                first += o;
+                slot += q;
             }
-            const int first = routes + before - n, slot = entries + parts_before - parts;
-            if (e < a.E) start[e] = first;
-            for (int i = 0; i < parts; ++i)
-                entry[slot + i] = {e, first + i * TOKENS, min(TOKENS, n - i * TOKENS)};
-            routes += __shfl_sync(FULL_MASK, before, 31);
-            entries += __shfl_sync(FULL_MASK, parts_before, 31);
         }
-        if (lane == 0) s.entries = entries;
-        __syncwarp();
-        for (int r0 = 0; r0 < R; r0 += 32) {
-            const int r = r0 + lane, e = r < R ? idx[r] : -1;
-            const unsigned same = __match_any_sync(FULL_MASK, e);
-            const int place = e >= 0 ? start[e] + __popc(same & ((1u << lane) - 1u)) : 0;
-            __syncwarp();
-            if (e >= 0) {
-                order[place] = r;
-                if ((same >> lane) == 1u) start[e] = place + 1;   // the last of them
-            }
-            __syncwarp();
+        if (lane == 31) s.entries = slot;
+        first -= routes;
+        slot -= entries;
+        for (int e = e0; e < e1; ++e) {
+            const int n = routes_of(e);
+            start[e] = first;
+            for (int i = 0; i < n; i += TOKENS) entry[slot++] = {e, first + i, min(TOKENS, n - i)};
+            first += n;
         }
+    }
+    __syncthreads();
+    for (int r = threadIdx.x; r < routes_there; r += LAYER_THREADS) {
+        const int e = idx[r], t = r / a.K;
+        if (e < 0) continue;
+        const unsigned low = tokens_of[2 * e], high = tokens_of[2 * e + 1], below = (1u << (t & 31)) - 1u;
+        order[start[e] + (t < 32 ? __popc(low & below) : __popc(low) + __popc(high & below))] = r;
     }
     __syncthreads();
 
@@ -629,11 +627,11 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
             for (Walk w(blockIdx.x, step, p == 0 ? blocks0 : blocks1); w.u < units; w.next(step)) {
                 const typename L::Entry en = entry[w.entry];
                 const int tiles = (en.count + 7) >> 3;
-                float acc[NT][2][4];   // two sums a tile: products that do not wait for one another
+                float acc[NT][CHAINS][4];   // sums of products that do not wait for one another
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) acc[t][i >> 2][i & 3] = 0.0f;
+                    for (int i = 0; i < 4 * CHAINS; ++i) acc[t][i >> 2][i & 3] = 0.0f;
                 uint32_t shift[2] = {0, 0};   // where a row's first value lies in its granule
                 if (ODD) {
 #pragma unroll
@@ -645,61 +643,68 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
                 for (int k0 = 0; k0 < K; k0 += KC) {
                     copy_wait<STAGES - 1>();
                     __syncwarp();
+                    const int n = min(KC, K - k0) - kg * STAGE_COLS;   // columns of this warp
+                    const uint32_t w_at = smem_u32(ring + ws * L::W_STAGE) + g * L::W_PITCH;
+                    uint4 a0[4], a1[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int col = q * 32 + c * 8;
+                        a0[q] = a1[q] = make_uint4(0, 0, 0, 0);
+                        if (col >= n) continue;
+                        if (!ODD) {
+                            const uint32_t from = w_at + ((q * 4 + c) ^ (g & 1) << 2) * 16;
+                            a0[q] = lds128(from);
+                            a1[q] = lds128(from + 8 * L::W_PITCH);
+                        } else {
+                            uint32_t v[2][4];
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const uint32_t from = w_at + 8 * i * L::W_PITCH + ((shift[i] + col * 2) & ~3u);
+                                const uint32_t by = (shift[i] & 2u) * 8u;
+                                uint32_t word[5];
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) word[j] = lds32(from + 4 * j);
+                                word[4] = by != 0 ? lds32(from + 16) : 0u;
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    // past the row's end is another row, or what the ring held before
+                                    const int left = n - col - 2 * j;
+                                    const uint32_t mask = left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
+                                    v[i][j] = __funnelshift_r(word[j], word[j + 1], by) & mask;
+                                }
+                            }
+                            a0[q] = make_uint4(v[0][0], v[0][1], v[0][2], v[0][3]);
+                            a1[q] = make_uint4(v[1][0], v[1][1], v[1][2], v[1][3]);
+                        }
+                    }
+                    __syncwarp();
+                    fetch(ws);   // the weights are in registers: their slot takes the next ones
                     if (on) on = warp_wait(smem_u32(&s.b_full[p][bs]), bp, gave_up);
                     if (on) {
-                        const int n = min(KC, K - k0) - kg * STAGE_COLS;   // columns of this warp
-                        const uint32_t w_at = smem_u32(ring + ws * L::W_STAGE) + g * L::W_PITCH;
                         const uint32_t b_at = b_ring + bs * slot + kg * STAGE_COLS * 2, b_rest = cuts.b_rows * pitch;
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const int col = q * 32 + c * 8;
-                            uint4 a0 = make_uint4(0, 0, 0, 0), a1 = a0;
-                            const bool in = col < n;
-                            if (!ODD) {
-                                if (in) {
-                                    const uint32_t from = w_at + ((q * 4 + c) ^ (g & 1) << 2) * 16;
-                                    a0 = lds128(from);
-                                    a1 = lds128(from + 8 * L::W_PITCH);
+                        for (int t = 0; t < NT; ++t) {
+                            if (t >= tiles) break;
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {   // of h: the nearest values, and the rest
+                                if (half > p) break;
+                                uint4 b[4];
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    const int col = q * 32 + c * 8;
+                                    b[q] = make_uint4(0, 0, 0, 0);
+                                    if (col < n) b[q] = lds128(b_at + (half ? b_rest : 0u) + b_row[t] + col * 2);
                                 }
-                            } else if (in) {
-                                uint32_t v[2][4];
 #pragma unroll
-                                for (int i = 0; i < 2; ++i) {
-                                    const uint32_t from = w_at + 8 * i * L::W_PITCH + ((shift[i] + col * 2) & ~3u);
-                                    const uint32_t by = (shift[i] & 2u) * 8u;
-                                    uint32_t word[5];
-#pragma unroll
-                                    for (int j = 0; j < 4; ++j) word[j] = lds32(from + 4 * j);
-                                    word[4] = by != 0 ? lds32(from + 16) : 0u;
-#pragma unroll
-                                    for (int j = 0; j < 4; ++j) {
-                                        // past the row's end is another row, or what the ring held before
-                                        const int left = n - col - 2 * j;
-                                        const uint32_t mask = left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
-                                        v[i][j] = __funnelshift_r(word[j], word[j + 1], by) & mask;
-                                    }
-                                }
-                                a0 = make_uint4(v[0][0], v[0][1], v[0][2], v[0][3]);
-                                a1 = make_uint4(v[1][0], v[1][1], v[1][2], v[1][3]);
-                            }
-#pragma unroll
-                            for (int t = 0; t < NT; ++t) {
-                                if (t >= tiles) break;
-                                uint4 b = make_uint4(0, 0, 0, 0);
-                                if (in) b = lds128(b_at + b_row[t] + col * 2);
-                                mma16816(acc[t][0], a0.x, a1.x, a0.y, a1.y, b.x, b.y);
-                                mma16816(acc[t][1], a0.z, a1.z, a0.w, a1.w, b.z, b.w);
-                                if (p == 1) {
-                                    if (in) b = lds128(b_at + b_rest + b_row[t] + col * 2);
-                                    mma16816(acc[t][0], a0.x, a1.x, a0.y, a1.y, b.x, b.y);
-                                    mma16816(acc[t][1], a0.z, a1.z, a0.w, a1.w, b.z, b.w);
+                                for (int q = 0; q < 4; ++q) {
+                                    mma16816(acc[t][2 * q % CHAINS], a0[q].x, a1[q].x, a0[q].y, a1[q].y, b[q].x, b[q].y);
+                                    mma16816(acc[t][(2 * q + 1) % CHAINS], a0[q].z, a1[q].z, a0[q].w, a1[q].w, b[q].z, b[q].w);
                                 }
                             }
                         }
                         __syncwarp();
                         if (lane == 0) mbar_arrive(smem_u32(&s.b_empty[p][bs]));
                     }
-                    fetch(ws);
                     if (++ws == STAGES) ws = 0;
                     if (++bs == cut.b_stages) {
                         bs = 0;
@@ -714,7 +719,9 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
                         if (t >= tiles) break;
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            to[(kg * TOKENS + t * 8 + 2 * c + (i & 1)) * UP + rg * 16 + g + (i & 2 ? 8 : 0)] = acc[t][0][i] + acc[t][1][i];
+                            to[(kg * TOKENS + t * 8 + 2 * c + (i & 1)) * UP + rg * 16 + g + (i & 2 ? 8 : 0)] =
+                                CHAINS == 4 ? (acc[t][0][i] + acc[t][1][i]) + (acc[t][2 % CHAINS][i] + acc[t][3 % CHAINS][i])
+                                            : acc[t][0][i] + acc[t][1][i];
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&s.red_full[reds]));
@@ -798,6 +805,22 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
             __threadfence();
             join_barrier();
             if (tid == 0) grid_arrive(&a.control->arrived[p]);
+            if (p == 0 && tid == 0) {
+                // While the last CTAs finish, memory goes on with this one's weights of the second
+                // product: rows of a unit lie one after another.
+                const uintptr_t base = reinterpret_cast<uintptr_t>(a.w2), last = base + static_cast<uint64_t>(a.E) * a.O * a.F * 2;
+                int64_t left = PREFETCH;
+                for (Walk w(blockIdx.x, step, blocks1); w.u < entries * blocks1 && left > 0; w.next(step)) {
+                    const int row = w.block * cuts.of[1].u(), rows = min(cuts.of[1].u(), a.O - row);
+                    uintptr_t from = base + (static_cast<uint64_t>(entry[w.entry].expert) * a.O + row) * a.F * 2;
+                    uintptr_t to = min(from + static_cast<uint64_t>(rows) * a.F * 2, last) & ~static_cast<uintptr_t>(15);
+                    from = (from + 15) & ~static_cast<uintptr_t>(15);
+                    if (to <= from) continue;
+                    const uint32_t bytes = static_cast<uint32_t>(min(to - from, static_cast<uintptr_t>(PREFETCH)));
+                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(bytes) : "memory");
+                    left -= bytes;
+                }
+            }
         }
         if (tid == 0) (void)grid_wait(&a.control->arrived[1], gridDim.x, gave_up);
     }
@@ -977,7 +1000,7 @@ extern "C" mp_status_t mp_moe_layer(const mp_bf16_t *x, const void *router, int3
     if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < space.bytes) return MP_ERR_WORKSPACE;
     uint8_t *const ws = static_cast<uint8_t *>(workspace);
     const cudaStream_t s = as_stream(stream);
-    route.T = T;
+    route.T = T; route.idx = idx; route.weights = weights;
     LayerArgs a = {};
     a.x = x; a.w1 = w1; a.b1 = b1; a.w2 = w2; a.b2 = b2; a.router = router; a.route = route;
     a.T = static_cast<int>(T); a.E = E; a.K = K; a.H = H; a.F = F; a.O = O; a.act = act;
@@ -988,18 +1011,12 @@ extern "C" mp_status_t mp_moe_layer(const mp_bf16_t *x, const void *router, int3
     a.xp = H % 8 == 0 && aligned16(x) ? nullptr : reinterpret_cast<mp_bf16_t *>(ws + space.xp);
     a.h = reinterpret_cast<mp_bf16_t *>(ws + space.h);
     a.out = reinterpret_cast<float *>(ws + space.out);
-    a.routed = T > ROUTE_TOKENS;
     switch (router_dtype) {
     case MP_DTYPE_BF16: launch_logits<__nv_bfloat16>(a, s); break;
     case MP_DTYPE_FP16: launch_logits<__half>(a, s); break;
     default: launch_logits<float>(a, s); break;
     }
     if (const mp_status_t st = check_launch(); st != MP_OK) return st;
-    if (a.routed) {
-        const mp_status_t st = mp_route(a.logits, MP_DTYPE_FP32, bias, T, E, K, score, n_groups, topk_groups, group_top,
-                                        renorm, scale, idx, weights, stream);
-        if (st != MP_OK) return st;
-    }
     const bool even = H % 8 == 0 && F % 8 == 0 && aligned16(w1) && aligned16(w2);
     return even ? choose_layer<false>(a, s) : choose_layer<true>(a, s);
 }

@@ -18,6 +18,7 @@
 
 #include <type_traits>
 
+#include "pairs.cuh"
 #include "tc.cuh"
 
 namespace mp {
@@ -47,44 +48,6 @@ __device__ __forceinline__ float norm_value(__half v) { return __half2float(v); 
 __device__ __forceinline__ void norm_put(float *p, float v) { *p = v; }
 __device__ __forceinline__ void norm_put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void norm_put(__half *p, float v) { *p = __float2half_rn(v); }
-
-// Two fp32 values in a register pair, and arithmetic on both at once.
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 pair(float a, float b)
-{
-    f2 v;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
-    return v;
-}
-__device__ __forceinline__ float2 both(f2 v)
-{
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c)
-{
-    f2 v;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
-    return v;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b)
-{
-    f2 v;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
-    return v;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b)
-{
-    f2 v;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
-    return v;
-}
-__device__ __forceinline__ float sum2(f2 v)
-{
-    const float2 r = both(v);
-    return r.x + r.y;
-}
 
 // The values of a 16-byte vector, in pairs.
 __device__ __forceinline__ void vec_values(const uint4 &v, f2 *f, const __nv_bfloat16 *)
