@@ -20,8 +20,9 @@
 // eight never wait for a unit's end.
 // (mma.m16n8k16: weight rows are its 16, tokens its 8.  Bytes bound it, so the tensor cores'
 // older form is enough, and it needs no tile of 128 rows.)  The rings do not stop between the
-// two products: while the grid waits at the barrier after the first one for the last
-// activations h, the second's weights are already on their way.  h is kept as two bf16 values, the
+// two products: the second's units of an expert need the activations h of that expert alone, and
+// a count for each expert's entry says when they are there, long before its turn; with a barrier
+// of the grid instead, the SMs stood idle for 6 us (one token) to 12 us (64).  h is kept as two bf16 values, the
 // nearest one and the nearest of what is left, 16 bits of it in all: the second product takes
 // both, which costs no time, and y's error is that of its own rounding (with one: 1.4 times that).
 // Sums over an expert's rows stay in fp32 until every slot of a token is there; a second
@@ -45,7 +46,6 @@ namespace mp {
 namespace {
 
 constexpr int LOGIT_THREADS = 128, LOGIT_WARPS = LOGIT_THREADS / 32;
-constexpr int64_t PREFETCH = 384 * 1024; // bytes of the second product's weights that a CTA asks into L2 early
 constexpr int MATH_WARPS = 8, MATH_THREADS = 32 * MATH_WARPS;
 constexpr int JOIN_WARPS = 3, JOIN_THREADS = 32 * JOIN_WARPS;   // 12 warps in all: 168 registers a thread
 constexpr int LAYER_THREADS = MATH_THREADS + 32 + JOIN_THREADS;   // and a warp of copies
@@ -55,7 +55,8 @@ constexpr int B_MOST = 8, RED_MOST = 4;  // slots for tokens' rows, buffers of s
 constexpr size_t LAYER_SMEM = 227 * 1024;
 
 struct LayerControl {
-    unsigned arrived[3];   // CTAs at the barriers of k_layer: after the products and, before them, the choice
+    unsigned arrived[2];   // CTAs at the barriers of k_layer: after the choice, after the products
+    unsigned done[MP_MAX_EXPERTS + MP_MAX_LAYER_TOKENS * 32 / 8];   // units of the first product, by entry
 };
 
 struct LayerArgs {
@@ -117,7 +118,7 @@ struct PairSums {
     }
 };
 
-// Logits of one expert and TB tokens, a CTA each; the first CTAs also clear k_layer's barriers and
+// Logits of one expert and TB tokens, a CTA each; the first CTAs also clear k_layer's counts and
 // lay x out in rows of whole 16 bytes where k_layer wants that.  VEC: rows of x and the
 // router are whole chunks of 4 on 16 (8) bytes.
 template <typename L, int TB, bool VEC> __global__ void __launch_bounds__(LOGIT_THREADS) k_layer_logits(const LayerArgs a)
@@ -126,7 +127,9 @@ template <typename L, int TB, bool VEC> __global__ void __launch_bounds__(LOGIT_
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x, t0 = blockIdx.y * TB;
-    if (e == 0 && t0 == 0 && threadIdx.x < 3) a.control->arrived[threadIdx.x] = 0;
+    if (e == 0 && t0 == 0)
+        for (int i = threadIdx.x; i < static_cast<int>(sizeof(LayerControl) / 4); i += LOGIT_THREADS)
+            reinterpret_cast<unsigned *>(a.control)[i] = 0;
     if (a.xp != nullptr)
         for (int t = t0 + e; t < min(t0 + TB, a.T); t += gridDim.x)
             for (int c = threadIdx.x; c < a.Hp; c += LOGIT_THREADS)
@@ -235,7 +238,7 @@ __device__ __forceinline__ void most_barrier()
     asm volatile("bar.sync 2, %0;" ::"n"(LAYER_THREADS - 32) : "memory");
 }
 
-// Waits until `count` CTAs have arrived; at most 4 s.
+// Waits until there have been `count` arrivals; at most 4 s.
 __device__ __forceinline__ bool grid_wait(const unsigned *arrived, unsigned count, volatile int *gave_up)
 {
     const uint64_t t0 = now_ns();
@@ -291,6 +294,7 @@ struct Cut {
 struct LayerCuts {
     Cut of[2];      // of the first product and of the second
     int b_rows;     // tokens' rows in a slot; twice as many of the second product, both values of h
+    int b_second;   // bytes from the first product's slots to the second's
     int reds;       // buffers for the units' sums
 };
 
@@ -308,7 +312,7 @@ template <int NT, bool ODD> struct Layer {
         uint64_t b_full[2][B_MOST], b_empty[2][B_MOST], red_full[RED_MOST], red_empty[RED_MOST];
         int32_t idx[32];      // of one token
         float weights[32];
-        int gave_up, entries;
+        int gave_up, join_off, entries;
     };
     // After the rings: what is above, the units' sums, and the routes: tokens of each expert (a bit
     // each), where an expert's routes start, routes by expert, entries.
@@ -347,7 +351,7 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
             mbar_init(smem_u32(&s.red_empty[i]), JOIN_WARPS);
         }
         mbar_init_fence();
-        s.gave_up = 0;
+        s.gave_up = s.join_off = 0;
     }
     for (int e = threadIdx.x; e < 2 * a.E; e += LAYER_THREADS) tokens_of[e] = 0;
     pdl_trigger();
@@ -377,8 +381,8 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
             __threadfence();
             __syncwarp();
             if (lane == 0) {
-                grid_arrive(&a.control->arrived[2]);
-                (void)grid_wait(&a.control->arrived[2], gridDim.x, gave_up);
+                grid_arrive(&a.control->arrived[0]);
+                (void)grid_wait(&a.control->arrived[0], gridDim.x, gave_up);
             }
         }
         __syncthreads();
@@ -456,23 +460,27 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
     };
 
     if (warp == MATH_WARPS) {
-        // The tokens' rows: x, and after the grid's barrier h.
+        // The tokens' rows: x, then h.
         bool on = true;
         for (int p = 0; p < 2 && on; ++p) {
             const Cut cut = cuts.of[p];
             const int K = p == 0 ? a.Hp : a.Fp, units = entries * (p == 0 ? blocks0 : blocks1), KC = cut.kc();
             const int pitch = cut.b_pitch(), slot = cuts.b_rows * (p + 1) * pitch;
+            const uint32_t ring = b_ring + (p == 0 ? 0 : cuts.b_second);
             const mp_bf16_t *const base = p == 0 ? (a.xp != nullptr ? a.xp : a.x) : a.h;
-            if (p == 1) {
-                if (lane == 0) on = grid_wait(&a.control->arrived[0], gridDim.x, gave_up);
-                on = __shfl_sync(FULL_MASK, static_cast<int>(on), 0) != 0;
-                __syncwarp();
-                fence_async();   // what other SMs stored, by the copies to come
-            }
+            int there = -1;   // the last entry whose h is
             int at_stage = 0, issued = 0;
             uint32_t phase = 0;
             for (Walk w(blockIdx.x, step, p == 0 ? blocks0 : blocks1); w.u < units && on; w.next(step)) {
                 const typename L::Entry en = entry[w.entry];
+                if (p == 1 && w.entry != there) {
+                    there = w.entry;
+                    if (lane == 0) on = grid_wait(&a.control->done[there], blocks0, gave_up);
+                    on = __shfl_sync(FULL_MASK, static_cast<int>(on), 0) != 0;
+                    if (!on) break;
+                    __syncwarp();
+                    fence_async();   // what other SMs stored, by the copies to come
+                }
                 const mp_bf16_t *row = base;
                 if (lane < en.count) {
                     const int r = order[en.first + lane];
@@ -481,7 +489,7 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
                 for (int k0 = 0; k0 < K; k0 += KC) {
                     on = warp_wait(smem_u32(&s.b_empty[p][at_stage]), phase ^ 1u, gave_up);
                     if (!on) break;
-                    const uint32_t bar = smem_u32(&s.b_full[p][at_stage]), to = b_ring + at_stage * slot;
+                    const uint32_t bar = smem_u32(&s.b_full[p][at_stage]), to = ring + at_stage * slot;
                     const uint32_t bytes = static_cast<uint32_t>(min(KC, K - k0)) * 2u;
                     if (lane == 0) mbar_expect(bar, bytes * en.count * (p + 1));
                     __syncwarp();
@@ -681,7 +689,7 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
                     fetch(ws);   // the weights are in registers: their slot takes the next ones
                     if (on) on = warp_wait(smem_u32(&s.b_full[p][bs]), bp, gave_up);
                     if (on) {
-                        const uint32_t b_at = b_ring + bs * slot + kg * STAGE_COLS * 2, b_rest = cuts.b_rows * pitch;
+                        const uint32_t b_at = b_ring + (p == 0 ? 0 : cuts.b_second) + bs * slot + kg * STAGE_COLS * 2, b_rest = cuts.b_rows * pitch;
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
                             if (t >= tiles) break;
@@ -746,6 +754,12 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
                 const typename L::Entry en = entry[w.entry];
                 const int block = w.block;
                 if (on) on = warp_wait(smem_u32(&s.red_full[reds]), rp, gave_up);
+                if (p == 0) {
+                    // All three warps, or none: a barrier follows.
+                    if (!on) s.join_off = 1;
+                    join_barrier();
+                    on = *static_cast<volatile int *>(&s.join_off) == 0;
+                }
                 if (on) {
                     const float *const from = red + reds * L::RED;
                     // The warps' shares of the columns, in order.
@@ -794,34 +808,23 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&s.red_empty[reds]));
+                    if (p == 0) {   // h of this unit is there for the copies of all SMs
+                        fence_async();
+                        __threadfence();
+                        join_barrier();
+                        if (tid == 0) grid_arrive(&a.control->done[w.entry]);
+                    }
                 }
                 if (++reds == cuts.reds) {
                     reds = 0;
                     rp ^= 1u;
                 }
             }
-            // What this CTA made is there for the others: their copies read h.
-            if (p == 0) fence_async();
-            __threadfence();
-            join_barrier();
-            if (tid == 0) grid_arrive(&a.control->arrived[p]);
-            if (p == 0 && tid == 0) {
-                // While the last CTAs finish, memory goes on with this one's weights of the second
-                // product: rows of a unit lie one after another.
-                const uintptr_t base = reinterpret_cast<uintptr_t>(a.w2), last = base + static_cast<uint64_t>(a.E) * a.O * a.F * 2;
-                int64_t left = PREFETCH;
-                for (Walk w(blockIdx.x, step, blocks1); w.u < entries * blocks1 && left > 0; w.next(step)) {
-                    const int row = w.block * cuts.of[1].u(), rows = min(cuts.of[1].u(), a.O - row);
-                    uintptr_t from = base + (static_cast<uint64_t>(entry[w.entry].expert) * a.O + row) * a.F * 2;
-                    uintptr_t to = min(from + static_cast<uint64_t>(rows) * a.F * 2, last) & ~static_cast<uintptr_t>(15);
-                    from = (from + 15) & ~static_cast<uintptr_t>(15);
-                    if (to <= from) continue;
-                    const uint32_t bytes = static_cast<uint32_t>(min(to - from, static_cast<uintptr_t>(PREFETCH)));
-                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(bytes) : "memory");
-                    left -= bytes;
-                }
-            }
         }
+        // What this CTA made is there for the others.
+        __threadfence();
+        join_barrier();
+        if (tid == 0) grid_arrive(&a.control->arrived[1]);
         if (tid == 0) (void)grid_wait(&a.control->arrived[1], gridDim.x, gave_up);
     }
     if (warp == MATH_WARPS) return;
@@ -893,24 +896,35 @@ template <int NT, bool ODD> mp_status_t launch_layer(const LayerArgs &a, cudaStr
     for (int t = 0; t < a.T; ++t) missed *= 1.0 - static_cast<double>(a.K) / a.E;
     const double busy = a.E * (1.0 - missed), tokens = R / busy;
     const int64_t entries = static_cast<int64_t>(busy * ((tokens + L::TOKENS - 1) / L::TOKENS > 1.5 ? 2 : 1) + 0.5);
-    const int most_log = NT == 1 ? 3 : NT == 2 ? 2 : 1;   // so that two slots for the tokens' rows fit
+    // So that slots for the tokens' rows fit: two or more of each product but with the largest tables.
+    constexpr int most_log[2] = {NT == 1 ? 3 : NT == 2 ? 1 : 0, NT == 1 ? 2 : NT == 2 ? 1 : 0};
     LayerCuts cuts;
-    cuts.of[0] = cut_product(entries, a.F * (gated ? 2 : 1), a.H, tokens, most_log);
-    cuts.of[1] = cut_product(entries, a.O, a.F, 2.0 * tokens, most_log);
+    cuts.of[0] = cut_product(entries, a.F * (gated ? 2 : 1), a.H, tokens, most_log[0]);
+    cuts.of[1] = cut_product(entries, a.O, a.F, 2.0 * tokens, most_log[1]);
     cuts.b_rows = a.T < L::TOKENS ? a.T : L::TOKENS;
     const size_t fixed = L::tables(a.E, R) + static_cast<size_t>(L::STAGES) * L::W_STAGE;
     const size_t slots[2] = {static_cast<size_t>(cuts.b_rows) * cuts.of[0].b_pitch(),
                              static_cast<size_t>(cuts.b_rows) * 2 * cuts.of[1].b_pitch()};
-    const size_t slot = slots[0] > slots[1] ? slots[0] : slots[1];
-    for (cuts.reds = RED_MOST; cuts.reds > 1 && fixed + cuts.reds * L::RED * 4 + 3 * slot > LAYER_SMEM; --cuts.reds) {
+    for (cuts.reds = RED_MOST; cuts.reds > 1 && fixed + cuts.reds * L::RED * 4 + 2 * (slots[0] + slots[1]) > LAYER_SMEM; --cuts.reds) {
     }
-    size_t room = LAYER_SMEM - fixed - static_cast<size_t>(cuts.reds) * L::RED * 4;
-    if (room > B_MOST * slot) room = B_MOST * slot;
-    room = room / 16 * 16;
-    for (int p = 0; p < 2; ++p) {
-        cuts.of[p].b_stages = static_cast<int>(room / slots[p]);
-        if (cuts.of[p].b_stages > B_MOST) cuts.of[p].b_stages = B_MOST;
+    size_t bytes = fixed + static_cast<size_t>(cuts.reds) * L::RED * 4 + slots[0] + slots[1];
+    if (bytes > LAYER_SMEM) return MP_ERR_UNSUPPORTED;
+    int n[2] = {1, 1};
+    for (bool more = true; more;) {   // of the product with fewer, as long as there is room
+        more = false;
+        for (int i = 0; i < 2 && !more; ++i) {
+            const int p = (n[1] < n[0]) ^ (i == 1);
+            if (n[p] < B_MOST && bytes + slots[p] <= LAYER_SMEM) {
+                bytes += slots[p];
+                ++n[p];
+                more = true;
+            }
+        }
     }
+    cuts.of[0].b_stages = n[0];
+    cuts.of[1].b_stages = n[1];
+    cuts.b_second = static_cast<int>(n[0] * slots[0]);
+    const int room = static_cast<int>(n[0] * slots[0] + n[1] * slots[1]);
     // No more CTAs than units: a barrier of few is quicker.
     const int64_t most = (a.E < R ? a.E : R) + R / L::TOKENS;
     int64_t wide = 0;
@@ -922,7 +936,7 @@ template <int NT, bool ODD> mp_status_t launch_layer(const LayerArgs &a, cudaStr
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = static_cast<unsigned>(most * wide < sms ? most * wide : sms);
     cfg.blockDim = LAYER_THREADS;
-    cfg.dynamicSmemBytes = fixed + static_cast<size_t>(cuts.reds) * L::RED * 4 + room;
+    cfg.dynamicSmemBytes = bytes;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeCooperative;
@@ -931,7 +945,7 @@ template <int NT, bool ODD> mp_status_t launch_layer(const LayerArgs &a, cudaStr
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    (void)cudaLaunchKernelEx(&cfg, k_layer<NT, ODD>, a, cuts, static_cast<int>(room));
+    (void)cudaLaunchKernelEx(&cfg, k_layer<NT, ODD>, a, cuts, room);
     return check_launch();
 }
 
@@ -959,7 +973,7 @@ struct LayerSpace {
     LayerSpace(int64_t T, int64_t E, int64_t K, int H, int F, int64_t O)
     {
         const auto next = [](size_t from, size_t bytes) { return (from + bytes + 255) / 256 * 256; };
-        logits = 256;
+        logits = next(0, sizeof(LayerControl));
         xp = next(logits, static_cast<size_t>(T * E) * 4);
         h = next(xp, static_cast<size_t>(T) * whole(H) * 2);
         out = next(h, static_cast<size_t>(T * K) * whole(F) * 4);
