@@ -190,9 +190,18 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  "l"(src), "r"(bytes), "r"(bar)
                  : "memory");
 }
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes = 16)
+// Weights are read once: they leave L2 before anything else does.
+__device__ __forceinline__ uint64_t read_once()
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    uint64_t policy;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    return policy;
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint64_t policy, int bytes = 16)
+{
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(bytes),
+                 "l"(policy)
+                 : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // All but this thread's last S groups of copies have landed.
@@ -528,6 +537,7 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
             return f < (p == 0 ? a.F : a.O) ? f : -1;
         };
         const int rows_of[2] = {a.F * (gated ? 2 : 1), a.O};   // of one expert
+        const uint64_t policy = read_once();
         // The stage that is copied next: its product, unit and first column, and where this lane's
         // part of the unit's rows is: pieces of 16 bytes lane & 15, of rows lane >> 4 and every other on.
         int f_p = 0, f_k = 0, f_depth = a.H, f_kc = cuts.of[0].kc(), f_rg = warp >> cuts.of[0].log_kg;
@@ -577,7 +587,7 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
                         for (int i = 0; i < 8; ++i)
                             if (f_rows >> i & 1)
                                 copy16(dst + 2 * i * L::W_PITCH,
-                                       f_row[i >> 2] + off + piece * 16 + static_cast<int64_t>(i & 3) * 4 * f_depth);
+                                       f_row[i >> 2] + off + piece * 16 + static_cast<int64_t>(i & 3) * 4 * f_depth, policy);
                     }
                 } else if (n > 0) {
                     // The granules of 16 bytes that hold the piece; of the tensor's first and last,
@@ -600,7 +610,7 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
                                 for (const char *v = first; v < from + 16 && v < last; v += 2)
                                     *reinterpret_cast<uint16_t *>(row + (v - src)) = __ldg(reinterpret_cast<const uint16_t *>(v));
                             } else {
-                                copy16(smem_u32(row) + gran * 16, from, end - from < 16 ? static_cast<int>(end - from) : 16);
+                                copy16(smem_u32(row) + gran * 16, from, policy, end - from < 16 ? static_cast<int>(end - from) : 16);
                             }
                         }
                     }
