@@ -15,9 +15,10 @@
 // k_layer: one CTA an SM, launched cooperatively.  A unit of work is U rows of an expert's
 // weights against all tokens of that expert (an entry: up to 8 NT of them).  Each of eight
 // warps multiplies 16 weight rows by its share of the columns, 128 a stage, which it copies
-// itself, by cp.async into a ring of its own; one more warp copies the tokens' rows for all, and
-// three join the eight warps' sums, in a fixed order, and apply bias and activation, so that the
-// eight never wait for a unit's end.
+// itself, by cp.async into a ring of its own; one more warp copies the tokens' rows for all, two
+// join the eight warps' sums, in a fixed order, and apply bias and activation, so that the
+// eight never wait for a unit's end, and one claims the units, in order and a little ahead, since
+// SMs do not get equal shares of the memory (an equal share of units each: 10% at 64 tokens).
 // (mma.m16n8k16: weight rows are its 16, tokens its 8.  Bytes bound it, so the tensor cores'
 // older form is enough, and it needs no tile of 128 rows.)  The rings do not stop between the
 // two products: the second's units of an expert need the activations h of that expert alone, and
@@ -47,8 +48,9 @@ namespace {
 
 constexpr int LOGIT_THREADS = 128, LOGIT_WARPS = LOGIT_THREADS / 32;
 constexpr int MATH_WARPS = 8, MATH_THREADS = 32 * MATH_WARPS;
-constexpr int JOIN_WARPS = 3, JOIN_THREADS = 32 * JOIN_WARPS;   // 12 warps in all: 168 registers a thread
-constexpr int LAYER_THREADS = MATH_THREADS + 32 + JOIN_THREADS;   // and a warp of copies
+constexpr int COPY_WARP = MATH_WARPS, CLAIM_WARP = MATH_WARPS + 1, JOIN_WARPS = 2, JOIN_THREADS = 32 * JOIN_WARPS;
+constexpr int LAYER_THREADS = MATH_THREADS + 64 + JOIN_THREADS;   // 12 warps: 168 registers a thread
+constexpr int CLAIMS = 16, CLAIM_AHEAD = 2;   // units known to a CTA at most; beyond the one whose copies start
 constexpr int STAGE_COLS = 128;          // of a warp
 constexpr int ROW_PAD = 64;              // bytes between tokens' rows
 constexpr int B_MOST = 8, RED_MOST = 4;  // slots for tokens' rows, buffers of sums
@@ -56,6 +58,7 @@ constexpr size_t LAYER_SMEM = 227 * 1024;
 
 struct LayerControl {
     unsigned arrived[2];   // CTAs at the barriers of k_layer: after the choice, after the products
+    unsigned claimed;      // units
     unsigned done[MP_MAX_EXPERTS + MP_MAX_LAYER_TOKENS * 32 / 8];   // units of the first product, by entry
 };
 
@@ -235,7 +238,7 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 {
     return __all_sync(FULL_MASK, mbar_wait(bar, parity, gave_up)) != 0;
 }
-// The joining warps; all but the warp of copies.  A warp comes to a barrier as a whole.
+// The joining warps; they and the multiplying ones.  A warp comes to a barrier as a whole.
 __device__ __forceinline__ void join_barrier()
 {
     __syncwarp();
@@ -244,7 +247,7 @@ __device__ __forceinline__ void join_barrier()
 __device__ __forceinline__ void most_barrier()
 {
     __syncwarp();
-    asm volatile("bar.sync 2, %0;" ::"n"(LAYER_THREADS - 32) : "memory");
+    asm volatile("bar.sync 2, %0;" ::"n"(MATH_THREADS + JOIN_THREADS) : "memory");
 }
 
 // Waits until there have been `count` arrivals; at most 4 s.
@@ -317,8 +320,13 @@ template <int NT, bool ODD> struct Layer {
     struct Entry {
         int expert, first, count;   // tokens' routes: order[first ..]
     };
+    struct Unit {
+        int p, entry, block;   // product (2: no more units), entry, rows
+    };
     struct Shared {
         uint64_t b_full[2][B_MOST], b_empty[2][B_MOST], red_full[RED_MOST], red_empty[RED_MOST];
+        uint64_t claim_full[CLAIMS], claim_seen[CLAIMS], claim_empty[CLAIMS];
+        Unit unit[CLAIMS];
         int32_t idx[32];      // of one token
         float weights[32];
         int gave_up, join_off, entries;
@@ -358,6 +366,11 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
         for (int i = 0; i < RED_MOST; ++i) {
             mbar_init(smem_u32(&s.red_full[i]), MATH_WARPS);
             mbar_init(smem_u32(&s.red_empty[i]), JOIN_WARPS);
+        }
+        for (int i = 0; i < CLAIMS; ++i) {
+            mbar_init(smem_u32(&s.claim_full[i]), 1);
+            mbar_init(smem_u32(&s.claim_seen[i]), MATH_WARPS);
+            mbar_init(smem_u32(&s.claim_empty[i]), MATH_WARPS + 1 + JOIN_WARPS);
         }
         mbar_init_fence();
         s.gave_up = s.join_off = 0;
@@ -446,181 +459,182 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
     const int entries = s.entries;
     const int FU = gated ? cuts.of[0].u() / 2 : cuts.of[0].u();   // columns of h that a unit makes
     const int blocks0 = (a.F + FU - 1) / FU, blocks1 = (a.O + cuts.of[1].u() - 1) / cuts.of[1].u();
-    const int step = gridDim.x;
-
-    // The units of a CTA, one after another.
-    struct Walk {
-        int u, entry, block, nb, by_entry, by_block;
-        __device__ __forceinline__ Walk(int from, int step, int blocks) : u(from), nb(blocks)
-        {
-            entry = from / blocks; block = from - entry * blocks;
-            by_entry = step / blocks; by_block = step - by_entry * blocks;
-        }
-        __device__ __forceinline__ void next(int step)
-        {
-            u += step;
-            entry += by_entry;
-            block += by_block;
-            if (block >= nb) {
-                block -= nb;
-                ++entry;
-            }
-        }
+    const int rows_of[2] = {a.F * (gated ? 2 : 1), a.O};   // of one expert
+    // Unit i of this CTA, once it is claimed.
+    const auto unit_at = [&](int i, typename L::Unit &u) {
+        const bool there = warp_wait(smem_u32(&s.claim_full[i % CLAIMS]), (i / CLAIMS) & 1, gave_up);
+        if (there) u = s.unit[i % CLAIMS];
+        return there && u.p < 2;
+    };
+    const auto unit_done = [&](int i) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s.claim_empty[i % CLAIMS]));
     };
 
-    if (warp == MATH_WARPS) {
+    if (warp == CLAIM_WARP) {
+        // Units of the first product come before all of the second: those wait for them.
+        if (lane != 0) return;
+        const int first = entries * blocks0, all = first + entries * blocks1;
+        for (int i = 0;; ++i) {
+            if (i > CLAIM_AHEAD) {
+                const int seen = i - 1 - CLAIM_AHEAD;
+                if (!mbar_wait(smem_u32(&s.claim_seen[seen % CLAIMS]), (seen / CLAIMS) & 1, gave_up)) return;
+            }
+            if (!mbar_wait(smem_u32(&s.claim_empty[i % CLAIMS]), ((i / CLAIMS) & 1) ^ 1, gave_up)) return;
+            const int u = static_cast<int>(atomicAdd(&a.control->claimed, 1u));
+            const int p = u >= first, at = p ? u - first : u, nb = p ? blocks1 : blocks0;
+            typename L::Unit &to = s.unit[i % CLAIMS];
+            to.entry = at / nb;
+            to.block = at - to.entry * nb;
+            to.p = u < all ? p : 2;
+            mbar_arrive(smem_u32(&s.claim_full[i % CLAIMS]));
+            if (u >= all) return;
+        }
+    }
+    if (warp == COPY_WARP) {
         // The tokens' rows: x, then h.
+        int at_stage[2] = {0, 0}, issued[2] = {0, 0}, there = -1;   // there: the last entry whose h is
+        uint32_t phase[2] = {0, 0};
         bool on = true;
-        for (int p = 0; p < 2 && on; ++p) {
-            const Cut cut = cuts.of[p];
-            const int K = p == 0 ? a.Hp : a.Fp, units = entries * (p == 0 ? blocks0 : blocks1), KC = cut.kc();
-            const int pitch = cut.b_pitch(), slot = cuts.b_rows * (p + 1) * pitch;
+        typename L::Unit u;
+        for (int i = 0; on && unit_at(i, u); ++i) {
+            const int p = u.p, K = p == 0 ? a.Hp : a.Fp, KC = cuts.of[p].kc();
+            const int pitch = cuts.of[p].b_pitch(), slot = cuts.b_rows * (p + 1) * pitch;
             const uint32_t ring = b_ring + (p == 0 ? 0 : cuts.b_second);
-            const mp_bf16_t *const base = p == 0 ? (a.xp != nullptr ? a.xp : a.x) : a.h;
-            int there = -1;   // the last entry whose h is
-            int at_stage = 0, issued = 0;
-            uint32_t phase = 0;
-            for (Walk w(blockIdx.x, step, p == 0 ? blocks0 : blocks1); w.u < units && on; w.next(step)) {
-                const typename L::Entry en = entry[w.entry];
-                if (p == 1 && w.entry != there) {
-                    there = w.entry;
-                    if (lane == 0) on = grid_wait(&a.control->done[there], blocks0, gave_up);
-                    on = __shfl_sync(FULL_MASK, static_cast<int>(on), 0) != 0;
-                    if (!on) break;
-                    __syncwarp();
-                    fence_async();   // what other SMs stored, by the copies to come
-                }
-                const mp_bf16_t *row = base;
+            const typename L::Entry en = entry[u.entry];
+            if (p == 1 && u.entry != there) {
+                there = u.entry;
+                if (lane == 0) on = grid_wait(&a.control->done[there], blocks0, gave_up);
+                on = __shfl_sync(FULL_MASK, static_cast<int>(on), 0) != 0;
+                if (!on) break;
+                __syncwarp();
+                fence_async();   // what other SMs stored, by the copies to come
+            }
+            const mp_bf16_t *row = p == 0 ? (a.xp != nullptr ? a.xp : a.x) : a.h;
+            if (lane < en.count) {
+                const int r = order[en.first + lane];
+                row += static_cast<int64_t>(p == 0 ? r / a.K : 2 * r) * K;
+            }
+            int st = at_stage[p], n = issued[p];
+            uint32_t ph = phase[p];
+            for (int k0 = 0; k0 < K; k0 += KC) {
+                on = warp_wait(smem_u32(&s.b_empty[p][st]), ph ^ 1u, gave_up);
+                if (!on) break;
+                const uint32_t bar = smem_u32(&s.b_full[p][st]), to = ring + st * slot;
+                const uint32_t bytes = static_cast<uint32_t>(min(KC, K - k0)) * 2u;
+                if (lane == 0) mbar_expect(bar, bytes * en.count * (p + 1));
+                __syncwarp();
                 if (lane < en.count) {
-                    const int r = order[en.first + lane];
-                    row += static_cast<int64_t>(p == 0 ? r / a.K : 2 * r) * K;
+                    bulk_load(to + lane * pitch, row + k0, bytes, bar);
+                    if (p == 1) bulk_load(to + (cuts.b_rows + lane) * pitch, row + K + k0, bytes, bar);
                 }
-                for (int k0 = 0; k0 < K; k0 += KC) {
-                    on = warp_wait(smem_u32(&s.b_empty[p][at_stage]), phase ^ 1u, gave_up);
-                    if (!on) break;
-                    const uint32_t bar = smem_u32(&s.b_full[p][at_stage]), to = ring + at_stage * slot;
-                    const uint32_t bytes = static_cast<uint32_t>(min(KC, K - k0)) * 2u;
-                    if (lane == 0) mbar_expect(bar, bytes * en.count * (p + 1));
-                    __syncwarp();
-                    if (lane < en.count) {
-                        bulk_load(to + lane * pitch, row + k0, bytes, bar);
-                        if (p == 1) bulk_load(to + (cuts.b_rows + lane) * pitch, row + K + k0, bytes, bar);
-                    }
-                    if (issued < B_MOST) ++issued;
-                    if (++at_stage == cut.b_stages) {
-                        at_stage = 0;
-                        phase ^= 1u;
-                    }
+                if (n < B_MOST) ++n;
+                if (++st == cuts.of[p].b_stages) {
+                    st = 0;
+                    ph ^= 1u;
                 }
             }
-            if (*gave_up && lane == 0)   // copies in flight land before the shared memory goes
-                for (int i = 0; i < cut.b_stages && i < issued; ++i) {
-                    if (--at_stage < 0) {
-                        at_stage = cut.b_stages - 1;
-                        phase ^= 1u;
-                    }
-                    mbar_drain(smem_u32(&s.b_full[p][at_stage]), phase);
-                }
+            at_stage[p] = st; issued[p] = n; phase[p] = ph;
+            unit_done(i);
         }
-    } else if (warp < MATH_WARPS) {
-        // A warp that gives up a wait goes on without waiting or multiplying, so that the barriers
-        // of the others come to their ends.
+        if (*gave_up && lane == 0)   // copies in flight land before the shared memory goes
+            for (int p = 0; p < 2; ++p)
+                for (int i = 0; i < cuts.of[p].b_stages && i < issued[p]; ++i) {
+                    if (--at_stage[p] < 0) {
+                        at_stage[p] = cuts.of[p].b_stages - 1;
+                        phase[p] ^= 1u;
+                    }
+                    mbar_drain(smem_u32(&s.b_full[p][at_stage[p]]), phase[p]);
+                }
+        return;
+    }
+    if (warp < MATH_WARPS) {
         const int g = lane >> 2, c = lane & 3;
         uint8_t *const ring = smem + warp * 16 * L::W_PITCH;
-        // Row i of group rg of a unit of product p: its row in the expert's weights, -1: there is none.
-        const auto weight_row = [&](int p, int block, int rg, int i) {
-            if (p == 0 && gated) {   // 8 rows of the gate, 8 of the other half
-                const int f = block * FU + rg * 8 + (i & 7);
-                return f < a.F ? f + (i & 8 ? a.F : 0) : -1;
-            }
-            const int f = block * cuts.of[p].u() + rg * 16 + i;
-            return f < (p == 0 ? a.F : a.O) ? f : -1;
-        };
-        const int rows_of[2] = {a.F * (gated ? 2 : 1), a.O};   // of one expert
         const uint64_t policy = read_once();
-        // The stage that is copied next: its product, unit and first column, and where this lane's
-        // part of the unit's rows is: pieces of 16 bytes lane & 15, of rows lane >> 4 and every other on.
-        int f_p = 0, f_k = 0, f_depth = a.H, f_kc = cuts.of[0].kc(), f_rg = warp >> cuts.of[0].log_kg;
-        int f_col = (warp & (cuts.of[0].kg() - 1)) * STAGE_COLS;   // this warp's columns of a stage
-        Walk f_walk(blockIdx.x, step, blocks0);
-        const char *f_row[2];
-        unsigned f_rows = 0;   // a bit for each of the eight rows that is there
+        // Rows of a group of 16, as they lie in the expert's weights: 8 from `first` on, and 8 from
+        // first + 8 + jump on, of which some are there.
+        struct Rows {
+            int first, jump, there[2];
+        };
+        const auto rows_at = [&](int p, int block, int rg) {
+            Rows r;
+            if (p == 0 && gated) {   // 8 of the gate, 8 of the other half
+                r.first = block * FU + rg * 8;
+                r.jump = a.F - 8;
+                r.there[0] = r.there[1] = a.F - r.first;
+            } else {
+                r.first = block * cuts.of[p].u() + rg * 16;
+                r.jump = 0;
+                r.there[0] = (p == 0 ? a.F : a.O) - r.first;
+                r.there[1] = r.there[0] - 8;
+            }
+            return r;
+        };
+        // The stage that is copied next.
+        int f_i = 0, f_p = 0, f_k = 0, f_depth = 0, f_col = 0;   // unit, product, first column, all columns, this warp's first
+        const char *f_row = nullptr;   // the first row, at this warp's columns
+        int64_t f_jump = 0;
+        unsigned f_rows = 0;           // a bit for each of the 16 rows that is there
         const auto aim = [&]() {
-            if (f_p == 0 && f_walk.u >= entries * blocks0) {
-                f_p = 1;
-                f_walk = Walk(blockIdx.x, step, blocks1);
-                f_depth = a.F;
-                f_kc = cuts.of[1].kc();
-                f_rg = warp >> cuts.of[1].log_kg;
-                f_col = (warp & (cuts.of[1].kg() - 1)) * STAGE_COLS;
+            typename L::Unit u;
+            if (!unit_at(f_i, u)) {
+                f_p = 2;
+                return;
             }
-            if (f_p == 1 && f_walk.u >= entries * blocks1) f_p = 2;
-            if (f_p == 2) return;
-            const char *const base = reinterpret_cast<const char *>(f_p == 0 ? a.w1 : a.w2) +
-                                     static_cast<int64_t>(entry[f_walk.entry].expert) * (f_p == 0 ? rows_of[0] : rows_of[1]) * f_depth * 2;
-            // Rows 2 apart lie 2 rows apart, but for the step into the other half.
-            f_rows = 0;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int first = weight_row(f_p, f_walk.block, f_rg, (lane >> 4) + 8 * i);
-                const int last = weight_row(f_p, f_walk.block, f_rg, (lane >> 4) + 8 * i + 6);
-                f_row[i] = base + static_cast<int64_t>(first) * f_depth * 2;
-                if (last >= 0) {
-                    f_rows |= 15u << 4 * i;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 3; ++j)
-                        f_rows |= static_cast<unsigned>(weight_row(f_p, f_walk.block, f_rg, (lane >> 4) + 8 * i + 2 * j) >= 0) << (4 * i + j);
-                }
-            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&s.claim_seen[f_i % CLAIMS]));
+            ++f_i;
+            f_p = u.p;
+            f_k = 0;
+            f_depth = f_p == 0 ? a.H : a.F;
+            f_col = (warp & (cuts.of[f_p].kg() - 1)) * STAGE_COLS;
+            const Rows r = rows_at(f_p, u.block, warp >> cuts.of[f_p].log_kg);
+            f_row = reinterpret_cast<const char *>(f_p == 0 ? a.w1 : a.w2) +
+                    ((static_cast<int64_t>(entry[u.entry].expert) * (f_p == 0 ? rows_of[0] : rows_of[1]) + r.first) * f_depth + f_col) * 2;
+            f_jump = static_cast<int64_t>(r.jump) * f_depth * 2;
+            f_rows = ((1u << min(max(r.there[0], 0), 8)) - 1u) | ((1u << min(max(r.there[1], 0), 8)) - 1u) << 8;
         };
         const auto fetch = [&](int stage) {
             if (f_p < 2) {
                 const int n = f_depth - f_k - f_col;   // columns that are there
-                const int piece = lane & 15;
-                uint8_t *const to = ring + stage * L::W_STAGE;
-                const int64_t off = (static_cast<int64_t>(f_k) + f_col) * 2;
+                const uint32_t to = smem_u32(ring + stage * L::W_STAGE);
                 if (!ODD) {
+                    // A lane: 16 bytes of each other row.
+                    const int piece = lane & 15, row = lane >> 4;
                     if (piece * 8 < n) {
-                        const uint32_t dst = smem_u32(to) + (lane >> 4) * L::W_PITCH + (piece ^ ((lane >> 4) & 1) << 2) * 16;
+                        const uint32_t dst = to + row * L::W_PITCH + (piece ^ row << 2) * 16;
+                        const char *const src = f_row + f_k * 2 + piece * 16 + static_cast<int64_t>(row) * 2 * f_depth;
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            if (f_rows >> i & 1)
-                                copy16(dst + 2 * i * L::W_PITCH,
-                                       f_row[i >> 2] + off + piece * 16 + static_cast<int64_t>(i & 3) * 4 * f_depth, policy);
+                            if (f_rows >> (row + 2 * i) & 1)
+                                copy16(dst + 2 * i * L::W_PITCH, src + static_cast<int64_t>(i) * 4 * f_depth + (i >= 4 ? f_jump : 0), policy);
                     }
                 } else if (n > 0) {
-                    // The granules of 16 bytes that hold the piece; of the tensor's first and last,
-                    // which may reach beyond it, only what is of it is read.
+                    // The granules of 16 bytes, up to 17 a row, that hold the piece; of the tensor's first
+                    // and last, which may reach beyond it, only what is of it is read.
                     const char *const base = reinterpret_cast<const char *>(f_p == 0 ? a.w1 : a.w2);
                     const char *const end = base + static_cast<int64_t>(f_p == 0 ? rows_of[0] : rows_of[1]) * a.E * f_depth * 2;
+                    const int bytes = min(n, STAGE_COLS) * 2;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if (!(f_rows >> i & 1)) continue;
-                        const char *const first = f_row[i >> 2] + off + static_cast<int64_t>(i & 3) * 4 * f_depth;
-                        const char *const last = first + min(n, STAGE_COLS) * 2;
-                        uint8_t *const row = to + ((lane >> 4) + 2 * i) * L::W_PITCH;
-                        const char *src = reinterpret_cast<const char *>(reinterpret_cast<uintptr_t>(first) & ~static_cast<uintptr_t>(15));
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {   // and the seventeenth granule, by the first lane
-                            const int gran = q == 0 ? piece : 16;
-                            const char *const from = src + gran * 16;
-                            if ((q == 1 && piece != 0) || from >= last) continue;
-                            if (from < base) {
-                                for (const char *v = first; v < from + 16 && v < last; v += 2)
-                                    *reinterpret_cast<uint16_t *>(row + (v - src)) = __ldg(reinterpret_cast<const uint16_t *>(v));
-                            } else {
-                                copy16(smem_u32(row) + gran * 16, from, policy, end - from < 16 ? static_cast<int>(end - from) : 16);
-                            }
+                    for (int i = 0; i < 9; ++i) {
+                        const int j = lane + 32 * i, row = j / 17, gran = j - 17 * row;
+                        if (j >= 16 * 17 || !(f_rows >> row & 1)) continue;
+                        const char *const first = f_row + f_k * 2 + static_cast<int64_t>(row) * 2 * f_depth + (row >= 8 ? f_jump : 0);
+                        const char *const src = reinterpret_cast<const char *>(reinterpret_cast<uintptr_t>(first) & ~static_cast<uintptr_t>(15)) + gran * 16;
+                        if (src >= first + bytes) continue;
+                        const uint32_t dst = to + row * L::W_PITCH + gran * 16;
+                        if (src >= base) {
+                            copy16(dst, src, policy, end - src < 16 ? static_cast<int>(end - src) : 16);
+                        } else {
+                            for (const char *v = first; v < src + 16 && v < first + bytes; v += 2)
+                                asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + static_cast<uint32_t>(v - src)),
+                                             "h"(__ldg(reinterpret_cast<const uint16_t *>(v))) : "memory");
                         }
                     }
                 }
-                f_k += f_kc;
-                if (f_k >= f_depth) {
-                    f_k = 0;
-                    f_walk.next(step);
-                    aim();
-                }
+                f_k += cuts.of[f_p].kc();
+                if (f_k >= f_depth) aim();
             }
             copy_commit();
         };
@@ -631,19 +645,24 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
         int ws = 0, reds = 0;
         uint32_t rp = 0;
         bool on = true;
-        for (int p = 0; p < 2; ++p) {
+        int b_stage[2] = {0, 0};
+        uint32_t b_phase[2] = {0, 0};
+        typename L::Unit u;
+        for (int at_unit = 0; on && unit_at(at_unit, u); ++at_unit) {
+            const int p = u.p;
             const Cut cut = cuts.of[p];
-            const int K = p == 0 ? a.H : a.F, units = entries * (p == 0 ? blocks0 : blocks1), KC = cut.kc();
+            const int K = p == 0 ? a.H : a.F, KC = cut.kc();
             const int rg = warp >> cut.log_kg, kg = warp & (cut.kg() - 1), UP = cut.u() + 4;
             const int pitch = cut.b_pitch(), slot = cuts.b_rows * (p + 1) * pitch;
+            const uint32_t b_first = b_ring + (p == 0 ? 0 : cuts.b_second) + kg * STAGE_COLS * 2, b_rest = cuts.b_rows * pitch;
             // A column past the last token takes any row that is there: nobody reads its sums.
             int b_row[NT];
 #pragma unroll
             for (int t = 0; t < NT; ++t) b_row[t] = min(t * 8 + g, cuts.b_rows - 1) * pitch;
-            int bs = 0;
-            uint32_t bp = 0;
-            for (Walk w(blockIdx.x, step, p == 0 ? blocks0 : blocks1); w.u < units; w.next(step)) {
-                const typename L::Entry en = entry[w.entry];
+            int bs = b_stage[p];
+            uint32_t bp = b_phase[p];
+            {
+                const typename L::Entry en = entry[u.entry];
                 const int tiles = (en.count + 7) >> 3;
                 float acc[NT][CHAINS][4];   // sums of products that do not wait for one another
 #pragma unroll
@@ -652,11 +671,11 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
                     for (int i = 0; i < 4 * CHAINS; ++i) acc[t][i >> 2][i & 3] = 0.0f;
                 uint32_t shift[2] = {0, 0};   // where a row's first value lies in its granule
                 if (ODD) {
+                    const Rows r = rows_at(p, u.block, rg);
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
                         shift[i] = static_cast<uint32_t>((reinterpret_cast<uintptr_t>(p == 0 ? a.w1 : a.w2) +
-                                                          (static_cast<int64_t>(en.expert) * rows_of[p] +
-                                                           weight_row(p, w.block, rg, g + 8 * i)) * K * 2) & 15u);
+                                                          (static_cast<int64_t>(en.expert) * rows_of[p] + r.first + g + i * (8 + r.jump)) * K * 2) & 15u);
                 }
                 for (int k0 = 0; k0 < K; k0 += KC) {
                     copy_wait<STAGES - 1>();
@@ -699,7 +718,7 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
                     fetch(ws);   // the weights are in registers: their slot takes the next ones
                     if (on) on = warp_wait(smem_u32(&s.b_full[p][bs]), bp, gave_up);
                     if (on) {
-                        const uint32_t b_at = b_ring + (p == 0 ? 0 : cuts.b_second) + bs * slot + kg * STAGE_COLS * 2, b_rest = cuts.b_rows * pitch;
+                        const uint32_t b_at = b_first + bs * slot;
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
                             if (t >= tiles) break;
@@ -749,28 +768,28 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
                     rp ^= 1u;
                 }
             }
+            b_stage[p] = bs;
+            b_phase[p] = bp;
+            unit_done(at_unit);
         }
         copy_wait<0>();
     } else {
-        const int tid = threadIdx.x - MATH_THREADS - 32;
+        const int tid = threadIdx.x - MATH_THREADS - 64;
         int reds = 0;
         uint32_t rp = 0;
-        bool on = true;
-        for (int p = 0; p < 2; ++p) {
-            const Cut cut = cuts.of[p];
-            const int units = entries * (p == 0 ? blocks0 : blocks1), KG = cut.kg(), U = cut.u(), UP = U + 4;
-            const int log_fu = 7 - cut.log_kg - (gated ? 1 : 0), log_u = 7 - cut.log_kg;
-            for (Walk w(blockIdx.x, step, p == 0 ? blocks0 : blocks1); w.u < units; w.next(step)) {
-                const typename L::Entry en = entry[w.entry];
-                const int block = w.block;
-                if (on) on = warp_wait(smem_u32(&s.red_full[reds]), rp, gave_up);
-                if (p == 0) {
-                    // All three warps, or none: a barrier follows.
-                    if (!on) s.join_off = 1;
-                    join_barrier();
-                    on = *static_cast<volatile int *>(&s.join_off) == 0;
-                }
-                if (on) {
+        for (int i = 0;; ++i) {
+            typename L::Unit u;
+            u.p = 0;
+            bool on = unit_at(i, u);
+            if (on) on = warp_wait(smem_u32(&s.red_full[reds]), rp, gave_up);
+            if (!on) s.join_off = 1;   // both warps, or none: barriers follow
+            join_barrier();
+            if (*static_cast<volatile int *>(&s.join_off) != 0) break;
+            const int p = u.p, block = u.block, KG = cuts.of[p].kg(), U = cuts.of[p].u(), UP = U + 4;
+            const int log_u = 7 - cuts.of[p].log_kg, log_fu = log_u - (gated ? 1 : 0);
+            const typename L::Entry en = entry[u.entry];
+            {
+                {
                     const float *const from = red + reds * L::RED;
                     // The warps' shares of the columns, in order.
                     const auto joined = [&](int token, int row) {
@@ -822,7 +841,7 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
                         fence_async();
                         __threadfence();
                         join_barrier();
-                        if (tid == 0) grid_arrive(&a.control->done[w.entry]);
+                        if (tid == 0) grid_arrive(&a.control->done[u.entry]);
                     }
                 }
                 if (++reds == cuts.reds) {
@@ -830,6 +849,7 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
                     rp ^= 1u;
                 }
             }
+            unit_done(i);
         }
         // What this CTA made is there for the others.
         __threadfence();
@@ -837,11 +857,11 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
         if (tid == 0) grid_arrive(&a.control->arrived[1]);
         if (tid == 0) (void)grid_wait(&a.control->arrived[1], gridDim.x, gave_up);
     }
-    if (warp == MATH_WARPS) return;
     most_barrier();
-    const int tid = threadIdx.x < MATH_THREADS ? threadIdx.x : threadIdx.x - 32;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * (LAYER_THREADS - 32) + tid; i < static_cast<int64_t>(a.T) * a.O;
-         i += static_cast<int64_t>(gridDim.x) * (LAYER_THREADS - 32)) {
+    constexpr int LEFT = MATH_THREADS + JOIN_THREADS;
+    const int tid = threadIdx.x < MATH_THREADS ? threadIdx.x : threadIdx.x - 64;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * LEFT + tid; i < static_cast<int64_t>(a.T) * a.O;
+         i += static_cast<int64_t>(gridDim.x) * LEFT) {
         const int t = static_cast<int>(i / a.O), o = static_cast<int>(i - static_cast<int64_t>(t) * a.O);
         const float *const from = a.out + static_cast<int64_t>(t) * a.K * a.O + o;
         float y = 0.0f;
