@@ -244,6 +244,20 @@ __device__ __forceinline__ void join_barrier()
     __syncwarp();
     asm volatile("bar.sync 1, %0;" ::"n"(JOIN_THREADS) : "memory");
 }
+// Whether all of the joining threads say so; a barrier of them too.
+__device__ __forceinline__ bool join_all(bool v)
+{
+    uint32_t all;
+    __syncwarp();
+    asm volatile("{\n\t.reg .pred p, q;\n\t"
+                 "setp.ne.u32 q, %1, 0;\n\t"
+                 "bar.red.and.pred p, 1, %2, q;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(all)
+                 : "r"(static_cast<uint32_t>(v)), "n"(JOIN_THREADS)
+                 : "memory");
+    return all != 0;
+}
 __device__ __forceinline__ void most_barrier()
 {
     __syncwarp();
@@ -329,7 +343,7 @@ template <int NT, bool ODD> struct Layer {
         Unit unit[CLAIMS];
         int32_t idx[32];      // of one token
         float weights[32];
-        int gave_up, join_off, entries;
+        int gave_up, entries;
     };
     // After the rings: what is above, the units' sums, and the routes: tokens of each expert (a bit
     // each), where an expert's routes start, routes by expert, entries.
@@ -373,7 +387,7 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
             mbar_init(smem_u32(&s.claim_empty[i]), MATH_WARPS + 1 + JOIN_WARPS);
         }
         mbar_init_fence();
-        s.gave_up = s.join_off = 0;
+        s.gave_up = 0;
     }
     for (int e = threadIdx.x; e < 2 * a.E; e += LAYER_THREADS) tokens_of[e] = 0;
     pdl_trigger();
@@ -661,112 +675,110 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
             for (int t = 0; t < NT; ++t) b_row[t] = min(t * 8 + g, cuts.b_rows - 1) * pitch;
             int bs = b_stage[p];
             uint32_t bp = b_phase[p];
-            {
-                const typename L::Entry en = entry[u.entry];
-                const int tiles = (en.count + 7) >> 3;
-                float acc[NT][CHAINS][4];   // sums of products that do not wait for one another
+            const typename L::Entry en = entry[u.entry];
+            const int tiles = (en.count + 7) >> 3;
+            float acc[NT][CHAINS][4];   // sums of products that do not wait for one another
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int i = 0; i < 4 * CHAINS; ++i) acc[t][i >> 2][i & 3] = 0.0f;
-                uint32_t shift[2] = {0, 0};   // where a row's first value lies in its granule
-                if (ODD) {
-                    const Rows r = rows_at(p, u.block, rg);
+                for (int i = 0; i < 4 * CHAINS; ++i) acc[t][i >> 2][i & 3] = 0.0f;
+            uint32_t shift[2] = {0, 0};   // where a row's first value lies in its granule
+            if (ODD) {
+                const Rows r = rows_at(p, u.block, rg);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        shift[i] = static_cast<uint32_t>((reinterpret_cast<uintptr_t>(p == 0 ? a.w1 : a.w2) +
-                                                          (static_cast<int64_t>(en.expert) * rows_of[p] + r.first + g + i * (8 + r.jump)) * K * 2) & 15u);
-                }
-                for (int k0 = 0; k0 < K; k0 += KC) {
-                    copy_wait<STAGES - 1>();
-                    __syncwarp();
-                    const int n = min(KC, K - k0) - kg * STAGE_COLS;   // columns of this warp
-                    const uint32_t w_at = smem_u32(ring + ws * L::W_STAGE) + g * L::W_PITCH;
-                    uint4 a0[4], a1[4];
+                for (int i = 0; i < 2; ++i)
+                    shift[i] = static_cast<uint32_t>((reinterpret_cast<uintptr_t>(p == 0 ? a.w1 : a.w2) +
+                                                      (static_cast<int64_t>(en.expert) * rows_of[p] + r.first + g + i * (8 + r.jump)) * K * 2) & 15u);
+            }
+            for (int k0 = 0; k0 < K; k0 += KC) {
+                copy_wait<STAGES - 1>();
+                __syncwarp();
+                const int n = min(KC, K - k0) - kg * STAGE_COLS;   // columns of this warp
+                const uint32_t w_at = smem_u32(ring + ws * L::W_STAGE) + g * L::W_PITCH;
+                uint4 a0[4], a1[4];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int col = q * 32 + c * 8;
-                        a0[q] = a1[q] = make_uint4(0, 0, 0, 0);
-                        if (col >= n) continue;
-                        if (!ODD) {
-                            const uint32_t from = w_at + ((q * 4 + c) ^ (g & 1) << 2) * 16;
-                            a0[q] = lds128(from);
-                            a1[q] = lds128(from + 8 * L::W_PITCH);
-                        } else {
-                            uint32_t v[2][4];
+                for (int q = 0; q < 4; ++q) {
+                    const int col = q * 32 + c * 8;
+                    a0[q] = a1[q] = make_uint4(0, 0, 0, 0);
+                    if (col >= n) continue;
+                    if (!ODD) {
+                        const uint32_t from = w_at + ((q * 4 + c) ^ (g & 1) << 2) * 16;
+                        a0[q] = lds128(from);
+                        a1[q] = lds128(from + 8 * L::W_PITCH);
+                    } else {
+                        uint32_t v[2][4];
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const uint32_t from = w_at + 8 * i * L::W_PITCH + ((shift[i] + col * 2) & ~3u);
-                                const uint32_t by = (shift[i] & 2u) * 8u;
-                                uint32_t word[5];
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t from = w_at + 8 * i * L::W_PITCH + ((shift[i] + col * 2) & ~3u);
+                            const uint32_t by = (shift[i] & 2u) * 8u;
+                            uint32_t word[5];
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) word[j] = lds32(from + 4 * j);
-                                word[4] = by != 0 ? lds32(from + 16) : 0u;
+                            for (int j = 0; j < 4; ++j) word[j] = lds32(from + 4 * j);
+                            word[4] = by != 0 ? lds32(from + 16) : 0u;
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    // past the row's end is another row, or what the ring held before
-                                    const int left = n - col - 2 * j;
-                                    const uint32_t mask = left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
-                                    v[i][j] = __funnelshift_r(word[j], word[j + 1], by) & mask;
-                                }
-                            }
-                            a0[q] = make_uint4(v[0][0], v[0][1], v[0][2], v[0][3]);
-                            a1[q] = make_uint4(v[1][0], v[1][1], v[1][2], v[1][3]);
-                        }
-                    }
-                    __syncwarp();
-                    fetch(ws);   // the weights are in registers: their slot takes the next ones
-                    if (on) on = warp_wait(smem_u32(&s.b_full[p][bs]), bp, gave_up);
-                    if (on) {
-                        const uint32_t b_at = b_first + bs * slot;
-#pragma unroll
-                        for (int t = 0; t < NT; ++t) {
-                            if (t >= tiles) break;
-#pragma unroll
-                            for (int half = 0; half < 2; ++half) {   // of h: the nearest values, and the rest
-                                if (half > p) break;
-                                uint4 b[4];
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    const int col = q * 32 + c * 8;
-                                    b[q] = make_uint4(0, 0, 0, 0);
-                                    if (col < n) b[q] = lds128(b_at + (half ? b_rest : 0u) + b_row[t] + col * 2);
-                                }
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    mma16816(acc[t][2 * q % CHAINS], a0[q].x, a1[q].x, a0[q].y, a1[q].y, b[q].x, b[q].y);
-                                    mma16816(acc[t][(2 * q + 1) % CHAINS], a0[q].z, a1[q].z, a0[q].w, a1[q].w, b[q].z, b[q].w);
-                                }
+                            for (int j = 0; j < 4; ++j) {
+                                // past the row's end is another row, or what the ring held before
+                                const int left = n - col - 2 * j;
+                                const uint32_t mask = left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
+                                v[i][j] = __funnelshift_r(word[j], word[j + 1], by) & mask;
                             }
                         }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&s.b_empty[p][bs]));
-                    }
-                    if (++ws == STAGES) ws = 0;
-                    if (++bs == cut.b_stages) {
-                        bs = 0;
-                        bp ^= 1u;
+                        a0[q] = make_uint4(v[0][0], v[0][1], v[0][2], v[0][3]);
+                        a1[q] = make_uint4(v[1][0], v[1][1], v[1][2], v[1][3]);
                     }
                 }
-                if (on) on = warp_wait(smem_u32(&s.red_empty[reds]), rp ^ 1u, gave_up);
+                __syncwarp();
+                fetch(ws);   // the weights are in registers: their slot takes the next ones
+                if (on) on = warp_wait(smem_u32(&s.b_full[p][bs]), bp, gave_up);
                 if (on) {
-                    float *const to = red + reds * L::RED;
+                    const uint32_t b_at = b_first + bs * slot;
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
                         if (t >= tiles) break;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            to[(kg * TOKENS + t * 8 + 2 * c + (i & 1)) * UP + rg * 16 + g + (i & 2 ? 8 : 0)] =
-                                CHAINS == 4 ? (acc[t][0][i] + acc[t][1][i]) + (acc[t][2 % CHAINS][i] + acc[t][3 % CHAINS][i])
-                                            : acc[t][0][i] + acc[t][1][i];
+                        for (int half = 0; half < 2; ++half) {   // of h: the nearest values, and the rest
+                            if (half > p) break;
+                            uint4 b[4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const int col = q * 32 + c * 8;
+                                b[q] = make_uint4(0, 0, 0, 0);
+                                if (col < n) b[q] = lds128(b_at + (half ? b_rest : 0u) + b_row[t] + col * 2);
+                            }
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                mma16816(acc[t][2 * q % CHAINS], a0[q].x, a1[q].x, a0[q].y, a1[q].y, b[q].x, b[q].y);
+                                mma16816(acc[t][(2 * q + 1) % CHAINS], a0[q].z, a1[q].z, a0[q].w, a1[q].w, b[q].z, b[q].w);
+                            }
+                        }
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&s.red_full[reds]));
+                    if (lane == 0) mbar_arrive(smem_u32(&s.b_empty[p][bs]));
                 }
-                if (++reds == cuts.reds) {
-                    reds = 0;
-                    rp ^= 1u;
+                if (++ws == STAGES) ws = 0;
+                if (++bs == cut.b_stages) {
+                    bs = 0;
+                    bp ^= 1u;
                 }
+            }
+            if (on) on = warp_wait(smem_u32(&s.red_empty[reds]), rp ^ 1u, gave_up);
+            if (on) {
+                float *const to = red + reds * L::RED;
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    if (t >= tiles) break;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        to[(kg * TOKENS + t * 8 + 2 * c + (i & 1)) * UP + rg * 16 + g + (i & 2 ? 8 : 0)] =
+                            CHAINS == 4 ? (acc[t][0][i] + acc[t][1][i]) + (acc[t][2 % CHAINS][i] + acc[t][3 % CHAINS][i])
+                                        : acc[t][0][i] + acc[t][1][i];
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&s.red_full[reds]));
+            }
+            if (++reds == cuts.reds) {
+                reds = 0;
+                rp ^= 1u;
             }
             b_stage[p] = bs;
             b_phase[p] = bp;
@@ -782,72 +794,66 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
             u.p = 0;
             bool on = unit_at(i, u);
             if (on) on = warp_wait(smem_u32(&s.red_full[reds]), rp, gave_up);
-            if (!on) s.join_off = 1;   // both warps, or none: barriers follow
-            join_barrier();
-            if (*static_cast<volatile int *>(&s.join_off) != 0) break;
+            if (!join_all(on)) break;   // both warps, or none: barriers follow
             const int p = u.p, block = u.block, KG = cuts.of[p].kg(), U = cuts.of[p].u(), UP = U + 4;
             const int log_u = 7 - cuts.of[p].log_kg, log_fu = log_u - (gated ? 1 : 0);
             const typename L::Entry en = entry[u.entry];
-            {
-                {
-                    const float *const from = red + reds * L::RED;
-                    // The warps' shares of the columns, in order.
-                    const auto joined = [&](int token, int row) {
-                        float v = from[token * UP + row];
+            const float *const from = red + reds * L::RED;
+            // The warps' shares of the columns, in order.
+            const auto joined = [&](int token, int row) {
+                float v = from[token * UP + row];
 #pragma unroll 2
-                        for (int k = 1; k < KG; ++k) v += from[(k * TOKENS + token) * UP + row];
-                        return v;
-                    };
-                    if (p == 0) {
-                        const mp_bf16_t *b1 = a.b1 == nullptr ? nullptr
-                                                              : a.b1 + static_cast<int64_t>(en.expert) * a.F * (gated ? 2 : 1);
-                        for (int i = tid; i < FU * en.count; i += JOIN_THREADS) {
-                            const int token = i >> log_fu, j = i & (FU - 1), f = block * FU + j;
-                            if (f >= a.Fp) continue;
-                            float h = 0.0f;   // up to a row's last 16 bytes
-                            if (f < a.F) {
-                                // Rows of the products: tiles of 8 of the gate and 8 of the other half.
-                                h = joined(token, gated ? (j >> 3) * 16 + (j & 7) : j);
-                                if (b1 != nullptr) h += bf16_value(b1 + f);
-                                h = act_of(a.act, h);
-                                if (gated) {
-                                    float o = joined(token, (j >> 3) * 16 + (j & 7) + 8);
-                                    if (b1 != nullptr) o += bf16_value(b1 + a.F + f);
-                                    h *= o;
-                                }
-                            }
-                            mp_bf16_t *const to = a.h + static_cast<int64_t>(order[en.first + token]) * 2 * a.Fp + f;
-                            const float value[1] = {h};
-                            const mp_bf16_t near = pack(value);
-                            float back[1];
-                            unpack(near, back);
-                            const float rest[1] = {isfinite(back[0]) ? h - back[0] : 0.0f};
-                            to[0] = near;
-                            to[a.Fp] = pack(rest);
-                        }
-                    } else {
-                        const mp_bf16_t *b2 = a.b2 == nullptr ? nullptr : a.b2 + static_cast<int64_t>(en.expert) * a.O;
-                        for (int i = tid; i < U * en.count; i += JOIN_THREADS) {
-                            const int token = i >> log_u, j = i & (U - 1), o = block * U + j;
-                            if (o >= a.O) continue;
-                            float v = joined(token, j);
-                            if (b2 != nullptr) v += bf16_value(b2 + o);
-                            a.out[static_cast<int64_t>(order[en.first + token]) * a.O + o] = v;
+                for (int k = 1; k < KG; ++k) v += from[(k * TOKENS + token) * UP + row];
+                return v;
+            };
+            if (p == 0) {
+                const mp_bf16_t *b1 = a.b1 == nullptr ? nullptr
+                                                      : a.b1 + static_cast<int64_t>(en.expert) * a.F * (gated ? 2 : 1);
+                for (int i = tid; i < FU * en.count; i += JOIN_THREADS) {
+                    const int token = i >> log_fu, j = i & (FU - 1), f = block * FU + j;
+                    if (f >= a.Fp) continue;
+                    float h = 0.0f;   // up to a row's last 16 bytes
+                    if (f < a.F) {
+                        // Rows of the products: tiles of 8 of the gate and 8 of the other half.
+                        h = joined(token, gated ? (j >> 3) * 16 + (j & 7) : j);
+                        if (b1 != nullptr) h += bf16_value(b1 + f);
+                        h = act_of(a.act, h);
+                        if (gated) {
+                            float o = joined(token, (j >> 3) * 16 + (j & 7) + 8);
+                            if (b1 != nullptr) o += bf16_value(b1 + a.F + f);
+                            h *= o;
                         }
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&s.red_empty[reds]));
-                    if (p == 0) {   // h of this unit is there for the copies of all SMs
-                        fence_async();
-                        __threadfence();
-                        join_barrier();
-                        if (tid == 0) grid_arrive(&a.control->done[u.entry]);
-                    }
+                    mp_bf16_t *const to = a.h + static_cast<int64_t>(order[en.first + token]) * 2 * a.Fp + f;
+                    const float value[1] = {h};
+                    const mp_bf16_t near = pack(value);
+                    float back[1];
+                    unpack(near, back);
+                    const float rest[1] = {isfinite(back[0]) ? h - back[0] : 0.0f};
+                    to[0] = near;
+                    to[a.Fp] = pack(rest);
                 }
-                if (++reds == cuts.reds) {
-                    reds = 0;
-                    rp ^= 1u;
+            } else {
+                const mp_bf16_t *b2 = a.b2 == nullptr ? nullptr : a.b2 + static_cast<int64_t>(en.expert) * a.O;
+                for (int i = tid; i < U * en.count; i += JOIN_THREADS) {
+                    const int token = i >> log_u, j = i & (U - 1), o = block * U + j;
+                    if (o >= a.O) continue;
+                    float v = joined(token, j);
+                    if (b2 != nullptr) v += bf16_value(b2 + o);
+                    a.out[static_cast<int64_t>(order[en.first + token]) * a.O + o] = v;
                 }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&s.red_empty[reds]));
+            if (p == 0) {   // h of this unit is there for the copies of all SMs
+                fence_async();
+                __threadfence();
+                join_barrier();
+                if (tid == 0) grid_arrive(&a.control->done[u.entry]);
+            }
+            if (++reds == cuts.reds) {
+                reds = 0;
+                rp ^= 1u;
             }
             unit_done(i);
         }
@@ -860,22 +866,38 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
     most_barrier();
     constexpr int LEFT = MATH_THREADS + JOIN_THREADS;
     const int tid = threadIdx.x < MATH_THREADS ? threadIdx.x : threadIdx.x - 64;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * LEFT + tid; i < static_cast<int64_t>(a.T) * a.O;
+    // The slots of each token, in order; four columns a thread where rows of sums are whole 16 bytes.
+    const int wide = a.O % 4 == 0 ? 4 : 1, across = a.O / wide;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * LEFT + tid; i < static_cast<int64_t>(a.T) * across;
          i += static_cast<int64_t>(gridDim.x) * LEFT) {
-        const int t = static_cast<int>(i / a.O), o = static_cast<int>(i - static_cast<int64_t>(t) * a.O);
+        const int t = static_cast<int>(i / across), o = static_cast<int>(i - static_cast<int64_t>(t) * across) * wide;
         const float *const from = a.out + static_cast<int64_t>(t) * a.K * a.O + o;
-        float y = 0.0f;
+        float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         for (int k0 = 0; k0 < a.K; k0 += 8) {   // eight loads at a time
-            float v[8];
+            float4 v[8];
+            float w[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                v[k] = k0 + k < a.K && idx[t * a.K + k0 + k] >= 0 ? __ldcg(from + static_cast<int64_t>(k0 + k) * a.O) : 0.0f;
+            for (int k = 0; k < 8; ++k) {
+                const bool there = k0 + k < a.K && idx[t * a.K + k0 + k] >= 0;
+                const float *const at = from + static_cast<int64_t>(k0 + k) * a.O;
+                w[k] = there ? weights[t * a.K + k0 + k] : 0.0f;
+                v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (there && wide == 4) v[k] = __ldcg(reinterpret_cast<const float4 *>(at));
+                if (there && wide == 1) v[k].x = __ldcg(at);
+            }
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (k0 + k < a.K && idx[t * a.K + k0 + k] >= 0) y = fmaf(weights[t * a.K + k0 + k], v[k], y);
+            for (int k = 0; k < 8; ++k) {   // a slot that is not there adds 0 times 0
+                y[0] = fmaf(w[k], v[k].x, y[0]);
+                y[1] = fmaf(w[k], v[k].y, y[1]);
+                y[2] = fmaf(w[k], v[k].z, y[2]);
+                y[3] = fmaf(w[k], v[k].w, y[3]);
+            }
         }
-        const float v[1] = {y};
-        a.y[i] = pack(v);
+        mp_bf16_t *const to = a.y + static_cast<int64_t>(t) * a.O + o;
+        for (int j = 0; j < wide; ++j) {
+            const float v[1] = {y[j]};
+            to[j] = pack(v);
+        }
     }
     if (tid == 0 && *gave_up) or_status(a.status, MP_STATUS_STALLED);
 }
@@ -894,18 +916,20 @@ template <typename L> void launch_logits(const LayerArgs &a, cudaStream_t s)
 
 // The cut of a product of `rows` by `depth`, of `entries` entries: the fewest cycles by this count.
 // A stage of 32 KB takes 1,400 cycles at the copy bandwidth and more with many tokens' rows beside
-// it (which it reads for U rows each); a unit's end 300.  Large U is lighter on those rows, small
-// U divides evenly, and columns that a stage has and the product has not are idle warps.
-Cut cut_product(int64_t entries, int rows, int depth, double tokens, int most_log)
+// it (which it reads for U rows each), a unit's end 800.  Columns that a stage has and the product
+// has not are idle warps.  At the end SMs wait for the last units, and at the start of the second
+// product for about half a unit of the first (`late`).  One token through 8 experts of 1,024 x
+// 4,096, U of the first and second product: 128, 128 57.8 us; 64, 64 51.3; 32, 64 47.5; 32, 32 47.9;
+// 16, 32 50.4.  8 tokens through 57 of 512 x 7,168: 32, 128 209; 32, 64 221; 32, 32 246.
+Cut cut_product(int64_t entries, int rows, int depth, double tokens, int most_log, double late)
 {
     Cut best = {0, 0};
     double least = 0;
-    const int sms = sm_count();
     for (int log = 0; log <= most_log; ++log) {
         const Cut c = {log, 0};
-        const int64_t units = entries * ((rows + c.u() - 1) / c.u()), waves = (units + sms - 1) / sms;
-        const int64_t stages = (depth + c.kc() - 1) / c.kc();
-        const double cycles = static_cast<double>(waves) * (stages * 1400.0 * (1.0 + tokens / c.u()) + 300.0);
+        const int64_t units = entries * ((rows + c.u() - 1) / c.u()), stages = (depth + c.kc() - 1) / c.kc();
+        const double unit = static_cast<double>(stages) * 1400.0 * (1.0 + tokens / c.u()) + 800.0;
+        const double cycles = unit * (static_cast<double>(units) / sm_count() + late);
         if (log == 0 || cycles < least) {
             best = c;
             least = cycles;
@@ -929,8 +953,8 @@ template <int NT, bool ODD> mp_status_t launch_layer(const LayerArgs &a, cudaStr
     // So that slots for the tokens' rows fit: two or more of each product but with the largest tables.
     constexpr int most_log[2] = {NT == 1 ? 3 : NT == 2 ? 1 : 0, NT == 1 ? 2 : NT == 2 ? 1 : 0};
     LayerCuts cuts;
-    cuts.of[0] = cut_product(entries, a.F * (gated ? 2 : 1), a.H, tokens, most_log[0]);
-    cuts.of[1] = cut_product(entries, a.O, a.F, 2.0 * tokens, most_log[1]);
+    cuts.of[0] = cut_product(entries, a.F * (gated ? 2 : 1), a.H, tokens, most_log[0], 0.5);
+    cuts.of[1] = cut_product(entries, a.O, a.F, 2.0 * tokens, most_log[1], 1.0);
     cuts.b_rows = a.T < L::TOKENS ? a.T : L::TOKENS;
     const size_t fixed = L::tables(a.E, R) + static_cast<size_t>(L::STAGES) * L::W_STAGE;
     const size_t slots[2] = {static_cast<size_t>(cuts.b_rows) * cuts.of[0].b_pitch(),
