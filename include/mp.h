@@ -445,6 +445,7 @@ mp_status_t mp_moe_layer(const mp_bf16_t *x, const void *router, int32_t router_
  *   y            device [T,H] out, given exactly when pre_weight is
  *   stats        device fp32 [T,4] out or NULL, 16-byte aligned: mean and 1/sqrt(...)
  *                of x (0 without a post_weight; mean 0 for rms), the same of s
+ *   dev_status   device int32 or NULL: MP_STATUS_STALLED
  * s and y may each be the buffer of x, of residual or of a [T,H] gate.  A row's result
  * depends on nothing but that row and on whether rows are whole 16-byte vectors on 16-byte
  * boundaries, which is the faster way.  Limits: H <= MP_MAX_NORM_WIDTH; T < 2^31.
@@ -453,7 +454,7 @@ mp_status_t mp_block_norm(const void *x, const void *residual, int64_t T, int32_
                           int32_t dtype, int32_t kind, float eps, const void *post_weight,
                           const void *post_bias, const void *gate, int32_t gate_form,
                           float scale, const void *pre_weight, const void *pre_bias, void *s,
-                          void *y, float *stats, mp_stream_t stream);
+                          void *y, float *stats, int32_t *dev_status, mp_stream_t stream);
 
 /* Bytes of device workspace mp_block_norm_bwd needs: a multiple of 256, at least 256; 0
  * only for invalid sizes. */
@@ -479,6 +480,7 @@ size_t mp_block_norm_bwd_workspace_size(int64_t T, int32_t H);
  *              dtype or MP_DTYPE_FP32; the rest of type dtype.
  *   workspace  device, >= mp_block_norm_bwd_workspace_size(T,H) bytes, 16-byte
  *              aligned; may be NULL if no gradient of the shape [H] is wanted
+ *   dev_status device int32 or NULL: MP_STATUS_STALLED
  * g_residual may be the buffer of g_s or g_y, g_x that of any [T,H] input, g_gate the gate's.
  * Sums over rows are made in an order that depends on the sizes, types, alignment and
  * device alone.
@@ -490,7 +492,8 @@ mp_status_t mp_block_norm_bwd(const void *g_s, const void *g_y, const void *x, c
                               const void *pre_weight, void *g_x, void *g_residual,
                               void *g_gate, void *g_post_weight, void *g_post_bias,
                               void *g_pre_weight, void *g_pre_bias, int32_t grad_dtype,
-                              void *workspace, size_t workspace_bytes, mp_stream_t stream);
+                              void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                              mp_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Permute / unpermute  [d9d _permute_kernel, _unpermute_kernel; MBI]        */

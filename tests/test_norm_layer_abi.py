@@ -28,7 +28,7 @@ def changed(base, **new):
 
 NORM = dict(x=FAKE, residual=FAKE, T=4, H=64, dtype=0, kind=0, eps=1e-6, post_weight=FAKE, post_bias=None,
             gate=None, gate_form=0, scale=1.0, pre_weight=FAKE, pre_bias=None, s=FAKE, y=FAKE, stats=None,
-            stream=None)
+            status=None, stream=None)
 
 
 @pytest.mark.parametrize("new,code", [
@@ -51,7 +51,7 @@ def test_block_norm_rejects(lib, new, code):
 BWD = dict(g_s=FAKE, g_y=FAKE, x=FAKE, s=FAKE, stats=FAKE, T=4, H=64, dtype=0, kind=0, post_weight=FAKE,
            post_bias=None, gate=None, gate_form=0, scale=1.0, pre_weight=FAKE, g_x=FAKE, g_residual=None,
            g_gate=None, g_post_weight=None, g_post_bias=None, g_pre_weight=FAKE, g_pre_bias=None, grad_dtype=2,
-           workspace=FAKE, workspace_bytes=1 << 30, stream=None)
+           workspace=FAKE, workspace_bytes=1 << 30, status=None, stream=None)
 
 
 @pytest.mark.parametrize("new,code", [

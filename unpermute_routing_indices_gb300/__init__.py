@@ -614,7 +614,8 @@ def _gate_form(gate, like):
 
 def mp_block_norm(x, residual=None, *, post_weight=None, post_bias=None, gate=None,
                   scale: float = 1.0, pre_weight=None, pre_bias=None, kind: str = "rms",
-                  eps: float = 1e-6, with_stats: bool = False, s=None, y=None, stats=None):
+                  eps: float = 1e-6, with_stats: bool = False, s=None, y=None, stats=None,
+                  status=None):
     """The norm after a block and the one before the next, with gate, residual scale and
     residual between them: x [T,H] (fp32, bf16 or fp16) -> (s [T,H], y [T,H] or None,
     stats fp32 [T,4] or None):
@@ -647,11 +648,12 @@ def mp_block_norm(x, residual=None, *, post_weight=None, post_bias=None, gate=No
     if stats is not None:
         _need(stats, "stats", torch.float32, 2, dev)
         _shape(stats, "stats", (T, 4))
+    _opt(status, "status", torch.int32, 1, dev)
     with _on(dev):
         _check("mp_block_norm", _lib.load().mp_block_norm(
             _ptr(x), _ptr(residual), T, H, dt, _named(kind, NORMS, "kind"), float(eps),
             _ptr(post_weight), _ptr(post_bias), _ptr(gate), form, float(scale), _ptr(pre_weight),
-            _ptr(pre_bias), _ptr(s), _ptr(y), _ptr(stats), _stream(dev)))
+            _ptr(pre_bias), _ptr(s), _ptr(y), _ptr(stats), _ptr(status), _stream(dev)))
     return (x if as_is else s), y, stats
 
 
@@ -664,7 +666,7 @@ def mp_block_norm_bwd_workspace_size(num_tokens: int, width: int) -> int:
 
 def mp_block_norm_bwd(g_s, g_y, x, s, stats, *, post_weight=None, post_bias=None, gate=None,
                       scale: float = 1.0, pre_weight=None, pre_bias=None, kind: str = "rms",
-                      need=(True,) * 7, grad_dtype=None, workspace=None):
+                      need=(True,) * 7, grad_dtype=None, workspace=None, status=None):
     """Gradients of mp_block_norm at the s and stats that it gave: (g_x, g_residual, g_gate,
     g_post_weight, g_post_bias, g_pre_weight, g_pre_bias), None where `need` is false or
     the argument is absent.  g_s (None: zero) and g_y (None without a pre_weight) are
@@ -700,13 +702,14 @@ def mp_block_norm_bwd(g_s, g_y, x, s, stats, *, post_weight=None, post_bias=None
             workspace = torch.empty(mp_block_norm_bwd_workspace_size(T, H), dtype=torch.uint8, device=dev)
     else:
         _need(workspace, "workspace", torch.uint8, 1, dev)
+    _opt(status, "status", torch.int32, 1, dev)
     with _on(dev):
         _check("mp_block_norm_bwd", _lib.load().mp_block_norm_bwd(
             _ptr(g_s), _ptr(g_y), _ptr(x), _ptr(s), _ptr(stats), T, H, dt,
             _named(kind, NORMS, "kind"), _ptr(post_weight), _ptr(post_bias), _ptr(gate), form,
             float(scale), _ptr(pre_weight), _ptr(g_x), _ptr(g_residual), _ptr(g_gate),
             *(_ptr(t) for t in shared), DTYPES[grad_dtype], _ptr(workspace),
-            0 if workspace is None else workspace.numel(), _stream(dev)))
+            0 if workspace is None else workspace.numel(), _ptr(status), _stream(dev)))
     return (g_residual if same and need[0] else g_x), (g_residual if need[1] else None), g_gate, *shared
 
 

@@ -35,10 +35,10 @@ SIGNATURES = {
     "mp_moe_layer_workspace_size": (SZ, [I64, I32, I32, I32, I32, I32]),
     "mp_moe_layer": (I32, [P, P, I32, P, P, P, P, P, I64, I32, I32, I32, I32, I32, I32, I32, I32,
                            I32, I32, I32, F32, P, P, P, P, SZ, P, P]),
-    "mp_block_norm": (I32, [P, P, I64, I32, I32, I32, F32, P, P, P, I32, F32, P, P, P, P, P, P]),
+    "mp_block_norm": (I32, [P, P, I64, I32, I32, I32, F32, P, P, P, I32, F32, P, P, P, P, P, P, P]),
     "mp_block_norm_bwd_workspace_size": (SZ, [I64, I32]),
     "mp_block_norm_bwd": (I32, [P, P, P, P, P, I64, I32, I32, I32, P, P, P, I32, F32, P, P, P, P,
-                                P, P, P, P, I32, P, SZ, P]),
+                                P, P, P, P, I32, P, SZ, P, P]),
     "mp_permute": (I32, [P, P, P, I64, I32, I32, P, P, P]),
     "mp_unpermute": (I32, [P, P, P, I64, I32, I32, P, P]),
     "mp_unpermute_ep": (I32, [P, P, P, P, I64, I32, I32, I32, I32, I32, P, P]),

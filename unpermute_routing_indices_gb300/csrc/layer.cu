@@ -187,12 +187,6 @@ template <typename L, int TB, bool VEC> __global__ void __launch_bounds__(LOGIT_
 // from the choice to the result
 // ---------------------------------------------------------------------------
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
-}
 // Weights are read once: they leave L2 before anything else does.
 __device__ __forceinline__ uint64_t read_once()
 {

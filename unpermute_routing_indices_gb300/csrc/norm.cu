@@ -68,7 +68,8 @@ using namespace mp;
 extern "C" mp_status_t mp_block_norm(const void *x, const void *residual, int64_t T, int32_t H, int32_t dtype,
                                      int32_t kind, float eps, const void *post_weight, const void *post_bias,
                                      const void *gate, int32_t gate_form, float scale, const void *pre_weight,
-                                     const void *pre_bias, void *s, void *y, float *stats, mp_stream_t stream)
+                                     const void *pre_bias, void *s, void *y, float *stats, int32_t *dev_status,
+                                     mp_stream_t stream)
 {
     if (const mp_status_t st = norm_sizes(T, H, dtype, kind, gate_form, gate); st != MP_OK) return st;
     if (!(eps >= 0.0f)) return MP_ERR_INVALID_ARG;
@@ -84,7 +85,7 @@ extern "C" mp_status_t mp_block_norm(const void *x, const void *residual, int64_
     if (residual != nullptr) c.residual = rows_of(residual, c, dtype);
     if (gate_form == MP_GATE_ELEMENT) c.gate_rows = rows_of(gate, c, dtype);
     c.post_w = post_weight; c.post_b = post_bias; c.gate = gate; c.pre_w = pre_weight; c.pre_b = pre_bias;
-    c.s_out = s; c.y = y; c.stats = stats; c.stream = as_stream(stream);
+    c.s_out = s; c.y = y; c.stats = stats; c.status = dev_status; c.stream = as_stream(stream);
     c.vec = vectors(H, dtype, {x, residual, gate_form == MP_GATE_TOKEN ? nullptr : gate, post_weight, post_bias,
                                pre_weight, pre_bias, s, y});
     return dtype == MP_DTYPE_BF16   ? norm_forward<__nv_bfloat16>(c)
@@ -106,7 +107,7 @@ extern "C" mp_status_t mp_block_norm_bwd(const void *g_s, const void *g_y, const
                                          int32_t gate_form, float scale, const void *pre_weight, void *g_x,
                                          void *g_residual, void *g_gate, void *g_post_weight, void *g_post_bias,
                                          void *g_pre_weight, void *g_pre_bias, int32_t grad_dtype, void *workspace,
-                                         size_t workspace_bytes, mp_stream_t stream)
+                                         size_t workspace_bytes, int32_t *dev_status, mp_stream_t stream)
 {
     if (const mp_status_t st = norm_sizes(T, H, dtype, kind, gate_form, gate); st != MP_OK) return st;
     if (grad_dtype != dtype && grad_dtype != MP_DTYPE_FP32) return MP_ERR_INVALID_ARG;
@@ -151,7 +152,7 @@ extern "C" mp_status_t mp_block_norm_bwd(const void *g_s, const void *g_y, const
         c.g_x = g_x; c.g_residual = g_residual;
         c.g_gate = gate_form == MP_GATE_CHANNEL ? nullptr : g_gate;
         for (int i = 0; i < NORM_SHARED; ++i) c.sums[i] = sums[i];
-        c.stream = as_stream(stream);
+        c.status = dev_status; c.stream = as_stream(stream);
         const bool with_x = post_weight != nullptr || gate != nullptr;
         c.vec = vectors(H, dtype, {g_s, g_y, with_x ? x : nullptr, pre_weight != nullptr ? s : nullptr,
                                    gate_form == MP_GATE_TOKEN ? nullptr : gate, post_weight, post_bias, pre_weight,

@@ -4,13 +4,15 @@
 // Bytes bound these operators: a row is read once, worked on in registers, and written once.
 // W threads own a row, 16 values each, and a CTA of up to 512 threads works on R rows at a
 // time, each a group of its own with a barrier of its own.  While a group works on a row, its
-// next ones are on their way into shared memory by cp.async, STAGES of them in all.  What
+// next ones are on their way into shared memory, in as many slots as there is room for.  What
 // counts next is instructions: 8 values a thread took 81 a value (two norms, 4,096 wide: 188
 // us, the issue slots 81% full); hence 16, and arithmetic on pairs of fp32 (fma.rn.f32x2).
-//   VEC      rows of whole 16-byte vectors on 16-byte boundaries: a thread copies and reads
-//            vectors tid, tid + W, ... of the row, and nobody else's.
-//   not VEC  rows that start anywhere: the group copies the 16-byte granules that hold the
-//            row, and a thread reads values tid, tid + W, ...; a barrier in between.
+//   ROWS_BULK  rows of whole 16-byte vectors on 16-byte boundaries, 2 KB or more: one bulk copy a
+//              row and tensor (gradient at one norm, 16,384 x 4,096, alone: 88 us, by cp.async 96).
+//   ROWS_VEC   shorter ones: a thread copies vectors tid, tid + W, ... of the row by cp.async
+//              and reads nobody else's.
+//   ROWS_ANY   rows that start anywhere: the group copies the 16-byte granules that hold the row,
+//              and a thread reads values tid, tid + W, ...; a barrier in between.
 //   C 4      rows of more than 8192 values: not staged, 1024 threads read them as they need them.
 #pragma once
 
@@ -28,7 +30,9 @@ constexpr int NORM_PARTS = 304;     // partial sums of each: two CTAs on an SM
 constexpr int NORM_THREADS = 512;   // of a CTA, C 4: twice as many
 constexpr int NORM_BUDGET = 112 * 1024;   // shared memory of one of two CTAs on an SM
 constexpr int NORM_MOST = 225 * 1024;     // of one alone
-// What a barrier of a group costs is hidden by the other groups of the SM.
+constexpr int NORM_SLOTS = 4;
+
+enum { ROWS_ANY, ROWS_VEC, ROWS_BULK };
 
 // How T rows of H values are laid out.
 struct NormPlan {
@@ -40,6 +44,12 @@ struct NormPlan {
 struct NormRows {
     const void *at;   // [T,H]
     int64_t end;      // address past its last byte
+};
+// The tensors whose rows go through shared memory, and a row's place in a slot (-1: absent).
+struct NormInputs {
+    NormRows rows[5];
+    int slot[5], tensors;
+    void add(int i, const NormRows &r) { rows[i] = r; slot[i] = r.at != nullptr ? tensors++ : -1; }
 };
 
 __device__ __forceinline__ float norm_value(float v) { return v; }
@@ -108,7 +118,8 @@ __device__ __forceinline__ void cp_wait(int left)
 }
 
 // One group's view of its rows: N values a thread, in N2 pairs.
-template <typename D, bool VEC, int C> struct NormGroup {
+template <typename D, int M, int C> struct NormGroup {
+    static constexpr bool VEC = M != ROWS_ANY;
     static constexpr int N = 8 * C, N2 = 4 * C;
     static constexpr int NV = 16 / sizeof(D);    // values a vector
     static constexpr int VECS = N / NV;
@@ -116,8 +127,35 @@ template <typename D, bool VEC, int C> struct NormGroup {
     static constexpr int WARPS = 32;   // of a row at most
 
     int W, H, tid, group;
-    float *red;   // [2][WARPS] float4 of this group: see sums()
+    float *red;           // [2][M_MOST][WARPS] of this group: see sums()
+    uint32_t bars;        // ROWS_BULK: an mbarrier for each slot
+    volatile int *gave_up;
     int phase = 0;
+    uint32_t slot_phase = 0;
+
+    // What comes first in shared memory: the groups' sums, their mbarriers, a flag.  (Groups of
+    // less than a warp need neither of the first.)
+    static constexpr int RED = 2 * 3 * 32;   // floats a group
+    static constexpr __host__ __device__ size_t head(int W, int R) { return (W < 32 ? 1 : R) * (RED * 4 + NORM_SLOTS * 8) + 16; }
+    __device__ __forceinline__ void begin(uint8_t *smem, int W_, int R, int H_)
+    {
+        W = W_;
+        H = H_;
+        group = threadIdx.x / W;
+        tid = threadIdx.x - group * W;
+        const int own = W < 32 ? 0 : group;
+        red = reinterpret_cast<float *>(smem) + own * RED;
+        for (int i = tid; i < RED; i += W) red[i] = 0.0f;
+        bars = smem_u32(smem + (W < 32 ? 1 : R) * RED * 4 + own * NORM_SLOTS * 8);
+        int *const flag = reinterpret_cast<int *>(smem + head(W, R) - 16);
+        gave_up = flag;
+        if (M == ROWS_BULK && tid == 0) {
+            for (int i = 0; i < NORM_SLOTS; ++i) mbar_init(bars + 8 * i, 1);
+            mbar_init_fence();
+        }
+        if (threadIdx.x == 0) *flag = 0;
+        __syncthreads();
+    }
 
     __device__ __forceinline__ void barrier() const
     {
@@ -130,47 +168,41 @@ template <typename D, bool VEC, int C> struct NormGroup {
     // warp's lanes first (W <= 32: the W lanes of the row), then the warps.  Two
     // buffers in turn: a thread that is still reading one is waited for by the barrier
     // of the next sum.
-    template <int M> __device__ __forceinline__ void sums(float (&v)[M])
+    template <int S> __device__ __forceinline__ void sums(float (&v)[S])
     {
 #pragma unroll
         for (int d = 16; d; d >>= 1)
             if (d < W) {
 #pragma unroll
-                for (int i = 0; i < M; ++i) v[i] += __shfl_xor_sync(FULL_MASK, v[i], d);
+                for (int i = 0; i < S; ++i) v[i] += __shfl_xor_sync(FULL_MASK, v[i], d);
             }
         if (W <= 32) return;
         float *to = red + (phase & 1) * M_MOST * WARPS;
         phase ^= 1;
         if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-            for (int i = 0; i < M; ++i) to[i * WARPS + (tid >> 5)] = v[i];
+            for (int i = 0; i < S; ++i) to[i * WARPS + (tid >> 5)] = v[i];
         }
         barrier();
         const int warps = W >> 5;   // slots past the last warp hold 0
         if (warps <= 8) {
 #pragma unroll
-            for (int i = 0; i < M; ++i) {
+            for (int i = 0; i < S; ++i) {
                 const float4 p = reinterpret_cast<const float4 *>(to + i * WARPS)[0];
                 const float4 q = reinterpret_cast<const float4 *>(to + i * WARPS)[1];
                 v[i] = ((p.x + p.y) + (p.z + p.w)) + ((q.x + q.y) + (q.z + q.w));
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < M; ++i) v[i] = to[i * WARPS + (threadIdx.x & 31)];
+            for (int i = 0; i < S; ++i) v[i] = to[i * WARPS + (threadIdx.x & 31)];
 #pragma unroll
             for (int d = 16; d; d >>= 1) {
 #pragma unroll
-                for (int i = 0; i < M; ++i) v[i] += __shfl_xor_sync(FULL_MASK, v[i], d);
+                for (int i = 0; i < S; ++i) v[i] += __shfl_xor_sync(FULL_MASK, v[i], d);
             }
         }
     }
     static constexpr int M_MOST = 3;
-    static constexpr int RED = 2 * M_MOST * WARPS;   // floats a group
-    __device__ __forceinline__ void clear_sums() const
-    {
-        if (W > 32)
-            for (int i = tid; i < RED; i += W) red[i] = 0.0f;   // before the group's first barrier
-    }
 
     // Column of pair i; the second of the pair is `beside` further on.
     __device__ __forceinline__ int col(int i) const
@@ -235,8 +267,8 @@ template <typename D, bool VEC, int C> struct NormGroup {
         return pair(col(i) < H ? r.x : 0.0f, col(i) + W < H ? r.y : 0.0f);
     }
 
-    // Starts the copy of row t of `rows` into `slot`.
-    __device__ __forceinline__ void fetch(const NormRows &rows, uint32_t t, uint8_t *slot) const
+    // Starts the copy of row t of `rows` into `slot`, by cp.async.
+    __device__ __forceinline__ void fetch_one(const NormRows &rows, uint32_t t, uint8_t *slot) const
     {
         if (!STAGED) return;
         const char *row = static_cast<const char *>(rows.at) + static_cast<uint64_t>(t) * (H * static_cast<uint32_t>(sizeof(D)));
@@ -262,6 +294,68 @@ template <typename D, bool VEC, int C> struct NormGroup {
             }
         }
     }
+    // Starts the copy of row t, if there is one, into slot `i` at `slot`.
+    __device__ __forceinline__ void fetch(const NormInputs &in, uint32_t t, uint32_t T, uint8_t *slot, int pitch, int i) const
+    {
+        if (!STAGED) return;
+        if (M != ROWS_VEC && W <= 32) __syncwarp();   // the warp has read the slot, where no barrier says so
+        if (M == ROWS_BULK) {
+            if (tid != 0 || t >= T) return;
+            const uint32_t bytes = static_cast<uint32_t>(H) * sizeof(D);
+            mbar_expect(bars + 8 * i, bytes * in.tensors);
+#pragma unroll
+            for (int k = 0; k < 5; ++k)
+                if (in.slot[k] >= 0)
+                    bulk_load(smem_u32(slot) + in.slot[k] * pitch,
+                              static_cast<const char *>(in.rows[k].at) + static_cast<uint64_t>(t) * bytes, bytes, bars + 8 * i);
+        } else {
+            if (t < T) {
+#pragma unroll
+                for (int k = 0; k < 5; ++k)
+                    if (in.slot[k] >= 0) fetch_one(in.rows[k], t, slot + in.slot[k] * pitch);
+            }
+            cp_commit();
+        }
+    }
+    // Waits for the row in slot i of `slots`; `there`: whether there is one.
+    __device__ __forceinline__ void arrived(int i, int slots, bool there) const
+    {
+        if (!STAGED) return;
+        if (M == ROWS_BULK) {
+            if (there) (void)mbar_wait(bars + 8 * i, slot_phase, gave_up);
+        } else {
+            cp_wait(slots - 1);
+            if (M == ROWS_ANY) barrier();
+        }
+    }
+    // The slot after slot i.
+    __device__ __forceinline__ int after(int i, int slots)
+    {
+        if (i + 1 < slots) return i + 1;
+        slot_phase ^= 1u;
+        return 0;
+    }
+    // At the end: no copy is left in flight.  `i`: the slot that would be next.
+    __device__ __forceinline__ void finish(int i, int slots, int32_t *status) const
+    {
+        if (!STAGED) return;
+        if (M != ROWS_BULK) {
+            cp_wait(0);
+        } else if (*gave_up && tid == 0) {
+            for (int k = 0; k < slots; ++k) mbar_drain(bars + 8 * k, k < i ? slot_phase ^ 1u : slot_phase);
+            or_status(status, MP_STATUS_STALLED);
+        }
+    }
+    // What the rows share, copied to `to` by the whole CTA: there after finish_held() and a barrier.
+    __device__ __forceinline__ void hold(const D *from, uint8_t *to) const
+    {
+        if (VEC) {
+            for (int c = threadIdx.x; c < H / NV; c += blockDim.x) cp_async16(smem_u32(to) + c * 16, from + c * NV);
+        } else {
+            for (int c = threadIdx.x; c < H; c += blockDim.x) reinterpret_cast<D *>(to)[c] = from[c];
+        }
+    }
+
     // Where row t of `rows` can be read: in `slot`, or where it is.
     __device__ __forceinline__ const D *row(const NormRows &rows, uint32_t t, const uint8_t *slot) const
     {
@@ -282,7 +376,7 @@ __host__ __device__ inline int norm_wide(int H) { return (H + 3) / 4 * 4; }
 
 // Threads a row, rows at a time, and slots for `tensors` staged rows; `held` vectors that the
 // rows share lie beside them, and `sums` fp32 sums a column of each group.  Two CTAs on an SM wherever two slots or more fit in half of it.
-template <typename D> NormPlan norm_plan(int64_t T, int H, int C, int threads, int tensors, int held, int sums, bool two)
+template <typename D> NormPlan norm_plan(int64_t T, int H, int C, int threads, bool bulk, int tensors, int held, int sums, bool two)
 {
     NormPlan p;
     const int need = (H + 8 * C - 1) / (8 * C);
@@ -293,22 +387,24 @@ template <typename D> NormPlan norm_plan(int64_t T, int H, int C, int threads, i
         p.W = (need + 31) / 32 * 32;
     p.R = C < 4 ? threads / p.W : 1;
     while (p.R > 1 && p.W * (p.R / 2) >= 32 && (T + p.R / 2 - 1) / (p.R / 2) <= sm_count()) p.R /= 2;   // few rows: spread
-    const int red = 2 * 3 * 32 * 4;
     p.pitch = (H * static_cast<int>(sizeof(D)) + 15) / 16 * 16 + 16;
     const int64_t extra = C < 4 ? static_cast<int64_t>(held) * p.pitch + static_cast<int64_t>(sums) * p.R * norm_wide(H) * 4 : 0;
-    const size_t fixed = static_cast<size_t>(p.W > 32 ? p.R : 1) * red + static_cast<size_t>(extra);
+    const size_t fixed = NormGroup<D, ROWS_ANY, 2>::head(p.W, p.R) + static_cast<size_t>(extra);
     const size_t slot = static_cast<size_t>(p.pitch) * tensors * p.R;
     p.stages = 0;
     if (C < 4) {
         const size_t room = two && fixed + 2 * slot <= NORM_BUDGET ? NORM_BUDGET : NORM_MOST;
         p.stages = fixed < room ? static_cast<int>((room - fixed) / slot) : 0;
-        if (p.stages > 4) p.stages = 4;
+        if (p.stages > (bulk ? 3 : NORM_SLOTS)) p.stages = bulk ? 3 : NORM_SLOTS;   // of bulk copies more are slower (88.6, 88.7, 90.7 us with 2, 3, 4)
     }
     const int64_t steps = (T + p.R - 1) / p.R;
     if (p.stages > steps) p.stages = static_cast<int>(steps);
     p.smem = fixed + slot * p.stages;
     return p;
 }
+
+// How the rows of a call are staged.
+template <typename D> bool norm_by_bulk(int H) { return H * static_cast<int>(sizeof(D)) >= 2048; }
 
 // The launchers of the types' kernels (norm_fwd.cu, norm_bwd_*.cu).
 struct NormCall {
@@ -318,6 +414,7 @@ struct NormCall {
     int H, kind, gate_form;
     float eps, scale;
     bool vec;                  // every tensor is whole 16-byte vectors
+    int32_t *status;
     void *s_out, *y;
     float *stats;
     void *g_x, *g_residual, *g_gate;

@@ -16,9 +16,7 @@ namespace {
 enum { SUM_POST_W, SUM_POST_B, SUM_PRE_W, SUM_PRE_B, SUM_GATE };
 
 struct NormBwdArgs {
-    NormRows rows[5];    // staged, of these that are there: g_s, g_y, s, x, gate
-    int slot[5];         // a row's place in a slot, -1: absent
-    int tensors;
+    NormInputs in;
     const void *post_w, *post_b, *gate, *pre_w;
     const float *stats;
     int64_t T;
@@ -26,41 +24,37 @@ struct NormBwdArgs {
     float scale;
     void *g_x, *g_residual, *g_gate;
     float *sums[NORM_SHARED];
+    int32_t *status;
 };
 enum { ROW_G_S, ROW_G_Y, ROW_S, ROW_X, ROW_GATE };
 
-template <typename D, bool VEC, int C, bool POST, bool PRE>
+template <typename D, int M, int C, bool POST, bool PRE>
 __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, 1)
     k_block_norm_bwd(const NormBwdArgs a, const NormPlan p)
 {
-    typedef NormGroup<D, VEC, C> G;
+    typedef NormGroup<D, M, C> G;
     constexpr int N2 = G::N2;
     extern __shared__ __align__(16) uint8_t smem[];
     pdl_trigger();
     pdl_wait();
     G g;
     const int H = a.H;
-    g.W = p.W; g.H = H;
-    g.group = threadIdx.x / p.W;
-    g.tid = threadIdx.x - g.group * p.W;
-    g.red = reinterpret_cast<float *>(smem) + (p.W > 32 ? g.group * G::RED : 0);
-    g.clear_sums();
-    uint8_t *const rings = smem + (p.W > 32 ? p.R : 1) * G::RED * 4;
-    const int slot_bytes = a.tensors * p.pitch;
+    g.begin(smem, p.W, p.R, H);
+    uint8_t *const rings = smem + G::head(p.W, p.R);
+    const int slot_bytes = a.in.tensors * p.pitch;
     uint8_t *const ring = rings + static_cast<size_t>(g.group) * p.stages * slot_bytes;
     // What the rows share, behind the slots.
     uint8_t *held = rings + static_cast<size_t>(p.R) * p.stages * slot_bytes;
     const auto hold = [&](const void *v) {
-        const D *from = static_cast<const D *>(v);
         if constexpr (G::STAGED) {
-            D *const to = reinterpret_cast<D *>(held);
+            const D *const to = reinterpret_cast<const D *>(held);
             if (v != nullptr) {
+                g.hold(static_cast<const D *>(v), held);
                 held += p.pitch;
-                for (int c = threadIdx.x; c < H; c += blockDim.x) to[c] = from[c];
             }
-            return static_cast<const D *>(to);
+            return to;
         } else {
-            return from;
+            return static_cast<const D *>(v);
         }
     };
     const D *const post_w = hold(POST ? a.post_w : nullptr), *const pre_w = hold(PRE ? a.pre_w : nullptr);
@@ -90,16 +84,9 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, 1)
     }
 
     const uint32_t T = static_cast<uint32_t>(a.T), step = gridDim.x * p.R, first = blockIdx.x * p.R;
-    const auto fetch = [&](uint32_t t, uint8_t *slot) {
-        if (t < T) {
-#pragma unroll
-            for (int i = 0; i < 5; ++i)
-                if (a.slot[i] >= 0) g.fetch(a.rows[i], t, slot + a.slot[i] * p.pitch);
-        }
-        cp_commit();
-    };
+    cp_commit();
     if (G::STAGED)
-        for (int i = 0; i < p.stages; ++i) fetch(first + i * step + g.group, ring + i * slot_bytes);
+        for (int i = 0; i < p.stages; ++i) g.fetch(a.in, first + i * step + g.group, T, ring + i * slot_bytes, p.pitch, i);
 
     const bool layer = a.kind == MP_NORM_LAYER, token = a.gate_form == MP_GATE_TOKEN;
     const float inv = 1.0f / static_cast<float>(H);
@@ -116,6 +103,11 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, 1)
     };
     float4 next = stats_of(first + g.group);
     float next_gate = gate_of(first + g.group);
+    // The oldest copies are those of what the rows share.
+    if (M == ROWS_BULK)
+        cp_wait(0);
+    else
+        cp_wait(p.stages);
     __syncthreads();
     int at = 0;
     for (uint32_t t0 = first; t0 < T; t0 += step) {   // the same count for every group
@@ -127,14 +119,18 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, 1)
         const float gate = next_gate;
         next = stats_of(t + step);
         next_gate = gate_of(t + step);
-        if (G::STAGED) {
-            cp_wait(p.stages - 1);
-            if (!VEC) g.barrier();
-        }
+        g.arrived(at, p.stages, there);
+        // Once everyone has read the row, which is so after the last sum that follows the last load,
+        // its slot takes the one `stages` steps on.
+        bool refilled = false;
+        const auto refill = [&]() {
+            if (G::STAGED) g.fetch(a.in, t + p.stages * step, T, slot, p.pitch, at);
+            refilled = true;
+        };
         const auto load = [&](int which, f2 (&f)[N2]) {
 #pragma unroll
             for (int i = 0; i < N2; ++i) f[i] = 0ull;
-            if (there && a.slot[which] >= 0) g.load(g.row(a.rows[which], t, slot + a.slot[which] * p.pitch), f);
+            if (there && a.in.slot[which] >= 0) g.load(g.row(a.in.rows[which], t, slot + a.in.slot[which] * p.pitch), f);
         };
         // (v - mean) rstd
         const auto standard = [&](f2 (&v)[N2], float mean, float rstd) {
@@ -162,6 +158,7 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, 1)
                 d[i] = mul2(d[i], w[i]);
                 along2 = fma2(d[i], hat[i], along2);
             }
+            load(ROW_G_S, total);
             float t2[2] = {sum2(along2), 0.0f};
             if (layer) {
 #pragma unroll
@@ -176,7 +173,7 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, 1)
             // total = g_s + rstd (d - flat - hat along)
             const float along = -t2[0] * inv, flat = -t2[1] * inv;
             const f2 m = pair(along, along), f = pair(flat, flat), r = pair(st.w, st.w);
-            load(ROW_G_S, total);
+            if (!POST && a.gate_form == MP_GATE_NONE) refill();
             if (layer) {
 #pragma unroll
                 for (int i = 0; i < N2; ++i) d[i] = add2(d[i], f);
@@ -252,6 +249,7 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, 1)
                 g.sums(t1);
                 t3[0] = t1[0];
             }
+            if (POST || layer || token) refill();
             if (token && a.g_gate != nullptr && g.tid == 0 && there) norm_put(static_cast<D *>(a.g_gate) + t, t3[2]);
             if (POST) {
                 const float along = -t3[0] * inv, flat = layer ? -t3[1] * inv : 0.0f;
@@ -265,13 +263,13 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, 1)
             }
         }
         if (a.g_x != nullptr && there) g.store(static_cast<D *>(a.g_x) + row, total);
-        if (G::STAGED) {
-            if (!VEC) g.barrier();   // everyone has read the slot
-            fetch(t + p.stages * step, slot);
-            at = at + 1 == p.stages ? 0 : at + 1;
+        if (!refilled) {
+            if (G::STAGED) g.barrier();
+            refill();
         }
+        at = g.after(at, p.stages);
     }
-    if (G::STAGED) cp_wait(0);
+    g.finish(at, p.stages, a.status);
 
     // The groups' sums, in their order, into this CTA's partial sums.  The slots are free now.
     float *const stack = reinterpret_cast<float *>(rings);
@@ -312,40 +310,41 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, 1)
     pile_up(a.sums[SUM_GATE], nullptr, from);
 }
 
-template <typename D, bool VEC, int C, bool POST, bool PRE> mp_status_t run(const NormCall &c, int &parts)
+template <typename D, int M, int C, bool POST, bool PRE> mp_status_t run(const NormCall &c, int &parts)
 {
     static std::atomic<uint64_t> allowed{0};
     NormBwdArgs a = {};
-    const bool with_x = POST || c.gate_form != MP_GATE_NONE;
-    const NormRows rows[5] = {c.g_s, c.g_y, c.s, c.x, c.gate_rows};
-    const bool there[5] = {c.g_s.at != nullptr, PRE, PRE, with_x, c.gate_rows.at != nullptr};
-    for (int i = 0; i < 5; ++i) {
-        a.rows[i] = rows[i];
-        a.slot[i] = there[i] ? a.tensors++ : -1;
-    }
+    a.in.add(ROW_G_S, c.g_s);
+    a.in.add(ROW_G_Y, c.g_y);
+    a.in.add(ROW_S, c.s);
+    a.in.add(ROW_X, POST || c.gate_form != MP_GATE_NONE ? c.x : NormRows{});
+    a.in.add(ROW_GATE, c.gate_rows);
     a.post_w = c.post_w; a.post_b = c.post_b; a.gate = c.gate; a.pre_w = c.pre_w;
     a.stats = c.stats; a.T = c.T; a.H = c.H; a.kind = c.kind; a.gate_form = c.gate_form; a.scale = c.scale;
-    a.g_x = c.g_x; a.g_residual = c.g_residual; a.g_gate = c.g_gate;
+    a.g_x = c.g_x; a.g_residual = c.g_residual; a.g_gate = c.g_gate; a.status = c.status;
     for (int i = 0; i < NORM_SHARED; ++i) a.sums[i] = c.sums[i];
     const int more = (c.sums[SUM_POST_B] != nullptr) + (c.sums[SUM_PRE_B] != nullptr) + (c.sums[SUM_GATE] != nullptr);
     const int held = POST + PRE + (c.post_b != nullptr) + (c.gate_form == MP_GATE_CHANNEL);
-    const NormPlan p = norm_plan<D>(c.T, c.H, C, C < 4 ? NORM_THREADS : 2 * NORM_THREADS, a.tensors, held, more, false);
-    if (C < 4 && p.stages < 1) return run<D, VEC, 4, POST, PRE>(c, parts);   // fp32 rows and several sums beside them
-    return norm_launch(k_block_norm_bwd<D, VEC, C, POST, PRE>, allowed, p, false, c.T, c.stream, parts, a);
+    const NormPlan p = norm_plan<D>(c.T, c.H, C, C < 4 ? NORM_THREADS : 2 * NORM_THREADS, M == ROWS_BULK, a.in.tensors,
+                                    held, more, false);
+    if constexpr (C < 4)   // fp32 rows and several sums beside them
+        if (p.stages < 1) return run<D, M == ROWS_ANY ? ROWS_ANY : ROWS_VEC, 4, POST, PRE>(c, parts);
+    return norm_launch(k_block_norm_bwd<D, M, C, POST, PRE>, allowed, p, false, c.T, c.stream, parts, a);
 }
 
-template <typename D, bool VEC, int C> mp_status_t by_norms(const NormCall &c, int &parts)
+template <typename D, int M, int C> mp_status_t by_norms(const NormCall &c, int &parts)
 {
-    if (c.post_w == nullptr) return run<D, VEC, C, false, true>(c, parts);
-    return c.pre_w == nullptr ? run<D, VEC, C, true, false>(c, parts) : run<D, VEC, C, true, true>(c, parts);
+    if (c.post_w == nullptr) return run<D, M, C, false, true>(c, parts);
+    return c.pre_w == nullptr ? run<D, M, C, true, false>(c, parts) : run<D, M, C, true, true>(c, parts);
 }
 
 }  // namespace
 
 template <typename D> mp_status_t norm_backward(const NormCall &c, int &parts)
 {
-    if (c.H <= 16 * NORM_THREADS) return c.vec ? by_norms<D, true, 2>(c, parts) : by_norms<D, false, 2>(c, parts);
-    return c.vec ? by_norms<D, true, 4>(c, parts) : by_norms<D, false, 4>(c, parts);
+    if (c.H > 16 * NORM_THREADS) return c.vec ? by_norms<D, ROWS_VEC, 4>(c, parts) : by_norms<D, ROWS_ANY, 4>(c, parts);
+    if (!c.vec) return by_norms<D, ROWS_ANY, 2>(c, parts);
+    return norm_by_bulk<D>(c.H) ? by_norms<D, ROWS_BULK, 2>(c, parts) : by_norms<D, ROWS_VEC, 2>(c, parts);
 }
 
 }  // namespace mp

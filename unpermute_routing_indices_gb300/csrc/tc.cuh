@@ -170,6 +170,14 @@ __device__ __forceinline__ void tma_store(const CUtensorMap *m, uint32_t src, in
 __device__ __forceinline__ void tma_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void tma_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
+// Untiled: `bytes`, a multiple of 16, between addresses on 16 bytes.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
 // --- tcgen05 ---------------------------------------------------------------
 
 // CG 2: one warp of each CTA of a pair.
