@@ -12,26 +12,44 @@ struct NormSums {
 
 constexpr int SUM_COLS = 32, SUM_ROWS = 16;
 
-// out[c] = the CTAs' partial sums of column c, in 64 bits and a fixed order: 16 threads a column, each
-// every 16th of them, so that up to 304 loads are 19 in flight a thread; then the 16.
+// A sum and what its roundings lost (Knuth's two-sum).
+__device__ __forceinline__ void add_to(float2 &v, float p)
+{
+    const float t = __fadd_rn(v.x, p), z = __fsub_rn(t, v.x);
+    v.y = __fadd_rn(v.y, __fadd_rn(__fsub_rn(v.x, __fsub_rn(t, z)), __fsub_rn(p, z)));
+    v.x = t;
+}
+
+// out[c] = the CTAs' partial sums of column c, in pairs of fp32 and a fixed order: 16 threads a column,
+// each every 16th of up to 304 of them, then the 16.  (In 64 bits, whose units are few, the
+// gradient at one norm, 16,384 x 4,096, took 96 us in all.)
 template <typename D> __global__ void __launch_bounds__(SUM_COLS *SUM_ROWS) k_norm_sums(const NormSums a, int parts, int H)
 {
-    __shared__ double part[SUM_ROWS][SUM_COLS];
+    __shared__ float2 part[SUM_ROWS][SUM_COLS];
     pdl_trigger();
     pdl_wait();
     const float *from = a.sums[blockIdx.y];
     const int col = threadIdx.x % SUM_COLS, row = threadIdx.x / SUM_COLS, c = blockIdx.x * SUM_COLS + col;
-    double v = 0.0;
+    float2 v = make_float2(0.0f, 0.0f);
     if (c < H) {
-#pragma unroll 10
-        for (int i = row; i < parts; i += SUM_ROWS) v += from[static_cast<int64_t>(i) * H + c];
+        constexpr int MOST = NORM_PARTS / SUM_ROWS;
+        float p[MOST];
+#pragma unroll
+        for (int i = 0; i < MOST; ++i)
+            p[i] = row + i * SUM_ROWS < parts ? from[static_cast<int64_t>(row + i * SUM_ROWS) * H + c] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < MOST; ++i) add_to(v, p[i]);
     }
     part[row][col] = v;
     __syncthreads();
     if (row != 0 || c >= H) return;
 #pragma unroll
-    for (int i = 1; i < SUM_ROWS; ++i) v += part[i][col];
-    norm_put(static_cast<D *>(a.out[blockIdx.y]) + c, static_cast<float>(v));
+    for (int i = 1; i < SUM_ROWS; ++i) {
+        const float2 o = part[i][col];
+        add_to(v, o.x);
+        v.y = __fadd_rn(v.y, o.y);
+    }
+    norm_put(static_cast<D *>(a.out[blockIdx.y]) + c, isfinite(v.x) ? __fadd_rn(v.x, v.y) : v.x);
 }
 
 mp_status_t norm_sizes(int64_t T, int32_t H, int32_t dtype, int32_t kind, int32_t gate_form, const void *gate)
