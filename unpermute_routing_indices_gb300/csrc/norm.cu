@@ -21,7 +21,7 @@ __device__ __forceinline__ void add_to(float2 &v, float p)
 }
 
 // out[c] = the CTAs' partial sums of column c, in pairs of fp32 and a fixed order: 16 threads a column,
-// each every 16th of up to 304 of them, then the 16.  (In 64 bits, whose units are few, the
+// each every 16th of up to 152 of them, then the 16.  (In 64 bits, whose units are few, the
 // gradient at one norm, 16,384 x 4,096, took 96 us in all.)
 template <typename D> __global__ void __launch_bounds__(SUM_COLS *SUM_ROWS) k_norm_sums(const NormSums a, int parts, int H)
 {
@@ -32,7 +32,7 @@ template <typename D> __global__ void __launch_bounds__(SUM_COLS *SUM_ROWS) k_no
     const int col = threadIdx.x % SUM_COLS, row = threadIdx.x / SUM_COLS, c = blockIdx.x * SUM_COLS + col;
     float2 v = make_float2(0.0f, 0.0f);
     if (c < H) {
-        constexpr int MOST = NORM_PARTS / SUM_ROWS;
+        constexpr int MOST = (NORM_PARTS + SUM_ROWS - 1) / SUM_ROWS;
         float p[MOST];
 #pragma unroll
         for (int i = 0; i < MOST; ++i)

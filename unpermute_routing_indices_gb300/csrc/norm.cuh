@@ -26,7 +26,7 @@
 namespace mp {
 
 constexpr int NORM_SHARED = 5;      // gradients shared by rows: two weights, two biases, the gate
-constexpr int NORM_PARTS = 304;     // partial sums of each: two CTAs on an SM
+constexpr int NORM_PARTS = 152;     // partial sums of each at most: a CTA an SM
 constexpr int NORM_THREADS = 512;   // of a CTA, C 4: twice as many
 constexpr int NORM_BUDGET = 112 * 1024;   // shared memory of one of two CTAs on an SM
 constexpr int NORM_MOST = 225 * 1024;     // of one alone
@@ -432,7 +432,7 @@ mp_status_t norm_launch(K kernel, std::atomic<uint64_t> &allowed, NormPlan p, bo
     if (!allow_smem(kernel, allowed, NORM_MOST)) return MP_ERR_CUDA;
     const int64_t steps = (T + p.R - 1) / p.R, most = sm_count() * (two && p.smem <= NORM_BUDGET ? 2 : 1);
     grid = static_cast<int>(steps < most ? steps : most);
-    if (grid > NORM_PARTS) grid = NORM_PARTS;
+    if (!two && grid > NORM_PARTS) grid = NORM_PARTS;   // gradients
     (void)launch_pdl(kernel, grid, p.W * p.R, p.smem, stream, args..., p);
     return check_launch();
 }

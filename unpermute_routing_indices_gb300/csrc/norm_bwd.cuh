@@ -190,22 +190,24 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, 1)
             for (int i = 0; i < N2; ++i) total[i] = mul2(total[i], by);
         }
         if (POST || a.gate_form != MP_GATE_NONE) {
-            f2 hat[N2], w[N2];
+            f2 hat[N2];
             load(ROW_X, hat);
-            if (POST) {
-                g.load(post_w, w);
-                standard(hat, st.x, st.y);
-            }
+            if (POST) standard(hat, st.x, st.y);
             float t3[3] = {0.0f, 0.0f, 0.0f};
             if (a.gate_form != MP_GATE_NONE) {
                 f2 u[N2], k[N2];
-                if (POST && a.post_b != nullptr) {
-                    g.load(post_b, k);
+                if (POST) {
+                    g.load(post_w, k);
 #pragma unroll
-                    for (int i = 0; i < N2; ++i) u[i] = fma2(hat[i], w[i], k[i]);
+                    for (int i = 0; i < N2; ++i) u[i] = mul2(hat[i], k[i]);
+                    if (a.post_b != nullptr) {
+                        g.load(post_b, k);
+#pragma unroll
+                        for (int i = 0; i < N2; ++i) u[i] = add2(u[i], k[i]);
+                    }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < N2; ++i) u[i] = POST ? mul2(hat[i], w[i]) : hat[i];
+                    for (int i = 0; i < N2; ++i) u[i] = hat[i];
                 }
                 f2 gate2 = 0ull;
 #pragma unroll
@@ -231,7 +233,9 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, 1)
             }
             if (POST) {
                 if (a.sums[SUM_POST_B] != nullptr && there) g.template columns<true>(more[0], total);
-                f2 along2 = 0ull, flat2 = 0ull;
+                asm volatile("" ::: "memory");   // the weights are read again: registers are short
+                f2 along2 = 0ull, flat2 = 0ull, w[N2];
+                g.load(post_w, w);
 #pragma unroll
                 for (int i = 0; i < N2; ++i) {
                     post_sum[i] = fma2(total[i], hat[i], post_sum[i]);
