@@ -547,17 +547,15 @@ def mp_moe_layer(x, router, w1, w2, topk: int, *, b1=None, b2=None, act: str = "
     if P != F * _parts(act):
         raise ValueError(f"w1 has {P} columns for the {F} of w2 and act {act}")
     dt = _token_dtype(router, "router")
-    _need(router, "router", router.dtype, 2, dev)
-    _shape(router, "router", (E, H))
+    _fits(router, "router", (E, H), router.dtype, dev)
     K = int(topk)
     for t, name, shape, dtype in ((b1, "b1", (E, P), torch.bfloat16),
                                   (b2, "b2", (E, O), torch.bfloat16),
                                   (bias, "bias", (E,), torch.float32)):
         if t is not None:
-            _need(t, name, dtype, len(shape), dev)
-            _shape(t, name, shape)
-    n = lib.mp_moe_layer_workspace_size(T, E, K, H, F, O)
+            _fits(t, name, shape, dtype, dev)
     if workspace is None:
+        n = lib.mp_moe_layer_workspace_size(T, E, K, H, F, O)
         workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
     else:
         _need(workspace, "workspace", torch.uint8, 1, dev)
@@ -567,8 +565,7 @@ def mp_moe_layer(x, router, w1, w2, topk: int, *, b1=None, b2=None, act: str = "
         if t is None:
             t = torch.empty(shape, dtype=dtype, device=dev)
         else:
-            _need(t, name, dtype, 2, dev)
-            _shape(t, name, shape)
+            _fits(t, name, shape, dtype, dev)
         outs.append(t)
     y, idx, weights = outs
     _opt(status, "status", torch.int32, 1, dev)
@@ -585,18 +582,12 @@ def mp_moe_layer(x, router, w1, w2, topk: int, *, b1=None, b2=None, act: str = "
 # the norms before and after a block
 # --------------------------------------------------------------------------
 
-def _rows_of(t, name, like):
-    if t is not None:
-        _need(t, name, like.dtype, 2, like.device)
-        if t.shape != like.shape:
-            _shape(t, name, like.shape)
-
-
-def _channels_of(t, name, like):
-    if t is not None:
-        _need(t, name, like.dtype, 1, like.device)
-        if t.shape[0] != like.shape[1]:
-            _shape(t, name, like.shape[1:])
+def _fits(t, name, shape, dtype, dev):
+    """Checks a tensor (or None) against all that is asked of it."""
+    if t is None or (t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous()):
+        return
+    _need(t, name, dtype, len(shape), dev)
+    _shape(t, name, shape)
 
 
 def _gate_form(gate, like):
@@ -631,23 +622,26 @@ def mp_block_norm(x, residual=None, *, post_weight=None, post_bias=None, gate=No
     _need(x, "x", x.dtype, 2)
     dev = x.device
     T, H = x.shape
-    _rows_of(residual, "residual", x)
-    form = _gate_form(gate, x)
+    shape, dtype = x.shape, x.dtype
+    _fits(residual, "residual", shape, dtype, dev)
+    form = 0 if gate is None else _gate_form(gate, x)
     for t, name in ((post_weight, "post_weight"), (post_bias, "post_bias"),
                     (pre_weight, "pre_weight"), (pre_bias, "pre_bias")):
-        _channels_of(t, name, x)
+        if t is not None:
+            _fits(t, name, shape[1:], dtype, dev)
     as_is = s is None and residual is None and post_weight is None and gate is None and scale == 1.0
-    if not as_is and s is None:
+    if s is not None:
+        _fits(s, "s", shape, dtype, dev)
+    elif not as_is:
         s = torch.empty_like(x)
-    if y is None and pre_weight is not None:
+    if y is not None:
+        _fits(y, "y", shape, dtype, dev)
+    elif pre_weight is not None:
         y = torch.empty_like(x)
-    _rows_of(s, "s", x)
-    _rows_of(y, "y", x)
-    if stats is None and with_stats:
-        stats = torch.empty((T, 4), dtype=torch.float32, device=dev)
     if stats is not None:
-        _need(stats, "stats", torch.float32, 2, dev)
-        _shape(stats, "stats", (T, 4))
+        _fits(stats, "stats", (T, 4), torch.float32, dev)
+    elif with_stats:
+        stats = torch.empty((T, 4), dtype=torch.float32, device=dev)
     _opt(status, "status", torch.int32, 1, dev)
     with _on(dev):
         _check("mp_block_norm", _lib.load().mp_block_norm(
@@ -678,14 +672,18 @@ def mp_block_norm_bwd(g_s, g_y, x, s, stats, *, post_weight=None, post_bias=None
     _need(like, "x", like.dtype, 2)
     dev = like.device
     T, H = like.shape
+    shape, dtype = like.shape, like.dtype
     for t, name in ((x, "x"), (s, "s"), (g_s, "g_s"), (g_y, "g_y")):
-        _rows_of(t, name, like)
-    form = _gate_form(gate, like)
+        if t is not None and t is not like:
+            _fits(t, name, shape, dtype, dev)
+    form = 0 if gate is None else _gate_form(gate, like)
     for t, name in ((post_weight, "post_weight"), (post_bias, "post_bias"),
                     (pre_weight, "pre_weight"), (pre_bias, "pre_bias")):
-        _channels_of(t, name, like)
-    _need(stats, "stats", torch.float32, 2, dev)
-    _shape(stats, "stats", (T, 4))
+        if t is not None:
+            _fits(t, name, shape[1:], dtype, dev)
+    if stats is None:
+        raise TypeError("stats must be a torch.Tensor")
+    _fits(stats, "stats", (T, 4), torch.float32, dev)
     grad_dtype = like.dtype if grad_dtype is None else grad_dtype
     if grad_dtype not in (like.dtype, torch.float32):
         raise TypeError(f"grad_dtype must be {like.dtype} or torch.float32, got {grad_dtype}")
@@ -695,7 +693,8 @@ def mp_block_norm_bwd(g_s, g_y, x, s, stats, *, post_weight=None, post_bias=None
     g_gate = None
     if gate is not None and need[2]:
         g_gate = torch.empty_like(gate, dtype=grad_dtype if form == 1 else like.dtype)
-    shared = [torch.empty(H, dtype=grad_dtype, device=dev) if t is not None and n else None
+    shared = [None if t is None or not n else
+              torch.empty_like(t) if grad_dtype is dtype else torch.empty(H, dtype=grad_dtype, device=dev)
               for t, n in zip((post_weight, post_bias, pre_weight, pre_bias), need[3:])]
     if workspace is None:
         if form == 1 and g_gate is not None or any(t is not None for t in shared):
