@@ -108,7 +108,7 @@ __device__ __forceinline__ int last_le(const int64_t *a, int lo, int hi, int64_t
 // lane, addresses by immediate offsets from the row base); narrower rows are
 // spread over the CTA as one flat range.
 template <typename V, bool SCATTER, int RP = 1, int THREADS = CH_THREADS>
-__device__ __forceinline__ void copy_rows(const V *__restrict__ in, V *__restrict__ out,
+__device__ __forceinline__ void copy_rows(const V *in, V *__restrict__ out,
                                           const int32_t *s_map, int64_t row0, int nrows, int nvec)
 {
     // the same bytes in flight per lane for 16- and 32-byte vectors
@@ -361,9 +361,9 @@ __device__ void sort_pad_meta_cta(const SortPadMeta &m, const int32_t *split,
 
 template <typename V, bool FAST_META, int RP, int THREADS, int ROWS>
 __global__ void __launch_bounds__(THREADS, MP_CH_MIN_BLOCKS)
-    k_sort_pad(const V *__restrict__ x, const float *__restrict__ probs,
-               const int32_t *__restrict__ split, const int32_t *__restrict__ order,
-               const int32_t *__restrict__ padded_sizes, int C, int G,
+    k_sort_pad(const V *x, const float *probs,
+               const int32_t *split, const int32_t *order,
+               const int32_t *padded_sizes, int C, int G,
                int align, int64_t N, int64_t out_rows, int nvec, V *__restrict__ out,
                float *__restrict__ out_probs, int32_t *__restrict__ row_map,
                int64_t *__restrict__ group_off, int32_t *status)
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(THREADS, MP_CH_MIN_BLOCKS)
         }
         s_src[tid] = src;
         row_map[d] = src;
-        if (out_probs != nullptr && src >= 0) pv = __ldg(probs + src);
+        if (out_probs != nullptr && src >= 0) pv = ld_in(probs + src);
     }
     __syncthreads();
     if (nrows > 0) copy_rows<V, false, RP, THREADS>(x, out, s_src, row0, nrows, nvec);
@@ -425,8 +425,8 @@ __global__ void __launch_bounds__(THREADS, MP_CH_MIN_BLOCKS)
 
 template <typename V, bool SCATTER>
 __global__ void __launch_bounds__(CH_THREADS, MP_CH_MIN_BLOCKS)
-    k_rows_remap(const V *__restrict__ in, const float *__restrict__ in_probs,
-                 const int32_t *__restrict__ map, int64_t out_rows, int64_t N, int nvec,
+    k_rows_remap(const V *in, const float *in_probs,
+                 const int32_t *map, int64_t out_rows, int64_t N, int nvec,
                  V *__restrict__ out, float *__restrict__ out_probs, int32_t *status)
 {
     pdl_trigger();
@@ -442,14 +442,14 @@ __global__ void __launch_bounds__(CH_THREADS, MP_CH_MIN_BLOCKS)
     int32_t m = -1;
     if (tid < nrows) {
         const int64_t d = row0 + tid;
-        if (SCATTER && in_probs != nullptr) pv = __ldg(in_probs + d);
-        m = __ldg(map + d);
+        if (SCATTER && in_probs != nullptr) pv = ld_in(in_probs + d);
+        m = ld_in(map + d);
         if (m < -1 || m >= N) {
             or_status(status, MP_STATUS_BAD_ROW);
             m = -1;
         }
         s_map[tid] = m;
-        if (!SCATTER && in_probs != nullptr && m >= 0) pv = __ldg(in_probs + m);
+        if (!SCATTER && in_probs != nullptr && m >= 0) pv = ld_in(in_probs + m);
     }
     __syncthreads();
     copy_rows<V, SCATTER>(in, out, s_map, row0, nrows, nvec);

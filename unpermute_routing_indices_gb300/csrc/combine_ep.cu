@@ -320,16 +320,16 @@ struct EpSlots {
 };
 
 template <bool PROBS, int KM>
-__device__ __forceinline__ void ep_load(EpRaw<KM> &r, const int32_t *__restrict__ map,
-                                        const int32_t *__restrict__ idx,
-                                        const float *__restrict__ probs, int64_t t, int K)
+__device__ __forceinline__ void ep_load(EpRaw<KM> &r, const int32_t *map,
+                                        const int32_t *idx,
+                                        const float *probs, int64_t t, int K)
 {
 #pragma unroll
     for (int i = 0; i < KM; ++i) {
         const bool in = i < K;
-        r.row[i] = in ? __ldg(map + t * K + i) : -1;
-        r.expert[i] = in ? __ldg(idx + t * K + i) : 0;
-        r.p[i] = (PROBS && in) ? __ldg(probs + t * K + i) : 1.0f;
+        r.row[i] = in ? ld_in(map + t * K + i) : -1;
+        r.expert[i] = in ? ld_in(idx + t * K + i) : 0;
+        r.p[i] = (PROBS && in) ? ld_in(probs + t * K + i) : 1.0f;
     }
 }
 
@@ -459,7 +459,7 @@ __device__ __forceinline__ V ep_vec(Get row, const EpSlots<KM> &s)
 // Copies this thread's vector cc of every routed sorted slot into its column
 // of a stage buffer (cp.async, 16 bytes each), as one commit group.
 template <int KM>
-__device__ __forceinline__ void ep_issue(uint4 *buf, const uint4 *__restrict__ rows,
+__device__ __forceinline__ void ep_issue(uint4 *buf, const uint4 *rows,
                                          const EpSlots<KM> &s, int nvec, int cc)
 {
     uint4 *const dst = buf + threadIdx.x;
@@ -475,8 +475,8 @@ __device__ __forceinline__ void ep_issue(uint4 *buf, const uint4 *__restrict__ r
 
 template <typename V, bool PROBS, bool BF16P, bool FP64, int KM>
 __global__ void __launch_bounds__(EP_THREADS, ep_min_blocks(KM))
-    k_unpermute_ep(const V *__restrict__ rows, const float *__restrict__ probs,
-                   const int32_t *__restrict__ map, const int32_t *__restrict__ idx, int64_t T,
+    k_unpermute_ep(const V *rows, const float *probs,
+                   const int32_t *map, const int32_t *idx, int64_t T,
                    int K, int nvec, int tpt_log2, int per_rank, V *__restrict__ out)
 {
     pdl_trigger();
@@ -572,8 +572,8 @@ constexpr size_t ep_token_stage_bytes() { return (size_t)ep_token_bufs<FP64>() *
 
 template <bool PROBS, bool BF16P, bool FP64>
 __global__ void __launch_bounds__(EP_THREADS, FP64 ? 8 : 6)
-    k_unpermute_ep_token(const uint4 *__restrict__ rows, const float *__restrict__ probs,
-                         const int32_t *__restrict__ map, const int32_t *__restrict__ idx,
+    k_unpermute_ep_token(const uint4 *rows, const float *probs,
+                         const int32_t *map, const int32_t *idx,
                          int64_t T, int K, int nvec, int per_rank, uint4 *__restrict__ out)
 {
     constexpr int KM = 8;

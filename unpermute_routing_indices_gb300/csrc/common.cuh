@@ -74,14 +74,48 @@ inline int ceil_log2(int v)
 }
 
 // ---------------------------------------------------------------------------
-// Global memory access.  Rows are streamed: read once through the
-// non-coherent path without L1 allocation; written with plain stores.
+// Global memory access.  Inputs are read by ordinary loads that stay where they stand
+// (asm volatile), never by the read-only path (ld.global.nc, __ldg, const __restrict__): that
+// one is for memory that nobody writes while the kernel runs, and a kernel that is launched
+// early runs while the one before it still writes its inputs.  (A captured training step
+// zeroed all rows of a permuted buffer: the routed row count was read that way, and was what
+// had been in its place before.)  Rows are streamed: read once without L1 allocation; written
+// with plain stores.
 // ---------------------------------------------------------------------------
+
+template <typename T> __device__ __forceinline__ T ld_in(const T *p)
+{
+    static_assert(sizeof(T) == 1 || sizeof(T) == 2 || sizeof(T) == 4 || sizeof(T) == 8 || sizeof(T) == 16, "a load");
+    T v;
+    if constexpr (sizeof(T) == 1) {
+        uint32_t u;
+        asm volatile("ld.global.u8 %0, [%1];" : "=r"(u) : "l"(p));
+        const uint8_t b = static_cast<uint8_t>(u);
+        memcpy(&v, &b, 1);
+    } else if constexpr (sizeof(T) == 2) {
+        uint16_t u;
+        asm volatile("ld.global.u16 %0, [%1];" : "=h"(u) : "l"(p));
+        memcpy(&v, &u, 2);
+    } else if constexpr (sizeof(T) == 4) {
+        uint32_t u;
+        asm volatile("ld.global.u32 %0, [%1];" : "=r"(u) : "l"(p));
+        memcpy(&v, &u, 4);
+    } else if constexpr (sizeof(T) == 8) {
+        uint2 u;
+        asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(u.x), "=r"(u.y) : "l"(p));
+        memcpy(&v, &u, 8);
+    } else {
+        uint4 u;
+        asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
+        memcpy(&v, &u, 16);
+    }
+    return v;
+}
 
 __device__ __forceinline__ uint4 ld_stream(const uint4 *p)
 {
     uint4 v;
-    asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
         : "l"(p));
     return v;
@@ -90,7 +124,7 @@ __device__ __forceinline__ uint4 ld_stream(const uint4 *p)
 __device__ __forceinline__ uint16_t ld_stream(const uint16_t *p)
 {
     unsigned short v;
-    asm("ld.global.nc.L1::no_allocate.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    asm volatile("ld.global.L1::no_allocate.u16 %0, [%1];" : "=h"(v) : "l"(p));
     return v;
 }
 
@@ -109,7 +143,7 @@ struct alignas(32) u32x8 {
 __device__ __forceinline__ u32x8 ld_stream(const u32x8 *p)
 {
     u32x8 v;
-    asm("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
         : "=r"(v.a.x), "=r"(v.a.y), "=r"(v.a.z), "=r"(v.a.w), "=r"(v.b.x), "=r"(v.b.y),
           "=r"(v.b.z), "=r"(v.b.w)
         : "l"(p));

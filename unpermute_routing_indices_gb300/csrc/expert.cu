@@ -16,7 +16,7 @@ constexpr int BIAS_THREADS = 256, BIAS_WARPS = BIAS_THREADS / 32;
 // operands; this serves the others, and biases whose weights want no gradient.
 template <int V>
 __global__ void __launch_bounds__(BIAS_THREADS)
-    k_expert_bias(const mp_bf16_t *__restrict__ g, const int32_t *__restrict__ offsets, int R,
+    k_expert_bias(const mp_bf16_t *g, const int32_t *offsets, int R,
                   int E, int N, mp_bf16_t *out, float *out_f32, bool add)
 {
     pdl_trigger();
@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(BIAS_THREADS)
     int a = 0, b = 0;
 #pragma unroll 8
     for (int i = lane; i <= e + 1; i += 32) {
-        const int v = min(max(__ldg(offsets + i), 0), R);
+        const int v = min(max(ld_in(offsets + i), 0), R);
         b = max(b, v);
         if (i <= e) a = max(a, v);
     }

@@ -109,43 +109,10 @@ __device__ __forceinline__ unsigned low_bits(const void *p)
     return static_cast<unsigned>(reinterpret_cast<uintptr_t>(p)) & 31u;
 }
 
-// Loads of rows that the same kernel may write (a residual that is the result's own
-// buffer): the coherent path, where ld_stream's asks for memory that nobody writes.
-__device__ __forceinline__ uint4 ld_row(const uint4 *p)
-{
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-__device__ __forceinline__ uint16_t ld_row(const uint16_t *p)
-{
-    unsigned short v;
-    asm volatile("ld.global.L1::no_allocate.u16 %0, [%1];" : "=h"(v) : "l"(p));
-    return v;
-}
-__device__ __forceinline__ u32x8 ld_row(const u32x8 *p)
-{
-    u32x8 v;
-    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(v.a.x), "=r"(v.a.y), "=r"(v.a.z), "=r"(v.a.w), "=r"(v.b.x), "=r"(v.b.y),
-                   "=r"(v.b.z), "=r"(v.b.w)
-                 : "l"(p));
-    return v;
-}
-template <bool WRITTEN, typename V> __device__ __forceinline__ V ld_of(const V *p)
-{
-    if constexpr (WRITTEN)
-        return ld_row(p);
-    else
-        return ld_stream(p);
-}
-
-template <bool WRITTEN> __device__ __forceinline__ void load32(const mp_bf16_t *p, float (&f)[EPI_COLS])
+__device__ __forceinline__ void load32(const mp_bf16_t *p, float (&f)[EPI_COLS])
 {
     const u32x8 *q = reinterpret_cast<const u32x8 *>(p);
-    const u32x8 v0 = ld_of<WRITTEN>(q), v1 = ld_of<WRITTEN>(q + 1);
+    const u32x8 v0 = ld_stream(q), v1 = ld_stream(q + 1);
     unpack16(v0, f);
     unpack16(v1, f + 16);
 }
@@ -244,7 +211,7 @@ __device__ __forceinline__ void ckpt_write32(uint8_t *codes, uint8_t *exponent, 
 __device__ __forceinline__ void ckpt_read32(const uint8_t *codes, const uint8_t *exponent, int n,
                                             float (&z)[EPI_COLS])
 {
-    const float unit = pow2_biased(__ldg(exponent));
+    const float unit = pow2_biased(ld_in(exponent));
     const unsigned low = low_bits(codes);
     uint32_t c[8];
     if (n >= EPI_COLS && low == 0) {
@@ -255,7 +222,7 @@ __device__ __forceinline__ void ckpt_read32(const uint8_t *codes, const uint8_t 
         const uint2 *q = reinterpret_cast<const uint2 *>(codes);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint2 v = __ldg(q + j);
+            const uint2 v = ld_in(q + j);
             c[2 * j] = v.x;
             c[2 * j + 1] = v.y;
         }
@@ -265,7 +232,7 @@ __device__ __forceinline__ void ckpt_read32(const uint8_t *codes, const uint8_t 
             c[j] = 0u;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (4 * j + i < n) c[j] |= static_cast<uint32_t>(__ldg(codes + 4 * j + i)) << (8 * i);
+                if (4 * j + i < n) c[j] |= static_cast<uint32_t>(ld_in(codes + 4 * j + i)) << (8 * i);
         }
     }
 #pragma unroll
@@ -333,7 +300,7 @@ __device__ __forceinline__ void read32(const ExpertEpi &p, W &w, int64_t row, in
                                        int n, float (&z)[EPI_COLS])
 {
     if (p.save == MP_SAVE_BF16)
-        w.template get<false>(static_cast<const mp_bf16_t *>(p.z), static_cast<int64_t>(parts) * p.cols, row,
+        w.get(static_cast<const mp_bf16_t *>(p.z), static_cast<int64_t>(parts) * p.cols, row,
                               static_cast<int64_t>(part) * p.cols + c, n, z);
     else
         ckpt_read32(static_cast<const uint8_t *>(p.z) + (row * parts + part) * p.cols + c,
@@ -384,7 +351,7 @@ __device__ __forceinline__ void epi_fwd(const ExpertEpi &p, W &w, int e, int64_t
     }
     if (p.residual != nullptr) {
         float f[EPI_COLS];
-        w.template get<true>(p.residual, p.cols, row, c, n, f);   // it may be out itself
+        w.get(p.residual, p.cols, row, c, n, f);   // it may be out itself
 #pragma unroll
         for (int i = 0; i < EPI_COLS; ++i) z[i] += f[i];
     }
@@ -465,7 +432,7 @@ __device__ __forceinline__ void expert_starts(const int32_t *offsets, int E, int
                                               int lane, int *start, int *tiles, int32_t *status)
 {
 #pragma unroll 8
-    for (int i = lane; i <= E; i += 32) start[i] = __ldg(offsets + i);
+    for (int i = lane; i <= E; i += 32) start[i] = ld_in(offsets + i);
     __syncwarp();
     const int run = (E + 32) / 32, i0 = lane * run, i1 = min(i0 + run, E + 1);
     int high = 0;

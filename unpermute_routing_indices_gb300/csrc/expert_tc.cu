@@ -219,14 +219,13 @@ struct WarpWriter {
     // Rows whose 32-byte sectors a lane cannot read whole are read as they are written,
     // and turned: 20,000 rows by 64 experts of 1,016 x 1,024 with a residual 87 -> 65 us,
     // 2,999 rows by 40 experts of 1,009 x 1,000 106 -> 41.
-    // WRITTEN: what is read may be what the kernel writes, each element after it is read.
-    template <bool WRITTEN>
+    // (What is read may be what the kernel writes, each element after it is read.)
     __device__ __forceinline__ void get(const mp_bf16_t *base, int64_t pitch, int64_t row, int64_t c, int n,
                                         float (&f)[EPI_COLS])
     {
         const unsigned low = low_bits(base) | ((static_cast<unsigned>(pitch | c) & 15u) * 2);
         if (n == EPI_COLS && low == 0) {
-            load32<WRITTEN>(base + row * pitch + c, f);
+            load32(base + row * pitch + c, f);
             return;
         }
         if (lane == 0) tma_store_read();   // the tile before this one has left
@@ -238,7 +237,7 @@ struct WarpWriter {
             for (int i = 0; i < 4; ++i) {
                 const int r = (lane >> 2) + 8 * i;
                 if (r < rows && (lane & 3) * 8 < n)
-                    v[i] = ld_of<WRITTEN>(reinterpret_cast<const uint4 *>(from + r * pitch) + (lane & 3));
+                    v[i] = ld_stream(reinterpret_cast<const uint4 *>(from + r * pitch) + (lane & 3));
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) *piece((lane >> 2) + 8 * i, lane & 3) = v[i];
@@ -246,7 +245,7 @@ struct WarpWriter {
             uint16_t v[32] = {};
 #pragma unroll
             for (int r = 0; r < 32; ++r)
-                if (r < rows && lane < n) v[r] = ld_of<WRITTEN>(from + r * pitch + lane);
+                if (r < rows && lane < n) v[r] = ld_stream(from + r * pitch + lane);
 #pragma unroll
             for (int r = 0; r < 32; ++r) *element(r, lane) = v[r];
         }
@@ -268,14 +267,14 @@ struct WarpWriter {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 float t[8];
-                unpack(__ldg(q + j), t);
+                unpack(ld_in(q + j), t);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) f[8 * j + i] = t[i];
             }
             return;
         }
         float t[1] = {0.0f};
-        if (lane < n) unpack(__ldg(p + lane), t);
+        if (lane < n) unpack(ld_in(p + lane), t);
 #pragma unroll
         for (int i = 0; i < EPI_COLS; ++i) f[i] = __shfl_sync(FULL_MASK, t[0], i);
     }
@@ -303,7 +302,7 @@ __device__ __forceinline__ uint32_t ld_word_if(const uint32_t *p, bool there)
 {
     uint32_t v;
     asm volatile("{\n\t.reg .pred there;\n\tsetp.ne.u32 there, %2, 0;\n\tmov.u32 %0, 0;\n\t"
-                 "@there ld.global.nc.u32 %0, [%1];\n\t}"
+                 "@there ld.global.u32 %0, [%1];\n\t}"
                  : "=r"(v)
                  : "l"(p), "r"(static_cast<uint32_t>(there)));
     return v;

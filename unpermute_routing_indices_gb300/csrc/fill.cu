@@ -29,11 +29,11 @@ constexpr int FILL_MAX_BLOCKS = MP_FILL_MAX_BLOCKS;
 template <typename V>
 __global__ void __launch_bounds__(FILL_THREADS)
     k_zero_rows_from(V *__restrict__ buf, int64_t rows, int64_t units_per_row,
-                     const int32_t *__restrict__ first_row)
+                     const int32_t *first_row)
 {
     pdl_trigger();
     pdl_wait();
-    int64_t s = __ldg(first_row);
+    int64_t s = ld_in(first_row);
     s = s < 0 ? 0 : (s > rows ? rows : s);
     const int64_t end = rows * units_per_row;
     const int64_t step = (int64_t)gridDim.x * FILL_THREADS;

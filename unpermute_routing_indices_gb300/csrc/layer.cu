@@ -82,7 +82,7 @@ struct LayerArgs {
 
 __device__ __forceinline__ float bf16_value(const mp_bf16_t *p)
 {
-    return __uint_as_float(static_cast<uint32_t>(__ldg(p)) << 16);
+    return __uint_as_float(static_cast<uint32_t>(ld_in(p)) << 16);
 }
 
 // ---------------------------------------------------------------------------
@@ -146,12 +146,12 @@ template <typename L, int TB, bool VEC> __global__ void __launch_bounds__(LOGIT_
         typedef typename std::conditional<sizeof(L) == 4, float4, uint2>::type Four;
 #pragma unroll(TB == 1 ? 8 : 4)
         for (int c = threadIdx.x * 4; c < a.H; c += LOGIT_THREADS * 4) {
-            const Four w = __ldg(reinterpret_cast<const Four *>(r + c));
+            const Four w = ld_in(reinterpret_cast<const Four *>(r + c));
             const L *wl = reinterpret_cast<const L *>(&w);
             const f2 w0 = pair(logit_value(wl[0]), logit_value(wl[1])), w1 = pair(logit_value(wl[2]), logit_value(wl[3]));
 #pragma unroll
             for (int b = 0; b < TB; ++b) {
-                const uint2 u = __ldg(reinterpret_cast<const uint2 *>(x[b] + c));
+                const uint2 u = ld_in(reinterpret_cast<const uint2 *>(x[b] + c));
                 v[b].template add_product<sizeof(L) == 2>(pair(bf16_lo(u.x), bf16_hi(u.x)), w0);
                 v[b].template add_product<sizeof(L) == 2>(pair(bf16_lo(u.y), bf16_hi(u.y)), w1);
             }
@@ -637,7 +637,7 @@ __global__ void __launch_bounds__(LAYER_THREADS, 1) k_layer(const LayerArgs a, c
                         } else {
                             for (const char *v = first; v < src + 16 && v < first + bytes; v += 2)
                                 asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + static_cast<uint32_t>(v - src)),
-                                             "h"(__ldg(reinterpret_cast<const uint16_t *>(v))) : "memory");
+                                             "h"(ld_in(reinterpret_cast<const uint16_t *>(v))) : "memory");
                         }
                     }
                 }

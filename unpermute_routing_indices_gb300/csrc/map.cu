@@ -120,7 +120,7 @@ __device__ __forceinline__ int32_t ld_cluster(const int32_t *p, unsigned rank)
 }
 
 // Buckets of this lane's 8 routes of one warp group; -1 past the end.
-__device__ __forceinline__ void load_buckets(const int32_t *__restrict__ idx, int64_t n, int E,
+__device__ __forceinline__ void load_buckets(const int32_t *idx, int64_t n, int E,
                                              int64_t base, int lane, int (&bk)[MAP_CHUNKS],
                                              bool &bad)
 {
@@ -128,7 +128,7 @@ __device__ __forceinline__ void load_buckets(const int32_t *__restrict__ idx, in
 #pragma unroll
     for (int c = 0; c < MAP_CHUNKS; ++c) {
         const int64_t i = base + c * 32 + lane;
-        v[c] = (i < n) ? __ldg(idx + i) : -1;
+        v[c] = (i < n) ? ld_in(idx + i) : -1;
     }
 #pragma unroll
     for (int c = 0; c < MAP_CHUNKS; ++c) {
@@ -145,7 +145,7 @@ __device__ __forceinline__ int64_t warp_base(int tile, int warp, int f)
 }
 
 __global__ void __launch_bounds__(MAP_THREADS)
-    k_map_count(const int32_t *__restrict__ idx, int64_t n, int E, int f, int ntiles,
+    k_map_count(const int32_t *idx, int64_t n, int E, int f, int ntiles,
                 int32_t *__restrict__ tile_counts, int32_t *status)
 {
     // Wait before the trigger: the rank kernel reads idx before its own wait,
@@ -357,8 +357,8 @@ static_assert(MAP_SINGLE_MAX <= (int64_t)MAP_SUB * MAP_MAX_F, "one tile must hol
 #endif
 template <int MODE, bool CACHE>
 __global__ void __launch_bounds__(MAP_THREADS)
-    k_map_rank(const int32_t *__restrict__ idx, int64_t n, int E, int f, int ntiles, int cap,
-               const int32_t *__restrict__ tile_counts, int32_t *__restrict__ row_id_map,
+    k_map_rank(const int32_t *idx, int64_t n, int E, int f, int ntiles, int cap,
+               const int32_t *tile_counts, int32_t *__restrict__ row_id_map,
                int32_t *__restrict__ sorted_to_flat, int32_t *__restrict__ counts,
                int32_t *__restrict__ offsets, int32_t *status)
 {
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(MAP_THREADS)
 #pragma unroll
             for (int c = 0; c < MAP_CHUNKS; ++c) {
                 const int64_t i = base + g * MAP_GROUP + c * 32 + lane;
-                cb[g][c] = (g < f && i < n) ? __ldg(idx + i) : -1;   // raw value first
+                cb[g][c] = (g < f && i < n) ? ld_in(idx + i) : -1;   // raw value first
             }
 #pragma unroll
         for (int g = 0; g < CF; ++g) {

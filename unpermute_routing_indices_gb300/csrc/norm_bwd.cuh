@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, 1)
 
     // What a row has one of, read one row ahead.
     const auto stats_of = [&](uint32_t t) {
-        return t < T ? __ldg(reinterpret_cast<const float4 *>(a.stats) + t) : make_float4(0, 0, 0, 0);
+        return t < T ? ld_in(reinterpret_cast<const float4 *>(a.stats) + t) : make_float4(0, 0, 0, 0);
     };
     const auto gate_of = [&](uint32_t t) {
         return token && t < T ? norm_value(static_cast<const D *>(a.gate)[t]) : 1.0f;

@@ -75,9 +75,9 @@ __global__ void __launch_bounds__(RT_THREADS) k_route_bwd(const RouteBwdArgs a)
     if (t >= a.T) return;
     const L *l = static_cast<const L *>(a.logits) + t * a.E;
     L *gl = static_cast<L *>(a.g_logits) + t * a.E;
-    int pick = lane < a.K ? __ldg(a.idx + t * a.K + lane) : -1;
+    int pick = lane < a.K ? ld_in(a.idx + t * a.K + lane) : -1;
     if (pick >= a.E) pick = -1;
-    const float g = pick >= 0 ? a.scale * __ldg(a.g_weights + t * a.K + lane) : 0.0f;
+    const float g = pick >= 0 ? a.scale * ld_in(a.g_weights + t * a.K + lane) : 0.0f;
     const float pv = pick >= 0 ? fminf(logit(l + pick), FLT_MAX) : -INFINITY;
     const bool dense = a.score == MP_SCORE_SOFTMAX && !a.renorm;
     float at_pick;

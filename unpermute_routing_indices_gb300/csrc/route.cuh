@@ -21,12 +21,12 @@ struct RouteArgs {
     float *weights;
 };
 
-__device__ __forceinline__ float logit(const float *p) { return __ldg(p); }
+__device__ __forceinline__ float logit(const float *p) { return ld_in(p); }
 __device__ __forceinline__ float logit(const __nv_bfloat16 *p)
 {
-    return __uint_as_float(static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t *>(p))) << 16);
+    return __uint_as_float(static_cast<uint32_t>(ld_in(reinterpret_cast<const uint16_t *>(p))) << 16);
 }
-__device__ __forceinline__ float logit(const __half *p) { return __half2float(__ldg(p)); }
+__device__ __forceinline__ float logit(const __half *p) { return __half2float(ld_in(p)); }
 // A logit in shared memory.
 struct SharedLogit {
     float v;
@@ -109,7 +109,7 @@ __device__ __forceinline__ void load_token(const RouteArgs &a, const L *l, int l
     for (int j = 0; j < PER; ++j) {
         const int e = lane + 32 * j;
         v[j] = e < a.E ? logit(l + e) : -INFINITY;
-        b[j] = (e < a.E && a.bias != nullptr) ? __ldg(a.bias + e) : 0.0f;
+        b[j] = (e < a.E && a.bias != nullptr) ? ld_in(a.bias + e) : 0.0f;
     }
 #pragma unroll
     for (int j = 0; j < PER; ++j) v[j] = usable(v[j]) ? fminf(v[j], FLT_MAX) : -INFINITY;   // NaN is not usable
@@ -161,7 +161,7 @@ __device__ __forceinline__ double rcp_exact(double x)
 template <typename L>
 __device__ __forceinline__ uint64_t exact_key(const RouteArgs &a, const L *l, int e, float m)
 {
-    const float v = logit(l + e), b = a.bias != nullptr ? __ldg(a.bias + e) : 0.0f;
+    const float v = logit(l + e), b = a.bias != nullptr ? ld_in(a.bias + e) : 0.0f;
     if (!usable(v) || !usable(b)) return 0ull;
     const double x = fminf(v, FLT_MAX);
     double c;
@@ -557,7 +557,7 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs &a, const L *l, cons
         }
         bool unsure = false;
         if (lane < K && too_near(my_key, next, err))
-            unsure = !(logit(l + my_i) == logit(l + next_i) && __ldg(a.bias + my_i) == __ldg(a.bias + next_i));
+            unsure = !(logit(l + my_i) == logit(l + next_i) && ld_in(a.bias + my_i) == ld_in(a.bias + next_i));
         if (!near && __any_sync(FULL_MASK, unsure)) {
             // Mostly the picks and the best of the rest have to be ordered, and what
             // comes after is out of reach of the last place.

@@ -70,7 +70,7 @@ __device__ __forceinline__ void pick_rounds(uint32_t (&key)[N], uint32_t (&ex)[N
 // grouped T=32,768, E=256 one: 31.5 -> 30.8 us).
 template <int PER, int KT = 0>
 __global__ void __launch_bounds__(RT_THREADS)
-    k_topk_softmax(const float *__restrict__ logits, int64_t T, int E, int K, int n_groups,
+    k_topk_softmax(const float *logits, int64_t T, int E, int K, int n_groups,
                    int topk_groups, int32_t *__restrict__ idx, float *__restrict__ probs)
 {
     pdl_trigger();
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(RT_THREADS)
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
         const int e = lane + 32 * j;
-        v[j] = e < E ? __ldg(l + e) : -FLT_MAX;
+        v[j] = e < E ? ld_in(l + e) : -FLT_MAX;
     }
     // Experts still eligible: bit j of `live` stands for expert lane + 32*j.
     unsigned live = 0;
@@ -235,8 +235,8 @@ __global__ void __launch_bounds__(RT_THREADS)
 }
 
 __global__ void __launch_bounds__(RT_THREADS)
-    k_topk_softmax_bwd(const float *__restrict__ g_probs, const float *__restrict__ probs,
-                       const int32_t *__restrict__ idx, int64_t T, int E, int K,
+    k_topk_softmax_bwd(const float *g_probs, const float *probs,
+                       const int32_t *idx, int64_t T, int E, int K,
                        float *__restrict__ g_logits)
 {
     pdl_trigger();
@@ -246,9 +246,9 @@ __global__ void __launch_bounds__(RT_THREADS)
     if (t >= T) return;
     float *gl = g_logits + t * E;
     for (int e = lane; e < E; e += 32) gl[e] = 0.0f;
-    const float p = lane < K ? __ldg(probs + t * K + lane) : 0.0f;
-    const float g = lane < K ? __ldg(g_probs + t * K + lane) : 0.0f;
-    const int32_t ex = lane < K ? __ldg(idx + t * K + lane) : -1;
+    const float p = lane < K ? ld_in(probs + t * K + lane) : 0.0f;
+    const float g = lane < K ? ld_in(g_probs + t * K + lane) : 0.0f;
+    const int32_t ex = lane < K ? ld_in(idx + t * K + lane) : -1;
     float dsum = 0.0f;
     for (int k = 0; k < K; ++k)
         dsum = __fmaf_rn(__shfl_sync(FULL_MASK, p, k), __shfl_sync(FULL_MASK, g, k), dsum);

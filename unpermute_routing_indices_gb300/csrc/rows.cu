@@ -83,8 +83,8 @@ inline RowGrid row_grid(int64_t T, int nvec, int vpt)
 
 template <typename V, int VPT, bool PROBS>
 __global__ void __launch_bounds__(ROW_THREADS)
-    k_permute(const V *__restrict__ x, const float *__restrict__ probs,
-              const int32_t *__restrict__ map, int64_t T, int K, int nvec, int tpt_log2,
+    k_permute(const V *x, const float *probs,
+              const int32_t *map, int64_t T, int K, int nvec, int tpt_log2,
               V *__restrict__ out, float *__restrict__ out_probs)
 {
     pdl_trigger();
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(ROW_THREADS)
             v[j] = (c < nvec) ? ld_stream(src + c) : zero_vec<V>();
         }
         for (int k = 0; k < K; ++k) {
-            const int32_t row = __ldg(m + k);
+            const int32_t row = ld_in(m + k);
             if (row < 0) continue;
             V *dst = out + (int64_t)row * nvec;
 #pragma unroll
@@ -115,8 +115,8 @@ __global__ void __launch_bounds__(ROW_THREADS)
     }
     if (PROBS && lane == 0) {
         for (int k = 0; k < K; ++k) {
-            const int32_t row = __ldg(m + k);
-            if (row >= 0) out_probs[row] = __ldg(probs + t * K + k);
+            const int32_t row = ld_in(m + k);
+            if (row >= 0) out_probs[row] = ld_in(probs + t * K + k);
         }
     }
 }
@@ -124,9 +124,9 @@ __global__ void __launch_bounds__(ROW_THREADS)
 // acc = fmaf(p, r, acc) per slot in slot order (PROBS), or acc = acc + r.
 template <typename V, int VPT, bool PROBS, bool GATHER_PROBS, int SB>
 __global__ void __launch_bounds__(ROW_THREADS)
-    k_unpermute(const V *__restrict__ rows, const float *__restrict__ probs,
-                const int32_t *__restrict__ map, int64_t T, int K, int nvec, int tpt_log2,
-                V *__restrict__ out, const float *__restrict__ g_out_probs,
+    k_unpermute(const V *rows, const float *probs,
+                const int32_t *map, int64_t T, int K, int nvec, int tpt_log2,
+                V *__restrict__ out, const float *g_out_probs,
                 float *__restrict__ g_probs)
 {
     pdl_trigger();
@@ -149,8 +149,8 @@ __global__ void __launch_bounds__(ROW_THREADS)
 #pragma unroll
             for (int i = 0; i < SB; ++i) {
                 const int k = kb + i;
-                rk[i] = (k < K) ? __ldg(m + k) : -1;
-                pk[i] = (PROBS && k < K) ? __ldg(probs + t * K + k) : 1.0f;
+                rk[i] = (k < K) ? ld_in(m + k) : -1;
+                pk[i] = (PROBS && k < K) ? ld_in(probs + t * K + k) : 1.0f;
             }
             V r[SB][VPT];
 #pragma unroll
@@ -182,8 +182,8 @@ __global__ void __launch_bounds__(ROW_THREADS)
     }
     if (GATHER_PROBS && lane == 0) {
         for (int k = 0; k < K; ++k) {
-            const int32_t row = __ldg(m + k);
-            g_probs[t * K + k] = row >= 0 ? __ldg(g_out_probs + row) : 0.0f;
+            const int32_t row = ld_in(m + k);
+            g_probs[t * K + k] = row >= 0 ? ld_in(g_out_probs + row) : 0.0f;
         }
     }
 }
@@ -192,8 +192,8 @@ __global__ void __launch_bounds__(ROW_THREADS)
 // gradient is a CTA reduction), so tokens past T run with no routed slot.
 template <typename V, int VPT, int SB>
 __global__ void __launch_bounds__(ROW_THREADS, bwd_min_blocks(Lanes<V>::N == 8, SB))
-    k_unpermute_bwd(const V *__restrict__ gy, const V *__restrict__ rows,
-                    const float *__restrict__ probs, const int32_t *__restrict__ map, int64_t T,
+    k_unpermute_bwd(const V *gy, const V *rows,
+                    const float *probs, const int32_t *map, int64_t T,
                     int K, int nvec, int tpt_log2, V *__restrict__ g_rows,
                     float *__restrict__ g_probs)
 {
@@ -213,8 +213,8 @@ __global__ void __launch_bounds__(ROW_THREADS, bwd_min_blocks(Lanes<V>::N == 8, 
 #pragma unroll
         for (int i = 0; i < SB; ++i) {
             const int k = kb + i;
-            rk[i] = (active && k < K) ? __ldg(m + k) : -1;
-            pk[i] = (active && k < K) ? __ldg(probs + t * K + k) : 0.0f;
+            rk[i] = (active && k < K) ? ld_in(m + k) : -1;
+            pk[i] = (active && k < K) ? ld_in(probs + t * K + k) : 0.0f;
             dot[i] = 0.0f;
         }
         for (int c0 = 0; c0 < nvec; c0 += tpt * VPT) {
@@ -340,10 +340,10 @@ __device__ __forceinline__ void cp_async_wait()
 
 template <bool PROBS, bool GATHER_PROBS, int SB>
 __global__ void __launch_bounds__(ROW_THREADS)
-    k_unpermute_staged(const uint4 *__restrict__ rows, const float *__restrict__ probs,
-                       const int32_t *__restrict__ map, int64_t T, int K, int nvec,
+    k_unpermute_staged(const uint4 *rows, const float *probs,
+                       const int32_t *map, int64_t T, int K, int nvec,
                        int tpt_log2, uint4 *__restrict__ out,
-                       const float *__restrict__ g_out_probs, float *__restrict__ g_probs)
+                       const float *g_out_probs, float *__restrict__ g_probs)
 {
     pdl_trigger();
     pdl_wait();
@@ -357,8 +357,8 @@ __global__ void __launch_bounds__(ROW_THREADS)
     float pk[SB];
 #pragma unroll
     for (int i = 0; i < SB; ++i) {
-        rk[i] = (i < K) ? __ldg(m + i) : -1;
-        pk[i] = (PROBS && i < K) ? __ldg(probs + t * K + i) : 1.0f;
+        rk[i] = (i < K) ? ld_in(m + i) : -1;
+        pk[i] = (PROBS && i < K) ? ld_in(probs + t * K + i) : 1.0f;
     }
     const auto issue = [&](int c, int buf) {
         uint4 *const dst = row_stage + buf * SB * ROW_THREADS + threadIdx.x;
@@ -393,16 +393,16 @@ __global__ void __launch_bounds__(ROW_THREADS)
     }
     if (GATHER_PROBS && lane == 0) {
         for (int k = 0; k < K; ++k) {
-            const int32_t row = __ldg(m + k);
-            g_probs[t * K + k] = row >= 0 ? __ldg(g_out_probs + row) : 0.0f;
+            const int32_t row = ld_in(m + k);
+            g_probs[t * K + k] = row >= 0 ? ld_in(g_out_probs + row) : 0.0f;
         }
     }
 }
 
 template <int SB>
 __global__ void __launch_bounds__(ROW_THREADS)
-    k_unpermute_bwd_staged(const uint4 *__restrict__ gy, const uint4 *__restrict__ rows,
-                           const float *__restrict__ probs, const int32_t *__restrict__ map,
+    k_unpermute_bwd_staged(const uint4 *gy, const uint4 *rows,
+                           const float *probs, const int32_t *map,
                            int64_t T, int K, int nvec, int tpt_log2,
                            uint4 *__restrict__ g_rows, float *__restrict__ g_probs)
 {
@@ -419,8 +419,8 @@ __global__ void __launch_bounds__(ROW_THREADS)
     float pk[SB], dot[SB];
 #pragma unroll
     for (int i = 0; i < SB; ++i) {
-        rk[i] = (active && i < K) ? __ldg(m + i) : -1;
-        pk[i] = (active && i < K) ? __ldg(probs + t * K + i) : 0.0f;
+        rk[i] = (active && i < K) ? ld_in(m + i) : -1;
+        pk[i] = (active && i < K) ? ld_in(probs + t * K + i) : 0.0f;
         dot[i] = 0.0f;
     }
     const auto issue = [&](int c, int buf) {
