@@ -29,8 +29,8 @@ from dataclasses import dataclass
 
 import torch
 
-from . import (mp_block_norm, mp_block_norm_bwd, mp_build_map, mp_build_map_capacity, mp_expert_mlp, mp_expert_mlp_bwd,
-               mp_permute, mp_permute_bwd, mp_route, mp_route_bwd,
+from . import (mp_block_norm, mp_block_norm_bwd, mp_build_map, mp_build_map_capacity,
+               mp_expert_mlp, mp_expert_mlp_bwd, mp_permute, mp_permute_bwd, mp_route, mp_route_bwd,
                mp_sort_chunks_pad, mp_sort_chunks_pad_bwd, mp_topk_softmax,
                mp_topk_softmax_bwd, mp_unpad_restore, mp_unpad_restore_bwd, mp_unpermute,
                mp_unpermute_bwd, mp_unpermute_ep, mp_zero_rows_from)
@@ -196,17 +196,18 @@ class _ExpertMlp(torch.autograd.Function):
 class _BlockNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, gate, post_weight, post_bias, pre_weight, pre_bias, kind, eps, scale,
-                keep):
+                keep, status):
         s, y, stats = mp_block_norm(x, residual, post_weight=post_weight, post_bias=post_bias,
                                     gate=gate, scale=scale, pre_weight=pre_weight,
-                                    pre_bias=pre_bias, kind=kind, eps=eps, with_stats=keep)
+                                    pre_bias=pre_bias, kind=kind, eps=eps, with_stats=keep,
+                                    status=status)
         ctx.set_materialize_grads(False)
         ctx.has_stream = s is not x
         if keep:
             ctx.save_for_backward(x if post_weight is not None or gate is not None else None,
                                   s if pre_weight is not None else None, stats, gate, post_weight,
                                   post_bias, pre_weight, pre_bias)
-            ctx.kind, ctx.scale = kind, scale
+            ctx.kind, ctx.scale, ctx.status = kind, scale, status
         return (s if ctx.has_stream else None), y
 
     @staticmethod
@@ -214,7 +215,7 @@ class _BlockNorm(torch.autograd.Function):
     def backward(ctx, g_s, g_y):
         x, s, stats, gate, post_weight, post_bias, pre_weight, pre_bias = ctx.saved_tensors
         if g_s is None and g_y is None:
-            return (None,) * 11
+            return (None,) * 12
         if pre_weight is not None and g_y is None:
             g_y = torch.zeros_like(s)
         if pre_weight is None and g_s is None:
@@ -222,8 +223,9 @@ class _BlockNorm(torch.autograd.Function):
         g = mp_block_norm_bwd(
             None if g_s is None else g_s.contiguous(), None if g_y is None else g_y.contiguous(),
             x, s, stats, post_weight=post_weight, post_bias=post_bias, gate=gate, scale=ctx.scale,
-            pre_weight=pre_weight, pre_bias=pre_bias, kind=ctx.kind, need=ctx.needs_input_grad[:7])
-        return *g, None, None, None, None
+            pre_weight=pre_weight, pre_bias=pre_bias, kind=ctx.kind, need=ctx.needs_input_grad[:7],
+            status=ctx.status)
+        return *g, None, None, None, None, None
 
 
 class _SortChunksPad(torch.autograd.Function):
@@ -297,7 +299,7 @@ def route(logits: torch.Tensor, topk: int, *, score: str = "softmax", bias=None,
 
 def block_norm(x: torch.Tensor, residual=None, *, post_weight=None, post_bias=None, gate=None,
                scale: float = 1.0, pre_weight=None, pre_bias=None, kind: str = "rms",
-               eps: float = 1e-6):
+               eps: float = 1e-6, status=None):
     """The norm after a block and the one before the next, with gate, residual scale and
     residual between them (mp_block_norm): x [T,H] -> (s, y),
 
@@ -306,10 +308,11 @@ def block_norm(x: torch.Tensor, residual=None, *, post_weight=None, post_bias=No
         y = norm(s) * pre_weight + pre_bias    (None without a pre_weight)
 
     differentiable w.r.t. x, residual, gate ([H], [T,1] or [T,H]), weights and biases.
-    For the backward pass x, s and four fp32 values a row are kept."""
+    For the backward pass x, s and four fp32 values a row are kept.  `status` (int32 [1])
+    gets "stalled" where results of either pass are invalid."""
     tensors = (x, residual, gate, post_weight, post_bias, pre_weight, pre_bias)
     keep = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
-    s, y = _BlockNorm.apply(*tensors, kind, float(eps), float(scale), keep)
+    s, y = _BlockNorm.apply(*tensors, kind, float(eps), float(scale), keep, status)
     return (x if s is None else s), y
 
 

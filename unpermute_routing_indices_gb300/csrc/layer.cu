@@ -955,8 +955,8 @@ template <int NT, bool ODD> mp_status_t launch_layer(const LayerArgs &a, cudaStr
                              static_cast<size_t>(cuts.b_rows) * 2 * cuts.of[1].b_pitch()};
     for (cuts.reds = RED_MOST; cuts.reds > 1 && fixed + cuts.reds * L::RED * 4 + 2 * (slots[0] + slots[1]) > LAYER_SMEM; --cuts.reds) {
     }
+    // (1,024 experts and 2,048 routes leave room for one slot of each.)
     size_t bytes = fixed + static_cast<size_t>(cuts.reds) * L::RED * 4 + slots[0] + slots[1];
-    if (bytes > LAYER_SMEM) return MP_ERR_UNSUPPORTED;
     int n[2] = {1, 1};
     for (bool more = true; more;) {   // of the product with fewer, as long as there is room
         more = false;
