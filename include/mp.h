@@ -394,9 +394,10 @@ mp_status_t mp_expert_mlp_bwd(const mp_bf16_t *g_y, const mp_bf16_t *x, const mp
  *   idx, weights as mp_route gives them for l
  *   y[t,:]  = sum over k in slot order, fp32 from +0, of weights[t,k] *
  *             (h[t,k,:] w2[e]^T + b2[e]),  e = idx[t,k], empty slots skipped
- *   h[t,k,:] = act(x[t,:] w1[e]^T + b1[e])        (fp32 sums, rounded to bf16)
- * rounded once: what the calls mp_route, mp_build_map, mp_permute, mp_expert_mlp and
- * mp_unpermute give, but for their rounding of each expert's result to bf16.
+ *   h[t,k,:] = act(x[t,:] w1[e]^T + b1[e])        (fp32 sums, kept to 16 bits: the nearest
+ *             bf16 value and the nearest of what is left)
+ * y rounded once: what the calls mp_route, mp_build_map, mp_permute, mp_expert_mlp and
+ * mp_unpermute give, but for their rounding of h and of each expert's result to bf16.
  *   x        device bf16 [T,H]
  *   router   device [E,H] of type router_dtype (MP_DTYPE_*)
  *   bias, score, n_groups, topk_groups, group_top, renorm, scale   as mp_route
@@ -446,9 +447,10 @@ mp_status_t mp_moe_layer(const mp_bf16_t *x, const void *router, int32_t router_
  *   stats        device fp32 [T,4] out or NULL, 16-byte aligned: mean and 1/sqrt(...)
  *                of x (0 without a post_weight; mean 0 for rms), the same of s
  *   dev_status   device int32 or NULL: MP_STATUS_STALLED
- * s and y may each be the buffer of x, of residual or of a [T,H] gate.  A row's result
- * depends on nothing but that row and on whether rows are whole 16-byte vectors on 16-byte
- * boundaries, which is the faster way.  Limits: H <= MP_MAX_NORM_WIDTH; T < 2^31.
+ * s and y may each be the buffer of x, of residual or of a [T,H] gate, but not both the
+ * same one.  A row's result depends on nothing but that row and on whether rows are whole
+ * 16-byte vectors on 16-byte boundaries, which is the faster way.
+ * Limits: H <= MP_MAX_NORM_WIDTH; T < 2^31.
  */
 mp_status_t mp_block_norm(const void *x, const void *residual, int64_t T, int32_t H,
                           int32_t dtype, int32_t kind, float eps, const void *post_weight,

@@ -156,7 +156,7 @@ def check_backward(t, how, g_s, g_y, s, stats, got):
         if g is None:
             continue
         w, size, summed = want[name]
-        # fp32 sums over the rows: runs of T/152 of them, then 152 in 64 bits
+        # fp32 sums over the rows: runs of T/152 of them, then 152 in pairs of fp32
         within(g, w, half(g.dtype) * w.abs() + (2 * terms(H) + summed / 64) * U32 * size, name)
 
 
@@ -188,9 +188,10 @@ def _act(z, act):
     return z
 
 
-def layer(x, w1, w2, b1, b2, act, idx, weights):
-    """y in 64 bits for the given choice and weights, and how far a result may be off: h
-    rounded to bf16 (and, for the activation, 2^-16 of it), y rounded once, sums in fp32."""
+def layer(x, w1, w2, b1, b2, act, idx, weights, kept=2.0 ** -16):
+    """y in 64 bits for the given choice and weights, and how far a result may be off: h off by
+    `kept` of it (the nearest bf16 value is off by 2^-8 of it at most, and the rest, kept as
+    bf16 too, by 2^-8 of that) and, for the activation, 2^-15, y rounded once, sums in fp32."""
     T, H = x.shape
     F, O = w2.shape[2], w2.shape[1]
     inner = dict(swiglu="silu", geglu="gelu").get(act, act)
@@ -211,7 +212,7 @@ def layer(x, w1, w2, b1, b2, act, idx, weights):
             h, d = v * u, 1.2 * n1 * size * u.abs() + n1 * usize * (v.abs() + 1.2 * n1 * size)
         else:
             h, d = _act(z, inner), 1.2 * n1 * size
-        d = d + (2.0 ** -8 + 2.0 ** -15) * (h.abs() + d) + 2.0 ** -60
+        d = d + (kept + 2.0 ** -15) * (h.abs() + d) + 2.0 ** -60
         b = w2[e].double()
         out, osize = h @ b.T, d @ b.abs().T + n2 * (h.abs() @ b.abs().T)
         if b2 is not None:

@@ -4,6 +4,7 @@ from __future__ import annotations
 
 import itertools
 import math
+import threading
 
 import pytest
 import torch
@@ -44,6 +45,8 @@ SIZES = [  # T, E, K, H, F, O
     (64, 1, 1, 128, 64, 128), (3, 300, 10, 96, 40, 96), (5, 1024, 32, 72, 16, 64), (64, 40, 32, 40, 24, 48),
     (9, 16, 4, 1000, 1000, 1000), (1, 3, 2, 4099, 17, 5), (4, 12, 2, 7168, 24, 16), (2, 4, 1, 16, 4100, 24),
     (12, 5, 3, 2050, 1022, 2046), (1, 2, 1, 40000, 64, 40),
+    (2, 3, 2, 65536, 16, 8), (2, 3, 2, 8, 65536, 8), (3, 3, 2, 16, 8, 65536),   # the widest
+    (64, 1024, 32, 24, 16, 40), (64, 170, 32, 40, 24, 40),                      # the largest tables
 ]
 
 
@@ -226,6 +229,53 @@ def test_graph_streams_and_repeats():
     assert all(torch.equal(a, b) for out in outs for a, b in zip(out, want))
 
 
+def test_weights_past_32_bits():
+    """Experts whose weights lie beyond 2^32 values; the others' are not read."""
+    E, H, F = 10, 4096, 65536
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    t = dict(w1=torch.full((E, 2 * F, H), float("nan"), dtype=torch.bfloat16, device="cuda"),
+             w2=torch.full((E, H, F), float("nan"), dtype=torch.bfloat16, device="cuda"), b1=None, b2=None,
+             router=nu.rows(E, H, torch.float32, 1, mean=0.0, std=H ** -0.5))
+    for e in (8, 9):
+        t["w1"][e].normal_(0.0, H ** -0.5, generator=gen)
+        t["w2"][e].normal_(0.0, F ** -0.5, generator=gen)
+    bias = torch.zeros(E, device="cuda")
+    bias[8:] = 100.0
+    x = nu.rows(2, H, torch.bfloat16, 3, mean=0.0)
+    y, idx, _ = check(x, t, 2, "swiglu", bias=bias)
+    assert bool((idx >= 8).all()) and bool(y.isfinite().all())
+
+
+def test_two_host_threads():
+    t = weights_of(24, 512, 96, 512, "swiglu", 2)
+    norm = nu.rows(1, 512, torch.bfloat16, 9, mean=1.0)[0]
+    x = nu.rows(6, 512, torch.bfloat16, 3, mean=0.0)
+
+    def call():
+        s, n, _ = mp.mp_block_norm(x, pre_weight=norm)
+        y, idx, w = mp.mp_moe_layer(n, t["router"], t["w1"], t["w2"], 4)
+        return mp.mp_block_norm(y, s, post_weight=norm)[0], idx, w
+    want = call()
+    torch.cuda.synchronize()
+    results, errors = [], []
+
+    def work():
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                mine = [call() for _ in range(30)]
+                torch.cuda.current_stream().synchronize()
+            results.extend(mine)
+        except Exception as e:   # noqa: BLE001 - told to the test below
+            errors.append(e)
+    threads = [threading.Thread(target=work) for _ in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not errors and len(results) == 60
+    assert all(torch.equal(a, b) for r in results for a, b in zip(r, want))
+
+
 def test_beside_the_chain():
     """The layer and the calls that it stands for: the same choice, results within both bounds."""
     t = weights_of(32, 512, 128, 512, "swiglu", 5)
@@ -237,7 +287,8 @@ def test_beside_the_chain():
     rows, _ = mp.mp_permute(x, rim)
     out, _, _ = mp.mp_expert_mlp(rows, t["w1"], t["w2"], offsets)
     chain = mp.mp_unpermute(out, rim, w)
-    want, bound = nu.layer(x, t["w1"], t["w2"], None, None, "swiglu", idx, w)
+    # the chain keeps h as one bf16 value
+    want, bound = nu.layer(x, t["w1"], t["w2"], None, None, "swiglu", idx, w, kept=2.0 ** -8)
     each = torch.zeros_like(want)
     for k in range(4):
         ek = idx[:, k:k + 1]

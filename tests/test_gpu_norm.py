@@ -287,3 +287,22 @@ def test_graph_streams_and_repeats(H):
     fresh = step()
     assert all(torch.equal(a, b) for a, b in zip(out, fresh))
     assert not torch.equal(out[0], want[0])
+
+
+@pytest.mark.parametrize("T,H", [(1048580, 4096), (1048581, 4097)])
+def test_rows_past_32_bits(T, H):
+    """Rows beyond 2^32 values, beside the same rows alone."""
+    assert (T - 3) * H > 2 ** 32
+    x = torch.empty(T, H, dtype=torch.bfloat16, device="cuda").normal_()
+    w, v = (nu.rows(1, H, torch.bfloat16, i, mean=1.0)[0] for i in (1, 2))
+    ends = torch.tensor([0, 1, T - 3, T - 2, T - 1], device="cuda")
+    few = x[ends].contiguous()
+    s, y, stats = mp.mp_block_norm(x, x, post_weight=w, pre_weight=v, scale=0.5, with_stats=True)
+    s1, y1, stats1 = mp.mp_block_norm(few, few, post_weight=w, pre_weight=v, scale=0.5, with_stats=True)
+    for a, b in ((s, s1), (y, y1), (stats, stats1)):
+        assert torch.equal(a[ends], b)
+    need = (True, True, False, False, False, False, False)
+    g = mp.mp_block_norm_bwd(y, x, x, s, stats, post_weight=w, pre_weight=v, scale=0.5, need=need)
+    g1 = mp.mp_block_norm_bwd(y1, few, few, s1, stats1, post_weight=w, pre_weight=v, scale=0.5, need=need)
+    for a, b in zip(g[:2], g1[:2]):
+        assert torch.equal(a[ends], b)

@@ -12,6 +12,7 @@ from tests import norm_util as nu
 from unpermute_routing_indices_gb300 import _build, _lib
 
 FAKE = ctypes.c_void_p(0x1000)   # never dereferenced: every call fails validation
+OTHER = ctypes.c_void_p(0x2000)
 INVALID, WORKSPACE, UNSUPPORTED = -1, -2, -3
 
 
@@ -27,7 +28,7 @@ def changed(base, **new):
 
 
 NORM = dict(x=FAKE, residual=FAKE, T=4, H=64, dtype=0, kind=0, eps=1e-6, post_weight=FAKE, post_bias=None,
-            gate=None, gate_form=0, scale=1.0, pre_weight=FAKE, pre_bias=None, s=FAKE, y=FAKE, stats=None,
+            gate=None, gate_form=0, scale=1.0, pre_weight=FAKE, pre_bias=None, s=FAKE, y=OTHER, stats=None,
             status=None, stream=None)
 
 
@@ -36,6 +37,7 @@ NORM = dict(x=FAKE, residual=FAKE, T=4, H=64, dtype=0, kind=0, eps=1e-6, post_we
     (dict(dtype=3), INVALID), (dict(dtype=-1), INVALID), (dict(kind=2), INVALID), (dict(kind=-1), INVALID),
     (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID),
     (dict(x=None), INVALID), (dict(s=None), INVALID), (dict(y=None), INVALID),
+    (dict(s=OTHER), INVALID),   # one buffer for both
     (dict(gate_form=4), INVALID), (dict(gate_form=1), INVALID), (dict(gate=FAKE), INVALID),
     (dict(post_weight=None, pre_weight=None, y=None), INVALID), (dict(pre_weight=None), INVALID),
     (dict(pre_weight=None, pre_bias=FAKE, y=None), INVALID), (dict(post_weight=None, post_bias=FAKE), INVALID),

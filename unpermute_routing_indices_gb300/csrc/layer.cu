@@ -9,8 +9,8 @@
 // spread over the CTAs, and the grid waits for them.
 //
 // Logits are sums in pairs of fp32 (a sum and what its roundings lost), so that they are those
-// of 64 bits rounded once, and the choice with them: sums in 64 bits would take 16 times the
-// instructions' time on this part.
+// of 64 bits rounded once, and the choice with them.  (FP64 units are few on this part: 1.25
+// TFLOP/s by its data sheet.)
 //
 // k_layer: one CTA an SM, launched cooperatively.  A unit of work is U rows of an expert's
 // weights against all tokens of that expert (an entry: up to 8 NT of them).  Each of eight

@@ -95,7 +95,8 @@ extern "C" mp_status_t mp_block_norm(const void *x, const void *residual, int64_
     const bool as_is = residual == nullptr && post_weight == nullptr && gate == nullptr && scale == 1.0f;
     if (x == nullptr || (post_weight == nullptr && pre_weight == nullptr) ||
         (post_bias != nullptr && post_weight == nullptr) || (pre_bias != nullptr && pre_weight == nullptr) ||
-        (y != nullptr) != (pre_weight != nullptr) || (s == nullptr && !as_is) || !aligned16(stats))
+        (y != nullptr) != (pre_weight != nullptr) || (s == nullptr && !as_is) || (y != nullptr && s == y) ||
+        !aligned16(stats))
         return MP_ERR_INVALID_ARG;
     NormCall c = {};
     c.T = T; c.H = H; c.kind = kind; c.gate_form = gate_form; c.eps = eps; c.scale = scale;

@@ -5,7 +5,7 @@
 // the gate's gradient written once.  Of what the rows share, a thread sums its columns'
 // gradients over its rows in registers (the weights') or in shared memory (biases and a
 // gate a channel, which few calls have); a CTA adds up its groups in order and leaves one
-// partial sum a column, and a second kernel adds those of the CTAs in order, in 64 bits.
+// partial sum a column, and a second kernel adds those of the CTAs in order, in pairs of fp32.
 #pragma once
 
 #include "norm.cuh"

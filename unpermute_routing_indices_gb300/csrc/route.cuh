@@ -27,11 +27,6 @@ __device__ __forceinline__ float logit(const __nv_bfloat16 *p)
     return __uint_as_float(static_cast<uint32_t>(ld_in(reinterpret_cast<const uint16_t *>(p))) << 16);
 }
 __device__ __forceinline__ float logit(const __half *p) { return __half2float(ld_in(p)); }
-// A logit in shared memory.
-struct SharedLogit {
-    float v;
-};
-__device__ __forceinline__ float logit(const SharedLogit *p) { return p->v; }
 __device__ __forceinline__ float logit_value(float v) { return v; }
 __device__ __forceinline__ float logit_value(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float logit_value(__half v) { return __half2float(v); }
