@@ -113,12 +113,11 @@ __global__ void __launch_bounds__(ROW_THREADS)
             }
         }
     }
-    if (PROBS && lane == 0) {
-        for (int k = 0; k < K; ++k) {
+    if (PROBS)   // a slot a lane (one lane for all: 185.0 us, 16,384 x 4,096, K = 8; so 182.6)
+        for (int k = lane; k < K; k += tpt) {
             const int32_t row = ld_in(m + k);
             if (row >= 0) out_probs[row] = ld_in(probs + t * K + k);
         }
-    }
 }
 
 // acc = fmaf(p, r, acc) per slot in slot order (PROBS), or acc = acc + r.
@@ -180,12 +179,11 @@ __global__ void __launch_bounds__(ROW_THREADS)
             if (c < nvec) st_row(out + t * nvec + c, pack(acc[j]));
         }
     }
-    if (GATHER_PROBS && lane == 0) {
-        for (int k = 0; k < K; ++k) {
+    if (GATHER_PROBS)   // a slot a lane
+        for (int k = lane; k < K; k += tpt) {
             const int32_t row = ld_in(m + k);
             g_probs[t * K + k] = row >= 0 ? ld_in(g_out_probs + row) : 0.0f;
         }
-    }
 }
 
 // Backward of the weighted combine.  All threads stay to the end (the probs
@@ -391,12 +389,11 @@ __global__ void __launch_bounds__(ROW_THREADS)
         }
         st_row(out + t * nvec + c, pack(acc));
     }
-    if (GATHER_PROBS && lane == 0) {
-        for (int k = 0; k < K; ++k) {
+    if (GATHER_PROBS)   // a slot a lane
+        for (int k = lane; k < K; k += tpt) {
             const int32_t row = ld_in(m + k);
             g_probs[t * K + k] = row >= 0 ? ld_in(g_out_probs + row) : 0.0f;
         }
-    }
 }
 
 template <int SB>
