@@ -12,7 +12,9 @@
 //   ROWS_VEC   shorter ones: a thread copies vectors tid, tid + W, ... of the row by cp.async
 //              and reads nobody else's.
 //   ROWS_ANY   rows that start anywhere: the group copies the 16-byte granules that hold the row,
-//              and a thread reads values tid, tid + W, ...; a barrier in between.
+//              and lane l of a warp reads values l, l + 32, ... of the warp's run of 512; a barrier
+//              in between.  All but a row's last warp have a whole run and ask nothing for each value.
+//   ROWS_NARROW  such rows of up to 256 values, several a warp: values tid, tid + W, ...
 //   C 4      rows of more than 8192 values: not staged, 1024 threads read them as they need them.
 #pragma once
 
@@ -32,7 +34,7 @@ constexpr int NORM_BUDGET = 112 * 1024;   // shared memory of one of two CTAs on
 constexpr int NORM_MOST = 225 * 1024;     // of one alone
 constexpr int NORM_SLOTS = 4;
 
-enum { ROWS_ANY, ROWS_VEC, ROWS_BULK };
+enum { ROWS_ANY, ROWS_NARROW, ROWS_VEC, ROWS_BULK };
 
 // How T rows of H values are laid out.
 struct NormPlan {
@@ -119,12 +121,14 @@ __device__ __forceinline__ void cp_wait(int left)
 
 // One group's view of its rows: N values a thread, in N2 pairs.
 template <typename D, int M, int C> struct NormGroup {
-    static constexpr bool VEC = M != ROWS_ANY;
+    static constexpr bool VEC = M == ROWS_VEC || M == ROWS_BULK;
     static constexpr int N = 8 * C, N2 = 4 * C;
     static constexpr int NV = 16 / sizeof(D);    // values a vector
     static constexpr int VECS = N / NV;
     static constexpr bool STAGED = C < 4;
     static constexpr int WARPS = 32;   // of a row at most
+    static constexpr bool RUNS = M == ROWS_ANY;   // a warp's values lie side by side
+    static constexpr int RUN = 32 * N;            // of a warp
 
     int W, H, tid, group;
     float *red;           // [2][M_MOST][WARPS] of this group: see sums()
@@ -207,9 +211,12 @@ template <typename D, int M, int C> struct NormGroup {
     // Column of pair i; the second of the pair is `beside` further on.
     __device__ __forceinline__ int col(int i) const
     {
-        return VEC ? (2 * i / NV * W + tid) * NV + 2 * i % NV : 2 * i * W + tid;
+        return VEC ? (2 * i / NV * W + tid) * NV + 2 * i % NV : RUNS ? first() + 64 * i : 2 * i * W + tid;
     }
-    __device__ __forceinline__ int beside() const { return VEC ? 1 : W; }
+    __device__ __forceinline__ int beside() const { return VEC ? 1 : RUNS ? 32 : W; }
+    __device__ __forceinline__ int first() const { return (tid >> 5) * RUN + (tid & 31); }
+    // Whether the row has all of this warp's run: then nothing is asked for each value.
+    __device__ __forceinline__ bool whole() const { return (tid >> 5) * RUN + RUN <= H; }
 
     // Values of a row (or of what is shared by the rows) at `p`, 0 past its end.
     __device__ __forceinline__ void load(const D *p, f2 (&f)[N2]) const
@@ -222,10 +229,14 @@ template <typename D, int M, int C> struct NormGroup {
                 if (at < H) u = *reinterpret_cast<const uint4 *>(p + at);
                 vec_values(u, f + v * (NV / 2), p);
             }
+        } else if (RUNS && whole()) {
+            const D *const from = p + first();
+#pragma unroll
+            for (int i = 0; i < N2; ++i) f[i] = pair(norm_value(from[64 * i]), norm_value(from[64 * i + 32]));
         } else {
 #pragma unroll
             for (int i = 0; i < N2; ++i) {
-                const int at = col(i), next = at + W;
+                const int at = col(i), next = at + beside();
                 f[i] = pair(at < H ? norm_value(p[at]) : 0.0f, next < H ? norm_value(p[next]) : 0.0f);
             }
         }
@@ -238,10 +249,18 @@ template <typename D, int M, int C> struct NormGroup {
                 const int at = (v * W + tid) * NV;
                 if (at < H) *reinterpret_cast<uint4 *>(p + at) = vec_of(f + v * (NV / 2), p);
             }
+        } else if (RUNS && whole()) {
+            D *const to = p + first();
+#pragma unroll
+            for (int i = 0; i < N2; ++i) {
+                const float2 r = both(f[i]);
+                norm_put(to + 64 * i, r.x);
+                norm_put(to + 64 * i + 32, r.y);
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < N2; ++i) {
-                const int at = col(i), next = at + W;
+                const int at = col(i), next = at + beside();
                 const float2 r = both(f[i]);
                 if (at < H) norm_put(p + at, r.x);
                 if (next < H) norm_put(p + next, r.y);
@@ -251,6 +270,16 @@ template <typename D, int M, int C> struct NormGroup {
     // fp32 sums a column: set, or added to.
     template <bool ADD> __device__ __forceinline__ void columns(float *p, const f2 (&f)[N2]) const
     {
+        if (RUNS && whole()) {
+            float *const to = p + first();
+#pragma unroll
+            for (int i = 0; i < N2; ++i) {
+                const float2 r = both(f[i]);
+                to[64 * i] = ADD ? to[64 * i] + r.x : r.x;
+                to[64 * i + 32] = ADD ? to[64 * i + 32] + r.y : r.y;
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < N2; ++i) {
             const int at = col(i), next = at + beside();
@@ -264,7 +293,7 @@ template <typename D, int M, int C> struct NormGroup {
     {
         if (VEC) return col(i) < H ? v : 0ull;
         const float2 r = both(v);
-        return pair(col(i) < H ? r.x : 0.0f, col(i) + W < H ? r.y : 0.0f);
+        return pair(col(i) < H ? r.x : 0.0f, col(i) + beside() < H ? r.y : 0.0f);
     }
 
     // Starts the copy of row t of `rows` into `slot`, by cp.async.
@@ -325,7 +354,7 @@ template <typename D, int M, int C> struct NormGroup {
             if (there) (void)mbar_wait(bars + 8 * i, slot_phase, gave_up);
         } else {
             cp_wait(slots - 1);
-            if (M == ROWS_ANY) barrier();
+            if (!VEC) barrier();
         }
     }
     // The slot after slot i.
@@ -405,6 +434,7 @@ template <typename D> NormPlan norm_plan(int64_t T, int H, int C, int threads, b
 
 // How the rows of a call are staged.
 template <typename D> bool norm_by_bulk(int H) { return H * static_cast<int>(sizeof(D)) >= 2048; }
+inline bool norm_is_narrow(int H) { return H <= 256; }   // less than a warp's lanes of 16 values
 
 // The launchers of the types' kernels (norm_fwd.cu, norm_bwd_*.cu).
 struct NormCall {

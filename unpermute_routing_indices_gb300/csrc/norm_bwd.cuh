@@ -332,7 +332,7 @@ template <typename D, int M, int C, bool POST, bool PRE> mp_status_t run(const N
     const NormPlan p = norm_plan<D>(c.T, c.H, C, C < 4 ? NORM_THREADS : 2 * NORM_THREADS, M == ROWS_BULK, a.in.tensors,
                                     held, more, false);
     if constexpr (C < 4)   // fp32 rows and several sums beside them
-        if (p.stages < 1) return run<D, M == ROWS_ANY ? ROWS_ANY : ROWS_VEC, 4, POST, PRE>(c, parts);
+        if (p.stages < 1) return run<D, NormGroup<D, M, C>::VEC ? ROWS_VEC : ROWS_ANY, 4, POST, PRE>(c, parts);
     return norm_launch(k_block_norm_bwd<D, M, C, POST, PRE>, allowed, p, false, c.T, c.stream, parts, a);
 }
 
@@ -347,7 +347,7 @@ template <typename D, int M, int C> mp_status_t by_norms(const NormCall &c, int 
 template <typename D> mp_status_t norm_backward(const NormCall &c, int &parts)
 {
     if (c.H > 16 * NORM_THREADS) return c.vec ? by_norms<D, ROWS_VEC, 4>(c, parts) : by_norms<D, ROWS_ANY, 4>(c, parts);
-    if (!c.vec) return by_norms<D, ROWS_ANY, 2>(c, parts);
+    if (!c.vec) return norm_is_narrow(c.H) ? by_norms<D, ROWS_NARROW, 2>(c, parts) : by_norms<D, ROWS_ANY, 2>(c, parts);
     return norm_by_bulk<D>(c.H) ? by_norms<D, ROWS_BULK, 2>(c, parts) : by_norms<D, ROWS_VEC, 2>(c, parts);
 }
 

@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, C < 4
             normalise(g, v, layer, mean1, rstd1, pre_w, pre_b, a.pre_b != nullptr);
             if (there) g.store(static_cast<D *>(a.y) + row, v);
         }
-        if (M == ROWS_ANY || (M == ROWS_BULK && a.pre_w == nullptr)) {
+        if (!G::VEC || (M == ROWS_BULK && a.pre_w == nullptr)) {
             if (G::STAGED) g.barrier();
             refill();
         }
@@ -200,7 +200,7 @@ template <typename D, int M, int C> mp_status_t forward(const NormCall &c)
     const NormPlan p = norm_plan<D>(c.T, c.H, C, C < 4 ? NORM_THREADS : 2 * NORM_THREADS, M == ROWS_BULK, a.in.tensors,
                                     held, 0, true);
     if constexpr (C < 4)
-        if (p.stages < 1) return forward<D, M == ROWS_ANY ? ROWS_ANY : ROWS_VEC, 4>(c);
+        if (p.stages < 1) return forward<D, NormGroup<D, M, C>::VEC ? ROWS_VEC : ROWS_ANY, 4>(c);
     int grid;
     return norm_launch(k_block_norm<D, M, C>, allowed, p, true, c.T, c.stream, grid, a);
 }
@@ -210,7 +210,7 @@ template <typename D, int M, int C> mp_status_t forward(const NormCall &c)
 template <typename D> mp_status_t norm_forward(const NormCall &c)
 {
     if (c.H > 16 * NORM_THREADS) return c.vec ? forward<D, ROWS_VEC, 4>(c) : forward<D, ROWS_ANY, 4>(c);
-    if (!c.vec) return forward<D, ROWS_ANY, 2>(c);
+    if (!c.vec) return norm_is_narrow(c.H) ? forward<D, ROWS_NARROW, 2>(c) : forward<D, ROWS_ANY, 2>(c);
     return norm_by_bulk<D>(c.H) ? forward<D, ROWS_BULK, 2>(c) : forward<D, ROWS_VEC, 2>(c);
 }
 template mp_status_t norm_forward<__nv_bfloat16>(const NormCall &);
