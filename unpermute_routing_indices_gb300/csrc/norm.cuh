@@ -40,6 +40,7 @@ enum { ROWS_ANY, ROWS_NARROW, ROWS_VEC, ROWS_BULK };
 struct NormPlan {
     int W, R;         // threads a row, rows a CTA at a time
     int stages, pitch;   // slots of a group, bytes of one tensor's row in a slot
+    int held;            // bytes of a vector that the rows share
     size_t smem;
 };
 
@@ -211,10 +212,11 @@ template <typename D, int M, int C> struct NormGroup {
     // Column of pair i; the second of the pair is `beside` further on.
     __device__ __forceinline__ int col(int i) const
     {
-        return VEC ? (2 * i / NV * W + tid) * NV + 2 * i % NV : RUNS ? first() + 64 * i : 2 * i * W + tid;
+        return VEC ? (2 * i / NV * W + tid) * NV + 2 * i % NV : first() + step(i);
     }
+    __device__ __forceinline__ int step(int i) const { return RUNS ? 64 * i : 2 * i * W; }
     __device__ __forceinline__ int beside() const { return VEC ? 1 : RUNS ? 32 : W; }
-    __device__ __forceinline__ int first() const { return (tid >> 5) * RUN + (tid & 31); }
+    __device__ __forceinline__ int first() const { return RUNS ? (tid >> 5) * RUN + (tid & 31) : tid; }
     // Whether the row has all of this warp's run: then nothing is asked for each value.
     __device__ __forceinline__ bool whole() const { return (tid >> 5) * RUN + RUN <= H; }
 
@@ -234,11 +236,24 @@ template <typename D, int M, int C> struct NormGroup {
 #pragma unroll
             for (int i = 0; i < N2; ++i) f[i] = pair(norm_value(from[64 * i]), norm_value(from[64 * i + 32]));
         } else {
+            const D *const from = p + first();
+            const int left = H - first();
 #pragma unroll
             for (int i = 0; i < N2; ++i) {
-                const int at = col(i), next = at + beside();
-                f[i] = pair(at < H ? norm_value(p[at]) : 0.0f, next < H ? norm_value(p[next]) : 0.0f);
+                const int at = step(i), next = at + beside();
+                f[i] = pair(at < left ? norm_value(from[at]) : 0.0f, next < left ? norm_value(from[next]) : 0.0f);
             }
+        }
+    }
+    // The same of what hold() has copied (STAGED; else of where it is).
+    __device__ __forceinline__ void load_shared(const D *p, f2 (&f)[N2]) const
+    {
+        if (RUNS && STAGED) {
+            const D *const from = p + first();
+#pragma unroll
+            for (int i = 0; i < N2; ++i) f[i] = pair(norm_value(from[64 * i]), norm_value(from[64 * i + 32]));
+        } else {
+            load(p, f);
         }
     }
     __device__ __forceinline__ void store(D *p, const f2 (&f)[N2]) const
@@ -258,28 +273,41 @@ template <typename D, int M, int C> struct NormGroup {
                 norm_put(to + 64 * i + 32, r.y);
             }
         } else {
+            D *const to = p + first();
+            const int left = H - first();
 #pragma unroll
             for (int i = 0; i < N2; ++i) {
-                const int at = col(i), next = at + beside();
+                const int at = step(i), next = at + beside();
                 const float2 r = both(f[i]);
-                if (at < H) norm_put(p + at, r.x);
-                if (next < H) norm_put(p + next, r.y);
+                if (at < left) norm_put(to + at, r.x);
+                if (next < left) norm_put(to + next, r.y);
             }
         }
+    }
+    // Sums of the rows' values in shared memory, [N2][W] pairs, each thread's its own: banks are
+    // used evenly, and what is past the row's end adds 0.  (In the order of the columns, eight
+    // threads to a bank, two biases took 2/3 of a gradient's time.)
+    __device__ __forceinline__ void pile(f2 *p, const f2 (&f)[N2]) const
+    {
+#pragma unroll
+        for (int i = 0; i < N2; ++i) p[i * W + tid] = add2(p[i * W + tid], f[i]);
+    }
+    // The sum of column c there.
+    __device__ __forceinline__ float piled(const f2 *p, int c) const
+    {
+        int i, t, second;
+        if (VEC) {
+            const int v = c / NV, e = c % NV;
+            i = v / W * (NV / 2) + (e >> 1); t = v % W; second = e & 1;
+        } else {
+            const int k = RUNS ? (c % RUN) >> 5 : c / W;
+            i = k >> 1; t = RUNS ? c / RUN * 32 + (c & 31) : c % W; second = k & 1;
+        }
+        return reinterpret_cast<const float *>(p + i * W + t)[second];
     }
     // fp32 sums a column: set, or added to.
     template <bool ADD> __device__ __forceinline__ void columns(float *p, const f2 (&f)[N2]) const
     {
-        if (RUNS && whole()) {
-            float *const to = p + first();
-#pragma unroll
-            for (int i = 0; i < N2; ++i) {
-                const float2 r = both(f[i]);
-                to[64 * i] = ADD ? to[64 * i] + r.x : r.x;
-                to[64 * i + 32] = ADD ? to[64 * i + 32] + r.y : r.y;
-            }
-            return;
-        }
 #pragma unroll
         for (int i = 0; i < N2; ++i) {
             const int at = col(i), next = at + beside();
@@ -311,6 +339,15 @@ template <typename D, int M, int C> struct NormGroup {
         } else {
             const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15u);
             const int granules = (off + H * static_cast<int>(sizeof(D)) + 15) / 16;
+            const char *from = row - off;
+            if (from >= static_cast<const char *>(rows.at) && reinterpret_cast<int64_t>(from) + granules * 16 <= rows.end) {
+                from += tid * 16;   // not the tensor's first or last row: nothing is asked for each granule
+                uint32_t dst = to + tid * 16;
+#pragma unroll 1
+                for (int q = tid; q < granules; q += W, from += W * 16, dst += W * 16) cp_async16(dst, from);
+                return;
+            }
+#pragma unroll 1
             for (int q = tid; q < granules; q += W) {
                 const char *src = row - off + q * 16;
                 const int64_t left = rows.end - reinterpret_cast<int64_t>(src);
@@ -323,7 +360,10 @@ template <typename D, int M, int C> struct NormGroup {
             }
         }
     }
-    // Starts the copy of row t, if there is one, into slot `i` at `slot`.
+    // Starts the copy of row t, if there is one, into slot `i` at `slot`.  Where this is done in several
+    // places the tensors are a loop (U 1): copies of granules are much code, and gradients of rows
+    // that start anywhere wait for instructions (4,099 x 4,097 143 -> 128 us).
+    template <int U>
     __device__ __forceinline__ void fetch(const NormInputs &in, uint32_t t, uint32_t T, uint8_t *slot, int pitch, int i) const
     {
         if (!STAGED) return;
@@ -339,7 +379,7 @@ template <typename D, int M, int C> struct NormGroup {
                               static_cast<const char *>(in.rows[k].at) + static_cast<uint64_t>(t) * bytes, bytes, bars + 8 * i);
         } else {
             if (t < T) {
-#pragma unroll
+#pragma unroll(VEC ? 5 : U)
                 for (int k = 0; k < 5; ++k)
                     if (in.slot[k] >= 0) fetch_one(in.rows[k], t, slot + in.slot[k] * pitch);
             }
@@ -381,7 +421,8 @@ template <typename D, int M, int C> struct NormGroup {
         if (VEC) {
             for (int c = threadIdx.x; c < H / NV; c += blockDim.x) cp_async16(smem_u32(to) + c * 16, from + c * NV);
         } else {
-            for (int c = threadIdx.x; c < H; c += blockDim.x) reinterpret_cast<D *>(to)[c] = from[c];
+            const int end = RUNS ? W * N : H;   // to the end of the last warp's run: 0
+            for (int c = threadIdx.x; c < end; c += blockDim.x) norm_put(reinterpret_cast<D *>(to) + c, c < H ? norm_value(from[c]) : 0.0f);
         }
     }
 
@@ -404,8 +445,8 @@ template <typename D, int M, int C> struct NormGroup {
 __host__ __device__ inline int norm_wide(int H) { return (H + 3) / 4 * 4; }
 
 // Threads a row, rows at a time, and slots for `tensors` staged rows; `held` vectors that the
-// rows share lie beside them, and `sums` fp32 sums a column of each group.  Two CTAs on an SM wherever two slots or more fit in half of it.
-template <typename D> NormPlan norm_plan(int64_t T, int H, int C, int threads, bool bulk, int tensors, int held, int sums, bool two)
+// rows share lie beside them, and `sums` of the rows' values of each group.  Two CTAs on an SM wherever two slots or more fit in half of it.
+template <typename D> NormPlan norm_plan(int64_t T, int H, int C, int threads, int form, int tensors, int held, int sums, bool two)
 {
     NormPlan p;
     const int need = (H + 8 * C - 1) / (8 * C);
@@ -417,14 +458,24 @@ template <typename D> NormPlan norm_plan(int64_t T, int H, int C, int threads, b
     p.R = C < 4 ? threads / p.W : 1;
     while (p.R > 1 && p.W * (p.R / 2) >= 32 && (T + p.R / 2 - 1) / (p.R / 2) <= sm_count()) p.R /= 2;   // few rows: spread
     p.pitch = (H * static_cast<int>(sizeof(D)) + 15) / 16 * 16 + 16;
-    const int64_t extra = C < 4 ? static_cast<int64_t>(held) * p.pitch + static_cast<int64_t>(sums) * p.R * norm_wide(H) * 4 : 0;
-    const size_t fixed = NormGroup<D, ROWS_ANY, 2>::head(p.W, p.R) + static_cast<size_t>(extra);
-    const size_t slot = static_cast<size_t>(p.pitch) * tensors * p.R;
-    p.stages = 0;
-    if (C < 4) {
-        const size_t room = two && fixed + 2 * slot <= NORM_BUDGET ? NORM_BUDGET : NORM_MOST;
-        p.stages = fixed < room ? static_cast<int>((room - fixed) / slot) : 0;
-        if (p.stages > (bulk ? 3 : NORM_SLOTS)) p.stages = bulk ? 3 : NORM_SLOTS;   // of bulk copies more are slower (88.6, 88.7, 90.7 us with 2, 3, 4)
+    const bool bulk = form == ROWS_BULK;
+    const int runs = p.W * 8 * C * static_cast<int>(sizeof(D));   // what the warps' runs take
+    p.held = form == ROWS_ANY && runs > p.pitch ? runs : p.pitch;
+    size_t fixed, slot;
+    for (;; --p.R) {
+        const int64_t extra = C < 4 ? static_cast<int64_t>(held) * p.held + static_cast<int64_t>(sums) * p.R * p.W * 32 * C : 0;
+        fixed = NormGroup<D, ROWS_ANY, 2>::head(p.W, p.R) + static_cast<size_t>(extra);
+        slot = static_cast<size_t>(p.pitch) * tensors * p.R;
+        p.stages = 0;
+        if (C < 4) {
+            const size_t room = two && fixed + 2 * slot <= NORM_BUDGET ? NORM_BUDGET : NORM_MOST;
+            p.stages = fixed < room ? static_cast<int>((room - fixed) / slot) : 0;
+            if (p.stages > (bulk ? 3 : NORM_SLOTS)) p.stages = bulk ? 3 : NORM_SLOTS;   // of bulk copies more are slower (88.6, 88.7, 90.7 us with 2, 3, 4)
+        }
+        // Fewer rows at a time rather than none on their way, where bytes count (gradients at both norms,
+        // fp32: 2,048 x 2,048 26.8 -> 23.8 us); rows that start anywhere are bound by instructions (2,047 x
+        // 2,050 42.9 -> 48.6) and only have to fit.
+        if (p.stages >= (bulk ? 2 : 1) || p.R == 1 || p.W < 32) break;
     }
     const int64_t steps = (T + p.R - 1) / p.R;
     if (p.stages > steps) p.stages = static_cast<int>(steps);

@@ -57,7 +57,7 @@ __device__ __forceinline__ void normalise(const G &g, f2 (&v)[G::N2], bool layer
                                           const D *b, bool with_b)
 {
     f2 t[G::N2];
-    g.load(w, t);
+    g.load_shared(w, t);
     const f2 off = pair(-mean, -mean), r = pair(rstd, rstd);
     if (layer) {
 #pragma unroll
@@ -66,7 +66,7 @@ __device__ __forceinline__ void normalise(const G &g, f2 (&v)[G::N2], bool layer
 #pragma unroll
     for (int i = 0; i < G::N2; ++i) v[i] = mul2(mul2(v[i], r), t[i]);
     if (with_b) {
-        g.load(b, t);
+        g.load_shared(b, t);
 #pragma unroll
         for (int i = 0; i < G::N2; ++i) v[i] = add2(v[i], t[i]);
     }
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, C < 4
             const D *const to = reinterpret_cast<const D *>(held);
             if (v != nullptr) {
                 g.hold(static_cast<const D *>(v), held);
-                held += p.pitch;
+                held += p.held;
             }
             return to;
         } else {
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, C < 4
     const D *const pre_w = hold(a.pre_w), *const pre_b = hold(a.pre_b);
     cp_commit();
     if (G::STAGED)
-        for (int i = 0; i < p.stages; ++i) g.fetch(a.in, first + i * step + g.group, T, ring + i * slot_bytes, p.pitch, i);
+        for (int i = 0; i < p.stages; ++i) g.template fetch<5>(a.in, first + i * step + g.group, T, ring + i * slot_bytes, p.pitch, i);
     // A token's gate, read one row ahead.
     const auto gate_of = [&](uint32_t t) {
         return a.gate_form == MP_GATE_TOKEN && t < T ? norm_value(static_cast<const D *>(a.gate)[t]) : 1.0f;
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, C < 4
             normalise(g, v, layer, mean0, rstd0, post_w, post_b, a.post_b != nullptr);
         }
         if (by_channel) {
-            g.load(channel, w);
+            g.load_shared(channel, w);
 #pragma unroll
             for (int i = 0; i < G::N2; ++i) v[i] = mul2(v[i], w[i]);
         } else if (with_gate && there) {
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(C < 4 ? NORM_THREADS : 2 * NORM_THREADS, C < 4
         // one `stages` steps on.
         const auto refill = [&]() {
             if (G::STAGED) {
-                g.fetch(a.in, t + p.stages * step, T, slot, p.pitch, at);
+                g.template fetch<5>(a.in, t + p.stages * step, T, slot, p.pitch, at);
                 at = g.after(at, p.stages);
             }
         };
@@ -197,7 +197,7 @@ template <typename D, int M, int C> mp_status_t forward(const NormCall &c)
     a.s = c.s_out; a.y = c.y; a.stats = c.stats; a.status = c.status;
     const int held = (c.post_w != nullptr) + (c.post_b != nullptr) + (c.gate_form == MP_GATE_CHANNEL) +
                      (c.pre_w != nullptr) + (c.pre_b != nullptr);
-    const NormPlan p = norm_plan<D>(c.T, c.H, C, C < 4 ? NORM_THREADS : 2 * NORM_THREADS, M == ROWS_BULK, a.in.tensors,
+    const NormPlan p = norm_plan<D>(c.T, c.H, C, C < 4 ? NORM_THREADS : 2 * NORM_THREADS, M, a.in.tensors,
                                     held, 0, true);
     if constexpr (C < 4)
         if (p.stages < 1) return forward<D, NormGroup<D, M, C>::VEC ? ROWS_VEC : ROWS_ANY, 4>(c);
