@@ -210,13 +210,13 @@ template <typename D, int M, int C> struct NormGroup {
     static constexpr int M_MOST = 3;
 
     // Column of pair i; the second of the pair is `beside` further on.
-    __device__ __forceinline__ int col(int i) const
+    __host__ __device__ __forceinline__ int col(int i) const
     {
         return VEC ? (2 * i / NV * W + tid) * NV + 2 * i % NV : first() + step(i);
     }
-    __device__ __forceinline__ int step(int i) const { return RUNS ? 64 * i : 2 * i * W; }
-    __device__ __forceinline__ int beside() const { return VEC ? 1 : RUNS ? 32 : W; }
-    __device__ __forceinline__ int first() const { return RUNS ? (tid >> 5) * RUN + (tid & 31) : tid; }
+    __host__ __device__ __forceinline__ int step(int i) const { return RUNS ? 64 * i : 2 * i * W; }
+    __host__ __device__ __forceinline__ int beside() const { return VEC ? 1 : RUNS ? 32 : W; }
+    __host__ __device__ __forceinline__ int first() const { return RUNS ? (tid >> 5) * RUN + (tid & 31) : tid; }
     // Whether the row has all of this warp's run: then nothing is asked for each value.
     __device__ __forceinline__ bool whole() const { return (tid >> 5) * RUN + RUN <= H; }
 
@@ -462,7 +462,7 @@ template <typename D> NormPlan norm_plan(int64_t T, int H, int C, int threads, i
     const int runs = p.W * 8 * C * static_cast<int>(sizeof(D));   // what the warps' runs take
     p.held = form == ROWS_ANY && runs > p.pitch ? runs : p.pitch;
     size_t fixed, slot;
-    for (;; --p.R) {
+    for (;; p.R = p.W < 32 ? p.R / 2 : p.R - 1) {
         const int64_t extra = C < 4 ? static_cast<int64_t>(held) * p.held + static_cast<int64_t>(sums) * p.R * p.W * 32 * C : 0;
         fixed = NormGroup<D, ROWS_ANY, 2>::head(p.W, p.R) + static_cast<size_t>(extra);
         slot = static_cast<size_t>(p.pitch) * tensors * p.R;
@@ -474,8 +474,8 @@ template <typename D> NormPlan norm_plan(int64_t T, int H, int C, int threads, i
         }
         // Fewer rows at a time rather than none on their way, where bytes count (gradients at both norms,
         // fp32: 2,048 x 2,048 26.8 -> 23.8 us); rows that start anywhere are bound by instructions (2,047 x
-        // 2,050 42.9 -> 48.6) and only have to fit.
-        if (p.stages >= (bulk ? 2 : 1) || p.R == 1 || p.W < 32) break;
+        // 2,050 42.9 -> 48.6) and only have to fit.  A CTA stays whole warps; rows of less than a warp always fit.
+        if (p.stages >= (bulk ? 2 : 1) || p.R == 1 || p.W * p.R <= 32) break;
     }
     const int64_t steps = (T + p.R - 1) / p.R;
     if (p.stages > steps) p.stages = static_cast<int>(steps);
@@ -507,9 +507,11 @@ template <typename D> mp_status_t norm_backward(const NormCall &c, int &parts);
 
 // Launches `kernel` over the rows.  `two`: compiled for two CTAs on an SM.
 template <typename K, typename... A>
-mp_status_t norm_launch(K kernel, std::atomic<uint64_t> &allowed, NormPlan p, bool two, int64_t T, cudaStream_t stream,
-                        int &grid, A... args)
+mp_status_t norm_launch(K kernel, std::atomic<uint64_t> &allowed, NormPlan p, int form, bool two, int64_t T,
+                        cudaStream_t stream, int &grid, A... args)
 {
+    // Rows in runs belong to whole warps, and sums cross whole warps: norm_plan gives nothing else.
+    if (p.W * p.R % 32 != 0 || (form == ROWS_ANY && p.W % 32 != 0)) return MP_ERR_UNSUPPORTED;
     if (!allow_smem(kernel, allowed, NORM_MOST)) return MP_ERR_CUDA;
     const int64_t steps = (T + p.R - 1) / p.R, most = sm_count() * (two && p.smem <= NORM_BUDGET ? 2 : 1);
     grid = static_cast<int>(steps < most ? steps : most);

@@ -329,7 +329,7 @@ template <typename D, int M, int C, bool POST, bool PRE, bool MORE> mp_status_t 
                                                                                          const NormPlan &p, int &parts)
 {
     static std::atomic<uint64_t> allowed{0};
-    return norm_launch(k_block_norm_bwd<D, M, C, POST, PRE, MORE>, allowed, p, false, c.T, c.stream, parts, a);
+    return norm_launch(k_block_norm_bwd<D, M, C, POST, PRE, MORE>, allowed, p, M, false, c.T, c.stream, parts, a);
 }
 
 template <typename D, int M, int C, bool POST, bool PRE> mp_status_t run(const NormCall &c, int &parts)
@@ -349,7 +349,7 @@ template <typename D, int M, int C, bool POST, bool PRE> mp_status_t run(const N
     const NormPlan p = norm_plan<D>(c.T, c.H, C, C < 4 ? NORM_THREADS : 2 * NORM_THREADS, M, a.in.tensors,
                                     held, more, false);
     if constexpr (C < 4) {
-        if (p.stages < 1)   // fp32 rows and several sums beside them
+        if (p.stages < 1)   // one fp32 row and the sums beside it are more than shared memory: 5,124 wide or more
             return run<D, NormGroup<D, M, C>::VEC ? ROWS_VEC : ROWS_ANY, 4, POST, PRE>(c, parts);
         if (more == 0) return launch<D, M, C, POST, PRE, false>(c, a, p, parts);
     }

@@ -202,7 +202,7 @@ template <typename D, int M, int C> mp_status_t forward(const NormCall &c)
     if constexpr (C < 4)
         if (p.stages < 1) return forward<D, NormGroup<D, M, C>::VEC ? ROWS_VEC : ROWS_ANY, 4>(c);
     int grid;
-    return norm_launch(k_block_norm<D, M, C>, allowed, p, true, c.T, c.stream, grid, a);
+    return norm_launch(k_block_norm<D, M, C>, allowed, p, M, true, c.T, c.stream, grid, a);
 }
 
 }  // namespace
