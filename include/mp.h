@@ -81,7 +81,8 @@ typedef void *mp_stream_t;    /* a cudaStream_t                             */
 #define MP_STATUS_BAD_ROW 0x20       /* row_map entry outside [-1,N): skipped    */
 #define MP_STATUS_BAD_PADDED 0x40    /* a padded size below its group's rows     */
 #define MP_STATUS_BAD_OFFSETS 0x80   /* offsets fall, or leave [0,R]: clamped    */
-#define MP_STATUS_STALLED 0x100      /* a kernel gave up a wait: outputs invalid */
+#define MP_STATUS_STALLED 0x100      /* a kernel gave up a wait: outputs invalid, and
+                                      * inputs whose place they take        */
 
 /* Token types of the chunk entry points with a dtype argument. */
 #define MP_DTYPE_BF16 0
