@@ -484,7 +484,8 @@ size_t mp_block_norm_bwd_workspace_size(int64_t T, int32_t H);
  *   workspace  device, >= mp_block_norm_bwd_workspace_size(T,H) bytes, 16-byte
  *              aligned; may be NULL if no gradient of the shape [H] is wanted
  *   dev_status device int32 or NULL: MP_STATUS_STALLED
- * g_residual may be the buffer of g_s or g_y, g_x that of any [T,H] input, g_gate the gate's.
+ * g_residual may be the buffer of g_s, g_y or s, g_x that of any [T,H] input, g_gate the gate's;
+ * no two results may be one buffer, but g_x and g_residual where nothing makes them differ.
  * Sums over rows are made in an order that depends on the sizes, types, alignment and
  * device alone.
  */

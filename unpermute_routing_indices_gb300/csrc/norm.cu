@@ -140,6 +140,14 @@ extern "C" mp_status_t mp_block_norm_bwd(const void *g_s, const void *g_y, const
                   (pre_weight != nullptr) != (g_y != nullptr) || (pre_weight == nullptr && g_s == nullptr) ||
                   ((post_weight != nullptr || gate != nullptr) && x == nullptr)))
         return MP_ERR_INVALID_ARG;
+    // Rows are written one result after another, g_residual before x and the gate are read.
+    const bool with_x = post_weight != nullptr || gate != nullptr;
+    const void *const g_elements = gate_form == MP_GATE_ELEMENT ? g_gate : nullptr;
+    if (g_residual != nullptr &&
+        ((g_residual == g_x && (with_x || scale != 1.0f)) || g_residual == g_elements || (with_x && g_residual == x) ||
+         (gate_form == MP_GATE_ELEMENT && g_residual == gate)))
+        return MP_ERR_INVALID_ARG;
+    if (g_elements != nullptr && g_elements == g_x) return MP_ERR_INVALID_ARG;
     void *const shared[NORM_SHARED] = {g_post_weight, g_post_bias, g_pre_weight, g_pre_bias,
                                        gate_form == MP_GATE_CHANNEL ? g_gate : nullptr};
     NormSums n = {};
@@ -172,7 +180,6 @@ extern "C" mp_status_t mp_block_norm_bwd(const void *g_s, const void *g_y, const
         c.g_gate = gate_form == MP_GATE_CHANNEL ? nullptr : g_gate;
         for (int i = 0; i < NORM_SHARED; ++i) c.sums[i] = sums[i];
         c.status = dev_status; c.stream = as_stream(stream);
-        const bool with_x = post_weight != nullptr || gate != nullptr;
         c.vec = vectors(H, dtype, {g_s, g_y, with_x ? x : nullptr, pre_weight != nullptr ? s : nullptr,
                                    gate_form == MP_GATE_TOKEN ? nullptr : gate, post_weight, post_bias, pre_weight,
                                    g_x, g_residual, c.g_gate != nullptr && gate_form == MP_GATE_ELEMENT ? g_gate : nullptr});
