@@ -218,8 +218,6 @@ class _BlockNorm(torch.autograd.Function):
             return (None,) * 12
         if pre_weight is not None and g_y is None:
             g_y = torch.zeros_like(s)
-        if pre_weight is None and g_s is None:
-            g_s = torch.zeros_like(x)
         g = mp_block_norm_bwd(
             None if g_s is None else g_s.contiguous(), None if g_y is None else g_y.contiguous(),
             x, s, stats, post_weight=post_weight, post_bias=post_bias, gate=gate, scale=ctx.scale,
