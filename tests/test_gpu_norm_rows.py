@@ -42,3 +42,21 @@ def check(T, H, dtype, kind="layer", gate="channel", seed=0, off=0):
 def test_narrow_fp32(T, H, off, gate):
     """Rows of less than a warp's 32 x 16 values, where sums of several groups fill shared memory."""
     check(T, H, torch.float32, gate=gate, seed=T + H, off=off)
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("gate", ["channel", "token", "element"])
+@pytest.mark.parametrize("T,H,dtype", [(4099, 4096, "bf16"), (4099, 1009, "fp16"), (40000, 64, "bf16"), (20011, 264, "fp32"),
+                                       (3001, 2048, "fp32"), (5003, 4097, "bf16"), (30011, 33, "fp16"), (2203, 8192, "bf16")])
+def test_sums_over_many_rows(T, H, dtype, kind, gate):
+    """Biases' and a channel gate's sums beside the weights', each group of threads over 2 to 30 rows."""
+    check(T, H, DT[dtype], kind, gate, seed=H)
+
+
+@pytest.mark.parametrize("gate", ["channel", "element"])
+@pytest.mark.parametrize("T,H,dtype", [(400, 8200, "bf16"), (403, 8201, "fp16"), (460, 16384, "bf16"), (333, 16385, "fp32"),
+                                       (320, 32768, "fp16"), (310, 32767, "bf16"), (412, 7168, "fp32"), (409, 7173, "fp32"),
+                                       (460, 5640, "fp32"), (460, 6300, "fp32")])
+def test_sums_of_wide_rows(T, H, dtype, gate):
+    """Rows too wide to be staged, or just not, 3 or 4 of each CTA."""
+    check(T, H, DT[dtype], gate=gate, seed=H)
