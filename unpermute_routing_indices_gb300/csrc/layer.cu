@@ -910,7 +910,8 @@ template <typename L> void launch_logits(const LayerArgs &a, cudaStream_t s)
 
 // The cut of a product of `rows` by `depth`, of `entries` entries: the fewest cycles by this count.
 // A stage of 32 KB takes 1,400 cycles at the copy bandwidth and more with many tokens' rows beside
-// it (which it reads for U rows each), a unit's end 800.  Columns that a stage has and the product
+// it (which it reads for U rows each), a unit's end 800.  (Rows that start anywhere take more of the
+// first; they are counted alike.)  Columns that a stage has and the product
 // has not are idle warps.  At the end SMs wait for the last units, and at the start of the second
 // product for about half a unit of the first (`late`).  One token through 8 experts of 1,024 x
 // 4,096, U of the first and second product: 128, 128 57.8 us; 64, 64 51.3; 32, 64 47.5; 32, 32 47.9;
@@ -997,10 +998,15 @@ template <int NT, bool ODD> mp_status_t launch_layer(const LayerArgs &a, cudaStr
     return check_launch();
 }
 
+// Up to 8, 16 or 32 tokens an entry.  An expert with more than 16 has its weights copied once with 32 an entry and
+// twice with 16; but such a unit is 128 rows, which share the SMs badly where experts are few.  64 tokens, 64 experts of
+// 1,024 x 2,048, 12, 14, 16, 24, 32 tokens an expert, us with 16 and 32: 190, 199; 220, 212; 251, 224; 341, 277; 422, 387.
+// 32 experts, 12, 16: 111, 117; 142, 129.  16 experts of 512 x 4,096, 14, 20, 26: 84, 100; 117, 117; 122, 136; 8
+// experts, 12, 32: 62, 76; 89, 122.
 template <bool ODD> mp_status_t choose_layer(const LayerArgs &a, cudaStream_t s)
 {
     if (a.T <= 8) return launch_layer<1, ODD>(a, s);
-    if (a.T * a.K <= 12 * a.E) return launch_layer<2, ODD>(a, s);
+    if (a.E < 32 || a.T * a.K <= 12 * a.E) return launch_layer<2, ODD>(a, s);
     return launch_layer<4, ODD>(a, s);
 }
 
