@@ -15,7 +15,10 @@
 //              and lane l of a warp reads values l, l + 32, ... of the warp's run of 512; a barrier
 //              in between.  All but a row's last warp have a whole run and ask nothing for each value.
 //   ROWS_NARROW  such rows of up to 256 values, several a warp: values tid, tid + W, ...
-//   C 4      rows of more than 8192 values: not staged, 1024 threads read them as they need them.
+//   C 4      rows of more than 8192 values, and fp32 gradients of which one row and the sums beside it are more than
+//            shared memory (both norms: from 6,145 wide with biases, 5,633 with a gate for each value too, 5,121 with
+//            one for each channel): not staged, the threads read them as they need them.  That costs gradients most
+//            (4,096 x 7,168 fp32, layer norms with biases: 1,230 us, floor 105; 4,096 x 6,144, staged: 171, floor 90).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -409,8 +412,8 @@ template <typename D, int M, int C> struct NormGroup {
     // them (fetch), the rows that were left have gone by as the slots were, since all threads have to come to the
     // barriers, and each slot's phase at hand is waited for here, whichever of the two it is; where nothing is on its way
     // that is 1 s.  (A verdict on each row, by which its results are not stored and the loop is left, makes a row's loads
-    // wait for it: the gradient at both norms, 32,768 x 7,168, took 703 to 770 us with one in place of 603, the norm of
-    // 16,384 x 4,096 89 to 94 in place of 87.)
+    // wait for it: the gradient at both norms, 32,768 x 7,168, took 639 to 770 us with one in place of 603, the norm of
+    // 16,384 x 4,096 88 to 94 in place of 87.)
     __device__ __forceinline__ void finish(int i, int slots, int32_t *status) const
     {
         if (!STAGED) return;

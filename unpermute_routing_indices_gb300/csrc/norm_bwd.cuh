@@ -5,7 +5,9 @@
 // the gate's gradient written once.  Of what the rows share, a thread sums its columns'
 // gradients over its rows in registers (the weights') or in shared memory (biases and a
 // gate a channel, for which registers are short); a CTA adds up its groups in order and leaves one
-// partial sum a column, and a second kernel adds those of the CTAs in order, in pairs of fp32.
+// partial sum a column, and a second kernel adds those of the CTAs in order, in pairs of fp32.  A thread adds up
+// T / (152 R) rows one after another (R rows a CTA at a time), a CTA its groups: by the count of roundings off by
+// (T / (152 R) + 40) 2^-24 of the sum of magnitudes, 1.5e-5 for 32,768 x 7,168, where a result in bf16 is rounded by 2^-8.
 #pragma once
 
 #include "norm.cuh"
