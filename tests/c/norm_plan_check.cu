@@ -45,6 +45,7 @@ template <typename D> void check(int H, int64_t T, bool vec, int tensors, int he
     NormPlan p = norm_plan<D>(T, H, staged ? 2 : 4, staged ? NORM_THREADS : 2 * NORM_THREADS, form, tensors, held, sums, forward);
     if (staged && p.stages < 1) {   // the unstaged form in its place
         WANT(!forward && !norm_is_narrow(H), "unstaged");
+        if (forward) return;
         staged = false;
         p = norm_plan<D>(T, H, 4, 2 * NORM_THREADS, vec ? ROWS_VEC : ROWS_ANY, tensors, held, sums, forward);
     }
@@ -66,7 +67,7 @@ template <typename D> void check(int H, int64_t T, bool vec, int tensors, int he
 
 template <typename D> void sweep()
 {
-    for (int H = 1; H <= MP_MAX_NORM_WIDTH; H += H < 320 ? 1 : H < 8200 ? 13 : 1021)
+    for (int H = 1; H <= MP_MAX_NORM_WIDTH; H += H < 320 || (H > 8150 && H < 8200) ? 1 : H < 8200 ? 13 : 1021)
         for (const int64_t T : {1ll, 2ll, 31ll, 153ll, 1000ll, 2433ll, 5000ll, 10000ll, 20000ll, 40000ll, 1ll << 30})
             for (int vec = 0; vec < (H * sizeof(D) % 16 == 0 ? 2 : 1); ++vec)
                 for (int norms = 1; norms <= 3; ++norms)

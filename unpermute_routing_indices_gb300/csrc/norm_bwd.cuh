@@ -351,7 +351,7 @@ template <typename D, int M, int C, bool POST, bool PRE> mp_status_t run(const N
     const NormPlan p = norm_plan<D>(c.T, c.H, C, C < 4 ? NORM_THREADS : 2 * NORM_THREADS, M, a.in.tensors,
                                     held, more, false);
     if constexpr (C < 4) {
-        if (p.stages < 1)   // one fp32 row and the sums beside it are more than shared memory: 5,124 wide or more
+        if (p.stages < 1)   // one fp32 row and the sums beside it are more than shared memory: 5,121 wide or more
             return run<D, NormGroup<D, M, C>::VEC ? ROWS_VEC : ROWS_ANY, 4, POST, PRE>(c, parts);
         if (more == 0) return launch<D, M, C, POST, PRE, false>(c, a, p, parts);
     }

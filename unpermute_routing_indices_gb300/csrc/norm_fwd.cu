@@ -199,8 +199,7 @@ template <typename D, int M, int C> mp_status_t forward(const NormCall &c)
                      (c.pre_w != nullptr) + (c.pre_b != nullptr);
     const NormPlan p = norm_plan<D>(c.T, c.H, C, C < 4 ? NORM_THREADS : 2 * NORM_THREADS, M, a.in.tensors,
                                     held, 0, true);
-    if constexpr (C < 4)
-        if (p.stages < 1) return forward<D, NormGroup<D, M, C>::VEC ? ROWS_VEC : ROWS_ANY, 4>(c);
+    if (C < 4 && p.stages < 1) return MP_ERR_UNSUPPORTED;   // there is room for a slot up to 8,192 values of fp32
     int grid;
     return norm_launch(k_block_norm<D, M, C>, allowed, p, M, true, c.T, c.stream, grid, a);
 }
