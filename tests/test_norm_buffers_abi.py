@@ -33,6 +33,10 @@ def lib():
     (dict(gate=A, gate_form=3, g_x=B, g_residual=A), INVALID),             # so is the gate
     (dict(x=A, gate=B, gate_form=3, g_x=A, g_residual=C), WORKSPACE),
     (dict(gate=B, gate_form=3, g_x=B, g_residual=C), WORKSPACE),
+    (dict(g_x=B, g_post_weight=A, g_pre_weight=A), INVALID),               # vectors that the rows share
+    (dict(g_x=B, g_pre_weight=A, g_pre_bias=A), INVALID),
+    (dict(g_x=B, gate=C, gate_form=1, g_gate=A, g_post_weight=A), INVALID),
+    (dict(g_x=B, gate=C, gate_form=1, g_gate=A, g_post_weight=C), WORKSPACE),
 ])
 def test_block_norm_bwd_buffers(lib, new, code):
     base = {**abi.BWD, "g_pre_weight": ctypes.c_void_p(0x900000), "workspace": None}

@@ -155,6 +155,8 @@ extern "C" mp_status_t mp_block_norm_bwd(const void *g_s, const void *g_y, const
     int vectors_wanted = 0;
     for (int i = 0; i < NORM_SHARED; ++i)
         if (shared[i] != nullptr) {
+            for (int k = 0; k < i; ++k)
+                if (shared[k] == shared[i]) return MP_ERR_INVALID_ARG;
             sums[i] = static_cast<float *>(workspace) +
                       static_cast<size_t>(vectors_wanted) * static_cast<size_t>(T < NORM_PARTS ? T : NORM_PARTS) * H;
             n.sums[vectors_wanted] = sums[i];
